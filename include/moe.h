@@ -49,7 +49,7 @@ enum moe_status {
     MOE_ERR_TIMEOUT = 5       /* a bounded device-side wait ran out (see moe_check_device_error) */
 };
 
-enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 };
+enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 /* the moe_fp4_* calls alone */ };
 
 /* Gating modes ("Megatron-LM ... （六）", section "Router": top-k on the logits with softmax or sigmoid
  * weights; "v6 长序列和 MoE ...", "Load balancing loss" bullet: DeepSeek-V3 selection-only bias). */
@@ -428,6 +428,69 @@ int moe_dispatch_fp8(const void* x, const int32_t* topk_ids, int T, int h, int E
 int moe_expert_up_gate_fp8(const uint8_t* buf8, const float* scales, const int32_t* tile_sched, const void* packed_w,
                            int E, int h, int F, int rows, void* act, void* stream);
 int moe_dequant_fp8(const uint8_t* buf8, const float* scales, int rows, int h, void* out, void* stream);
+
+/* ---------------------------------------------------------------------------------------------------
+ * 4-bit experts: block-scaled floating point (e2m1 codes under block scales), its products grouped by expert, and the
+ * SwiGLU expert FFN on them. Serving operators: the codes are piecewise constant in x, so there is no backward (train
+ * with the bf16 calls).
+ *   A value is code * scale of its block of columns; codes stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives,
+ *   two to a byte, the even column in the low half.
+ *     MOE_FP4_NV: blocks of 16 columns, scale s = e4m3(amax / 6) to nearest even, at most 448
+ *     MOE_FP4_MX: blocks of 32 columns, scale s = 2^(floor(log2 amax) - 2), stored as exponent + 127, held in [0, 254]
+ *   code = e2m1(v / s) to nearest, ties to even, held at +-6 (0 where s is 0); amax the largest |v| of the block, v = x or
+ *   x * gscale[0] in fp32 (gscale: a device fp32 scalar or NULL). Infinities end at the largest code; a NaN makes its
+ *   block's scale NaN (0x7F, 0xFF) and its codes 0. A partial last block counts its missing columns as 0.
+ *   dtype / out_dtype: MOE_F32, MOE_BF16 or MOE_F16. x and out may have row strides (ldx, ldo, in elements) and need be
+ *   aligned to their type only; rows that start on 16 bytes are the fast case. Sizes: 1 <= K, N, F <= MOE_FP4_MAX_K,
+ *   rows <= MOE_FP4_MAX_ROWS, 1 <= groups <= 1024. src: x's row of each row, -1 for a row of zeros, or NULL (row r of x).
+ *
+ * moe_fp4_quantize: x [x_rows, K] -> codes [rows, moe_fp4_codes_pitch(K)] (codes past K are 0) and scales
+ *   [rows, moe_fp4_scales_pitch(K, fmt)], as checkpoints hold them. moe_fp4_dequantize: code * scale (/ gscale[0]) in fp32,
+ *   rounded once to dtype.
+ * moe_fp4_pack_weight: codes [G, N, pitch] and scales [G, N, blocks] of a weight -> packed
+ *   (moe_fp4_packed_weight_bytes() bytes, opaque), once per weight. moe_fp4_pack_expert_weights: the gate and up [E, F, h]
+ *   and down [E, h, F] weights likewise (moe_fp4_packed_expert_weights_bytes()).
+ * moe_fp4_linear: x quantised (fmt, gscale), then for the rows r of group g
+ *     out[r] = alpha[g] * sum_k Q(x)[r, k] W[g, :, k]         alpha [G] fp32 or NULL (1); fp32 accumulation
+ *   The rows of a group are [offsets[g], offsets[g + 1]) (offsets [G + 1] int32, rising within [0, rows]; any other is
+ *   reported by moe_check_device_error as MOE_ERR_INVALID_ARG and nothing is computed), or those of tile_sched
+ *   (moe_dispatch's; exactly one of the two is given). Rows of no group are not written.
+ * moe_fp4_expert_ffn: for the rows of expert e
+ *     act = silu(alpha_gate[e] Q(x) W_gate[e]^T) * (alpha_up[e] Q(x) W_up[e]^T)
+ *     out = alpha_down[e] * Q(act * act_gscale[0]) W_down[e]^T
+ *   act crosses memory in 4 bits only. Each alpha [E] fp32 or NULL; gscale and act_gscale as above. A caller that
+ *   quantised with multipliers divides them out in the alphas.
+ *   ws: moe_fp4_linear_workspace_size() / moe_fp4_expert_ffn_workspace_size() bytes, 256-byte aligned.
+ *   Errors: MOE_ERR_UNSUPPORTED for a dtype or fmt outside the enums; MOE_ERR_INVALID_ARG for sizes out of range, a null or
+ *   misaligned pointer, x shorter than rows without src, both or neither of offsets and tile_sched; MOE_ERR_WORKSPACE. A
+ *   src outside [-1, x_rows) is taken as -1 and reported by moe_check_device_error. Deterministic.
+ * ------------------------------------------------------------------------------------------------- */
+enum moe_fp4_format { MOE_FP4_NV = 0, MOE_FP4_MX = 1 };
+#define MOE_FP4_MAX_K (1 << 20)
+#define MOE_FP4_MAX_ROWS (1 << 28)
+
+size_t moe_fp4_codes_pitch(int K);
+size_t moe_fp4_scales_pitch(int K, int fmt);
+int moe_fp4_quantize(const void* x, long long ldx, int x_rows, const int32_t* src, int rows, int K, int dtype, int fmt,
+                     const float* gscale, void* codes, void* scales, void* stream);
+int moe_fp4_dequantize(const void* codes, const void* scales, int rows, int K, int fmt, const float* gscale, int dtype,
+                       void* out, long long ldo, void* stream);
+size_t moe_fp4_packed_weight_bytes(int G, int N, int K, int fmt);
+int moe_fp4_pack_weight(const void* codes, const void* scales, int G, int N, int K, int fmt, void* packed, void* stream);
+size_t moe_fp4_linear_workspace_size(int G, int K, int rows, int fmt);
+int moe_fp4_linear(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* offsets,
+                   const int32_t* tile_sched, const void* packed, const float* alpha, const float* gscale, int G, int N,
+                   int K, int rows, int fmt, int dtype, void* out, long long ldo, int out_dtype, void* ws, size_t ws_bytes,
+                   void* stream);
+size_t moe_fp4_packed_expert_weights_bytes(int E, int h, int F, int fmt);
+int moe_fp4_pack_expert_weights(const void* gate_codes, const void* gate_scales, const void* up_codes,
+                                const void* up_scales, const void* down_codes, const void* down_scales, int E, int h, int F,
+                                int fmt, void* packed, void* stream);
+size_t moe_fp4_expert_ffn_workspace_size(int E, int h, int F, int rows, int fmt);
+int moe_fp4_expert_ffn(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* offsets,
+                       const int32_t* tile_sched, const void* packed, const float* alpha_gate, const float* alpha_up,
+                       const float* alpha_down, const float* gscale, const float* act_gscale, int E, int h, int F, int rows,
+                       int fmt, int dtype, void* out, long long ldo, int out_dtype, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------------------------
  * Backward of the layer ("专家并行" (formulaic), section "BWD（反向传播）" and the overlap notes: the

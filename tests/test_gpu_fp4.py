@@ -1,0 +1,296 @@
+"""The 4-bit expert operators on the GPU against the float64 oracle: codes and scales exactly, products and the FFN
+within bounds that count the fp32 sums, the output's rounding and the activations that lie at a rounding tie."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp4_oracle as Q
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+HALF_STEP = {k: torch.finfo(v).eps / 2 for k, v in DT.items()}
+
+
+def data(shape, dtype, seed=0, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(DT[dtype]).cuda()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def ok(moe):
+    torch.cuda.synchronize()
+    assert moe.moe_check_device_error() == moe.MOE_OK, moe.moe_last_error_string()
+
+
+def weight(moe, G, N, K, fmt, seed, gscale=None):
+    w = data((G * N, K), "bf16", seed, K**-0.5)
+    c, s = moe.moe_fp4_quantize(w, fmt, gscale=gscale)
+    v = Q.dequantize(Q.unpack_codes(c.cpu().numpy(), K), s.cpu().numpy(), fmt).reshape(G, N, K)
+    return c.view(G, N, -1), s.view(G, N, -1), v
+
+
+# ------------------------------------------------------------------------------------------ quantisation
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows,K", [(1, 1), (1, 7168), (3, 15), (5, 16), (7, 31), (2, 33), (129, 64), (33, 100), (17, 999),
+                                    (300, 512), (4, 1040), (70, 2048)])
+def test_quantize_is_the_definition(gpu_lib, fmt, dtype, rows, K):
+    x = data((rows, K), dtype, rows * 7919 + K, 3.0)
+    c, s = gpu_lib.moe_fp4_quantize(x, fmt)
+    ok(gpu_lib)
+    code, byte = Q.quantize(f64(x), fmt)
+    np.testing.assert_array_equal(s.cpu().numpy(), byte)
+    np.testing.assert_array_equal(Q.unpack_codes(c.cpu().numpy(), K), code)
+    for out in ("fp32", dtype):
+        y = gpu_lib.moe_fp4_dequantize(c, s, K, fmt, dtype=DT[out])
+        want = torch.from_numpy(Q.dequantize(code, byte, fmt)).to(DT[out])
+        assert torch.equal(y.cpu(), want)
+    ok(gpu_lib)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_quantize_with_a_multiplier(gpu_lib, fmt):
+    # a power of two times bf16 is exact, and so is the quotient on the way back: the definition to the bit
+    x = data((65, 96), "bf16", 5)
+    g = torch.tensor([0.0625], device="cuda")
+    c, s = gpu_lib.moe_fp4_quantize(x, fmt, gscale=g)
+    y = gpu_lib.moe_fp4_dequantize(c, s, 96, fmt, gscale=g, dtype=torch.float32)
+    code, byte = Q.quantize(f64(x) * 0.0625, fmt)
+    np.testing.assert_array_equal(s.cpu().numpy(), byte)
+    np.testing.assert_array_equal(Q.unpack_codes(c.cpu().numpy(), 96), code)
+    np.testing.assert_array_equal(f64(y), Q.dequantize(code, byte, fmt) / 0.0625)
+    # any other: the way back is the rounded quotient, one half step of fp32
+    g.fill_(58.35)
+    y = gpu_lib.moe_fp4_dequantize(c, s, 96, fmt, gscale=g, dtype=torch.float32)
+    want = Q.dequantize(code, byte, fmt) / float(g)
+    assert (np.abs(f64(y) - want) <= 2.0**-24 * np.abs(want)).all()
+    ok(gpu_lib)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_quantize_at_the_edges(gpu_lib, fmt, dtype):
+    """Zeros, values at ties, the type's largest and smallest, infinities and NaN, each in blocks of their own."""
+    fi = torch.finfo(DT[dtype])
+    x = torch.zeros((12, 64), dtype=torch.float64)
+    x[1, :] = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0]).repeat(8) * torch.tensor([1.0, -1.0]).repeat(32)
+    x[2, 0], x[2, 40] = fi.max, -fi.max
+    x[3, :] = fi.tiny
+    x[4, 3] = fi.smallest_normal * fi.eps
+    x[5, 0], x[5, 1], x[5, 63] = float("inf"), -1.0, float("-inf")
+    x[6, 5], x[6, 6] = float("nan"), 2.0
+    x[7, :] = 6 * 448.0 * 1.5
+    x[8, :] = 2.0**-10 * 6
+    x[9, :] = -0.0
+    x[10, 0], x[10, 1] = fi.max, 1.0
+    x[11, 16] = 6 * 17 / 16            # amax / 6 half way between two e4m3 values
+    x = x.to(DT[dtype]).cuda()
+    c, s = gpu_lib.moe_fp4_quantize(x, fmt)
+    ok(gpu_lib)
+    code, byte = Q.quantize(f64(x), fmt)
+    np.testing.assert_array_equal(s.cpu().numpy(), byte)
+    np.testing.assert_array_equal(Q.unpack_codes(c.cpu().numpy(), 64), code)
+    y = gpu_lib.moe_fp4_dequantize(c, s, 64, fmt, dtype=torch.float32)
+    with np.errstate(over="ignore"):
+        want = Q.dequantize(code, byte, fmt).astype(np.float32)
+    np.testing.assert_array_equal(f64(y), want.astype(np.float64))
+
+
+def test_quantize_rows_by_index_and_strides(gpu_lib):
+    base = data((50, 300), "bf16", 9)
+    x = base[:, 7:207]                                       # rows 600 bytes apart, starting on 14
+    src = torch.tensor([3, -1, 49, 0, 3, 11], dtype=torch.int32, device="cuda")
+    c, s = gpu_lib.moe_fp4_quantize(x, "nv", src=src)
+    want = np.where(src.cpu().numpy()[:, None] >= 0, f64(x)[src.cpu().numpy().clip(0)], 0.0)
+    code, byte = Q.quantize(want, "nv")
+    np.testing.assert_array_equal(s.cpu().numpy(), byte)
+    np.testing.assert_array_equal(Q.unpack_codes(c.cpu().numpy(), 200), code)
+    out = torch.full((6, 256), 7.0, device="cuda")[:, 5:205]
+    gpu_lib.moe_fp4_dequantize(c, s, 200, "nv", out=out)
+    np.testing.assert_array_equal(f64(out), Q.dequantize(code, byte, "nv"))
+    assert (out._base[:, :5] == 7).all() and (out._base[:, 205:] == 7).all()
+    ok(gpu_lib)
+    # an index outside x: a row of zeros, and reported
+    src[2] = 50
+    c, s = gpu_lib.moe_fp4_quantize(x, "nv", src=src)
+    torch.cuda.synchronize()
+    assert gpu_lib.moe_check_device_error() == gpu_lib.MOE_ERR_INVALID_ARG
+    assert (Q.unpack_codes(c.cpu().numpy(), 200)[2] == 0).all()
+    ok(gpu_lib)
+
+
+# ----------------------------------------------------------------------------------------------- product
+
+
+def check_linear(moe, counts, N, K, fmt, dtype, out_dtype=None, alpha=None, gscale=None, src=None, x_rows=None, seed=1):
+    out_dtype = out_dtype or dtype
+    G, rows = len(counts), int(sum(counts))
+    x = data((x_rows if x_rows is not None else rows, K), dtype, seed)
+    c, s, w = weight(moe, G, N, K, fmt, seed + 1)
+    packed = moe.moe_fp4_pack_weight(c, s, K, fmt)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    y = moe.moe_fp4_linear(x, torch.from_numpy(off).cuda(), packed, N, fmt, alpha=alpha, gscale=gscale, src=src,
+                           out_dtype=DT[out_dtype])
+    ok(moe)
+    xx = f64(x) if src is None else np.where(src.cpu().numpy()[:, None] >= 0, f64(x)[src.cpu().numpy().clip(0)], 0.0)
+    a = Q.dequantize(*Q.quantize(xx * (1.0 if gscale is None else float(gscale)), fmt), fmt)
+    for g in range(G):
+        lo, hi = off[g], off[g + 1]
+        al = 1.0 if alpha is None else float(alpha[g])
+        want = a[lo:hi] @ w[g].T * al
+        bound = Q.product_bound(a[lo:hi] * al, w[g], want, HALF_STEP[out_dtype])
+        assert (np.abs(f64(y[lo:hi]) - want) <= bound).all(), (g, np.abs(f64(y[lo:hi]) - want).max())
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("counts,N,K", [
+    ([1], 64, 64), ([1], 1, 1), ([0, 1, 0], 128, 256), ([3, 0, 130, 1], 192, 320), ([128, 129, 127], 200, 512),
+    ([5], 1000, 33), ([33, 64, 96, 97], 65, 1000), ([300], 448, 2048), ([1] * 40, 256, 768), ([0, 0], 64, 64),
+    ([700, 1], 640, 192)])
+def test_linear(gpu_lib, fmt, counts, N, K):
+    check_linear(gpu_lib, counts, N, K, fmt, "bf16")
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("dtype,out_dtype", [("bf16", "fp32"), ("fp16", "fp16"), ("fp32", "fp32"), ("fp32", "bf16")])
+def test_linear_types_multipliers_and_rows_by_index(gpu_lib, fmt, dtype, out_dtype):
+    src = torch.tensor([4, 0, 0, -1, 9, 8, 7, 1, 2, 2, 9], dtype=torch.int32, device="cuda")
+    check_linear(gpu_lib, [4, 0, 7], 96, 160, fmt, dtype, out_dtype, alpha=torch.tensor([0.5, 9.0, -3.0], device="cuda"),
+                 gscale=torch.tensor([8.0], device="cuda"), src=src, x_rows=10)
+
+
+@pytest.mark.parametrize("rows,N,K", [(2600, 2100, 256), (9000, 1300, 128), (20000, 600, 64)])
+def test_linear_of_many_tiles(gpu_lib, rows, N, K):
+    """Enough tiles for each tile width, and more tiles than SMs: the accumulators and the ring wrap around."""
+    check_linear(gpu_lib, [rows // 3, rows - rows // 3 - 5, 5], N, K, "nv", "bf16")
+
+
+def test_linear_keeps_other_rows_and_columns(gpu_lib):
+    moe = gpu_lib
+    c, s, w = weight(moe, 2, 40, 64, "nv", 3)
+    packed = moe.moe_fp4_pack_weight(c, s, 64, "nv")
+    x = data((20, 64), "bf16", 4)
+    full = torch.full((20, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([2, 6, 13], dtype=torch.int32, device="cuda")
+    moe.moe_fp4_linear(x, off, packed, 40, "nv", out=full[:, 3:43])
+    ok(moe)
+    assert (full[:2] == 5).all() and (full[13:] == 5).all() and (full[:, :3] == 5).all() and (full[:, 43:] == 5).all()
+    a = Q.dequantize(*Q.quantize(f64(x), "nv"), "nv")
+    for g, lo, hi in ((0, 2, 6), (1, 6, 13)):
+        want = a[lo:hi] @ w[g].T
+        assert (np.abs(f64(full[lo:hi, 3:43]) - want) <= Q.product_bound(a[lo:hi], w[g], want, 2.0**-8)).all()
+
+
+@pytest.mark.parametrize("off", [[0, 5, 3, 20], [-1, 5, 6, 20], [0, 5, 6, 21]])
+def test_bad_offsets_are_reported_and_nothing_is_written(gpu_lib, off):
+    moe = gpu_lib
+    c, s, _ = weight(moe, 3, 32, 64, "mx", 3)
+    packed = moe.moe_fp4_pack_weight(c, s, 64, "mx")
+    out = torch.full((20, 32), 5.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_fp4_linear(data((20, 64), "bf16"), torch.tensor(off, dtype=torch.int32, device="cuda"), packed, 32, "mx", out=out)
+    torch.cuda.synchronize()
+    assert moe.moe_check_device_error() == moe.MOE_ERR_INVALID_ARG
+    assert (out == 5).all()
+    ok(moe)
+
+
+def test_a_nan_row_stays_in_its_row(gpu_lib):
+    moe = gpu_lib
+    c, s, _ = weight(moe, 1, 64, 128, "nv", 3)
+    packed = moe.moe_fp4_pack_weight(c, s, 128, "nv")
+    x = data((150, 128), "bf16", 8)
+    off = torch.tensor([0, 150], dtype=torch.int32, device="cuda")
+    y0 = moe.moe_fp4_linear(x, off, packed, 64, "nv")
+    x[77, 5] = float("nan")
+    y1 = moe.moe_fp4_linear(x, off, packed, 64, "nv")
+    ok(moe)
+    assert torch.isnan(y1[77]).all()
+    keep = [i for i in range(150) if i != 77]
+    assert torch.equal(y0[keep], y1[keep])
+
+
+# --------------------------------------------------------------------------------------------------- FFN
+
+
+def check_ffn(moe, counts, h, F, fmt, dtype, out_dtype=None, scaled=False, T=None, seed=1):
+    out_dtype = out_dtype or dtype
+    E, rows = len(counts), int(sum(counts))
+    rng = np.random.default_rng(seed)
+    x = data((T or rows, h), dtype, seed)
+    src = None if T is None else torch.from_numpy(rng.integers(-1, T, rows).astype(np.int32)).cuda()
+    mats = [weight(moe, E, n, k, fmt, seed + 10 + i) for i, (n, k) in enumerate(((F, h), (F, h), (h, F)))]
+    packed = moe.moe_fp4_pack_expert_weights(*((m[0], m[1]) for m in mats), h, F, fmt)
+    al = [torch.from_numpy(rng.uniform(0.25, 1.5, E).astype(np.float32)).cuda() if scaled else None for _ in range(3)]
+    gs, ags = (torch.tensor([v], device="cuda") if scaled else None for v in (4.0, 32.0))
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    y = moe.moe_fp4_expert_ffn(x, torch.from_numpy(off).cuda(), packed, F, fmt, src=src, alpha_gate=al[0], alpha_up=al[1],
+                               alpha_down=al[2], gscale=gs, act_gscale=ags, out_dtype=DT[out_dtype])
+    ok(moe)
+    xx = f64(x) if src is None else np.where(src.cpu().numpy()[:, None] >= 0, f64(x)[src.cpu().numpy().clip(0)], 0.0)
+    a = Q.dequantize(*Q.quantize(xx * (4.0 if scaled else 1.0), fmt), fmt)
+    tight = []
+    for e in range(E):
+        lo, hi = off[e], off[e + 1]
+        if lo == hi:
+            continue
+        A = [1.0 if t is None else float(t[e]) for t in al]
+        g, u = (a[lo:hi] @ mats[i][2][e].T * A[i] for i in (0, 1))
+        eg, eu = (Q.product_bound(a[lo:hi] * A[i], mats[i][2][e], (g, u)[i], 2.0**-24) for i in (0, 1))
+        act, err = Q.swiglu_bound(g, eg, u, eu)
+        m = 32.0 if scaled else 1.0
+        q, dq = Q.requantized(act * m, err * m, fmt)
+        want = q @ mats[2][2][e].T * A[2]
+        bound = Q.product_bound(q * A[2], mats[2][2][e], want, HALF_STEP[out_dtype])
+        bound = bound + (1 + HALF_STEP[out_dtype]) * (dq * A[2]) @ np.abs(mats[2][2][e]).T
+        got = f64(y[lo:hi])
+        assert (np.abs(got - want) <= bound).all(), (e, np.abs(got - want).max(), bound.max())
+        tight.append((bound / (np.abs(want).mean() + 1e-30)).ravel() if want.any() else np.zeros(0))
+    # (of the test itself: over all experts the ties are few, and the bound stays near the output's own rounding)
+    assert np.median(np.concatenate(tight)) < max(0.02, 4 * HALF_STEP[out_dtype])
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("counts,h,F,T", [
+    ([1], 64, 64, None), ([0, 3, 1], 128, 96, 2), ([130, 1, 0, 40], 256, 200, None), ([64, 64], 520, 33, 40),
+    ([1] * 24, 512, 448, 3), ([257], 320, 1024, 100)])
+def test_expert_ffn(gpu_lib, fmt, counts, h, F, T):
+    check_ffn(gpu_lib, counts, h, F, fmt, "bf16", T=T)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("dtype,out_dtype", [("fp16", "fp16"), ("bf16", "fp32"), ("fp32", "bf16")])
+def test_expert_ffn_types_and_multipliers(gpu_lib, fmt, dtype, out_dtype):
+    check_ffn(gpu_lib, [17, 0, 150], 192, 160, fmt, dtype, out_dtype, scaled=True, T=60)
+
+
+def test_expert_ffn_is_deterministic_and_captures(gpu_lib):
+    """The same bits on every call, on another stream and from a captured graph."""
+    moe = gpu_lib
+    E, h, F, rows = 8, 256, 256, 600
+    mats = [weight(moe, E, n, k, "nv", 20 + i)[:2] for i, (n, k) in enumerate(((F, h), (F, h), (h, F)))]
+    packed = moe.moe_fp4_pack_expert_weights(*mats, h, F, "nv")
+    x = data((rows, h), "bf16", 6)
+    off = torch.arange(0, rows + 1, rows // E, dtype=torch.int32, device="cuda")
+    ws = torch.empty(moe.moe_fp4_expert_ffn_workspace_size(E, h, F, rows, "nv"), dtype=torch.uint8, device="cuda")
+    y0 = moe.moe_fp4_expert_ffn(x, off, packed, F, "nv", ws=ws).clone()
+    ws.random_(0, 256)                                   # nothing in the workspace outlives a call
+    y1 = moe.moe_fp4_expert_ffn(x, off, packed, F, "nv", ws=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y2 = torch.empty_like(y0)
+    moe.moe_fp4_expert_ffn(x, off, packed, F, "nv", ws=ws, out=y2, stream=side)
+    torch.cuda.synchronize()
+    y3 = torch.empty_like(y0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_fp4_expert_ffn(x, off, packed, F, "nv", ws=ws, out=y3)
+    graph.replay()
+    graph.replay()
+    ok(moe)
+    assert torch.equal(y0, y1) and torch.equal(y0, y2) and torch.equal(y0, y3)

@@ -128,6 +128,6 @@ extern "C" int moe_check_device_error(void* stream) {
     if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "moe_check_device_error: %s", cudaGetErrorString(e));
     if (w[0] & kDevErrTimeout)
         return set_error(MOE_ERR_TIMEOUT, "device wait ran out (flags 0x%x, site 0x%x)", w[0], w[1]);
-    return set_error(MOE_ERR_INVALID_ARG, "device input check failed: topk id out of range (flags 0x%x, site 0x%x)",
+    return set_error(MOE_ERR_INVALID_ARG, "device input check failed: index out of range (flags 0x%x, site 0x%x)",
                      w[0], w[1]);
 }

@@ -1,0 +1,531 @@
+// Quantisation to block-scaled e2m1 and back, the packing of 4-bit weights and the tile schedule of ragged groups.
+//
+// Quantisation and its inverse are bound by memory: x is read once and 0.5 + 1 / BLK bytes a value are written (or the
+// other way round). A lane owns 16 consecutive columns (two 16-byte loads of bf16, one 8-byte store of codes), so an NV
+// block lives in one lane and an MX block in a pair of lanes; a warp covers 512 columns of a row, or several rows where
+// rows are narrower. Each warp keeps the loads of four items in flight.
+#include <algorithm>
+#include "fp4.cuh"
+
+namespace moe {
+namespace fp4 {
+
+constexpr int QTHREADS = 256;
+constexpr int QWARPS = QTHREADS / 32;
+constexpr int UNIT = 16;             // columns per lane
+constexpr int SEG = 32 * UNIT;       // columns per warp
+
+__device__ __forceinline__ float as_f32(float v) { return v; }
+__device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float as_f32(__half v) { return __half2float(v); }
+template <typename T> __device__ __forceinline__ T rounded(float v);
+template <> __device__ __forceinline__ float rounded<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
+
+// 16 elements as they lie in memory.
+template <typename T> struct alignas(16) Raw16 { uint4 q[sizeof(T)]; };
+
+// Columns [k0, k0 + 16) of a row as stored, zero past K. VEC: the row starts on 16 bytes. The caller's lanes of one warp
+// hold consecutive units of the same row in the other case too, where the elements are fetched one by one.
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw16<T> load_unit(const T* __restrict__ row, int k0, int K) {
+    Raw16<T> r;
+    if (VEC && k0 + UNIT <= K) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T); ++i) r.q[i] = __ldcs(reinterpret_cast<const uint4*>(row + k0) + i);
+        return r;
+    }
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) r.q[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (k0 < K) {
+        T* e = reinterpret_cast<T*>(r.q);
+#pragma unroll
+        for (int i = 0; i < UNIT; ++i)
+            if (k0 + i < K) e[i] = row[k0 + i];
+    }
+    return r;
+}
+
+// The codes (2 words) and, on the lane that owns it, the scale byte of this lane's unit; MX blocks span lanes 2i, 2i + 1.
+template <class F, typename T>
+__device__ __forceinline__ uint2 quantize_unit(const Raw16<T>& raw, const float* gscale, float g, uint32_t& byte) {
+    const T* e = reinterpret_cast<const T*>(raw.q);
+    float v[32], amax = 0.f;             // (block_codes takes whole blocks: an MX lane uses the lower half alone)
+#pragma unroll
+    for (int i = 0; i < UNIT; ++i) {
+        v[i] = as_f32(e[i]);
+        if (gscale) v[i] *= g;
+        amax = max_nan(amax, fabsf(v[i]));
+    }
+    if constexpr (F::ID == MOE_FP4_MX) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    float s, r;
+    byte = block_scale<F>(amax, s, r);
+    uint32_t w[4];
+    if constexpr (F::ID == MOE_FP4_MX) {
+#pragma unroll
+        for (int i = UNIT; i < 32; ++i) v[i] = 0.f;
+    }
+    block_codes<F>(v, amax, s, r, w);
+    return make_uint2(w[0], w[1]);
+}
+
+// Row-major form: codes [rows][pitch], scales [rows][nb]. An item is one row segment of lpr units, 32 / lpr rows to a
+// warp (lpr: a power of two, the units of a row where there are fewer than 32).
+template <class F, typename T, bool VEC>
+__global__ void __launch_bounds__(QTHREADS)
+quantize_rows_kernel(const T* __restrict__ x, long long ldx, int x_rows, const int32_t* __restrict__ src, int rows, int K,
+                     int lpr, const float* __restrict__ gscale, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                     unsigned* err) {
+    constexpr int U = 4;
+    const int lane = threadIdx.x & 31;
+    const int units = (K + 31) / 32 * 2;
+    const int nseg = (units + lpr - 1) / lpr, rpw = 32 / lpr, sub = lane / lpr;
+    const int nb = (K + F::BLK - 1) / F::BLK;
+    const size_t pitch = (size_t)units * 8;
+    const float g = gscale ? __ldg(gscale) : 1.f;
+    const long long items = (long long)((rows + rpw - 1) / rpw) * nseg;
+    const long long step = (long long)gridDim.x * QWARPS;
+    for (long long it0 = (long long)blockIdx.x * QWARPS + (threadIdx.x >> 5); it0 < items; it0 += U * step) {
+        Raw16<T> raw[U];
+        int row[U], unit[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const long long it = it0 + i * step;
+            row[i] = rows;
+            unit[i] = units;
+            if (it < items) {
+                const int rg = (int)(it / nseg);
+                row[i] = rg * rpw + sub;
+                unit[i] = (int)(it - (long long)rg * nseg) * lpr + (lane - sub * lpr);
+            }
+            const bool live = row[i] < rows && unit[i] < units;
+            int from = row[i];
+            if (live && src) {
+                from = __ldg(src + row[i]);
+                if (from >= x_rows || from < -1) { latch_device_error(err, kDevErrBadIndex, 0x200u); from = -1; }
+            }
+            raw[i] = load_unit<T, VEC>(x + (long long)max(from, 0) * ldx, unit[i] * UNIT, live && from >= 0 ? K : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (it0 + i * step >= items) break;
+            uint32_t byte;
+            const uint2 w = quantize_unit<F>(raw[i], gscale, g, byte);
+            if (row[i] < rows && unit[i] < units) {
+                *reinterpret_cast<uint2*>(codes + row[i] * pitch + (size_t)unit[i] * 8) = w;
+                const int b = unit[i] * UNIT / F::BLK;
+                if (unit[i] * UNIT % F::BLK == 0 && b < nb) scales[(size_t)row[i] * nb + b] = (uint8_t)byte;
+            }
+        }
+    }
+}
+
+// Operand form: the rows of the schedule's tiles, codes [rows][pad64(K) / 2], scales in the tile layout. A block takes
+// one (tile, 512 columns) item at a time: its warps take the rows in turn, the scale bytes meet in shared memory (pieces
+// 528 bytes apart, so that the pieces of one row fall into different banks) and leave as whole pieces.
+template <class F, typename T, bool VEC>
+__global__ void __launch_bounds__(QTHREADS)
+quantize_operand_kernel(const T* __restrict__ x, long long ldx, int x_rows, const int32_t* __restrict__ src,
+                        const int32_t* __restrict__ sched, int G, int max_tiles, int K, const float* __restrict__ gscale,
+                        uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, unsigned* err) {
+    constexpr int U = 4, PIECES = 2 * SF_PIECES<F>, STRIDE = 528;
+    __shared__ __align__(16) uint8_t s_sf[PIECES * STRIDE];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int units = (K + 63) / 64 * 4, kst = (K + SEG_K - 1) / SEG_K;
+    const int nseg = (kst + 1) / 2;
+    const size_t pitch = (size_t)units * 8;
+    pdl_wait();                          // (a programmatic dependent of the kernel that wrote the schedule)
+    pdl_trigger();
+    const float g = gscale ? __ldg(gscale) : 1.f;
+    const bool fits = sched[1] == G && sched[0] <= max_tiles;        // (else: another call's schedule)
+    const int ntiles = fits ? sched[0] : 0;
+    if (!fits && blockIdx.x == 0 && threadIdx.x == 0) latch_device_error(err, kDevErrBadIndex, 0x203u);
+    const int4* tiles = reinterpret_cast<const int4*>(sched + sched_tiles_offset(G));
+    for (long long it = blockIdx.x; it < (long long)ntiles * nseg; it += gridDim.x) {
+        const int t = (int)(it / nseg), seg = (int)(it - (long long)t * nseg);
+        const int4 ent = tiles[t];
+        const int n = ent.z - ent.y, unit = seg * 32 + lane;
+        for (int i = threadIdx.x; i < PIECES * STRIDE / 16; i += QTHREADS)
+            reinterpret_cast<uint4*>(s_sf)[i] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+        for (int r0 = warp; r0 < n; r0 += U * QWARPS) {
+            Raw16<T> raw[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int r = r0 + i * QWARPS;
+                int from = r < n ? ent.y + r : -1;
+                if (from >= 0 && src) {
+                    from = __ldg(src + from);
+                    if (from >= x_rows || from < -1) { latch_device_error(err, kDevErrBadIndex, 0x201u); from = -1; }
+                }
+                raw[i] = load_unit<T, VEC>(x + (long long)max(from, 0) * ldx, unit * UNIT, from >= 0 ? K : 0);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int r = r0 + i * QWARPS;
+                if (r >= n) break;
+                uint32_t byte;
+                const uint2 w = quantize_unit<F>(raw[i], gscale, g, byte);
+                if (unit < units) *reinterpret_cast<uint2*>(codes + (size_t)(ent.y + r) * pitch + (size_t)unit * 8) = w;
+                const int b = lane * UNIT / F::BLK;
+                if (lane * UNIT % F::BLK == 0)
+                    s_sf[(b >> 2) * STRIDE + (r & 31) * 16 + (r >> 5) * 4 + (b & 3)] = (uint8_t)byte;
+            }
+        }
+        __syncthreads();
+        const int np = min(2, kst - 2 * seg) * SF_PIECES<F>;      // pieces of the stages that exist
+        uint4* dst = reinterpret_cast<uint4*>(sf + ((size_t)t * kst + 2 * seg) * SF_BYTES<F>);
+        for (int i = threadIdx.x; i < np * 32; i += QTHREADS)
+            dst[i] = *reinterpret_cast<const uint4*>(s_sf + (i >> 5) * STRIDE + (i & 31) * 16);
+        __syncthreads();
+    }
+}
+
+// Codes and scales -> rows. v = code * scale is exact in fp32 (2 and 4 significant bits); v / g as the rounded quotient:
+// with r the rounded reciprocal of g, q = v r and q + (v - q g) r (the correction of block_codes), or the division
+// itself where the exponents come near the ends of the range.
+template <class F, typename T, bool VEC>
+__global__ void __launch_bounds__(QTHREADS)
+dequantize_rows_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int rows, int K, int lpr,
+                       const float* __restrict__ gscale, T* __restrict__ out, long long ldo) {
+    constexpr int U = 4;
+    __shared__ T s_out[VEC ? 1 : QWARPS][VEC ? 1 : SEG];
+    const int lane = threadIdx.x & 31;
+    const int units = (K + 31) / 32 * 2;
+    const int nseg = (units + lpr - 1) / lpr, rpw = 32 / lpr, sub = lane / lpr;
+    const int nb = (K + F::BLK - 1) / F::BLK;
+    const size_t pitch = (size_t)units * 8;
+    const float g = gscale ? __ldg(gscale) : 1.f, r = __frcp_rn(g);
+    const bool mild = fabsf(g) > 1e-15f && fabsf(g) < 1e15f;
+    const long long items = (long long)((rows + rpw - 1) / rpw) * nseg;
+    const long long step = (long long)gridDim.x * QWARPS;
+    for (long long it0 = (long long)blockIdx.x * QWARPS + (threadIdx.x >> 5); it0 < items; it0 += U * step) {
+        uint2 c[U];
+        uint32_t sb[U];
+        int row[U], unit[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const long long it = it0 + i * step;
+            row[i] = rows;
+            unit[i] = units;
+            if (it < items) {
+                const int rg = (int)(it / nseg);
+                row[i] = rg * rpw + sub;
+                unit[i] = (int)(it - (long long)rg * nseg) * lpr + (lane - sub * lpr);
+            }
+            c[i] = make_uint2(0u, 0u);
+            sb[i] = 0u;
+            if (row[i] < rows && unit[i] < units) {
+                c[i] = __ldcs(reinterpret_cast<const uint2*>(codes + row[i] * pitch + (size_t)unit[i] * 8));
+                const int b = unit[i] * UNIT / F::BLK;
+                if (b < nb) sb[i] = __ldg(scales + (size_t)row[i] * nb + b);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (it0 + i * step >= items) break;
+            const float s = scale_value<F>(sb[i]);
+            const uint32_t w[2] = {c[i].x, c[i].y};
+            Raw16<T> o;
+            T* e = reinterpret_cast<T*>(o.q);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint32_t h2;
+                asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
+                    : "=r"(h2) : "r"((w[j >> 2] >> (8 * (j & 3))) & 0xFFu));
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                float v[2] = {f.x * s, f.y * s};
+                if (gscale) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float a = v[q] * r;
+                        const float d = fmaf(fmaf(-a, g, v[q]), r, a);
+                        v[q] = mild && fabsf(v[q]) > 1e-15f && fabsf(v[q]) < 1e15f ? d : __fdiv_rn(v[q], g);
+                    }
+                }
+                e[2 * j] = rounded<T>(v[0]);
+                e[2 * j + 1] = rounded<T>(v[1]);
+            }
+            const int k0 = unit[i] * UNIT;
+            const bool live = row[i] < rows && k0 < K;
+            T* dst = out + (long long)row[i] * ldo + k0;
+            if (VEC) {
+                if (live && k0 + UNIT <= K) {
+#pragma unroll
+                    for (int q = 0; q < (int)sizeof(T); ++q) __stcs(reinterpret_cast<uint4*>(dst) + q, o.q[q]);
+                } else if (live) {
+#pragma unroll
+                    for (int q = 0; q < UNIT; ++q)
+                        if (k0 + q < K) dst[q] = e[q];
+                }
+            } else if (lpr == 32) {              // one row segment a warp: through shared memory, a column a lane
+                T* box = s_out[threadIdx.x >> 5];
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < UNIT; ++q) box[lane * UNIT + q] = e[q];
+                __syncwarp();
+                const int base = (unit[i] - lane) * UNIT;
+                T* drow = out + (long long)row[i] * ldo + base;
+                for (int q = lane; q < SEG && base + q < K; q += 32) drow[q] = box[q];
+            } else if (live) {
+#pragma unroll
+                for (int q = 0; q < UNIT; ++q)
+                    if (k0 + q < K) dst[q] = e[q];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------
+// weight packing (once per weight)
+// ---------------------------------------------------------------------------------------------------
+// Row p of the packed matrix: row p of `c0`, or with c1 (gate and up) 32 rows of c0, the same 32 of c1, and so on.
+struct PackSrc { const uint8_t *c0, *c1; };
+__device__ __forceinline__ const uint8_t* pack_row(const PackSrc& s, int g, int p, int N, size_t bytes_per_row) {
+    int n = p;
+    const uint8_t* m = s.c0;
+    if (s.c1) {
+        n = (p >> 6) * 32 + (p & 31);
+        m = (p & 32) ? s.c1 : s.c0;
+    }
+    return n < N ? m + ((size_t)g * N + n) * bytes_per_row : nullptr;
+}
+
+// One 16-byte chunk of codes (32 columns) a thread, codes past K cleared.
+__global__ void __launch_bounds__(256)
+pack_codes_kernel(PackSrc src, int N, int K, WeightLayout L, long long chunks, uint8_t* __restrict__ dst) {
+    const size_t pitch = (size_t)(K + 31) / 32 * 16;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < chunks; i += (long long)gridDim.x * blockDim.x) {
+        const int c = (int)(i & 7), r = (int)(i >> 3 & 63);
+        long long q = i >> 9;                    // (group, stage, 64-row block)
+        const int nb = (int)(q % L.NB64);
+        q /= L.NB64;
+        const int st = (int)(q % L.KST), g = (int)(q / L.KST);
+        const int k0 = st * SEG_K + c * 32;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        const uint8_t* row = k0 < K ? pack_row(src, g, nb * 64 + r, N, pitch) : nullptr;
+        if (row) {
+            v = *reinterpret_cast<const uint4*>(row + k0 / 2);
+            uint32_t* w = &v.x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int left = K - (k0 + 8 * j);
+                if (left < 8) w[j] &= left <= 0 ? 0u : (1u << (4 * left)) - 1u;
+            }
+        }
+        *reinterpret_cast<uint4*>(dst + (i >> 9) * 8192 + r * 128 + ((c ^ (r & 7)) << 4)) = v;
+    }
+}
+
+// One scale byte a thread.
+__global__ void __launch_bounds__(256)
+pack_scales_kernel(PackSrc src, int N, int K, int blk, int sfb, WeightLayout L, long long bytes, uint8_t* __restrict__ dst) {
+    const int nblk = (K + blk - 1) / blk;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < bytes; i += (long long)gridDim.x * blockDim.x) {
+        const int at = (int)(i % sfb);
+        long long q = i / sfb;                   // (group, stage, 128-row block)
+        const int nb = (int)(q % L.NB128);
+        q /= L.NB128;
+        const int st = (int)(q % L.KST), g = (int)(q / L.KST);
+        const int r = (at >> 4 & 31) + (at >> 2 & 3) * 32, b = (at >> 9) * 4 + (at & 3) + st * (SEG_K / blk);
+        const uint8_t* row = b < nblk ? pack_row(src, g, nb * 128 + r, N, nblk) : nullptr;
+        dst[i] = row ? row[b] : 0;
+    }
+}
+
+static int pack(PackSrc codes, PackSrc scales, int G, int N, int n_packed, int K, int fmt, void* packed, cudaStream_t s) {
+    const WeightLayout L = weight_layout(G, n_packed, K, fmt);
+    uint8_t* p = static_cast<uint8_t*>(packed);
+    const long long chunks = (long long)L.sf_off / 16, bytes = (long long)(L.total - L.sf_off);
+    pack_codes_kernel<<<(int)std::min<long long>(cdiv(chunks, 256), 16384), 256, 0, s>>>(codes, N, K, L, chunks, p);
+    if (int rc = check_launch("pack_codes_kernel")) return rc;
+    pack_scales_kernel<<<(int)std::min<long long>(cdiv(bytes, 256), 16384), 256, 0, s>>>(scales, N, K, block_of(fmt),
+                                                                                      sf_bytes(fmt), L, bytes, p + L.sf_off);
+    return check_launch("pack_scales_kernel");
+}
+
+// ---------------------------------------------------------------------------------------------------
+// tile schedule of ragged groups
+// ---------------------------------------------------------------------------------------------------
+// offsets [G + 1], rising within [0, rows], G <= 1024: one block scans the groups' tile counts. Offsets that fall or leave
+// the range are latched, and the schedule is then empty.
+__global__ void __launch_bounds__(1024) group_sched_kernel(const int32_t* __restrict__ offsets, int G, int rows,
+                                                           int32_t* __restrict__ sched, unsigned* err) {
+    __shared__ int s_tmp[32];
+    __shared__ int s_bad;
+    const int g = threadIdx.x;
+    if (g == 0) s_bad = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    int lo = 0, hi = 0;
+    if (g < G) {
+        lo = offsets[g];
+        hi = offsets[g + 1];
+        if (lo < 0 || hi < lo || hi > rows) s_bad = 1;
+    }
+    __syncthreads();
+    const bool bad = s_bad != 0;
+    const int nt = bad ? 0 : (int)(((long long)hi - lo + MOE_TILE_M - 1) / MOE_TILE_M);
+    const int incl = block_inclusive_scan(nt, s_tmp);
+    if (g < G) {
+        if (g == 0) { sched[1] = G; sched[kSchedHeader] = 0; }
+        sched[kSchedHeader + g + 1] = incl;
+        if (g == G - 1) sched[0] = incl;
+        int4* tiles = reinterpret_cast<int4*>(sched + sched_tiles_offset(G)) + (incl - nt);
+        for (int t = 0; t < nt; ++t)
+            tiles[t] = make_int4(g, lo + t * MOE_TILE_M, min(lo + (t + 1) * MOE_TILE_M, hi), 0);
+    }
+    if (bad && g == 0) latch_device_error(err, kDevErrBadIndex, 0x202u);
+}
+
+int launch_group_sched(const int32_t* offsets, int G, int rows, int32_t* sched, cudaStream_t s) {
+    return check_launch(launch_pdl(group_sched_kernel, dim3(1), dim3(1024), 0, s, offsets, G, rows, sched,
+                                   device_error_word()), "group_sched_kernel");
+}
+
+// ---------------------------------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------------------------------
+static int el_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
+static bool dtype_ok(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16; }
+static bool vec_ok(const void* p, long long ld, int dtype) { return aligned16(p) && ld * el_bytes(dtype) % 16 == 0; }
+
+// Calls fn<Format, T, VEC>(...) for the run-time format, type and alignment.
+template <typename Fn>
+static int by_kind(int fmt, int dtype, bool vec, Fn fn) {
+    auto typed = [&](auto f) -> int {
+        auto go = [&](auto t) -> int { return vec ? fn(f, t, std::true_type{}) : fn(f, t, std::false_type{}); };
+        if (dtype == MOE_F32) return go(float{});
+        if (dtype == MOE_BF16) return go(__nv_bfloat16{});
+        return go(__half{});
+    };
+    return fmt == MOE_FP4_NV ? typed(Nv{}) : typed(Mx{});
+}
+
+static int lanes_per_row(int K) {
+    const int units = (K + 31) / 32 * 2;
+    int l = 2;
+    while (l < 32 && l < units) l *= 2;
+    return l;
+}
+static int row_grid(int rows, int K, int lpr) {
+    const long long items = (long long)cdiv(rows, 32 / lpr) * cdiv((K + 31) / 32 * 2, lpr);
+    return (int)std::max<long long>(1, std::min<long long>(cdiv(items, QWARPS), (long long)num_sms() * 8));
+}
+
+int launch_quantize_operand(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* sched, int G,
+                            int rows, int K, int dtype, int fmt, const float* gscale, void* codes, void* sf,
+                            cudaStream_t s) {
+    const long long items = (long long)sched_max_tiles(rows, G) * cdiv(stages_of(K), 2);
+    const int grid = (int)std::min<long long>(items, (long long)num_sms() * 6);
+    return by_kind(fmt, dtype, vec_ok(x, ldx, dtype), [&](auto f, auto t, auto v) {
+        using F = decltype(f);
+        using T = decltype(t);
+        return check_launch(launch_pdl(quantize_operand_kernel<F, T, decltype(v)::value>, dim3(grid), dim3(QTHREADS), 0, s,
+                                       static_cast<const T*>(x), ldx, x_rows, src, sched, G, (int)sched_max_tiles(rows, G), K, gscale,
+                                       static_cast<uint8_t*>(codes), static_cast<uint8_t*>(sf), device_error_word()),
+                            "quantize_operand_kernel");
+    });
+}
+
+}  // namespace fp4
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::fp4;
+
+static bool fmt_ok(int fmt) { return fmt == MOE_FP4_NV || fmt == MOE_FP4_MX; }
+
+extern "C" size_t moe_fp4_codes_pitch(int K) { return K < 1 ? 0 : (size_t)(((long long)K + 31) / 32) * 16; }
+extern "C" size_t moe_fp4_scales_pitch(int K, int fmt) {
+    return K < 1 || !fmt_ok(fmt) ? 0 : (size_t)((K + block_of(fmt) - 1) / block_of(fmt));
+}
+
+extern "C" int moe_fp4_quantize(const void* x, long long ldx, int x_rows, const int32_t* src, int rows, int K, int dtype,
+                                int fmt, const float* gscale, void* codes, void* scales, void* stream) {
+    MOE_REQUIRE(dtype_ok(dtype), MOE_ERR_UNSUPPORTED, "moe_fp4_quantize: dtype %d", dtype);
+    MOE_REQUIRE(fmt_ok(fmt), MOE_ERR_UNSUPPORTED, "moe_fp4_quantize: format %d", fmt);
+    MOE_REQUIRE(rows >= 0 && x_rows >= 0 && K >= 1 && K <= MOE_FP4_MAX_K && ldx >= K, MOE_ERR_INVALID_ARG,
+                "moe_fp4_quantize: rows=%d x_rows=%d K=%d ldx=%lld", rows, x_rows, K, ldx);
+    MOE_REQUIRE(src || x_rows >= rows, MOE_ERR_INVALID_ARG, "moe_fp4_quantize: x has %d rows, %d wanted", x_rows, rows);
+    if (rows == 0) return MOE_OK;
+    MOE_REQUIRE((x || x_rows == 0) && codes && scales, MOE_ERR_INVALID_ARG, "moe_fp4_quantize: null pointer");
+    MOE_REQUIRE(aligned16(codes) && reinterpret_cast<uintptr_t>(x) % el_bytes(dtype) == 0, MOE_ERR_INVALID_ARG,
+                "moe_fp4_quantize: codes must be 16-byte aligned, x aligned to its type");
+    const int lpr = lanes_per_row(K), grid = row_grid(rows, K, lpr);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return by_kind(fmt, dtype, vec_ok(x, ldx, dtype), [&](auto f, auto t, auto v) {
+        using T = decltype(t);
+        quantize_rows_kernel<decltype(f), T, decltype(v)::value><<<grid, QTHREADS, 0, s>>>(
+            static_cast<const T*>(x), ldx, x_rows, src, rows, K, lpr, gscale, static_cast<uint8_t*>(codes),
+            static_cast<uint8_t*>(scales), device_error_word());
+        return check_launch("quantize_rows_kernel");
+    });
+}
+
+extern "C" int moe_fp4_dequantize(const void* codes, const void* scales, int rows, int K, int fmt, const float* gscale,
+                                  int dtype, void* out, long long ldo, void* stream) {
+    MOE_REQUIRE(dtype_ok(dtype), MOE_ERR_UNSUPPORTED, "moe_fp4_dequantize: dtype %d", dtype);
+    MOE_REQUIRE(fmt_ok(fmt), MOE_ERR_UNSUPPORTED, "moe_fp4_dequantize: format %d", fmt);
+    MOE_REQUIRE(rows >= 0 && K >= 1 && K <= MOE_FP4_MAX_K && ldo >= K, MOE_ERR_INVALID_ARG,
+                "moe_fp4_dequantize: rows=%d K=%d ldo=%lld", rows, K, ldo);
+    if (rows == 0) return MOE_OK;
+    MOE_REQUIRE(codes && scales && out, MOE_ERR_INVALID_ARG, "moe_fp4_dequantize: null pointer");
+    MOE_REQUIRE(aligned16(codes) && reinterpret_cast<uintptr_t>(out) % el_bytes(dtype) == 0, MOE_ERR_INVALID_ARG,
+                "moe_fp4_dequantize: codes must be 16-byte aligned, out aligned to its type");
+    const int lpr = lanes_per_row(K), grid = row_grid(rows, K, lpr);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return by_kind(fmt, dtype, vec_ok(out, ldo, dtype), [&](auto f, auto t, auto v) {
+        using T = decltype(t);
+        dequantize_rows_kernel<decltype(f), T, decltype(v)::value><<<grid, QTHREADS, 0, s>>>(
+            static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), rows, K, lpr, gscale,
+            static_cast<T*>(out), ldo);
+        return check_launch("dequantize_rows_kernel");
+    });
+}
+
+// G * N * K in packed bytes stays far below what a 64-bit size holds; the kernels' row indices are 32-bit.
+static int check_weight(const char* who, int G, int N, int K, int fmt) {
+    MOE_REQUIRE(fmt_ok(fmt), MOE_ERR_UNSUPPORTED, "%s: format %d", who, fmt);
+    MOE_REQUIRE(G >= 1 && G <= 1024 && N >= 1 && N <= MOE_FP4_MAX_K && K >= 1 && K <= MOE_FP4_MAX_K, MOE_ERR_INVALID_ARG,
+                "%s: groups=%d N=%d K=%d", who, G, N, K);
+    return MOE_OK;
+}
+
+extern "C" size_t moe_fp4_packed_weight_bytes(int G, int N, int K, int fmt) {
+    return check_weight("moe_fp4_packed_weight_bytes", G, N, K, fmt) ? 0 : weight_layout(G, N, K, fmt).total;
+}
+
+extern "C" int moe_fp4_pack_weight(const void* codes, const void* scales, int G, int N, int K, int fmt, void* packed,
+                                   void* stream) {
+    if (int rc = check_weight("moe_fp4_pack_weight", G, N, K, fmt)) return rc;
+    MOE_REQUIRE(codes && scales && packed && aligned16(codes) && aligned16(packed), MOE_ERR_INVALID_ARG,
+                "moe_fp4_pack_weight: pointers must be non-null, codes and packed 16-byte aligned");
+    return pack(PackSrc{static_cast<const uint8_t*>(codes), nullptr}, PackSrc{static_cast<const uint8_t*>(scales), nullptr},
+                G, N, N, K, fmt, packed, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t moe_fp4_packed_expert_weights_bytes(int E, int h, int F, int fmt) {
+    if (check_weight("moe_fp4_packed_expert_weights_bytes", E, h, F, fmt)) return 0;
+    return expert_layout(E, h, F, fmt).total;
+}
+
+extern "C" int moe_fp4_pack_expert_weights(const void* gate_codes, const void* gate_scales, const void* up_codes,
+                                           const void* up_scales, const void* down_codes, const void* down_scales, int E,
+                                           int h, int F, int fmt, void* packed, void* stream) {
+    if (int rc = check_weight("moe_fp4_pack_expert_weights", E, h, F, fmt)) return rc;
+    MOE_REQUIRE(gate_codes && gate_scales && up_codes && up_scales && down_codes && down_scales && packed,
+                MOE_ERR_INVALID_ARG, "moe_fp4_pack_expert_weights: null pointer");
+    MOE_REQUIRE(aligned16(gate_codes) && aligned16(up_codes) && aligned16(down_codes) && aligned16(packed),
+                MOE_ERR_INVALID_ARG, "moe_fp4_pack_expert_weights: codes and packed must be 16-byte aligned");
+    const ExpertLayout L = expert_layout(E, h, F, fmt);
+    auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (int rc = pack(PackSrc{u8(gate_codes), u8(up_codes)}, PackSrc{u8(gate_scales), u8(up_scales)}, E, F, 2 * pad64(F), h,
+                      fmt, packed, s))
+        return rc;
+    return pack(PackSrc{u8(down_codes), nullptr}, PackSrc{u8(down_scales), nullptr}, E, h, h, F, fmt,
+                static_cast<uint8_t*>(packed) + L.down_off, s);
+}

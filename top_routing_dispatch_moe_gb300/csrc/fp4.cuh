@@ -1,0 +1,162 @@
+// Block-scaled 4-bit floating point (e2m1): formats, layouts and the arithmetic shared by the quantisation
+// kernels and the product's epilogue.
+//
+// A value is code * scale of its block. e2m1 codes (sign, 2 exponent bits, 1 mantissa bit) stand for 0, 0.5, 1, 1.5,
+// 2, 3, 4, 6; two codes to a byte, the even column in the low half.
+//   MOE_FP4_NV: blocks of 16 columns, scale s = e4m3(amax / 6), held below 448 (rounded to nearest even);
+//   MOE_FP4_MX: blocks of 32 columns, scale s = 2^(floor(log2 amax) - 2), stored as the exponent + 127.
+#pragma once
+
+#include <cuda_fp16.h>
+#include "common.cuh"
+
+namespace moe {
+namespace fp4 {
+
+constexpr int SEG_K = 256;           // columns of a shared-memory stage of the product: 128 bytes of codes a row
+
+struct Nv { static constexpr int ID = MOE_FP4_NV, BLK = 16; };
+struct Mx { static constexpr int ID = MOE_FP4_MX, BLK = 32; };
+
+// Bytes of block scales of 128 rows x SEG_K columns, in the tile layout: 512-byte pieces of 128 rows x 4 blocks,
+// block b of row r of a piece at byte (r % 32) * 16 + (r / 32) * 4 + b: the order in which a piece lands in tensor
+// memory as the scale operand of the block-scaled tcgen05.mma (lane r % 32, column r / 32, byte b).
+template <class F> constexpr int SF_PIECES = SEG_K / F::BLK / 4;
+template <class F> constexpr int SF_BYTES = SF_PIECES<F> * 512;
+__host__ __device__ constexpr int sf_bytes(int fmt) { return fmt == MOE_FP4_NV ? 2048 : 1024; }
+__host__ __device__ constexpr int block_of(int fmt) { return fmt == MOE_FP4_NV ? 16 : 32; }
+
+inline int pad64(int k) { return (k + 63) / 64 * 64; }
+inline int stages_of(int k) { return (k + SEG_K - 1) / SEG_K; }
+
+// A packed weight [G][N][K]: codes [G][stage][N / 64 padded to pairs][64 rows x 128 bytes, the 16-byte chunk c of row r
+// at chunk c ^ (r % 8): a K-major operand tile with 128-byte swizzling], zero past N and K; then, from the next
+// 256-byte boundary, scales [G][stage][N / 128][SF_BYTES] in the tile layout. A stage's codes of any run of 64-row
+// blocks are contiguous, and so are its scales: the product fetches each with one bulk copy.
+struct WeightLayout {
+    int NB64, NB128, KST;
+    size_t sf_off, total;
+};
+inline WeightLayout weight_layout(int G, int N, int K, int fmt) {
+    WeightLayout L;
+    L.NB128 = (N + 127) / 128;
+    L.NB64 = 2 * L.NB128;
+    L.KST = stages_of(K);
+    L.sf_off = (size_t)G * L.KST * L.NB64 * 8192;
+    L.total = L.sf_off + (size_t)G * L.KST * L.NB128 * sf_bytes(fmt);
+    return L;
+}
+
+// The expert FFN's packed weight: the gate/up matrix (N = 2 pad64(F): 32 gate rows, then the 32 up rows of the same f,
+// and so on; K = h) and the down matrix (N = h, K = F) from the next 256-byte boundary.
+struct ExpertLayout { WeightLayout gu, down; size_t down_off, total; };
+inline ExpertLayout expert_layout(int E, int h, int F, int fmt) {
+    ExpertLayout L;
+    L.gu = weight_layout(E, 2 * pad64(F), h, fmt);
+    L.down = weight_layout(E, h, F, fmt);
+    L.down_off = align_up(L.gu.total, 256);
+    L.total = L.down_off + L.down.total;
+    return L;
+}
+
+// A quantised row operand of the product: codes [rows][pad64(K) / 2] and scales [tile of the schedule][stage][SF_BYTES].
+inline size_t operand_codes_bytes(long long rows, int K) { return align_up((size_t)rows * (pad64(K) / 2), 1024); }
+inline size_t operand_sf_bytes(long long rows, int G, int K, int fmt) {
+    return align_up(sched_max_tiles(rows, G) * stages_of(K) * sf_bytes(fmt), 1024);
+}
+
+#ifdef __CUDACC__
+// NaN if either is: a NaN has to reach its block's scale.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// Eight values -> eight codes, to nearest, ties to even, held at +-6.
+__device__ __forceinline__ uint32_t e2m1x8(const float* v) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+__device__ __forceinline__ float e4m3_value(uint32_t byte) {
+    uint32_t h2;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h2) : "r"(byte));
+    return __low2float(*reinterpret_cast<const __half2*>(&h2));
+}
+__device__ __forceinline__ uint32_t e4m3_byte(float v) {           // v >= 0 or NaN, held at 448
+    uint32_t r;
+    asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(r) : "f"(v), "f"(0.f));
+    return r & 0xFFu;
+}
+
+// The scale byte of a block whose largest magnitude is `amax` (NaN if one of its values is), the scale itself and its
+// reciprocal (0 where the scale is 0 or NaN).
+template <class F>
+__device__ __forceinline__ uint32_t block_scale(float amax, float& s, float& r) {
+    if constexpr (F::ID == MOE_FP4_NV) {
+        const uint32_t b = e4m3_byte(__fdiv_rn(amax, 6.f));
+        s = e4m3_value(b);
+        r = s > 0.f ? __frcp_rn(s) : 0.f;
+        return b;
+    } else {
+        if (amax != amax) { s = amax; r = 0.f; return 255u; }
+        const int f = max((int)(__float_as_uint(amax) >> 23) - 2, 0);   // (inf: 253, its block ends at +-6 * 2^126)
+        s = f ? __uint_as_float((uint32_t)f << 23) : __uint_as_float(1u << 22);
+        r = f < 254 ? __uint_as_float((uint32_t)(254 - f) << 23) : __uint_as_float(1u << 22);
+        return (uint32_t)f;
+    }
+}
+
+// BLK values of one block -> codes, as the correctly rounded quotient v / s rounded to e2m1, so that a quotient half
+// way between two codes is one here too. MX: s is a power of two and v * r exact. NV: q = v r is off by less than two
+// units in its last place; with r the rounded reciprocal, q + (v - q s) r is the rounded quotient (Markstein's
+// correction, as r has no error beyond its own rounding and v - q s is exact in one fused step). Past 1e30 the products
+// could overflow: such a block is one whose scale is at its ceiling, and its values are cut to 1e30 first (they end at
+// +-6 either way).
+template <class F>
+__device__ __forceinline__ void block_codes(float* v, float amax, float s, float r, uint32_t* w) {
+    if constexpr (F::ID == MOE_FP4_NV) {
+        if (amax > 1e30f) {
+#pragma unroll
+            for (int i = 0; i < F::BLK; ++i) v[i] = fminf(fmaxf(v[i], -1e30f), 1e30f);
+        }
+#pragma unroll
+        for (int i = 0; i < F::BLK; ++i) {
+            const float q = v[i] * r;
+            v[i] = fmaf(fmaf(-q, s, v[i]), r, q);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < F::BLK; ++i) v[i] *= r;
+    }
+    if (amax != amax) {
+#pragma unroll
+        for (int i = 0; i < F::BLK / 8; ++i) w[i] = 0u;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < F::BLK / 8; ++i) w[i] = e2m1x8(v + 8 * i);
+}
+
+template <class F>
+__device__ __forceinline__ float scale_value(uint32_t b) {
+    if constexpr (F::ID == MOE_FP4_NV) return e4m3_value(b);
+    return b == 255u ? __uint_as_float(0x7FC00000u) : b ? __uint_as_float(b << 23) : __uint_as_float(1u << 22);
+}
+#endif
+
+// Launches shared between the two files.
+int launch_group_sched(const int32_t* offsets, int G, int rows, int32_t* sched, cudaStream_t s);
+int launch_quantize_operand(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* sched, int G,
+                            int rows, int K, int dtype, int fmt, const float* gscale, void* codes, void* sf,
+                            cudaStream_t s);
+
+}  // namespace fp4
+}  // namespace moe

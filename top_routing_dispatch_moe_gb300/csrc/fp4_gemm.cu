@@ -1,0 +1,554 @@
+// Grouped products of block-scaled e2m1 operands on the 5th-generation tensor cores, and the SwiGLU expert FFN made of two.
+//
+//   y[r] = alpha[g] * sum_k A[r, k] W[g, n, k]     for the rows r of group g,
+// A and W codes times their block scales, accumulated in fp32 in tensor memory by tcgen05.mma with block scaling
+// (kind::mxf4nvf4, 16-column blocks with e4m3 scales, and kind::mxf4, 32-column blocks with powers of two; K = 64 an
+// instruction).
+//
+// One persistent CTA per SM with ten warps:
+//   warp 0     producer: per stage of 256 columns a 128-row tile of codes of A by TMA (boxes of 32 rows where the tile has
+//              fewer rows), BN weight rows, and both operands' block scales, each one bulk copy of contiguous packed bytes;
+//   warp 1     per stage: tcgen05.cp of the scale pieces into tensor memory, then the MMAs, from one thread;
+//   warps 2-9  epilogue, two warps to a quarter of the tensor memory lanes, taking 64-column chunks in turn: either
+//              silu(gate) * up requantised to the next product's operand, or alpha times the accumulator in the output type.
+// Two accumulators: the epilogue of one tile runs under the MMAs of the next.
+//
+// Every wait is bounded, as in the bf16 grouped GEMM: one that runs out latches MOE_ERR_TIMEOUT, every role leaves, the
+// copies and MMAs in flight are waited for and the tensor memory is freed.
+#include <cudaTypedefs.h>
+#include <algorithm>
+#include "fp4.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace fp4 {
+using namespace moe::tc;
+
+constexpr int BM = 128;
+constexpr int A_BYTES = BM * SEG_K / 2;          // 16 KB of codes
+constexpr int THREADS = 320;
+constexpr int EPI_WARPS = 8;
+constexpr int TMEM_COLS = 512;
+
+enum Epi : int { EPI_OUT = 0, EPI_SWIGLU = 1 };
+
+template <int BN_, int STAGES_>
+struct Cfg {
+    static constexpr int BN = BN_, STAGES = STAGES_;
+    static constexpr int B_BYTES = BN * SEG_K / 2;
+    static constexpr int SF_BLOCKS = (BN + 127) / 128;               // 128-row scale tiles a weight tile touches
+    template <class F> static constexpr int SFS = (1 + SF_BLOCKS) * SF_BYTES<F>;   // scale bytes of a stage
+    template <class F> static constexpr int SMEM = 1024 + STAGES * (A_BYTES + B_BYTES + SFS<F>) + 256;
+    static constexpr int ACC_COLS = BN == 192 ? 192 : BN;            // columns of one accumulator
+    static constexpr int SF_COL = 2 * ACC_COLS;                      // scale columns follow the two accumulators
+    static_assert(2 * ACC_COLS + 48 <= TMEM_COLS, "tensor memory columns");
+};
+
+struct Params {
+    const int32_t* sched;
+    int G, max_tiles;            // what the schedule has to agree with
+    const uint8_t *a_sf, *w, *w_sf;
+    int steps, kst;              // 64-column MMA steps, 256-column stages
+    int NT, NB64, NB128;         // n-tiles; 64-row and 128-row blocks of the packed weight
+    int N, ldo;                  // EPI_OUT: columns and row stride of the output
+    int out_dtype;
+    void* out;
+    const float *alpha, *alpha_up;   // per group, or null (1)
+    const float* act_gscale;     // EPI_SWIGLU: multiplier of act before it is quantised, or null
+    uint8_t *act_codes, *act_sf;
+    int act_pitch, act_kst;
+    unsigned* err;
+    long long wait_limit;
+};
+
+struct Work { int g, tile, row0, row1, n; };
+
+// Item w: group by group, n-tile next, m-tile fastest: CTAs that run together share a weight tile.
+__device__ __forceinline__ Work map_work(const int32_t* sched, int G, int NT, int w) {
+    const int32_t* prefix = sched + kSchedHeader;
+    int lo = 0, hi = G;
+    while (lo < hi) {                    // last g with prefix[g] * NT <= w
+        const int mid = (lo + hi + 1) >> 1;
+        if ((long long)prefix[mid] * NT <= w) lo = mid; else hi = mid - 1;
+    }
+    const int p0 = prefix[lo], mt = prefix[lo + 1] - p0, local = w - p0 * NT;
+    const int n = local / mt, t = p0 + local % mt;
+    const int4 e = reinterpret_cast<const int4*>(sched + sched_tiles_offset(G))[t];
+    return Work{e.x, t, e.y, e.z, n};
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+// 32 rows of 16 bytes (8-row groups 128 bytes apart) -> the same 4 columns of each quarter of the lanes.
+__device__ __forceinline__ void sf_to_tmem(uint32_t taddr, uint32_t saddr) {
+    const uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1 << 46;
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+template <class F>
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                           uint32_t accumulate) {
+    if constexpr (F::ID == MOE_FP4_NV)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb) : "memory");
+}
+// Instruction descriptor of the block-scaled kinds: A and B e2m1 (bits 7-9 and 10-12 = 1), both K-major, N >> 3 at bits
+// 17-22, scale type at bit 23 (0: e4m3, 1: power of two), M >> 4 at bits 24-28, K = 64 (bit 31 = 0). Bits 4-5 and 29-30:
+// which byte of a scale word is the step's first (0, and 2 for the second 64 columns of an MX piece).
+template <class F, int M, int N>
+__device__ constexpr uint32_t idesc_scaled(int sub) {
+    return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((F::ID == MOE_FP4_MX ? 1u : 0u) << 23) |
+           ((uint32_t)(M >> 4) << 24) | ((uint32_t)(2 * sub) << 4) | ((uint32_t)(2 * sub) << 29);
+}
+
+// 32 consecutive columns of an output row in its type; whole 16-byte vectors where the row allows them.
+template <typename T>
+__device__ __forceinline__ void store_row(T* dst, const float* v, int n, bool vec) {
+    constexpr int PER = 16 / sizeof(T);
+#pragma unroll
+    for (int c = 0; c < 32; c += PER) {
+        alignas(16) T o[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if constexpr (sizeof(T) == 4) o[i] = v[c + i];
+            else if constexpr (std::is_same<T, __half>::value) o[i] = __float2half_rn(v[c + i]);
+            else o[i] = __float2bfloat16_rn(v[c + i]);
+        }
+        if (vec && c + PER <= n) {
+            *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(o);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (c + i < n) dst[c + i] = o[i];
+        }
+    }
+}
+
+// Chunk `q` (64 accumulator columns) of a tile, this thread's row `row` (live: one of the tile's rows).
+template <class F, int EPI>
+__device__ __forceinline__ void epilogue_chunk(const Params& p, const Work& wk, uint32_t tcol, int c0, int r, bool live) {
+    const int row = wk.row0 + r;
+    if constexpr (EPI == EPI_SWIGLU) {
+        float g[32], u[32];
+        tmem_ld32(tcol, g);
+        tmem_ld32(tcol + 32, u);
+        if (!live) return;
+        const float ag = p.alpha ? __ldg(p.alpha + wk.g) : 1.f, au = p.alpha_up ? __ldg(p.alpha_up + wk.g) : 1.f;
+        const float gs = p.act_gscale ? __ldg(p.act_gscale) : 1.f;
+        const int f0 = c0 / 2;                   // first column of act
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float gv = g[i] * ag;
+            u[i] = gv / (1.f + __expf(-gv)) * (u[i] * au) * gs;
+        }
+        uint32_t w[4], bytes = 0u;
+#pragma unroll
+        for (int b = 0; b < 32 / F::BLK; ++b) {
+            float amax = 0.f, s, rc;
+#pragma unroll
+            for (int i = 0; i < F::BLK; ++i) amax = max_nan(amax, fabsf(u[b * F::BLK + i]));
+            bytes |= block_scale<F>(amax, s, rc) << (8 * b);
+            block_codes<F>(u + b * F::BLK, amax, s, rc, w + b * (F::BLK / 8));
+        }
+        *reinterpret_cast<uint4*>(p.act_codes + (size_t)row * p.act_pitch + f0 / 2) = make_uint4(w[0], w[1], w[2], w[3]);
+        const int b0 = f0 / F::BLK;
+        uint8_t* sf = p.act_sf + (size_t)wk.tile * p.act_kst * SF_BYTES<F> + (size_t)(b0 >> 2) * 512 + (r & 31) * 16 +
+                      (r >> 5) * 4 + (b0 & 3);
+        if constexpr (F::ID == MOE_FP4_NV) *reinterpret_cast<uint16_t*>(sf) = (uint16_t)bytes;
+        else *sf = (uint8_t)bytes;
+    } else {
+        const float al = p.alpha ? __ldg(p.alpha + wk.g) : 1.f;
+        const int el = p.out_dtype == MOE_F32 ? 4 : 2;
+        uint8_t* dst = static_cast<uint8_t*>(p.out) + ((size_t)row * p.ldo + c0) * el;
+        const bool vec = ((reinterpret_cast<uintptr_t>(p.out) | (size_t)p.ldo * el) & 15u) == 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[32];
+            tmem_ld32(tcol + 32 * h, v);
+            const int n = p.N - c0 - 32 * h;
+            if (!live || n <= 0) continue;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= al;
+            if (p.out_dtype == MOE_F32) store_row(reinterpret_cast<float*>(dst) + 32 * h, v, n, vec);
+            else if (p.out_dtype == MOE_BF16) store_row(reinterpret_cast<__nv_bfloat16*>(dst) + 32 * h, v, n, vec);
+            else store_row(reinterpret_cast<__half*>(dst) + 32 * h, v, n, vec);
+        }
+    }
+}
+
+template <class F, class C, int EPI>
+__global__ void __launch_bounds__(THREADS, 1)
+fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32, Params p) {
+    constexpr int BN = C::BN, STAGES = C::STAGES, B_BYTES = C::B_BYTES, SFS = C::template SFS<F>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sA = smem_u32(smem), sB = sA + STAGES * A_BYTES, sS = sB + STAGES * B_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * (A_BYTES + B_BYTES + SFS));
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto tfull = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+    auto tempty = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+    const uint32_t mma_done = bar0 + 8u * (2 * STAGES + 4);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
+        for (int a = 0; a < 2; ++a) { mbar_init(tfull(a), 1); mbar_init(tempty(a), EPI_WARPS); }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmA32);
+    }
+    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // (a programmatic dependent: the schedule and the operands are read only from here on)
+    pdl_wait();
+    pdl_trigger();
+    const int G = p.G, ntiles = p.sched[0];
+    const bool fits = p.sched[1] == G && ntiles <= p.max_tiles;      // (else: another call's schedule)
+    const int total = fits ? ntiles * p.NT : 0;
+    if (!fits && blockIdx.x == 0 && threadIdx.x == 0) latch_device_error(p.err, kDevErrBadIndex, 0x203u);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, last_par = 0;
+            for (int w = blockIdx.x; w < total && !*abort_flag; w += gridDim.x) {
+                const Work wk = map_work(p.sched, G, p.NT, w);
+                const int boxes = (wk.row1 - wk.row0 + 31) >> 5;
+                const int nb = min(BN / 64, p.NB64 - wk.n * (BN / 64));
+                const int t0 = wk.n * BN / 128, nt = min((wk.n * BN + BN + 127) / 128, p.NB128) - t0;
+                const uint8_t* w0 = p.w + (size_t)wk.g * p.kst * p.NB64 * 8192 + (size_t)wk.n * (BN / 64) * 8192;
+                const uint8_t* s0 = p.w_sf + ((size_t)wk.g * p.kst * p.NB128 + t0) * SF_BYTES<F>;
+                const uint8_t* a0 = p.a_sf + (size_t)wk.tile * p.kst * SF_BYTES<F>;
+                const uint32_t tx = (uint32_t)(boxes * 4096 + nb * 8192 + (1 + nt) * SF_BYTES<F>);
+                bool ok = true;
+                for (int kb = 0; kb < p.kst; ++kb) {
+                    if (!wait_phase(empty(stage), phase ^ 1u, p.wait_limit, abort_flag, p.err, 0x210u)) { ok = false; break; }
+                    const uint32_t f = full(stage), sf = sS + stage * SFS;
+                    mbar_expect_tx(f, tx);
+                    bulk_load(sB + stage * B_BYTES, w0 + (size_t)kb * p.NB64 * 8192, nb * 8192, f);
+                    if (boxes == 4) tma_load_2d(sA + stage * A_BYTES, &tmA, kb * (SEG_K / 2), wk.row0, f);
+                    else
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d(sA + stage * A_BYTES + b * 4096, &tmA32, kb * (SEG_K / 2), wk.row0 + 32 * b, f);
+                    bulk_load(sf, a0 + (size_t)kb * SF_BYTES<F>, SF_BYTES<F>, f);
+                    bulk_load(sf + SF_BYTES<F>, s0 + (size_t)kb * p.NB128 * SF_BYTES<F>, nt * SF_BYTES<F>, f);
+                    issued |= 1u << stage;
+                    last_par = (last_par & ~(1u << stage)) | (phase << stage);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+            }
+            for (int s = 0; s < STAGES; ++s)        // every issued copy has landed before the CTA exits
+                if (issued & (1u << s)) drain_phase(full(s), (last_par >> s) & 1u, p.err, 0x211u);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr int PIECES = SF_PIECES<F>, BC = C::SF_BLOCKS * 4;
+            int stage = 0, iter = 0;
+            uint32_t phase = 0;
+            for (int w = blockIdx.x; w < total && !*abort_flag; w += gridDim.x, ++iter) {
+                const int a = iter & 1;
+                if (!wait_phase(tempty(a), ((iter >> 1) & 1) ^ 1u, p.wait_limit, abort_flag, p.err, 0x220u)) break;
+                tc_fence_after();
+                const Work wk = map_work(p.sched, G, p.NT, w);
+                const uint32_t d = tmem + a * C::ACC_COLS, sfa = tmem + C::SF_COL, sfb = sfa + PIECES * 4;
+                const uint32_t shift = (wk.n * BN & 64) ? 2u : 0u;   // a tile that starts in the middle of a scale tile
+                bool ok = true;
+                for (int kb = 0; kb < p.kst; ++kb) {
+                    if (!wait_phase(full(stage), phase, p.wait_limit, abort_flag, p.err, 0x221u)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t a_s = sA + stage * A_BYTES, b_s = sB + stage * B_BYTES, s_s = sS + stage * SFS;
+                    // the scales of all pieces, then the steps: copies and MMAs of one thread run in order
+#pragma unroll
+                    for (int q = 0; q < PIECES; ++q) {
+                        sf_to_tmem(sfa + 4 * q, s_s + q * 512);
+#pragma unroll
+                        for (int t = 0; t < C::SF_BLOCKS; ++t)
+                            sf_to_tmem(sfb + q * BC + 4 * t, s_s + (1 + t) * SF_BYTES<F> + q * 512);
+                    }
+                    const int n = min(4, p.steps - 4 * kb);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k >= n) break;
+                        const int q = F::ID == MOE_FP4_NV ? k : k / 2;
+                        const uint32_t id = idesc_scaled<F, BM, BN>(F::ID == MOE_FP4_NV ? 0 : k & 1);
+                        mma_scaled<F>(d, sw128_desc(a_s + 32 * k), sw128_desc(b_s + 32 * k), id, sfa + 4 * q,
+                                      sfb + q * BC + shift, (kb | k) != 0);
+                    }
+                    umma_commit(empty(stage));
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                umma_commit(tfull(a));
+            }
+            umma_commit(mma_done);                  // all MMAs finished before the columns are freed
+            drain_phase(mma_done, 0, p.err, 0x222u);
+        }
+    } else {
+        const int quarter = 32 * (warp & 3), half = (warp - 2) >> 2, r = quarter + lane;
+        int iter = 0;
+        for (int w = blockIdx.x; w < total; w += gridDim.x, ++iter) {
+            const int a = iter & 1;
+            if (!wait_phase(tfull(a), (iter >> 1) & 1, p.wait_limit, abort_flag, p.err, 0x230u)) break;
+            tc_fence_after();
+            const Work wk = map_work(p.sched, G, p.NT, w);
+            const uint32_t tbase = tmem + a * C::ACC_COLS + ((uint32_t)quarter << 16);
+            if (wk.row0 + quarter < wk.row1) {
+                const int nb = min(BN / 64, p.NB64 - wk.n * (BN / 64));
+#pragma unroll 1
+                for (int q = (half + iter) & 1; q < nb; q += 2)
+                    epilogue_chunk<F, EPI>(p, wk, tbase + 64 * q, wk.n * BN + 64 * q, r, wk.row0 + r < wk.row1);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty(a));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------------------------------
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// Codes [rows][pitch bytes], boxes of box_rows x 128 bytes with 128-byte swizzling; zero past the pitch and the rows.
+static int codes_map(CUtensorMap* m, const void* base, long long rows, int pitch, int box_rows) {
+    auto fn = encode_fn();
+    MOE_REQUIRE(fn, MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable from the driver");
+    cuuint64_t dims[2] = {(cuuint64_t)pitch, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    MOE_REQUIRE(r == CUDA_SUCCESS, MOE_ERR_CUDA, "cuTensorMapEncodeTiled (codes) failed (%d) rows=%lld pitch=%d", (int)r,
+                rows, pitch);
+    return MOE_OK;
+}
+
+template <class F, class C, int EPI>
+static int launch(const void* a_codes, long long rows, int K, Params p, cudaStream_t s) {
+    constexpr int smem = C::template SMEM<F>;
+    static_assert(smem <= 227 * 1024, "shared memory per CTA");
+    static unsigned long long attr_ctx[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return set_error(MOE_ERR_CUDA, "fp4 product: no usable current device");
+    const unsigned long long ctx = context_id();
+    if (ctx == 0 || attr_ctx[dev] != ctx) {
+        const cudaError_t e = cudaFuncSetAttribute(fp4_gemm_kernel<F, C, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "fp4 product smem attribute: %s", cudaGetErrorString(e));
+        attr_ctx[dev] = context_id();
+    }
+    CUtensorMap m, m32;
+    const int pitch = pad64(K) / 2;
+    if (int rc = codes_map(&m, a_codes, rows, pitch, BM)) return rc;
+    if (int rc = codes_map(&m32, a_codes, rows, pitch, 32)) return rc;
+    p.NT = cdiv(p.NB64, C::BN / 64);
+    return check_launch(launch_pdl(fp4_gemm_kernel<F, C, EPI>, dim3(num_sms()), dim3(THREADS), smem, s, m, m32, p),
+                        EPI == EPI_SWIGLU ? "fp4_gemm_kernel<swiglu>" : "fp4_gemm_kernel");
+}
+
+using Wide = Cfg<192, 4>;
+using Mid = Cfg<128, 5>;
+using Narrow = Cfg<64, 6>;
+
+// The tile's width by the work there is: narrow tiles spread a few rows' weights over all SMs, wide ones do the most
+// products per operand byte.
+template <class F, int EPI>
+static int product(const void* a_codes, long long rows, int G, int K, const Params& p, cudaStream_t s) {
+    const long long tiles = std::min<long long>(rows, G) + rows / BM;      // about this many m-tiles
+    if (tiles * cdiv(p.NB64, 3) >= 2LL * num_sms()) return launch<F, Wide, EPI>(a_codes, rows, K, p, s);
+    if (tiles * cdiv(p.NB64, 2) >= 2LL * num_sms()) return launch<F, Mid, EPI>(a_codes, rows, K, p, s);
+    return launch<F, Narrow, EPI>(a_codes, rows, K, p, s);
+}
+
+static Params params_for(const int32_t* sched, int G, int rows, const void* a_sf, const void* packed, const WeightLayout& L,
+                         int K) {
+    Params p{};
+    p.sched = sched;
+    p.G = G;
+    p.max_tiles = (int)sched_max_tiles(rows, G);
+    p.a_sf = static_cast<const uint8_t*>(a_sf);
+    p.w = static_cast<const uint8_t*>(packed);
+    p.w_sf = p.w + L.sf_off;
+    p.steps = (K + 63) / 64;
+    p.kst = L.KST;
+    p.NB64 = L.NB64;
+    p.NB128 = L.NB128;
+    p.err = device_error_word();
+    p.wait_limit = wait_limit();
+    return p;
+}
+
+// Workspace: the schedule of the groups (when the caller has none), then each operand's codes and scales.
+struct LinearWs { size_t sched, codes, sf, total; };
+static LinearWs linear_ws(int G, int K, int rows, int fmt) {
+    LinearWs w;
+    w.sched = 0;
+    w.codes = align_up(sched_words(rows, G) * sizeof(int32_t), 1024);
+    w.sf = w.codes + operand_codes_bytes(rows, K);
+    w.total = w.sf + operand_sf_bytes(rows, G, K, fmt);
+    return w;
+}
+struct FfnWs { LinearWs x; size_t act_codes, act_sf, total; };
+static FfnWs ffn_ws(int E, int h, int F, int rows, int fmt) {
+    FfnWs w;
+    w.x = linear_ws(E, h, rows, fmt);
+    w.act_codes = w.x.total;
+    w.act_sf = w.act_codes + operand_codes_bytes(rows, F);
+    w.total = w.act_sf + operand_sf_bytes(rows, E, F, fmt);
+    return w;
+}
+
+}  // namespace fp4
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::fp4;
+
+static bool fp4_dtype_ok(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16; }
+static int fp4_el(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
+
+// The checks that the product and the FFN share. K: x's columns, N: the output's.
+static int check_call(const char* who, const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* offsets,
+                      const int32_t* tile_sched, const void* packed, int G, int N, int K, int rows, int fmt, int dtype,
+                      const void* out, long long ldo, int out_dtype, const void* ws) {
+    MOE_REQUIRE(fp4_dtype_ok(dtype) && fp4_dtype_ok(out_dtype), MOE_ERR_UNSUPPORTED, "%s: dtype %d, out_dtype %d", who, dtype,
+                out_dtype);
+    MOE_REQUIRE(fmt == MOE_FP4_NV || fmt == MOE_FP4_MX, MOE_ERR_UNSUPPORTED, "%s: format %d", who, fmt);
+    MOE_REQUIRE(G >= 1 && G <= 1024 && N >= 1 && N <= MOE_FP4_MAX_K && K >= 1 && K <= MOE_FP4_MAX_K && rows >= 0 &&
+                    rows <= MOE_FP4_MAX_ROWS && x_rows >= 0,
+                MOE_ERR_INVALID_ARG, "%s: groups=%d N=%d K=%d rows=%d x_rows=%d", who, G, N, K, rows, x_rows);
+    MOE_REQUIRE(ldx >= K && ldo >= N && ldo <= 0x7FFFFFFFLL, MOE_ERR_INVALID_ARG, "%s: ldx=%lld ldo=%lld", who, ldx, ldo);
+    MOE_REQUIRE(src || x_rows >= rows, MOE_ERR_INVALID_ARG, "%s: x has %d rows, %d wanted", who, x_rows, rows);
+    MOE_REQUIRE((offsets != nullptr) != (tile_sched != nullptr), MOE_ERR_INVALID_ARG,
+                "%s: offsets or tile_sched, one of the two", who);
+    if (rows == 0) return MOE_OK;
+    MOE_REQUIRE((x || x_rows == 0) && packed && out && ws, MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+    MOE_REQUIRE(aligned16(packed) && (!tile_sched || aligned16(tile_sched)) &&
+                    (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 && reinterpret_cast<uintptr_t>(x) % fp4_el(dtype) == 0 &&
+                    reinterpret_cast<uintptr_t>(out) % fp4_el(out_dtype) == 0,
+                MOE_ERR_INVALID_ARG, "%s: packed and tile_sched must be 16-byte aligned, ws 256-byte, x and out to their type",
+                who);
+    return MOE_OK;
+}
+
+extern "C" size_t moe_fp4_linear_workspace_size(int G, int K, int rows, int fmt) {
+    if (G < 1 || G > 1024 || K < 1 || K > MOE_FP4_MAX_K || rows < 0 || rows > MOE_FP4_MAX_ROWS) return 0;
+    return linear_ws(G, K, rows, fmt).total;
+}
+
+extern "C" int moe_fp4_linear(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* offsets,
+                              const int32_t* tile_sched, const void* packed, const float* alpha, const float* gscale, int G,
+                              int N, int K, int rows, int fmt, int dtype, void* out, long long ldo, int out_dtype, void* ws,
+                              size_t ws_bytes, void* stream) {
+    if (int rc = check_call("moe_fp4_linear", x, ldx, x_rows, src, offsets, tile_sched, packed, G, N, K, rows, fmt, dtype, out,
+                            ldo, out_dtype, ws))
+        return rc;
+    if (rows == 0) return MOE_OK;
+    const LinearWs L = linear_ws(G, K, rows, fmt);
+    MOE_REQUIRE(ws_bytes >= L.total, MOE_ERR_WORKSPACE, "moe_fp4_linear: workspace %zu < %zu", ws_bytes, L.total);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    if (offsets) {
+        int32_t* sched = reinterpret_cast<int32_t*>(w + L.sched);
+        if (int rc = launch_group_sched(offsets, G, rows, sched, s)) return rc;
+        tile_sched = sched;
+    }
+    if (int rc = launch_quantize_operand(x, ldx, x_rows, src, tile_sched, G, rows, K, dtype, fmt, gscale, w + L.codes,
+                                         w + L.sf, s))
+        return rc;
+    Params p = params_for(tile_sched, G, rows, w + L.sf, packed, weight_layout(G, N, K, fmt), K);
+    p.N = N;
+    p.ldo = (int)ldo;
+    p.out = out;
+    p.out_dtype = out_dtype;
+    p.alpha = alpha;
+    return fmt == MOE_FP4_NV ? product<Nv, EPI_OUT>(w + L.codes, rows, G, K, p, s)
+                             : product<Mx, EPI_OUT>(w + L.codes, rows, G, K, p, s);
+}
+
+extern "C" size_t moe_fp4_expert_ffn_workspace_size(int E, int h, int F, int rows, int fmt) {
+    if (E < 1 || E > 1024 || h < 1 || h > MOE_FP4_MAX_K || F < 1 || F > MOE_FP4_MAX_K || rows < 0 || rows > MOE_FP4_MAX_ROWS)
+        return 0;
+    return ffn_ws(E, h, F, rows, fmt).total;
+}
+
+extern "C" int moe_fp4_expert_ffn(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* offsets,
+                                  const int32_t* tile_sched, const void* packed, const float* alpha_gate,
+                                  const float* alpha_up, const float* alpha_down, const float* gscale,
+                                  const float* act_gscale, int E, int h, int F, int rows, int fmt, int dtype, void* out,
+                                  long long ldo, int out_dtype, void* ws, size_t ws_bytes, void* stream) {
+    if (int rc = check_call("moe_fp4_expert_ffn", x, ldx, x_rows, src, offsets, tile_sched, packed, E, h, h, rows, fmt, dtype,
+                            out, ldo, out_dtype, ws))
+        return rc;
+    MOE_REQUIRE(F >= 1 && F <= MOE_FP4_MAX_K, MOE_ERR_INVALID_ARG, "moe_fp4_expert_ffn: F=%d", F);
+    if (rows == 0) return MOE_OK;
+    const FfnWs L = ffn_ws(E, h, F, rows, fmt);
+    MOE_REQUIRE(ws_bytes >= L.total, MOE_ERR_WORKSPACE, "moe_fp4_expert_ffn: workspace %zu < %zu", ws_bytes, L.total);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    if (offsets) {
+        int32_t* sched = reinterpret_cast<int32_t*>(w + L.x.sched);
+        if (int rc = launch_group_sched(offsets, E, rows, sched, s)) return rc;
+        tile_sched = sched;
+    }
+    if (int rc = launch_quantize_operand(x, ldx, x_rows, src, tile_sched, E, rows, h, dtype, fmt, gscale, w + L.x.codes,
+                                         w + L.x.sf, s))
+        return rc;
+    const ExpertLayout W = expert_layout(E, h, F, fmt);
+    Params p = params_for(tile_sched, E, rows, w + L.x.sf, packed, W.gu, h);
+    p.alpha = alpha_gate;
+    p.alpha_up = alpha_up;
+    p.act_gscale = act_gscale;
+    p.act_codes = w + L.act_codes;
+    p.act_sf = w + L.act_sf;
+    p.act_pitch = pad64(F) / 2;
+    p.act_kst = stages_of(F);
+    if (int rc = fmt == MOE_FP4_NV ? product<Nv, EPI_SWIGLU>(w + L.x.codes, rows, E, h, p, s)
+                                   : product<Mx, EPI_SWIGLU>(w + L.x.codes, rows, E, h, p, s))
+        return rc;
+    Params d = params_for(tile_sched, E, rows, w + L.act_sf, static_cast<const uint8_t*>(packed) + W.down_off, W.down, F);
+    d.N = h;
+    d.ldo = (int)ldo;
+    d.out = out;
+    d.out_dtype = out_dtype;
+    d.alpha = alpha_down;
+    return fmt == MOE_FP4_NV ? product<Nv, EPI_OUT>(w + L.act_codes, rows, E, F, d, s)
+                             : product<Mx, EPI_OUT>(w + L.act_codes, rows, E, F, d, s);
+}

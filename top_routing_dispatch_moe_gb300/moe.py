@@ -17,7 +17,8 @@ if not os.path.exists(_LIB_PATH):
 _lib = ctypes.CDLL(_LIB_PATH)
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_TIMEOUT = range(6)
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
+FP4_FORMAT = {"nv": 0, "mx": 1}
 GATING = {"softmax": 0, "softmax_renorm": 1, "sigmoid_bias_renorm": 2, "softmax_selbias": 3}
 TILE_M = 128
 
@@ -50,6 +51,19 @@ _SIGS = {
     "moe_dispatch_fp8": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
     "moe_expert_up_gate_fp8": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_dequant_fp8": (_I, [_P, _P, _I, _I, _P, _P]),
+    "moe_fp4_codes_pitch": (_Z, [_I]),
+    "moe_fp4_scales_pitch": (_Z, [_I, _I]),
+    "moe_fp4_quantize": (_I, [_P, _LL, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "moe_fp4_dequantize": (_I, [_P, _P, _I, _I, _I, _P, _I, _P, _LL, _P]),
+    "moe_fp4_packed_weight_bytes": (_Z, [_I, _I, _I, _I]),
+    "moe_fp4_pack_weight": (_I, [_P, _P, _I, _I, _I, _I, _P, _P]),
+    "moe_fp4_linear_workspace_size": (_Z, [_I, _I, _I, _I]),
+    "moe_fp4_linear": (_I, [_P, _LL, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _LL, _I, _P, _Z, _P]),
+    "moe_fp4_packed_expert_weights_bytes": (_Z, [_I, _I, _I, _I]),
+    "moe_fp4_pack_expert_weights": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "moe_fp4_expert_ffn_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
+    "moe_fp4_expert_ffn": (_I, [_P, _LL, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _LL, _I, _P,
+                                _Z, _P]),
     "moe_combine_backward": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
     "moe_router_backward_workspace_size": (_Z, [_I, _I]),
     "moe_router_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _F, _P, _P, _P, _Z, _P]),
@@ -709,3 +723,169 @@ def moe_expert_weight_grads(buf, act, d_gu, d_eout, offsets, kept_counts, E: int
                                         _ptr(dW_up), _ptr(dW_down), _ptr(ws), ws.numel(), _stream(stream)))
     return dW_gate, dW_up, dW_down
 
+
+# ----------------------------------------------------------------------------------------- 4-bit experts
+
+_FP4_DTYPE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+
+
+def _fp4_dtype(dt: torch.dtype) -> int:
+    if dt not in _FP4_DTYPE:
+        raise MoEError(MOE_ERR_UNSUPPORTED, f"dtype {dt}")
+    return _FP4_DTYPE[dt]
+
+
+def _fp4_format(fmt: str | int) -> int:
+    if isinstance(fmt, str):
+        if fmt not in FP4_FORMAT:
+            raise MoEError(MOE_ERR_UNSUPPORTED, f"4-bit format {fmt!r}")
+        return FP4_FORMAT[fmt]
+    return int(fmt)
+
+
+def _fp4_require(ok: bool, what: str):
+    if not ok:
+        raise MoEError(MOE_ERR_INVALID_ARG, what)
+
+
+def _fp4_rows(t, what: str) -> int:
+    """The row stride of a 2-D tensor with contiguous rows."""
+    _fp4_require(t.dim() == 2 and t.is_cuda and (t.stride(1) == 1 or t.shape[1] == 1),
+                 f"{what}: a 2-D device tensor with contiguous rows")
+    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def _fp4_vector(t, n: int, dtype, what: str):
+    """An optional contiguous vector of at least n elements of dtype."""
+    _fp4_require(t is None or (t.dtype == dtype and t.numel() >= n and t.is_cuda and t.is_contiguous()),
+                 f"{what}: a contiguous {dtype} device tensor of {n} elements")
+    return t
+
+
+def moe_fp4_codes_pitch(K: int) -> int:
+    """Bytes of codes a row: 16 for every 32 columns begun."""
+    return _lib.moe_fp4_codes_pitch(K)
+
+
+def moe_fp4_scales_pitch(K: int, fmt) -> int:
+    """Block scales a row."""
+    return _lib.moe_fp4_scales_pitch(K, _fp4_format(fmt))
+
+
+def moe_fp4_quantize(x, fmt="nv", *, gscale=None, src=None, codes=None, scales=None, stream=None):
+    """x [*, K] (bf16, fp16 or fp32, row stride free) -> (codes uint8 [rows, pitch], scales uint8 [rows, blocks]): e2m1
+    codes under e4m3 scales of 16 columns ("nv") or powers of two of 32 ("mx"). gscale: an fp32 scalar tensor that x is
+    multiplied with first; src [rows] int32: x's row of each row, -1 for zeros."""
+    f, K, ldx = _fp4_format(fmt), x.shape[-1], _fp4_rows(x, "x")
+    rows = x.shape[0] if src is None else src.numel()
+    _fp4_vector(src, 0, torch.int32, "src")
+    _fp4_vector(gscale, 1, torch.float32, "gscale")
+    nb, pitch = moe_fp4_scales_pitch(K, f), moe_fp4_codes_pitch(K)
+    codes = torch.empty((rows, pitch), dtype=torch.uint8, device=x.device) if codes is None else codes
+    scales = torch.empty((rows, nb), dtype=torch.uint8, device=x.device) if scales is None else scales
+    _fp4_vector(codes, rows * pitch, torch.uint8, "codes")
+    _fp4_vector(scales, rows * nb, torch.uint8, "scales")
+    _check(_lib.moe_fp4_quantize(_ptr(x), ldx, x.shape[0], _ptr(src), rows, K, _fp4_dtype(x.dtype), f, _ptr(gscale),
+                                 _ptr(codes), _ptr(scales), _stream(stream)))
+    return codes, scales
+
+
+def moe_fp4_dequantize(codes, scales, K: int, fmt="nv", *, gscale=None, dtype=torch.bfloat16, out=None, stream=None):
+    """The rows [rows, K] that codes and scales stand for, divided by gscale where it is given."""
+    f, rows = _fp4_format(fmt), codes.shape[0]
+    out = torch.empty((rows, K), dtype=dtype, device=codes.device) if out is None else out
+    _fp4_require(tuple(out.shape) == (rows, K), f"out: [{rows}, {K}]")
+    _fp4_vector(codes, rows * moe_fp4_codes_pitch(K), torch.uint8, "codes")
+    _fp4_vector(scales, rows * moe_fp4_scales_pitch(K, f), torch.uint8, "scales")
+    _fp4_vector(gscale, 1, torch.float32, "gscale")
+    _check(_lib.moe_fp4_dequantize(_ptr(codes), _ptr(scales), rows, K, f, _ptr(gscale), _fp4_dtype(out.dtype), _ptr(out),
+                                   _fp4_rows(out, "out"), _stream(stream)))
+    return out
+
+
+def moe_fp4_pack_weight(codes, scales, K: int, fmt="nv", packed=None, stream=None):
+    """A weight [G, N, K] as moe_fp4_quantize (or a checkpoint) holds it, codes [G, N, pitch] and scales [G, N, blocks],
+    in the operand layout of moe_fp4_linear."""
+    f, (G, N) = _fp4_format(fmt), codes.shape[:2]
+    need = _lib.moe_fp4_packed_weight_bytes(G, N, K, f)
+    _fp4_vector(codes, G * N * moe_fp4_codes_pitch(K), torch.uint8, "codes")
+    _fp4_vector(scales, G * N * moe_fp4_scales_pitch(K, f), torch.uint8, "scales")
+    packed = _bytes_tensor(need, codes.device) if packed is None else packed
+    _fp4_vector(packed, need, torch.uint8, "packed")
+    _check(_lib.moe_fp4_pack_weight(_ptr(codes), _ptr(scales), G, N, K, f, _ptr(packed), _stream(stream)))
+    return packed
+
+
+def moe_fp4_linear_workspace_size(G: int, K: int, rows: int, fmt="nv") -> int:
+    return _lib.moe_fp4_linear_workspace_size(G, K, rows, _fp4_format(fmt))
+
+
+def moe_fp4_linear(x, offsets, packed, N: int, fmt="nv", *, G: int | None = None, src=None, tile_sched=None, alpha=None,
+                   gscale=None, out=None, out_dtype=None, ws=None, stream=None):
+    """out [rows, N]: x's rows [offsets[g], offsets[g + 1]) quantised, times group g's packed 4-bit weight, times alpha[g].
+    offsets [G + 1] int32 on the device, or None with tile_sched (moe_dispatch's) and G. src as for moe_fp4_quantize.
+    out: x's dtype unless out or out_dtype say otherwise. ws: moe_fp4_linear_workspace_size bytes, kept across calls."""
+    f, K, ldx = _fp4_format(fmt), x.shape[-1], _fp4_rows(x, "x")
+    rows = x.shape[0] if src is None else src.numel()
+    G = offsets.numel() - 1 if offsets is not None else G
+    _fp4_require(G is not None, "G: the number of groups of tile_sched")
+    _fp4_vector(offsets, 2, torch.int32, "offsets")
+    _fp4_vector(src, 0, torch.int32, "src")
+    _fp4_vector(tile_sched, 4, torch.int32, "tile_sched")
+    _fp4_vector(alpha, G, torch.float32, "alpha")
+    _fp4_vector(gscale, 1, torch.float32, "gscale")
+    _fp4_vector(packed, _lib.moe_fp4_packed_weight_bytes(G, N, K, f), torch.uint8, "packed")
+    out = torch.empty((rows, N), dtype=out_dtype or x.dtype, device=x.device) if out is None else out
+    _fp4_require(tuple(out.shape) == (rows, N), f"out: [{rows}, {N}]")
+    ws = _bytes_tensor(moe_fp4_linear_workspace_size(G, K, rows, f), x.device) if ws is None else ws
+    _fp4_vector(ws, 0, torch.uint8, "ws")
+    _check(_lib.moe_fp4_linear(_ptr(x), ldx, x.shape[0], _ptr(src), _ptr(offsets), _ptr(tile_sched), _ptr(packed),
+                               _ptr(alpha), _ptr(gscale), G, N, K, rows, f, _fp4_dtype(x.dtype), _ptr(out),
+                               _fp4_rows(out, "out"), _fp4_dtype(out.dtype), _ptr(ws), ws.numel(), _stream(stream)))
+    return out
+
+
+def moe_fp4_pack_expert_weights(gate, up, down, h: int, F: int, fmt="nv", packed=None, stream=None):
+    """gate, up [E, F, h] and down [E, h, F], each as (codes, scales), in the operand layout of moe_fp4_expert_ffn."""
+    f, E = _fp4_format(fmt), gate[0].shape[0]
+    for (c, s), n, k, what in ((gate, F, h, "gate"), (up, F, h, "up"), (down, h, F, "down")):
+        _fp4_vector(c, E * n * moe_fp4_codes_pitch(k), torch.uint8, what + " codes")
+        _fp4_vector(s, E * n * moe_fp4_scales_pitch(k, f), torch.uint8, what + " scales")
+    need = _lib.moe_fp4_packed_expert_weights_bytes(E, h, F, f)
+    packed = _bytes_tensor(need, gate[0].device) if packed is None else packed
+    _fp4_vector(packed, need, torch.uint8, "packed")
+    _check(_lib.moe_fp4_pack_expert_weights(*(_ptr(t) for m in (gate, up, down) for t in m), E, h, F, f, _ptr(packed),
+                                            _stream(stream)))
+    return packed
+
+
+def moe_fp4_expert_ffn_workspace_size(E: int, h: int, F: int, rows: int, fmt="nv") -> int:
+    return _lib.moe_fp4_expert_ffn_workspace_size(E, h, F, rows, _fp4_format(fmt))
+
+
+def moe_fp4_expert_ffn(x, offsets, packed, F: int, fmt="nv", *, E: int | None = None, src=None, tile_sched=None,
+                       alpha_gate=None, alpha_up=None, alpha_down=None, gscale=None, act_gscale=None, out=None,
+                       out_dtype=None, ws=None, stream=None):
+    """out [rows, h]: the SwiGLU expert FFN in 4 bits on the rows of each expert (offsets, tile_sched, src as for
+    moe_fp4_linear); act is quantised inside. ws: moe_fp4_expert_ffn_workspace_size bytes, kept across calls."""
+    f, h, ldx = _fp4_format(fmt), x.shape[-1], _fp4_rows(x, "x")
+    rows = x.shape[0] if src is None else src.numel()
+    E = offsets.numel() - 1 if offsets is not None else E
+    _fp4_require(E is not None, "E: the number of experts of tile_sched")
+    _fp4_vector(offsets, 2, torch.int32, "offsets")
+    _fp4_vector(src, 0, torch.int32, "src")
+    _fp4_vector(tile_sched, 4, torch.int32, "tile_sched")
+    for t, what in ((alpha_gate, "alpha_gate"), (alpha_up, "alpha_up"), (alpha_down, "alpha_down")):
+        _fp4_vector(t, E, torch.float32, what)
+    _fp4_vector(gscale, 1, torch.float32, "gscale")
+    _fp4_vector(act_gscale, 1, torch.float32, "act_gscale")
+    _fp4_vector(packed, _lib.moe_fp4_packed_expert_weights_bytes(E, h, F, f), torch.uint8, "packed")
+    out = torch.empty((rows, h), dtype=out_dtype or x.dtype, device=x.device) if out is None else out
+    _fp4_require(tuple(out.shape) == (rows, h), f"out: [{rows}, {h}]")
+    ws = _bytes_tensor(moe_fp4_expert_ffn_workspace_size(E, h, F, rows, f), x.device) if ws is None else ws
+    _fp4_vector(ws, 0, torch.uint8, "ws")
+    _check(_lib.moe_fp4_expert_ffn(_ptr(x), ldx, x.shape[0], _ptr(src), _ptr(offsets), _ptr(tile_sched), _ptr(packed),
+                                   _ptr(alpha_gate), _ptr(alpha_up), _ptr(alpha_down), _ptr(gscale), _ptr(act_gscale), E, h,
+                                   F, rows, f, _fp4_dtype(x.dtype), _ptr(out), _fp4_rows(out, "out"),
+                                   _fp4_dtype(out.dtype), _ptr(ws), ws.numel(), _stream(stream)))
+    return out
