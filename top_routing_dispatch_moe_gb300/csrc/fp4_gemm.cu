@@ -5,12 +5,14 @@
 // (kind::mxf4nvf4, 16-column blocks with e4m3 scales, and kind::mxf4, 32-column blocks with powers of two; K = 64 an
 // instruction).
 //
-// One persistent CTA per SM with ten warps:
+// One persistent CTA per SM with fourteen warps:
 //   warp 0     producer: per stage of 256 columns a 128-row tile of codes of A by TMA (boxes of 32 rows where the tile has
 //              fewer rows), BN weight rows, and both operands' block scales, each one bulk copy of contiguous packed bytes;
-//   warp 1     per stage: tcgen05.cp of the scale pieces into tensor memory, then the MMAs, from one thread;
+//   warp 1     the MMAs of a stage;
 //   warps 2-9  epilogue, two warps to a quarter of the tensor memory lanes, taking 64-column chunks in turn: either
-//              silu(gate) * up requantised to the next product's operand, or alpha times the accumulator in the output type.
+//              silu(gate) * up requantised to the next product's operand, or alpha times the accumulator in the output type;
+//   warps 10-13  scales: each brings a stage's scale pieces from shared memory into its quarter of the tensor memory
+//              lanes (every quarter holds all of them), one stage ahead of the MMAs.
 // Two accumulators: the epilogue of one tile runs under the MMAs of the next.
 //
 // Every wait is bounded, as in the bf16 grouped GEMM: one that runs out latches MOE_ERR_TIMEOUT, every role leaves, the
@@ -26,8 +28,8 @@ using namespace moe::tc;
 
 constexpr int BM = 128;
 constexpr int A_BYTES = BM * SEG_K / 2;          // 16 KB of codes
-constexpr int THREADS = 320;
-constexpr int EPI_WARPS = 8;
+constexpr int EPI_WARPS = 8, SF_WARPS = 4;
+constexpr int THREADS = 32 * (2 + EPI_WARPS + SF_WARPS);
 constexpr int TMEM_COLS = 512;
 
 enum Epi : int { EPI_OUT = 0, EPI_SWIGLU = 1 };
@@ -39,9 +41,9 @@ struct Cfg {
     static constexpr int SF_BLOCKS = (BN + 127) / 128;               // 128-row scale tiles a weight tile touches
     template <class F> static constexpr int SFS = (1 + SF_BLOCKS) * SF_BYTES<F>;   // scale bytes of a stage
     template <class F> static constexpr int SMEM = 1024 + STAGES * (A_BYTES + B_BYTES + SFS<F>) + 256;
-    static constexpr int ACC_COLS = BN == 192 ? 192 : BN;            // columns of one accumulator
-    static constexpr int SF_COL = 2 * ACC_COLS;                      // scale columns follow the two accumulators
-    static_assert(2 * ACC_COLS + 48 <= TMEM_COLS, "tensor memory columns");
+    static constexpr int SF_COL = 2 * BN;                            // scale columns follow the two accumulators
+    template <class F> static constexpr int SF_COLS = SF_PIECES<F> * 4 * (1 + SF_BLOCKS);   // of a stage
+    static_assert(SF_COL + 2 * SF_COLS<Nv> <= TMEM_COLS, "tensor memory columns");
 };
 
 struct Params {
@@ -81,24 +83,53 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
-// 32 rows of 16 bytes (8-row groups 128 bytes apart) -> the same 4 columns of each quarter of the lanes.
-__device__ __forceinline__ void sf_to_tmem(uint32_t taddr, uint32_t saddr) {
-    const uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1 << 46;
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
-}
+// The MMA warp's operations. The whole warp runs its loop, with conditions that are the same in all lanes (votes), and one
+// elected lane, the same each time, issues: the operands then stay in uniform registers. Issued from a branch that one
+// lane takes, an MMA cost 94 cycles of issue and a stage 690, where its four MMAs take 4 x 96 (N = 192).
 template <class F>
 __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                            uint32_t accumulate) {
     if constexpr (F::ID == MOE_FP4_NV)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
             ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb) : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
             ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb) : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar) : "memory");
+}
+// wait_phase for a whole warp, the same answer in every lane.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, long long limit, volatile int* abort_flag, unsigned* err,
+                                          unsigned site) {
+    for (long long i = 0; i < limit; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *abort_flag)) return false;
+    }
+    if ((threadIdx.x & 31) == 0) {
+        *abort_flag = 1;
+        latch_device_error(err, kDevErrTimeout, site);
+    }
+    __syncwarp();
+    return false;
+}
+// 16 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+                 "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+}
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t* v) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
 }
 // Instruction descriptor of the block-scaled kinds: A and B e2m1 (bits 7-9 and 10-12 = 1), both K-major, N >> 3 at bits
 // 17-22, scale type at bit 23 (0: e4m3, 1: power of two), M >> 4 at bits 24-28, K = 64 (bit 31 = 0). Bits 4-5 and 29-30:
@@ -198,13 +229,14 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     auto tfull = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
     auto tempty = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
     const uint32_t mma_done = bar0 + 8u * (2 * STAGES + 4);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+    auto sfull = [&](int b) { return bar0 + 8u * (2 * STAGES + 5 + b); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 7);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
-        for (int a = 0; a < 2; ++a) { mbar_init(tfull(a), 1); mbar_init(tempty(a), EPI_WARPS); }
+        for (int a = 0; a < 2; ++a) { mbar_init(tfull(a), 1); mbar_init(tempty(a), EPI_WARPS); mbar_init(sfull(a), SF_WARPS); }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -259,47 +291,81 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 if (issued & (1u << s)) drain_phase(full(s), (last_par >> s) & 1u, p.err, 0x211u);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr int PIECES = SF_PIECES<F>, BC = C::SF_BLOCKS * 4;
-            int stage = 0, iter = 0;
-            uint32_t phase = 0;
-            for (int w = blockIdx.x; w < total && !*abort_flag; w += gridDim.x, ++iter) {
-                const int a = iter & 1;
-                if (!wait_phase(tempty(a), ((iter >> 1) & 1) ^ 1u, p.wait_limit, abort_flag, p.err, 0x220u)) break;
+        constexpr int PIECES = SF_PIECES<F>, BC = C::SF_BLOCKS * 4;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        int stage = 0, iter = 0, b = 0;
+        uint32_t phase = 0, bphase = 0;
+        bool ok = true;
+        for (int w = blockIdx.x; w < total && ok; w += gridDim.x, ++iter) {
+            const int a = iter & 1;
+            const uint32_t shift = __shfl_sync(0xffffffffu, map_work(p.sched, G, p.NT, w).n * BN & 64 ? 2u : 0u, 0);
+            ok = wait_warp(tempty(a), ((iter >> 1) & 1) ^ 1u, p.wait_limit, abort_flag, p.err, 0x220u);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = tm + a * BN;
+            for (int kb = 0; kb < p.kst; ++kb) {
+                ok = wait_warp(full(stage), phase, p.wait_limit, abort_flag, p.err, 0x221u) &&
+                     wait_warp(sfull(b), bphase, p.wait_limit, abort_flag, p.err, 0x223u);
+                if (!ok) break;
                 tc_fence_after();
-                const Work wk = map_work(p.sched, G, p.NT, w);
-                const uint32_t d = tmem + a * C::ACC_COLS, sfa = tmem + C::SF_COL, sfb = sfa + PIECES * 4;
-                const uint32_t shift = (wk.n * BN & 64) ? 2u : 0u;   // a tile that starts in the middle of a scale tile
-                bool ok = true;
-                for (int kb = 0; kb < p.kst; ++kb) {
-                    if (!wait_phase(full(stage), phase, p.wait_limit, abort_flag, p.err, 0x221u)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t a_s = sA + stage * A_BYTES, b_s = sB + stage * B_BYTES, s_s = sS + stage * SFS;
-                    // the scales of all pieces, then the steps: copies and MMAs of one thread run in order
+                const uint64_t da = sw128_desc(sA + stage * A_BYTES), db = sw128_desc(sB + stage * B_BYTES);
+                const uint32_t sfa = tm + C::SF_COL + b * C::template SF_COLS<F>, sfb = sfa + PIECES * 4 + shift;
+                const int n = min(4, p.steps - 4 * kb);
 #pragma unroll
-                    for (int q = 0; q < PIECES; ++q) {
-                        sf_to_tmem(sfa + 4 * q, s_s + q * 512);
-#pragma unroll
-                        for (int t = 0; t < C::SF_BLOCKS; ++t)
-                            sf_to_tmem(sfb + q * BC + 4 * t, s_s + (1 + t) * SF_BYTES<F> + q * 512);
-                    }
-                    const int n = min(4, p.steps - 4 * kb);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k >= n) break;
+                for (int k = 0; k < 4; ++k) {
+                    if (k < n) {
                         const int q = F::ID == MOE_FP4_NV ? k : k / 2;
                         const uint32_t id = idesc_scaled<F, BM, BN>(F::ID == MOE_FP4_NV ? 0 : k & 1);
-                        mma_scaled<F>(d, sw128_desc(a_s + 32 * k), sw128_desc(b_s + 32 * k), id, sfa + 4 * q,
-                                      sfb + q * BC + shift, (kb | k) != 0);
+                        mma_scaled<F>(d, da + 2 * k, db + 2 * k, id, sfa + 4 * q, sfb + q * BC, (kb | k) != 0);
                     }
-                    umma_commit(empty(stage));
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
-                if (!ok) break;
-                umma_commit(tfull(a));
+                commit_elected(empty(stage));
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                if (++b == 2) { b = 0; bphase ^= 1u; }
             }
-            umma_commit(mma_done);                  // all MMAs finished before the columns are freed
-            drain_phase(mma_done, 0, p.err, 0x222u);
+            if (ok) commit_elected(tfull(a));
+        }
+        commit_elected(mma_done);                   // all MMAs finished before the columns are freed
+        if (lane == 0) drain_phase(mma_done, 0, p.err, 0x222u);
+        __syncwarp();
+    } else if (warp >= 2 + EPI_WARPS) {
+        // stage i's scales go to buffer i % 2 once the MMAs of stage i - 2 have completed (they free its ring stage)
+        constexpr int PIECES = SF_PIECES<F>, COLS = C::template SF_COLS<F>;
+        const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16;
+        int stage = 0, b = 0, old = STAGES - 2;
+        uint32_t phase = 0, ophase = 1;             // (the two rounds before the first count as complete)
+        bool ok = true;
+        for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
+            for (int kb = 0; kb < p.kst; ++kb) {
+                ok = wait_warp(empty(old), ophase, p.wait_limit, abort_flag, p.err, 0x240u) &&
+                     wait_warp(full(stage), phase, p.wait_limit, abort_flag, p.err, 0x241u);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t v[COLS];
+                const uint32_t src = sS + stage * SFS + lane * 16, dst = tmem + quarter + C::SF_COL + b * COLS;
+#pragma unroll
+                for (int q = 0; q < PIECES; ++q) {
+                    ld_shared_v4(src + q * 512, v + 4 * q);
+#pragma unroll
+                    for (int t = 0; t < C::SF_BLOCKS; ++t)
+                        ld_shared_v4(src + (1 + t) * SF_BYTES<F> + q * 512, v + 4 * (PIECES + q * C::SF_BLOCKS + t));
+                }
+#pragma unroll
+                for (int c = 0; c < COLS; c += 16) {
+                    uint32_t x[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = v[min(c + i, COLS - 1)];
+                    if (c + 16 <= COLS) tmem_st16(dst + c, x);
+                    else tmem_st8(dst + c, x);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sfull(b));
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                if (++old == STAGES) { old = 0; ophase ^= 1u; }
+                b ^= 1;
+            }
         }
     } else {
         const int quarter = 32 * (warp & 3), half = (warp - 2) >> 2, r = quarter + lane;
@@ -309,7 +375,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             if (!wait_phase(tfull(a), (iter >> 1) & 1, p.wait_limit, abort_flag, p.err, 0x230u)) break;
             tc_fence_after();
             const Work wk = map_work(p.sched, G, p.NT, w);
-            const uint32_t tbase = tmem + a * C::ACC_COLS + ((uint32_t)quarter << 16);
+            const uint32_t tbase = tmem + a * BN + ((uint32_t)quarter << 16);
             if (wk.row0 + quarter < wk.row1) {
                 const int nb = min(BN / 64, p.NB64 - wk.n * (BN / 64));
 #pragma unroll 1
