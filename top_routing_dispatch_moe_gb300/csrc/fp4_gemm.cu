@@ -12,7 +12,7 @@
 //   warps 2-9  epilogue, two warps to a quarter of the tensor memory lanes, taking 64-column chunks in turn: either
 //              silu(gate) * up requantised to the next product's operand, or alpha times the accumulator in the output type;
 //   warps 10-13  scales: each brings a stage's scale pieces from shared memory into its quarter of the tensor memory
-//              lanes (every quarter holds all of them), one stage ahead of the MMAs.
+//              lanes (every quarter holds all of them), ahead of the MMAs.
 // Two accumulators: the epilogue of one tile runs under the MMAs of the next.
 //
 // Every wait is bounded, as in the bf16 grouped GEMM: one that runs out latches MOE_ERR_TIMEOUT, every role leaves, the
@@ -31,6 +31,7 @@ constexpr int A_BYTES = BM * SEG_K / 2;          // 16 KB of codes
 constexpr int EPI_WARPS = 8, SF_WARPS = 4;
 constexpr int THREADS = 32 * (2 + EPI_WARPS + SF_WARPS);
 constexpr int TMEM_COLS = 512;
+constexpr int SF_BUFS = 3;                       // stages of scales in tensor memory
 
 enum Epi : int { EPI_OUT = 0, EPI_SWIGLU = 1 };
 
@@ -42,8 +43,9 @@ struct Cfg {
     template <class F> static constexpr int SFS = (1 + SF_BLOCKS) * SF_BYTES<F>;   // scale bytes of a stage
     template <class F> static constexpr int SMEM = 1024 + STAGES * (A_BYTES + B_BYTES + SFS<F>) + 256;
     static constexpr int SF_COL = 2 * BN;                            // scale columns follow the two accumulators
-    template <class F> static constexpr int SF_COLS = SF_PIECES<F> * 4 * (1 + SF_BLOCKS);   // of a stage
-    static_assert(SF_COL + 2 * SF_COLS<Nv> <= TMEM_COLS, "tensor memory columns");
+    static constexpr int B_COLS = BN / 32;                           // scale columns of the weight rows in a piece
+    template <class F> static constexpr int SF_COLS = SF_PIECES<F> * (4 + B_COLS);   // of a stage
+    static_assert(SF_COL + SF_BUFS * SF_COLS<Nv> <= TMEM_COLS, "tensor memory columns");
 };
 
 struct Params {
@@ -85,7 +87,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 // The MMA warp's operations. The whole warp runs its loop, with conditions that are the same in all lanes (votes), and one
 // elected lane, the same each time, issues: the operands then stay in uniform registers. Issued from a branch that one
-// lane takes, an MMA cost 94 cycles of issue and a stage 690, where its four MMAs take 4 x 96 (N = 192).
+// lane takes, a stage cost 690 cycles, where its four MMAs take 4 x 96 (N = 192).
 template <class F>
 __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                            uint32_t accumulate) {
@@ -118,13 +120,25 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, long lo
     __syncwarp();
     return false;
 }
+// Whether a phase has completed, without waiting. Even a wait that succeeds at once takes some 180 cycles to answer; asked
+// before a stage's work and read after it, the answer about the next stage costs nothing.
+__device__ __forceinline__ bool test_phase(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
 // 16 columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
                  ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
                  "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};"
+                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                  ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
 }
@@ -230,13 +244,14 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     auto tempty = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
     const uint32_t mma_done = bar0 + 8u * (2 * STAGES + 4);
     auto sfull = [&](int b) { return bar0 + 8u * (2 * STAGES + 5 + b); };
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 7);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5 + SF_BUFS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
-        for (int a = 0; a < 2; ++a) { mbar_init(tfull(a), 1); mbar_init(tempty(a), EPI_WARPS); mbar_init(sfull(a), SF_WARPS); }
+        for (int a = 0; a < 2; ++a) { mbar_init(tfull(a), 1); mbar_init(tempty(a), EPI_WARPS); }
+        for (int b = 0; b < SF_BUFS; ++b) mbar_init(sfull(b), SF_WARPS);
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -291,80 +306,92 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 if (issued & (1u << s)) drain_phase(full(s), (last_par >> s) & 1u, p.err, 0x211u);
         }
     } else if (warp == 1) {
-        constexpr int PIECES = SF_PIECES<F>, BC = C::SF_BLOCKS * 4;
+        constexpr int PIECES = SF_PIECES<F>;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        int stage = 0, iter = 0, b = 0;
-        uint32_t phase = 0, bphase = 0;
-        bool ok = true;
-        for (int w = blockIdx.x; w < total && ok; w += gridDim.x, ++iter) {
-            const int a = iter & 1;
-            const uint32_t shift = __shfl_sync(0xffffffffu, map_work(p.sched, G, p.NT, w).n * BN & 64 ? 2u : 0u, 0);
-            ok = wait_warp(tempty(a), ((iter >> 1) & 1) ^ 1u, p.wait_limit, abort_flag, p.err, 0x220u);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t d = tm + a * BN;
+        int stage = 0, b = 0, acc = 0;
+        uint32_t phase = 0, bphase = 0, aphase = 1;
+        bool ok = true, ready = false;              // ready: all that the stage waits for was seen complete
+        for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
             for (int kb = 0; kb < p.kst; ++kb) {
-                ok = wait_warp(full(stage), phase, p.wait_limit, abort_flag, p.err, 0x221u) &&
-                     wait_warp(sfull(b), bphase, p.wait_limit, abort_flag, p.err, 0x223u);
+                if (!ready)
+                    ok = (kb > 0 || wait_warp(tempty(acc), aphase, p.wait_limit, abort_flag, p.err, 0x220u)) &&
+                         wait_warp(full(stage), phase, p.wait_limit, abort_flag, p.err, 0x221u) &&
+                         wait_warp(sfull(b), bphase, p.wait_limit, abort_flag, p.err, 0x223u);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t da = sw128_desc(sA + stage * A_BYTES), db = sw128_desc(sB + stage * B_BYTES);
-                const uint32_t sfa = tm + C::SF_COL + b * C::template SF_COLS<F>, sfb = sfa + PIECES * 4 + shift;
+                const uint32_t s0 = stage, b0 = b, a0 = acc;
+                const bool last = kb + 1 == p.kst;
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                if (++b == SF_BUFS) { b = 0; bphase ^= 1u; }
+                if (last && ++acc == 2) { acc = 0; aphase ^= 1u; }
+                const bool t0 = test_phase(full(stage), phase), t1 = test_phase(sfull(b), bphase),
+                           t2 = test_phase(tempty(acc), aphase);
+                const uint64_t da = sw128_desc(sA + s0 * A_BYTES), db = sw128_desc(sB + s0 * B_BYTES);
+                const uint32_t d = tm + a0 * BN, sfa = tm + C::SF_COL + b0 * C::template SF_COLS<F>, sfb = sfa + PIECES * 4;
                 const int n = min(4, p.steps - 4 * kb);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if (k < n) {
                         const int q = F::ID == MOE_FP4_NV ? k : k / 2;
                         const uint32_t id = idesc_scaled<F, BM, BN>(F::ID == MOE_FP4_NV ? 0 : k & 1);
-                        mma_scaled<F>(d, da + 2 * k, db + 2 * k, id, sfa + 4 * q, sfb + q * BC, (kb | k) != 0);
+                        mma_scaled<F>(d, da + 2 * k, db + 2 * k, id, sfa + 4 * q, sfb + C::B_COLS * q, (kb | k) != 0);
                     }
                 }
-                commit_elected(empty(stage));
-                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                if (++b == 2) { b = 0; bphase ^= 1u; }
+                commit_elected(empty(s0));
+                if (last) commit_elected(tfull(a0));
+                ready = __all_sync(0xffffffffu, t0 && t1 && (t2 || !last));
             }
-            if (ok) commit_elected(tfull(a));
         }
         commit_elected(mma_done);                   // all MMAs finished before the columns are freed
         if (lane == 0) drain_phase(mma_done, 0, p.err, 0x222u);
         __syncwarp();
     } else if (warp >= 2 + EPI_WARPS) {
-        // stage i's scales go to buffer i % 2 once the MMAs of stage i - 2 have completed (they free its ring stage)
-        constexpr int PIECES = SF_PIECES<F>, COLS = C::template SF_COLS<F>;
+        // Stage i's scales go to buffer i % SF_BUFS once the MMAs of stage i - SF_BUFS have completed (they free its ring
+        // stage too). A tile that starts in the middle of a 128-row scale tile takes the second half of the first one.
+        constexpr int PIECES = SF_PIECES<F>, COLS = C::template SF_COLS<F>, BC = C::B_COLS;
         const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16;
-        int stage = 0, b = 0, old = STAGES - 2;
-        uint32_t phase = 0, ophase = 1;             // (the two rounds before the first count as complete)
-        bool ok = true;
+        int stage = 0, b = 0, old = STAGES - SF_BUFS;
+        uint32_t phase = 0, ophase = 1;             // (the rounds before the first count as complete)
+        bool ok = true, loaded = false, freed = false;
         for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
+            const bool odd = BN % 128 == 64 && (map_work(p.sched, G, p.NT, w).n & 1);
             for (int kb = 0; kb < p.kst; ++kb) {
-                ok = wait_warp(empty(old), ophase, p.wait_limit, abort_flag, p.err, 0x240u) &&
-                     wait_warp(full(stage), phase, p.wait_limit, abort_flag, p.err, 0x241u);
+                if (!loaded) ok = wait_warp(full(stage), phase, p.wait_limit, abort_flag, p.err, 0x241u);
                 if (!ok) break;
-                tc_fence_after();
+                const bool t0 = test_phase(empty(old), ophase);
                 uint32_t v[COLS];
-                const uint32_t src = sS + stage * SFS + lane * 16, dst = tmem + quarter + C::SF_COL + b * COLS;
+                const uint32_t src = sS + stage * SFS + lane * 16;
 #pragma unroll
                 for (int q = 0; q < PIECES; ++q) {
                     ld_shared_v4(src + q * 512, v + 4 * q);
+                    uint32_t x[4 * C::SF_BLOCKS];
 #pragma unroll
-                    for (int t = 0; t < C::SF_BLOCKS; ++t)
-                        ld_shared_v4(src + (1 + t) * SF_BYTES<F> + q * 512, v + 4 * (PIECES + q * C::SF_BLOCKS + t));
+                    for (int t = 0; t < C::SF_BLOCKS; ++t) ld_shared_v4(src + (1 + t) * SF_BYTES<F> + q * 512, x + 4 * t);
+#pragma unroll
+                    for (int c = 0; c < BC; ++c) v[4 * PIECES + BC * q + c] = odd ? x[(c + 2) % (4 * C::SF_BLOCKS)] : x[c];
                 }
+                freed = __all_sync(0xffffffffu, t0);
+                if (!freed) ok = wait_warp(empty(old), ophase, p.wait_limit, abort_flag, p.err, 0x240u);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t dst = tmem + quarter + C::SF_COL + b * COLS;
 #pragma unroll
                 for (int c = 0; c < COLS; c += 16) {
-                    uint32_t x[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = v[min(c + i, COLS - 1)];
-                    if (c + 16 <= COLS) tmem_st16(dst + c, x);
-                    else tmem_st8(dst + c, x);
+                    if (c + 16 <= COLS) tmem_st16(dst + c, v + c);
+                    else if (c + 8 <= COLS) {
+                        tmem_st8(dst + c, v + c);
+                        if (c + 12 <= COLS) tmem_st4(dst + c + 8, v + c + 8);
+                    } else tmem_st4(dst + c, v + c);
                 }
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sfull(b));
+                const uint32_t sb = sfull(b);
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 if (++old == STAGES) { old = 0; ophase ^= 1u; }
-                b ^= 1;
+                if (++b == SF_BUFS) b = 0;
+                const bool t1 = test_phase(full(stage), phase);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                loaded = __all_sync(0xffffffffu, t1);
+                if (lane == 0) mbar_arrive(sb);
             }
         }
     } else {
