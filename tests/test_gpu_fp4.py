@@ -165,10 +165,13 @@ def test_linear_types_multipliers_and_rows_by_index(gpu_lib, fmt, dtype, out_dty
                  gscale=torch.tensor([8.0], device="cuda"), src=src, x_rows=10)
 
 
-@pytest.mark.parametrize("rows,N,K", [(2600, 2100, 256), (9000, 1300, 128), (20000, 600, 64)])
-def test_linear_of_many_tiles(gpu_lib, rows, N, K):
-    """Enough tiles for each tile width, and more tiles than SMs: the accumulators and the ring wrap around."""
-    check_linear(gpu_lib, [rows // 3, rows - rows // 3 - 5, 5], N, K, "nv", "bf16")
+@pytest.mark.parametrize("fmt,dtype", [("nv", "bf16"), ("mx", "fp32")])
+@pytest.mark.parametrize("counts,N,K", [([866, 1729, 5], 2100, 256), ([3000, 5995, 5], 1300, 128), ([6666, 13329, 5], 600, 64),
+                                        ([200] * 23 + [131], 1304, 1100), ([300, 5401], 2240, 1344), ([5000], 1000, 2048)])
+def test_linear_of_many_tiles(gpu_lib, counts, N, K, fmt, dtype):
+    """Enough tiles for each tile width and for pairs of SMs, and more tiles than SMs: the accumulators and the ring wrap
+    around, groups end on half a pair, and the output is stored in whole boxes and row by row."""
+    check_linear(gpu_lib, counts, N, K, fmt, dtype)
 
 
 def test_linear_keeps_other_rows_and_columns(gpu_lib):
@@ -261,6 +264,11 @@ def check_ffn(moe, counts, h, F, fmt, dtype, out_dtype=None, scaled=False, T=Non
     ([1] * 24, 512, 448, 3), ([257], 320, 1024, 100)])
 def test_expert_ffn(gpu_lib, fmt, counts, h, F, T):
     check_ffn(gpu_lib, counts, h, F, fmt, "bf16", T=T)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_expert_ffn_of_many_tiles(gpu_lib, fmt):
+    check_ffn(gpu_lib, [1000, 1620], 128, 2080, fmt, "bf16", T=900)
 
 
 @pytest.mark.parametrize("fmt", ["nv", "mx"])

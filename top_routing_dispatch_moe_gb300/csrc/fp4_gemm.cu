@@ -41,7 +41,7 @@ struct Cfg {
     static constexpr int B_BYTES = BN * SEG_K / 2;
     static constexpr int SF_BLOCKS = (BN + 127) / 128;               // 128-row scale tiles a weight tile touches
     template <class F> static constexpr int SFS = (1 + SF_BLOCKS) * SF_BYTES<F>;   // scale bytes of a stage
-    template <class F> static constexpr int SMEM = 1024 + STAGES * (A_BYTES + B_BYTES + SFS<F>) + 256;
+    template <class F> static constexpr int SMEM = 1024 + EPI_WARPS * 4096 + STAGES * (A_BYTES + B_BYTES + SFS<F>) + 256;
     static constexpr int SF_COL = 2 * BN;                            // scale columns follow the two accumulators
     static constexpr int B_COLS = BN / 32;                           // scale columns of the weight rows in a piece
     template <class F> static constexpr int SF_COLS = SF_PIECES<F> * (4 + B_COLS);   // of a stage
@@ -56,6 +56,7 @@ struct Params {
     int NT, NB64, NB128;         // n-tiles; 64-row and 128-row blocks of the packed weight
     int N, ldo;                  // EPI_OUT: columns and row stride of the output
     int out_dtype;
+    bool vec, boxed;             // rows of the output start on 16 bytes; it is stored by TMA where a warp's rows are all valid
     void* out;
     const float *alpha, *alpha_up;   // per group, or null (1)
     const float* act_gscale;     // EPI_SWIGLU: multiplier of act before it is quantised, or null
@@ -155,18 +156,18 @@ __device__ constexpr uint32_t idesc_scaled(int sub) {
 }
 
 // 32 consecutive columns of an output row in its type; whole 16-byte vectors where the row allows them.
+template <typename T> __device__ __forceinline__ T out_round(float v);
+template <> __device__ __forceinline__ float out_round<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half out_round<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 out_round<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <typename T>
-__device__ __forceinline__ void store_row(T* dst, const float* v, int n, bool vec) {
+__device__ __forceinline__ void store_row(T* dst, const float* v, float al, int n, bool vec) {
     constexpr int PER = 16 / sizeof(T);
 #pragma unroll
     for (int c = 0; c < 32; c += PER) {
         alignas(16) T o[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            if constexpr (sizeof(T) == 4) o[i] = v[c + i];
-            else if constexpr (std::is_same<T, __half>::value) o[i] = __float2half_rn(v[c + i]);
-            else o[i] = __float2bfloat16_rn(v[c + i]);
-        }
+        for (int i = 0; i < PER; ++i) o[i] = out_round<T>(v[c + i] * al);
         if (vec && c + PER <= n) {
             *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(o);
         } else {
@@ -176,22 +177,50 @@ __device__ __forceinline__ void store_row(T* dst, const float* v, int n, bool ve
         }
     }
 }
+// A box of 32 rows x 128 bytes of the output through the warp's staging buffer `stg` (1024-byte aligned, the layout of
+// 128-byte swizzling) and one TMA store: whole lines reach L2, where a thread's own 16-byte stores touch a sector of each
+// of 32 rows. v: the 128 bytes' values of this lane's row.
+template <typename T>
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t stg, const float* v, float al, int col, int row0) {
+    constexpr int PER = 16 / sizeof(T);
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) bulk_wait_read_all();             // the previous box has left the buffer
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        alignas(16) T o[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) o[i] = out_round<T>(v[c * PER + i] * al);
+        const uint4 w = *reinterpret_cast<const uint4*>(o);
+        st_shared_v4u(stg + lane * 128u + ((uint32_t)(c ^ (lane & 7)) << 4), w.x, w.y, w.z, w.w);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_2d(map, stg, col, row0);
+        bulk_commit();
+    }
+}
 
-// Chunk `q` (64 accumulator columns) of a tile, this thread's row `row` (live: one of the tile's rows).
-template <class F, int EPI>
-__device__ __forceinline__ void epilogue_chunk(const Params& p, const Work& wk, uint32_t tcol, int c0, int r, bool live) {
+// Chunk of 64 accumulator columns at column c0 of the tile's output, this thread's row r of the tile (live: one of its
+// rows). `read` runs once the chunk's columns are in registers.
+template <class F, int EPI, typename Fn>
+__device__ __forceinline__ void epilogue_chunk(const Params& p, const CUtensorMap* map, uint32_t stg, const Work& wk, uint32_t tcol,
+                                               int c0, int r, bool live, Fn read) {
     const int row = wk.row0 + r;
+    float v[64];
+    tmem_ld32(tcol, *reinterpret_cast<float (*)[32]>(v));
+    tmem_ld32(tcol + 32, *reinterpret_cast<float (*)[32]>(v + 32));
+    read();
     if constexpr (EPI == EPI_SWIGLU) {
-        float g[32], u[32];
-        tmem_ld32(tcol, g);
-        tmem_ld32(tcol + 32, u);
         if (!live) return;
         const float ag = p.alpha ? __ldg(p.alpha + wk.g) : 1.f, au = p.alpha_up ? __ldg(p.alpha_up + wk.g) : 1.f;
         const float gs = p.act_gscale ? __ldg(p.act_gscale) : 1.f;
         const int f0 = c0 / 2;                   // first column of act
+        float* u = v + 32;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            const float gv = g[i] * ag;
+            const float gv = v[i] * ag;
             u[i] = gv / (1.f + __expf(-gv)) * (u[i] * au) * gs;
         }
         uint32_t w[4], bytes = 0u;
@@ -211,32 +240,41 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const Work& wk, 
         else *sf = (uint8_t)bytes;
     } else {
         const float al = p.alpha ? __ldg(p.alpha + wk.g) : 1.f;
+        const int n = p.N - c0;
+        if (n <= 0) return;
+        if (p.boxed && wk.row0 + (r & ~31) + 31 < wk.row1) {     // all of the warp's rows (the map drops columns past N)
+            const int base = wk.row0 + (r & ~31);
+            if (p.out_dtype == MOE_F32) {
+                store_box<float>(map, stg, v, al, c0, base);
+                if (n > 32) store_box<float>(map, stg, v + 32, al, c0 + 32, base);
+            } else if (p.out_dtype == MOE_BF16) store_box<__nv_bfloat16>(map, stg, v, al, c0, base);
+            else store_box<__half>(map, stg, v, al, c0, base);
+            return;
+        }
+        if (!live) return;
         const int el = p.out_dtype == MOE_F32 ? 4 : 2;
         uint8_t* dst = static_cast<uint8_t*>(p.out) + ((size_t)row * p.ldo + c0) * el;
-        const bool vec = ((reinterpret_cast<uintptr_t>(p.out) | (size_t)p.ldo * el) & 15u) == 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float v[32];
-            tmem_ld32(tcol + 32 * h, v);
-            const int n = p.N - c0 - 32 * h;
-            if (!live || n <= 0) continue;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= al;
-            if (p.out_dtype == MOE_F32) store_row(reinterpret_cast<float*>(dst) + 32 * h, v, n, vec);
-            else if (p.out_dtype == MOE_BF16) store_row(reinterpret_cast<__nv_bfloat16*>(dst) + 32 * h, v, n, vec);
-            else store_row(reinterpret_cast<__half*>(dst) + 32 * h, v, n, vec);
+            if (n - 32 * h <= 0) break;
+            if (p.out_dtype == MOE_F32) store_row(reinterpret_cast<float*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h, p.vec);
+            else if (p.out_dtype == MOE_BF16)
+                store_row(reinterpret_cast<__nv_bfloat16*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h, p.vec);
+            else store_row(reinterpret_cast<__half*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h, p.vec);
         }
     }
 }
 
 template <class F, class C, int EPI>
 __global__ void __launch_bounds__(THREADS, 1)
-fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32, Params p) {
+fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
+                const __grid_constant__ CUtensorMap tmO, Params p) {
     constexpr int BN = C::BN, STAGES = C::STAGES, B_BYTES = C::B_BYTES, SFS = C::template SFS<F>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const uint32_t sA = smem_u32(smem), sB = sA + STAGES * A_BYTES, sS = sB + STAGES * B_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * (A_BYTES + B_BYTES + SFS));
+    const uint32_t sA = smem_u32(smem), sB = sA + STAGES * A_BYTES, sO = sB + STAGES * B_BYTES,
+                   sS = sO + EPI_WARPS * 4096;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * (A_BYTES + B_BYTES + SFS) + EPI_WARPS * 4096);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
@@ -399,7 +437,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         int iter = 0;
         for (int w = blockIdx.x; w < total; w += gridDim.x, ++iter) {
             const int a = iter & 1;
-            if (!wait_phase(tfull(a), (iter >> 1) & 1, p.wait_limit, abort_flag, p.err, 0x230u)) break;
+            if (!wait_warp(tfull(a), (iter >> 1) & 1, p.wait_limit, abort_flag, p.err, 0x230u)) break;
             tc_fence_after();
             const Work wk = map_work(p.sched, G, p.NT, w);
             const uint32_t tbase = tmem + a * BN + ((uint32_t)quarter << 16);
@@ -407,12 +445,14 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 const int nb = min(BN / 64, p.NB64 - wk.n * (BN / 64));
 #pragma unroll 1
                 for (int q = (half + iter) & 1; q < nb; q += 2)
-                    epilogue_chunk<F, EPI>(p, wk, tbase + 64 * q, wk.n * BN + 64 * q, r, wk.row0 + r < wk.row1);
+                    epilogue_chunk<F, EPI>(p, &tmO, sO + (warp - 2) * 4096, wk, tbase + 64 * q, wk.n * BN + 64 * q, r,
+                                           wk.row0 + r < wk.row1, [] {});
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(tempty(a));
         }
+        if (lane == 0) bulk_wait_read_all();         // every box read out of shared memory before the CTA exits
     }
     tc_fence_before();
     __syncthreads();
@@ -421,6 +461,301 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         tmem_dealloc(tmem, TMEM_COLS);
     }
 }
+
+// ---------------------------------------------------------------------------------------------------
+// two SMs to a tile: a cluster of two CTAs computes 256 rows x 256 columns with tcgen05.mma.cta_group::2
+// ---------------------------------------------------------------------------------------------------
+// The one-SM kernel is bound by the bytes that reach an SM: 47 KB a stage of four MMAs (N = 192), about 55 bytes a cycle of
+// 1.9 GHz, twice the MMAs' own time. In a pair each SM holds its own 128 rows of A and half of the weight rows (and the
+// scales of all of them, which its tensor core needs): 38 KB for MMAs a third larger.
+// The even CTA issues the MMAs for both. Every copy of a CTA completes on its own barrier; the odd CTA's scale warps, which
+// wait for it, pass the news on with their arrival on the even CTA's scale barrier, so that barrier tells of both CTAs'
+// operands. A pair takes two consecutive tiles of one group; where the second does not exist the odd CTA computes the
+// first one again and stores nothing.
+// Tensor memory has no room for two accumulators of 256 columns next to the scales: they overlap by 96 columns. The
+// epilogue reads the shared columns into registers first and frees them at once, so the next tile's MMAs wait for a read
+// of two of its four chunks and not for their conversion and stores.
+constexpr int PB_BYTES = 128 * SEG_K / 2;        // a CTA's half of the weight rows
+constexpr int P_STAGES = 4, P_BN = 256, P_SF_BUFS = 2, P_ACC2 = 160, P_SF_COL = P_ACC2 + P_BN;
+constexpr int P_MAX_G = 1024;
+template <class F> constexpr int P_SFS = 3 * SF_BYTES<F>;
+template <class F> constexpr int P_SMEM = 1024 + EPI_WARPS * 4096 + P_STAGES * (A_BYTES + PB_BYTES + P_SFS<F>) + 256 +
+                                          (P_MAX_G + 1) * 4;
+template <class F> constexpr int P_COLS = SF_PIECES<F> * 12;
+static_assert(P_SF_COL + P_SF_BUFS * P_COLS<Nv> <= TMEM_COLS, "tensor memory columns");
+static_assert(P_SMEM<Nv> <= 227 * 1024, "shared memory per CTA");
+
+template <class F>
+__device__ __forceinline__ void mma_scaled_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                                uint32_t accumulate) {
+    if constexpr (F::ID == MOE_FP4_NV)
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb) : "memory");
+}
+// On both CTAs' barrier at this offset.
+__device__ __forceinline__ void commit_pair_elected(uint32_t bar) {
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+                 ::"r"(bar), "h"((uint16_t)3) : "memory");
+}
+__device__ __forceinline__ bool test_phase_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_warp_pair(uint32_t bar, uint32_t parity, long long limit, volatile int* abort_flag,
+                                               uint32_t peer_abort, unsigned* err, unsigned site) {
+    for (long long i = 0; i < limit; ++i) {
+        if (__all_sync(0xffffffffu, CLUSTER ? mbar_try_wait_acq_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *abort_flag)) return false;
+    }
+    if ((threadIdx.x & 31) == 0) {
+        *abort_flag = 1;
+        st_cluster(peer_abort, 1u);
+        latch_device_error(err, kDevErrTimeout, site);
+    }
+    __syncwarp();
+    return false;
+}
+
+// Item w: group by group, n-tile next, pair fastest. tile, arow: what this CTA loads; row0, row1: what it stores.
+struct PairItem { Work wk; int arow, rows; };
+__device__ __forceinline__ PairItem map_pair_item(const int32_t* sched, const int* pp, int G, int NT, int w, int rank) {
+    int lo = 0, hi = G;
+    while (lo < hi) {                    // last g with pp[g] * NT <= w
+        const int mid = (lo + hi + 1) >> 1;
+        if ((long long)pp[mid] * NT <= w) lo = mid; else hi = mid - 1;
+    }
+    const int np = pp[lo + 1] - pp[lo], local = w - pp[lo] * NT;
+    const int n = local / np, q = local % np;
+    const int32_t* prefix = sched + kSchedHeader;
+    const int p0 = prefix[lo], mt = prefix[lo + 1] - p0;
+    const bool has = 2 * q + rank < mt;
+    const int t = p0 + 2 * q + (has ? rank : 0);
+    const int4 e = reinterpret_cast<const int4*>(sched + sched_tiles_offset(G))[t];
+    return PairItem{Work{e.x, t, has ? e.y : 0, has ? e.z : 0, n}, e.y, e.z - e.y};
+}
+
+template <class F, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
+                     const __grid_constant__ CUtensorMap tmO, Params p) {
+    constexpr int STAGES = P_STAGES, SFS = P_SFS<F>, PIECES = SF_PIECES<F>, COLS = P_COLS<F>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sA = smem_u32(smem), sB = sA + STAGES * A_BYTES, sO = sB + STAGES * PB_BYTES, sS = sO + EPI_WARPS * 4096;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * (A_BYTES + PB_BYTES + SFS) + EPI_WARPS * 4096);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto sfull = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
+    const uint32_t tfull = bar0 + 8u * (2 * STAGES + P_SF_BUFS), tempty = tfull + 8u, mma_done = tempty + 8u;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + P_SF_BUFS + 3);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* pp = reinterpret_cast<int*>(bars + 32);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
+        for (int b = 0; b < P_SF_BUFS; ++b) mbar_init(sfull(b), 2 * SF_WARPS);
+        mbar_init(tfull, 1);
+        mbar_init(tempty, 2 * EPI_WARPS);
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmA32);
+    }
+    // (a programmatic dependent: the schedule and the operands are read only from here on)
+    pdl_wait();
+    pdl_trigger();
+    const int G = p.G, ntiles = p.sched[0];
+    const bool fits = p.sched[1] == G && ntiles <= p.max_tiles;      // (else: another call's schedule)
+    if (!fits && blockIdx.x == 0 && threadIdx.x == 0) latch_device_error(p.err, kDevErrBadIndex, 0x203u);
+    if (warp == 2) {                             // pairs of tiles of each group, summed up
+        const int32_t* prefix = p.sched + kSchedHeader;
+        int carry = 0;
+        if (lane == 0) pp[0] = 0;
+        for (int base = 0; base < G; base += 32) {
+            const int g = base + lane;
+            int v = fits && g < G ? (prefix[g + 1] - prefix[g] + 1) >> 1 : 0;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, v, off);
+                if (lane >= off) v += t;
+            }
+            if (g < G) pp[g + 1] = carry + v;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+    tc_fence_before();
+    cluster_sync_all();                          // barriers initialised and both CTAs' tensor memory allocated
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t peer_abort = map_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
+    const int NC = gridDim.x >> 1, cid = blockIdx.x >> 1, total = pp[G] * p.NT;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, last_par = 0;
+            for (int w = cid; w < total && !*abort_flag; w += NC) {
+                const PairItem it = map_pair_item(p.sched, pp, G, p.NT, w, rank);
+                const int boxes = (it.rows + 31) >> 5, n = it.wk.n;
+                const int nb = min(2, max(0, p.NB64 - n * 4 - 2 * (int)rank)), nt = min(2, p.NB128 - 2 * n);
+                const uint8_t* w0 = p.w + (size_t)it.wk.g * p.kst * p.NB64 * 8192 + (size_t)(n * 4 + 2 * (int)rank) * 8192;
+                const uint8_t* s0 = p.w_sf + ((size_t)it.wk.g * p.kst * p.NB128 + 2 * n) * SF_BYTES<F>;
+                const uint8_t* a0 = p.a_sf + (size_t)it.wk.tile * p.kst * SF_BYTES<F>;
+                const uint32_t tx = (uint32_t)(boxes * 4096 + nb * 8192 + (1 + nt) * SF_BYTES<F>);
+                bool ok = true;
+                for (int kb = 0; kb < p.kst; ++kb) {
+                    if (!wait_phase_pair(empty(stage), phase ^ 1u, p.wait_limit, abort_flag, peer_abort, p.err, 0x250u)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t f = full(stage), sf = sS + stage * SFS;
+                    mbar_expect_tx(f, tx);
+                    if (nb) bulk_load(sB + stage * PB_BYTES, w0 + (size_t)kb * p.NB64 * 8192, nb * 8192, f);
+                    if (boxes == 4) tma_load_2d(sA + stage * A_BYTES, &tmA, kb * (SEG_K / 2), it.arow, f);
+                    else
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d(sA + stage * A_BYTES + b * 4096, &tmA32, kb * (SEG_K / 2), it.arow + 32 * b, f);
+                    bulk_load(sf, a0 + (size_t)kb * SF_BYTES<F>, SF_BYTES<F>, f);
+                    bulk_load(sf + SF_BYTES<F>, s0 + (size_t)kb * p.NB128 * SF_BYTES<F>, nt * SF_BYTES<F>, f);
+                    issued |= 1u << stage;
+                    last_par = (last_par & ~(1u << stage)) | (phase << stage);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+            }
+            for (int s = 0; s < STAGES; ++s)        // every issued copy has landed before the CTA exits
+                if (issued & (1u << s)) drain_phase(full(s), (last_par >> s) & 1u, p.err, 0x251u);
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            int stage = 0, b = 0, iter = 0;
+            uint32_t phase = 0, bphase = 0;
+            bool ok = true, ready = false;
+            for (int w = cid; w < total && ok; w += NC, ++iter) {
+                for (int kb = 0; kb < p.kst; ++kb) {
+                    if (!ready)
+                        ok = (kb > 0 || wait_warp_pair<true>(tempty, (iter & 1) ^ 1u, p.wait_limit, abort_flag, peer_abort, p.err, 0x260u)) &&
+                             wait_warp_pair(full(stage), phase, p.wait_limit, abort_flag, peer_abort, p.err, 0x261u) &&
+                             wait_warp_pair<true>(sfull(b), bphase, p.wait_limit, abort_flag, peer_abort, p.err, 0x263u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t s0 = stage, b0 = b;
+                    const bool last = kb + 1 == p.kst;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (++b == P_SF_BUFS) { b = 0; bphase ^= 1u; }
+                    const bool t0 = test_phase(full(stage), phase), t1 = test_phase_cluster(sfull(b), bphase);
+                    const uint64_t da = sw128_desc(sA + s0 * A_BYTES), db = sw128_desc(sB + s0 * PB_BYTES);
+                    const uint32_t d = tm + (iter & 1) * P_ACC2, sfa = tm + P_SF_COL + b0 * COLS, sfb = sfa + PIECES * 4;
+                    const int n = min(4, p.steps - 4 * kb);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k < n) {
+                            const int q = F::ID == MOE_FP4_NV ? k : k / 2;
+                            const uint32_t id = idesc_scaled<F, 2 * BM, P_BN>(F::ID == MOE_FP4_NV ? 0 : k & 1);
+                            mma_scaled_pair<F>(d, da + 2 * k, db + 2 * k, id, sfa + 4 * q, sfb + 8 * q, (kb | k) != 0);
+                        }
+                    }
+                    commit_pair_elected(empty(s0));
+                    if (last) commit_pair_elected(tfull);
+                    ready = __all_sync(0xffffffffu, t0 && t1 && !last);
+                }
+            }
+            commit_pair_elected(mma_done);          // both CTAs learn when every MMA has finished
+        }
+    } else if (warp >= 2 + EPI_WARPS) {
+        const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16, sfull0 = map_rank(sfull(0), 0);
+        int stage = 0, b = 0, old = STAGES - P_SF_BUFS;
+        uint32_t phase = 0, ophase = 1;             // (the rounds before the first count as complete)
+        bool ok = true, loaded = false;
+        for (int w = cid; w < total && ok; w += NC) {
+            for (int kb = 0; kb < p.kst; ++kb) {
+                if (!loaded) ok = wait_warp_pair(full(stage), phase, p.wait_limit, abort_flag, peer_abort, p.err, 0x271u);
+                if (!ok) break;
+                const bool t0 = test_phase(empty(old), ophase);
+                uint32_t v[COLS];
+                const uint32_t src = sS + stage * SFS + lane * 16;
+#pragma unroll
+                for (int q = 0; q < PIECES; ++q) {
+                    ld_shared_v4(src + q * 512, v + 4 * q);
+                    ld_shared_v4(src + SF_BYTES<F> + q * 512, v + 4 * PIECES + 8 * q);
+                    ld_shared_v4(src + 2 * SF_BYTES<F> + q * 512, v + 4 * PIECES + 8 * q + 4);
+                }
+                if (!__all_sync(0xffffffffu, t0))
+                    ok = wait_warp_pair(empty(old), ophase, p.wait_limit, abort_flag, peer_abort, p.err, 0x270u);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t dst = tmem + quarter + P_SF_COL + b * COLS;
+#pragma unroll
+                for (int c = 0; c < COLS; c += 16) {
+                    if (c + 16 <= COLS) tmem_st16(dst + c, v + c);
+                    else tmem_st8(dst + c, v + c);
+                }
+                const uint32_t sb = sfull0 + 8u * b;
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                if (++old == STAGES) { old = 0; ophase ^= 1u; }
+                if (++b == P_SF_BUFS) b = 0;
+                const bool t1 = test_phase(full(stage), phase);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                loaded = __all_sync(0xffffffffu, t1);
+                if (lane == 0) mbar_arrive_cluster(sb);
+            }
+        }
+    } else {
+        const int quarter = 32 * (warp & 3), half = (warp - 2) >> 2, r = quarter + lane;
+        const uint32_t tempty0 = map_rank(tempty, 0);
+        int iter = 0;
+        for (int w = cid; w < total; w += NC, ++iter) {
+            if (!wait_warp_pair(tfull, iter & 1, p.wait_limit, abort_flag, peer_abort, p.err, 0x280u)) break;
+            tc_fence_after();
+            const Work wk = map_pair_item(p.sched, pp, G, p.NT, w, rank).wk;
+            const uint32_t tbase = tmem + (iter & 1) * P_ACC2 + ((uint32_t)quarter << 16);
+            const int nb = min(4, p.NB64 - wk.n * 4);
+            auto hand_back = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(tempty0);
+            };
+            // the chunks whose columns the next tile shares come first: the last two of an even tile, the first two of an odd
+            const int first = (iter & 1 ? 0 : 2) + half, second = first ^ 2;
+            const bool rows = wk.row0 + quarter < wk.row1, live = wk.row0 + r < wk.row1;
+            if (rows && first < nb)
+                epilogue_chunk<F, EPI>(p, &tmO, sO + (warp - 2) * 4096, wk, tbase + 64 * first, wk.n * P_BN + 64 * first, r, live,
+                                       hand_back);
+            else hand_back();
+            if (rows && second < nb)
+                epilogue_chunk<F, EPI>(p, &tmO, sO + (warp - 2) * 4096, wk, tbase + 64 * second, wk.n * P_BN + 64 * second, r, live,
+                                       [] {});
+        }
+        if (lane == 0) bulk_wait_read_all();         // every box read out of shared memory before the CTA exits
+    }
+    cluster_sync_all();                          // every role of both CTAs has left its loop
+    if (warp == 1 && lane == 0) drain_phase(mma_done, 0, p.err, 0x262u);
+    tc_fence_before();
+    cluster_sync_all();                      // MMAs done, both CTAs' copies landed, all arrivals on the other CTA made
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, TMEM_COLS);
+    }
+}
+
 
 // ---------------------------------------------------------------------------------------------------
 // host
@@ -453,6 +788,40 @@ static int codes_map(CUtensorMap* m, const void* base, long long rows, int pitch
     return MOE_OK;
 }
 
+// Output [rows][N] of any supported type, boxes of 32 rows x 128 bytes.
+static int out_map(CUtensorMap* m, void* base, long long rows, int N, long long ldo, int dtype) {
+    auto fn = encode_fn();
+    MOE_REQUIRE(fn, MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable from the driver");
+    const int el = dtype == MOE_F32 ? 4 : 2;
+    cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ldo * el};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / el), 32};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(m, dtype == MOE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                          2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    MOE_REQUIRE(r == CUDA_SUCCESS, MOE_ERR_CUDA, "cuTensorMapEncodeTiled (output) failed (%d) rows=%lld N=%d", (int)r, rows, N);
+    return MOE_OK;
+}
+
+// The tensor maps of a launch; the output is stored by TMA where its rows allow a map (16-byte aligned rows).
+template <int EPI>
+static int make_maps(const void* a_codes, long long rows, int K, Params& p, CUtensorMap* m, CUtensorMap* m32, CUtensorMap* mo) {
+    const int pitch = pad64(K) / 2;
+    if (int rc = codes_map(m, a_codes, rows, pitch, BM)) return rc;
+    if (int rc = codes_map(m32, a_codes, rows, pitch, 32)) return rc;
+    *mo = *m;
+    if (EPI == EPI_OUT) {
+        const int el = p.out_dtype == MOE_F32 ? 4 : 2;
+        p.vec = aligned16(p.out) && (long long)p.ldo * el % 16 == 0;
+        p.boxed = p.vec && rows >= 32;
+        if (p.boxed)
+            if (int rc = out_map(mo, p.out, rows, p.N, p.ldo, p.out_dtype)) return rc;
+    }
+    return MOE_OK;
+}
+
 template <class F, class C, int EPI>
 static int launch(const void* a_codes, long long rows, int K, Params p, cudaStream_t s) {
     constexpr int smem = C::template SMEM<F>;
@@ -467,13 +836,41 @@ static int launch(const void* a_codes, long long rows, int K, Params p, cudaStre
         if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "fp4 product smem attribute: %s", cudaGetErrorString(e));
         attr_ctx[dev] = context_id();
     }
-    CUtensorMap m, m32;
-    const int pitch = pad64(K) / 2;
-    if (int rc = codes_map(&m, a_codes, rows, pitch, BM)) return rc;
-    if (int rc = codes_map(&m32, a_codes, rows, pitch, 32)) return rc;
+    CUtensorMap m, m32, mo;
+    if (int rc = make_maps<EPI>(a_codes, rows, K, p, &m, &m32, &mo)) return rc;
     p.NT = cdiv(p.NB64, C::BN / 64);
-    return check_launch(launch_pdl(fp4_gemm_kernel<F, C, EPI>, dim3(num_sms()), dim3(THREADS), smem, s, m, m32, p),
+    return check_launch(launch_pdl(fp4_gemm_kernel<F, C, EPI>, dim3(num_sms()), dim3(THREADS), smem, s, m, m32, mo, p),
                         EPI == EPI_SWIGLU ? "fp4_gemm_kernel<swiglu>" : "fp4_gemm_kernel");
+}
+
+template <class F, int EPI>
+static int launch_pair(const void* a_codes, long long rows, int K, Params p, cudaStream_t s) {
+    constexpr int smem = P_SMEM<F>;
+    static int clusters[64];                     // resident pairs, in the context they were asked for
+    static unsigned long long attr_ctx[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return set_error(MOE_ERR_CUDA, "fp4 product: no usable current device");
+    const unsigned long long ctx = context_id();
+    if (!clusters[dev] || ctx == 0 || attr_ctx[dev] != ctx) {
+        cudaError_t e = cudaFuncSetAttribute(fp4_gemm_pair_kernel<F, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "fp4 product smem attribute: %s", cudaGetErrorString(e));
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * (num_sms() / 2));
+        cfg.blockDim = dim3(THREADS);
+        cfg.dynamicSmemBytes = smem;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, fp4_gemm_pair_kernel<F, EPI>, &cfg);
+        if (e != cudaSuccess || n <= 0)
+            return set_error(MOE_ERR_CUDA, "fp4 product: no resident cluster of two CTAs (%s)", cudaGetErrorString(e));
+        clusters[dev] = std::min(n, num_sms() / 2);
+        attr_ctx[dev] = context_id();
+    }
+    CUtensorMap m, m32, mo;
+    if (int rc = make_maps<EPI>(a_codes, rows, K, p, &m, &m32, &mo)) return rc;
+    p.NT = cdiv(p.NB64, 4);
+    return check_launch(launch_pdl(fp4_gemm_pair_kernel<F, EPI>, dim3(2 * clusters[dev]), dim3(THREADS), smem, s, m, m32, mo, p),
+                        EPI == EPI_SWIGLU ? "fp4_gemm_pair_kernel<swiglu>" : "fp4_gemm_pair_kernel");
 }
 
 using Wide = Cfg<192, 4>;
@@ -485,6 +882,7 @@ using Narrow = Cfg<64, 6>;
 template <class F, int EPI>
 static int product(const void* a_codes, long long rows, int G, int K, const Params& p, cudaStream_t s) {
     const long long tiles = std::min<long long>(rows, G) + rows / BM;      // about this many m-tiles
+    if (rows >= 256LL * G && tiles * cdiv(p.NB64, 4) >= 2LL * num_sms()) return launch_pair<F, EPI>(a_codes, rows, K, p, s);
     if (tiles * cdiv(p.NB64, 3) >= 2LL * num_sms()) return launch<F, Wide, EPI>(a_codes, rows, K, p, s);
     if (tiles * cdiv(p.NB64, 2) >= 2LL * num_sms()) return launch<F, Mid, EPI>(a_codes, rows, K, p, s);
     return launch<F, Narrow, EPI>(a_codes, rows, K, p, s);
