@@ -129,6 +129,9 @@ __device__ __forceinline__ bool test_phase(uint32_t bar, uint32_t parity) {
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
+__device__ __forceinline__ bool test_warp(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, test_phase(bar, parity));
+}
 // 16 columns of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
@@ -472,17 +475,19 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 // wait for it, pass the news on with their arrival on the even CTA's scale barrier, so that barrier tells of both CTAs'
 // operands. A pair takes two consecutive tiles of one group; where the second does not exist the odd CTA computes the
 // first one again and stores nothing.
-// Tensor memory has no room for two accumulators of 256 columns next to the scales: they overlap by 96 columns. The
-// epilogue reads the shared columns into registers first and frees them at once, so the next tile's MMAs wait for a read
-// of two of its four chunks and not for their conversion and stores.
+// The scales of the weight rows come from the scale warps, those of A's rows by tcgen05.cp from the MMA warp: four copies
+// a stage fit beside four MMAs of 256 columns at no cost, and leave tensor memory for three stages of the others.
+// Tensor memory has no room for two accumulators of 256 columns next to the scales: they share 128 columns. The epilogue
+// reads the shared columns into registers first and frees them at once, so the next tile's MMAs wait for a read of two of
+// its four chunks and not for their conversion and stores.
 constexpr int PB_BYTES = 128 * SEG_K / 2;        // a CTA's half of the weight rows
-constexpr int P_STAGES = 4, P_BN = 256, P_SF_BUFS = 2, P_ACC2 = 160, P_SF_COL = P_ACC2 + P_BN;
+constexpr int P_STAGES = 4, P_BN = 256, P_SF_BUFS = 3, P_ACC2 = 128, P_SF_COL = P_ACC2 + P_BN, P_SFA_COL = P_SF_COL + 96;
 constexpr int P_MAX_G = 1024;
 template <class F> constexpr int P_SFS = 3 * SF_BYTES<F>;
 template <class F> constexpr int P_SMEM = 1024 + EPI_WARPS * 4096 + P_STAGES * (A_BYTES + PB_BYTES + P_SFS<F>) + 256 +
                                           (P_MAX_G + 1) * 4;
-template <class F> constexpr int P_COLS = SF_PIECES<F> * 12;
-static_assert(P_SF_COL + P_SF_BUFS * P_COLS<Nv> <= TMEM_COLS, "tensor memory columns");
+template <class F> constexpr int P_COLS = SF_PIECES<F> * 8;      // scale columns of the weight rows in a stage
+static_assert(P_SF_BUFS * P_COLS<Nv> <= 96 && P_SFA_COL + 2 * SF_PIECES<Nv> * 4 <= TMEM_COLS, "tensor memory columns");
 static_assert(P_SMEM<Nv> <= 227 * 1024, "shared memory per CTA");
 
 template <class F>
@@ -499,23 +504,28 @@ __device__ __forceinline__ void mma_scaled_pair(uint32_t d, uint64_t a, uint64_t
             "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
             ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb) : "memory");
 }
+// 32 rows of 16 bytes (8-row groups 128 bytes apart) of each CTA's shared memory -> the same 4 columns of each quarter of
+// its tensor memory lanes.
+__device__ __forceinline__ void sf_copy_pair(uint32_t taddr, uint32_t saddr) {
+    const uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1 << 46;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(d) : "memory");
+}
 // On both CTAs' barrier at this offset.
 __device__ __forceinline__ void commit_pair_elected(uint32_t bar) {
     asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
                  "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
                  ::"r"(bar), "h"((uint16_t)3) : "memory");
 }
-__device__ __forceinline__ bool test_phase_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
+__device__ __forceinline__ void arrive_pair(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-template <bool CLUSTER = false>
+// (What the other CTA's arrivals tell of lies in tensor memory and in asynchronously filled shared memory, ordered by the
+// tcgen05 fences on both sides; an acquire at cluster scope, which orders ordinary loads too, cost 450 cycles a wait.)
 __device__ __forceinline__ bool wait_warp_pair(uint32_t bar, uint32_t parity, long long limit, volatile int* abort_flag,
                                                uint32_t peer_abort, unsigned* err, unsigned site) {
     for (long long i = 0; i < limit; ++i) {
-        if (__all_sync(0xffffffffu, CLUSTER ? mbar_try_wait_acq_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
         if (__any_sync(0xffffffffu, *abort_flag)) return false;
     }
     if ((threadIdx.x & 31) == 0) {
@@ -651,27 +661,34 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             for (int w = cid; w < total && ok; w += NC, ++iter) {
                 for (int kb = 0; kb < p.kst; ++kb) {
                     if (!ready)
-                        ok = (kb > 0 || wait_warp_pair<true>(tempty, (iter & 1) ^ 1u, p.wait_limit, abort_flag, peer_abort, p.err, 0x260u)) &&
-                             wait_warp_pair(full(stage), phase, p.wait_limit, abort_flag, peer_abort, p.err, 0x261u) &&
-                             wait_warp_pair<true>(sfull(b), bphase, p.wait_limit, abort_flag, peer_abort, p.err, 0x263u);
+                        ok = (kb > 0 || wait_warp_pair(tempty, (iter & 1) ^ 1u, p.wait_limit, abort_flag, peer_abort, p.err, 0x260u)) &&
+                             wait_warp_pair(sfull(b), bphase, p.wait_limit, abort_flag, peer_abort, p.err, 0x263u) &&
+                             (test_warp(full(stage), phase) ||
+                              wait_warp_pair(full(stage), phase, p.wait_limit, abort_flag, peer_abort, p.err, 0x261u));
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t s0 = stage, b0 = b;
                     const bool last = kb + 1 == p.kst;
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                    if (++b == P_SF_BUFS) { b = 0; bphase ^= 1u; }
-                    const bool t0 = test_phase(full(stage), phase), t1 = test_phase_cluster(sfull(b), bphase);
                     const uint64_t da = sw128_desc(sA + s0 * A_BYTES), db = sw128_desc(sB + s0 * PB_BYTES);
-                    const uint32_t d = tm + (iter & 1) * P_ACC2, sfa = tm + P_SF_COL + b0 * COLS, sfb = sfa + PIECES * 4;
-                    const int n = min(4, p.steps - 4 * kb);
+                    const uint32_t d = tm + (iter & 1) * P_ACC2, sfb = tm + P_SF_COL + b0 * COLS,
+                                   sfa = tm + P_SFA_COL + (kb & 1) * PIECES * 4;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int q = 0; q < PIECES; ++q) sf_copy_pair(sfa + 4 * q, sS + s0 * SFS + q * 512);
+                    const int n = min(4, p.steps - 4 * kb);
+                    auto step = [&](int k) {
                         if (k < n) {
                             const int q = F::ID == MOE_FP4_NV ? k : k / 2;
                             const uint32_t id = idesc_scaled<F, 2 * BM, P_BN>(F::ID == MOE_FP4_NV ? 0 : k & 1);
                             mma_scaled_pair<F>(d, da + 2 * k, db + 2 * k, id, sfa + 4 * q, sfb + 8 * q, (kb | k) != 0);
                         }
-                    }
+                    };
+                    step(0);
+                    step(1);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (++b == P_SF_BUFS) { b = 0; bphase ^= 1u; }
+                    const bool t0 = test_phase(full(stage), phase), t1 = test_phase(sfull(b), bphase);
+                    step(2);
+                    step(3);
                     commit_pair_elected(empty(s0));
                     if (last) commit_pair_elected(tfull);
                     ready = __all_sync(0xffffffffu, t0 && t1 && !last);
@@ -690,12 +707,11 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 if (!ok) break;
                 const bool t0 = test_phase(empty(old), ophase);
                 uint32_t v[COLS];
-                const uint32_t src = sS + stage * SFS + lane * 16;
+                const uint32_t src = sS + stage * SFS + SF_BYTES<F> + lane * 16;
 #pragma unroll
                 for (int q = 0; q < PIECES; ++q) {
-                    ld_shared_v4(src + q * 512, v + 4 * q);
-                    ld_shared_v4(src + SF_BYTES<F> + q * 512, v + 4 * PIECES + 8 * q);
-                    ld_shared_v4(src + 2 * SF_BYTES<F> + q * 512, v + 4 * PIECES + 8 * q + 4);
+                    ld_shared_v4(src + q * 512, v + 8 * q);
+                    ld_shared_v4(src + SF_BYTES<F> + q * 512, v + 8 * q + 4);
                 }
                 if (!__all_sync(0xffffffffu, t0))
                     ok = wait_warp_pair(empty(old), ophase, p.wait_limit, abort_flag, peer_abort, p.err, 0x270u);
@@ -704,8 +720,7 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 const uint32_t dst = tmem + quarter + P_SF_COL + b * COLS;
 #pragma unroll
                 for (int c = 0; c < COLS; c += 16) {
-                    if (c + 16 <= COLS) tmem_st16(dst + c, v + c);
-                    else tmem_st8(dst + c, v + c);
+                    tmem_st16(dst + c, v + c);
                 }
                 const uint32_t sb = sfull0 + 8u * b;
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -715,7 +730,7 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 loaded = __all_sync(0xffffffffu, t1);
-                if (lane == 0) mbar_arrive_cluster(sb);
+                if (lane == 0) arrive_pair(sb);
             }
         }
     } else {
@@ -731,7 +746,7 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             auto hand_back = [&] {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(tempty0);
+                if (lane == 0) arrive_pair(tempty0);
             };
             // the chunks whose columns the next tile shares come first: the last two of an even tile, the first two of an odd
             const int first = (iter & 1 ? 0 : 2) + half, second = first ^ 2;
