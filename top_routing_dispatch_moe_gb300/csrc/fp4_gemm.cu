@@ -66,6 +66,9 @@ struct Params {
     long long wait_limit;
 };
 
+// The value of lane 0, known to the compiler to be the same in the warp: branches on it and what depends on it stay uniform.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 struct Work { int g, tile, row0, row1, n; };
 
 // Item w: group by group, n-tile next, m-tile fastest: CTAs that run together share a weight tile.
@@ -288,7 +291,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5 + SF_BUFS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
         for (int a = 0; a < 2; ++a) { mbar_init(tfull(a), 1); mbar_init(tempty(a), EPI_WARPS); }
@@ -309,7 +312,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     pdl_trigger();
     const int G = p.G, ntiles = p.sched[0];
     const bool fits = p.sched[1] == G && ntiles <= p.max_tiles;      // (else: another call's schedule)
-    const int total = fits ? ntiles * p.NT : 0;
+    const int total = uniform(fits ? ntiles * p.NT : 0);
     if (!fits && blockIdx.x == 0 && threadIdx.x == 0) latch_device_error(p.err, kDevErrBadIndex, 0x203u);
 
     if (warp == 0) {
@@ -440,9 +443,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         int iter = 0;
         for (int w = blockIdx.x; w < total; w += gridDim.x, ++iter) {
             const int a = iter & 1;
+            const Work wk = map_work(p.sched, G, p.NT, w);       // (before the wait: its loads take a while)
             if (!wait_warp(tfull(a), (iter >> 1) & 1, p.wait_limit, abort_flag, p.err, 0x230u)) break;
             tc_fence_after();
-            const Work wk = map_work(p.sched, G, p.NT, w);
             const uint32_t tbase = tmem + a * BN + ((uint32_t)quarter << 16);
             if (wk.row0 + quarter < wk.row1) {
                 const int nb = min(BN / 64, p.NB64 - wk.n * (BN / 64));
@@ -573,7 +576,7 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* pp = reinterpret_cast<int*>(bars + 32);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
@@ -614,7 +617,7 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t peer_abort = map_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
-    const int NC = gridDim.x >> 1, cid = blockIdx.x >> 1, total = pp[G] * p.NT;
+    const int NC = gridDim.x >> 1, cid = blockIdx.x >> 1, total = uniform(pp[G] * p.NT);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -738,9 +741,9 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         const uint32_t tempty0 = map_rank(tempty, 0);
         int iter = 0;
         for (int w = cid; w < total; w += NC, ++iter) {
+            const Work wk = map_pair_item(p.sched, pp, G, p.NT, w, rank).wk;   // (before the wait: its loads take a while)
             if (!wait_warp_pair(tfull, iter & 1, p.wait_limit, abort_flag, peer_abort, p.err, 0x280u)) break;
             tc_fence_after();
-            const Work wk = map_pair_item(p.sched, pp, G, p.NT, w, rank).wk;
             const uint32_t tbase = tmem + (iter & 1) * P_ACC2 + ((uint32_t)quarter << 16);
             const int nb = min(4, p.NB64 - wk.n * 4);
             auto hand_back = [&] {
