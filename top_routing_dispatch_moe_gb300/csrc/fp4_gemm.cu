@@ -85,13 +85,22 @@ __device__ __forceinline__ Work map_work(const int32_t* sched, int G, int NT, in
     return Work{e.x, t, e.y, e.z, n};
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+// The producer's and the MMA warp's operations. The whole warp runs its loop, with conditions that are the same in all lanes
+// (votes, uniform()), and one elected lane, the same each time, issues: addresses and descriptors then stay in uniform
+// registers. Issued from a branch that one lane takes, a stage of four MMAs cost 690 cycles, where they take 4 x 96 (N = 192).
+#define MOE_ELECTED(op) "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t@e " op "\n\t}"
+__device__ __forceinline__ void expect_elected(uint32_t bar, uint32_t bytes) {
+    asm volatile(MOE_ELECTED("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;") ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_elected(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(MOE_ELECTED("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];")
                  ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
-// The MMA warp's operations. The whole warp runs its loop, with conditions that are the same in all lanes (votes), and one
-// elected lane, the same each time, issues: the operands then stay in uniform registers. Issued from a branch that one
-// lane takes, a stage cost 690 cycles, where its four MMAs take 4 x 96 (N = 192).
+__device__ __forceinline__ void tma_elected(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(MOE_ELECTED("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                             " [%0], [%1, {%2, %3}], [%4];")
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
 template <class F>
 __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                            uint32_t accumulate) {
@@ -316,39 +325,40 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     if (!fits && blockIdx.x == 0 && threadIdx.x == 0) latch_device_error(p.err, kDevErrBadIndex, 0x203u);
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, issued = 0, last_par = 0;
-            for (int w = blockIdx.x; w < total && !*abort_flag; w += gridDim.x) {
-                const Work wk = map_work(p.sched, G, p.NT, w);
-                const int boxes = (wk.row1 - wk.row0 + 31) >> 5;
-                const int nb = min(BN / 64, p.NB64 - wk.n * (BN / 64));
-                const int t0 = wk.n * BN / 128, nt = min((wk.n * BN + BN + 127) / 128, p.NB128) - t0;
-                const uint8_t* w0 = p.w + (size_t)wk.g * p.kst * p.NB64 * 8192 + (size_t)wk.n * (BN / 64) * 8192;
-                const uint8_t* s0 = p.w_sf + ((size_t)wk.g * p.kst * p.NB128 + t0) * SF_BYTES<F>;
-                const uint8_t* a0 = p.a_sf + (size_t)wk.tile * p.kst * SF_BYTES<F>;
-                const uint32_t tx = (uint32_t)(boxes * 4096 + nb * 8192 + (1 + nt) * SF_BYTES<F>);
-                bool ok = true;
-                for (int kb = 0; kb < p.kst; ++kb) {
-                    if (!wait_phase(empty(stage), phase ^ 1u, p.wait_limit, abort_flag, p.err, 0x210u)) { ok = false; break; }
-                    const uint32_t f = full(stage), sf = sS + stage * SFS;
-                    mbar_expect_tx(f, tx);
-                    bulk_load(sB + stage * B_BYTES, w0 + (size_t)kb * p.NB64 * 8192, nb * 8192, f);
-                    if (boxes == 4) tma_load_2d(sA + stage * A_BYTES, &tmA, kb * (SEG_K / 2), wk.row0, f);
-                    else
-                        for (int b = 0; b < boxes; ++b)
-                            tma_load_2d(sA + stage * A_BYTES + b * 4096, &tmA32, kb * (SEG_K / 2), wk.row0 + 32 * b, f);
-                    bulk_load(sf, a0 + (size_t)kb * SF_BYTES<F>, SF_BYTES<F>, f);
-                    bulk_load(sf + SF_BYTES<F>, s0 + (size_t)kb * p.NB128 * SF_BYTES<F>, nt * SF_BYTES<F>, f);
-                    issued |= 1u << stage;
-                    last_par = (last_par & ~(1u << stage)) | (phase << stage);
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                }
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, last_par = 0;
+        bool ok = true, ready = false;              // ready: the next ring stage was seen free
+        for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
+            const Work wk = map_work(p.sched, G, p.NT, w);
+            const int n = uniform(wk.n), g = uniform(wk.g), tile = uniform(wk.tile), row0 = uniform(wk.row0);
+            const int boxes = uniform((wk.row1 - wk.row0 + 31) >> 5);
+            const int nb = min(BN / 64, p.NB64 - n * (BN / 64));
+            const int t0 = n * BN / 128, nt = min((n * BN + BN + 127) / 128, p.NB128) - t0;
+            const uint8_t* w0 = p.w + (size_t)g * p.kst * p.NB64 * 8192 + (size_t)n * (BN / 64) * 8192;
+            const uint8_t* s0 = p.w_sf + ((size_t)g * p.kst * p.NB128 + t0) * SF_BYTES<F>;
+            const uint8_t* a0 = p.a_sf + (size_t)tile * p.kst * SF_BYTES<F>;
+            const uint32_t tx = (uint32_t)(boxes * 4096 + nb * 8192 + (1 + nt) * SF_BYTES<F>);
+            for (int kb = 0; kb < p.kst; ++kb) {
+                if (!ready) ok = wait_warp(empty(stage), phase ^ 1u, p.wait_limit, abort_flag, p.err, 0x210u);
                 if (!ok) break;
+                const uint32_t f = full(stage), sf = sS + stage * SFS, sa = sA + stage * A_BYTES;
+                expect_elected(f, tx);
+                bulk_elected(sB + stage * B_BYTES, w0 + (size_t)kb * p.NB64 * 8192, nb * 8192, f);
+                if (boxes == 4) tma_elected(sa, &tmA, kb * (SEG_K / 2), row0, f);
+                else
+                    for (int b = 0; b < boxes; ++b) tma_elected(sa + b * 4096, &tmA32, kb * (SEG_K / 2), row0 + 32 * b, f);
+                bulk_elected(sf + SF_BYTES<F>, s0 + (size_t)kb * p.NB128 * SF_BYTES<F>, nt * SF_BYTES<F>, f);
+                bulk_elected(sf, a0 + (size_t)kb * SF_BYTES<F>, SF_BYTES<F>, f);
+                issued |= 1u << stage;
+                last_par = (last_par & ~(1u << stage)) | (phase << stage);
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                ready = test_warp(empty(stage), phase ^ 1u);
             }
+        }
+        if (lane == 0)
             for (int s = 0; s < STAGES; ++s)        // every issued copy has landed before the CTA exits
                 if (issued & (1u << s)) drain_phase(full(s), (last_par >> s) & 1u, p.err, 0x211u);
-        }
+        __syncwarp();
     } else if (warp == 1) {
         constexpr int PIECES = SF_PIECES<F>;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -620,41 +630,39 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     const int NC = gridDim.x >> 1, cid = blockIdx.x >> 1, total = uniform(pp[G] * p.NT);
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, issued = 0, last_par = 0;
-            for (int w = cid; w < total && !*abort_flag; w += NC) {
-                const PairItem it = map_pair_item(p.sched, pp, G, p.NT, w, rank);
-                const int boxes = (it.rows + 31) >> 5, n = it.wk.n;
-                const int nb = min(2, max(0, p.NB64 - n * 4 - 2 * (int)rank)), nt = min(2, p.NB128 - 2 * n);
-                const uint8_t* w0 = p.w + (size_t)it.wk.g * p.kst * p.NB64 * 8192 + (size_t)(n * 4 + 2 * (int)rank) * 8192;
-                const uint8_t* s0 = p.w_sf + ((size_t)it.wk.g * p.kst * p.NB128 + 2 * n) * SF_BYTES<F>;
-                const uint8_t* a0 = p.a_sf + (size_t)it.wk.tile * p.kst * SF_BYTES<F>;
-                const uint32_t tx = (uint32_t)(boxes * 4096 + nb * 8192 + (1 + nt) * SF_BYTES<F>);
-                bool ok = true;
-                for (int kb = 0; kb < p.kst; ++kb) {
-                    if (!wait_phase_pair(empty(stage), phase ^ 1u, p.wait_limit, abort_flag, peer_abort, p.err, 0x250u)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t f = full(stage), sf = sS + stage * SFS;
-                    mbar_expect_tx(f, tx);
-                    if (nb) bulk_load(sB + stage * PB_BYTES, w0 + (size_t)kb * p.NB64 * 8192, nb * 8192, f);
-                    if (boxes == 4) tma_load_2d(sA + stage * A_BYTES, &tmA, kb * (SEG_K / 2), it.arow, f);
-                    else
-                        for (int b = 0; b < boxes; ++b)
-                            tma_load_2d(sA + stage * A_BYTES + b * 4096, &tmA32, kb * (SEG_K / 2), it.arow + 32 * b, f);
-                    bulk_load(sf, a0 + (size_t)kb * SF_BYTES<F>, SF_BYTES<F>, f);
-                    bulk_load(sf + SF_BYTES<F>, s0 + (size_t)kb * p.NB128 * SF_BYTES<F>, nt * SF_BYTES<F>, f);
-                    issued |= 1u << stage;
-                    last_par = (last_par & ~(1u << stage)) | (phase << stage);
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                }
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, last_par = 0;
+        bool ok = true, ready = false;
+        for (int w = cid; w < total && ok; w += NC) {
+            const PairItem it = map_pair_item(p.sched, pp, G, p.NT, w, rank);
+            const int n = uniform(it.wk.n), g = uniform(it.wk.g), tile = uniform(it.wk.tile), arow = uniform(it.arow);
+            const int boxes = uniform((it.rows + 31) >> 5), half = uniform((int)rank);
+            const int nb = min(2, max(0, p.NB64 - n * 4 - 2 * half)), nt = min(2, p.NB128 - 2 * n);
+            const uint8_t* w0 = p.w + (size_t)g * p.kst * p.NB64 * 8192 + (size_t)(n * 4 + 2 * half) * 8192;
+            const uint8_t* s0 = p.w_sf + ((size_t)g * p.kst * p.NB128 + 2 * n) * SF_BYTES<F>;
+            const uint8_t* a0 = p.a_sf + (size_t)tile * p.kst * SF_BYTES<F>;
+            const uint32_t tx = (uint32_t)(boxes * 4096 + nb * 8192 + (1 + nt) * SF_BYTES<F>);
+            for (int kb = 0; kb < p.kst; ++kb) {
+                if (!ready) ok = wait_warp_pair(empty(stage), phase ^ 1u, p.wait_limit, abort_flag, peer_abort, p.err, 0x250u);
                 if (!ok) break;
+                const uint32_t f = full(stage), sf = sS + stage * SFS, sa = sA + stage * A_BYTES;
+                expect_elected(f, tx);
+                if (nb) bulk_elected(sB + stage * PB_BYTES, w0 + (size_t)kb * p.NB64 * 8192, nb * 8192, f);
+                if (boxes == 4) tma_elected(sa, &tmA, kb * (SEG_K / 2), arow, f);
+                else
+                    for (int b = 0; b < boxes; ++b) tma_elected(sa + b * 4096, &tmA32, kb * (SEG_K / 2), arow + 32 * b, f);
+                bulk_elected(sf + SF_BYTES<F>, s0 + (size_t)kb * p.NB128 * SF_BYTES<F>, nt * SF_BYTES<F>, f);
+                bulk_elected(sf, a0 + (size_t)kb * SF_BYTES<F>, SF_BYTES<F>, f);
+                issued |= 1u << stage;
+                last_par = (last_par & ~(1u << stage)) | (phase << stage);
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                ready = test_warp(empty(stage), phase ^ 1u);
             }
+        }
+        if (lane == 0)
             for (int s = 0; s < STAGES; ++s)        // every issued copy has landed before the CTA exits
                 if (issued & (1u << s)) drain_phase(full(s), (last_par >> s) & 1u, p.err, 0x251u);
-        }
+        __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
