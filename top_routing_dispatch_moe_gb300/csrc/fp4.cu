@@ -3,7 +3,7 @@
 // Quantisation and its inverse are bound by memory: x is read once and 0.5 + 1 / BLK bytes a value are written (or the
 // other way round). A lane owns 16 consecutive columns (two 16-byte loads of bf16, one 8-byte store of codes), so an NV
 // block lives in one lane and an MX block in a pair of lanes; a warp covers 512 columns of a row, or several rows where
-// rows are narrower. Each warp keeps the loads of four items in flight.
+// rows are narrower.
 #include <algorithm>
 #include "fp4.cuh"
 
@@ -23,6 +23,8 @@ template <> __device__ __forceinline__ float rounded<float>(float v) { return v;
 template <> __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
 
+// Units whose loads a lane keeps in flight: with four blocks of 256 threads an SM has 64 KB under way.
+template <typename T> constexpr int IN_FLIGHT = 4 / (int)sizeof(T);
 // 16 elements as they lie in memory.
 template <typename T> struct alignas(16) Raw16 { uint4 q[sizeof(T)]; };
 
@@ -47,71 +49,109 @@ __device__ __forceinline__ Raw16<T> load_unit(const T* __restrict__ row, int k0,
     return r;
 }
 
-// The codes (2 words) and, on the lane that owns it, the scale byte of this lane's unit; MX blocks span lanes 2i, 2i + 1.
+// The largest magnitude of a unit, NaN if an element is one; 16-bit types two at a time.
+__device__ __forceinline__ float unit_amax(const Raw16<float>& raw) {
+    const float* e = reinterpret_cast<const float*>(raw.q);
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < UNIT; ++i) m = max_nan(m, fabsf(e[i]));
+    return m;
+}
+__device__ __forceinline__ float unit_amax(const Raw16<__nv_bfloat16>& raw) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(raw.q);
+    uint32_t m = w[0];
+#pragma unroll
+    for (int i = 1; i < UNIT / 2; ++i) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+    return max_nan(fabsf(__uint_as_float(m << 16)), fabsf(__uint_as_float(m & 0xFFFF0000u)));
+}
+__device__ __forceinline__ float unit_amax(const Raw16<__half>& raw) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(raw.q);
+    uint32_t m = w[0];
+#pragma unroll
+    for (int i = 1; i < UNIT / 2; ++i) asm("max.NaN.xorsign.abs.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    return max_nan(fabsf(f.x), fabsf(f.y));
+}
+
+// The codes (2 words) and the scale byte of this lane's unit; an MX block spans lanes 2i and 2i + 1. (max |x g| is
+// max |x| times |g|: rounding keeps the order.)
 template <class F, typename T>
-__device__ __forceinline__ uint2 quantize_unit(const Raw16<T>& raw, const float* gscale, float g, uint32_t& byte) {
-    const T* e = reinterpret_cast<const T*>(raw.q);
-    float v[32], amax = 0.f;             // (block_codes takes whole blocks: an MX lane uses the lower half alone)
-#pragma unroll
-    for (int i = 0; i < UNIT; ++i) {
-        v[i] = as_f32(e[i]);
-        if (gscale) v[i] *= g;
-        amax = max_nan(amax, fabsf(v[i]));
-    }
+__device__ __forceinline__ uint2 quantize_unit(const Raw16<T>& raw, bool scaled, float g, uint32_t& byte) {
+    float amax = unit_amax(raw);
     if constexpr (F::ID == MOE_FP4_MX) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    float s, r;
-    byte = block_scale<F>(amax, s, r);
-    uint32_t w[4];
-    if constexpr (F::ID == MOE_FP4_MX) {
+    if (scaled) amax = fabsf(amax * g);
+    const T* e = reinterpret_cast<const T*>(raw.q);
+    float v[UNIT], s, r;
 #pragma unroll
-        for (int i = UNIT; i < 32; ++i) v[i] = 0.f;
+    for (int i = 0; i < UNIT; ++i) v[i] = as_f32(e[i]);
+    if (scaled) {
+#pragma unroll
+        for (int i = 0; i < UNIT; i += 2) mul2(v + i, v + i, g);
     }
-    block_codes<F>(v, amax, s, r, w);
+    byte = block_scale<F>(amax, s, r);
+    uint32_t w[2];
+    block_codes<F, UNIT>(v, amax, s, r, w);
     return make_uint2(w[0], w[1]);
 }
+
+// Items of the row-major kernels, `step` apart, as (row group, segment) without a division each.
+struct Walk {
+    int row, seg, drow, dseg, nseg;
+    long long left;                      // items still to come, this one included, in steps
+    __device__ __forceinline__ Walk(long long first, long long step, long long items, int nseg_) : nseg(nseg_) {
+        left = first < items ? (items - first + step - 1) / step : 0;
+        row = (int)(first / nseg);
+        seg = (int)(first - (long long)row * nseg);
+        drow = (int)(step / nseg);
+        dseg = (int)(step - (long long)drow * nseg);
+    }
+    __device__ __forceinline__ void next() {
+        --left;
+        row += drow;
+        seg += dseg;
+        if (seg >= nseg) { seg -= nseg; ++row; }
+    }
+};
 
 // Row-major form: codes [rows][pitch], scales [rows][nb]. An item is one row segment of lpr units, 32 / lpr rows to a
 // warp (lpr: a power of two, the units of a row where there are fewer than 32).
 template <class F, typename T, bool VEC>
-__global__ void __launch_bounds__(QTHREADS)
+__global__ void __launch_bounds__(QTHREADS, 4)
 quantize_rows_kernel(const T* __restrict__ x, long long ldx, int x_rows, const int32_t* __restrict__ src, int rows, int K,
                      int lpr, const float* __restrict__ gscale, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                      unsigned* err) {
-    constexpr int U = 4;
+    constexpr int U = IN_FLIGHT<T>;
     const int lane = threadIdx.x & 31;
     const int units = (K + 31) / 32 * 2;
     const int nseg = (units + lpr - 1) / lpr, rpw = 32 / lpr, sub = lane / lpr;
     const int nb = (K + F::BLK - 1) / F::BLK;
     const size_t pitch = (size_t)units * 8;
     const float g = gscale ? __ldg(gscale) : 1.f;
-    const long long items = (long long)((rows + rpw - 1) / rpw) * nseg;
-    const long long step = (long long)gridDim.x * QWARPS;
-    for (long long it0 = (long long)blockIdx.x * QWARPS + (threadIdx.x >> 5); it0 < items; it0 += U * step) {
+    const int col = lane - sub * lpr;
+    Walk at((long long)blockIdx.x * QWARPS + (threadIdx.x >> 5), (long long)gridDim.x * QWARPS,
+            (long long)((rows + rpw - 1) / rpw) * nseg, nseg);
+    while (at.left > 0) {
         Raw16<T> raw[U];
         int row[U], unit[U];
+        const int n = (int)min(at.left, (long long)U);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const long long it = it0 + i * step;
-            row[i] = rows;
-            unit[i] = units;
-            if (it < items) {
-                const int rg = (int)(it / nseg);
-                row[i] = rg * rpw + sub;
-                unit[i] = (int)(it - (long long)rg * nseg) * lpr + (lane - sub * lpr);
-            }
+            row[i] = i < n ? at.row * rpw + sub : rows;
+            unit[i] = at.seg * lpr + col;
             const bool live = row[i] < rows && unit[i] < units;
             int from = row[i];
             if (live && src) {
                 from = __ldg(src + row[i]);
                 if (from >= x_rows || from < -1) { latch_device_error(err, kDevErrBadIndex, 0x200u); from = -1; }
             }
-            raw[i] = load_unit<T, VEC>(x + (long long)max(from, 0) * ldx, unit[i] * UNIT, live && from >= 0 ? K : 0);
+            raw[i] = load_unit<T, VEC>(x + (long long)(live ? max(from, 0) : 0) * ldx, unit[i] * UNIT, live && from >= 0 ? K : 0);
+            at.next();
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            if (it0 + i * step >= items) break;
+            if (i >= n) break;
             uint32_t byte;
-            const uint2 w = quantize_unit<F>(raw[i], gscale, g, byte);
+            const uint2 w = quantize_unit<F>(raw[i], gscale != nullptr, g, byte);
             if (row[i] < rows && unit[i] < units) {
                 *reinterpret_cast<uint2*>(codes + row[i] * pitch + (size_t)unit[i] * 8) = w;
                 const int b = unit[i] * UNIT / F::BLK;
@@ -125,11 +165,11 @@ quantize_rows_kernel(const T* __restrict__ x, long long ldx, int x_rows, const i
 // one (tile, 512 columns) item at a time: its warps take the rows in turn, the scale bytes meet in shared memory (pieces
 // 528 bytes apart, so that the pieces of one row fall into different banks) and leave as whole pieces.
 template <class F, typename T, bool VEC>
-__global__ void __launch_bounds__(QTHREADS)
+__global__ void __launch_bounds__(QTHREADS, 4)
 quantize_operand_kernel(const T* __restrict__ x, long long ldx, int x_rows, const int32_t* __restrict__ src,
                         const int32_t* __restrict__ sched, int G, int max_tiles, int K, const float* __restrict__ gscale,
                         uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, unsigned* err) {
-    constexpr int U = 4, PIECES = 2 * SF_PIECES<F>, STRIDE = 528;
+    constexpr int U = IN_FLIGHT<T>, PIECES = 2 * SF_PIECES<F>, STRIDE = 528;
     __shared__ __align__(16) uint8_t s_sf[PIECES * STRIDE];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int units = (K + 63) / 64 * 4, kst = (K + SEG_K - 1) / SEG_K;
@@ -166,7 +206,7 @@ quantize_operand_kernel(const T* __restrict__ x, long long ldx, int x_rows, cons
                 const int r = r0 + i * QWARPS;
                 if (r >= n) break;
                 uint32_t byte;
-                const uint2 w = quantize_unit<F>(raw[i], gscale, g, byte);
+                const uint2 w = quantize_unit<F>(raw[i], gscale != nullptr, g, byte);
                 if (unit < units) *reinterpret_cast<uint2*>(codes + (size_t)(ent.y + r) * pitch + (size_t)unit * 8) = w;
                 const int b = lane * UNIT / F::BLK;
                 if (lane * UNIT % F::BLK == 0)
@@ -182,38 +222,59 @@ quantize_operand_kernel(const T* __restrict__ x, long long ldx, int x_rows, cons
     }
 }
 
-// Codes and scales -> rows. v = code * scale is exact in fp32 (2 and 4 significant bits); v / g as the rounded quotient:
-// with r the rounded reciprocal of g, q = v r and q + (v - q g) r (the correction of block_codes), or the division
-// itself where the exponents come near the ends of the range.
+// Sixteen codes under one scale -> values, exact in fp32 (2 and 4 significant bits; NV in fp16 too, two at a time), divided
+// by g where there is one: the rounded quotient (quotient2), or the division itself where scale or g come near the ends of
+// the range.
+template <class F>
+__device__ __forceinline__ void unit_values(uint2 c, uint32_t sb, bool scaled, float g, float r, float* v) {
+    const uint32_t w[2] = {c.x, c.y};
+    const float s = scale_value<F>(sb);
+    const __half2 sh = __float2half2_rn(s);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        uint32_t h2;
+        asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h2) : "r"(w[j >> 2] >> (8 * (j & 3))));
+        __half2 h = *reinterpret_cast<const __half2*>(&h2);
+        if constexpr (F::ID == MOE_FP4_NV) h = __hmul2(h, sh);
+        const float2 f = __half22float2(h);
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+        if constexpr (F::ID == MOE_FP4_MX) mul2(v + 2 * j, v + 2 * j, s);
+    }
+    if (!scaled) return;
+    const float m = fabsf(s), a = fabsf(g);
+    if ((m < 1e15f && m > 1e-15f && a < 1e15f && a > 1e-15f) || m == 0.f) {
+#pragma unroll
+        for (int j = 0; j < UNIT; j += 2) quotient2(v + j, g, r);
+    } else {
+#pragma unroll
+        for (int j = 0; j < UNIT; ++j) v[j] = __fdiv_rn(v[j], g);
+    }
+}
+
 template <class F, typename T, bool VEC>
-__global__ void __launch_bounds__(QTHREADS)
+__global__ void __launch_bounds__(QTHREADS, 4)
 dequantize_rows_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int rows, int K, int lpr,
                        const float* __restrict__ gscale, T* __restrict__ out, long long ldo) {
-    constexpr int U = 4;
+    constexpr int U = 2;
     __shared__ T s_out[VEC ? 1 : QWARPS][VEC ? 1 : SEG];
     const int lane = threadIdx.x & 31;
     const int units = (K + 31) / 32 * 2;
-    const int nseg = (units + lpr - 1) / lpr, rpw = 32 / lpr, sub = lane / lpr;
+    const int nseg = (units + lpr - 1) / lpr, rpw = 32 / lpr, sub = lane / lpr, col = lane - sub * lpr;
     const int nb = (K + F::BLK - 1) / F::BLK;
     const size_t pitch = (size_t)units * 8;
     const float g = gscale ? __ldg(gscale) : 1.f, r = __frcp_rn(g);
-    const bool mild = fabsf(g) > 1e-15f && fabsf(g) < 1e15f;
-    const long long items = (long long)((rows + rpw - 1) / rpw) * nseg;
-    const long long step = (long long)gridDim.x * QWARPS;
-    for (long long it0 = (long long)blockIdx.x * QWARPS + (threadIdx.x >> 5); it0 < items; it0 += U * step) {
+    Walk at((long long)blockIdx.x * QWARPS + (threadIdx.x >> 5), (long long)gridDim.x * QWARPS,
+            (long long)((rows + rpw - 1) / rpw) * nseg, nseg);
+    while (at.left > 0) {
         uint2 c[U];
         uint32_t sb[U];
         int row[U], unit[U];
+        const int n = (int)min(at.left, (long long)U);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const long long it = it0 + i * step;
-            row[i] = rows;
-            unit[i] = units;
-            if (it < items) {
-                const int rg = (int)(it / nseg);
-                row[i] = rg * rpw + sub;
-                unit[i] = (int)(it - (long long)rg * nseg) * lpr + (lane - sub * lpr);
-            }
+            row[i] = i < n ? at.row * rpw + sub : rows;
+            unit[i] = at.seg * lpr + col;
             c[i] = make_uint2(0u, 0u);
             sb[i] = 0u;
             if (row[i] < rows && unit[i] < units) {
@@ -221,32 +282,17 @@ dequantize_rows_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restr
                 const int b = unit[i] * UNIT / F::BLK;
                 if (b < nb) sb[i] = __ldg(scales + (size_t)row[i] * nb + b);
             }
+            at.next();
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            if (it0 + i * step >= items) break;
-            const float s = scale_value<F>(sb[i]);
-            const uint32_t w[2] = {c[i].x, c[i].y};
+            if (i >= n) break;
+            float v[UNIT];
+            unit_values<F>(c[i], sb[i], gscale != nullptr, g, r, v);
             Raw16<T> o;
             T* e = reinterpret_cast<T*>(o.q);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t h2;
-                asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
-                    : "=r"(h2) : "r"((w[j >> 2] >> (8 * (j & 3))) & 0xFFu));
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                float v[2] = {f.x * s, f.y * s};
-                if (gscale) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float a = v[q] * r;
-                        const float d = fmaf(fmaf(-a, g, v[q]), r, a);
-                        v[q] = mild && fabsf(v[q]) > 1e-15f && fabsf(v[q]) < 1e15f ? d : __fdiv_rn(v[q], g);
-                    }
-                }
-                e[2 * j] = rounded<T>(v[0]);
-                e[2 * j + 1] = rounded<T>(v[1]);
-            }
+            for (int j = 0; j < UNIT; ++j) e[j] = rounded<T>(v[j]);
             const int k0 = unit[i] * UNIT;
             const bool live = row[i] < rows && k0 < K;
             T* dst = out + (long long)row[i] * ldo + k0;
@@ -267,7 +313,8 @@ dequantize_rows_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restr
                 __syncwarp();
                 const int base = (unit[i] - lane) * UNIT;
                 T* drow = out + (long long)row[i] * ldo + base;
-                for (int q = lane; q < SEG && base + q < K; q += 32) drow[q] = box[q];
+                if (row[i] < rows)
+                    for (int q = lane; q < SEG && base + q < K; q += 32) drow[q] = box[q];
             } else if (live) {
 #pragma unroll
                 for (int q = 0; q < UNIT; ++q)

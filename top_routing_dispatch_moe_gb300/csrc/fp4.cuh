@@ -114,35 +114,49 @@ __device__ __forceinline__ uint32_t block_scale(float amax, float& s, float& r) 
     }
 }
 
-// BLK values of one block -> codes, as the correctly rounded quotient v / s rounded to e2m1, so that a quotient half
-// way between two codes is one here too. MX: s is a power of two and v * r exact. NV: q = v r is off by less than two
-// units in its last place; with r the rounded reciprocal, q + (v - q s) r is the rounded quotient (Markstein's
-// correction, as r has no error beyond its own rounding and v - q s is exact in one fused step). Past 1e30 the products
-// could overflow: such a block is one whose scale is at its ceiling, and its values are cut to 1e30 first (they end at
-// +-6 either way).
-template <class F>
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ void mul2(float* d, const float* a, float b) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d[0]), "=f"(d[1]) : "f"(a[0]), "f"(a[1]), "f"(b));
+}
+__device__ __forceinline__ void fma2(float* d, const float* a, float b, const float* c) {
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %6};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d[0]), "=f"(d[1]) : "f"(a[0]), "f"(a[1]), "f"(b), "f"(c[0]), "f"(c[1]));
+}
+// The rounded quotients v / s of two values, given the rounded reciprocal r of s: q = v r is off by less than two units in
+// its last place, and q + (v - q s) r is the rounded quotient (Markstein's correction: v - q s is exact in one fused step,
+// and r has no error beyond its own rounding), as long as neither product leaves the normal range.
+__device__ __forceinline__ void quotient2(float* v, float s, float r) {
+    float q[2], e[2];
+    mul2(q, v, r);
+    fma2(e, q, -s, v);
+    fma2(v, e, r, q);
+}
+
+// N values of one block -> codes, as the correctly rounded quotient v / s rounded to e2m1, so that a quotient half way
+// between two codes is one here too. MX: s is a power of two and v * r exact. NV: quotient2. Past 1e30 its products could
+// overflow: such a block is one whose scale is at its ceiling, and its values are cut to 1e30 first (they end at +-6 either
+// way). (Where v is so small that v - q s is no longer exact, the code is 0 either way.)
+template <class F, int N = F::BLK>
 __device__ __forceinline__ void block_codes(float* v, float amax, float s, float r, uint32_t* w) {
     if constexpr (F::ID == MOE_FP4_NV) {
         if (amax > 1e30f) {
 #pragma unroll
-            for (int i = 0; i < F::BLK; ++i) v[i] = fminf(fmaxf(v[i], -1e30f), 1e30f);
+            for (int i = 0; i < N; ++i) v[i] = fminf(fmaxf(v[i], -1e30f), 1e30f);
         }
 #pragma unroll
-        for (int i = 0; i < F::BLK; ++i) {
-            const float q = v[i] * r;
-            v[i] = fmaf(fmaf(-q, s, v[i]), r, q);
-        }
+        for (int i = 0; i < N; i += 2) quotient2(v + i, s, r);
     } else {
 #pragma unroll
-        for (int i = 0; i < F::BLK; ++i) v[i] *= r;
+        for (int i = 0; i < N; i += 2) mul2(v + i, v + i, r);
     }
-    if (amax != amax) {
+    const bool bad = amax != amax;
 #pragma unroll
-        for (int i = 0; i < F::BLK / 8; ++i) w[i] = 0u;
-        return;
+    for (int i = 0; i < N / 8; ++i) {
+        const uint32_t c = e2m1x8(v + 8 * i);
+        w[i] = bad ? 0u : c;
     }
-#pragma unroll
-    for (int i = 0; i < F::BLK / 8; ++i) w[i] = e2m1x8(v + 8 * i);
 }
 
 template <class F>
