@@ -1,4 +1,4 @@
-// Quantisation to block-scaled e2m1 and back, the packing of 4-bit weights and the tile schedule of ragged groups.
+// Quantisation to block-scaled e2m1 and back, with the tile schedule of ragged groups, and the packing of 4-bit weights.
 //
 // Quantisation and its inverse are bound by memory: x is read once and 0.5 + 1 / BLK bytes a value are written (or the
 // other way round). A lane owns 16 consecutive columns (two 16-byte loads of bf16, one 8-byte store of codes), so an NV
@@ -161,40 +161,112 @@ quantize_rows_kernel(const T* __restrict__ x, long long ldx, int x_rows, const i
     }
 }
 
-// Operand form: the rows of the schedule's tiles, codes [rows][pad64(K) / 2], scales in the tile layout. A block takes
-// one (tile, 512 columns) item at a time: its warps take the rows in turn, the scale bytes meet in shared memory (pieces
-// 528 bytes apart, so that the pieces of one row fall into different banks) and leave as whole pieces.
+// Tile counts of the groups [offsets[g], offsets[g + 1]) summed up into first[0 .. G] (G <= 1024) by a block of QTHREADS;
+// 0 everywhere, and true, if an offset falls or leaves [0, rows].
+__device__ __forceinline__ bool scan_groups(const int32_t* __restrict__ offsets, int G, int rows, int* first) {
+    constexpr int PER = 1024 / QTHREADS;
+    __shared__ int s_warp[QWARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g0 = threadIdx.x * PER;
+    int n[PER], sum = 0;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        n[i] = 0;
+        if (g0 + i < G) {
+            const int lo = __ldg(offsets + g0 + i), hi = __ldg(offsets + g0 + i + 1);
+            if (lo < 0 || hi < lo || hi > rows) bad = true;
+            else n[i] = (int)(((long long)hi - lo + MOE_TILE_M - 1) / MOE_TILE_M);
+        }
+        sum += n[i];
+    }
+    bad = __syncthreads_or(bad);
+    int v = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+    }
+    if (lane == 31) s_warp[warp] = v;
+    __syncthreads();
+    int at = v - sum;
+    for (int i = 0; i < warp; ++i) at += s_warp[i];
+    if (threadIdx.x == 0) first[0] = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        at += n[i];
+        if (g0 + i < G) first[g0 + i + 1] = bad ? 0 : at;
+    }
+    __syncthreads();
+    return bad;
+}
+
+// Operand form: the rows of the tiles, codes [rows][pad64(K) / 2], scales in the tile layout. The tiles are those of `sched`,
+// or with `offsets` those of the groups, found by every block for itself (a launch fewer than a kernel of its own); block 0
+// then writes the schedule for the products. A block takes one item at a time, 512 columns of a tile's rows or, where there
+// are few tiles, of a quarter of them (parts = 2; 4 granules of the scale pieces: the rows r with r % 32 in its range): its
+// warps take the rows in turn, the scale bytes meet in shared memory (pieces 528 bytes apart, so that the pieces of one row fall into different
+// banks) and leave as whole pieces.
 template <class F, typename T, bool VEC>
 __global__ void __launch_bounds__(QTHREADS, 4)
 quantize_operand_kernel(const T* __restrict__ x, long long ldx, int x_rows, const int32_t* __restrict__ src,
-                        const int32_t* __restrict__ sched, int G, int max_tiles, int K, const float* __restrict__ gscale,
-                        uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, unsigned* err) {
+                        const int32_t* __restrict__ offsets, int32_t* sched, int G, int rows, int max_tiles, int parts, int K,
+                        const float* __restrict__ gscale, uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, unsigned* err) {
     constexpr int U = IN_FLIGHT<T>, PIECES = 2 * SF_PIECES<F>, STRIDE = 528;
     __shared__ __align__(16) uint8_t s_sf[PIECES * STRIDE];
+    __shared__ int s_first[1025];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int units = (K + 63) / 64 * 4, kst = (K + SEG_K - 1) / SEG_K;
     const int nseg = (kst + 1) / 2;
     const size_t pitch = (size_t)units * 8;
-    pdl_wait();                          // (a programmatic dependent of the kernel that wrote the schedule)
+    pdl_wait();                          // (a programmatic dependent of the kernel that wrote x or the schedule)
     pdl_trigger();
     const float g = gscale ? __ldg(gscale) : 1.f;
-    const bool fits = sched[1] == G && sched[0] <= max_tiles;        // (else: another call's schedule)
-    const int ntiles = fits ? sched[0] : 0;
-    if (!fits && blockIdx.x == 0 && threadIdx.x == 0) latch_device_error(err, kDevErrBadIndex, 0x203u);
     const int4* tiles = reinterpret_cast<const int4*>(sched + sched_tiles_offset(G));
-    for (long long it = blockIdx.x; it < (long long)ntiles * nseg; it += gridDim.x) {
-        const int t = (int)(it / nseg), seg = (int)(it - (long long)t * nseg);
-        const int4 ent = tiles[t];
+    auto tile_of = [&](int t) -> int4 {
+        if (!offsets) return tiles[t];
+        int lo = 0, hi = G;
+        while (lo < hi) {                // last group with first[g] <= t
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_first[mid] <= t) lo = mid; else hi = mid - 1;
+        }
+        const int row0 = __ldg(offsets + lo) + (t - s_first[lo]) * MOE_TILE_M;
+        return make_int4(lo, row0, min(row0 + MOE_TILE_M, __ldg(offsets + lo + 1)), 0);
+    };
+    int ntiles;
+    if (offsets) {
+        const bool bad = scan_groups(offsets, G, rows, s_first);
+        ntiles = s_first[G];
+        if (blockIdx.x == 0) {
+            if (threadIdx.x == 0) {
+                sched[0] = ntiles;
+                sched[1] = G;
+                if (bad) latch_device_error(err, kDevErrBadIndex, 0x202u);
+            }
+            for (int i = threadIdx.x; i <= G; i += QTHREADS) sched[kSchedHeader + i] = s_first[i];
+            for (int t = threadIdx.x; t < ntiles; t += QTHREADS)
+                reinterpret_cast<int4*>(sched + sched_tiles_offset(G))[t] = tile_of(t);
+        }
+    } else {
+        const bool fits = sched[1] == G && sched[0] <= max_tiles;        // (else: another call's schedule)
+        ntiles = fits ? sched[0] : 0;
+        if (!fits && blockIdx.x == 0 && threadIdx.x == 0) latch_device_error(err, kDevErrBadIndex, 0x203u);
+    }
+    const int shift = 5 - parts, per = 1 << shift, ip = nseg << parts;      // granules of four rows in a part; items of a tile
+    for (long long it = blockIdx.x; it < (long long)ntiles * ip; it += gridDim.x) {
+        const int t = (int)(it / ip), at = (int)(it - (long long)t * ip), seg = at >> parts, part = at & ((1 << parts) - 1);
+        const int4 ent = tile_of(t);
         const int n = ent.z - ent.y, unit = seg * 32 + lane;
         for (int i = threadIdx.x; i < PIECES * STRIDE / 16; i += QTHREADS)
             reinterpret_cast<uint4*>(s_sf)[i] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
-        for (int r0 = warp; r0 < n; r0 += U * QWARPS) {
+        for (int i0 = warp; i0 < 4 * per; i0 += U * QWARPS) {
             Raw16<T> raw[U];
+            int r[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const int r = r0 + i * QWARPS;
-                int from = r < n ? ent.y + r : -1;
+                const int j = i0 + i * QWARPS;               // row j of the part: granule j % per, quarter j / per
+                r[i] = j < 4 * per ? (j >> shift) * 32 + part * per + (j & (per - 1)) : n;
+                int from = r[i] < n ? ent.y + r[i] : -1;
                 if (from >= 0 && src) {
                     from = __ldg(src + from);
                     if (from >= x_rows || from < -1) { latch_device_error(err, kDevErrBadIndex, 0x201u); from = -1; }
@@ -203,21 +275,22 @@ quantize_operand_kernel(const T* __restrict__ x, long long ldx, int x_rows, cons
             }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const int r = r0 + i * QWARPS;
-                if (r >= n) break;
+                if (r[i] >= n) continue;
                 uint32_t byte;
                 const uint2 w = quantize_unit<F>(raw[i], gscale != nullptr, g, byte);
-                if (unit < units) *reinterpret_cast<uint2*>(codes + (size_t)(ent.y + r) * pitch + (size_t)unit * 8) = w;
+                if (unit < units) *reinterpret_cast<uint2*>(codes + (size_t)(ent.y + r[i]) * pitch + (size_t)unit * 8) = w;
                 const int b = lane * UNIT / F::BLK;
                 if (lane * UNIT % F::BLK == 0)
-                    s_sf[(b >> 2) * STRIDE + (r & 31) * 16 + (r >> 5) * 4 + (b & 3)] = (uint8_t)byte;
+                    s_sf[(b >> 2) * STRIDE + (r[i] & 31) * 16 + (r[i] >> 5) * 4 + (b & 3)] = (uint8_t)byte;
             }
         }
         __syncthreads();
         const int np = min(2, kst - 2 * seg) * SF_PIECES<F>;      // pieces of the stages that exist
         uint4* dst = reinterpret_cast<uint4*>(sf + ((size_t)t * kst + 2 * seg) * SF_BYTES<F>);
-        for (int i = threadIdx.x; i < np * 32; i += QTHREADS)
-            dst[i] = *reinterpret_cast<const uint4*>(s_sf + (i >> 5) * STRIDE + (i & 31) * 16);
+        for (int i = threadIdx.x; i < np << shift; i += QTHREADS) {
+            const int q = i >> shift, gr = part * per + (i & (per - 1));
+            dst[q * 32 + gr] = *reinterpret_cast<const uint4*>(s_sf + q * STRIDE + gr * 16);
+        }
         __syncthreads();
     }
 }
@@ -393,46 +466,6 @@ static int pack(PackSrc codes, PackSrc scales, int G, int N, int n_packed, int K
 }
 
 // ---------------------------------------------------------------------------------------------------
-// tile schedule of ragged groups
-// ---------------------------------------------------------------------------------------------------
-// offsets [G + 1], rising within [0, rows], G <= 1024: one block scans the groups' tile counts. Offsets that fall or leave
-// the range are latched, and the schedule is then empty.
-__global__ void __launch_bounds__(1024) group_sched_kernel(const int32_t* __restrict__ offsets, int G, int rows,
-                                                           int32_t* __restrict__ sched, unsigned* err) {
-    __shared__ int s_tmp[32];
-    __shared__ int s_bad;
-    const int g = threadIdx.x;
-    if (g == 0) s_bad = 0;
-    __syncthreads();
-    pdl_wait();
-    pdl_trigger();
-    int lo = 0, hi = 0;
-    if (g < G) {
-        lo = offsets[g];
-        hi = offsets[g + 1];
-        if (lo < 0 || hi < lo || hi > rows) s_bad = 1;
-    }
-    __syncthreads();
-    const bool bad = s_bad != 0;
-    const int nt = bad ? 0 : (int)(((long long)hi - lo + MOE_TILE_M - 1) / MOE_TILE_M);
-    const int incl = block_inclusive_scan(nt, s_tmp);
-    if (g < G) {
-        if (g == 0) { sched[1] = G; sched[kSchedHeader] = 0; }
-        sched[kSchedHeader + g + 1] = incl;
-        if (g == G - 1) sched[0] = incl;
-        int4* tiles = reinterpret_cast<int4*>(sched + sched_tiles_offset(G)) + (incl - nt);
-        for (int t = 0; t < nt; ++t)
-            tiles[t] = make_int4(g, lo + t * MOE_TILE_M, min(lo + (t + 1) * MOE_TILE_M, hi), 0);
-    }
-    if (bad && g == 0) latch_device_error(err, kDevErrBadIndex, 0x202u);
-}
-
-int launch_group_sched(const int32_t* offsets, int G, int rows, int32_t* sched, cudaStream_t s) {
-    return check_launch(launch_pdl(group_sched_kernel, dim3(1), dim3(1024), 0, s, offsets, G, rows, sched,
-                                   device_error_word()), "group_sched_kernel");
-}
-
-// ---------------------------------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------------------------------
 static int el_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
@@ -462,17 +495,19 @@ static int row_grid(int rows, int K, int lpr) {
     return (int)std::max<long long>(1, std::min<long long>(cdiv(items, QWARPS), (long long)num_sms() * 8));
 }
 
-int launch_quantize_operand(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* sched, int G,
-                            int rows, int K, int dtype, int fmt, const float* gscale, void* codes, void* sf,
-                            cudaStream_t s) {
-    const long long items = (long long)sched_max_tiles(rows, G) * cdiv(stages_of(K), 2);
-    const int grid = (int)std::min<long long>(items, (long long)num_sms() * 6);
+int launch_quantize_operand(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* offsets, int32_t* sched,
+                            int G, int rows, int K, int dtype, int fmt, const float* gscale, void* codes, void* sf,
+                            unsigned* err, cudaStream_t s) {
+    const long long items = (long long)sched_max_tiles(rows, std::min(G, rows)) * cdiv(stages_of(K), 2);
+    const int parts = items < 4LL * num_sms() ? 2 : 0;
+    const int grid = (int)std::min<long long>(items << parts, (long long)num_sms() * 4);
     return by_kind(fmt, dtype, vec_ok(x, ldx, dtype), [&](auto f, auto t, auto v) {
         using F = decltype(f);
         using T = decltype(t);
         return check_launch(launch_pdl(quantize_operand_kernel<F, T, decltype(v)::value>, dim3(grid), dim3(QTHREADS), 0, s,
-                                       static_cast<const T*>(x), ldx, x_rows, src, sched, G, (int)sched_max_tiles(rows, G), K, gscale,
-                                       static_cast<uint8_t*>(codes), static_cast<uint8_t*>(sf), device_error_word()),
+                                       static_cast<const T*>(x), ldx, x_rows, src, offsets, sched, G, rows,
+                                       (int)sched_max_tiles(rows, G), parts, K, gscale, static_cast<uint8_t*>(codes),
+                                       static_cast<uint8_t*>(sf), err),
                             "quantize_operand_kernel");
     });
 }

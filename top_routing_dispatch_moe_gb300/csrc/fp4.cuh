@@ -166,11 +166,11 @@ __device__ __forceinline__ float scale_value(uint32_t b) {
 }
 #endif
 
-// Launches shared between the two files.
-int launch_group_sched(const int32_t* offsets, int G, int rows, int32_t* sched, cudaStream_t s);
-int launch_quantize_operand(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* sched, int G,
-                            int rows, int K, int dtype, int fmt, const float* gscale, void* codes, void* sf,
-                            cudaStream_t s);
+// The rows of the groups, quantised into the product's operand: of `offsets`, whose schedule is then written to `sched`, or
+// (offsets null) of the schedule that `sched` holds.
+int launch_quantize_operand(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* offsets, int32_t* sched,
+                            int G, int rows, int K, int dtype, int fmt, const float* gscale, void* codes, void* sf,
+                            unsigned* err, cudaStream_t s);
 
 }  // namespace fp4
 }  // namespace moe

@@ -31,6 +31,7 @@ constexpr int A_BYTES = BM * SEG_K / 2;          // 16 KB of codes
 constexpr int EPI_WARPS = 8, SF_WARPS = 4;
 constexpr int THREADS = 32 * (2 + EPI_WARPS + SF_WARPS);
 constexpr int TMEM_COLS = 512;
+constexpr int MAX_G = 1024;
 constexpr int SF_BUFS = 3;                       // stages of scales in tensor memory
 
 enum Epi : int { EPI_OUT = 0, EPI_SWIGLU = 1 };
@@ -41,7 +42,7 @@ struct Cfg {
     static constexpr int B_BYTES = BN * SEG_K / 2;
     static constexpr int SF_BLOCKS = (BN + 127) / 128;               // 128-row scale tiles a weight tile touches
     template <class F> static constexpr int SFS = (1 + SF_BLOCKS) * SF_BYTES<F>;   // scale bytes of a stage
-    template <class F> static constexpr int SMEM = 1024 + EPI_WARPS * 4096 + STAGES * (A_BYTES + B_BYTES + SFS<F>) + 256;
+    template <class F> static constexpr int SMEM = 1024 + EPI_WARPS * 4096 + STAGES * (A_BYTES + B_BYTES + SFS<F>) + 256 + (MAX_G + 1) * 4;
     static constexpr int SF_COL = 2 * BN;                            // scale columns follow the two accumulators
     static constexpr int B_COLS = BN / 32;                           // scale columns of the weight rows in a piece
     template <class F> static constexpr int SF_COLS = SF_PIECES<F> * (4 + B_COLS);   // of a stage
@@ -71,9 +72,9 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 
 struct Work { int g, tile, row0, row1, n; };
 
-// Item w: group by group, n-tile next, m-tile fastest: CTAs that run together share a weight tile.
-__device__ __forceinline__ Work map_work(const int32_t* sched, int G, int NT, int w) {
-    const int32_t* prefix = sched + kSchedHeader;
+// Item w: group by group, n-tile next, m-tile fastest: CTAs that run together share a weight tile. prefix: the schedule's
+// tiles of each group summed up, in shared memory (a search through global memory costs a decode call microseconds).
+__device__ __forceinline__ Work map_work(const int32_t* sched, const int* prefix, int G, int NT, int w) {
     int lo = 0, hi = G;
     while (lo < hi) {                    // last g with prefix[g] * NT <= w
         const int mid = (lo + hi + 1) >> 1;
@@ -298,6 +299,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const uint32_t mma_done = bar0 + 8u * (2 * STAGES + 4);
     auto sfull = [&](int b) { return bar0 + 8u * (2 * STAGES + 5 + b); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5 + SF_BUFS);
+    int* prefix = reinterpret_cast<int*>(bars + 32);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -323,13 +325,16 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const bool fits = p.sched[1] == G && ntiles <= p.max_tiles;      // (else: another call's schedule)
     const int total = uniform(fits ? ntiles * p.NT : 0);
     if (!fits && blockIdx.x == 0 && threadIdx.x == 0) latch_device_error(p.err, kDevErrBadIndex, 0x203u);
+    if (fits)
+        for (int i = threadIdx.x; i <= G; i += THREADS) prefix[i] = p.sched[kSchedHeader + i];
+    __syncthreads();
 
     if (warp == 0) {
         int stage = 0;
         uint32_t phase = 0, issued = 0, last_par = 0;
         bool ok = true, ready = false;              // ready: the next ring stage was seen free
         for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
-            const Work wk = map_work(p.sched, G, p.NT, w);
+            const Work wk = map_work(p.sched, prefix, G, p.NT, w);
             const int n = uniform(wk.n), g = uniform(wk.g), tile = uniform(wk.tile), row0 = uniform(wk.row0);
             const int boxes = uniform((wk.row1 - wk.row0 + 31) >> 5);
             const int nb = min(BN / 64, p.NB64 - n * (BN / 64));
@@ -408,7 +413,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         uint32_t phase = 0, ophase = 1;             // (the rounds before the first count as complete)
         bool ok = true, loaded = false, freed = false;
         for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
-            const bool odd = BN % 128 == 64 && (map_work(p.sched, G, p.NT, w).n & 1);
+            const bool odd = BN % 128 == 64 && (map_work(p.sched, prefix, G, p.NT, w).n & 1);
             for (int kb = 0; kb < p.kst; ++kb) {
                 if (!loaded) ok = wait_warp(full(stage), phase, p.wait_limit, abort_flag, p.err, 0x241u);
                 if (!ok) break;
@@ -453,7 +458,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         int iter = 0;
         for (int w = blockIdx.x; w < total; w += gridDim.x, ++iter) {
             const int a = iter & 1;
-            const Work wk = map_work(p.sched, G, p.NT, w);       // (before the wait: its loads take a while)
+            const Work wk = map_work(p.sched, prefix, G, p.NT, w);       // (before the wait: its loads take a while)
             if (!wait_warp(tfull(a), (iter >> 1) & 1, p.wait_limit, abort_flag, p.err, 0x230u)) break;
             tc_fence_after();
             const uint32_t tbase = tmem + a * BN + ((uint32_t)quarter << 16);
@@ -495,10 +500,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 // its four chunks and not for their conversion and stores.
 constexpr int PB_BYTES = 128 * SEG_K / 2;        // a CTA's half of the weight rows
 constexpr int P_STAGES = 4, P_BN = 256, P_SF_BUFS = 3, P_ACC2 = 128, P_SF_COL = P_ACC2 + P_BN, P_SFA_COL = P_SF_COL + 96;
-constexpr int P_MAX_G = 1024;
 template <class F> constexpr int P_SFS = 3 * SF_BYTES<F>;
 template <class F> constexpr int P_SMEM = 1024 + EPI_WARPS * 4096 + P_STAGES * (A_BYTES + PB_BYTES + P_SFS<F>) + 256 +
-                                          (P_MAX_G + 1) * 4;
+                                          (MAX_G + 1) * 4;
 template <class F> constexpr int P_COLS = SF_PIECES<F> * 8;      // scale columns of the weight rows in a stage
 static_assert(P_SF_BUFS * P_COLS<Nv> <= 96 && P_SFA_COL + 2 * SF_PIECES<Nv> * 4 <= TMEM_COLS, "tensor memory columns");
 static_assert(P_SMEM<Nv> <= 227 * 1024, "shared memory per CTA");
@@ -914,7 +918,7 @@ static int product(const void* a_codes, long long rows, int G, int K, const Para
     return launch<F, Narrow, EPI>(a_codes, rows, K, p, s);
 }
 
-static Params params_for(const int32_t* sched, int G, int rows, const void* a_sf, const void* packed, const WeightLayout& L,
+static Params params_for(const int32_t* sched, unsigned* err, int G, int rows, const void* a_sf, const void* packed, const WeightLayout& L,
                          int K) {
     Params p{};
     p.sched = sched;
@@ -927,7 +931,7 @@ static Params params_for(const int32_t* sched, int G, int rows, const void* a_sf
     p.kst = L.KST;
     p.NB64 = L.NB64;
     p.NB128 = L.NB128;
-    p.err = device_error_word();
+    p.err = err;
     p.wait_limit = wait_limit();
     return p;
 }
@@ -1002,15 +1006,12 @@ extern "C" int moe_fp4_linear(const void* x, long long ldx, int x_rows, const in
     MOE_REQUIRE(ws_bytes >= L.total, MOE_ERR_WORKSPACE, "moe_fp4_linear: workspace %zu < %zu", ws_bytes, L.total);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t* w = static_cast<uint8_t*>(ws);
-    if (offsets) {
-        int32_t* sched = reinterpret_cast<int32_t*>(w + L.sched);
-        if (int rc = launch_group_sched(offsets, G, rows, sched, s)) return rc;
-        tile_sched = sched;
-    }
-    if (int rc = launch_quantize_operand(x, ldx, x_rows, src, tile_sched, G, rows, K, dtype, fmt, gscale, w + L.codes,
-                                         w + L.sf, s))
+    unsigned* err = device_error_word();
+    int32_t* sched = offsets ? reinterpret_cast<int32_t*>(w + L.sched) : const_cast<int32_t*>(tile_sched);
+    if (int rc = launch_quantize_operand(x, ldx, x_rows, src, offsets, sched, G, rows, K, dtype, fmt, gscale, w + L.codes,
+                                         w + L.sf, err, s))
         return rc;
-    Params p = params_for(tile_sched, G, rows, w + L.sf, packed, weight_layout(G, N, K, fmt), K);
+    Params p = params_for(sched, err, G, rows, w + L.sf, packed, weight_layout(G, N, K, fmt), K);
     p.N = N;
     p.ldo = (int)ldo;
     p.out = out;
@@ -1040,16 +1041,13 @@ extern "C" int moe_fp4_expert_ffn(const void* x, long long ldx, int x_rows, cons
     MOE_REQUIRE(ws_bytes >= L.total, MOE_ERR_WORKSPACE, "moe_fp4_expert_ffn: workspace %zu < %zu", ws_bytes, L.total);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t* w = static_cast<uint8_t*>(ws);
-    if (offsets) {
-        int32_t* sched = reinterpret_cast<int32_t*>(w + L.x.sched);
-        if (int rc = launch_group_sched(offsets, E, rows, sched, s)) return rc;
-        tile_sched = sched;
-    }
-    if (int rc = launch_quantize_operand(x, ldx, x_rows, src, tile_sched, E, rows, h, dtype, fmt, gscale, w + L.x.codes,
-                                         w + L.x.sf, s))
+    unsigned* err = device_error_word();
+    int32_t* sched = offsets ? reinterpret_cast<int32_t*>(w + L.x.sched) : const_cast<int32_t*>(tile_sched);
+    if (int rc = launch_quantize_operand(x, ldx, x_rows, src, offsets, sched, E, rows, h, dtype, fmt, gscale, w + L.x.codes,
+                                         w + L.x.sf, err, s))
         return rc;
     const ExpertLayout W = expert_layout(E, h, F, fmt);
-    Params p = params_for(tile_sched, E, rows, w + L.x.sf, packed, W.gu, h);
+    Params p = params_for(sched, err, E, rows, w + L.x.sf, packed, W.gu, h);
     p.alpha = alpha_gate;
     p.alpha_up = alpha_up;
     p.act_gscale = act_gscale;
@@ -1060,7 +1058,7 @@ extern "C" int moe_fp4_expert_ffn(const void* x, long long ldx, int x_rows, cons
     if (int rc = fmt == MOE_FP4_NV ? product<Nv, EPI_SWIGLU>(w + L.x.codes, rows, E, h, p, s)
                                    : product<Mx, EPI_SWIGLU>(w + L.x.codes, rows, E, h, p, s))
         return rc;
-    Params d = params_for(tile_sched, E, rows, w + L.act_sf, static_cast<const uint8_t*>(packed) + W.down_off, W.down, F);
+    Params d = params_for(sched, err, E, rows, w + L.act_sf, static_cast<const uint8_t*>(packed) + W.down_off, W.down, F);
     d.N = h;
     d.ldo = (int)ldo;
     d.out = out;

@@ -743,23 +743,35 @@ def _fp4_format(fmt: str | int) -> int:
     return int(fmt)
 
 
-def _fp4_require(ok: bool, what: str):
-    if not ok:
-        raise MoEError(MOE_ERR_INVALID_ARG, what)
+def _fp4_fail(what: str):
+    raise MoEError(MOE_ERR_INVALID_ARG, what)
 
 
 def _fp4_rows(t, what: str) -> int:
-    """The row stride of a 2-D tensor with contiguous rows."""
-    _fp4_require(t.dim() == 2 and t.is_cuda and (t.stride(1) == 1 or t.shape[1] == 1),
-                 f"{what}: a 2-D device tensor with contiguous rows")
-    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+    """The row stride of a 2-D device tensor with contiguous rows."""
+    if t.dim() != 2 or not t.is_cuda or (t.stride(1) != 1 and t.shape[1] != 1):
+        _fp4_fail(f"{what}: a 2-D device tensor with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
-def _fp4_vector(t, n: int, dtype, what: str):
-    """An optional contiguous vector of at least n elements of dtype."""
-    _fp4_require(t is None or (t.dtype == dtype and t.numel() >= n and t.is_cuda and t.is_contiguous()),
-                 f"{what}: a contiguous {dtype} device tensor of {n} elements")
-    return t
+def _fp4_data(t, n: int, dtype, what: str):
+    """The address of a contiguous device tensor of at least n elements of dtype (None of None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or not t.is_cuda or t.numel() < n or not t.is_contiguous():
+        _fp4_fail(f"{what}: a contiguous {dtype} device tensor of {n} elements")
+    return t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _fp4_stream(stream, t):
+    """The address of `stream`, or of the current stream of t's device (asked for directly where torch allows it: the
+    torch.cuda.Stream object alone costs a small call three microseconds)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(t.device.index) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
 
 
 def moe_fp4_codes_pitch(K: int) -> int:
@@ -778,15 +790,13 @@ def moe_fp4_quantize(x, fmt="nv", *, gscale=None, src=None, codes=None, scales=N
     multiplied with first; src [rows] int32: x's row of each row, -1 for zeros."""
     f, K, ldx = _fp4_format(fmt), x.shape[-1], _fp4_rows(x, "x")
     rows = x.shape[0] if src is None else src.numel()
-    _fp4_vector(src, 0, torch.int32, "src")
-    _fp4_vector(gscale, 1, torch.float32, "gscale")
-    nb, pitch = moe_fp4_scales_pitch(K, f), moe_fp4_codes_pitch(K)
+    nb, pitch = _lib.moe_fp4_scales_pitch(K, f), _lib.moe_fp4_codes_pitch(K)
     codes = torch.empty((rows, pitch), dtype=torch.uint8, device=x.device) if codes is None else codes
     scales = torch.empty((rows, nb), dtype=torch.uint8, device=x.device) if scales is None else scales
-    _fp4_vector(codes, rows * pitch, torch.uint8, "codes")
-    _fp4_vector(scales, rows * nb, torch.uint8, "scales")
-    _check(_lib.moe_fp4_quantize(_ptr(x), ldx, x.shape[0], _ptr(src), rows, K, _fp4_dtype(x.dtype), f, _ptr(gscale),
-                                 _ptr(codes), _ptr(scales), _stream(stream)))
+    _check(_lib.moe_fp4_quantize(x.data_ptr(), ldx, x.shape[0], _fp4_data(src, 0, torch.int32, "src"), rows, K,
+                                 _fp4_dtype(x.dtype), f, _fp4_data(gscale, 1, torch.float32, "gscale"),
+                                 _fp4_data(codes, rows * pitch, torch.uint8, "codes"),
+                                 _fp4_data(scales, rows * nb, torch.uint8, "scales"), _fp4_stream(stream, x)))
     return codes, scales
 
 
@@ -794,12 +804,13 @@ def moe_fp4_dequantize(codes, scales, K: int, fmt="nv", *, gscale=None, dtype=to
     """The rows [rows, K] that codes and scales stand for, divided by gscale where it is given."""
     f, rows = _fp4_format(fmt), codes.shape[0]
     out = torch.empty((rows, K), dtype=dtype, device=codes.device) if out is None else out
-    _fp4_require(tuple(out.shape) == (rows, K), f"out: [{rows}, {K}]")
-    _fp4_vector(codes, rows * moe_fp4_codes_pitch(K), torch.uint8, "codes")
-    _fp4_vector(scales, rows * moe_fp4_scales_pitch(K, f), torch.uint8, "scales")
-    _fp4_vector(gscale, 1, torch.float32, "gscale")
-    _check(_lib.moe_fp4_dequantize(_ptr(codes), _ptr(scales), rows, K, f, _ptr(gscale), _fp4_dtype(out.dtype), _ptr(out),
-                                   _fp4_rows(out, "out"), _stream(stream)))
+    ldo = _fp4_rows(out, "out")
+    if out.shape[0] != rows or out.shape[1] != K:
+        _fp4_fail(f"out: [{rows}, {K}]")
+    _check(_lib.moe_fp4_dequantize(_fp4_data(codes, rows * _lib.moe_fp4_codes_pitch(K), torch.uint8, "codes"),
+                                   _fp4_data(scales, rows * _lib.moe_fp4_scales_pitch(K, f), torch.uint8, "scales"), rows, K,
+                                   f, _fp4_data(gscale, 1, torch.float32, "gscale"), _fp4_dtype(out.dtype), out.data_ptr(),
+                                   ldo, _fp4_stream(stream, codes)))
     return out
 
 
@@ -808,11 +819,10 @@ def moe_fp4_pack_weight(codes, scales, K: int, fmt="nv", packed=None, stream=Non
     in the operand layout of moe_fp4_linear."""
     f, (G, N) = _fp4_format(fmt), codes.shape[:2]
     need = _lib.moe_fp4_packed_weight_bytes(G, N, K, f)
-    _fp4_vector(codes, G * N * moe_fp4_codes_pitch(K), torch.uint8, "codes")
-    _fp4_vector(scales, G * N * moe_fp4_scales_pitch(K, f), torch.uint8, "scales")
     packed = _bytes_tensor(need, codes.device) if packed is None else packed
-    _fp4_vector(packed, need, torch.uint8, "packed")
-    _check(_lib.moe_fp4_pack_weight(_ptr(codes), _ptr(scales), G, N, K, f, _ptr(packed), _stream(stream)))
+    _check(_lib.moe_fp4_pack_weight(_fp4_data(codes, G * N * moe_fp4_codes_pitch(K), torch.uint8, "codes"),
+                                    _fp4_data(scales, G * N * moe_fp4_scales_pitch(K, f), torch.uint8, "scales"), G, N, K, f,
+                                    _fp4_data(packed, need, torch.uint8, "packed"), _fp4_stream(stream, codes)))
     return packed
 
 
@@ -828,34 +838,34 @@ def moe_fp4_linear(x, offsets, packed, N: int, fmt="nv", *, G: int | None = None
     f, K, ldx = _fp4_format(fmt), x.shape[-1], _fp4_rows(x, "x")
     rows = x.shape[0] if src is None else src.numel()
     G = offsets.numel() - 1 if offsets is not None else G
-    _fp4_require(G is not None, "G: the number of groups of tile_sched")
-    _fp4_vector(offsets, 2, torch.int32, "offsets")
-    _fp4_vector(src, 0, torch.int32, "src")
-    _fp4_vector(tile_sched, 4, torch.int32, "tile_sched")
-    _fp4_vector(alpha, G, torch.float32, "alpha")
-    _fp4_vector(gscale, 1, torch.float32, "gscale")
-    _fp4_vector(packed, _lib.moe_fp4_packed_weight_bytes(G, N, K, f), torch.uint8, "packed")
+    if G is None:
+        _fp4_fail("G: the number of groups of tile_sched")
     out = torch.empty((rows, N), dtype=out_dtype or x.dtype, device=x.device) if out is None else out
-    _fp4_require(tuple(out.shape) == (rows, N), f"out: [{rows}, {N}]")
-    ws = _bytes_tensor(moe_fp4_linear_workspace_size(G, K, rows, f), x.device) if ws is None else ws
-    _fp4_vector(ws, 0, torch.uint8, "ws")
-    _check(_lib.moe_fp4_linear(_ptr(x), ldx, x.shape[0], _ptr(src), _ptr(offsets), _ptr(tile_sched), _ptr(packed),
-                               _ptr(alpha), _ptr(gscale), G, N, K, rows, f, _fp4_dtype(x.dtype), _ptr(out),
-                               _fp4_rows(out, "out"), _fp4_dtype(out.dtype), _ptr(ws), ws.numel(), _stream(stream)))
+    ldo = _fp4_rows(out, "out")
+    if out.shape[0] != rows or out.shape[1] != N:
+        _fp4_fail(f"out: [{rows}, {N}]")
+    ws = _bytes_tensor(_lib.moe_fp4_linear_workspace_size(G, K, rows, f), x.device) if ws is None else ws
+    _check(_lib.moe_fp4_linear(x.data_ptr(), ldx, x.shape[0], _fp4_data(src, 0, torch.int32, "src"),
+                               _fp4_data(offsets, 2, torch.int32, "offsets"),
+                               _fp4_data(tile_sched, 4, torch.int32, "tile_sched"),
+                               _fp4_data(packed, _lib.moe_fp4_packed_weight_bytes(G, N, K, f), torch.uint8, "packed"),
+                               _fp4_data(alpha, G, torch.float32, "alpha"), _fp4_data(gscale, 1, torch.float32, "gscale"),
+                               G, N, K, rows, f, _fp4_dtype(x.dtype), out.data_ptr(), ldo, _fp4_dtype(out.dtype),
+                               _fp4_data(ws, 0, torch.uint8, "ws"), ws.numel(), _fp4_stream(stream, x)))
     return out
 
 
 def moe_fp4_pack_expert_weights(gate, up, down, h: int, F: int, fmt="nv", packed=None, stream=None):
     """gate, up [E, F, h] and down [E, h, F], each as (codes, scales), in the operand layout of moe_fp4_expert_ffn."""
     f, E = _fp4_format(fmt), gate[0].shape[0]
+    data = []
     for (c, s), n, k, what in ((gate, F, h, "gate"), (up, F, h, "up"), (down, h, F, "down")):
-        _fp4_vector(c, E * n * moe_fp4_codes_pitch(k), torch.uint8, what + " codes")
-        _fp4_vector(s, E * n * moe_fp4_scales_pitch(k, f), torch.uint8, what + " scales")
+        data.append(_fp4_data(c, E * n * moe_fp4_codes_pitch(k), torch.uint8, what + " codes"))
+        data.append(_fp4_data(s, E * n * moe_fp4_scales_pitch(k, f), torch.uint8, what + " scales"))
     need = _lib.moe_fp4_packed_expert_weights_bytes(E, h, F, f)
     packed = _bytes_tensor(need, gate[0].device) if packed is None else packed
-    _fp4_vector(packed, need, torch.uint8, "packed")
-    _check(_lib.moe_fp4_pack_expert_weights(*(_ptr(t) for m in (gate, up, down) for t in m), E, h, F, f, _ptr(packed),
-                                            _stream(stream)))
+    _check(_lib.moe_fp4_pack_expert_weights(*data, E, h, F, f, _fp4_data(packed, need, torch.uint8, "packed"),
+                                            _fp4_stream(stream, packed)))
     return packed
 
 
@@ -871,21 +881,23 @@ def moe_fp4_expert_ffn(x, offsets, packed, F: int, fmt="nv", *, E: int | None = 
     f, h, ldx = _fp4_format(fmt), x.shape[-1], _fp4_rows(x, "x")
     rows = x.shape[0] if src is None else src.numel()
     E = offsets.numel() - 1 if offsets is not None else E
-    _fp4_require(E is not None, "E: the number of experts of tile_sched")
-    _fp4_vector(offsets, 2, torch.int32, "offsets")
-    _fp4_vector(src, 0, torch.int32, "src")
-    _fp4_vector(tile_sched, 4, torch.int32, "tile_sched")
-    for t, what in ((alpha_gate, "alpha_gate"), (alpha_up, "alpha_up"), (alpha_down, "alpha_down")):
-        _fp4_vector(t, E, torch.float32, what)
-    _fp4_vector(gscale, 1, torch.float32, "gscale")
-    _fp4_vector(act_gscale, 1, torch.float32, "act_gscale")
-    _fp4_vector(packed, _lib.moe_fp4_packed_expert_weights_bytes(E, h, F, f), torch.uint8, "packed")
+    if E is None:
+        _fp4_fail("E: the number of experts of tile_sched")
     out = torch.empty((rows, h), dtype=out_dtype or x.dtype, device=x.device) if out is None else out
-    _fp4_require(tuple(out.shape) == (rows, h), f"out: [{rows}, {h}]")
-    ws = _bytes_tensor(moe_fp4_expert_ffn_workspace_size(E, h, F, rows, f), x.device) if ws is None else ws
-    _fp4_vector(ws, 0, torch.uint8, "ws")
-    _check(_lib.moe_fp4_expert_ffn(_ptr(x), ldx, x.shape[0], _ptr(src), _ptr(offsets), _ptr(tile_sched), _ptr(packed),
-                                   _ptr(alpha_gate), _ptr(alpha_up), _ptr(alpha_down), _ptr(gscale), _ptr(act_gscale), E, h,
-                                   F, rows, f, _fp4_dtype(x.dtype), _ptr(out), _fp4_rows(out, "out"),
-                                   _fp4_dtype(out.dtype), _ptr(ws), ws.numel(), _stream(stream)))
+    ldo = _fp4_rows(out, "out")
+    if out.shape[0] != rows or out.shape[1] != h:
+        _fp4_fail(f"out: [{rows}, {h}]")
+    ws = _bytes_tensor(_lib.moe_fp4_expert_ffn_workspace_size(E, h, F, rows, f), x.device) if ws is None else ws
+    _check(_lib.moe_fp4_expert_ffn(x.data_ptr(), ldx, x.shape[0], _fp4_data(src, 0, torch.int32, "src"),
+                                   _fp4_data(offsets, 2, torch.int32, "offsets"),
+                                   _fp4_data(tile_sched, 4, torch.int32, "tile_sched"),
+                                   _fp4_data(packed, _lib.moe_fp4_packed_expert_weights_bytes(E, h, F, f), torch.uint8,
+                                             "packed"),
+                                   _fp4_data(alpha_gate, E, torch.float32, "alpha_gate"),
+                                   _fp4_data(alpha_up, E, torch.float32, "alpha_up"),
+                                   _fp4_data(alpha_down, E, torch.float32, "alpha_down"),
+                                   _fp4_data(gscale, 1, torch.float32, "gscale"),
+                                   _fp4_data(act_gscale, 1, torch.float32, "act_gscale"), E, h, F, rows, f,
+                                   _fp4_dtype(x.dtype), out.data_ptr(), ldo, _fp4_dtype(out.dtype),
+                                   _fp4_data(ws, 0, torch.uint8, "ws"), ws.numel(), _fp4_stream(stream, x)))
     return out
