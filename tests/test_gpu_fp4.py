@@ -267,6 +267,15 @@ def test_expert_ffn(gpu_lib, fmt, counts, h, F, T):
 
 
 @pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("K", [1024, 1100, 1350])
+def test_linear_of_rows_used_many_times(gpu_lib, fmt, K):
+    """Rows that src names several times are quantised once and copied: the same values, pads and a group of one row."""
+    g = torch.Generator().manual_seed(K)
+    src = torch.randint(-1, 600, (4500,), generator=g, dtype=torch.int32).cuda()
+    check_linear(gpu_lib, [1, 0, 3000, 1499], 96, K, fmt, "bf16", src=src, x_rows=600, gscale=torch.tensor([4.0], device="cuda"))
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
 def test_expert_ffn_of_many_tiles(gpu_lib, fmt):
     check_ffn(gpu_lib, [1000, 1620], 128, 2080, fmt, "bf16", T=900)
 

@@ -113,14 +113,84 @@ struct Walk {
     }
 };
 
+// Tile counts of the groups [offsets[g], offsets[g + 1]) summed up into first[0 .. G] (G <= 1024) by a block of QTHREADS;
+// 0 everywhere, and true, if an offset falls or leaves [0, rows].
+__device__ __forceinline__ bool scan_groups(const int32_t* __restrict__ offsets, int G, int rows, int* first) {
+    constexpr int PER = 1024 / QTHREADS;
+    __shared__ int s_warp[QWARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g0 = threadIdx.x * PER;
+    int n[PER], sum = 0;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        n[i] = 0;
+        if (g0 + i < G) {
+            const int lo = __ldg(offsets + g0 + i), hi = __ldg(offsets + g0 + i + 1);
+            if (lo < 0 || hi < lo || hi > rows) bad = true;
+            else n[i] = (int)(((long long)hi - lo + MOE_TILE_M - 1) / MOE_TILE_M);
+        }
+        sum += n[i];
+    }
+    bad = __syncthreads_or(bad);
+    int v = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+    }
+    if (lane == 31) s_warp[warp] = v;
+    __syncthreads();
+    int at = v - sum;
+    for (int i = 0; i < warp; ++i) at += s_warp[i];
+    if (threadIdx.x == 0) first[0] = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        at += n[i];
+        if (g0 + i < G) first[g0 + i + 1] = bad ? 0 : at;
+    }
+    __syncthreads();
+    return bad;
+}
+
+// Tile t of the groups: {group, first row, end, 0}.
+__device__ __forceinline__ int4 group_tile(const int32_t* __restrict__ offsets, const int* first, int G, int t) {
+    int lo = 0, hi = G;
+    while (lo < hi) {                    // last group with first[g] <= t
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    const int row0 = __ldg(offsets + lo) + (t - first[lo]) * MOE_TILE_M;
+    return make_int4(lo, row0, min(row0 + MOE_TILE_M, __ldg(offsets + lo + 1)), 0);
+}
+// The schedule of the groups, by one block; first: scan_groups' result, `bad` its answer.
+__device__ __forceinline__ void put_schedule(const int32_t* __restrict__ offsets, const int* first, bool bad, int G, int32_t* sched,
+                                             unsigned* err) {
+    if (threadIdx.x == 0) {
+        sched[0] = first[G];
+        sched[1] = G;
+        if (bad) latch_device_error(err, kDevErrBadIndex, 0x202u);
+    }
+    for (int i = threadIdx.x; i <= G; i += QTHREADS) sched[kSchedHeader + i] = first[i];
+    for (int t = threadIdx.x; t < first[G]; t += QTHREADS)
+        reinterpret_cast<int4*>(sched + sched_tiles_offset(G))[t] = group_tile(offsets, first, G, t);
+}
+__device__ __noinline__ void write_schedule(const int32_t* offsets, int G, int rows, int32_t* sched, unsigned* err) {
+    __shared__ int s_first[1025];
+    const bool bad = scan_groups(offsets, G, rows, s_first);
+    put_schedule(offsets, s_first, bad, G, sched, err);
+}
+
 // Row-major form: codes [rows][pitch], scales [rows][nb]. An item is one row segment of lpr units, 32 / lpr rows to a
 // warp (lpr: a power of two, the units of a row where there are fewer than 32).
 template <class F, typename T, bool VEC>
 __global__ void __launch_bounds__(QTHREADS, 4)
 quantize_rows_kernel(const T* __restrict__ x, long long ldx, int x_rows, const int32_t* __restrict__ src, int rows, int K,
                      int lpr, const float* __restrict__ gscale, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                     unsigned* err) {
+                     const int32_t* __restrict__ offsets, int32_t* sched, int G, int group_rows, unsigned* err) {
     constexpr int U = IN_FLIGHT<T>;
+    pdl_wait();
+    pdl_trigger();
+    if (offsets && blockIdx.x == gridDim.x - 1) write_schedule(offsets, G, group_rows, sched, err);
     const int lane = threadIdx.x & 31;
     const int units = (K + 31) / 32 * 2;
     const int nseg = (units + lpr - 1) / lpr, rpw = 32 / lpr, sub = lane / lpr;
@@ -161,45 +231,6 @@ quantize_rows_kernel(const T* __restrict__ x, long long ldx, int x_rows, const i
     }
 }
 
-// Tile counts of the groups [offsets[g], offsets[g + 1]) summed up into first[0 .. G] (G <= 1024) by a block of QTHREADS;
-// 0 everywhere, and true, if an offset falls or leaves [0, rows].
-__device__ __forceinline__ bool scan_groups(const int32_t* __restrict__ offsets, int G, int rows, int* first) {
-    constexpr int PER = 1024 / QTHREADS;
-    __shared__ int s_warp[QWARPS];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g0 = threadIdx.x * PER;
-    int n[PER], sum = 0;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        n[i] = 0;
-        if (g0 + i < G) {
-            const int lo = __ldg(offsets + g0 + i), hi = __ldg(offsets + g0 + i + 1);
-            if (lo < 0 || hi < lo || hi > rows) bad = true;
-            else n[i] = (int)(((long long)hi - lo + MOE_TILE_M - 1) / MOE_TILE_M);
-        }
-        sum += n[i];
-    }
-    bad = __syncthreads_or(bad);
-    int v = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += t;
-    }
-    if (lane == 31) s_warp[warp] = v;
-    __syncthreads();
-    int at = v - sum;
-    for (int i = 0; i < warp; ++i) at += s_warp[i];
-    if (threadIdx.x == 0) first[0] = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        at += n[i];
-        if (g0 + i < G) first[g0 + i + 1] = bad ? 0 : at;
-    }
-    __syncthreads();
-    return bad;
-}
-
 // Operand form: the rows of the tiles, codes [rows][pad64(K) / 2], scales in the tile layout. The tiles are those of `sched`,
 // or with `offsets` those of the groups, found by every block for itself (a launch fewer than a kernel of its own); block 0
 // then writes the schedule for the products. A block takes one item at a time, 512 columns of a tile's rows or, where there
@@ -222,30 +253,12 @@ quantize_operand_kernel(const T* __restrict__ x, long long ldx, int x_rows, cons
     pdl_trigger();
     const float g = gscale ? __ldg(gscale) : 1.f;
     const int4* tiles = reinterpret_cast<const int4*>(sched + sched_tiles_offset(G));
-    auto tile_of = [&](int t) -> int4 {
-        if (!offsets) return tiles[t];
-        int lo = 0, hi = G;
-        while (lo < hi) {                // last group with first[g] <= t
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_first[mid] <= t) lo = mid; else hi = mid - 1;
-        }
-        const int row0 = __ldg(offsets + lo) + (t - s_first[lo]) * MOE_TILE_M;
-        return make_int4(lo, row0, min(row0 + MOE_TILE_M, __ldg(offsets + lo + 1)), 0);
-    };
+    auto tile_of = [&](int t) -> int4 { return offsets ? group_tile(offsets, s_first, G, t) : tiles[t]; };
     int ntiles;
     if (offsets) {
         const bool bad = scan_groups(offsets, G, rows, s_first);
         ntiles = s_first[G];
-        if (blockIdx.x == 0) {
-            if (threadIdx.x == 0) {
-                sched[0] = ntiles;
-                sched[1] = G;
-                if (bad) latch_device_error(err, kDevErrBadIndex, 0x202u);
-            }
-            for (int i = threadIdx.x; i <= G; i += QTHREADS) sched[kSchedHeader + i] = s_first[i];
-            for (int t = threadIdx.x; t < ntiles; t += QTHREADS)
-                reinterpret_cast<int4*>(sched + sched_tiles_offset(G))[t] = tile_of(t);
-        }
+        if (blockIdx.x == 0) put_schedule(offsets, s_first, bad, G, sched, err);
     } else {
         const bool fits = sched[1] == G && sched[0] <= max_tiles;        // (else: another call's schedule)
         ntiles = fits ? sched[0] : 0;
@@ -292,6 +305,81 @@ quantize_operand_kernel(const T* __restrict__ x, long long ldx, int x_rows, cons
             dst[q * 32 + gr] = *reinterpret_cast<const uint4*>(s_sf + q * STRIDE + gr * 16);
         }
         __syncthreads();
+    }
+}
+
+// Operand form from rows that are quantised already (row-major, codes [x_rows][q_pitch], scales [x_rows][nb]): a token's rows
+// in several groups are quantised once and copied. Tiles, parts and items as in quantize_operand_kernel; a lane copies 16
+// bytes of codes at a time (four of a warp's rows at once) and moves the scales of a row and piece as words.
+template <class F>
+__global__ void __launch_bounds__(QTHREADS)
+gather_operand_kernel(const uint8_t* __restrict__ q_codes, const uint8_t* __restrict__ q_scales, int x_rows,
+                      const int32_t* __restrict__ src, const int32_t* __restrict__ sched, int G, int max_tiles, int K,
+                      uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, unsigned* err) {
+    constexpr int U = 4, PIECES = 2 * SF_PIECES<F>;
+    __shared__ int s_from[MOE_TILE_M];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int kst = (K + SEG_K - 1) / SEG_K, nseg = (kst + 1) / 2, nb = (K + F::BLK - 1) / F::BLK;
+    const int pitch = (K + 63) / 64 * 32, q_pitch = (K + 31) / 32 * 16;
+    pdl_wait();
+    pdl_trigger();
+    const bool fits = sched[1] == G && sched[0] <= max_tiles;            // (else: another call's schedule)
+    const int ntiles = fits ? sched[0] : 0;
+    if (!fits && blockIdx.x == 0 && threadIdx.x == 0) latch_device_error(err, kDevErrBadIndex, 0x203u);
+    const int4* tiles = reinterpret_cast<const int4*>(sched + sched_tiles_offset(G));
+    for (long long it = blockIdx.x; it < (long long)ntiles * nseg; it += gridDim.x) {
+        const int t = (int)(it / nseg), seg = (int)(it - (long long)t * nseg);
+        const int4 ent = tiles[t];
+        const int n = ent.z - ent.y;
+        __syncthreads();
+        if (threadIdx.x < MOE_TILE_M) {
+            int from = -1;
+            if ((int)threadIdx.x < n) {
+                from = __ldg(src + ent.y + threadIdx.x);
+                if (from >= x_rows || from < -1) { latch_device_error(err, kDevErrBadIndex, 0x201u); from = -1; }
+            }
+            s_from[threadIdx.x] = from;
+        }
+        __syncthreads();
+        // codes: 16 lanes to a row's 256 bytes
+        const int c = seg * 256 + (lane & 15) * 16;
+        for (int r0 = warp * 2 + (lane >> 4); r0 < n; r0 += U * 2 * QWARPS) {
+            uint4 v[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int r = r0 + i * 2 * QWARPS, from = r < n ? s_from[r] : -1;
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (from >= 0 && c < q_pitch) v[i] = __ldg(reinterpret_cast<const uint4*>(q_codes + (size_t)from * q_pitch + c));
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int r = r0 + i * 2 * QWARPS;
+                if (r < n && c < pitch) *reinterpret_cast<uint4*>(codes + (size_t)(ent.y + r) * pitch + c) = v[i];
+            }
+        }
+        // scales: a thread writes a granule (16 bytes: four rows' words) of a piece
+        const int np = min(2, kst - 2 * seg) * SF_PIECES<F>;
+        uint4* dst = reinterpret_cast<uint4*>(sf + ((size_t)t * kst + 2 * seg) * SF_BYTES<F>);
+        for (int i = threadIdx.x; i < np * 32; i += QTHREADS) {
+            const int q = i >> 5, b0 = (seg * PIECES + q) * 4;
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int from = s_from[(i & 31) + 32 * j];
+                w[j] = 0u;
+                if (from >= 0) {
+                    const uint8_t* row = q_scales + (size_t)from * nb + b0;
+                    if ((nb & 3) == 0) {
+                        if (b0 < nb) w[j] = __ldg(reinterpret_cast<const uint32_t*>(row));
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (b0 + b < nb) w[j] |= (uint32_t)__ldg(row + b) << (8 * b);
+                    }
+                }
+            }
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
 }
 
@@ -497,7 +585,28 @@ static int row_grid(int rows, int K, int lpr) {
 
 int launch_quantize_operand(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* offsets, int32_t* sched,
                             int G, int rows, int K, int dtype, int fmt, const float* gscale, void* codes, void* sf,
-                            unsigned* err, cudaStream_t s) {
+                            void* rows_ws, unsigned* err, cudaStream_t s) {
+    if (rows_ws) {
+        // once per row of x, then a copy per use
+        uint8_t *qc = static_cast<uint8_t*>(rows_ws), *qs = qc + align_up((size_t)x_rows * ((K + 31) / 32 * 16), 1024);
+        const int lpr = lanes_per_row(K), grid = row_grid(x_rows, K, lpr);
+        if (int rc = by_kind(fmt, dtype, vec_ok(x, ldx, dtype), [&](auto f, auto t, auto v) {
+                using T = decltype(t);
+                return check_launch(launch_pdl(quantize_rows_kernel<decltype(f), T, decltype(v)::value>, dim3(grid), dim3(QTHREADS), 0, s,
+                                               static_cast<const T*>(x), ldx, x_rows, nullptr, x_rows, K, lpr, gscale, qc, qs,
+                                               offsets, sched, G, rows, err),
+                                    "quantize_rows_kernel");
+            }))
+            return rc;
+        const int g2 = (int)std::min<long long>((long long)sched_max_tiles(rows, std::min(G, rows)) * cdiv(stages_of(K), 2),
+                                                (long long)num_sms() * 8);
+        auto gather = [&](auto f) {
+            return check_launch(launch_pdl(gather_operand_kernel<decltype(f)>, dim3(g2), dim3(QTHREADS), 0, s, qc, qs, x_rows, src,
+                                           sched, G, (int)sched_max_tiles(rows, G), K, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(sf), err),
+                                "gather_operand_kernel");
+        };
+        return fmt == MOE_FP4_NV ? gather(Nv{}) : gather(Mx{});
+    }
     const long long items = (long long)sched_max_tiles(rows, std::min(G, rows)) * cdiv(stages_of(K), 2);
     const int parts = items < 4LL * num_sms() ? 2 : 0;
     const int grid = (int)std::min<long long>(items << parts, (long long)num_sms() * 4);
@@ -542,7 +651,7 @@ extern "C" int moe_fp4_quantize(const void* x, long long ldx, int x_rows, const 
         using T = decltype(t);
         quantize_rows_kernel<decltype(f), T, decltype(v)::value><<<grid, QTHREADS, 0, s>>>(
             static_cast<const T*>(x), ldx, x_rows, src, rows, K, lpr, gscale, static_cast<uint8_t*>(codes),
-            static_cast<uint8_t*>(scales), device_error_word());
+            static_cast<uint8_t*>(scales), nullptr, nullptr, 0, 0, device_error_word());
         return check_launch("quantize_rows_kernel");
     });
 }

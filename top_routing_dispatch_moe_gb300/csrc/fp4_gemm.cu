@@ -233,11 +233,22 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const CUtensorMa
         const float ag = p.alpha ? __ldg(p.alpha + wk.g) : 1.f, au = p.alpha_up ? __ldg(p.alpha_up + wk.g) : 1.f;
         const float gs = p.act_gscale ? __ldg(p.act_gscale) : 1.f;
         const int f0 = c0 / 2;                   // first column of act
+        // g / (1 + exp(-g)) * u: the exponential and the reciprocal by the MUFU (a few units in the last place each)
         float* u = v + 32;
+        const float ae = ag * -1.44269504f, c = au * gs;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float gv = v[i] * ag;
-            u[i] = gv / (1.f + __expf(-gv)) * (u[i] * au) * gs;
+        for (int i = 0; i < 32; i += 2) {
+            float e[2], t[2];
+            mul2(t, v + i, ae);
+            mul2(v + i, v + i, ag);
+            mul2(u + i, u + i, c);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                asm("ex2.approx.f32 %0, %1;" : "=f"(e[j]) : "f"(t[j]));
+                asm("rcp.approx.f32 %0, %1;" : "=f"(e[j]) : "f"(e[j] + 1.f));
+            }
+            mul2v(v + i, v + i, e);
+            mul2v(u + i, u + i, v + i);
         }
         uint32_t w[4], bytes = 0u;
 #pragma unroll
@@ -907,14 +918,26 @@ using Wide = Cfg<192, 4>;
 using Mid = Cfg<128, 5>;
 using Narrow = Cfg<64, 6>;
 
-// The tile's width by the work there is: narrow tiles spread a few rows' weights over all SMs, wide ones do the most
-// products per operand byte.
+// The tile by the time that its waves take on the SMs there are: a stage takes the MMA warp 490, 500 or 530 cycles (64, 128,
+// 192 columns; a pair 560), and its bytes about one cycle for each 55, a tile's start and end 2000. The host does not know
+// the groups' sizes: a group is taken to end in the middle of a tile. With few rows a call is bound by the weights' bytes,
+// and a narrow tile moves too few of them a stage: one token through 8 of 32 experts of 7168 x 2048, gate and up, 36 us with
+// 64 columns and 26 with 128; 8192 rows by 8 x 4096 x 12288 (MX), 225 us with 192 columns and 199 by pairs.
 template <class F, int EPI>
 static int product(const void* a_codes, long long rows, int G, int K, const Params& p, cudaStream_t s) {
-    const long long tiles = std::min<long long>(rows, G) + rows / BM;      // about this many m-tiles
-    if (rows >= 256LL * G && tiles * cdiv(p.NB64, 4) >= 2LL * num_sms()) return launch_pair<F, EPI>(a_codes, rows, K, p, s);
-    if (tiles * cdiv(p.NB64, 3) >= 2LL * num_sms()) return launch<F, Wide, EPI>(a_codes, rows, K, p, s);
-    if (tiles * cdiv(p.NB64, 2) >= 2LL * num_sms()) return launch<F, Mid, EPI>(a_codes, rows, K, p, s);
+    const long long used = std::min<long long>(rows, G), kst = stages_of(K), sms = num_sms();
+    const long long tiles = std::max(used, used / 2 + rows / BM), pairs = std::max(used, used / 2 + rows / (2 * BM));
+    const long long a_bytes = std::min<long long>(4, cdiv(rows, 32 * tiles)) * 4096 + SF_BYTES<F>;
+    auto cost = [&](long long m, int blocks, long long units, long long issue, long long b_bytes) {
+        return (m * cdiv(p.NB64, blocks) + units - 1) / units * (kst * std::max(issue, (a_bytes + b_bytes) / 55) + 2000);
+    };
+    const long long c1 = cost(tiles, 1, sms, 490, 8192 + SF_BYTES<F>), c2 = cost(tiles, 2, sms, 500, 16384 + SF_BYTES<F>),
+                    c3 = cost(tiles, 3, sms, 530, 24576 + 2 * SF_BYTES<F>);
+    const long long c4 = rows >= 128LL * G ? cost(pairs, 4, std::max(1LL, sms / 2), 560, 16384 + 2 * SF_BYTES<F>) : c3 + 1;
+    const long long best = std::min(std::min(c1, c2), std::min(c3, c4));
+    if (c4 == best) return launch_pair<F, EPI>(a_codes, rows, K, p, s);
+    if (c3 == best) return launch<F, Wide, EPI>(a_codes, rows, K, p, s);
+    if (c2 == best) return launch<F, Mid, EPI>(a_codes, rows, K, p, s);
     return launch<F, Narrow, EPI>(a_codes, rows, K, p, s);
 }
 
@@ -936,14 +959,16 @@ static Params params_for(const int32_t* sched, unsigned* err, int G, int rows, c
     return p;
 }
 
-// Workspace: the schedule of the groups (when the caller has none), then each operand's codes and scales.
-struct LinearWs { size_t sched, codes, sf, total; };
+// Workspace: the schedule of the groups (when the caller has none), each operand's codes and scales, and x's rows quantised
+// once where src names them several times.
+struct LinearWs { size_t sched, codes, sf, once, total; };
 static LinearWs linear_ws(int G, int K, int rows, int fmt) {
     LinearWs w;
     w.sched = 0;
     w.codes = align_up(sched_words(rows, G) * sizeof(int32_t), 1024);
     w.sf = w.codes + operand_codes_bytes(rows, K);
-    w.total = w.sf + operand_sf_bytes(rows, G, K, fmt);
+    w.once = w.sf + operand_sf_bytes(rows, G, K, fmt);
+    w.total = w.once + gathered_bytes(rows / 2, K, fmt);     // (x has at most rows / 2 rows where they are quantised once)
     return w;
 }
 struct FfnWs { LinearWs x; size_t act_codes, act_sf, total; };
@@ -1009,7 +1034,7 @@ extern "C" int moe_fp4_linear(const void* x, long long ldx, int x_rows, const in
     unsigned* err = device_error_word();
     int32_t* sched = offsets ? reinterpret_cast<int32_t*>(w + L.sched) : const_cast<int32_t*>(tile_sched);
     if (int rc = launch_quantize_operand(x, ldx, x_rows, src, offsets, sched, G, rows, K, dtype, fmt, gscale, w + L.codes,
-                                         w + L.sf, err, s))
+                                         w + L.sf, quantize_once(src, x_rows, rows, K) ? w + L.once : nullptr, err, s))
         return rc;
     Params p = params_for(sched, err, G, rows, w + L.sf, packed, weight_layout(G, N, K, fmt), K);
     p.N = N;
@@ -1044,7 +1069,7 @@ extern "C" int moe_fp4_expert_ffn(const void* x, long long ldx, int x_rows, cons
     unsigned* err = device_error_word();
     int32_t* sched = offsets ? reinterpret_cast<int32_t*>(w + L.x.sched) : const_cast<int32_t*>(tile_sched);
     if (int rc = launch_quantize_operand(x, ldx, x_rows, src, offsets, sched, E, rows, h, dtype, fmt, gscale, w + L.x.codes,
-                                         w + L.x.sf, err, s))
+                                         w + L.x.sf, quantize_once(src, x_rows, rows, h) ? w + L.x.once : nullptr, err, s))
         return rc;
     const ExpertLayout W = expert_layout(E, h, F, fmt);
     Params p = params_for(sched, err, E, rows, w + L.x.sf, packed, W.gu, h);
