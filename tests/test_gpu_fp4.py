@@ -218,6 +218,45 @@ def test_a_nan_row_stays_in_its_row(gpu_lib):
     assert torch.equal(y0[keep], y1[keep])
 
 
+@pytest.mark.parametrize("counts,N", [([3, 2], 96), ([900, 1000], 2304)])
+def test_a_wait_that_runs_out_is_reported(gpu_lib, counts, N):
+    """With one poll to a wait the roles give up (the epilogue waits for 32768 columns of products): the call reports
+    MOE_ERR_TIMEOUT, and the next one is whole again (one SM and a pair of SMs to a tile)."""
+    moe = gpu_lib
+    K = 32768
+    g = torch.Generator("cuda").manual_seed(1)
+    c = torch.randint(0, 256, (2, N, K // 2), dtype=torch.uint8, device="cuda", generator=g)
+    packed = moe.moe_fp4_pack_weight(c, torch.full((2, N, K // 16), 0x28, dtype=torch.uint8, device="cuda"), K, "nv")
+    x = torch.randn((sum(counts), K), device="cuda", generator=g).bfloat16()
+    off = torch.tensor([0, counts[0], sum(counts)], dtype=torch.int32, device="cuda")
+    want = moe.moe_fp4_linear(x, off, packed, N, "nv")
+    ok(moe)
+    moe.moe_set_wait_limit(1)
+    try:
+        moe.moe_fp4_linear(x, off, packed, N, "nv")
+        torch.cuda.synchronize()
+        assert moe.moe_check_device_error() == moe.MOE_ERR_TIMEOUT
+    finally:
+        moe.moe_set_wait_limit(0)
+    assert torch.equal(moe.moe_fp4_linear(x, off, packed, N, "nv"), want)
+    ok(moe)
+
+
+@pytest.mark.parametrize("G", [1, 5])
+def test_another_calls_schedule_is_reported(gpu_lib, G):
+    """A tile schedule of another number of groups, or of more rows than the call has, computes nothing."""
+    moe = gpu_lib
+    c, s, _ = weight(moe, 5, 32, 64, "mx", 3)
+    packed = moe.moe_fp4_pack_weight(c, s, 64, "mx")
+    sched = moe.moe_dense_tile_sched(128 * 20)
+    out = torch.full((40, 32), 5.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_fp4_linear(data((40, 64), "bf16"), None, packed, 32, "mx", G=G, tile_sched=sched, out=out)
+    torch.cuda.synchronize()
+    assert moe.moe_check_device_error() == moe.MOE_ERR_INVALID_ARG
+    assert (out == 5).all()
+    ok(moe)
+
+
 # --------------------------------------------------------------------------------------------------- FFN
 
 
@@ -311,3 +350,77 @@ def test_expert_ffn_is_deterministic_and_captures(gpu_lib):
     graph.replay()
     ok(moe)
     assert torch.equal(y0, y1) and torch.equal(y0, y2) and torch.equal(y0, y3)
+
+
+# ------------------------------------------------------------------------------------------------- layer
+
+
+@pytest.mark.parametrize("experts,name,over", [
+    ("nvfp4", "page3_cf1.25", dict(T=700, h=256, F=192)),            # capacity, drops and pad rows
+    ("mxfp4", "deepseek_v3", dict(T=300, h=256, F=128, E=32, k=4)),  # shared expert, groups of few rows
+    ("nvfp4", "page3_expert_choice", dict(T=512, h=256, F=128)),
+    ("mxfp4", "mixtral_sinkhorn", dict(T=512, h=256, F=192, bias="none"))])
+def test_layer_with_experts_in_4_bits(gpu_lib, experts, name, over):
+    """MoELayer(experts=...) against the float64 layer on the quantised weights and rows: normwise 2e-2, as the bf16 layer's
+    outputs; and the same bits from a captured graph."""
+    import moe_inputs
+    from oracle import moe_oracle as O
+    from tests import cases
+    from top_routing_dispatch_moe_gb300.layer import MoELayer
+    cfg = moe_inputs.get_config(name, **over)
+    inp = cases.ec_inputs(cfg) if cfg.routing == "expert_choice" else cases.router_inputs(cfg)
+    dev = torch.device("cuda")
+    up = lambda a: cases.to_device(a, cfg, dev)   # noqa: E731
+    ws = [up(w) for w in moe_inputs.all_expert_weights(cfg)]
+    sh = [up(np.ascontiguousarray(w[0])[None]) for w in moe_inputs.all_expert_weights(cfg, shared=True)] if cfg.n_shared else None
+    gs, ags = torch.tensor([64.0], device=dev), torch.tensor([256.0], device=dev)
+    fmt = experts[:2]
+    if fmt == "mx":
+        gs = ags = None
+    layer = MoELayer(T=cfg.T, h=cfg.h, E=cfg.E, k=cfg.k, F=cfg.F, gating=cfg.gating, cf=cfg.cf, R=cfg.R, alpha=cfg.alpha,
+                     w_r=up(inp["w_r"]), bias=torch.from_numpy(inp["bias"]).to(dev) if inp["bias"] is not None else None,
+                     w_gate=ws[0], w_up=ws[1], w_down=ws[2], shared=sh, device=dev, routing=cfg.routing, experts=experts,
+                     fp4_gscale=gs, fp4_act_gscale=ags)
+    x = up(inp["x"])
+    y = layer.forward(x).clone()
+    ok(gpu_lib)
+
+    def quantised(w):                                    # [n, k] -> the values it is held as
+        m = 2.0 ** np.floor(np.log2(448.0 * 6.0 / np.abs(w).max())) if fmt == "nv" else 1.0
+        return Q.dequantize(*Q.quantize(w * m, fmt), fmt) / m
+
+    def through(v, m):
+        m = float(m) if m is not None else 1.0
+        return Q.dequantize(*Q.quantize(v * m, fmt), fmt) / m
+
+    def ffn(rows, w):
+        g, u = (through(rows, gs) @ quantised(t).T for t in w[:2])
+        return through(g / (1 + np.exp(-g)) * u, ags) @ quantised(w[2]).T
+
+    x64 = f64(x)
+    w64 = [f64(w) for w in ws]
+    if cfg.routing == "expert_choice":
+        tokens = layer.ec["tokens"].cpu().numpy()
+        gates = layer.ec["gates"].double().cpu().numpy()
+        want = np.zeros_like(x64)
+        for e in range(cfg.E):
+            want[tokens[e]] += gates[e][:, None] * ffn(x64[tokens[e]], [w[e] for w in w64])
+    else:
+        want = np.zeros_like(x64) if sh is None else ffn(x64, [f64(w[0]) for w in sh])
+        ids, gates = layer.r_out["topk_ids"].cpu().numpy(), layer.r_out["gates"].double().cpu().numpy()
+        kept = layer.d_out["drop_mask"].cpu().numpy() == 0
+        np.testing.assert_array_equal(ids, inp["route"]["ids"])
+        for e in range(cfg.E):
+            t, j = np.nonzero((ids == e) & kept)
+            if len(t):
+                want[t] += gates[t, j][:, None] * ffn(x64[t], [w[e] for w in w64])
+    assert cases.rel_l2(f64(y), want) <= 2e-2
+    graph = layer.capture_forward(x)
+    layer.y.zero_()
+    graph.replay()
+    ok(gpu_lib)
+    assert torch.equal(layer.y, y)
+    with pytest.raises(NotImplementedError):
+        layer.native_desc()
+    with pytest.raises(RuntimeError):
+        layer.backward(x, y)

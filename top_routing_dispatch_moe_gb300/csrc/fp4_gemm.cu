@@ -925,6 +925,8 @@ using Narrow = Cfg<64, 6>;
 // 64 columns and 26 with 128; 8192 rows by 8 x 4096 x 12288 (MX), 225 us with 192 columns and 199 by pairs.
 template <class F, int EPI>
 static int product(const void* a_codes, long long rows, int G, int K, const Params& p, cudaStream_t s) {
+    MOE_REQUIRE((long long)sched_max_tiles(rows, G) * p.NB64 < (1LL << 31), MOE_ERR_INVALID_ARG,
+                "4-bit product: %lld rows by %d columns are over 2^31 tiles", rows, p.NB64 * 64);
     const long long used = std::min<long long>(rows, G), kst = stages_of(K), sms = num_sms();
     const long long tiles = std::max(used, used / 2 + rows / BM), pairs = std::max(used, used / 2 + rows / (2 * BM));
     const long long a_bytes = std::min<long long>(4, cdiv(rows, 32 * tiles)) * 4096 + SF_BYTES<F>;

@@ -28,12 +28,19 @@ class MoELayer:
     forward(x, events=...) records one CUDA event before the first stage and after each stage when given
     a dict of lists, so callers can time the stages on the launching stream. forward(x, save=True) (a layer built
     with backward=True, bf16 token-choice or Sinkhorn routing, bf16 payload) also keeps the experts'
-    pre-activations g and u, so that the next backward() needs no recompute of the up/gate GEMM."""
+    pre-activations g and u, so that the next backward() needs no recompute of the up/gate GEMM.
+
+    experts="nvfp4" or "mxfp4" (bf16, forward only) holds the experts in 4 bits: the weights are quantised at construction
+    (nvfp4: each expert's matrix times a power of two first that brings its largest magnitude near 448 * 6), the tokens' rows and the activations inside
+    the FFN (fp4_gscale, fp4_act_gscale: fp32 scalar tensors that they are multiplied with before, e.g. calibrated to
+    448 * 6 / the largest magnitude expected; None: 1). The FFN reads x through the dispatch's row indices; both products
+    and the quantisations between them are the stage "up_gate", and "down" is empty."""
 
     STAGES = ("router", "dispatch", "up_gate", "down", "shared_up_gate", "shared_down", "combine")
 
     def __init__(self, *, T, h, E, k, F, gating, cf, R, alpha, w_r, bias, w_gate, w_up, w_down,
-                 shared=None, device="cuda", routing="token", backward=False, payload="bf16", fuse_combine=False):
+                 shared=None, device="cuda", routing="token", backward=False, payload="bf16", fuse_combine=False,
+                 experts="dtype", fp4_gscale=None, fp4_act_gscale=None):
         self.T, self.h, self.E, self.k, self.F = T, h, E, k, F
         self.gating, self.R, self.alpha = gating, R, alpha
         self.C = capacity_slots(cf, k, T, E)
@@ -44,8 +51,15 @@ class MoELayer:
         self.w_r = w_r
         self.w_r_packed = moe.moe_pack_router_weight(w_r)    # the router's operand layout, packed once
         self.bias = bias
-        self.packed = moe.moe_pack_expert_weights(w_gate, w_up, w_down)
-        self.shared_packed = moe.moe_pack_expert_weights(*shared) if shared is not None else None
+        if experts not in ("dtype", "nvfp4", "mxfp4"):
+            raise ValueError("experts: 'dtype', 'nvfp4' or 'mxfp4'")
+        self.fp4 = None if experts == "dtype" else experts[:2]
+        if self.fp4 and (dt != torch.bfloat16 or backward or payload != "bf16" or fuse_combine):
+            raise ValueError("experts in 4 bits: bf16 with the bf16 send buffer, the separate combine and no backward")
+        self.fp4_gscale, self.fp4_act_gscale = fp4_gscale, fp4_act_gscale
+        pack = moe.moe_pack_expert_weights if self.fp4 is None else self._pack_fp4
+        self.packed = pack(w_gate, w_up, w_down)
+        self.shared_packed = pack(*shared) if shared is not None else None
         # the dgrad GEMMs' weight operands (only when the layer will run backward: twice the weight memory)
         self.packed_bwd = moe.moe_pack_expert_weights_backward(w_gate, w_up, w_down) if backward else None
         self.shared_packed_bwd = (moe.moe_pack_expert_weights_backward(*shared)
@@ -93,11 +107,14 @@ class MoELayer:
             self.d_out["buf8"] = torch.empty((self.rows, h), dtype=torch.uint8, device=dev)
             self.d_out["scales"] = torch.empty((self.rows, h // 128), dtype=f32, device=dev)
             self.buf_deq = torch.empty((self.rows, h), dtype=dt, device=dev)   # the receive side, dequantised
-        self.act = torch.empty((self.rows, F), dtype=dt, device=dev)
+        if self.fp4:                                 # act stays in 4 bits, in the FFN's workspace
+            self.fp4_ws = moe._bytes_tensor(max(moe.moe_fp4_expert_ffn_workspace_size(E, h, F, self.rows, self.fp4),
+                                                moe.moe_fp4_expert_ffn_workspace_size(1, h, F, T, self.fp4)), dev)
+        self.act = torch.empty((0 if self.fp4 else self.rows, F), dtype=dt, device=dev)
         self.eout = torch.empty((self.rows, h), dtype=dt, device=dev)
         if self.shared_packed is not None:
             self.sh_sched = moe.moe_dense_tile_sched(T, device=dev)
-            self.sh_act = torch.empty((T, F), dtype=dt, device=dev)
+            self.sh_act = torch.empty((0 if self.fp4 else T, F), dtype=dt, device=dev)
             self.sh_out = torch.empty((T, h), dtype=dt, device=dev)
         self.y = torch.empty((T, h), dtype=dt, device=dev)
         # combine fused into the down GEMM's epilogue (bf16, token-choice or Sinkhorn routing): one launch fewer,
@@ -113,6 +130,35 @@ class MoELayer:
             self.gu = torch.empty((self.rows, moe.gu_cols(F)), dtype=dt, device=dev)
             self.sh_gu = (torch.empty((T, moe.gu_cols(F)), dtype=dt, device=dev)
                           if self.shared_packed is not None else None)
+
+    @staticmethod
+    def _fp4_multiplier(w):
+        """For each expert the power of two that brings the largest magnitude of w [E, ...] into (224 * 6, 448 * 6]: the
+        products are exact, and the block scales stay in e4m3's normal range."""
+        return torch.exp2(torch.floor(torch.log2(448.0 * 6.0 / w.abs().amax((1, 2)).float().clamp_min(1e-30))))
+
+    def _pack_fp4(self, gate, up, down):
+        """(packed 4-bit weights, the three alphas [E] of moe_fp4_expert_ffn) of bf16 weights [E, ...]."""
+        quantised, alphas = [], []
+        div = (self.fp4_gscale, self.fp4_gscale, self.fp4_act_gscale)     # what the operand's multiplier left to divide out
+        for w, by in zip((gate, up, down), div):
+            E, n, k = w.shape
+            alpha = torch.ones(E, dtype=torch.float32, device=w.device)
+            if self.fp4 == "nv":
+                mult = self._fp4_multiplier(w)
+                alpha = alpha / mult
+                parts = [moe.moe_fp4_quantize(w[e], "nv", gscale=mult[e:e + 1]) for e in range(E)]
+                quantised.append(tuple(torch.stack(t) for t in zip(*parts)))
+            else:
+                c, sc = moe.moe_fp4_quantize(w.reshape(E * n, k), "mx")
+                quantised.append((c.view(E, n, -1), sc.view(E, n, -1)))
+            alphas.append(alpha if by is None else alpha / by)
+        return moe.moe_fp4_pack_expert_weights(*quantised, gate.shape[2], gate.shape[1], self.fp4), alphas
+
+    def _ffn_fp4(self, x, packed, out, stream, **rows):
+        moe.moe_fp4_expert_ffn(x, rows.pop("offsets", None), packed[0], self.F, self.fp4, alpha_gate=packed[1][0],
+                               alpha_up=packed[1][1], alpha_down=packed[1][2], gscale=self.fp4_gscale,
+                               act_gscale=self.fp4_act_gscale, out=out, ws=self.fp4_ws, stream=stream, **rows)
 
     def forward(self, x, stream=None, events=None, y=None, save=False):
         if save and (self.packed_bwd is None or self.routing not in ("token", "sinkhorn")
@@ -153,7 +199,17 @@ class MoELayer:
         sched = self.d_out["tile_sched"]
         shared_out = None
         out = self.y if y is None else y
-        if self.payload == "fp8":
+        if self.fp4:
+            src = self.ec["tokens"].view(-1) if self.routing == "expert_choice" else self.d_out["src_token"]
+            self._ffn_fp4(x, self.packed, self.eout, stream, E=self.E, tile_sched=sched, src=src)
+            mark("up_gate")
+            mark("down")
+            if self.shared_packed is not None:
+                self._ffn_fp4(x, self.shared_packed, self.sh_out, stream, E=1, tile_sched=self.sh_sched)
+                mark("shared_up_gate")
+                mark("shared_down")
+                shared_out = self.sh_out
+        elif self.payload == "fp8":
             # dequantise the e4m3 send buffer in a pass of its own, then the bf16 GEMM (on GB300 faster than
             # moe_expert_up_gate_fp8's dequantisation inside the GEMM, with the same act)
             moe.moe_dequant_fp8(self.d_out["buf8"], self.d_out["scales"], out=self.buf_deq, stream=stream)
@@ -338,6 +394,8 @@ class MoELayer:
         """The moe_layer_desc of this layer for the one-call C entry points moe_layer_forward and
         moe_layer_forward_host (every routing mode and send buffer of `forward`, with the separate combine: the
         same launches): it points at this layer's packed parameters, which must outlive its use."""
+        if self.fp4:
+            raise NotImplementedError("moe_layer_forward runs the experts in the layer's dtype (MoELayer(experts='dtype'))")
         if self.fuse_combine:
             raise NotImplementedError("moe_layer_forward runs the separate combine (MoELayer(fuse_combine=False))")
         return moe.moe_layer_desc(T=self.T, h=self.h, E=self.E, k=self.k, F=self.F, dtype=self.dtype,
