@@ -608,7 +608,7 @@ int launch_quantize_operand(const void* x, long long ldx, int x_rows, const int3
         return fmt == MOE_FP4_NV ? gather(Nv{}) : gather(Mx{});
     }
     const long long items = (long long)sched_max_tiles(rows, std::min(G, rows)) * cdiv(stages_of(K), 2);
-    const int parts = items < 4LL * num_sms() ? 2 : 0;
+    const int parts = items < 4LL * num_sms() && rows > 32LL * std::min(G, rows) ? 2 : 0;
     const int grid = (int)std::min<long long>(items << parts, (long long)num_sms() * 4);
     return by_kind(fmt, dtype, vec_ok(x, ldx, dtype), [&](auto f, auto t, auto v) {
         using F = decltype(f);

@@ -130,6 +130,11 @@ __device__ __forceinline__ void fma2(float* d, const float* a, float b, const fl
         "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
         : "=f"(d[0]), "=f"(d[1]) : "f"(a[0]), "f"(a[1]), "f"(b), "f"(c[0]), "f"(c[1]));
 }
+__device__ __forceinline__ void fma2v(float* d, const float* a, const float* b, const float* c) {
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d[0]), "=f"(d[1]) : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]), "f"(c[0]), "f"(c[1]));
+}
 // The rounded quotients v / s of two values, given the rounded reciprocal r of s: q = v r is off by less than two units in
 // its last place, and q + (v - q s) r is the rounded quotient (Markstein's correction: v - q s is exact in one fused step,
 // and r has no error beyond its own rounding), as long as neither product leaves the normal range.
@@ -138,6 +143,15 @@ __device__ __forceinline__ void quotient2(float* v, float s, float r) {
     mul2(q, v, r);
     fma2(e, q, -s, v);
     fma2(v, e, r, q);
+}
+// The same of two quotients v / d, r within a unit in the last place of 1 / d (the result is then within one rounding of the
+// quotient, and all but always the rounded quotient).
+__device__ __forceinline__ void quotient2v(float* v, const float* d, const float* r) {
+    float q[2], e[2];
+    mul2v(q, v, r);
+    const float n[2] = {-q[0], -q[1]};
+    fma2v(e, n, d, v);
+    fma2v(v, e, r, q);
 }
 
 // N values of one block -> codes, as the correctly rounded quotient v / s rounded to e2m1, so that a quotient half way

@@ -233,22 +233,25 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const CUtensorMa
         const float ag = p.alpha ? __ldg(p.alpha + wk.g) : 1.f, au = p.alpha_up ? __ldg(p.alpha_up + wk.g) : 1.f;
         const float gs = p.act_gscale ? __ldg(p.act_gscale) : 1.f;
         const int f0 = c0 / 2;                   // first column of act
-        // g / (1 + exp(-g)) * u: the exponential and the reciprocal by the MUFU (a few units in the last place each)
+        // g / (1 + exp(-g)) * u, each step rounded as written, so that an activation at a rounding tie of its code goes the
+        // way that the plain fp32 formula takes: with the quotient as g times the MUFU's reciprocal alone, two in a million
+        // codes went the other way. (1 + exp(-g) is cut to 1e30: the quotient is 0 in 4 bits by then.)
         float* u = v + 32;
-        const float ae = ag * -1.44269504f, c = au * gs;
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-            float e[2], t[2];
-            mul2(t, v + i, ae);
+            float t[2], d[2], r[2];
             mul2(v + i, v + i, ag);
-            mul2(u + i, u + i, c);
+            mul2(t, v + i, -1.44269504f);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                asm("ex2.approx.f32 %0, %1;" : "=f"(e[j]) : "f"(t[j]));
-                asm("rcp.approx.f32 %0, %1;" : "=f"(e[j]) : "f"(e[j] + 1.f));
+                asm("ex2.approx.f32 %0, %1;" : "=f"(d[j]) : "f"(t[j]));
+                d[j] = fminf(1.f + d[j], 1e30f);
+                asm("rcp.approx.f32 %0, %1;" : "=f"(r[j]) : "f"(d[j]));
             }
-            mul2v(v + i, v + i, e);
-            mul2v(u + i, u + i, v + i);
+            quotient2v(v + i, d, r);
+            mul2(u + i, u + i, au);
+            mul2v(u + i, v + i, u + i);
+            mul2(u + i, u + i, gs);
         }
         uint32_t w[4], bytes = 0u;
 #pragma unroll
