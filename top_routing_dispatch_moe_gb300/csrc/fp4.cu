@@ -272,7 +272,7 @@ quantize_operand_kernel(const T* __restrict__ x, long long ldx, int x_rows, cons
         for (int i = threadIdx.x; i < PIECES * STRIDE / 16; i += QTHREADS)
             reinterpret_cast<uint4*>(s_sf)[i] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
-        for (int i0 = warp; i0 < 4 * per; i0 += U * QWARPS) {
+        for (int i0 = warp; i0 < (parts ? 4 * per : n); i0 += U * QWARPS) {
             Raw16<T> raw[U];
             int r[U];
 #pragma unroll

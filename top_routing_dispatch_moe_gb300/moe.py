@@ -7,6 +7,7 @@ Importing this module fails loudly if the library has not been built (there is n
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -774,14 +775,26 @@ def _fp4_stream(stream, t):
     return _raw_stream(t.device.index) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
 
 
+@functools.lru_cache(maxsize=None)
 def moe_fp4_codes_pitch(K: int) -> int:
     """Bytes of codes a row: 16 for every 32 columns begun."""
     return _lib.moe_fp4_codes_pitch(K)
 
 
+@functools.lru_cache(maxsize=None)
 def moe_fp4_scales_pitch(K: int, fmt) -> int:
     """Block scales a row."""
     return _lib.moe_fp4_scales_pitch(K, _fp4_format(fmt))
+
+
+@functools.lru_cache(maxsize=None)
+def _fp4_weight_bytes(G: int, N: int, K: int, fmt: int) -> int:
+    return _lib.moe_fp4_packed_weight_bytes(G, N, K, fmt)
+
+
+@functools.lru_cache(maxsize=None)
+def _fp4_experts_bytes(E: int, h: int, F: int, fmt: int) -> int:
+    return _lib.moe_fp4_packed_expert_weights_bytes(E, h, F, fmt)
 
 
 def moe_fp4_quantize(x, fmt="nv", *, gscale=None, src=None, codes=None, scales=None, stream=None):
@@ -790,7 +803,7 @@ def moe_fp4_quantize(x, fmt="nv", *, gscale=None, src=None, codes=None, scales=N
     multiplied with first; src [rows] int32: x's row of each row, -1 for zeros."""
     f, K, ldx = _fp4_format(fmt), x.shape[-1], _fp4_rows(x, "x")
     rows = x.shape[0] if src is None else src.numel()
-    nb, pitch = _lib.moe_fp4_scales_pitch(K, f), _lib.moe_fp4_codes_pitch(K)
+    nb, pitch = moe_fp4_scales_pitch(K, f), moe_fp4_codes_pitch(K)
     codes = torch.empty((rows, pitch), dtype=torch.uint8, device=x.device) if codes is None else codes
     scales = torch.empty((rows, nb), dtype=torch.uint8, device=x.device) if scales is None else scales
     _check(_lib.moe_fp4_quantize(x.data_ptr(), ldx, x.shape[0], _fp4_data(src, 0, torch.int32, "src"), rows, K,
@@ -807,8 +820,8 @@ def moe_fp4_dequantize(codes, scales, K: int, fmt="nv", *, gscale=None, dtype=to
     ldo = _fp4_rows(out, "out")
     if out.shape[0] != rows or out.shape[1] != K:
         _fp4_fail(f"out: [{rows}, {K}]")
-    _check(_lib.moe_fp4_dequantize(_fp4_data(codes, rows * _lib.moe_fp4_codes_pitch(K), torch.uint8, "codes"),
-                                   _fp4_data(scales, rows * _lib.moe_fp4_scales_pitch(K, f), torch.uint8, "scales"), rows, K,
+    _check(_lib.moe_fp4_dequantize(_fp4_data(codes, rows * moe_fp4_codes_pitch(K), torch.uint8, "codes"),
+                                   _fp4_data(scales, rows * moe_fp4_scales_pitch(K, f), torch.uint8, "scales"), rows, K,
                                    f, _fp4_data(gscale, 1, torch.float32, "gscale"), _fp4_dtype(out.dtype), out.data_ptr(),
                                    ldo, _fp4_stream(stream, codes)))
     return out
@@ -818,7 +831,7 @@ def moe_fp4_pack_weight(codes, scales, K: int, fmt="nv", packed=None, stream=Non
     """A weight [G, N, K] as moe_fp4_quantize (or a checkpoint) holds it, codes [G, N, pitch] and scales [G, N, blocks],
     in the operand layout of moe_fp4_linear."""
     f, (G, N) = _fp4_format(fmt), codes.shape[:2]
-    need = _lib.moe_fp4_packed_weight_bytes(G, N, K, f)
+    need = _fp4_weight_bytes(G, N, K, f)
     packed = _bytes_tensor(need, codes.device) if packed is None else packed
     _check(_lib.moe_fp4_pack_weight(_fp4_data(codes, G * N * moe_fp4_codes_pitch(K), torch.uint8, "codes"),
                                     _fp4_data(scales, G * N * moe_fp4_scales_pitch(K, f), torch.uint8, "scales"), G, N, K, f,
@@ -848,7 +861,7 @@ def moe_fp4_linear(x, offsets, packed, N: int, fmt="nv", *, G: int | None = None
     _check(_lib.moe_fp4_linear(x.data_ptr(), ldx, x.shape[0], _fp4_data(src, 0, torch.int32, "src"),
                                _fp4_data(offsets, 2, torch.int32, "offsets"),
                                _fp4_data(tile_sched, 4, torch.int32, "tile_sched"),
-                               _fp4_data(packed, _lib.moe_fp4_packed_weight_bytes(G, N, K, f), torch.uint8, "packed"),
+                               _fp4_data(packed, _fp4_weight_bytes(G, N, K, f), torch.uint8, "packed"),
                                _fp4_data(alpha, G, torch.float32, "alpha"), _fp4_data(gscale, 1, torch.float32, "gscale"),
                                G, N, K, rows, f, _fp4_dtype(x.dtype), out.data_ptr(), ldo, _fp4_dtype(out.dtype),
                                _fp4_data(ws, 0, torch.uint8, "ws"), ws.numel(), _fp4_stream(stream, x)))
@@ -862,7 +875,7 @@ def moe_fp4_pack_expert_weights(gate, up, down, h: int, F: int, fmt="nv", packed
     for (c, s), n, k, what in ((gate, F, h, "gate"), (up, F, h, "up"), (down, h, F, "down")):
         data.append(_fp4_data(c, E * n * moe_fp4_codes_pitch(k), torch.uint8, what + " codes"))
         data.append(_fp4_data(s, E * n * moe_fp4_scales_pitch(k, f), torch.uint8, what + " scales"))
-    need = _lib.moe_fp4_packed_expert_weights_bytes(E, h, F, f)
+    need = _fp4_experts_bytes(E, h, F, f)
     packed = _bytes_tensor(need, gate[0].device) if packed is None else packed
     _check(_lib.moe_fp4_pack_expert_weights(*data, E, h, F, f, _fp4_data(packed, need, torch.uint8, "packed"),
                                             _fp4_stream(stream, packed)))
@@ -891,7 +904,7 @@ def moe_fp4_expert_ffn(x, offsets, packed, F: int, fmt="nv", *, E: int | None = 
     _check(_lib.moe_fp4_expert_ffn(x.data_ptr(), ldx, x.shape[0], _fp4_data(src, 0, torch.int32, "src"),
                                    _fp4_data(offsets, 2, torch.int32, "offsets"),
                                    _fp4_data(tile_sched, 4, torch.int32, "tile_sched"),
-                                   _fp4_data(packed, _lib.moe_fp4_packed_expert_weights_bytes(E, h, F, f), torch.uint8,
+                                   _fp4_data(packed, _fp4_experts_bytes(E, h, F, f), torch.uint8,
                                              "packed"),
                                    _fp4_data(alpha_gate, E, torch.float32, "alpha_gate"),
                                    _fp4_data(alpha_up, E, torch.float32, "alpha_up"),
