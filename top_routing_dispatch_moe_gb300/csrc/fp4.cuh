@@ -184,6 +184,57 @@ __device__ __forceinline__ float scale_value(uint32_t b) {
     if constexpr (F::ID == MOE_FP4_NV) return e4m3_value(b);
     return b == 255u ? __uint_as_float(0x7FC00000u) : b ? __uint_as_float(b << 23) : __uint_as_float(1u << 22);
 }
+
+// Tile counts of the groups [offsets[g], offsets[g + 1]) summed up into first[0 .. G] (G <= 1024) by a block of NT threads;
+// 0 everywhere, and true, if an offset falls or leaves [0, rows].
+template <int NT>
+__device__ __forceinline__ bool scan_groups(const int32_t* __restrict__ offsets, int G, int rows, int* first) {
+    constexpr int PER = (1024 + NT - 1) / NT;
+    __shared__ int s_warp[NT / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g0 = threadIdx.x * PER;
+    int n[PER], sum = 0;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        n[i] = 0;
+        if (g0 + i < G) {
+            const int lo = __ldg(offsets + g0 + i), hi = __ldg(offsets + g0 + i + 1);
+            if (lo < 0 || hi < lo || hi > rows) bad = true;
+            else n[i] = (int)(((long long)hi - lo + MOE_TILE_M - 1) / MOE_TILE_M);
+        }
+        sum += n[i];
+    }
+    bad = __syncthreads_or(bad);
+    int v = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+    }
+    if (lane == 31) s_warp[warp] = v;
+    __syncthreads();
+    int at = v - sum;
+    for (int i = 0; i < warp; ++i) at += s_warp[i];
+    if (threadIdx.x == 0) first[0] = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        at += n[i];
+        if (g0 + i < G) first[g0 + i + 1] = bad ? 0 : at;
+    }
+    __syncthreads();
+    return bad;
+}
+
+// Tile t of the groups: {group, first row, end, 0}.
+__device__ __forceinline__ int4 group_tile(const int32_t* __restrict__ offsets, const int* first, int G, int t) {
+    int lo = 0, hi = G;
+    while (lo < hi) {                    // last group with first[g] <= t
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    const int row0 = __ldg(offsets + lo) + (t - first[lo]) * MOE_TILE_M;
+    return make_int4(lo, row0, min(row0 + MOE_TILE_M, __ldg(offsets + lo + 1)), 0);
+}
 #endif
 
 // The rows of the groups, quantised into the product's operand: of `offsets`, whose schedule is then written to `sched`, or

@@ -50,8 +50,9 @@ struct Cfg {
 };
 
 struct Params {
+    const int32_t* offsets;      // the groups' rows, or null: the tiles of `sched`
     const int32_t* sched;
-    int G, max_tiles;            // what the schedule has to agree with
+    int G, rows, max_tiles;      // (groups and tiles: what a schedule has to agree with)
     const uint8_t *a_sf, *w, *w_sf;
     int steps, kst;              // 64-column MMA steps, 256-column stages
     int NT, NB64, NB128;         // n-tiles; 64-row and 128-row blocks of the packed weight
@@ -72,17 +73,33 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 
 struct Work { int g, tile, row0, row1, n; };
 
-// Item w: group by group, n-tile next, m-tile fastest: CTAs that run together share a weight tile. prefix: the schedule's
-// tiles of each group summed up, in shared memory (a search through global memory costs a decode call microseconds).
-__device__ __forceinline__ Work map_work(const int32_t* sched, const int* prefix, int G, int NT, int w) {
-    int lo = 0, hi = G;
-    while (lo < hi) {                    // last g with prefix[g] * NT <= w
-        const int mid = (lo + hi + 1) >> 1;
-        if ((long long)prefix[mid] * NT <= w) lo = mid; else hi = mid - 1;
+// first[g]: tiles before group g, first[G]: all of them (0 where offsets or schedule are no good; the quantisation reports it),
+// in shared memory: a search through global memory costs a decode call microseconds. From the offsets, which are older than
+// the kernel before this one, it is found without waiting for that kernel.
+__device__ __forceinline__ void find_tiles(const Params& p, int* first) {
+    if (p.offsets) {
+        scan_groups<THREADS>(p.offsets, p.G, p.rows, first);
+        return;
     }
-    const int p0 = prefix[lo], mt = prefix[lo + 1] - p0, local = w - p0 * NT;
+    const bool fits = p.sched[1] == p.G && p.sched[0] <= p.max_tiles;
+    for (int i = threadIdx.x; i <= p.G; i += THREADS) first[i] = fits ? p.sched[kSchedHeader + i] : 0;
+    __syncthreads();
+}
+__device__ __forceinline__ int4 tile_entry(const Params& p, const int* first, int g, int t) {
+    if (!p.offsets) return reinterpret_cast<const int4*>(p.sched + sched_tiles_offset(p.G))[t];
+    const int row0 = __ldg(p.offsets + g) + (t - first[g]) * BM;
+    return make_int4(g, row0, min(row0 + BM, __ldg(p.offsets + g + 1)), 0);
+}
+// Item w: group by group, n-tile next, m-tile fastest: CTAs that run together share a weight tile.
+__device__ __forceinline__ Work map_work(const Params& p, const int* first, int w) {
+    int lo = 0, hi = p.G;
+    while (lo < hi) {                    // last g with first[g] * NT <= w
+        const int mid = (lo + hi + 1) >> 1;
+        if ((long long)first[mid] * p.NT <= w) lo = mid; else hi = mid - 1;
+    }
+    const int p0 = first[lo], mt = first[lo + 1] - p0, local = w - p0 * p.NT;
     const int n = local / mt, t = p0 + local % mt;
-    const int4 e = reinterpret_cast<const int4*>(sched + sched_tiles_offset(G))[t];
+    const int4 e = tile_entry(p, first, lo, t);
     return Work{e.x, t, e.y, e.z, n};
 }
 
@@ -313,7 +330,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const uint32_t mma_done = bar0 + 8u * (2 * STAGES + 4);
     auto sfull = [&](int b) { return bar0 + 8u * (2 * STAGES + 5 + b); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5 + SF_BUFS);
-    int* prefix = reinterpret_cast<int*>(bars + 32);
+    int* first = reinterpret_cast<int*>(bars + 32);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -328,27 +345,25 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         prefetch_tmap(&tmA32);
     }
     if (warp == 1) tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+    find_tiles(p, first);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // (a programmatic dependent: the schedule and the operands are read only from here on)
-    pdl_wait();
-    pdl_trigger();
-    const int G = p.G, ntiles = p.sched[0];
-    const bool fits = p.sched[1] == G && ntiles <= p.max_tiles;      // (else: another call's schedule)
-    const int total = uniform(fits ? ntiles * p.NT : 0);
-    if (!fits && blockIdx.x == 0 && threadIdx.x == 0) latch_device_error(p.err, kDevErrBadIndex, 0x203u);
-    if (fits)
-        for (int i = threadIdx.x; i <= G; i += THREADS) prefix[i] = p.sched[kSchedHeader + i];
-    __syncthreads();
+    // (a programmatic dependent of the kernel that writes the row operand: the groups, the weights and everything above do
+    // not wait for it)
+    const int total = uniform(first[p.G] * p.NT);
+    if (warp != 0) {
+        pdl_wait();
+        pdl_trigger();
+    }
 
     if (warp == 0) {
         int stage = 0;
         uint32_t phase = 0, issued = 0, last_par = 0;
         bool ok = true, ready = false;              // ready: the next ring stage was seen free
         for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
-            const Work wk = map_work(p.sched, prefix, G, p.NT, w);
+            const Work wk = map_work(p, first, w);
             const int n = uniform(wk.n), g = uniform(wk.g), tile = uniform(wk.tile), row0 = uniform(wk.row0);
             const int boxes = uniform((wk.row1 - wk.row0 + 31) >> 5);
             const int nb = min(BN / 64, p.NB64 - n * (BN / 64));
@@ -357,21 +372,32 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             const uint8_t* s0 = p.w_sf + ((size_t)g * p.kst * p.NB128 + t0) * SF_BYTES<F>;
             const uint8_t* a0 = p.a_sf + (size_t)tile * p.kst * SF_BYTES<F>;
             const uint32_t tx = (uint32_t)(boxes * 4096 + nb * 8192 + (1 + nt) * SF_BYTES<F>);
+            auto weights = [&](int st, int kb) {
+                expect_elected(full(st), tx);
+                bulk_elected(sB + st * B_BYTES, w0 + (size_t)kb * p.NB64 * 8192, nb * 8192, full(st));
+                bulk_elected(sS + st * SFS + SF_BYTES<F>, s0 + (size_t)kb * p.NB128 * SF_BYTES<F>, nt * SF_BYTES<F>, full(st));
+            };
+            int early = 0;                          // stages whose weights are on their way before the row operand is there
+            if (w == (int)blockIdx.x) {
+                for (; early < min(STAGES, p.kst); ++early) weights(early, early);
+                pdl_wait();
+                pdl_trigger();
+            }
             for (int kb = 0; kb < p.kst; ++kb) {
-                if (!ready) ok = wait_warp(empty(stage), phase ^ 1u, p.wait_limit, abort_flag, p.err, 0x210u);
-                if (!ok) break;
-                const uint32_t f = full(stage), sf = sS + stage * SFS, sa = sA + stage * A_BYTES;
-                expect_elected(f, tx);
-                bulk_elected(sB + stage * B_BYTES, w0 + (size_t)kb * p.NB64 * 8192, nb * 8192, f);
+                if (kb >= early) {
+                    if (!ready) ok = wait_warp(empty(stage), phase ^ 1u, p.wait_limit, abort_flag, p.err, 0x210u);
+                    if (!ok) break;
+                    weights(stage, kb);
+                }
+                const uint32_t f = full(stage), sa = sA + stage * A_BYTES;
                 if (boxes == 4) tma_elected(sa, &tmA, kb * (SEG_K / 2), row0, f);
                 else
                     for (int b = 0; b < boxes; ++b) tma_elected(sa + b * 4096, &tmA32, kb * (SEG_K / 2), row0 + 32 * b, f);
-                bulk_elected(sf + SF_BYTES<F>, s0 + (size_t)kb * p.NB128 * SF_BYTES<F>, nt * SF_BYTES<F>, f);
-                bulk_elected(sf, a0 + (size_t)kb * SF_BYTES<F>, SF_BYTES<F>, f);
+                bulk_elected(sS + stage * SFS, a0 + (size_t)kb * SF_BYTES<F>, SF_BYTES<F>, f);
                 issued |= 1u << stage;
                 last_par = (last_par & ~(1u << stage)) | (phase << stage);
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                ready = test_warp(empty(stage), phase ^ 1u);
+                ready = kb + 1 >= early && test_warp(empty(stage), phase ^ 1u);
             }
         }
         if (lane == 0)
@@ -427,7 +453,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         uint32_t phase = 0, ophase = 1;             // (the rounds before the first count as complete)
         bool ok = true, loaded = false, freed = false;
         for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
-            const bool odd = BN % 128 == 64 && (map_work(p.sched, prefix, G, p.NT, w).n & 1);
+            const bool odd = BN % 128 == 64 && (map_work(p, first, w).n & 1);
             for (int kb = 0; kb < p.kst; ++kb) {
                 if (!loaded) ok = wait_warp(full(stage), phase, p.wait_limit, abort_flag, p.err, 0x241u);
                 if (!ok) break;
@@ -472,7 +498,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         int iter = 0;
         for (int w = blockIdx.x; w < total; w += gridDim.x, ++iter) {
             const int a = iter & 1;
-            const Work wk = map_work(p.sched, prefix, G, p.NT, w);       // (before the wait: its loads take a while)
+            const Work wk = map_work(p, first, w);       // (before the wait: its loads take a while)
             if (!wait_warp(tfull(a), (iter >> 1) & 1, p.wait_limit, abort_flag, p.err, 0x230u)) break;
             tc_fence_after();
             const uint32_t tbase = tmem + a * BN + ((uint32_t)quarter << 16);
@@ -516,7 +542,7 @@ constexpr int PB_BYTES = 128 * SEG_K / 2;        // a CTA's half of the weight r
 constexpr int P_STAGES = 4, P_BN = 256, P_SF_BUFS = 3, P_ACC2 = 128, P_SF_COL = P_ACC2 + P_BN, P_SFA_COL = P_SF_COL + 96;
 template <class F> constexpr int P_SFS = 3 * SF_BYTES<F>;
 template <class F> constexpr int P_SMEM = 1024 + EPI_WARPS * 4096 + P_STAGES * (A_BYTES + PB_BYTES + P_SFS<F>) + 256 +
-                                          (MAX_G + 1) * 4;
+                                          2 * (MAX_G + 1) * 4;
 template <class F> constexpr int P_COLS = SF_PIECES<F> * 8;      // scale columns of the weight rows in a stage
 static_assert(P_SF_BUFS * P_COLS<Nv> <= 96 && P_SFA_COL + 2 * SF_PIECES<Nv> * 4 <= TMEM_COLS, "tensor memory columns");
 static_assert(P_SMEM<Nv> <= 227 * 1024, "shared memory per CTA");
@@ -570,19 +596,20 @@ __device__ __forceinline__ bool wait_warp_pair(uint32_t bar, uint32_t parity, lo
 
 // Item w: group by group, n-tile next, pair fastest. tile, arow: what this CTA loads; row0, row1: what it stores.
 struct PairItem { Work wk; int arow, rows; };
-__device__ __forceinline__ PairItem map_pair_item(const int32_t* sched, const int* pp, int G, int NT, int w, int rank) {
-    int lo = 0, hi = G;
+__device__ __forceinline__ int pairs_of(const int* first, int g) { return (first[g + 1] - first[g] + 1) >> 1; }
+// pp[g]: pairs before group g.
+__device__ __forceinline__ PairItem map_pair_item(const Params& p, const int* first, const int* pp, int w, int rank) {
+    int lo = 0, hi = p.G;
     while (lo < hi) {                    // last g with pp[g] * NT <= w
         const int mid = (lo + hi + 1) >> 1;
-        if ((long long)pp[mid] * NT <= w) lo = mid; else hi = mid - 1;
+        if ((long long)pp[mid] * p.NT <= w) lo = mid; else hi = mid - 1;
     }
-    const int np = pp[lo + 1] - pp[lo], local = w - pp[lo] * NT;
+    const int np = pp[lo + 1] - pp[lo], local = w - pp[lo] * p.NT;
     const int n = local / np, q = local % np;
-    const int32_t* prefix = sched + kSchedHeader;
-    const int p0 = prefix[lo], mt = prefix[lo + 1] - p0;
+    const int p0 = first[lo], mt = first[lo + 1] - p0;
     const bool has = 2 * q + rank < mt;
     const int t = p0 + 2 * q + (has ? rank : 0);
-    const int4 e = reinterpret_cast<const int4*>(sched + sched_tiles_offset(G))[t];
+    const int4 e = tile_entry(p, first, lo, t);
     return PairItem{Work{e.x, t, has ? e.y : 0, has ? e.z : 0, n}, e.y, e.z - e.y};
 }
 
@@ -602,7 +629,8 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     const uint32_t tfull = bar0 + 8u * (2 * STAGES + P_SF_BUFS), tempty = tfull + 8u, mma_done = tempty + 8u;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + P_SF_BUFS + 3);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* pp = reinterpret_cast<int*>(bars + 32);
+    int* first = reinterpret_cast<int*>(bars + 32);
+    int* pp = first + MAX_G + 1;
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -617,25 +645,21 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmA32);
     }
-    // (a programmatic dependent: the schedule and the operands are read only from here on)
-    pdl_wait();
-    pdl_trigger();
-    const int G = p.G, ntiles = p.sched[0];
-    const bool fits = p.sched[1] == G && ntiles <= p.max_tiles;      // (else: another call's schedule)
-    if (!fits && blockIdx.x == 0 && threadIdx.x == 0) latch_device_error(p.err, kDevErrBadIndex, 0x203u);
+    // (a programmatic dependent of the kernel that writes the row operand: the groups, the weights and the set-up do not wait
+    // for it)
+    find_tiles(p, first);
     if (warp == 2) {                             // pairs of tiles of each group, summed up
-        const int32_t* prefix = p.sched + kSchedHeader;
         int carry = 0;
         if (lane == 0) pp[0] = 0;
-        for (int base = 0; base < G; base += 32) {
+        for (int base = 0; base < p.G; base += 32) {
             const int g = base + lane;
-            int v = fits && g < G ? (prefix[g + 1] - prefix[g] + 1) >> 1 : 0;
+            int v = g < p.G ? pairs_of(first, g) : 0;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int t = __shfl_up_sync(0xffffffffu, v, off);
                 if (lane >= off) v += t;
             }
-            if (g < G) pp[g + 1] = carry + v;
+            if (g < p.G) pp[g + 1] = carry + v;
             carry += __shfl_sync(0xffffffffu, v, 31);
         }
     }
@@ -645,14 +669,18 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t peer_abort = map_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
-    const int NC = gridDim.x >> 1, cid = blockIdx.x >> 1, total = uniform(pp[G] * p.NT);
+    const int NC = gridDim.x >> 1, cid = blockIdx.x >> 1, total = uniform(pp[p.G] * p.NT);
+    if (warp != 0) {
+        pdl_wait();
+        pdl_trigger();
+    }
 
     if (warp == 0) {
         int stage = 0;
         uint32_t phase = 0, issued = 0, last_par = 0;
         bool ok = true, ready = false;
         for (int w = cid; w < total && ok; w += NC) {
-            const PairItem it = map_pair_item(p.sched, pp, G, p.NT, w, rank);
+            const PairItem it = map_pair_item(p, first, pp, w, rank);
             const int n = uniform(it.wk.n), g = uniform(it.wk.g), tile = uniform(it.wk.tile), arow = uniform(it.arow);
             const int boxes = uniform((it.rows + 31) >> 5), half = uniform((int)rank);
             const int nb = min(2, max(0, p.NB64 - n * 4 - 2 * half)), nt = min(2, p.NB128 - 2 * n);
@@ -660,21 +688,32 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             const uint8_t* s0 = p.w_sf + ((size_t)g * p.kst * p.NB128 + 2 * n) * SF_BYTES<F>;
             const uint8_t* a0 = p.a_sf + (size_t)tile * p.kst * SF_BYTES<F>;
             const uint32_t tx = (uint32_t)(boxes * 4096 + nb * 8192 + (1 + nt) * SF_BYTES<F>);
+            auto weights = [&](int st, int kb) {
+                expect_elected(full(st), tx);
+                if (nb) bulk_elected(sB + st * PB_BYTES, w0 + (size_t)kb * p.NB64 * 8192, nb * 8192, full(st));
+                bulk_elected(sS + st * SFS + SF_BYTES<F>, s0 + (size_t)kb * p.NB128 * SF_BYTES<F>, nt * SF_BYTES<F>, full(st));
+            };
+            int early = 0;
+            if (w == cid) {
+                for (; early < min(STAGES, p.kst); ++early) weights(early, early);
+                pdl_wait();
+                pdl_trigger();
+            }
             for (int kb = 0; kb < p.kst; ++kb) {
-                if (!ready) ok = wait_warp_pair(empty(stage), phase ^ 1u, p.wait_limit, abort_flag, peer_abort, p.err, 0x250u);
-                if (!ok) break;
-                const uint32_t f = full(stage), sf = sS + stage * SFS, sa = sA + stage * A_BYTES;
-                expect_elected(f, tx);
-                if (nb) bulk_elected(sB + stage * PB_BYTES, w0 + (size_t)kb * p.NB64 * 8192, nb * 8192, f);
+                if (kb >= early) {
+                    if (!ready) ok = wait_warp_pair(empty(stage), phase ^ 1u, p.wait_limit, abort_flag, peer_abort, p.err, 0x250u);
+                    if (!ok) break;
+                    weights(stage, kb);
+                }
+                const uint32_t f = full(stage), sa = sA + stage * A_BYTES;
                 if (boxes == 4) tma_elected(sa, &tmA, kb * (SEG_K / 2), arow, f);
                 else
                     for (int b = 0; b < boxes; ++b) tma_elected(sa + b * 4096, &tmA32, kb * (SEG_K / 2), arow + 32 * b, f);
-                bulk_elected(sf + SF_BYTES<F>, s0 + (size_t)kb * p.NB128 * SF_BYTES<F>, nt * SF_BYTES<F>, f);
-                bulk_elected(sf, a0 + (size_t)kb * SF_BYTES<F>, SF_BYTES<F>, f);
+                bulk_elected(sS + stage * SFS, a0 + (size_t)kb * SF_BYTES<F>, SF_BYTES<F>, f);
                 issued |= 1u << stage;
                 last_par = (last_par & ~(1u << stage)) | (phase << stage);
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                ready = test_warp(empty(stage), phase ^ 1u);
+                ready = kb + 1 >= early && test_warp(empty(stage), phase ^ 1u);
             }
         }
         if (lane == 0)
@@ -767,7 +806,7 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         const uint32_t tempty0 = map_rank(tempty, 0);
         int iter = 0;
         for (int w = cid; w < total; w += NC, ++iter) {
-            const Work wk = map_pair_item(p.sched, pp, G, p.NT, w, rank).wk;   // (before the wait: its loads take a while)
+            const Work wk = map_pair_item(p, first, pp, w, rank).wk;   // (before the wait: its loads take a while)
             if (!wait_warp_pair(tfull, iter & 1, p.wait_limit, abort_flag, peer_abort, p.err, 0x280u)) break;
             tc_fence_after();
             const uint32_t tbase = tmem + (iter & 1) * P_ACC2 + ((uint32_t)quarter << 16);
@@ -946,11 +985,13 @@ static int product(const void* a_codes, long long rows, int G, int K, const Para
     return launch<F, Narrow, EPI>(a_codes, rows, K, p, s);
 }
 
-static Params params_for(const int32_t* sched, unsigned* err, int G, int rows, const void* a_sf, const void* packed, const WeightLayout& L,
+static Params params_for(const int32_t* offsets, const int32_t* sched, unsigned* err, int G, int rows, const void* a_sf, const void* packed, const WeightLayout& L,
                          int K) {
     Params p{};
+    p.offsets = offsets;
     p.sched = sched;
     p.G = G;
+    p.rows = rows;
     p.max_tiles = (int)sched_max_tiles(rows, G);
     p.a_sf = static_cast<const uint8_t*>(a_sf);
     p.w = static_cast<const uint8_t*>(packed);
@@ -1041,7 +1082,7 @@ extern "C" int moe_fp4_linear(const void* x, long long ldx, int x_rows, const in
     if (int rc = launch_quantize_operand(x, ldx, x_rows, src, offsets, sched, G, rows, K, dtype, fmt, gscale, w + L.codes,
                                          w + L.sf, quantize_once(src, x_rows, rows, K) ? w + L.once : nullptr, err, s))
         return rc;
-    Params p = params_for(sched, err, G, rows, w + L.sf, packed, weight_layout(G, N, K, fmt), K);
+    Params p = params_for(offsets, sched, err, G, rows, w + L.sf, packed, weight_layout(G, N, K, fmt), K);
     p.N = N;
     p.ldo = (int)ldo;
     p.out = out;
@@ -1077,7 +1118,7 @@ extern "C" int moe_fp4_expert_ffn(const void* x, long long ldx, int x_rows, cons
                                          w + L.x.sf, quantize_once(src, x_rows, rows, h) ? w + L.x.once : nullptr, err, s))
         return rc;
     const ExpertLayout W = expert_layout(E, h, F, fmt);
-    Params p = params_for(sched, err, E, rows, w + L.x.sf, packed, W.gu, h);
+    Params p = params_for(offsets, sched, err, E, rows, w + L.x.sf, packed, W.gu, h);
     p.alpha = alpha_gate;
     p.alpha_up = alpha_up;
     p.act_gscale = act_gscale;
@@ -1088,7 +1129,7 @@ extern "C" int moe_fp4_expert_ffn(const void* x, long long ldx, int x_rows, cons
     if (int rc = fmt == MOE_FP4_NV ? product<Nv, EPI_SWIGLU>(w + L.x.codes, rows, E, h, p, s)
                                    : product<Mx, EPI_SWIGLU>(w + L.x.codes, rows, E, h, p, s))
         return rc;
-    Params d = params_for(sched, err, E, rows, w + L.act_sf, static_cast<const uint8_t*>(packed) + W.down_off, W.down, F);
+    Params d = params_for(offsets, sched, err, E, rows, w + L.act_sf, static_cast<const uint8_t*>(packed) + W.down_off, W.down, F);
     d.N = h;
     d.ldo = (int)ldo;
     d.out = out;
