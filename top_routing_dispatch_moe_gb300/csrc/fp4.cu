@@ -28,14 +28,32 @@ template <typename T> constexpr int IN_FLIGHT = 4 / (int)sizeof(T);
 // 16 elements as they lie in memory.
 template <typename T> struct alignas(16) Raw16 { uint4 q[sizeof(T)]; };
 
+// 32 bytes at an address on 32, for the 64 bytes of an fp32 unit: one request for a whole sector, where requests of 16 bytes
+// 64 apart touch each sector twice (12288 x 4096 fp32 there and back 97 -> 81 us; 16-bit types measured no faster).
+__device__ __forceinline__ void ld32(uint4* d, const void* p) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(d[0].x), "=r"(d[0].y), "=r"(d[0].z), "=r"(d[0].w), "=r"(d[1].x), "=r"(d[1].y), "=r"(d[1].z), "=r"(d[1].w)
+                 : "l"(p));
+}
+__device__ __forceinline__ void st32(void* p, const uint4* d) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"l"(p), "r"(d[0].x), "r"(d[0].y), "r"(d[0].z), "r"(d[0].w), "r"(d[1].x), "r"(d[1].y), "r"(d[1].z), "r"(d[1].w)
+                 : "memory");
+}
+
 // Columns [k0, k0 + 16) of a row as stored, zero past K. VEC: the row starts on 16 bytes. The caller's lanes of one warp
 // hold consecutive units of the same row in the other case too, where the elements are fetched one by one.
 template <typename T, bool VEC>
 __device__ __forceinline__ Raw16<T> load_unit(const T* __restrict__ row, int k0, int K) {
     Raw16<T> r;
     if (VEC && k0 + UNIT <= K) {
+        if (sizeof(T) == 4 && (reinterpret_cast<uintptr_t>(row) & 31u) == 0) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T); ++i) r.q[i] = __ldcs(reinterpret_cast<const uint4*>(row + k0) + i);
+            for (int i = 0; i < (int)sizeof(T); i += 2) ld32(r.q + i, reinterpret_cast<const uint4*>(row + k0) + i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T); ++i) r.q[i] = __ldcs(reinterpret_cast<const uint4*>(row + k0) + i);
+        }
         return r;
     }
 #pragma unroll
@@ -142,6 +160,7 @@ quantize_rows_kernel(const T* __restrict__ x, long long ldx, int x_rows, const i
     pdl_wait();
     pdl_trigger();
     if (offsets && blockIdx.x == gridDim.x - 1) write_schedule(offsets, G, group_rows, sched, err);
+    __shared__ __align__(16) T s_in[VEC ? 1 : QWARPS][VEC ? 1 : SEG + 8 * 31];
     const int lane = threadIdx.x & 31;
     const int units = (K + 31) / 32 * 2;
     const int nseg = (units + lpr - 1) / lpr, rpw = 32 / lpr, sub = lane / lpr;
@@ -165,12 +184,36 @@ quantize_rows_kernel(const T* __restrict__ x, long long ldx, int x_rows, const i
                 from = __ldg(src + row[i]);
                 if (from >= x_rows || from < -1) { latch_device_error(err, kDevErrBadIndex, 0x200u); from = -1; }
             }
-            raw[i] = load_unit<T, VEC>(x + (long long)(live ? max(from, 0) : 0) * ldx, unit[i] * UNIT, live && from >= 0 ? K : 0);
+            if (!VEC && lpr == 32) {             // one row segment a warp, a column a lane: taken apart below
+                from = live ? from : -1;
+                from = __shfl_sync(0xffffffffu, from, 0);
+                const int base = at.seg * SEG;
+                const T* row0 = x + (long long)max(from, 0) * ldx + base;
+                T* e = reinterpret_cast<T*>(raw[i].q);
+#pragma unroll
+                for (int j = 0; j < UNIT; ++j) {
+                    const int c = j * 32 + lane;
+                    e[j] = from >= 0 && base + c < K ? row0[c] : T(0.f);
+                }
+            } else {
+                raw[i] = load_unit<T, VEC>(x + (long long)(live ? max(from, 0) : 0) * ldx, unit[i] * UNIT, live && from >= 0 ? K : 0);
+            }
             at.next();
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             if (i >= n) break;
+            if (!VEC && lpr == 32) {             // (8 elements between the lanes' units, for the banks)
+                T* box = s_in[threadIdx.x >> 5];
+                T* e = reinterpret_cast<T*>(raw[i].q);
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < UNIT; ++j) box[j * 32 + lane + ((j * 32 + lane) >> 4) * 8] = e[j];
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < (int)sizeof(T); ++j)
+                    raw[i].q[j] = *reinterpret_cast<const uint4*>(box + lane * (UNIT + 8) + j * (16 / (int)sizeof(T)));
+            }
             uint32_t byte;
             const uint2 w = quantize_unit<F>(raw[i], gscale != nullptr, g, byte);
             if (row[i] < rows && unit[i] < units) {
@@ -410,8 +453,13 @@ dequantize_rows_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restr
             T* dst = out + (long long)row[i] * ldo + k0;
             if (VEC) {
                 if (live && k0 + UNIT <= K) {
+                    if (sizeof(T) == 4 && (reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
 #pragma unroll
-                    for (int q = 0; q < (int)sizeof(T); ++q) __stcs(reinterpret_cast<uint4*>(dst) + q, o.q[q]);
+                        for (int q = 0; q < (int)sizeof(T); q += 2) st32(reinterpret_cast<uint4*>(dst) + q, o.q + q);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < (int)sizeof(T); ++q) __stcs(reinterpret_cast<uint4*>(dst) + q, o.q[q]);
+                    }
                 } else if (live) {
 #pragma unroll
                     for (int q = 0; q < UNIT; ++q)

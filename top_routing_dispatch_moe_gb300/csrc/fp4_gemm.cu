@@ -892,8 +892,10 @@ static int out_map(CUtensorMap* m, void* base, long long rows, int N, long long 
 template <int EPI>
 static int make_maps(const void* a_codes, long long rows, int K, Params& p, CUtensorMap* m, CUtensorMap* m32, CUtensorMap* mo) {
     const int pitch = pad64(K) / 2;
-    if (int rc = codes_map(m, a_codes, rows, pitch, BM)) return rc;
     if (int rc = codes_map(m32, a_codes, rows, pitch, 32)) return rc;
+    *m = *m32;                                   // (no tile of 128 rows: the map of whole tiles is not used)
+    if (rows > 96)
+        if (int rc = codes_map(m, a_codes, rows, pitch, BM)) return rc;
     *mo = *m;
     if (EPI == EPI_OUT) {
         const int el = p.out_dtype == MOE_F32 ? 4 : 2;
