@@ -125,6 +125,29 @@ def test_quantize_rows_by_index_and_strides(gpu_lib):
     ok(gpu_lib)
 
 
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_offsets_past_32_bits(gpu_lib, fmt):
+    """2.2e9 values: the last rows are those of a call of their own, there and back, and through the product."""
+    moe = gpu_lib
+    rows, K, N = 1 << 20, 2080, 40
+    x = torch.zeros((rows, K), dtype=torch.bfloat16, device="cuda")
+    x[-300:] = data((300, K), "bf16", 3)
+    c, s = moe.moe_fp4_quantize(x, fmt)
+    c1, s1 = moe.moe_fp4_quantize(x[-300:], fmt)
+    assert torch.equal(c[-300:], c1) and torch.equal(s[-300:], s1)
+    y = moe.moe_fp4_dequantize(c, s, K, fmt)
+    assert torch.equal(y[-300:], moe.moe_fp4_dequantize(c1, s1, K, fmt))
+    ok(moe)
+    del y, c, s
+    wc, wsc, _ = weight(moe, 2, N, K, fmt, 5)
+    packed = moe.moe_fp4_pack_weight(wc, wsc, K, fmt)
+    off = torch.tensor([0, rows - 200, rows], dtype=torch.int32, device="cuda")
+    y = moe.moe_fp4_linear(x, off, packed, N, fmt)
+    off = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+    assert torch.equal(y[-300:], moe.moe_fp4_linear(x[-300:].contiguous(), off, packed, N, fmt))
+    ok(moe)
+
+
 # ----------------------------------------------------------------------------------------------- product
 
 
@@ -255,6 +278,21 @@ def test_another_calls_schedule_is_reported(gpu_lib, G):
     assert moe.moe_check_device_error() == moe.MOE_ERR_INVALID_ARG
     assert (out == 5).all()
     ok(moe)
+
+
+def test_a_schedule_past_the_rows_is_cut(gpu_lib):
+    """A tile schedule whose tile ends past the call's rows: the rows there are, and nothing after them."""
+    moe = gpu_lib
+    c, s, w = weight(moe, 1, 32, 64, "mx", 3)
+    packed = moe.moe_fp4_pack_weight(c, s, 64, "mx")
+    x = data((40, 64), "bf16")
+    full = torch.full((60, 32), 5.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_fp4_linear(x, None, packed, 32, "mx", G=1, tile_sched=moe.moe_dense_tile_sched(128), out=full[:40])
+    ok(moe)
+    assert (full[40:] == 5).all()
+    a = Q.dequantize(*Q.quantize(f64(x), "mx"), "mx")
+    want = a @ w[0].T
+    assert (np.abs(f64(full[:40]) - want) <= Q.product_bound(a, w[0], want, 2.0**-8)).all()
 
 
 # --------------------------------------------------------------------------------------------------- FFN

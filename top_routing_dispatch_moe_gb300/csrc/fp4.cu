@@ -247,7 +247,11 @@ quantize_operand_kernel(const T* __restrict__ x, long long ldx, int x_rows, cons
     pdl_trigger();
     const float g = gscale ? __ldg(gscale) : 1.f;
     const int4* tiles = reinterpret_cast<const int4*>(sched + sched_tiles_offset(G));
-    auto tile_of = [&](int t) -> int4 { return offsets ? group_tile(offsets, s_first, G, t) : tiles[t]; };
+    auto tile_of = [&](int t) -> int4 {
+        if (offsets) return group_tile(offsets, s_first, G, t);
+        const int4 e = tiles[t];
+        return make_int4(e.x, min(e.y, rows), min(e.z, rows), 0);
+    };
     int ntiles;
     if (offsets) {
         const bool bad = scan_groups<QTHREADS>(offsets, G, rows, s_first);
@@ -308,7 +312,7 @@ quantize_operand_kernel(const T* __restrict__ x, long long ldx, int x_rows, cons
 template <class F>
 __global__ void __launch_bounds__(QTHREADS)
 gather_operand_kernel(const uint8_t* __restrict__ q_codes, const uint8_t* __restrict__ q_scales, int x_rows,
-                      const int32_t* __restrict__ src, const int32_t* __restrict__ sched, int G, int max_tiles, int K,
+                      const int32_t* __restrict__ src, const int32_t* __restrict__ sched, int G, int rows, int max_tiles, int K,
                       uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, unsigned* err) {
     constexpr int U = 4, PIECES = 2 * SF_PIECES<F>;
     __shared__ int s_from[MOE_TILE_M];
@@ -324,7 +328,7 @@ gather_operand_kernel(const uint8_t* __restrict__ q_codes, const uint8_t* __rest
     for (long long it = blockIdx.x; it < (long long)ntiles * nseg; it += gridDim.x) {
         const int t = (int)(it / nseg), seg = (int)(it - (long long)t * nseg);
         const int4 ent = tiles[t];
-        const int n = ent.z - ent.y;
+        const int n = min(ent.z, rows) - ent.y;
         __syncthreads();
         if (threadIdx.x < MOE_TILE_M) {
             int from = -1;
@@ -601,7 +605,7 @@ int launch_quantize_operand(const void* x, long long ldx, int x_rows, const int3
                                                 (long long)num_sms() * 8);
         auto gather = [&](auto f) {
             return check_launch(launch_pdl(gather_operand_kernel<decltype(f)>, dim3(g2), dim3(QTHREADS), 0, s, qc, qs, x_rows, src,
-                                           sched, G, (int)sched_max_tiles(rows, G), K, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(sf), err),
+                                           sched, G, rows, (int)sched_max_tiles(rows, G), K, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(sf), err),
                                 "gather_operand_kernel");
         };
         return fmt == MOE_FP4_NV ? gather(Nv{}) : gather(Mx{});

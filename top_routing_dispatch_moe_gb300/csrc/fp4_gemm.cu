@@ -86,7 +86,10 @@ __device__ __forceinline__ void find_tiles(const Params& p, int* first) {
     __syncthreads();
 }
 __device__ __forceinline__ int4 tile_entry(const Params& p, const int* first, int g, int t) {
-    if (!p.offsets) return reinterpret_cast<const int4*>(p.sched + sched_tiles_offset(p.G))[t];
+    if (!p.offsets) {
+        const int4 e = reinterpret_cast<const int4*>(p.sched + sched_tiles_offset(p.G))[t];
+        return make_int4(g, min(e.y, p.rows), min(e.z, p.rows), 0);
+    }
     const int row0 = __ldg(p.offsets + g) + (t - first[g]) * BM;
     return make_int4(g, row0, min(row0 + BM, __ldg(p.offsets + g + 1)), 0);
 }
