@@ -32,6 +32,7 @@ constexpr int EPI_WARPS = 8, SF_WARPS = 4;
 constexpr int THREADS = 32 * (2 + EPI_WARPS + SF_WARPS);
 constexpr int TMEM_COLS = 512;
 constexpr int MAX_G = 1024;
+constexpr int BOX_BYTES = 2048;                  // an epilogue warp's staging buffer
 constexpr int SF_BUFS = 3;                       // stages of scales in tensor memory
 
 enum Epi : int { EPI_OUT = 0, EPI_SWIGLU = 1 };
@@ -42,7 +43,7 @@ struct Cfg {
     static constexpr int B_BYTES = BN * SEG_K / 2;
     static constexpr int SF_BLOCKS = (BN + 127) / 128;               // 128-row scale tiles a weight tile touches
     template <class F> static constexpr int SFS = (1 + SF_BLOCKS) * SF_BYTES<F>;   // scale bytes of a stage
-    template <class F> static constexpr int SMEM = 1024 + EPI_WARPS * 4096 + STAGES * (A_BYTES + B_BYTES + SFS<F>) + 256 + (MAX_G + 1) * 4;
+    template <class F> static constexpr int SMEM = 1024 + EPI_WARPS * BOX_BYTES + STAGES * (A_BYTES + B_BYTES + SFS<F>) + 256 + (MAX_G + 1) * 4;
     static constexpr int SF_COL = 2 * BN;                            // scale columns follow the two accumulators
     static constexpr int B_COLS = BN / 32;                           // scale columns of the weight rows in a piece
     template <class F> static constexpr int SF_COLS = SF_PIECES<F> * (4 + B_COLS);   // of a stage
@@ -213,9 +214,9 @@ __device__ __forceinline__ void store_row(T* dst, const float* v, float al, int 
         }
     }
 }
-// A box of 32 rows x 128 bytes of the output through the warp's staging buffer `stg` (1024-byte aligned, the layout of
-// 128-byte swizzling) and one TMA store: whole lines reach L2, where a thread's own 16-byte stores touch a sector of each
-// of 32 rows. v: the 128 bytes' values of this lane's row.
+// A box of 32 rows x 64 bytes of the output through the warp's staging buffer `stg` (the layout of 64-byte swizzling: 16-byte
+// chunk c of row r at chunk c ^ (r / 2 % 4)) and one TMA store: whole sectors reach L2, where a thread's own 16-byte stores
+// touch half a sector of each of 32 rows. v: the 64 bytes' values of this lane's row.
 template <typename T>
 __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t stg, const float* v, float al, int col, int row0) {
     constexpr int PER = 16 / sizeof(T);
@@ -223,12 +224,12 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t stg, 
     if (lane == 0) bulk_wait_read_all();             // the previous box has left the buffer
     __syncwarp();
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < 4; ++c) {
         alignas(16) T o[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) o[i] = out_round<T>(v[c * PER + i] * al);
         const uint4 w = *reinterpret_cast<const uint4*>(o);
-        st_shared_v4u(stg + lane * 128u + ((uint32_t)(c ^ (lane & 7)) << 4), w.x, w.y, w.z, w.w);
+        st_shared_v4u(stg + lane * 64u + ((uint32_t)(c ^ (lane >> 1 & 3)) << 4), w.x, w.y, w.z, w.w);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
@@ -236,6 +237,13 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t stg, 
         tma_store_2d(map, stg, col, row0);
         bulk_commit();
     }
+}
+template <typename T>
+__device__ __forceinline__ void store_boxes(const CUtensorMap* map, uint32_t stg, const float* v, float al, int col, int n, int row0) {
+    constexpr int COLS = 64 / sizeof(T);
+#pragma unroll
+    for (int c = 0; c < 64; c += COLS)
+        if (c < n) store_box<T>(map, stg, v + c, al, col + c, row0);
 }
 
 // Chunk of 64 accumulator columns at column c0 of the tile's output, this thread's row r of the tile (live: one of its
@@ -294,11 +302,9 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const CUtensorMa
         if (n <= 0) return;
         if (p.boxed && wk.row0 + (r & ~31) + 31 < wk.row1) {     // all of the warp's rows (the map drops columns past N)
             const int base = wk.row0 + (r & ~31);
-            if (p.out_dtype == MOE_F32) {
-                store_box<float>(map, stg, v, al, c0, base);
-                if (n > 32) store_box<float>(map, stg, v + 32, al, c0 + 32, base);
-            } else if (p.out_dtype == MOE_BF16) store_box<__nv_bfloat16>(map, stg, v, al, c0, base);
-            else store_box<__half>(map, stg, v, al, c0, base);
+            if (p.out_dtype == MOE_F32) store_boxes<float>(map, stg, v, al, c0, n, base);
+            else if (p.out_dtype == MOE_BF16) store_boxes<__nv_bfloat16>(map, stg, v, al, c0, n, base);
+            else store_boxes<__half>(map, stg, v, al, c0, n, base);
             return;
         }
         if (!live) return;
@@ -323,8 +329,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sA = smem_u32(smem), sB = sA + STAGES * A_BYTES, sO = sB + STAGES * B_BYTES,
-                   sS = sO + EPI_WARPS * 4096;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * (A_BYTES + B_BYTES + SFS) + EPI_WARPS * 4096);
+                   sS = sO + EPI_WARPS * BOX_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * (A_BYTES + B_BYTES + SFS) + EPI_WARPS * BOX_BYTES);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
@@ -509,7 +515,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 const int nb = min(BN / 64, p.NB64 - wk.n * (BN / 64));
 #pragma unroll 1
                 for (int q = (half + iter) & 1; q < nb; q += 2)
-                    epilogue_chunk<F, EPI>(p, &tmO, sO + (warp - 2) * 4096, wk, tbase + 64 * q, wk.n * BN + 64 * q, r,
+                    epilogue_chunk<F, EPI>(p, &tmO, sO + (warp - 2) * BOX_BYTES, wk, tbase + 64 * q, wk.n * BN + 64 * q, r,
                                            wk.row0 + r < wk.row1, [] {});
             }
             tc_fence_before();
@@ -529,9 +535,11 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 // ---------------------------------------------------------------------------------------------------
 // two SMs to a tile: a cluster of two CTAs computes 256 rows x 256 columns with tcgen05.mma.cta_group::2
 // ---------------------------------------------------------------------------------------------------
-// The one-SM kernel is bound by the bytes that reach an SM: 47 KB a stage of four MMAs (N = 192), about 55 bytes a cycle of
-// 1.9 GHz, twice the MMAs' own time. In a pair each SM holds its own 128 rows of A and half of the weight rows (and the
-// scales of all of them, which its tensor core needs): 38 KB for MMAs a third larger.
+// The one-SM kernel waits for its operands: a stage of four MMAs (N = 192) takes 385 cycles and needs 47 KB, and with 150 to
+// 190 KB under way some 55 bytes a cycle arrive. In a pair each SM holds its own 128 rows of A and half of the weight rows
+// (and the scales of all of them, which its tensor core needs): 38 KB for MMAs a third larger, and five stages of them.
+// 16384 skewed rows by 8 x 14336 x 4096 (NV): 456 us by single SMs, 349 by pairs with the quantisation of 41 in both; 300 of
+// the pairs' time at 6.2 PFLOP/s, the tensor pipe 62 % busy. The MMAs alone, without loads and epilogue, took 233.
 // The even CTA issues the MMAs for both. Every copy of a CTA completes on its own barrier; the odd CTA's scale warps, which
 // wait for it, pass the news on with their arrival on the even CTA's scale barrier, so that barrier tells of both CTAs'
 // operands. A pair takes two consecutive tiles of one group; where the second does not exist the odd CTA computes the
@@ -542,13 +550,17 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 // reads the shared columns into registers first and frees them at once, so the next tile's MMAs wait for a read of two of
 // its four chunks and not for their conversion and stores.
 constexpr int PB_BYTES = 128 * SEG_K / 2;        // a CTA's half of the weight rows
-constexpr int P_STAGES = 4, P_BN = 256, P_SF_BUFS = 3, P_ACC2 = 128, P_SF_COL = P_ACC2 + P_BN, P_SFA_COL = P_SF_COL + 96;
+constexpr int P_BN = 256, P_SF_BUFS = 3, P_ACC2 = 128, P_SF_COL = P_ACC2 + P_BN, P_SFA_COL = P_SF_COL + 96;
 template <class F> constexpr int P_SFS = 3 * SF_BYTES<F>;
-template <class F> constexpr int P_SMEM = 1024 + EPI_WARPS * 4096 + P_STAGES * (A_BYTES + PB_BYTES + P_SFS<F>) + 256 +
-                                          2 * (MAX_G + 1) * 4;
+// The loads' latency needs the bytes under way: five stages instead of four, for staging buffers of 2 KB instead of 4, took
+// the product above from 381 to 350 us and the FFN of 8192 tokens through 8 experts of 14336 from 1007 to 915.
+template <int EPI> constexpr int P_STAGES = 5;
+template <int EPI> constexpr int P_BOX = EPI == EPI_OUT ? BOX_BYTES : 0;
+template <class F, int EPI>
+constexpr int P_SMEM = 1024 + EPI_WARPS * P_BOX<EPI> + P_STAGES<EPI> * (A_BYTES + PB_BYTES + P_SFS<F>) + 256 + 2 * (MAX_G + 1) * 4;
 template <class F> constexpr int P_COLS = SF_PIECES<F> * 8;      // scale columns of the weight rows in a stage
 static_assert(P_SF_BUFS * P_COLS<Nv> <= 96 && P_SFA_COL + 2 * SF_PIECES<Nv> * 4 <= TMEM_COLS, "tensor memory columns");
-static_assert(P_SMEM<Nv> <= 227 * 1024, "shared memory per CTA");
+static_assert(P_SMEM<Nv, EPI_OUT> + 64 <= 227 * 1024, "shared memory per CTA");
 
 template <class F>
 __device__ __forceinline__ void mma_scaled_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
@@ -620,11 +632,11 @@ template <class F, int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
                      const __grid_constant__ CUtensorMap tmO, Params p) {
-    constexpr int STAGES = P_STAGES, SFS = P_SFS<F>, PIECES = SF_PIECES<F>, COLS = P_COLS<F>;
+    constexpr int STAGES = P_STAGES<EPI>, SFS = P_SFS<F>, PIECES = SF_PIECES<F>, COLS = P_COLS<F>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const uint32_t sA = smem_u32(smem), sB = sA + STAGES * A_BYTES, sO = sB + STAGES * PB_BYTES, sS = sO + EPI_WARPS * 4096;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * (A_BYTES + PB_BYTES + SFS) + EPI_WARPS * 4096);
+    const uint32_t sA = smem_u32(smem), sB = sA + STAGES * A_BYTES, sO = sB + STAGES * PB_BYTES, sS = sO + EPI_WARPS * P_BOX<EPI>;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * (A_BYTES + PB_BYTES + SFS) + EPI_WARPS * P_BOX<EPI>);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
@@ -823,11 +835,11 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             const int first = (iter & 1 ? 0 : 2) + half, second = first ^ 2;
             const bool rows = wk.row0 + quarter < wk.row1, live = wk.row0 + r < wk.row1;
             if (rows && first < nb)
-                epilogue_chunk<F, EPI>(p, &tmO, sO + (warp - 2) * 4096, wk, tbase + 64 * first, wk.n * P_BN + 64 * first, r, live,
+                epilogue_chunk<F, EPI>(p, &tmO, sO + (warp - 2) * P_BOX<EPI>, wk, tbase + 64 * first, wk.n * P_BN + 64 * first, r, live,
                                        hand_back);
             else hand_back();
             if (rows && second < nb)
-                epilogue_chunk<F, EPI>(p, &tmO, sO + (warp - 2) * 4096, wk, tbase + 64 * second, wk.n * P_BN + 64 * second, r, live,
+                epilogue_chunk<F, EPI>(p, &tmO, sO + (warp - 2) * P_BOX<EPI>, wk, tbase + 64 * second, wk.n * P_BN + 64 * second, r, live,
                                        [] {});
         }
         if (lane == 0) bulk_wait_read_all();         // every box read out of shared memory before the CTA exits
@@ -874,18 +886,18 @@ static int codes_map(CUtensorMap* m, const void* base, long long rows, int pitch
     return MOE_OK;
 }
 
-// Output [rows][N] of any supported type, boxes of 32 rows x 128 bytes.
+// Output [rows][N] of any supported type, boxes of 32 rows x 64 bytes.
 static int out_map(CUtensorMap* m, void* base, long long rows, int N, long long ldo, int dtype) {
     auto fn = encode_fn();
     MOE_REQUIRE(fn, MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable from the driver");
     const int el = dtype == MOE_F32 ? 4 : 2;
     cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)ldo * el};
-    cuuint32_t box[2] = {(cuuint32_t)(128 / el), 32};
+    cuuint32_t box[2] = {(cuuint32_t)(64 / el), 32};
     cuuint32_t estr[2] = {1, 1};
     const CUresult r = fn(m, dtype == MOE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                          2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     MOE_REQUIRE(r == CUDA_SUCCESS, MOE_ERR_CUDA, "cuTensorMapEncodeTiled (output) failed (%d) rows=%lld N=%d", (int)r, rows, N);
     return MOE_OK;
@@ -933,7 +945,7 @@ static int launch(const void* a_codes, long long rows, int K, Params p, cudaStre
 
 template <class F, int EPI>
 static int launch_pair(const void* a_codes, long long rows, int K, Params p, cudaStream_t s) {
-    constexpr int smem = P_SMEM<F>;
+    constexpr int smem = P_SMEM<F, EPI>;
     static int clusters[64];                     // resident pairs, in the context they were asked for
     static unsigned long long attr_ctx[64];
     int dev = 0;
@@ -963,13 +975,13 @@ static int launch_pair(const void* a_codes, long long rows, int K, Params p, cud
 
 using Wide = Cfg<192, 4>;
 using Mid = Cfg<128, 5>;
-using Narrow = Cfg<64, 6>;
+using Narrow = Cfg<64, 7>;
 
 // The tile by the time that its waves take on the SMs there are: a stage takes the MMA warp 490, 500 or 530 cycles (64, 128,
 // 192 columns; a pair 560), and its bytes about one cycle for each 55, a tile's start and end 2000. The host does not know
 // the groups' sizes: a group is taken to end in the middle of a tile. With few rows a call is bound by the weights' bytes,
 // and a narrow tile moves too few of them a stage: one token through 8 of 32 experts of 7168 x 2048, gate and up, 36 us with
-// 64 columns and 26 with 128; 8192 rows by 8 x 4096 x 12288 (MX), 225 us with 192 columns and 199 by pairs.
+// 64 columns and 26 with 128; 8192 rows by 8 x 4096 x 12288 (MX), 225 us with 192 columns and 185 by pairs.
 template <class F, int EPI>
 static int product(const void* a_codes, long long rows, int G, int K, const Params& p, cudaStream_t s) {
     MOE_REQUIRE((long long)sched_max_tiles(rows, G) * p.NB64 < (1LL << 31), MOE_ERR_INVALID_ARG,
