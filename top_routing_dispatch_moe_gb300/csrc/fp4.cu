@@ -23,6 +23,9 @@ template <> __device__ __forceinline__ float rounded<float>(float v) { return v;
 template <> __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
 
+// (The kernels that run as programmatic dependents read what the kernel before them may have written by plain loads through
+// pointers without __restrict__, which the compiler does not move ahead of the wait.)
+
 // Units whose loads a lane keeps in flight: with four blocks of 256 threads an SM has 64 KB under way.
 template <typename T> constexpr int IN_FLIGHT = 4 / (int)sizeof(T);
 // 16 elements as they lie in memory.
@@ -44,7 +47,7 @@ __device__ __forceinline__ void st32(void* p, const uint4* d) {
 // Columns [k0, k0 + 16) of a row as stored, zero past K. VEC: the row starts on 16 bytes. The caller's lanes of one warp
 // hold consecutive units of the same row in the other case too, where the elements are fetched one by one.
 template <typename T, bool VEC>
-__device__ __forceinline__ Raw16<T> load_unit(const T* __restrict__ row, int k0, int K) {
+__device__ __forceinline__ Raw16<T> load_unit(const T* row, int k0, int K) {
     Raw16<T> r;
     if (VEC && k0 + UNIT <= K) {
         if (sizeof(T) == 4 && (reinterpret_cast<uintptr_t>(row) & 31u) == 0) {
@@ -132,7 +135,7 @@ struct Walk {
 };
 
 // The schedule of the groups, by one block; first: scan_groups' result, `bad` its answer.
-__device__ __forceinline__ void put_schedule(const int32_t* __restrict__ offsets, const int* first, bool bad, int G, int32_t* sched,
+__device__ __forceinline__ void put_schedule(const int32_t* offsets, const int* first, bool bad, int G, int32_t* sched,
                                              unsigned* err) {
     if (threadIdx.x == 0) {
         sched[0] = first[G];
@@ -153,9 +156,9 @@ __device__ __noinline__ void write_schedule(const int32_t* offsets, int G, int r
 // warp (lpr: a power of two, the units of a row where there are fewer than 32).
 template <class F, typename T, bool VEC>
 __global__ void __launch_bounds__(QTHREADS, 4)
-quantize_rows_kernel(const T* __restrict__ x, long long ldx, int x_rows, const int32_t* __restrict__ src, int rows, int K,
+quantize_rows_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, int rows, int K,
                      int lpr, const float* __restrict__ gscale, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                     const int32_t* __restrict__ offsets, int32_t* sched, int G, int group_rows, unsigned* err) {
+                     const int32_t* offsets, int32_t* sched, int G, int group_rows, unsigned* err) {
     constexpr int U = IN_FLIGHT<T>;
     pdl_wait();
     pdl_trigger();
@@ -181,7 +184,7 @@ quantize_rows_kernel(const T* __restrict__ x, long long ldx, int x_rows, const i
             const bool live = row[i] < rows && unit[i] < units;
             int from = row[i];
             if (live && src) {
-                from = __ldg(src + row[i]);
+                from = src[row[i]];
                 if (from >= x_rows || from < -1) { latch_device_error(err, kDevErrBadIndex, 0x200u); from = -1; }
             }
             if (!VEC && lpr == 32) {             // one row segment a warp, a column a lane: taken apart below
@@ -228,13 +231,13 @@ quantize_rows_kernel(const T* __restrict__ x, long long ldx, int x_rows, const i
 // Operand form: the rows of the tiles, codes [rows][pad64(K) / 2], scales in the tile layout. The tiles are those of `sched`,
 // or with `offsets` those of the groups, found by every block for itself (a launch fewer than a kernel of its own); block 0
 // then writes the schedule for the products. A block takes one item at a time, 512 columns of a tile's rows or, where there
-// are few tiles, of a quarter of them (parts = 2; 4 granules of the scale pieces: the rows r with r % 32 in its range): its
-// warps take the rows in turn, the scale bytes meet in shared memory (pieces 528 bytes apart, so that the pieces of one row fall into different
-// banks) and leave as whole pieces.
+// are few full tiles, of a quarter of them (parts = 2: the rows r with r % 32 in its range of 8, whole 16-byte granules of
+// the scale pieces): its warps take the rows in turn, the scale bytes meet in shared memory (pieces 528 bytes apart, so that
+// the pieces of one row fall into different banks) and leave as whole granules.
 template <class F, typename T, bool VEC>
 __global__ void __launch_bounds__(QTHREADS, 4)
-quantize_operand_kernel(const T* __restrict__ x, long long ldx, int x_rows, const int32_t* __restrict__ src,
-                        const int32_t* __restrict__ offsets, int32_t* sched, int G, int rows, int max_tiles, int parts, int K,
+quantize_operand_kernel(const T* x, long long ldx, int x_rows, const int32_t* src,
+                        const int32_t* offsets, int32_t* sched, int G, int rows, int max_tiles, int parts, int K,
                         const float* __restrict__ gscale, uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, unsigned* err) {
     constexpr int U = IN_FLIGHT<T>, PIECES = 2 * SF_PIECES<F>, STRIDE = 528;
     __shared__ __align__(16) uint8_t s_sf[PIECES * STRIDE];
@@ -279,7 +282,7 @@ quantize_operand_kernel(const T* __restrict__ x, long long ldx, int x_rows, cons
                 r[i] = j < 4 * per ? (j >> shift) * 32 + part * per + (j & (per - 1)) : n;
                 int from = r[i] < n ? ent.y + r[i] : -1;
                 if (from >= 0 && src) {
-                    from = __ldg(src + from);
+                    from = src[from];
                     if (from >= x_rows || from < -1) { latch_device_error(err, kDevErrBadIndex, 0x201u); from = -1; }
                 }
                 raw[i] = load_unit<T, VEC>(x + (long long)max(from, 0) * ldx, unit * UNIT, from >= 0 ? K : 0);
@@ -307,12 +310,12 @@ quantize_operand_kernel(const T* __restrict__ x, long long ldx, int x_rows, cons
 }
 
 // Operand form from rows that are quantised already (row-major, codes [x_rows][q_pitch], scales [x_rows][nb]): a token's rows
-// in several groups are quantised once and copied. Tiles, parts and items as in quantize_operand_kernel; a lane copies 16
-// bytes of codes at a time (four of a warp's rows at once) and moves the scales of a row and piece as words.
+// in several groups are quantised once and copied. An item is 512 columns of a tile's rows; 16 lanes copy a row's 256 bytes
+// of codes, and a thread gathers a granule of scales, four rows' words.
 template <class F>
 __global__ void __launch_bounds__(QTHREADS)
-gather_operand_kernel(const uint8_t* __restrict__ q_codes, const uint8_t* __restrict__ q_scales, int x_rows,
-                      const int32_t* __restrict__ src, const int32_t* __restrict__ sched, int G, int rows, int max_tiles, int K,
+gather_operand_kernel(const uint8_t* q_codes, const uint8_t* q_scales, int x_rows,
+                      const int32_t* src, const int32_t* sched, int G, int rows, int max_tiles, int K,
                       uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, unsigned* err) {
     constexpr int U = 4, PIECES = 2 * SF_PIECES<F>;
     __shared__ int s_from[MOE_TILE_M];
@@ -333,7 +336,7 @@ gather_operand_kernel(const uint8_t* __restrict__ q_codes, const uint8_t* __rest
         if (threadIdx.x < MOE_TILE_M) {
             int from = -1;
             if ((int)threadIdx.x < n) {
-                from = __ldg(src + ent.y + threadIdx.x);
+                from = src[ent.y + threadIdx.x];
                 if (from >= x_rows || from < -1) { latch_device_error(err, kDevErrBadIndex, 0x201u); from = -1; }
             }
             s_from[threadIdx.x] = from;
@@ -343,15 +346,16 @@ gather_operand_kernel(const uint8_t* __restrict__ q_codes, const uint8_t* __rest
         const int c = seg * 256 + (lane & 15) * 16;
         for (int r0 = warp * 2 + (lane >> 4); r0 < n; r0 += U * 2 * QWARPS) {
             uint4 v[U];
+            int from[U];
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int r = r0 + i * 2 * QWARPS, from = r < n ? s_from[r] : -1;
-                v[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (from >= 0 && c < q_pitch) v[i] = __ldg(reinterpret_cast<const uint4*>(q_codes + (size_t)from * q_pitch + c));
+            for (int i = 0; i < U; ++i) {            // (loads without a branch: they stay in flight together)
+                from[i] = s_from[min(r0 + i * 2 * QWARPS, MOE_TILE_M - 1)];
+                v[i] = *reinterpret_cast<const uint4*>(q_codes + (size_t)max(from[i], 0) * q_pitch + min(c, q_pitch - 16));
             }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int r = r0 + i * 2 * QWARPS;
+                if (from[i] < 0 || c >= q_pitch) v[i] = make_uint4(0u, 0u, 0u, 0u);
                 if (r < n && c < pitch) *reinterpret_cast<uint4*>(codes + (size_t)(ent.y + r) * pitch + c) = v[i];
             }
         }
@@ -368,11 +372,11 @@ gather_operand_kernel(const uint8_t* __restrict__ q_codes, const uint8_t* __rest
                 if (from >= 0) {
                     const uint8_t* row = q_scales + (size_t)from * nb + b0;
                     if ((nb & 3) == 0) {
-                        if (b0 < nb) w[j] = __ldg(reinterpret_cast<const uint32_t*>(row));
+                        if (b0 < nb) w[j] = *reinterpret_cast<const uint32_t*>(row);
                     } else {
 #pragma unroll
                         for (int b = 0; b < 4; ++b)
-                            if (b0 + b < nb) w[j] |= (uint32_t)__ldg(row + b) << (8 * b);
+                            if (b0 + b < nb) w[j] |= (uint32_t)row[b] << (8 * b);
                     }
                 }
             }

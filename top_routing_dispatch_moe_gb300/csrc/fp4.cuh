@@ -188,7 +188,7 @@ __device__ __forceinline__ float scale_value(uint32_t b) {
 // Tile counts of the groups [offsets[g], offsets[g + 1]) summed up into first[0 .. G] (G <= 1024) by a block of NT threads;
 // 0 everywhere, and true, if an offset falls or leaves [0, rows].
 template <int NT>
-__device__ __forceinline__ bool scan_groups(const int32_t* __restrict__ offsets, int G, int rows, int* first) {
+__device__ __forceinline__ bool scan_groups(const int32_t* offsets, int G, int rows, int* first) {
     constexpr int PER = (1024 + NT - 1) / NT;
     __shared__ int s_warp[NT / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g0 = threadIdx.x * PER;
@@ -198,7 +198,7 @@ __device__ __forceinline__ bool scan_groups(const int32_t* __restrict__ offsets,
     for (int i = 0; i < PER; ++i) {
         n[i] = 0;
         if (g0 + i < G) {
-            const int lo = __ldg(offsets + g0 + i), hi = __ldg(offsets + g0 + i + 1);
+            const int lo = offsets[g0 + i], hi = offsets[g0 + i + 1];
             if (lo < 0 || hi < lo || hi > rows) bad = true;
             else n[i] = (int)(((long long)hi - lo + MOE_TILE_M - 1) / MOE_TILE_M);
         }
@@ -226,14 +226,14 @@ __device__ __forceinline__ bool scan_groups(const int32_t* __restrict__ offsets,
 }
 
 // Tile t of the groups: {group, first row, end, 0}.
-__device__ __forceinline__ int4 group_tile(const int32_t* __restrict__ offsets, const int* first, int G, int t) {
+__device__ __forceinline__ int4 group_tile(const int32_t* offsets, const int* first, int G, int t) {
     int lo = 0, hi = G;
     while (lo < hi) {                    // last group with first[g] <= t
         const int mid = (lo + hi + 1) >> 1;
         if (first[mid] <= t) lo = mid; else hi = mid - 1;
     }
-    const int row0 = __ldg(offsets + lo) + (t - first[lo]) * MOE_TILE_M;
-    return make_int4(lo, row0, min(row0 + MOE_TILE_M, __ldg(offsets + lo + 1)), 0);
+    const int row0 = offsets[lo] + (t - first[lo]) * MOE_TILE_M;
+    return make_int4(lo, row0, min(row0 + MOE_TILE_M, offsets[lo + 1]), 0);
 }
 #endif
 
