@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(QTHREADS)
 gather_operand_kernel(const uint8_t* q_codes, const uint8_t* q_scales, int x_rows,
                       const int32_t* src, const int32_t* sched, int G, int rows, int max_tiles, int K,
                       uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, unsigned* err) {
-    constexpr int U = 4, PIECES = 2 * SF_PIECES<F>;
+    constexpr int U = 8, PIECES = 2 * SF_PIECES<F>;
     __shared__ int s_from[MOE_TILE_M];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int kst = (K + SEG_K - 1) / SEG_K, nseg = (kst + 1) / 2, nb = (K + F::BLK - 1) / F::BLK;

@@ -192,20 +192,20 @@ __device__ constexpr uint32_t idesc_scaled(int sub) {
            ((uint32_t)(M >> 4) << 24) | ((uint32_t)(2 * sub) << 4) | ((uint32_t)(2 * sub) << 29);
 }
 
-// 32 consecutive columns of an output row in its type; whole 16-byte vectors where the row allows them.
+// 32 consecutive columns of an output row that starts on 16 bytes, in its type.
 template <typename T> __device__ __forceinline__ T out_round(float v);
 template <> __device__ __forceinline__ float out_round<float>(float v) { return v; }
 template <> __device__ __forceinline__ __half out_round<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 out_round<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <typename T>
-__device__ __forceinline__ void store_row(T* dst, const float* v, float al, int n, bool vec) {
+__device__ __forceinline__ void store_row(T* dst, const float* v, float al, int n) {
     constexpr int PER = 16 / sizeof(T);
 #pragma unroll
     for (int c = 0; c < 32; c += PER) {
         alignas(16) T o[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) o[i] = out_round<T>(v[c + i] * al);
-        if (vec && c + PER <= n) {
+        if (c + PER <= n) {
             *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(o);
         } else {
 #pragma unroll
@@ -244,6 +244,45 @@ __device__ __forceinline__ void store_boxes(const CUtensorMap* map, uint32_t stg
 #pragma unroll
     for (int c = 0; c < 64; c += COLS)
         if (c < n) store_box<T>(map, stg, v + c, al, col + c, row0);
+}
+
+// Rows that start on no boundary: 64 bytes of each of the warp's 32 rows at a time through the staging buffer, from where the
+// lanes write neighbouring columns (1003 x 1001 fp32 rows stored by a lane each touched 32 sectors a store).
+template <typename T>
+__device__ __forceinline__ void store_loose(T* out, long long ldo, uint32_t stg, const float* v, float al, int col, int n, int row0,
+                                            int rows) {
+    constexpr int PER = 16 / sizeof(T), COLS = 64 / sizeof(T);
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int g = 0; g < 64; g += COLS) {
+        if (g >= n) break;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            alignas(16) T o[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) o[i] = out_round<T>(v[g + c * PER + i] * al);
+            const uint4 w = *reinterpret_cast<const uint4*>(o);
+            st_shared_v4u(stg + lane * 64u + ((uint32_t)(c ^ (lane >> 1 & 3)) << 4), w.x, w.y, w.z, w.w);
+        }
+        __syncwarp();
+        const int c = lane % COLS;
+#pragma unroll 4
+        for (int r = lane / COLS; r < rows; r += 32 / COLS) {
+            const uint32_t a = stg + r * 64u + ((uint32_t)((c / PER) ^ (r >> 1 & 3)) << 4) + (uint32_t)(c % PER) * sizeof(T);
+            if (g + c < n) {
+                if constexpr (sizeof(T) == 4) {
+                    float x;
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
+                    out[(row0 + r) * ldo + col + g + c] = x;
+                } else {
+                    uint16_t x;
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a) : "memory");
+                    reinterpret_cast<uint16_t*>(out)[(row0 + r) * ldo + col + g + c] = x;
+                }
+            }
+        }
+        __syncwarp();
+    }
 }
 
 // Chunk of 64 accumulator columns at column c0 of the tile's output, this thread's row r of the tile (live: one of its
@@ -307,16 +346,23 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const CUtensorMa
             else store_boxes<__half>(map, stg, v, al, c0, n, base);
             return;
         }
+        if (!p.vec) {
+            const int base = wk.row0 + (r & ~31), rows = min(32, wk.row1 - base);
+            if (p.out_dtype == MOE_F32) store_loose(static_cast<float*>(p.out), p.ldo, stg, v, al, c0, n, base, rows);
+            else if (p.out_dtype == MOE_BF16) store_loose(static_cast<__nv_bfloat16*>(p.out), p.ldo, stg, v, al, c0, n, base, rows);
+            else store_loose(static_cast<__half*>(p.out), p.ldo, stg, v, al, c0, n, base, rows);
+            return;
+        }
         if (!live) return;
         const int el = p.out_dtype == MOE_F32 ? 4 : 2;
         uint8_t* dst = static_cast<uint8_t*>(p.out) + ((size_t)row * p.ldo + c0) * el;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (n - 32 * h <= 0) break;
-            if (p.out_dtype == MOE_F32) store_row(reinterpret_cast<float*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h, p.vec);
+            if (p.out_dtype == MOE_F32) store_row(reinterpret_cast<float*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
             else if (p.out_dtype == MOE_BF16)
-                store_row(reinterpret_cast<__nv_bfloat16*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h, p.vec);
-            else store_row(reinterpret_cast<__half*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h, p.vec);
+                store_row(reinterpret_cast<__nv_bfloat16*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
+            else store_row(reinterpret_cast<__half*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
         }
     }
 }
