@@ -163,7 +163,7 @@ quantize_rows_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, 
     pdl_wait();
     pdl_trigger();
     if (offsets && blockIdx.x == gridDim.x - 1) write_schedule(offsets, G, group_rows, sched, err);
-    __shared__ __align__(16) T s_in[VEC ? 1 : QWARPS][VEC ? 1 : SEG + 8 * 31];
+    __shared__ __align__(16) T s_in[VEC ? 1 : QWARPS][VEC ? 1 : SEG + 8 * 32];
     const int lane = threadIdx.x & 31;
     const int units = (K + 31) / 32 * 2;
     const int nseg = (units + lpr - 1) / lpr, rpw = 32 / lpr, sub = lane / lpr;
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(QTHREADS, 4)
 dequantize_rows_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int rows, int K, int lpr,
                        const float* __restrict__ gscale, T* __restrict__ out, long long ldo) {
     constexpr int U = 2;
-    __shared__ T s_out[VEC ? 1 : QWARPS][VEC ? 1 : SEG];
+    __shared__ __align__(16) T s_out[VEC ? 1 : QWARPS][VEC ? 1 : SEG + 8 * 32];
     const int lane = threadIdx.x & 31;
     const int units = (K + 31) / 32 * 2;
     const int nseg = (units + lpr - 1) / lpr, rpw = 32 / lpr, sub = lane / lpr, col = lane - sub * lpr;
@@ -477,12 +477,18 @@ dequantize_rows_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restr
                 T* box = s_out[threadIdx.x >> 5];
                 __syncwarp();
 #pragma unroll
-                for (int q = 0; q < UNIT; ++q) box[lane * UNIT + q] = e[q];
+                for (int q = 0; q < (int)sizeof(T); ++q)     // (8 elements between the lanes' units, for the banks)
+                    *reinterpret_cast<uint4*>(box + lane * (UNIT + 8) + q * (16 / (int)sizeof(T))) = o.q[q];
                 __syncwarp();
                 const int base = (unit[i] - lane) * UNIT;
                 T* drow = out + (long long)row[i] * ldo + base;
-                if (row[i] < rows)
-                    for (int q = lane; q < SEG && base + q < K; q += 32) drow[q] = box[q];
+                if (row[i] < rows) {
+#pragma unroll
+                    for (int j = 0; j < UNIT; ++j) {
+                        const int q = j * 32 + lane;
+                        if (base + q < K) drow[q] = box[q + (q >> 4) * 8];
+                    }
+                }
             } else if (live) {
 #pragma unroll
                 for (int q = 0; q < UNIT; ++q)
@@ -587,7 +593,7 @@ static int lanes_per_row(int K) {
 }
 static int row_grid(int rows, int K, int lpr) {
     const long long items = (long long)cdiv(rows, 32 / lpr) * cdiv((K + 31) / 32 * 2, lpr);
-    return (int)std::max<long long>(1, std::min<long long>(cdiv(items, QWARPS), (long long)num_sms() * 8));
+    return (int)std::max<long long>(1, std::min<long long>(cdiv(items, QWARPS), (long long)num_sms() * 4));
 }
 
 int launch_quantize_operand(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* offsets, int32_t* sched,
