@@ -157,7 +157,7 @@ __device__ __noinline__ void write_schedule(const int32_t* offsets, int G, int r
 template <class F, typename T, bool VEC>
 __global__ void __launch_bounds__(QTHREADS, 4)
 quantize_rows_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, int rows, int K,
-                     int lpr, const float* __restrict__ gscale, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                     int lpr, const float* gscale, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                      const int32_t* offsets, int32_t* sched, int G, int group_rows, unsigned* err) {
     constexpr int U = IN_FLIGHT<T>;
     pdl_wait();
@@ -169,7 +169,7 @@ quantize_rows_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, 
     const int nseg = (units + lpr - 1) / lpr, rpw = 32 / lpr, sub = lane / lpr;
     const int nb = (K + F::BLK - 1) / F::BLK;
     const size_t pitch = (size_t)units * 8;
-    const float g = gscale ? __ldg(gscale) : 1.f;
+    const float g = gscale ? *gscale : 1.f;
     const int col = lane - sub * lpr;
     Walk at((long long)blockIdx.x * QWARPS + (threadIdx.x >> 5), (long long)gridDim.x * QWARPS,
             (long long)((rows + rpw - 1) / rpw) * nseg, nseg);
@@ -238,7 +238,7 @@ template <class F, typename T, bool VEC>
 __global__ void __launch_bounds__(QTHREADS, 4)
 quantize_operand_kernel(const T* x, long long ldx, int x_rows, const int32_t* src,
                         const int32_t* offsets, int32_t* sched, int G, int rows, int max_tiles, int parts, int K,
-                        const float* __restrict__ gscale, uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, unsigned* err) {
+                        const float* gscale, uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, unsigned* err) {
     constexpr int U = IN_FLIGHT<T>, PIECES = 2 * SF_PIECES<F>, STRIDE = 528;
     __shared__ __align__(16) uint8_t s_sf[PIECES * STRIDE];
     __shared__ int s_first[1025];
@@ -248,7 +248,7 @@ quantize_operand_kernel(const T* x, long long ldx, int x_rows, const int32_t* sr
     const size_t pitch = (size_t)units * 8;
     pdl_wait();                          // (a programmatic dependent of the kernel that wrote x or the schedule)
     pdl_trigger();
-    const float g = gscale ? __ldg(gscale) : 1.f;
+    const float g = gscale ? *gscale : 1.f;
     const int4* tiles = reinterpret_cast<const int4*>(sched + sched_tiles_offset(G));
     auto tile_of = [&](int t) -> int4 {
         if (offsets) return group_tile(offsets, s_first, G, t);
@@ -417,16 +417,18 @@ __device__ __forceinline__ void unit_values(uint2 c, uint32_t sb, bool scaled, f
 
 template <class F, typename T, bool VEC>
 __global__ void __launch_bounds__(QTHREADS, 4)
-dequantize_rows_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int rows, int K, int lpr,
-                       const float* __restrict__ gscale, T* __restrict__ out, long long ldo) {
+dequantize_rows_kernel(const uint8_t* codes, const uint8_t* scales, int rows, int K, int lpr, const float* gscale, T* out,
+                       long long ldo) {
     constexpr int U = 2;
+    pdl_wait();
+    pdl_trigger();
     __shared__ __align__(16) T s_out[VEC ? 1 : QWARPS][VEC ? 1 : SEG + 8 * 32];
     const int lane = threadIdx.x & 31;
     const int units = (K + 31) / 32 * 2;
     const int nseg = (units + lpr - 1) / lpr, rpw = 32 / lpr, sub = lane / lpr, col = lane - sub * lpr;
     const int nb = (K + F::BLK - 1) / F::BLK;
     const size_t pitch = (size_t)units * 8;
-    const float g = gscale ? __ldg(gscale) : 1.f, r = __frcp_rn(g);
+    const float g = gscale ? *gscale : 1.f, r = __frcp_rn(g);
     Walk at((long long)blockIdx.x * QWARPS + (threadIdx.x >> 5), (long long)gridDim.x * QWARPS,
             (long long)((rows + rpw - 1) / rpw) * nseg, nseg);
     while (at.left > 0) {
@@ -443,7 +445,7 @@ dequantize_rows_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restr
             if (row[i] < rows && unit[i] < units) {
                 c[i] = __ldcs(reinterpret_cast<const uint2*>(codes + row[i] * pitch + (size_t)unit[i] * 8));
                 const int b = unit[i] * UNIT / F::BLK;
-                if (b < nb) sb[i] = __ldg(scales + (size_t)row[i] * nb + b);
+                if (b < nb) sb[i] = scales[(size_t)row[i] * nb + b];
             }
             at.next();
         }
@@ -662,10 +664,11 @@ extern "C" int moe_fp4_quantize(const void* x, long long ldx, int x_rows, const 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return by_kind(fmt, dtype, vec_ok(x, ldx, dtype), [&](auto f, auto t, auto v) {
         using T = decltype(t);
-        quantize_rows_kernel<decltype(f), T, decltype(v)::value><<<grid, QTHREADS, 0, s>>>(
-            static_cast<const T*>(x), ldx, x_rows, src, rows, K, lpr, gscale, static_cast<uint8_t*>(codes),
-            static_cast<uint8_t*>(scales), nullptr, nullptr, 0, 0, device_error_word());
-        return check_launch("quantize_rows_kernel");
+        return check_launch(launch_pdl(quantize_rows_kernel<decltype(f), T, decltype(v)::value>, dim3(grid), dim3(QTHREADS), 0, s,
+                                       static_cast<const T*>(x), ldx, x_rows, src, rows, K, lpr, gscale,
+                                       static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), nullptr, nullptr, 0, 0,
+                                       device_error_word()),
+                            "quantize_rows_kernel");
     });
 }
 
@@ -683,10 +686,10 @@ extern "C" int moe_fp4_dequantize(const void* codes, const void* scales, int row
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return by_kind(fmt, dtype, vec_ok(out, ldo, dtype), [&](auto f, auto t, auto v) {
         using T = decltype(t);
-        dequantize_rows_kernel<decltype(f), T, decltype(v)::value><<<grid, QTHREADS, 0, s>>>(
-            static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), rows, K, lpr, gscale,
-            static_cast<T*>(out), ldo);
-        return check_launch("dequantize_rows_kernel");
+        return check_launch(launch_pdl(dequantize_rows_kernel<decltype(f), T, decltype(v)::value>, dim3(grid), dim3(QTHREADS), 0, s,
+                                       static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), rows, K, lpr,
+                                       gscale, static_cast<T*>(out), ldo),
+                            "dequantize_rows_kernel");
     });
 }
 
