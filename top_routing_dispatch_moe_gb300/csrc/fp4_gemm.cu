@@ -32,6 +32,7 @@ constexpr int EPI_WARPS = 8, SF_WARPS = 4;
 constexpr int THREADS = 32 * (2 + EPI_WARPS + SF_WARPS);
 constexpr int TMEM_COLS = 512;
 constexpr int MAX_G = 1024;
+constexpr int GROUPS_BYTES = (3 * MAX_G + 1) * 4;
 constexpr int BOX_BYTES = 2048;                  // an epilogue warp's staging buffer
 constexpr int SF_BUFS = 3;                       // stages of scales in tensor memory
 
@@ -43,7 +44,7 @@ struct Cfg {
     static constexpr int B_BYTES = BN * SEG_K / 2;
     static constexpr int SF_BLOCKS = (BN + 127) / 128;               // 128-row scale tiles a weight tile touches
     template <class F> static constexpr int SFS = (1 + SF_BLOCKS) * SF_BYTES<F>;   // scale bytes of a stage
-    template <class F> static constexpr int SMEM = 1024 + EPI_WARPS * BOX_BYTES + STAGES * (A_BYTES + B_BYTES + SFS<F>) + 256 + (MAX_G + 1) * 4;
+    template <class F> static constexpr int SMEM = 1024 + EPI_WARPS * BOX_BYTES + STAGES * (A_BYTES + B_BYTES + SFS<F>) + 256 + GROUPS_BYTES;
     static constexpr int SF_COL = 2 * BN;                            // scale columns follow the two accumulators
     static constexpr int B_COLS = BN / 32;                           // scale columns of the weight rows in a piece
     template <class F> static constexpr int SF_COLS = SF_PIECES<F> * (4 + B_COLS);   // of a stage
@@ -74,37 +75,56 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 
 struct Work { int g, tile, row0, row1, n; };
 
-// first[g]: tiles before group g, first[G]: all of them (0 where offsets or schedule are no good; the quantisation reports it),
-// in shared memory: a search through global memory costs a decode call microseconds. From the offsets, which are older than
-// the kernel before this one, it is found without waiting for that kernel.
-__device__ __forceinline__ void find_tiles(const Params& p, int* first) {
+// The groups in shared memory: first[g] tiles before group g (first[G]: all of them; 0 where offsets or schedule are no good,
+// which the quantisation reports), its rows [beg[g], end[g]). A role finds its items without touching global memory: a
+// search there cost a decode call microseconds, and a search from scratch an epilogue 1100 cycles a tile. From the offsets,
+// which are older than the kernel before this one, they are found without waiting for that kernel.
+struct Groups { int *first, *beg, *end; };
+__device__ __forceinline__ Groups groups_at(void* smem) {
+    int* first = static_cast<int*>(smem);
+    return Groups{first, first + MAX_G + 1, first + 2 * MAX_G + 1};
+}
+__device__ __forceinline__ void find_groups(const Params& p, const Groups& gs) {
     if (p.offsets) {
-        scan_groups<THREADS>(p.offsets, p.G, p.rows, first);
-        return;
+        scan_groups<THREADS>(p.offsets, p.G, p.rows, gs.first);
+        for (int g = threadIdx.x; g < p.G; g += THREADS) {
+            gs.beg[g] = __ldg(p.offsets + g);
+            gs.end[g] = __ldg(p.offsets + g + 1);
+        }
+    } else {
+        const bool fits = p.sched[1] == p.G && p.sched[0] <= p.max_tiles;
+        const int32_t* prefix = p.sched + kSchedHeader;
+        const int4* tiles = reinterpret_cast<const int4*>(p.sched + sched_tiles_offset(p.G));
+        for (int g = threadIdx.x; g <= p.G; g += THREADS) gs.first[g] = fits ? prefix[g] : 0;
+        for (int g = threadIdx.x; g < p.G; g += THREADS) {
+            const int t0 = fits ? prefix[g] : 0, t1 = fits ? prefix[g + 1] : 0;
+            gs.beg[g] = t0 < t1 ? min(tiles[t0].y, p.rows) : 0;
+            gs.end[g] = t0 < t1 ? min(tiles[t1 - 1].z, p.rows) : 0;
+        }
     }
-    const bool fits = p.sched[1] == p.G && p.sched[0] <= p.max_tiles;
-    for (int i = threadIdx.x; i <= p.G; i += THREADS) first[i] = fits ? p.sched[kSchedHeader + i] : 0;
     __syncthreads();
 }
-__device__ __forceinline__ int4 tile_entry(const Params& p, const int* first, int g, int t) {
-    if (!p.offsets) {
-        const int4 e = reinterpret_cast<const int4*>(p.sched + sched_tiles_offset(p.G))[t];
-        return make_int4(g, min(e.y, p.rows), min(e.z, p.rows), 0);
+// The last group g from `g` on with before[g] * NT <= w: a few steps ahead for a role whose items rise, else by halving.
+__device__ __forceinline__ int group_of(const int* before, int G, int NT, int w, int g) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        if (g + 1 >= G || before[g + 1] * NT > w) return g;
+        ++g;
     }
-    const int row0 = __ldg(p.offsets + g) + (t - first[g]) * BM;
-    return make_int4(g, row0, min(row0 + BM, __ldg(p.offsets + g + 1)), 0);
-}
-// Item w: group by group, n-tile next, m-tile fastest: CTAs that run together share a weight tile.
-__device__ __forceinline__ Work map_work(const Params& p, const int* first, int w) {
-    int lo = 0, hi = p.G;
-    while (lo < hi) {                    // last g with first[g] * NT <= w
+    int lo = g, hi = G - 1;
+    while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((long long)first[mid] * p.NT <= w) lo = mid; else hi = mid - 1;
+        if (before[mid] * NT <= w) lo = mid; else hi = mid - 1;
     }
-    const int p0 = first[lo], mt = first[lo + 1] - p0, local = w - p0 * p.NT;
-    const int n = local / mt, t = p0 + local % mt;
-    const int4 e = tile_entry(p, first, lo, t);
-    return Work{e.x, t, e.y, e.z, n};
+    return lo;
+}
+// Item w: group by group, n-tile next, m-tile fastest: CTAs that run together share a weight tile. g: the group of the role's
+// item before, and of this one.
+__device__ __forceinline__ Work map_work(const Params& p, const Groups& gs, int w, int& g) {
+    g = group_of(gs.first, p.G, p.NT, w, g);
+    const int p0 = gs.first[g], mt = gs.first[g + 1] - p0, local = w - p0 * p.NT;
+    const int n = local / mt, m = local - n * mt, row0 = gs.beg[g] + m * BM;
+    return Work{g, p0 + m, row0, min(row0 + BM, gs.end[g]), n};
 }
 
 // The producer's and the MMA warp's operations. The whole warp runs its loop, with conditions that are the same in all lanes
@@ -385,7 +405,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const uint32_t mma_done = bar0 + 8u * (2 * STAGES + 4);
     auto sfull = [&](int b) { return bar0 + 8u * (2 * STAGES + 5 + b); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5 + SF_BUFS);
-    int* first = reinterpret_cast<int*>(bars + 32);
+    const Groups gs = groups_at(bars + 32);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -400,14 +420,14 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         prefetch_tmap(&tmA32);
     }
     if (warp == 1) tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
-    find_tiles(p, first);
+    find_groups(p, gs);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     // (a programmatic dependent of the kernel that writes the row operand: the groups, the weights and everything above do
     // not wait for it)
-    const int total = uniform(first[p.G] * p.NT);
+    const int total = uniform(gs.first[p.G] * p.NT);
     if (warp != 0) {
         pdl_wait();
         pdl_trigger();
@@ -417,8 +437,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         int stage = 0;
         uint32_t phase = 0, issued = 0, last_par = 0;
         bool ok = true, ready = false;              // ready: the next ring stage was seen free
+        int at = 0;
         for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
-            const Work wk = map_work(p, first, w);
+            const Work wk = map_work(p, gs, w, at);
             const int n = uniform(wk.n), g = uniform(wk.g), tile = uniform(wk.tile), row0 = uniform(wk.row0);
             const int boxes = uniform((wk.row1 - wk.row0 + 31) >> 5);
             const int nb = min(BN / 64, p.NB64 - n * (BN / 64));
@@ -507,8 +528,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         int stage = 0, b = 0, old = STAGES - SF_BUFS;
         uint32_t phase = 0, ophase = 1;             // (the rounds before the first count as complete)
         bool ok = true, loaded = false, freed = false;
+        int at = 0;
         for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
-            const bool odd = BN % 128 == 64 && (map_work(p, first, w).n & 1);
+            const bool odd = BN % 128 == 64 && (map_work(p, gs, w, at).n & 1);
             for (int kb = 0; kb < p.kst; ++kb) {
                 if (!loaded) ok = wait_warp(full(stage), phase, p.wait_limit, abort_flag, p.err, 0x241u);
                 if (!ok) break;
@@ -550,10 +572,10 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         }
     } else {
         const int quarter = 32 * (warp & 3), half = (warp - 2) >> 2, r = quarter + lane;
-        int iter = 0;
+        int iter = 0, at = 0;
         for (int w = blockIdx.x; w < total; w += gridDim.x, ++iter) {
             const int a = iter & 1;
-            const Work wk = map_work(p, first, w);       // (before the wait: its loads take a while)
+            const Work wk = map_work(p, gs, w, at);
             if (!wait_warp(tfull(a), (iter >> 1) & 1, p.wait_limit, abort_flag, p.err, 0x230u)) break;
             tc_fence_after();
             const uint32_t tbase = tmem + a * BN + ((uint32_t)quarter << 16);
@@ -603,7 +625,7 @@ template <class F> constexpr int P_SFS = 3 * SF_BYTES<F>;
 template <int EPI> constexpr int P_STAGES = 5;
 template <int EPI> constexpr int P_BOX = EPI == EPI_OUT ? BOX_BYTES : 0;
 template <class F, int EPI>
-constexpr int P_SMEM = 1024 + EPI_WARPS * P_BOX<EPI> + P_STAGES<EPI> * (A_BYTES + PB_BYTES + P_SFS<F>) + 256 + 2 * (MAX_G + 1) * 4;
+constexpr int P_SMEM = 1024 + EPI_WARPS * P_BOX<EPI> + P_STAGES<EPI> * (A_BYTES + PB_BYTES + P_SFS<F>) + 256 + GROUPS_BYTES + (MAX_G + 1) * 4;
 template <class F> constexpr int P_COLS = SF_PIECES<F> * 8;      // scale columns of the weight rows in a stage
 static_assert(P_SF_BUFS * P_COLS<Nv> <= 96 && P_SFA_COL + 2 * SF_PIECES<Nv> * 4 <= TMEM_COLS, "tensor memory columns");
 static_assert(P_SMEM<Nv, EPI_OUT> + 64 <= 227 * 1024, "shared memory per CTA");
@@ -659,19 +681,14 @@ __device__ __forceinline__ bool wait_warp_pair(uint32_t bar, uint32_t parity, lo
 struct PairItem { Work wk; int arow, rows; };
 __device__ __forceinline__ int pairs_of(const int* first, int g) { return (first[g + 1] - first[g] + 1) >> 1; }
 // pp[g]: pairs before group g.
-__device__ __forceinline__ PairItem map_pair_item(const Params& p, const int* first, const int* pp, int w, int rank) {
-    int lo = 0, hi = p.G;
-    while (lo < hi) {                    // last g with pp[g] * NT <= w
-        const int mid = (lo + hi + 1) >> 1;
-        if ((long long)pp[mid] * p.NT <= w) lo = mid; else hi = mid - 1;
-    }
-    const int np = pp[lo + 1] - pp[lo], local = w - pp[lo] * p.NT;
-    const int n = local / np, q = local % np;
-    const int p0 = first[lo], mt = first[lo + 1] - p0;
+__device__ __forceinline__ PairItem map_pair_item(const Params& p, const Groups& gs, const int* pp, int w, int rank, int& g) {
+    g = group_of(pp, p.G, p.NT, w, g);
+    const int np = pp[g + 1] - pp[g], local = w - pp[g] * p.NT;
+    const int n = local / np, q = local - n * np;
+    const int p0 = gs.first[g], mt = gs.first[g + 1] - p0;
     const bool has = 2 * q + rank < mt;
-    const int t = p0 + 2 * q + (has ? rank : 0);
-    const int4 e = tile_entry(p, first, lo, t);
-    return PairItem{Work{e.x, t, has ? e.y : 0, has ? e.z : 0, n}, e.y, e.z - e.y};
+    const int m = 2 * q + (has ? rank : 0), row0 = gs.beg[g] + m * BM, row1 = min(row0 + BM, gs.end[g]);
+    return PairItem{Work{g, p0 + m, has ? row0 : 0, has ? row1 : 0, n}, row0, row1 - row0};
 }
 
 template <class F, int EPI>
@@ -690,8 +707,8 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     const uint32_t tfull = bar0 + 8u * (2 * STAGES + P_SF_BUFS), tempty = tfull + 8u, mma_done = tempty + 8u;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + P_SF_BUFS + 3);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* first = reinterpret_cast<int*>(bars + 32);
-    int* pp = first + MAX_G + 1;
+    const Groups gs = groups_at(bars + 32);
+    int* pp = gs.first + 3 * MAX_G + 1;
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -708,13 +725,13 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     }
     // (a programmatic dependent of the kernel that writes the row operand: the groups, the weights and the set-up do not wait
     // for it)
-    find_tiles(p, first);
+    find_groups(p, gs);
     if (warp == 2) {                             // pairs of tiles of each group, summed up
         int carry = 0;
         if (lane == 0) pp[0] = 0;
         for (int base = 0; base < p.G; base += 32) {
             const int g = base + lane;
-            int v = g < p.G ? pairs_of(first, g) : 0;
+            int v = g < p.G ? pairs_of(gs.first, g) : 0;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int t = __shfl_up_sync(0xffffffffu, v, off);
@@ -740,8 +757,9 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         int stage = 0;
         uint32_t phase = 0, issued = 0, last_par = 0;
         bool ok = true, ready = false;
+        int at = 0;
         for (int w = cid; w < total && ok; w += NC) {
-            const PairItem it = map_pair_item(p, first, pp, w, rank);
+            const PairItem it = map_pair_item(p, gs, pp, w, rank, at);
             const int n = uniform(it.wk.n), g = uniform(it.wk.g), tile = uniform(it.wk.tile), arow = uniform(it.arow);
             const int boxes = uniform((it.rows + 31) >> 5), half = uniform((int)rank);
             const int nb = min(2, max(0, p.NB64 - n * 4 - 2 * half)), nt = min(2, p.NB128 - 2 * n);
@@ -865,9 +883,9 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     } else {
         const int quarter = 32 * (warp & 3), half = (warp - 2) >> 2, r = quarter + lane;
         const uint32_t tempty0 = map_rank(tempty, 0);
-        int iter = 0;
+        int iter = 0, at = 0;
         for (int w = cid; w < total; w += NC, ++iter) {
-            const Work wk = map_pair_item(p, first, pp, w, rank).wk;   // (before the wait: its loads take a while)
+            const Work wk = map_pair_item(p, gs, pp, w, rank, at).wk;
             if (!wait_warp_pair(tfull, iter & 1, p.wait_limit, abort_flag, peer_abort, p.err, 0x280u)) break;
             tc_fence_after();
             const uint32_t tbase = tmem + (iter & 1) * P_ACC2 + ((uint32_t)quarter << 16);
