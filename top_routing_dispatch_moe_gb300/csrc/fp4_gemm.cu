@@ -320,9 +320,11 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const CUtensorMa
         const float ag = p.alpha ? __ldg(p.alpha + wk.g) : 1.f, au = p.alpha_up ? __ldg(p.alpha_up + wk.g) : 1.f;
         const float gs = p.act_gscale ? __ldg(p.act_gscale) : 1.f;
         const int f0 = c0 / 2;                   // first column of act
-        // g / (1 + exp(-g)) * u, each step rounded as written, so that an activation at a rounding tie of its code goes the
-        // way that the plain fp32 formula takes: with the quotient as g times the MUFU's reciprocal alone, two in a million
-        // codes went the other way. (1 + exp(-g) is cut to 1e30: the quotient is 0 in 4 bits by then.)
+        // g / (1 + exp(-g)) * u, each step but the exponential rounded as written, so that an activation at a rounding tie of
+        // its code mostly goes the way that the plain fp32 formula takes: with the quotient as g times the MUFU's reciprocal,
+        // two codes in a million went the other way. The exponential is the MUFU's, a few units in the last place off; expf
+        // cost the FFN of 16384 tokens and 128 experts 384 -> 402 us. (1 + exp(-g) is cut to 1e30: the quotient is 0 in 4
+        // bits by then.)
         float* u = v + 32;
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
@@ -606,7 +608,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 // The one-SM kernel waits for its operands: a stage of four MMAs (N = 192) takes 385 cycles and needs 47 KB, and with 150 to
 // 190 KB under way some 55 bytes a cycle arrive. In a pair each SM holds its own 128 rows of A and half of the weight rows
 // (and the scales of all of them, which its tensor core needs): 38 KB for MMAs a third larger, and five stages of them.
-// 16384 skewed rows by 8 x 14336 x 4096 (NV): 456 us by single SMs, 349 by pairs with the quantisation of 41 in both; 300 of
+// 16384 skewed rows by 8 x 14336 x 4096 (NV): 456 us by single SMs, 343 by pairs with the quantisation of 41 in both; 300 of
 // the pairs' time at 6.2 PFLOP/s, the tensor pipe 62 % busy. The MMAs alone, without loads and epilogue, took 233.
 // The even CTA issues the MMAs for both. Every copy of a CTA completes on its own barrier; the odd CTA's scale warps, which
 // wait for it, pass the news on with their arrival on the even CTA's scale barrier, so that barrier tells of both CTAs'
