@@ -295,6 +295,35 @@ def test_a_schedule_past_the_rows_is_cut(gpu_lib):
     assert (np.abs(f64(full[:40]) - want) <= Q.product_bound(a, w[0], want, 2.0**-8)).all()
 
 
+@pytest.mark.parametrize("rows", [300, 3000])
+def test_buffers_rewritten_between_calls(gpu_lib, rows):
+    """Offsets, row indices, multipliers, rows and schedule rewritten in place between calls that follow at once: each call
+    sees its own (the kernels start ahead of those before them, and no call may see the last one's)."""
+    moe = gpu_lib
+    G, N, K = 6, 320, 512
+    c, s, _ = weight(moe, G, N, K, "nv", 3)
+    packed = moe.moe_fp4_pack_weight(c, s, K, "nv")
+    g = torch.Generator().manual_seed(rows)
+    sets = []
+    for i in range(6):
+        cuts = torch.sort(torch.randint(0, rows + 1, (G - 1,), generator=g)).values
+        off = torch.cat([torch.zeros(1, dtype=torch.long), cuts, torch.full((1,), rows)]).int().cuda()
+        sets.append((data((rows, K), "bf16", i), off, torch.rand(G, generator=g).cuda() + 0.5,
+                     torch.randperm(rows, generator=g).int().cuda()))
+    want = [moe.moe_fp4_linear(x, off, packed, N, "nv", alpha=al, src=src) for x, off, al, src in sets]
+    torch.cuda.synchronize()
+    x, off, al, src = (t.clone() for t in sets[0])
+    ws = torch.empty(moe.moe_fp4_linear_workspace_size(G, K, rows, "nv"), dtype=torch.uint8, device="cuda")
+    got = []
+    for k in range(90):
+        for t, new in zip((x, off, al, src), sets[k % 6]):
+            t.copy_(new)
+        got.append(moe.moe_fp4_linear(x, off, packed, N, "nv", alpha=al, src=src, ws=ws))
+    ok(moe)
+    for k, y in enumerate(got):
+        assert torch.equal(y, want[k % 6]), k
+
+
 # --------------------------------------------------------------------------------------------------- FFN
 
 

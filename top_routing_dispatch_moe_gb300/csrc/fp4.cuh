@@ -186,7 +186,8 @@ __device__ __forceinline__ float scale_value(uint32_t b) {
 }
 
 // Tile counts of the groups [offsets[g], offsets[g + 1]) summed up into first[0 .. G] (G <= 1024) by a block of NT threads;
-// 0 everywhere, and true, if an offset falls or leaves [0, rows].
+// 0 everywhere, and true, if an offset falls or leaves [0, rows]. (Read from L2: a product does so before it has waited for
+// the kernel before it, when an L1 line of an earlier call's offsets may still be there.)
 template <int NT>
 __device__ __forceinline__ bool scan_groups(const int32_t* offsets, int G, int rows, int* first) {
     constexpr int PER = (1024 + NT - 1) / NT;
@@ -198,7 +199,7 @@ __device__ __forceinline__ bool scan_groups(const int32_t* offsets, int G, int r
     for (int i = 0; i < PER; ++i) {
         n[i] = 0;
         if (g0 + i < G) {
-            const int lo = offsets[g0 + i], hi = offsets[g0 + i + 1];
+            const int lo = __ldcg(offsets + g0 + i), hi = __ldcg(offsets + g0 + i + 1);
             if (lo < 0 || hi < lo || hi > rows) bad = true;
             else n[i] = (int)(((long long)hi - lo + MOE_TILE_M - 1) / MOE_TILE_M);
         }

@@ -78,7 +78,8 @@ struct Work { int g, tile, row0, row1, n; };
 // The groups in shared memory: first[g] tiles before group g (first[G]: all of them; 0 where offsets or schedule are no good,
 // which the quantisation reports), its rows [beg[g], end[g]). A role finds its items without touching global memory: a
 // search there cost a decode call microseconds, and a search from scratch an epilogue 1100 cycles a tile. From the offsets,
-// which are older than the kernel before this one, they are found without waiting for that kernel.
+// which are older than the kernel before this one, they are found without waiting for that kernel (read from L2, where its
+// predecessors' writes are).
 struct Groups { int *first, *beg, *end; };
 __device__ __forceinline__ Groups groups_at(void* smem) {
     int* first = static_cast<int*>(smem);
@@ -88,18 +89,18 @@ __device__ __forceinline__ void find_groups(const Params& p, const Groups& gs) {
     if (p.offsets) {
         scan_groups<THREADS>(p.offsets, p.G, p.rows, gs.first);
         for (int g = threadIdx.x; g < p.G; g += THREADS) {
-            gs.beg[g] = __ldg(p.offsets + g);
-            gs.end[g] = __ldg(p.offsets + g + 1);
+            gs.beg[g] = __ldcg(p.offsets + g);
+            gs.end[g] = __ldcg(p.offsets + g + 1);
         }
     } else {
-        const bool fits = p.sched[1] == p.G && p.sched[0] <= p.max_tiles;
+        const bool fits = __ldcg(p.sched + 1) == p.G && __ldcg(p.sched) <= p.max_tiles;
         const int32_t* prefix = p.sched + kSchedHeader;
         const int4* tiles = reinterpret_cast<const int4*>(p.sched + sched_tiles_offset(p.G));
-        for (int g = threadIdx.x; g <= p.G; g += THREADS) gs.first[g] = fits ? prefix[g] : 0;
+        for (int g = threadIdx.x; g <= p.G; g += THREADS) gs.first[g] = fits ? __ldcg(prefix + g) : 0;
         for (int g = threadIdx.x; g < p.G; g += THREADS) {
-            const int t0 = fits ? prefix[g] : 0, t1 = fits ? prefix[g + 1] : 0;
-            gs.beg[g] = t0 < t1 ? min(tiles[t0].y, p.rows) : 0;
-            gs.end[g] = t0 < t1 ? min(tiles[t1 - 1].z, p.rows) : 0;
+            const int t0 = fits ? __ldcg(prefix + g) : 0, t1 = fits ? __ldcg(prefix + g + 1) : 0;
+            gs.beg[g] = t0 < t1 ? min(__ldcg(tiles + t0).y, p.rows) : 0;
+            gs.end[g] = t0 < t1 ? min(__ldcg(tiles + t1 - 1).z, p.rows) : 0;
         }
     }
     __syncthreads();
