@@ -487,6 +487,12 @@ def test_layer_with_experts_in_4_bits(gpu_lib, experts, name, over):
     graph.replay()
     ok(gpu_lib)
     assert torch.equal(layer.y, y)
+    x.mul_(0.5)                                          # other rows, other routes: the graph reads x where it is
+    y = layer.forward(x).clone()
+    layer.y.zero_()
+    graph.replay()
+    ok(gpu_lib)
+    assert torch.equal(layer.y, y)
     with pytest.raises(NotImplementedError):
         layer.native_desc()
     with pytest.raises(RuntimeError):

@@ -185,11 +185,13 @@ __device__ __forceinline__ float scale_value(uint32_t b) {
     return b == 255u ? __uint_as_float(0x7FC00000u) : b ? __uint_as_float(b << 23) : __uint_as_float(1u << 22);
 }
 
-// Tile counts of the groups [offsets[g], offsets[g + 1]) summed up into first[0 .. G] (G <= 1024) by a block of NT threads;
+// Tile counts of the groups [offsets[g], offsets[g + 1]) summed up into first[0 .. G] (G <= 1024) by a block of NT threads (and the
+// groups' first and last rows into beg and end);
 // 0 everywhere, and true, if an offset falls or leaves [0, rows]. (Read from L2: a product does so before it has waited for
 // the kernel before it, when an L1 line of an earlier call's offsets may still be there.)
 template <int NT>
-__device__ __forceinline__ bool scan_groups(const int32_t* offsets, int G, int rows, int* first) {
+__device__ __forceinline__ bool scan_groups(const int32_t* offsets, int G, int rows, int* first, int* beg = nullptr,
+                                            int* end = nullptr) {
     constexpr int PER = (1024 + NT - 1) / NT;
     __shared__ int s_warp[NT / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g0 = threadIdx.x * PER;
@@ -200,6 +202,7 @@ __device__ __forceinline__ bool scan_groups(const int32_t* offsets, int G, int r
         n[i] = 0;
         if (g0 + i < G) {
             const int lo = __ldcg(offsets + g0 + i), hi = __ldcg(offsets + g0 + i + 1);
+            if (beg) { beg[g0 + i] = lo; end[g0 + i] = hi; }
             if (lo < 0 || hi < lo || hi > rows) bad = true;
             else n[i] = (int)(((long long)hi - lo + MOE_TILE_M - 1) / MOE_TILE_M);
         }

@@ -87,37 +87,34 @@ __device__ __forceinline__ Groups groups_at(void* smem) {
 }
 __device__ __forceinline__ void find_groups(const Params& p, const Groups& gs) {
     if (p.offsets) {
-        scan_groups<THREADS>(p.offsets, p.G, p.rows, gs.first);
-        for (int g = threadIdx.x; g < p.G; g += THREADS) {
-            gs.beg[g] = __ldcg(p.offsets + g);
-            gs.end[g] = __ldcg(p.offsets + g + 1);
-        }
-    } else {
-        const bool fits = __ldcg(p.sched + 1) == p.G && __ldcg(p.sched) <= p.max_tiles;
-        const int32_t* prefix = p.sched + kSchedHeader;
-        const int4* tiles = reinterpret_cast<const int4*>(p.sched + sched_tiles_offset(p.G));
-        for (int g = threadIdx.x; g <= p.G; g += THREADS) gs.first[g] = fits ? __ldcg(prefix + g) : 0;
-        for (int g = threadIdx.x; g < p.G; g += THREADS) {
-            const int t0 = fits ? __ldcg(prefix + g) : 0, t1 = fits ? __ldcg(prefix + g + 1) : 0;
-            gs.beg[g] = t0 < t1 ? min(__ldcg(tiles + t0).y, p.rows) : 0;
-            gs.end[g] = t0 < t1 ? min(__ldcg(tiles + t1 - 1).z, p.rows) : 0;
-        }
+        scan_groups<THREADS>(p.offsets, p.G, p.rows, gs.first, gs.beg, gs.end);
+        return;
+    }
+    const bool fits = __ldcg(p.sched + 1) == p.G && __ldcg(p.sched) <= p.max_tiles;
+    const int32_t* prefix = p.sched + kSchedHeader;
+    const int4* tiles = reinterpret_cast<const int4*>(p.sched + sched_tiles_offset(p.G));
+    for (int g = threadIdx.x; g <= p.G; g += THREADS) gs.first[g] = fits ? __ldcg(prefix + g) : 0;
+    for (int g = threadIdx.x; g < p.G; g += THREADS) {
+        const int t0 = fits ? __ldcg(prefix + g) : 0, t1 = fits ? __ldcg(prefix + g + 1) : 0;
+        gs.beg[g] = t0 < t1 ? min(__ldcg(tiles + t0).y, p.rows) : 0;
+        gs.end[g] = t0 < t1 ? min(__ldcg(tiles + t1 - 1).z, p.rows) : 0;
     }
     __syncthreads();
 }
-// The last group g from `g` on with before[g] * NT <= w: a few steps ahead for a role whose items rise, else by halving.
+// The last group g from `g` on with before[g] * NT <= w: steps that double (a role's items rise), then halving.
 __device__ __forceinline__ int group_of(const int* before, int G, int NT, int w, int g) {
+    int hi = g + 1;                      // before[hi] * NT > w, or hi == G
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-        if (g + 1 >= G || before[g + 1] * NT > w) return g;
-        ++g;
+    for (int step = 1; hi < G && before[hi] * NT <= w; step *= 2) {
+        g = hi;
+        hi = min(hi + step, G);
     }
-    int lo = g, hi = G - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (before[mid] * NT <= w) lo = mid; else hi = mid - 1;
+#pragma unroll 1
+    while (hi - g > 1) {
+        const int mid = (g + hi) >> 1;
+        if (before[mid] * NT <= w) g = mid; else hi = mid;
     }
-    return lo;
+    return g;
 }
 // Item w: group by group, n-tile next, m-tile fastest: CTAs that run together share a weight tile. g: the group of the role's
 // item before, and of this one.
