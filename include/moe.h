@@ -454,7 +454,9 @@ int moe_dequant_fp8(const uint8_t* buf8, const float* scales, int rows, int h, v
  *     out[r] = alpha[g] * sum_k Q(x)[r, k] W[g, :, k]         alpha [G] fp32 or NULL (1); fp32 accumulation
  *   The rows of a group are [offsets[g], offsets[g + 1]) (offsets [G + 1] int32, rising within [0, rows]; any other is
  *   reported by moe_check_device_error as MOE_ERR_INVALID_ARG and nothing is computed), or those of tile_sched
- *   (moe_dispatch's; exactly one of the two is given). Rows of no group are not written.
+ *   (moe_dispatch's; exactly one of the two is given). A schedule of another number of groups, or with tiles past the
+ *   call's rows, is reported likewise; one whose last tile ends past them gives the rows that there are. Rows of no group
+ *   are not written.
  * moe_fp4_expert_ffn: for the rows of expert e
  *     act = silu(alpha_gate[e] Q(x) W_gate[e]^T) * (alpha_up[e] Q(x) W_up[e]^T)
  *     out = alpha_down[e] * Q(act * act_gscale[0]) W_down[e]^T

@@ -295,6 +295,47 @@ def test_a_schedule_past_the_rows_is_cut(gpu_lib):
     assert (np.abs(f64(full[:40]) - want) <= Q.product_bound(a, w[0], want, 2.0**-8)).all()
 
 
+def tile_sched(groups, first=None):
+    """The tile schedule of groups of rows [(begin, end)]; first: other words in the place of its tiles before each group."""
+    tiles = [(g, r, min(r + 128, hi), 0) for g, (lo, hi) in enumerate(groups) for r in range(lo, hi, 128)]
+    before = [sum(t[0] < g for t in tiles) for g in range(len(groups) + 1)]
+    words = [len(tiles), len(groups)] + (first or before)
+    words += [0] * (-len(words) % 4) + [v for t in tiles for v in t]
+    return torch.tensor(words, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("groups,first,rows,N,K", [
+    ([(0, 256)], None, 40, 32, 64),                      # its second tile starts past the rows
+    ([(0, 100), (200, 300)], None, 150, 96, 320),        # a group past the rows
+    ([(0, 100), (150, 300)], None, 150, 200, 64),        # a group that starts where the rows end
+    ([(0, 5120)], None, 4990, 1000, 2048),               # the same by pairs of SMs
+    ([(0, 5119), (5119, 5120)], None, 5000, 1000, 2048),
+    ([(0, 100), (100, 300)], [0, 2, 1], 300, 64, 64),    # counts that fall
+    ([(0, 100), (100, 300)], [1, 1, 3], 300, 64, 64),
+    ([(0, 100), (100, 300)], [0, 1, 2], 300, 64, 64)])   # a tile of no group
+def test_a_schedule_of_other_rows_is_reported(gpu_lib, groups, first, rows, N, K):
+    """A tile schedule that has as many groups and tiles as the call may have, but of other rows, computes nothing; the next
+    call is whole."""
+    moe = gpu_lib
+    G = len(groups)
+    c, s, _ = weight(moe, G, N, K, "mx", 3)
+    packed = moe.moe_fp4_pack_weight(c, s, K, "mx")
+    x = data((rows, K), "bf16", 4)
+    out = torch.full((rows, N), 5.0, dtype=torch.bfloat16, device="cuda")
+    sched = tile_sched(groups, first)
+    moe.moe_fp4_linear(x, None, packed, N, "mx", G=G, tile_sched=sched, out=out)
+    torch.cuda.synchronize()
+    assert moe.moe_check_device_error() == moe.MOE_ERR_INVALID_ARG
+    assert (out == 5).all()
+    own = [(min(lo, rows), min(hi, rows)) for lo, hi in groups]
+    y = moe.moe_fp4_linear(x, None, packed, N, "mx", G=G, tile_sched=tile_sched(own))
+    off = torch.tensor([lo for lo, _ in own] + [own[-1][1]], dtype=torch.int32, device="cuda")
+    z = moe.moe_fp4_linear(x, off, packed, N, "mx")
+    ok(moe)
+    for lo, hi in own:
+        assert torch.equal(y[lo:hi], z[lo:hi])
+
+
 @pytest.mark.parametrize("rows", [300, 3000])
 def test_buffers_rewritten_between_calls(gpu_lib, rows):
     """Offsets, row indices, multipliers, rows and schedule rewritten in place between calls that follow at once: each call

@@ -75,11 +75,11 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 
 struct Work { int g, tile, row0, row1, n; };
 
-// The groups in shared memory: first[g] tiles before group g (first[G]: all of them; 0 where offsets or schedule are no good,
-// which the quantisation reports), its rows [beg[g], end[g]). A role finds its items without touching global memory: a
-// search there cost a decode call microseconds, and a search from scratch an epilogue 1100 cycles a tile. From the offsets,
-// which are older than the kernel before this one, they are found without waiting for that kernel (read from L2, where its
-// predecessors' writes are).
+// The groups in shared memory: first[g] tiles before group g (first[G]: all of them; 0 where offsets or schedule are no good:
+// the quantisation reports the offsets, the product the schedule), its rows [beg[g], end[g]). A role finds its items without
+// touching global memory: a search there cost a decode call microseconds, and a search from scratch an epilogue 1100 cycles a
+// tile. From the offsets, which are older than the kernel before this one, they are found without waiting for that kernel
+// (read from L2, where its predecessors' writes are).
 struct Groups { int *first, *beg, *end; };
 __device__ __forceinline__ Groups groups_at(void* smem) {
     int* first = static_cast<int*>(smem);
@@ -90,16 +90,29 @@ __device__ __forceinline__ void find_groups(const Params& p, const Groups& gs) {
         scan_groups<THREADS>(p.offsets, p.G, p.rows, gs.first, gs.beg, gs.end);
         return;
     }
-    const bool fits = __ldcg(p.sched + 1) == p.G && __ldcg(p.sched) <= p.max_tiles;
+    // A schedule counts where its tiles are those of the groups' rows within the call: a tile that starts past the call's rows,
+    // as another call's can, would have the producer ask for a negative number of rows.
+    const int ntiles = __ldcg(p.sched);
+    const bool fits = __ldcg(p.sched + 1) == p.G && ntiles <= p.max_tiles;
     const int32_t* prefix = p.sched + kSchedHeader;
     const int4* tiles = reinterpret_cast<const int4*>(p.sched + sched_tiles_offset(p.G));
-    for (int g = threadIdx.x; g <= p.G; g += THREADS) gs.first[g] = fits ? __ldcg(prefix + g) : 0;
+    bool bad = !fits;
     for (int g = threadIdx.x; g < p.G; g += THREADS) {
         const int t0 = fits ? __ldcg(prefix + g) : 0, t1 = fits ? __ldcg(prefix + g + 1) : 0;
-        gs.beg[g] = t0 < t1 ? min(__ldcg(tiles + t0).y, p.rows) : 0;
-        gs.end[g] = t0 < t1 ? min(__ldcg(tiles + t1 - 1).z, p.rows) : 0;
+        const bool some = 0 <= t0 && t0 < t1 && t1 <= ntiles;
+        const int beg = some ? min(__ldcg(tiles + t0).y, p.rows) : 0, end = some ? min(__ldcg(tiles + t1 - 1).z, p.rows) : 0;
+        bad |= (some ? beg < 0 || (max(end - beg, 0) + BM - 1) / BM != t1 - t0 : t0 != t1) || (g == 0 && t0 != 0) ||
+               (g == p.G - 1 && t1 != ntiles);
+        gs.first[g + 1] = t1;
+        gs.beg[g] = beg;
+        gs.end[g] = end;
     }
-    __syncthreads();
+    if (threadIdx.x == 0) gs.first[0] = 0;
+    if (__syncthreads_or(bad)) {
+        for (int g = threadIdx.x; g <= p.G; g += THREADS) gs.first[g] = 0;
+        if (blockIdx.x == 0 && threadIdx.x == 0) latch_device_error(p.err, kDevErrBadIndex, 0x204u);
+        __syncthreads();
+    }
 }
 // The last group g from `g` on with before[g] * NT <= w: steps that double (a role's items rise), then halving.
 __device__ __forceinline__ int group_of(const int* before, int G, int NT, int w, int g) {
