@@ -433,6 +433,57 @@ def test_expert_ffn_types_and_multipliers(gpu_lib, fmt, dtype, out_dtype):
     check_ffn(gpu_lib, [17, 0, 150], 192, 160, fmt, dtype, out_dtype, scaled=True, T=60)
 
 
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("F", [64, 40])
+def test_expert_ffn_far_gates(gpu_lib, fmt, F):
+    """Gates g far from 0 and infinite, and the activations one by one: an expert a magnitude of g, made by its alpha, a row a
+    sign; u of many magnitudes; the down weights give each activation's 4-bit value back, times a number that the format
+    holds. silu(inf) u is infinite and ends at the largest code, silu(-inf) is NaN as in the formula, and what is left of
+    silu(g) at a very negative g is as small as it is: an MX scale follows it down to 2^-127.
+
+    Bound of act: 2^-18 of it, and fp32's last places below the normal range: exp(-|g|) and its product with g within 2^-149
+    each, the former times |g|, all times |u|, and act's own. Codes as the definition gives for an act within its bound."""
+    moe = gpu_lib
+    mags = [0.0, 1.0, 20.0, 47.9, 48.1, 63.0, 63.99, 64.01, 70.0, 75.0, 80.0, 86.0, 87.5, 89.0, 95.0, 110.0, 1e4, 1e10, 1e25, 1e35, 3e38, np.inf]
+    E, h = len(mags), 64
+    x = torch.zeros((2 * E, h), dtype=torch.float64)
+    x[0::2, 0], x[1::2, 0], x[:, 32] = 6.0, -6.0, 6.0
+    wg, wu, wd = torch.zeros(E, F, h), torch.zeros(E, F, h), torch.zeros(E, h, F)
+    wg[:, :, 0] = torch.where(torch.arange(F) % 7 == 0, 0.0, 6.0)
+    wu[:, :, 32] = 6.0 * 2.0 ** (torch.arange(F) % 12 - 6) * (1 - 2 * (torch.arange(F) % 2))
+    back = np.array([6.0 if fmt == "nv" else 6.0 * (2.0**-40 if m > 1e9 else 2.0**40 if m > 60 else 1.0) for m in mags])
+    wd[:, torch.arange(F), torch.arange(F)] = torch.from_numpy(back).float()[:, None]
+    mats = []
+    for w in (wg, wu, wd):
+        c, s = moe.moe_fp4_quantize(w.reshape(-1, w.shape[2]).cuda(), fmt)
+        held = Q.dequantize(Q.unpack_codes(c.cpu().numpy(), w.shape[2]), s.cpu().numpy(), fmt)
+        np.testing.assert_array_equal(held, w.double().reshape(-1, w.shape[2]).numpy())
+        mats.append((c.view(*w.shape[:2], -1), s.view(*w.shape[:2], -1)))
+    packed = moe.moe_fp4_pack_expert_weights(*mats, h, F, fmt)
+    alpha = np.array([np.float32(3e38 if np.isinf(m) else m / 36) for m in mags], np.float32)
+    off = torch.arange(0, 2 * E + 1, 2, dtype=torch.int32, device="cuda")
+    y = moe.moe_fp4_expert_ffn(x.bfloat16().cuda(), off, packed, F, fmt, alpha_gate=torch.from_numpy(alpha).cuda(),
+                               out_dtype=torch.float32)
+    ok(moe)
+    got = f64(y)
+    for r in range(2 * E):
+        e = r // 2
+        with np.errstate(over="ignore"):
+            g = np.float64(np.float32(float(x[r, 0]) * wg[e, :, 0].double().numpy() * np.float64(alpha[e])))
+        u = 6.0 * wu[e, :, 32].double().numpy()
+        if (g == -np.inf).any():
+            assert np.isnan(got[r]).all()
+            continue
+        n = np.minimum(g, 0.0)
+        act = np.where(g < 0, n * np.exp(n) / (1 + np.exp(n)), g / (1 + np.exp(-np.maximum(g, 0.0)))) * u
+        act = np.where(np.abs(act) > np.finfo(np.float32).max, np.copysign(np.inf, act), act)
+        fin = np.where(np.isfinite(act), act, 0.0)
+        err = 2.0**-18 * np.abs(fin) + np.where(np.isfinite(g), (2 * np.minimum(np.abs(g), 110.0) + 1) * np.abs(u) + 1, 0) * 2.0**-149
+        q, dq = Q.requantized(act[None], err[None], fmt)
+        assert (np.abs(got[r, :F] - q[0] * back[e]) <= dq[0] * back[e]).all(), (mags[e], r, got[r, :F] / back[e], q[0])
+        assert (got[r, F:] == 0).all()
+
+
 def test_expert_ffn_is_deterministic_and_captures(gpu_lib):
     """The same bits on every call, on another stream and from a captured graph."""
     moe = gpu_lib

@@ -35,6 +35,9 @@ constexpr int MAX_G = 1024;
 constexpr int GROUPS_BYTES = (3 * MAX_G + 1) * 4;
 constexpr int BOX_BYTES = 2048;                  // an epilogue warp's staging buffer
 constexpr int SF_BUFS = 3;                       // stages of scales in tensor memory
+// Gates below which the epilogue's quick quotient holds: 1 + exp(-g) and its products stay far inside fp32's normal range, and
+// the exponential is within 2^-18.
+constexpr float FAR_GATE = 48.f;
 
 enum Epi : int { EPI_OUT = 0, EPI_SWIGLU = 1 };
 
@@ -333,22 +336,40 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const CUtensorMa
         const int f0 = c0 / 2;                   // first column of act
         // g / (1 + exp(-g)) * u, each step but the exponential rounded as written, so that an activation at a rounding tie of
         // its code mostly goes the way that the plain fp32 formula takes: with the quotient as g times the MUFU's reciprocal,
-        // two codes in a million went the other way. The exponential is the MUFU's, a few units in the last place off; expf
-        // cost the FFN of 16384 tokens and 128 experts 384 -> 402 us. (1 + exp(-g) is cut to 1e30: the quotient is 0 in 4
-        // bits by then.)
+        // two codes in a million went the other way. The exponential is the MUFU's of the rounded g log2(e), off by
+        // about 2^-22 + 1.25 |g| 2^-24 of it; expf cost the FFN of 16384 tokens and 128 experts 384 -> 402 us.
         float* u = v + 32;
+        float far = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) mul2(v + i, v + i, ag);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) far = max_nan(far, fabsf(v[i]));
+        if (far < FAR_GATE) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float t[2], d[2], r[2];
+                mul2(t, v + i, -1.44269504f);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    asm("ex2.approx.f32 %0, %1;" : "=f"(d[j]) : "f"(t[j]));
+                    d[j] = 1.f + d[j];
+                    asm("rcp.approx.f32 %0, %1;" : "=f"(r[j]) : "f"(d[j]));
+                }
+                quotient2v(v + i, d, r);
+            }
+        } else {
+            // a gate far from 0, infinite or NaN among the 32: exp(-g) would overflow, and the correction of an infinite
+            // quotient is NaN. As g exp(-|g|) / (1 + exp(-|g|)), without the numerator's exponential from 0 on.
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float e = expf(-fabsf(v[i]));
+                float r;
+                asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+                v[i] = (v[i] < 0.f ? v[i] * e : v[i]) * r;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-            float t[2], d[2], r[2];
-            mul2(v + i, v + i, ag);
-            mul2(t, v + i, -1.44269504f);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                asm("ex2.approx.f32 %0, %1;" : "=f"(d[j]) : "f"(t[j]));
-                d[j] = fminf(1.f + d[j], 1e30f);
-                asm("rcp.approx.f32 %0, %1;" : "=f"(r[j]) : "f"(d[j]));
-            }
-            quotient2v(v + i, d, r);
             mul2(u + i, u + i, au);
             mul2v(u + i, v + i, u + i);
             mul2(u + i, u + i, gs);
