@@ -589,3 +589,25 @@ def test_layer_with_experts_in_4_bits(gpu_lib, experts, name, over):
         layer.native_desc()
     with pytest.raises(RuntimeError):
         layer.backward(x, y)
+
+
+def test_a_layers_multipliers_are_its_own(gpu_lib):
+    """The tensors given for fp4_gscale and fp4_act_gscale may change after construction: the layer computes as it was made, call
+    by call and from a graph."""
+    from top_routing_dispatch_moe_gb300.layer import MoELayer
+    T, h, E, F = 64, 128, 4, 96
+    gs, ags = torch.tensor([64.0], device="cuda"), torch.tensor([256.0], device="cuda")
+    layer = MoELayer(T=T, h=h, E=E, k=2, F=F, gating="softmax_renorm", cf=0.0, R=1, alpha=0.0,
+                     w_r=data((h, E), "bf16", 1, 0.1), bias=None,
+                     w_gate=data((E, F, h), "bf16", 2, 0.1), w_up=data((E, F, h), "bf16", 3, 0.1), w_down=data((E, h, F), "bf16", 4, 0.1),
+                     experts="nvfp4", fp4_gscale=gs, fp4_act_gscale=ags)
+    x = data((T, h), "bf16", 5)
+    want = layer.forward(x).clone()
+    graph = layer.capture_forward(x)
+    gs.mul_(4)
+    ags.mul_(0.5)
+    assert torch.equal(layer.forward(x), want)
+    layer.y.zero_()
+    graph.replay()
+    ok(gpu_lib)
+    assert torch.equal(layer.y, want)

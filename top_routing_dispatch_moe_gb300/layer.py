@@ -31,10 +31,11 @@ class MoELayer:
     pre-activations g and u, so that the next backward() needs no recompute of the up/gate GEMM.
 
     experts="nvfp4" or "mxfp4" (bf16, forward only) holds the experts in 4 bits: the weights are quantised at construction
-    (nvfp4: each expert's matrix times a power of two first that brings its largest magnitude near 448 * 6), the tokens' rows and the activations inside
-    the FFN (fp4_gscale, fp4_act_gscale: fp32 scalar tensors that they are multiplied with before, e.g. calibrated to
-    448 * 6 / the largest magnitude expected; None: 1). The FFN reads x through the dispatch's row indices; both products
-    and the quantisations between them are the stage "up_gate", and "down" is empty."""
+    (nvfp4: each expert's matrix times a power of two first that brings its largest magnitude near 448 * 6), the tokens'
+    rows and the activations inside the FFN (fp4_gscale, fp4_act_gscale: fp32 scalar tensors that they are multiplied with
+    before, e.g. calibrated to 448 * 6 / the largest magnitude expected; None: 1; copied at construction, where their
+    inverses go into the experts' factors: another calibration is another layer). The FFN reads x through the dispatch's
+    row indices; both products and the quantisations between them are the stage "up_gate", and "down" is empty."""
 
     STAGES = ("router", "dispatch", "up_gate", "down", "shared_up_gate", "shared_down", "combine")
 
@@ -56,7 +57,8 @@ class MoELayer:
         self.fp4 = None if experts == "dtype" else experts[:2]
         if self.fp4 and (dt != torch.bfloat16 or backward or payload != "bf16" or fuse_combine):
             raise ValueError("experts in 4 bits: bf16 with the bf16 send buffer, the separate combine and no backward")
-        self.fp4_gscale, self.fp4_act_gscale = fp4_gscale, fp4_act_gscale
+        # (the layer's own: the alphas hold their inverses, and the kernels read them in every call)
+        self.fp4_gscale, self.fp4_act_gscale = (None if g is None else g.clone() for g in (fp4_gscale, fp4_act_gscale))
         pack = moe.moe_pack_expert_weights if self.fp4 is None else self._pack_fp4
         self.packed = pack(w_gate, w_up, w_down)
         self.shared_packed = pack(*shared) if shared is not None else None
