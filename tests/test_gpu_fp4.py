@@ -511,6 +511,39 @@ def test_expert_ffn_is_deterministic_and_captures(gpu_lib):
     assert torch.equal(y0, y1) and torch.equal(y0, y2) and torch.equal(y0, y3)
 
 
+def test_what_a_call_allocates_is_its_streams(gpu_lib, monkeypatch):
+    """Outputs and workspaces that the calls allocate come from the pool of the stream that they launch on (a workspace of the
+    current stream's would be handed out again while the kernels use it); results as on the current stream."""
+    moe = gpu_lib
+    E, h, F, rows = 3, 128, 96, 70
+    mats = [weight(moe, E, n, k, "nv", 40 + i)[:2] for i, (n, k) in enumerate(((F, h), (F, h), (h, F)))]
+    x = data((rows, h), "bf16", 6)
+    off = torch.tensor([0, 10, 10, rows], dtype=torch.int32, device="cuda")
+    real, seen = torch.empty, []
+
+    def empty(*a, **k):
+        seen.append(torch.cuda.current_stream())
+        return real(*a, **k)
+
+    def calls(stream):
+        codes, scales = moe.moe_fp4_quantize(x, "nv", stream=stream)
+        back = moe.moe_fp4_dequantize(codes, scales, h, "nv", stream=stream)
+        linear = moe.moe_fp4_linear(x, off, moe.moe_fp4_pack_weight(*mats[0], h, "nv", stream=stream), F, "nv", stream=stream)
+        packed = moe.moe_fp4_pack_expert_weights(*mats, h, F, "nv", stream=stream)
+        return codes, scales, back, linear, packed, moe.moe_fp4_expert_ffn(x, off, packed, F, "nv", stream=stream)
+
+    want = [t.clone() for t in calls(None)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    monkeypatch.setattr(torch, "empty", empty)
+    got = calls(side)
+    monkeypatch.undo()
+    ok(moe)
+    assert len(seen) == 9 and all(s == side for s in seen)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------------------------------------- layer
 
 

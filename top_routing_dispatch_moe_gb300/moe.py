@@ -775,6 +775,19 @@ def _fp4_stream(stream, t):
     return _raw_stream(t.device.index) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
 
 
+def _fp4_empty(shape, dtype, t, stream):
+    """What a call allocates belongs to the stream that it launches on, as under `with torch.cuda.stream(stream)`: a workspace
+    freed on return would otherwise go to the current stream's next tensor while the kernels still use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=t.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=t.device)
+
+
+def _fp4_bytes(nbytes: int, t, stream):
+    return _fp4_empty(max(int(nbytes), 16), torch.uint8, t, stream)
+
+
 @functools.lru_cache(maxsize=None)
 def moe_fp4_codes_pitch(K: int) -> int:
     """Bytes of codes a row: 16 for every 32 columns begun."""
@@ -804,8 +817,8 @@ def moe_fp4_quantize(x, fmt="nv", *, gscale=None, src=None, codes=None, scales=N
     f, K, ldx = _fp4_format(fmt), x.shape[-1], _fp4_rows(x, "x")
     rows = x.shape[0] if src is None else src.numel()
     nb, pitch = moe_fp4_scales_pitch(K, f), moe_fp4_codes_pitch(K)
-    codes = torch.empty((rows, pitch), dtype=torch.uint8, device=x.device) if codes is None else codes
-    scales = torch.empty((rows, nb), dtype=torch.uint8, device=x.device) if scales is None else scales
+    codes = _fp4_empty((rows, pitch), torch.uint8, x, stream) if codes is None else codes
+    scales = _fp4_empty((rows, nb), torch.uint8, x, stream) if scales is None else scales
     _check(_lib.moe_fp4_quantize(x.data_ptr(), ldx, x.shape[0], _fp4_data(src, 0, torch.int32, "src"), rows, K,
                                  _fp4_dtype(x.dtype), f, _fp4_data(gscale, 1, torch.float32, "gscale"),
                                  _fp4_data(codes, rows * pitch, torch.uint8, "codes"),
@@ -816,7 +829,7 @@ def moe_fp4_quantize(x, fmt="nv", *, gscale=None, src=None, codes=None, scales=N
 def moe_fp4_dequantize(codes, scales, K: int, fmt="nv", *, gscale=None, dtype=torch.bfloat16, out=None, stream=None):
     """The rows [rows, K] that codes and scales stand for, divided by gscale where it is given."""
     f, rows = _fp4_format(fmt), codes.shape[0]
-    out = torch.empty((rows, K), dtype=dtype, device=codes.device) if out is None else out
+    out = _fp4_empty((rows, K), dtype, codes, stream) if out is None else out
     ldo = _fp4_rows(out, "out")
     if out.shape[0] != rows or out.shape[1] != K:
         _fp4_fail(f"out: [{rows}, {K}]")
@@ -832,7 +845,7 @@ def moe_fp4_pack_weight(codes, scales, K: int, fmt="nv", packed=None, stream=Non
     in the operand layout of moe_fp4_linear."""
     f, (G, N) = _fp4_format(fmt), codes.shape[:2]
     need = _fp4_weight_bytes(G, N, K, f)
-    packed = _bytes_tensor(need, codes.device) if packed is None else packed
+    packed = _fp4_bytes(need, codes, stream) if packed is None else packed
     _check(_lib.moe_fp4_pack_weight(_fp4_data(codes, G * N * moe_fp4_codes_pitch(K), torch.uint8, "codes"),
                                     _fp4_data(scales, G * N * moe_fp4_scales_pitch(K, f), torch.uint8, "scales"), G, N, K, f,
                                     _fp4_data(packed, need, torch.uint8, "packed"), _fp4_stream(stream, codes)))
@@ -853,11 +866,11 @@ def moe_fp4_linear(x, offsets, packed, N: int, fmt="nv", *, G: int | None = None
     G = offsets.numel() - 1 if offsets is not None else G
     if G is None:
         _fp4_fail("G: the number of groups of tile_sched")
-    out = torch.empty((rows, N), dtype=out_dtype or x.dtype, device=x.device) if out is None else out
+    out = _fp4_empty((rows, N), out_dtype or x.dtype, x, stream) if out is None else out
     ldo = _fp4_rows(out, "out")
     if out.shape[0] != rows or out.shape[1] != N:
         _fp4_fail(f"out: [{rows}, {N}]")
-    ws = _bytes_tensor(_lib.moe_fp4_linear_workspace_size(G, K, rows, f), x.device) if ws is None else ws
+    ws = _fp4_bytes(_lib.moe_fp4_linear_workspace_size(G, K, rows, f), x, stream) if ws is None else ws
     _check(_lib.moe_fp4_linear(x.data_ptr(), ldx, x.shape[0], _fp4_data(src, 0, torch.int32, "src"),
                                _fp4_data(offsets, 2, torch.int32, "offsets"),
                                _fp4_data(tile_sched, 4, torch.int32, "tile_sched"),
@@ -876,7 +889,7 @@ def moe_fp4_pack_expert_weights(gate, up, down, h: int, F: int, fmt="nv", packed
         data.append(_fp4_data(c, E * n * moe_fp4_codes_pitch(k), torch.uint8, what + " codes"))
         data.append(_fp4_data(s, E * n * moe_fp4_scales_pitch(k, f), torch.uint8, what + " scales"))
     need = _fp4_experts_bytes(E, h, F, f)
-    packed = _bytes_tensor(need, gate[0].device) if packed is None else packed
+    packed = _fp4_bytes(need, gate[0], stream) if packed is None else packed
     _check(_lib.moe_fp4_pack_expert_weights(*data, E, h, F, f, _fp4_data(packed, need, torch.uint8, "packed"),
                                             _fp4_stream(stream, packed)))
     return packed
@@ -896,11 +909,11 @@ def moe_fp4_expert_ffn(x, offsets, packed, F: int, fmt="nv", *, E: int | None = 
     E = offsets.numel() - 1 if offsets is not None else E
     if E is None:
         _fp4_fail("E: the number of experts of tile_sched")
-    out = torch.empty((rows, h), dtype=out_dtype or x.dtype, device=x.device) if out is None else out
+    out = _fp4_empty((rows, h), out_dtype or x.dtype, x, stream) if out is None else out
     ldo = _fp4_rows(out, "out")
     if out.shape[0] != rows or out.shape[1] != h:
         _fp4_fail(f"out: [{rows}, {h}]")
-    ws = _bytes_tensor(_lib.moe_fp4_expert_ffn_workspace_size(E, h, F, rows, f), x.device) if ws is None else ws
+    ws = _fp4_bytes(_lib.moe_fp4_expert_ffn_workspace_size(E, h, F, rows, f), x, stream) if ws is None else ws
     _check(_lib.moe_fp4_expert_ffn(x.data_ptr(), ldx, x.shape[0], _fp4_data(src, 0, torch.int32, "src"),
                                    _fp4_data(offsets, 2, torch.int32, "offsets"),
                                    _fp4_data(tile_sched, 4, torch.int32, "tile_sched"),
