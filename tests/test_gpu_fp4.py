@@ -511,6 +511,20 @@ def test_expert_ffn_is_deterministic_and_captures(gpu_lib):
     assert torch.equal(y0, y1) and torch.equal(y0, y2) and torch.equal(y0, y3)
 
 
+def test_codes_of_another_shape_are_refused(gpu_lib):
+    """A weight's codes [G, N, pitch] are no rows to bring back, and experts of another F or h are no experts of these."""
+    moe = gpu_lib
+    E, h, F = 2, 64, 96
+    mats = [weight(moe, E, n, k, "nv", 50 + i)[:2] for i, (n, k) in enumerate(((F, h), (F, h), (h, F)))]
+    with pytest.raises(moe.MoEError):
+        moe.moe_fp4_dequantize(*mats[0], h, "nv")
+    assert moe.moe_fp4_dequantize(*(t.flatten(0, 1) for t in mats[0]), h, "nv").shape == (E * F, h)
+    for bad_h, bad_F in ((h, 64), (32, F), (F, h)):
+        with pytest.raises(moe.MoEError):
+            moe.moe_fp4_pack_expert_weights(*mats, bad_h, bad_F, "nv")
+    ok(moe)
+
+
 def test_what_a_call_allocates_is_its_streams(gpu_lib, monkeypatch):
     """Outputs and workspaces that the calls allocate come from the pool of the stream that they launch on (a workspace of the
     current stream's would be handed out again while the kernels use it); results as on the current stream."""

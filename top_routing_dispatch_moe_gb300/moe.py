@@ -828,6 +828,8 @@ def moe_fp4_quantize(x, fmt="nv", *, gscale=None, src=None, codes=None, scales=N
 
 def moe_fp4_dequantize(codes, scales, K: int, fmt="nv", *, gscale=None, dtype=torch.bfloat16, out=None, stream=None):
     """The rows [rows, K] that codes and scales stand for, divided by gscale where it is given."""
+    if codes.dim() != 2:
+        _fp4_fail("codes: [rows, pitch]")
     f, rows = _fp4_format(fmt), codes.shape[0]
     out = _fp4_empty((rows, K), dtype, codes, stream) if out is None else out
     ldo = _fp4_rows(out, "out")
@@ -886,6 +888,8 @@ def moe_fp4_pack_expert_weights(gate, up, down, h: int, F: int, fmt="nv", packed
     f, E = _fp4_format(fmt), gate[0].shape[0]
     data = []
     for (c, s), n, k, what in ((gate, F, h, "gate"), (up, F, h, "up"), (down, h, F, "down")):
+        if c.shape[:2] != (E, n):
+            _fp4_fail(f"{what} codes: [{E}, {n}, pitch]")
         data.append(_fp4_data(c, E * n * moe_fp4_codes_pitch(k), torch.uint8, what + " codes"))
         data.append(_fp4_data(s, E * n * moe_fp4_scales_pitch(k, f), torch.uint8, what + " scales"))
     need = _fp4_experts_bytes(E, h, F, f)
