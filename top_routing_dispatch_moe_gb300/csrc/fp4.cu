@@ -134,9 +134,10 @@ struct Walk {
     }
 };
 
-// The schedule of the groups, by one block; first: scan_groups' result, `bad` its answer.
-__device__ __forceinline__ void put_schedule(const int32_t* offsets, const int* first, bool bad, int G, int32_t* sched,
-                                             unsigned* err) {
+// The schedule of the groups, by one block.
+__device__ __noinline__ void write_schedule(const int32_t* offsets, int G, int rows, int32_t* sched, unsigned* err) {
+    __shared__ int first[1025];
+    const bool bad = scan_groups<QTHREADS>(offsets, G, rows, first);
     if (threadIdx.x == 0) {
         sched[0] = first[G];
         sched[1] = G;
@@ -145,11 +146,6 @@ __device__ __forceinline__ void put_schedule(const int32_t* offsets, const int* 
     for (int i = threadIdx.x; i <= G; i += QTHREADS) sched[kSchedHeader + i] = first[i];
     for (int t = threadIdx.x; t < first[G]; t += QTHREADS)
         reinterpret_cast<int4*>(sched + sched_tiles_offset(G))[t] = group_tile(offsets, first, G, t);
-}
-__device__ __noinline__ void write_schedule(const int32_t* offsets, int G, int rows, int32_t* sched, unsigned* err) {
-    __shared__ int s_first[1025];
-    const bool bad = scan_groups<QTHREADS>(offsets, G, rows, s_first);
-    put_schedule(offsets, s_first, bad, G, sched, err);
 }
 
 // Row-major form: codes [rows][pitch], scales [rows][nb]. An item is one row segment of lpr units, 32 / lpr rows to a
@@ -229,15 +225,15 @@ quantize_rows_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, 
 }
 
 // Operand form: the rows of the tiles, codes [rows][pad64(K) / 2], scales in the tile layout. The tiles are those of `sched`,
-// or with `offsets` those of the groups, found by every block for itself (a launch fewer than a kernel of its own); block 0
-// then writes the schedule for the products. A block takes one item at a time, 512 columns of a tile's rows or, where there
-// are few full tiles, of a quarter of them (parts = 2: the rows r with r % 32 in its range of 8, whole 16-byte granules of
-// the scale pieces): its warps take the rows in turn, the scale bytes meet in shared memory (pieces 528 bytes apart, so that
-// the pieces of one row fall into different banks) and leave as whole granules.
+// or with `offsets` those of the groups, found by every block for itself (a launch fewer than a kernel of its own), as the
+// products do. A block takes one item at a time, 512 columns of a tile's rows or, where there are few full tiles, of a
+// quarter of them (parts = 2: the rows r with r % 32 in its range of 8, whole 16-byte granules of the scale pieces): its
+// warps take the rows in turn, the scale bytes meet in shared memory (pieces 528 bytes apart, so that the pieces of one row
+// fall into different banks) and leave as whole granules.
 template <class F, typename T, bool VEC>
 __global__ void __launch_bounds__(QTHREADS, 4)
 quantize_operand_kernel(const T* x, long long ldx, int x_rows, const int32_t* src,
-                        const int32_t* offsets, int32_t* sched, int G, int rows, int max_tiles, int parts, int K,
+                        const int32_t* offsets, const int32_t* sched, int G, int rows, int max_tiles, int parts, int K,
                         const float* gscale, uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, unsigned* err) {
     constexpr int U = IN_FLIGHT<T>, PIECES = 2 * SF_PIECES<F>, STRIDE = 528;
     __shared__ __align__(16) uint8_t s_sf[PIECES * STRIDE];
@@ -259,7 +255,7 @@ quantize_operand_kernel(const T* x, long long ldx, int x_rows, const int32_t* sr
     if (offsets) {
         const bool bad = scan_groups<QTHREADS>(offsets, G, rows, s_first);
         ntiles = s_first[G];
-        if (blockIdx.x == 0) put_schedule(offsets, s_first, bad, G, sched, err);
+        if (bad && blockIdx.x == 0 && threadIdx.x == 0) latch_device_error(err, kDevErrBadIndex, 0x202u);
     } else {
         const bool fits = sched[1] == G && sched[0] <= max_tiles;        // (else: another call's schedule)
         ntiles = fits ? sched[0] : 0;

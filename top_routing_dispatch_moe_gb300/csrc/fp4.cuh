@@ -241,9 +241,9 @@ __device__ __forceinline__ int4 group_tile(const int32_t* offsets, const int* fi
 }
 #endif
 
-// The rows of the groups, quantised into the product's operand: of `offsets`, whose schedule is then written to `sched`, or
-// (offsets null) of the schedule that `sched` holds. rows_ws: null, or room for x's rows quantised once
-// (gathered_bytes), from which the rows that src names are then copied.
+// The rows of the groups, quantised into the product's operand: of `offsets`, or (offsets null) of the schedule that `sched`
+// holds. rows_ws: null, or room for x's rows quantised once (gathered_bytes), from which the rows that src names are then
+// copied, by the schedule of `offsets` written to `sched`.
 int launch_quantize_operand(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* offsets, int32_t* sched,
                             int G, int rows, int K, int dtype, int fmt, const float* gscale, void* codes, void* sf,
                             void* rows_ws, unsigned* err, cudaStream_t s);
