@@ -438,8 +438,9 @@ int moe_dequant_fp8(const uint8_t* buf8, const float* scales, int rows, int h, v
  *     MOE_FP4_NV: blocks of 16 columns, scale s = e4m3(amax / 6) to nearest even, at most 448
  *     MOE_FP4_MX: blocks of 32 columns, scale s = 2^(floor(log2 amax) - 2), stored as exponent + 127, held in [0, 254]
  *   code = e2m1(v / s) to nearest, ties to even, held at +-6 (0 where s is 0); amax the largest |v| of the block, v = x or
- *   x * gscale[0] in fp32 (gscale: a device fp32 scalar or NULL). Infinities end at the largest code; a NaN makes its
- *   block's scale NaN (0x7F, 0xFF) and its codes 0. A partial last block counts its missing columns as 0.
+ *   x * gscale[0] in fp32 (gscale: a device fp32 scalar, finite, or NULL). Infinities end at the largest code; a NaN makes
+ *   its block's scale NaN (0x7F, 0xFF) and its codes 0. A negative value whose code is 0 may keep its sign bit (code 8,
+ *   which stands for 0 too). A partial last block counts its missing columns as 0.
  *   dtype / out_dtype: MOE_F32, MOE_BF16 or MOE_F16. x and out may have row strides (ldx, ldo, in elements) and need be
  *   aligned to their type only; rows that start on 16 bytes are the fast case. Sizes: 1 <= K, N, F <= MOE_FP4_MAX_K,
  *   rows <= MOE_FP4_MAX_ROWS, 1 <= groups <= 1024. src: x's row of each row, -1 for a row of zeros, or NULL (row r of x).

@@ -75,6 +75,20 @@ def test_quantize_with_a_multiplier(gpu_lib, fmt):
 
 @pytest.mark.parametrize("fmt", ["nv", "mx"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("g", [58.35, -0.7, 1e-3])
+def test_quantize_with_any_multiplier(gpu_lib, fmt, dtype, g):
+    """Codes and scales are those of x * g rounded to fp32, by the row-major kernel and element by element."""
+    x = data((300, 999), dtype, 5)
+    mult = torch.tensor([g], device="cuda")
+    c, s = gpu_lib.moe_fp4_quantize(x, fmt, gscale=mult)
+    ok(gpu_lib)
+    code, byte = Q.quantize(np.float64(np.float32(f64(x) * float(mult))), fmt)
+    np.testing.assert_array_equal(s.cpu().numpy(), byte)
+    np.testing.assert_array_equal(Q.unpack_codes(c.cpu().numpy(), 999), code)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 def test_quantize_at_the_edges(gpu_lib, fmt, dtype):
     """Zeros, values at ties, the type's largest and smallest, infinities and NaN, each in blocks of their own."""
     fi = torch.finfo(DT[dtype])

@@ -168,8 +168,9 @@ __device__ __forceinline__ void block_codes(float* v, float amax, float s, float
 #pragma unroll
         for (int i = 0; i < N; i += 2) quotient2(v + i, s, r);
     } else {
+        const float zero[2] = {0.f, 0.f};        // (-0, as a missing column times a negative multiplier, becomes 0)
 #pragma unroll
-        for (int i = 0; i < N; i += 2) mul2(v + i, v + i, r);
+        for (int i = 0; i < N; i += 2) fma2(v + i, v + i, r, zero);
     }
     const bool bad = amax != amax;
 #pragma unroll
