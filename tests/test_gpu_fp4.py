@@ -211,6 +211,43 @@ def test_linear_of_many_tiles(gpu_lib, counts, N, K, fmt, dtype):
     check_linear(gpu_lib, counts, N, K, fmt, dtype)
 
 
+def ragged(G, most, seed):
+    """Rows of G groups, a fifth of them empty."""
+    n = np.random.default_rng(seed).integers(0, most, G)
+    n[::5] = 0
+    return [int(v) for v in n]
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("G,most,N,K", [(129, 9, 48, 64), (449, 5, 48, 96), (1024, 4, 40, 64),     # one SM to a tile
+                                        (45, 700, 700, 512), (70, 600, 1100, 300)])                # pairs of SMs
+def test_linear_of_many_groups(gpu_lib, fmt, G, most, N, K):
+    """More groups than the threads' and warps' shares of the scans over them, by offsets, and the same bits by a schedule."""
+    moe = gpu_lib
+    counts = ragged(G, most, G)
+    check_linear(moe, counts, N, K, fmt, "bf16", "fp32")
+    x = data((sum(counts), K), "bf16", 1)
+    c, s, _ = weight(moe, G, N, K, fmt, 2)
+    packed = moe.moe_fp4_pack_weight(c, s, K, fmt)
+    at = [0] + [int(v) for v in np.cumsum(counts)]
+    y = moe.moe_fp4_linear(x, torch.tensor(at, dtype=torch.int32, device="cuda"), packed, N, fmt)
+    z = moe.moe_fp4_linear(x, None, packed, N, fmt, G=G, tile_sched=tile_sched(list(zip(at, at[1:]))))
+    ok(moe)
+    assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_linear_of_many_groups_and_rows_used_many_times(gpu_lib, fmt):
+    counts = ragged(300, 40, 3)
+    src = torch.randint(-1, 600, (sum(counts),), generator=torch.Generator().manual_seed(3), dtype=torch.int32).cuda()
+    check_linear(gpu_lib, counts, 48, 1100, fmt, "bf16", src=src, x_rows=600)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_expert_ffn_of_many_experts(gpu_lib, fmt):
+    check_ffn(gpu_lib, ragged(200, 9, 4), 64, 96, fmt, "bf16", T=100)
+
+
 def test_linear_keeps_other_rows_and_columns(gpu_lib):
     moe = gpu_lib
     c, s, w = weight(moe, 2, 40, 64, "nv", 3)
