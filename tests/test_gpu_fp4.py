@@ -88,6 +88,23 @@ def test_quantize_with_any_multiplier(gpu_lib, fmt, dtype, g):
 
 
 @pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("g", [1e-40, -1e-39, 1e-30, 1e16, -3e38])
+def test_dequantize_with_a_multiplier_at_the_ends_of_the_range(gpu_lib, fmt, g):
+    """The quotient code * scale / g rounded to fp32, where 1 / g is infinite or below the normal range too: zeros stay 0."""
+    x = data((40, 96), "fp32", 5)
+    x[::3] = 0.0
+    x[1::3] *= 2.0**-60
+    c, s = gpu_lib.moe_fp4_quantize(x, fmt)
+    mult = torch.tensor([g], device="cuda")
+    y = gpu_lib.moe_fp4_dequantize(c, s, 96, fmt, gscale=mult, dtype=torch.float32)
+    ok(gpu_lib)
+    with np.errstate(over="ignore"):
+        want = np.float32(f64(gpu_lib.moe_fp4_dequantize(c, s, 96, fmt, dtype=torch.float32)) / float(mult))
+    assert (want[::3] == 0).all()
+    np.testing.assert_array_equal(y.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 def test_quantize_at_the_edges(gpu_lib, fmt, dtype):
     """Zeros, values at ties, the type's largest and smallest, infinities and NaN, each in blocks of their own."""

@@ -402,7 +402,7 @@ __device__ __forceinline__ void unit_values(uint2 c, uint32_t sb, bool scaled, f
     }
     if (!scaled) return;
     const float m = fabsf(s), a = fabsf(g);
-    if ((m < 1e15f && m > 1e-15f && a < 1e15f && a > 1e-15f) || m == 0.f) {
+    if (((m < 1e15f && m > 1e-15f) || m == 0.f) && a < 1e15f && a > 1e-15f) {
 #pragma unroll
         for (int j = 0; j < UNIT; j += 2) quotient2(v + j, g, r);
     } else {
