@@ -218,7 +218,8 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t* v) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
 }
 // Instruction descriptor of the block-scaled kinds: A and B e2m1 (bits 7-9 and 10-12 = 1), both K-major, N >> 3 at bits
-// 17-22, scale type at bit 23 (0: e4m3, 1: power of two), M >> 4 at bits 24-28, K = 64 (bit 31 = 0). Bits 4-5 and 29-30:
+// 17-22, scale type at bit 23 (0: e4m3, 1: power of two), M >> 4 at bits 24-28, K = 64 (bit 31 = 0; the chip's highest 4-bit
+// rate, six times the bf16 one, is that of K = 96, which is not used: loads do not keep up with K = 64). Bits 4-5 and 29-30:
 // which byte of a scale word is the step's first (0, and 2 for the second 64 columns of an MX piece).
 template <class F, int M, int N>
 __device__ constexpr uint32_t idesc_scaled(int sub) {
@@ -640,8 +641,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 // The one-SM kernel waits for its operands: a stage of four MMAs (N = 192) takes 385 cycles and needs 47 KB, and with 150 to
 // 190 KB under way some 55 bytes a cycle arrive. In a pair each SM holds its own 128 rows of A and half of the weight rows
 // (and the scales of all of them, which its tensor core needs): 38 KB for MMAs a third larger, and five stages of them.
-// 16384 skewed rows by 8 x 14336 x 4096 (NV): 456 us by single SMs, 343 by pairs with the quantisation of 41 in both; 300 of
-// the pairs' time at 6.2 PFLOP/s, the tensor pipe 62 % busy. The MMAs alone, without loads and epilogue, took 233.
+// 16384 skewed rows by 8 x 14336 x 4096 (NV): 456 us by single SMs, 343 by pairs with the quantisation of 41 in both (short
+// runs; in long ones, under the power cap, pairs take 375); 300 of the pairs' time at 6.4 PFLOP/s. The MMAs alone, without
+// loads and epilogue, took 233. (8192 rows by 4 x 12288 x 4096: 6.2 PFLOP/s, the tensor pipe 64 % busy.)
 // The even CTA issues the MMAs for both. Every copy of a CTA completes on its own barrier; the odd CTA's scale warps, which
 // wait for it, pass the news on with their arrival on the even CTA's scale barrier, so that barrier tells of both CTAs'
 // operands. A pair takes two consecutive tiles of one group; where the second does not exist the odd CTA computes the
@@ -1079,7 +1081,9 @@ using Narrow = Cfg<64, 7>;
 // 192 columns; a pair 560), and its bytes about one cycle for each 55, a tile's start and end 2000. The host does not know
 // the groups' sizes: a group is taken to end in the middle of a tile. With few rows a call is bound by the weights' bytes,
 // and a narrow tile moves too few of them a stage: one token through 8 of 32 experts of 7168 x 2048, gate and up, 36 us with
-// 64 columns and 26 with 128; 8192 rows by 8 x 4096 x 12288 (MX), 225 us with 192 columns and 185 by pairs.
+// 64 columns and 26 with 128; 8192 rows by 8 x 4096 x 12288 (MX), 225 us with 192 columns and 185 by pairs. Pairs are left out
+// below 128 rows a group on average, where most groups fill half a pair: with them at 127 rows by 128 x 1536 x 2048 (NV)
+// 70 -> 76 us, by 32 x 4096 x 4096 70 -> 75; six groups of 2500 and 122 of 8, which the average leaves out too, 91 either way.
 template <class F, int EPI>
 static int product(const void* a_codes, long long rows, int G, int K, const Params& p, cudaStream_t s) {
     MOE_REQUIRE((long long)sched_max_tiles(rows, G) * p.NB64 < (1LL << 31), MOE_ERR_INVALID_ARG,

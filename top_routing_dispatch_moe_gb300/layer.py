@@ -35,7 +35,8 @@ class MoELayer:
     rows and the activations inside the FFN (fp4_gscale, fp4_act_gscale: fp32 scalar tensors that they are multiplied with
     before, e.g. calibrated to 448 * 6 / the largest magnitude expected; None: 1; copied at construction, where their
     inverses go into the experts' factors: another calibration is another layer). The FFN reads x through the dispatch's
-    row indices; both products and the quantisations between them are the stage "up_gate", and "down" is empty."""
+    row indices (the send buffer is written all the same); both products and the quantisations between them are the stage
+    "up_gate", and "down" is empty."""
 
     STAGES = ("router", "dispatch", "up_gate", "down", "shared_up_gate", "shared_down", "combine")
 
@@ -158,7 +159,7 @@ class MoELayer:
         return moe.moe_fp4_pack_expert_weights(*quantised, gate.shape[2], gate.shape[1], self.fp4), alphas
 
     def _ffn_fp4(self, x, packed, out, stream, **rows):
-        moe.moe_fp4_expert_ffn(x, rows.pop("offsets", None), packed[0], self.F, self.fp4, alpha_gate=packed[1][0],
+        moe.moe_fp4_expert_ffn(x, None, packed[0], self.F, self.fp4, alpha_gate=packed[1][0],
                                alpha_up=packed[1][1], alpha_down=packed[1][2], gscale=self.fp4_gscale,
                                act_gscale=self.fp4_act_gscale, out=out, ws=self.fp4_ws, stream=stream, **rows)
 
