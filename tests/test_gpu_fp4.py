@@ -281,6 +281,27 @@ def test_linear_keeps_other_rows_and_columns(gpu_lib):
         assert (np.abs(f64(full[lo:hi, 3:43]) - want) <= Q.product_bound(a[lo:hi], w[g], want, 2.0**-8)).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("N,ldo", [(45, 48), (1, 8), (37, 40), (75, 80), (97, 104), (127, 128), (2045, 2048), (1990, 2000)])
+@pytest.mark.parametrize("rows", [200, 2600])
+def test_linear_writes_its_columns_alone(gpu_lib, dtype, N, ldo, rows):
+    """Outputs of any width in rows that start on 16 bytes, one SM and pairs of SMs to a tile: the columns beside them stay."""
+    moe = gpu_lib
+    c, s, w = weight(moe, 2, N, 192, "mx", 3)
+    packed = moe.moe_fp4_pack_weight(c, s, 192, "mx")
+    x = data((rows, 192), "bf16", 4)
+    full = torch.full((rows, ldo), 5.0, dtype=DT[dtype], device="cuda")
+    off = torch.tensor([0, rows - 130, rows], dtype=torch.int32, device="cuda")
+    moe.moe_fp4_linear(x, off, packed, N, "mx", out=full[:, :N])
+    ok(moe)
+    assert (full[:, N:] == 5).all()
+    a = Q.dequantize(*Q.quantize(f64(x), "mx"), "mx")
+    for g, lo, hi in ((0, 0, rows - 130), (1, rows - 130, rows)):
+        want = a[lo:hi] @ w[g].T
+        bound = Q.product_bound(a[lo:hi], w[g], want, HALF_STEP[dtype]) + (2.0**-25 if dtype == "fp16" else 0.0)
+        assert (np.abs(f64(full[lo:hi, :N]) - want) <= bound).all()
+
+
 @pytest.mark.parametrize("off", [[0, 5, 3, 20], [-1, 5, 6, 20], [0, 5, 6, 21]])
 def test_bad_offsets_are_reported_and_nothing_is_written(gpu_lib, off):
     moe = gpu_lib

@@ -227,16 +227,16 @@ __device__ constexpr uint32_t idesc_scaled(int sub) {
            ((uint32_t)(M >> 4) << 24) | ((uint32_t)(2 * sub) << 4) | ((uint32_t)(2 * sub) << 29);
 }
 
-// 32 consecutive columns of an output row that starts on 16 bytes, in its type.
+// W consecutive columns of an output row that starts on 16 bytes, in its type, as far as its n columns go.
 template <typename T> __device__ __forceinline__ T out_round(float v);
 template <> __device__ __forceinline__ float out_round<float>(float v) { return v; }
 template <> __device__ __forceinline__ __half out_round<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 out_round<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <typename T>
+template <int W, typename T>
 __device__ __forceinline__ void store_row(T* dst, const float* v, float al, int n) {
     constexpr int PER = 16 / sizeof(T);
 #pragma unroll
-    for (int c = 0; c < 32; c += PER) {
+    for (int c = 0; c < W; c += PER) {
         alignas(16) T o[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) o[i] = out_round<T>(v[c + i] * al);
@@ -273,12 +273,17 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t stg, 
         bulk_commit();
     }
 }
+// The chunk's columns by boxes, and what is left for a last box by the lanes themselves: boxes that the map cut at 45 fp16
+// columns, in rows of 48, wrote the column after them too.
 template <typename T>
-__device__ __forceinline__ void store_boxes(const CUtensorMap* map, uint32_t stg, const float* v, float al, int col, int n, int row0) {
+__device__ __forceinline__ void store_boxes(const CUtensorMap* map, uint32_t stg, const float* v, float al, int col, int n, int row0,
+                                            T* out, long long ldo) {
     constexpr int COLS = 64 / sizeof(T);
 #pragma unroll
-    for (int c = 0; c < 64; c += COLS)
-        if (c < n) store_box<T>(map, stg, v + c, al, col + c, row0);
+    for (int c = 0; c < 64; c += COLS) {
+        if (c + COLS <= n) store_box<T>(map, stg, v + c, al, col + c, row0);
+        else if (c < n) store_row<COLS>(out + (row0 + (int)(threadIdx.x & 31)) * ldo + col + c, v + c, al, n - c);
+    }
 }
 
 // Rows that start on no boundary: 64 bytes of each of the warp's 32 rows at a time through the staging buffer, from where the
@@ -394,11 +399,11 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const CUtensorMa
         const float al = p.alpha ? __ldg(p.alpha + wk.g) : 1.f;
         const int n = p.N - c0;
         if (n <= 0) return;
-        if (p.boxed && wk.row0 + (r & ~31) + 31 < wk.row1) {     // all of the warp's rows (the map drops columns past N)
+        if (p.boxed && wk.row0 + (r & ~31) + 31 < wk.row1) {     // all of the warp's rows
             const int base = wk.row0 + (r & ~31);
-            if (p.out_dtype == MOE_F32) store_boxes<float>(map, stg, v, al, c0, n, base);
-            else if (p.out_dtype == MOE_BF16) store_boxes<__nv_bfloat16>(map, stg, v, al, c0, n, base);
-            else store_boxes<__half>(map, stg, v, al, c0, n, base);
+            if (p.out_dtype == MOE_F32) store_boxes(map, stg, v, al, c0, n, base, static_cast<float*>(p.out), p.ldo);
+            else if (p.out_dtype == MOE_BF16) store_boxes(map, stg, v, al, c0, n, base, static_cast<__nv_bfloat16*>(p.out), p.ldo);
+            else store_boxes(map, stg, v, al, c0, n, base, static_cast<__half*>(p.out), p.ldo);
             return;
         }
         if (!p.vec) {
@@ -414,10 +419,10 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const CUtensorMa
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (n - 32 * h <= 0) break;
-            if (p.out_dtype == MOE_F32) store_row(reinterpret_cast<float*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
+            if (p.out_dtype == MOE_F32) store_row<32>(reinterpret_cast<float*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
             else if (p.out_dtype == MOE_BF16)
-                store_row(reinterpret_cast<__nv_bfloat16*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
-            else store_row(reinterpret_cast<__half*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
+                store_row<32>(reinterpret_cast<__nv_bfloat16*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
+            else store_row<32>(reinterpret_cast<__half*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
         }
     }
 }
