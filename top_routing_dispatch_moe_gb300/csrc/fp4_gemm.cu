@@ -227,16 +227,16 @@ __device__ constexpr uint32_t idesc_scaled(int sub) {
            ((uint32_t)(M >> 4) << 24) | ((uint32_t)(2 * sub) << 4) | ((uint32_t)(2 * sub) << 29);
 }
 
-// W consecutive columns of an output row that starts on 16 bytes, in its type, as far as its n columns go.
+// 32 consecutive columns of an output row that starts on 16 bytes, in its type.
 template <typename T> __device__ __forceinline__ T out_round(float v);
 template <> __device__ __forceinline__ float out_round<float>(float v) { return v; }
 template <> __device__ __forceinline__ __half out_round<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 out_round<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <int W, typename T>
+template <typename T>
 __device__ __forceinline__ void store_row(T* dst, const float* v, float al, int n) {
     constexpr int PER = 16 / sizeof(T);
 #pragma unroll
-    for (int c = 0; c < W; c += PER) {
+    for (int c = 0; c < 32; c += PER) {
         alignas(16) T o[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) o[i] = out_round<T>(v[c + i] * al);
@@ -273,17 +273,12 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t stg, 
         bulk_commit();
     }
 }
-// The chunk's columns by boxes, and what is left for a last box by the lanes themselves: boxes that the map cut at 45 fp16
-// columns, in rows of 48, wrote the column after them too.
 template <typename T>
-__device__ __forceinline__ void store_boxes(const CUtensorMap* map, uint32_t stg, const float* v, float al, int col, int n, int row0,
-                                            T* out, long long ldo) {
+__device__ __forceinline__ void store_boxes(const CUtensorMap* map, uint32_t stg, const float* v, float al, int col, int n, int row0) {
     constexpr int COLS = 64 / sizeof(T);
 #pragma unroll
-    for (int c = 0; c < 64; c += COLS) {
-        if (c + COLS <= n) store_box<T>(map, stg, v + c, al, col + c, row0);
-        else if (c < n) store_row<COLS>(out + (row0 + (int)(threadIdx.x & 31)) * ldo + col + c, v + c, al, n - c);
-    }
+    for (int c = 0; c < 64; c += COLS)
+        if (c < n) store_box<T>(map, stg, v + c, al, col + c, row0);
 }
 
 // Rows that start on no boundary: 64 bytes of each of the warp's 32 rows at a time through the staging buffer, from where the
@@ -399,11 +394,11 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const CUtensorMa
         const float al = p.alpha ? __ldg(p.alpha + wk.g) : 1.f;
         const int n = p.N - c0;
         if (n <= 0) return;
-        if (p.boxed && wk.row0 + (r & ~31) + 31 < wk.row1) {     // all of the warp's rows
+        if (p.boxed && wk.row0 + (r & ~31) + 31 < wk.row1) {     // all of the warp's rows (the map drops columns past N)
             const int base = wk.row0 + (r & ~31);
-            if (p.out_dtype == MOE_F32) store_boxes(map, stg, v, al, c0, n, base, static_cast<float*>(p.out), p.ldo);
-            else if (p.out_dtype == MOE_BF16) store_boxes(map, stg, v, al, c0, n, base, static_cast<__nv_bfloat16*>(p.out), p.ldo);
-            else store_boxes(map, stg, v, al, c0, n, base, static_cast<__half*>(p.out), p.ldo);
+            if (p.out_dtype == MOE_F32) store_boxes<float>(map, stg, v, al, c0, n, base);
+            else if (p.out_dtype == MOE_BF16) store_boxes<__nv_bfloat16>(map, stg, v, al, c0, n, base);
+            else store_boxes<__half>(map, stg, v, al, c0, n, base);
             return;
         }
         if (!p.vec) {
@@ -419,10 +414,10 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const CUtensorMa
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (n - 32 * h <= 0) break;
-            if (p.out_dtype == MOE_F32) store_row<32>(reinterpret_cast<float*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
+            if (p.out_dtype == MOE_F32) store_row(reinterpret_cast<float*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
             else if (p.out_dtype == MOE_BF16)
-                store_row<32>(reinterpret_cast<__nv_bfloat16*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
-            else store_row<32>(reinterpret_cast<__half*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
+                store_row(reinterpret_cast<__nv_bfloat16*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
+            else store_row(reinterpret_cast<__half*>(dst) + 32 * h, v + 32 * h, al, n - 32 * h);
         }
     }
 }
@@ -1020,7 +1015,8 @@ static int make_maps(const void* a_codes, long long rows, int K, Params& p, CUte
     if (EPI == EPI_OUT) {
         const int el = p.out_dtype == MOE_F32 ? 4 : 2;
         p.vec = aligned16(p.out) && (long long)p.ldo * el % 16 == 0;
-        p.boxed = p.vec && rows >= 32;
+        // (a box that its map cuts is written in whole 16-byte pieces: 45 fp32 columns in rows of 48 came with three zeros)
+        p.boxed = p.vec && rows >= 32 && (long long)p.N * el % 16 == 0;
         if (p.boxed)
             if (int rc = out_map(mo, p.out, rows, p.N, p.ldo, p.out_dtype)) return rc;
     }
