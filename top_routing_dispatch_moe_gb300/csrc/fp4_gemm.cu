@@ -360,14 +360,20 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const CUtensorMa
             }
         } else {
             // a gate far from 0, infinite or NaN among the 32: exp(-g) would overflow, and the correction of an infinite
-            // quotient is NaN. As g exp(-|g|) / (1 + exp(-|g|)), without the numerator's exponential from 0 on.
+            // quotient is NaN. As g exp(-|g|) / (1 + exp(-|g|)), without the numerator's exponential from 0 on. (Rolled, through local
+            // memory: unrolled, the code that hardly runs cost the FFN of 16384 tokens and 128 experts 383 -> 388 us.)
+            float x[32];
 #pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = v[i];
+#pragma unroll 1
             for (int i = 0; i < 32; ++i) {
-                const float e = expf(-fabsf(v[i]));
+                const float e = expf(-fabsf(x[i]));
                 float r;
                 asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-                v[i] = (v[i] < 0.f ? v[i] * e : v[i]) * r;
+                x[i] = (x[i] < 0.f ? x[i] * e : x[i]) * r;
             }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = x[i];
         }
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
