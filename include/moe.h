@@ -442,8 +442,9 @@ int moe_dequant_fp8(const uint8_t* buf8, const float* scales, int rows, int h, v
  *   its block's scale NaN (0x7F, 0xFF) and its codes 0. A negative value whose code is 0 may keep its sign bit (code 8,
  *   which stands for 0 too). A partial last block counts its missing columns as 0.
  *   dtype / out_dtype: MOE_F32, MOE_BF16 or MOE_F16. x and out may have row strides (ldx, ldo, in elements) and need be
- *   aligned to their type only; rows that start on 16 bytes are the fast case. Sizes: 1 <= K, N, F <= MOE_FP4_MAX_K,
- *   rows <= MOE_FP4_MAX_ROWS, 1 <= groups <= 1024. src: x's row of each row, -1 for a row of zeros, or NULL (row r of x).
+ *   aligned to their type only; rows that start on 16 bytes, and outputs as wide as whole 16-byte pieces, are the fast case.
+ *   Sizes: 1 <= K, N, F <= MOE_FP4_MAX_K, rows <= MOE_FP4_MAX_ROWS, 1 <= groups <= 1024. src: x's row of each row, -1 for
+ *   a row of zeros, or NULL (row r of x).
  *
  * moe_fp4_quantize: x [x_rows, K] -> codes [rows, moe_fp4_codes_pitch(K)] (codes past K are 0) and scales
  *   [rows, moe_fp4_scales_pitch(K, fmt)], as checkpoints hold them. moe_fp4_dequantize: code * scale (/ gscale[0]) in fp32,

@@ -400,7 +400,7 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const CUtensorMa
         const float al = p.alpha ? __ldg(p.alpha + wk.g) : 1.f;
         const int n = p.N - c0;
         if (n <= 0) return;
-        if (p.boxed && wk.row0 + (r & ~31) + 31 < wk.row1) {     // all of the warp's rows (the map drops columns past N)
+        if (p.boxed && wk.row0 + (r & ~31) + 31 < wk.row1) {     // all of the warp's rows (the map drops pieces past N)
             const int base = wk.row0 + (r & ~31);
             if (p.out_dtype == MOE_F32) store_boxes<float>(map, stg, v, al, c0, n, base);
             else if (p.out_dtype == MOE_BF16) store_boxes<__nv_bfloat16>(map, stg, v, al, c0, n, base);
