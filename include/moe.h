@@ -115,6 +115,40 @@ int moe_router_from_logits(const float* logits, const float* bias, int T, int E,
                            int32_t* topk_ids, float* gates, int32_t* counts, float* f, float* P, float* aux,
                            void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------------------
+ * Routing by groups of experts ("v6 长序列和 MoE ...", "Load balancing loss" bullet: a bias that takes part in the choice alone;
+ * "专家并行" (formulaic), section on node-limited routing: a token's experts come from a limited number of groups, so that it
+ * travels to a limited number of places).
+ *   s = sigmoid(L) or softmax(L) (`score`); sel_e = s_e + bias_e, -1e30 where L_e is -inf (a masked expert) or NaN.
+ *   The E experts form `groups` groups of equal size, consecutive; a group's score is the sum of its `best` (1 or 2) largest
+ *   sel; the top_groups groups with the largest scores stay, and topk_ids are the k experts of those with the largest sel,
+ *   by falling sel. Equal scores: lower index. The choice is that of exact scores, not of rounded ones: what 32 bits cannot
+ *   tell apart is compared in 64; without a bias the experts are ranked by their logits.
+ *   gates[t,j] = scale * s, with renorm scale * s / (sum of the chosen s), 0 where that sum is 0 (all masked).
+ *   counts, f, aux as moe_router; P the mean of softmax(L), or of s_e / sum s (0 for a token whose experts are all masked).
+ *   Under softmax, a NaN or +inf logit makes its token's gates and P NaN.
+ * moe_group_route: on given fp32 logits [T,E]. moe_group_router: from x [T,h] and the packed router weight
+ *   (moe_pack_router_weight), the logits as moe_router_packed computes them, without a bias in them; logits [T,E] may be NULL.
+ * moe_group_route_backward: d_logits [T,E] fp32 from d_gates [T,k] and d_aux, the choice held fixed (the bias gets none):
+ *     ds_j = scale d_g_j, with renorm scale (d_g_j - sum_i d_g_i s_i / S) / S, S = sum_i s_i (0 where S is 0)
+ *     c_e = d_aux alpha E f_e / T;  softmax: dp = ds + c, d_logits = p (dp - <dp, p>);
+ *     sigmoid: d_logits = (ds + (c - <c, q>) / sum s) s (1 - s), q = s / sum s.
+ *   An id outside [0, E) counts as none and is reported by moe_check_device_error.
+ *   Sizes: T >= 0, E <= 1024, groups <= 32 dividing E, best <= E / groups, 1 <= k <= min(16, top_groups E / groups), scale
+ *   finite. Deterministic. Workspaces 16-byte aligned.
+ * ------------------------------------------------------------------------------------------------- */
+enum moe_score { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
+size_t moe_group_route_workspace_size(int T, int E);
+int moe_group_route(const float* logits, const float* bias, int T, int E, int k, int groups, int top_groups, int score, int best,
+                    int renorm, float scale, float alpha, int32_t* topk_ids, float* gates, int32_t* counts, float* f, float* P,
+                    float* aux, void* ws, size_t ws_bytes, void* stream);
+size_t moe_group_router_workspace_size(int T, int h, int E, int dtype);
+int moe_group_router(const void* x, const void* w_packed, const float* bias, int T, int h, int E, int k, int dtype, int groups,
+                     int top_groups, int score, int best, int renorm, float scale, float alpha, float* logits, int32_t* topk_ids,
+                     float* gates, int32_t* counts, float* f, float* P, float* aux, void* ws, size_t ws_bytes, void* stream);
+int moe_group_route_backward(const float* logits, const int32_t* topk_ids, const float* d_gates, const float* f, int T, int E,
+                             int k, int score, int renorm, float scale, float alpha, float d_aux, float* d_logits, void* stream);
+
 /* moe_sinkhorn_bias: Sinkhorn routing ("Megatron-LM ... （六）", section "Router": Sinkhorn iterations make the
  * routing matrix doubly stochastic, balancing the experts without an aux loss). On K = exp(L - rowmax) [T,E]
  * and starting from row scalings r = 1, n_iter times: c_e = (T/E) / sum_t K[t,e] r_t, then

@@ -6,94 +6,20 @@
 // rows are narrower.
 #include <algorithm>
 #include "fp4.cuh"
+#include "quant_io.cuh"
 
 namespace moe {
 namespace fp4 {
 
 constexpr int QTHREADS = 256;
 constexpr int QWARPS = QTHREADS / 32;
-constexpr int UNIT = 16;             // columns per lane
 constexpr int SEG = 32 * UNIT;       // columns per warp
-
-__device__ __forceinline__ float as_f32(float v) { return v; }
-__device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float as_f32(__half v) { return __half2float(v); }
-template <typename T> __device__ __forceinline__ T rounded(float v);
-template <> __device__ __forceinline__ float rounded<float>(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
 
 // (The kernels that run as programmatic dependents read what the kernel before them may have written by plain loads through
 // pointers without __restrict__, which the compiler does not move ahead of the wait.)
 
 // Units whose loads a lane keeps in flight: with four blocks of 256 threads an SM has 64 KB under way.
 template <typename T> constexpr int IN_FLIGHT = 4 / (int)sizeof(T);
-// 16 elements as they lie in memory.
-template <typename T> struct alignas(16) Raw16 { uint4 q[sizeof(T)]; };
-
-// 32 bytes at an address on 32, for the 64 bytes of an fp32 unit: one request for a whole sector, where requests of 16 bytes
-// 64 apart touch each sector twice (12288 x 4096 fp32 there and back 97 -> 81 us; 16-bit types measured no faster).
-__device__ __forceinline__ void ld32(uint4* d, const void* p) {
-    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(d[0].x), "=r"(d[0].y), "=r"(d[0].z), "=r"(d[0].w), "=r"(d[1].x), "=r"(d[1].y), "=r"(d[1].z), "=r"(d[1].w)
-                 : "l"(p));
-}
-__device__ __forceinline__ void st32(void* p, const uint4* d) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                 ::"l"(p), "r"(d[0].x), "r"(d[0].y), "r"(d[0].z), "r"(d[0].w), "r"(d[1].x), "r"(d[1].y), "r"(d[1].z), "r"(d[1].w)
-                 : "memory");
-}
-
-// Columns [k0, k0 + 16) of a row as stored, zero past K. VEC: the row starts on 16 bytes. The caller's lanes of one warp
-// hold consecutive units of the same row in the other case too, where the elements are fetched one by one.
-template <typename T, bool VEC>
-__device__ __forceinline__ Raw16<T> load_unit(const T* row, int k0, int K) {
-    Raw16<T> r;
-    if (VEC && k0 + UNIT <= K) {
-        if (sizeof(T) == 4 && (reinterpret_cast<uintptr_t>(row) & 31u) == 0) {
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T); i += 2) ld32(r.q + i, reinterpret_cast<const uint4*>(row + k0) + i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T); ++i) r.q[i] = __ldcs(reinterpret_cast<const uint4*>(row + k0) + i);
-        }
-        return r;
-    }
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T); ++i) r.q[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (k0 < K) {
-        T* e = reinterpret_cast<T*>(r.q);
-#pragma unroll
-        for (int i = 0; i < UNIT; ++i)
-            if (k0 + i < K) e[i] = row[k0 + i];
-    }
-    return r;
-}
-
-// The largest magnitude of a unit, NaN if an element is one; 16-bit types two at a time.
-__device__ __forceinline__ float unit_amax(const Raw16<float>& raw) {
-    const float* e = reinterpret_cast<const float*>(raw.q);
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < UNIT; ++i) m = max_nan(m, fabsf(e[i]));
-    return m;
-}
-__device__ __forceinline__ float unit_amax(const Raw16<__nv_bfloat16>& raw) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(raw.q);
-    uint32_t m = w[0];
-#pragma unroll
-    for (int i = 1; i < UNIT / 2; ++i) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
-    return max_nan(fabsf(__uint_as_float(m << 16)), fabsf(__uint_as_float(m & 0xFFFF0000u)));
-}
-__device__ __forceinline__ float unit_amax(const Raw16<__half>& raw) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(raw.q);
-    uint32_t m = w[0];
-#pragma unroll
-    for (int i = 1; i < UNIT / 2; ++i) asm("max.NaN.xorsign.abs.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
-    return max_nan(fabsf(f.x), fabsf(f.y));
-}
-
 // The codes (2 words) and the scale byte of this lane's unit; an MX block spans lanes 2i and 2i + 1. (max |x g| is
 // max |x| times |g|: rounding keeps the order.)
 template <class F, typename T>
@@ -114,25 +40,6 @@ __device__ __forceinline__ uint2 quantize_unit(const Raw16<T>& raw, bool scaled,
     block_codes<F, UNIT>(v, amax, s, r, w);
     return make_uint2(w[0], w[1]);
 }
-
-// Items of the row-major kernels, `step` apart, as (row group, segment) without a division each.
-struct Walk {
-    int row, seg, drow, dseg, nseg;
-    long long left;                      // items still to come, this one included, in steps
-    __device__ __forceinline__ Walk(long long first, long long step, long long items, int nseg_) : nseg(nseg_) {
-        left = first < items ? (items - first + step - 1) / step : 0;
-        row = (int)(first / nseg);
-        seg = (int)(first - (long long)row * nseg);
-        drow = (int)(step / nseg);
-        dseg = (int)(step - (long long)drow * nseg);
-    }
-    __device__ __forceinline__ void next() {
-        --left;
-        row += drow;
-        seg += dseg;
-        if (seg >= nseg) { seg -= nseg; ++row; }
-    }
-};
 
 // The schedule of the groups, by one block.
 __device__ __noinline__ void write_schedule(const int32_t* offsets, int G, int rows, int32_t* sched, unsigned* err) {

@@ -9,6 +9,7 @@
 
 #include <cuda_fp16.h>
 #include "common.cuh"
+#include "quant_io.cuh"
 
 namespace moe {
 namespace fp4 {
@@ -66,12 +67,6 @@ inline size_t operand_sf_bytes(long long rows, int G, int K, int fmt) {
 }
 
 #ifdef __CUDACC__
-// NaN if either is: a NaN has to reach its block's scale.
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
 // Eight values -> eight codes, to nearest, ties to even, held at +-6.
 __device__ __forceinline__ uint32_t e2m1x8(const float* v) {
     uint32_t r;
@@ -116,25 +111,6 @@ __device__ __forceinline__ uint32_t block_scale(float amax, float& s, float& r) 
     }
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ void mul2(float* d, const float* a, float b) {
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d[0]), "=f"(d[1]) : "f"(a[0]), "f"(a[1]), "f"(b));
-}
-__device__ __forceinline__ void mul2v(float* d, const float* a, const float* b) {
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d[0]), "=f"(d[1]) : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
-}
-__device__ __forceinline__ void fma2(float* d, const float* a, float b, const float* c) {
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %6};\n\t"
-        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d[0]), "=f"(d[1]) : "f"(a[0]), "f"(a[1]), "f"(b), "f"(c[0]), "f"(c[1]));
-}
-__device__ __forceinline__ void fma2v(float* d, const float* a, const float* b, const float* c) {
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d[0]), "=f"(d[1]) : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]), "f"(c[0]), "f"(c[1]));
-}
 // The rounded quotients v / s of two values, given the rounded reciprocal r of s: q = v r is off by less than two units in
 // its last place, and q + (v - q s) r is the rounded quotient (Markstein's correction: v - q s is exact in one fused step,
 // and r has no error beyond its own rounding), as long as neither product leaves the normal range.

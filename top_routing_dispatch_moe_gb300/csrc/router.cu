@@ -17,6 +17,8 @@
 #include <algorithm>
 #include "common.cuh"
 #include "ffn.cuh"
+#include "group_router.cuh"
+#include "router.cuh"
 
 namespace moe {
 
@@ -868,7 +870,15 @@ struct RouterWs {
 };
 
 // Blocks of the finalize: one per kFinExperts experts when gating blocks zeroed its arrival counter (T > 0).
-static int finalize_grid(int T, int E) { return T > 0 ? cdiv(E, kFinExperts) : 1; }
+int finalize_grid(int T, int E) { return T > 0 ? cdiv(E, kFinExperts) : 1; }
+
+int launch_router_finalize(const float* partial_P, const int32_t* partial_C, int G, int T, int E, int k, float alpha,
+                           int32_t* counts, float* f, float* P, float* aux, float* term_part, unsigned* ticket,
+                           cudaStream_t s) {
+    const cudaError_t le = launch_pdl(router_finalize, dim3(finalize_grid(T, E)), dim3(kFinThreads), 0, s, partial_P,
+                                      partial_C, T > 0 ? G : 0, T, E, k, alpha, counts, f, P, aux, term_part, ticket);
+    return check_launch(le, "router_finalize");
+}
 
 static RouterWs router_ws_layout(void* ws, int T, int h, int E, int el, bool small, bool need_logits, bool tc,
                                  int split) {
@@ -892,6 +902,32 @@ static RouterWs router_ws_layout(void* ws, int T, int h, int E, int el, bool sma
     if (split > 1) { w.parts = reinterpret_cast<float*>(base + off); off = align_up(off + (size_t)split * T * E * 4, 256); }
     w.bytes = off;
     return w;
+}
+
+// The logits of E > 32 (or a weight past the fused kernels' shared memory) into lg: [T][E], with lbias added; split (sp.S > 1):
+// the parts, without it.
+static int launch_logits(const void* x, const void* w_r, const void* w_rT, const float* lbias, int T, int h, int E, int dtype,
+                         bool tc, const RouterSplit& sp, const RouterWs& w, float* lg, cudaStream_t s) {
+    if (tc) {
+        const void* wt = w_rT;
+        if (!wt) {                           // not packed: transpose into the workspace on every call
+            router_transpose_kernel<__nv_bfloat16><<<dim3(cdiv(E, 32), cdiv(h, 32)), dim3(32, 8), 0, s>>>(
+                static_cast<const __nv_bfloat16*>(w_r), h, E, static_cast<__nv_bfloat16*>(w.w_rT));
+            if (int rc = check_launch("router_transpose_kernel")) return rc;
+            wt = w.w_rT;
+        }
+        if (sp.S > 1) return tc_gemm_f32_splitk(x, T, h, 0, wt, E, h, 0, h, sp.S, sp.kchunk, lg, s);
+        if (int rc = launch_dense_sched(T, w.sched, s)) return rc;
+        return tc_router_logits(x, wt, lbias, T, h, E, w.sched, lg, s);
+    }
+    dim3 grid(cdiv(E, 64), cdiv(T, 64));
+    if (dtype == MOE_BF16)
+        router_logits_gemm<__nv_bfloat16><<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x),
+            static_cast<const __nv_bfloat16*>(w_r ? w_r : w_rT), lbias, T, h, E, lg, w_r ? 0 : 1);
+    else
+        router_logits_gemm<float><<<grid, 256, 0, s>>>(static_cast<const float*>(x), static_cast<const float*>(w_r), lbias, T,
+                                                       h, E, lg, 0);
+    return check_launch("router_logits_gemm");
 }
 
 }  // namespace moe
@@ -966,30 +1002,7 @@ static int router_run(const void* x, const void* w_r, const void* w_rT, const fl
         } else {
             float* lg = sp.S > 1 ? w.parts : logits ? logits : w.logits;
             const float* lbias = bias_in_logits(gating) ? bias : nullptr;
-            if (tc) {
-                const void* wt = w_rT;
-                if (!wt) {                           // not packed: transpose into the workspace on every call
-                    router_transpose_kernel<__nv_bfloat16><<<dim3(cdiv(E, 32), cdiv(h, 32)), dim3(32, 8), 0, s>>>(
-                        static_cast<const __nv_bfloat16*>(w_r), h, E, static_cast<__nv_bfloat16*>(w.w_rT));
-                    if (int rc = check_launch("router_transpose_kernel")) return rc;
-                    wt = w.w_rT;
-                }
-                if (sp.S > 1) {
-                    if (int rc = tc_gemm_f32_splitk(x, T, h, 0, wt, E, h, 0, h, sp.S, sp.kchunk, lg, s)) return rc;
-                } else {
-                    if (int rc = launch_dense_sched(T, w.sched, s)) return rc;
-                    if (int rc = tc_router_logits(x, wt, lbias, T, h, E, w.sched, lg, s)) return rc;
-                }
-            } else {
-                dim3 grid(cdiv(E, 64), cdiv(T, 64));
-                if (dtype == MOE_BF16)
-                    router_logits_gemm<__nv_bfloat16><<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x),
-                        static_cast<const __nv_bfloat16*>(w_r ? w_r : w_rT), lbias, T, h, E, lg, w_r ? 0 : 1);
-                else
-                    router_logits_gemm<float><<<grid, 256, 0, s>>>(static_cast<const float*>(x),
-                        static_cast<const float*>(w_r), lbias, T, h, E, lg, 0);
-                if (int rc = check_launch("router_logits_gemm")) return rc;
-            }
+            if (int rc = launch_logits(x, w_r, w_rT, lbias, T, h, E, dtype, tc, sp, w, lg, s)) return rc;
             const size_t smem = (size_t)kRouterWarps * E * sizeof(float) + (size_t)E * sizeof(int);
             const int npl = cdiv(E, 32);
             // unsplit: the GEMM wrote the final logits (bias included); split: the gate adds the parts and the bias
@@ -1009,10 +1022,7 @@ static int router_run(const void* x, const void* w_r, const void* w_rT, const fl
             if (int rc = check_launch("router_gate_kernel")) return rc;
         }
     }
-    const cudaError_t le = launch_pdl(router_finalize, dim3(finalize_grid(T, E)), dim3(kFinThreads), 0, s,
-                                      (const float*)w.partial_P, (const int32_t*)w.partial_C, T > 0 ? G : 0, T, E, k,
-                                      alpha, counts, f, P, aux, w.term_part, w.ticket);
-    return check_launch(le, "router_finalize");
+    return launch_router_finalize(w.partial_P, w.partial_C, G, T, E, k, alpha, counts, f, P, aux, w.term_part, w.ticket, s);
 }
 
 extern "C" int moe_router(const void* x, const void* w_r, const float* bias, int T, int h, int E, int k, int dtype,
@@ -1091,8 +1101,77 @@ extern "C" int moe_router_from_logits(const float* logits, const float* bias, in
 #undef MOE_GATE_LAUNCH2
         if (int rc = check_launch("router_gate_kernel")) return rc;
     }
-    const cudaError_t le = launch_pdl(router_finalize, dim3(finalize_grid(T, E)), dim3(kFinThreads), 0, s,
-                                      (const float*)o.partial_P, (const int32_t*)o.partial_C, T > 0 ? G : 0, T, E, k,
-                                      alpha, counts, f, P, aux, w.term_part, w.ticket);
-    return check_launch(le, "router_finalize");
+    return launch_router_finalize(o.partial_P, o.partial_C, G, T, E, k, alpha, counts, f, P, aux, w.term_part, w.ticket, s);
+}
+
+// The workspace: the logits where the caller wants none, the logits step's own (with E <= 32 the fused router's outputs, of
+// which only the logits are wanted), the gating's.
+struct GroupRouterWs { float* logits; char* router; int32_t* ids; float* gates; int32_t* counts; float* f; char* gate; size_t bytes; };
+static GroupRouterWs group_router_ws(void* ws, int T, int h, int E, int dtype) {
+    GroupRouterWs w{};
+    const bool small = use_small_path(h, E, dtype == MOE_F32 ? 4 : 2);
+    char* base = static_cast<char*>(ws);
+    size_t off = 0;
+    w.logits = reinterpret_cast<float*>(base + off); off = align_up(off + (size_t)T * E * 4, 256);
+    w.router = base + off; off = align_up(off + moe_router_workspace_size(T, h, E, 1, dtype), 256);
+    if (small) {
+        w.ids = reinterpret_cast<int32_t*>(base + off); off = align_up(off + (size_t)T * 4, 256);
+        w.gates = reinterpret_cast<float*>(base + off); off = align_up(off + (size_t)T * 4, 256);
+        w.counts = reinterpret_cast<int32_t*>(base + off); off = align_up(off + (size_t)E * 4, 256);
+        w.f = reinterpret_cast<float*>(base + off); off = align_up(off + (size_t)(2 * E + 1) * 4, 256);
+    }
+    w.gate = base + off;
+    w.bytes = off + group_gate_ws_bytes(T, E);
+    return w;
+}
+
+extern "C" size_t moe_group_router_workspace_size(int T, int h, int E, int dtype) {
+    if (T < 0 || h <= 0 || E <= 0) return 0;
+    return group_router_ws(nullptr, T, h, E, dtype).bytes;
+}
+
+extern "C" int moe_group_router(const void* x, const void* w_packed, const float* bias, int T, int h, int E, int k, int dtype,
+                                int groups, int top_groups, int score, int best, int renorm, float scale, float alpha,
+                                float* logits, int32_t* topk_ids, float* gates, int32_t* counts, float* f, float* P, float* aux,
+                                void* ws, size_t ws_bytes, void* stream) {
+    const char* fn = "moe_group_router";
+    GroupGate g{};
+    g.bias = bias; g.nparts = 1;
+    g.T = T; g.E = E; g.k = k; g.groups = groups; g.top_groups = top_groups; g.score = score; g.best = best;
+    g.renorm = renorm != 0; g.scale = scale; g.alpha = alpha;
+    g.ids = topk_ids; g.gates = gates; g.counts = counts; g.f = f; g.P = P; g.aux = aux;
+    MOE_REQUIRE(dtype == MOE_F32 || dtype == MOE_BF16, MOE_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
+    MOE_REQUIRE(h > 0 && h % 8 == 0, MOE_ERR_INVALID_ARG, "%s: h=%d (need h%%8==0)", fn, h);
+    if (int rc = check_group_gate(fn, g)) return rc;
+    MOE_REQUIRE(T == 0 || (x && w_packed), MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+    MOE_REQUIRE(aligned16(x) && aligned16(w_packed) && aligned16(logits), MOE_ERR_INVALID_ARG,
+                "%s: x, w_packed and logits must be 16-byte aligned", fn);
+    const GroupRouterWs w = group_router_ws(ws, T, h, E, dtype);
+    MOE_REQUIRE(ws && aligned16(ws) && ws_bytes >= w.bytes, MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes (16-byte aligned)", fn,
+                ws_bytes, w.bytes);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T > 0) {
+        const int el = dtype == MOE_F32 ? 4 : 2;
+        const bool small = use_small_path(h, E, el), tc = use_tc_logits(E, dtype, small);
+        const void* w_r = dtype == MOE_F32 ? w_packed : nullptr;
+        const void* w_rT = dtype == MOE_F32 ? nullptr : w_packed;
+        float* lg = logits ? logits : w.logits;
+        if (small) {
+            if (int rc = router_run(x, w_r, w_rT, nullptr, T, h, E, 1, dtype, MOE_GATING_SOFTMAX, 0.f, lg, w.ids, w.gates, w.counts,
+                                    w.f, w.f + E, w.f + 2 * E, w.router, w.gate - w.router, stream))
+                return rc;
+        } else {
+            const RouterSplit sp = router_split(T, h, E, tc);
+            const RouterWs rw = router_ws_layout(w.router, T, h, E, el, small, false, tc, sp.S);
+            if (sp.S > 1) {                      // the gating adds the parts
+                g.logits_out = logits;
+                g.nparts = sp.S;
+                g.part_stride = (size_t)T * E;
+                lg = rw.parts;
+            }
+            if (int rc = launch_logits(x, w_r, w_rT, nullptr, T, h, E, dtype, tc, sp, rw, lg, s)) return rc;
+        }
+        g.logits = lg;
+    }
+    return launch_group_gate(g, w.gate, s);
 }

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 
 import torch
@@ -21,6 +22,7 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUD
 MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 FP4_FORMAT = {"nv": 0, "mx": 1}
 GATING = {"softmax": 0, "softmax_renorm": 1, "sigmoid_bias_renorm": 2, "softmax_selbias": 3}
+SCORE = {"sigmoid": 0, "softmax": 1}
 TILE_M = 128
 
 _P, _I, _Z, _F, _LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_longlong
@@ -32,6 +34,12 @@ _SIGS = {
     "moe_router_packed": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
     "moe_router_from_logits_workspace_size": (_Z, [_I, _I]),
     "moe_router_from_logits": (_I, [_P, _P, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "moe_group_route_workspace_size": (_Z, [_I, _I]),
+    "moe_group_route": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _F, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "moe_group_router_workspace_size": (_Z, [_I, _I, _I, _I]),
+    "moe_group_router": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _F, _P, _P, _P, _P, _P, _P, _P, _P, _Z,
+                              _P]),
+    "moe_group_route_backward": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _F, _P, _P]),
     "moe_sinkhorn_workspace_size": (_Z, [_I, _I]),
     "moe_sinkhorn_bias": (_I, [_P, _I, _I, _I, _P, _P, _Z, _P]),
     "moe_dispatch_rows": (_Z, [_I, _I, _I, _I]),
@@ -206,6 +214,91 @@ def moe_sinkhorn_bias(logits, n_iter: int = 16, *, sel_bias=None, ws=None, strea
     ws = _bytes_tensor(_lib.moe_sinkhorn_workspace_size(T, E), dev) if ws is None else ws
     _check(_lib.moe_sinkhorn_bias(_ptr(logits), T, E, n_iter, _ptr(sel_bias), _ptr(ws), ws.numel(), _stream(stream)))
     return sel_bias
+
+
+# ------------------------------------------------------------------------------------- routing by groups
+
+def _score(score: str | int) -> int:
+    if isinstance(score, str):
+        if score not in SCORE:
+            raise MoEError(MOE_ERR_UNSUPPORTED, f"score {score!r}")
+        return SCORE[score]
+    return int(score)
+
+
+def _route_outputs(T: int, E: int, k: int, t, stream, given: dict) -> dict:
+    """The routing outputs: those given, checked, and new ones for the rest."""
+    i32, f32 = torch.int32, torch.float32
+    want = dict(topk_ids=((T, k), i32), gates=((T, k), f32), counts=((E,), i32), f=((E,), f32), P=((E,), f32), aux=((1,), f32))
+    out = {}
+    for name, (shape, dtype) in want.items():
+        o = given.get(name)
+        out[name] = _fp4_empty(shape, dtype, t, stream) if o is None else o
+        if o is not None:
+            _fp4_data(o, math.prod(shape), dtype, name)
+    return out
+
+
+def moe_group_route_workspace_size(T: int, E: int) -> int:
+    return _lib.moe_group_route_workspace_size(T, E)
+
+
+def moe_group_route(logits, bias, k: int, groups: int, top_groups: int, *, score="sigmoid", best: int = 2, renorm: bool = True,
+                    scale: float = 1.0, alpha: float = 0.01, topk_ids=None, gates=None, counts=None, f=None, P=None, aux=None,
+                    ws=None, stream=None):
+    """The k experts of the top_groups best of `groups` groups of experts for each row of fp32 logits [T, E], their gates, and
+    the counts and balance-loss terms: dict(topk_ids, gates, counts, f, P, aux). A group's score is the sum of its `best`
+    largest selection scores (score + bias). ws: moe_group_route_workspace_size bytes, kept across calls."""
+    if logits.dim() != 2:
+        _fp4_fail("logits: [T, E]")
+    T, E = logits.shape
+    o = _route_outputs(T, E, k, logits, stream, dict(topk_ids=topk_ids, gates=gates, counts=counts, f=f, P=P, aux=aux))
+    ws = _fp4_bytes(_lib.moe_group_route_workspace_size(T, E), logits, stream) if ws is None else ws
+    _check(_lib.moe_group_route(_fp4_data(logits, T * E, torch.float32, "logits"), _fp4_data(bias, E, torch.float32, "bias"), T, E,
+                                k, groups, top_groups, _score(score), best, int(renorm), scale, alpha,
+                                *(t.data_ptr() for t in o.values()), _fp4_data(ws, 0, torch.uint8, "ws"), ws.numel(),
+                                _fp4_stream(stream, logits)))
+    return o
+
+
+def moe_group_router_workspace_size(T: int, h: int, E: int, dtype) -> int:
+    return _lib.moe_group_router_workspace_size(T, h, E, dtype_code(dtype) if isinstance(dtype, torch.dtype) else dtype)
+
+
+def moe_group_router(x, w_packed, E: int, bias, k: int, groups: int, top_groups: int, *, score="sigmoid", best: int = 2,
+                     renorm: bool = True, scale: float = 1.0, alpha: float = 0.01, logits=None, want_logits=True, topk_ids=None,
+                     gates=None, counts=None, f=None, P=None, aux=None, ws=None, stream=None):
+    """moe_group_route on the logits of x [T, h] (bf16 or fp32) and the packed router weight (moe_pack_router_weight) of E
+    experts; the dict also holds the logits [T, E] (None with want_logits=False, unless given)."""
+    T, h = x.shape
+    dt = dtype_code(x.dtype)
+    if not x.is_contiguous() or not x.is_cuda:
+        _fp4_fail("x: a contiguous device tensor")
+    if logits is None and want_logits:
+        logits = _fp4_empty((T, E), torch.float32, x, stream)
+    o = _route_outputs(T, E, k, x, stream, dict(topk_ids=topk_ids, gates=gates, counts=counts, f=f, P=P, aux=aux))
+    ws = _fp4_bytes(_lib.moe_group_router_workspace_size(T, h, E, dt), x, stream) if ws is None else ws
+    _check(_lib.moe_group_router(x.data_ptr(), _fp4_data(w_packed, _lib.moe_router_packed_bytes(h, E, dt), torch.uint8, "w_packed"),
+                                 _fp4_data(bias, E, torch.float32, "bias"), T, h, E, k, dt, groups, top_groups, _score(score), best,
+                                 int(renorm), scale, alpha, _fp4_data(logits, T * E, torch.float32, "logits"),
+                                 *(t.data_ptr() for t in o.values()), _fp4_data(ws, 0, torch.uint8, "ws"), ws.numel(),
+                                 _fp4_stream(stream, x)))
+    return dict(logits=logits, **o)
+
+
+def moe_group_route_backward(logits, topk_ids, d_gates, f, *, score="sigmoid", renorm: bool = True, scale: float = 1.0,
+                             alpha: float = 0.01, d_aux: float = 1.0, d_logits=None, stream=None):
+    """The gradient of the logits [T, E] for d_gates [T, k] and d_aux, from what moe_group_route gave (topk_ids, f)."""
+    if logits.dim() != 2 or topk_ids.dim() != 2 or topk_ids.shape[0] != logits.shape[0]:
+        _fp4_fail("logits: [T, E], topk_ids: [T, k]")
+    (T, E), k = logits.shape, topk_ids.shape[1]
+    d_logits = _fp4_empty((T, E), torch.float32, logits, stream) if d_logits is None else d_logits
+    _check(_lib.moe_group_route_backward(_fp4_data(logits, T * E, torch.float32, "logits"),
+                                         _fp4_data(topk_ids, T * k, torch.int32, "topk_ids"),
+                                         _fp4_data(d_gates, T * k, torch.float32, "d_gates"), _fp4_data(f, E, torch.float32, "f"),
+                                         T, E, k, _score(score), int(renorm), scale, alpha, d_aux,
+                                         _fp4_data(d_logits, T * E, torch.float32, "d_logits"), _fp4_stream(stream, logits)))
+    return d_logits
 
 
 # ---------------------------------------------------------------------------------------------- dispatch
