@@ -49,7 +49,7 @@ enum moe_status {
     MOE_ERR_TIMEOUT = 5       /* a bounded device-side wait ran out (see moe_check_device_error) */
 };
 
-enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 /* the moe_fp4_* calls alone */ };
+enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 /* the moe_fp4_*, moe_int8_* and moe_checkpoint8_* calls alone */ };
 
 /* Gating modes ("Megatron-LM ... （六）", section "Router": top-k on the logits with softmax or sigmoid
  * weights; "v6 长序列和 MoE ...", "Load balancing loss" bullet: DeepSeek-V3 selection-only bias). */
@@ -531,6 +531,53 @@ int moe_fp4_expert_ffn(const void* x, long long ldx, int x_rows, const int32_t* 
                        int fmt, int dtype, void* out, long long ldo, int out_dtype, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------------------------
+ * 8-bit experts: whole numbers with a scale for each token and one for each output channel, their products grouped by expert, and
+ * the SwiGLU expert FFN on them. Serving operators: the codes are piecewise constant in x, so there is no backward.
+ *   A row x [K] has scale = amax / 127 (fp32) and code_k = the whole number nearest to x_k * 127 / amax, ties to even (decided
+ *   exactly). A row whose amax is below 2^-96 has scale 0 and codes 0; one that holds an infinity or a NaN scale NaN and codes 0, so
+ *   that what is computed from it is NaN. A weight [N, K] quantised by rows has a scale for each output channel; its codes may be
+ *   -128 too.
+ *   dtype / out_dtype: MOE_F32, MOE_BF16 or MOE_F16. x and out may have row strides (ldx, ldo, in elements) and need be aligned to
+ *   their type only; rows that start on 16 bytes with K a multiple of 16 are the fast case. Sizes: 1 <= K, N, h <= MOE_INT8_MAX_K,
+ *   F <= MOE_INT8_MAX_K / 2, rows <= MOE_INT8_MAX_ROWS, 1 <= groups <= 1024. src: x's row of each row, -1 for a row of zeros, or NULL.
+ *
+ * moe_int8_quantize: x [x_rows, K] -> codes [rows, K] int8 and scales [rows]. moe_int8_dequantize: code * scale, rounded once.
+ * moe_int8_pack_weight: codes [G, N, K] -> packed (moe_int8_packed_weight_bytes() bytes, opaque, a byte a value), once per weight.
+ *   moe_int8_pack_expert_weights: gate and up [E, F, h] and down [E, h, F] likewise.
+ * moe_int8_linear: x quantised by rows, then for the rows r of group g
+ *     out[r, n] = (sum_k code(x)[r, k] W[g, n, k]) * scale(x)[r] * w_scales[g, n]
+ *   the sum exact up to 2^24 and in fp32 beyond. The rows of a group are [offsets[g], offsets[g + 1]) (offsets [G + 1] int32, rising
+ *   within [0, rows]; any other is reported by moe_check_device_error as MOE_ERR_INVALID_ARG and nothing is computed), or those of
+ *   tile_sched (moe_dispatch's; exactly one of the two is given). A schedule of another number of groups, or with tiles past the
+ *   call's rows, is reported likewise. Rows of no group are not written.
+ * moe_int8_expert_ffn: for the rows of expert e
+ *     act = silu(linear(x, gate)) * linear(x, up) in fp32;  out = linear(act, down), act quantised by rows
+ *   ws: moe_int8_linear_workspace_size() / moe_int8_expert_ffn_workspace_size() bytes, 256-byte aligned.
+ *   Errors: MOE_ERR_UNSUPPORTED for a dtype outside the enum; MOE_ERR_INVALID_ARG for sizes out of range, a null or misaligned pointer,
+ *   x shorter than rows without src, both or neither of offsets and tile_sched; MOE_ERR_WORKSPACE. A src outside [-1, x_rows) is
+ *   taken as -1 and reported by moe_check_device_error. Deterministic.
+ * ------------------------------------------------------------------------------------------------- */
+#define MOE_INT8_MAX_K (1 << 17)
+#define MOE_INT8_MAX_ROWS (1 << 28)
+
+int moe_int8_quantize(const void* x, long long ldx, int x_rows, const int32_t* src, int rows, int K, int dtype, void* codes,
+                      float* scales, void* stream);
+int moe_int8_dequantize(const void* codes, const float* scales, int rows, int K, int dtype, void* out, long long ldo, void* stream);
+size_t moe_int8_packed_weight_bytes(int G, int N, int K);
+int moe_int8_pack_weight(const void* codes, int G, int N, int K, void* packed, void* stream);
+size_t moe_int8_linear_workspace_size(int G, int N, int K, int rows);
+int moe_int8_linear(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* offsets, const int32_t* tile_sched,
+                    const void* packed, const float* w_scales, int G, int N, int K, int rows, int dtype, void* out, long long ldo,
+                    int out_dtype, void* ws, size_t ws_bytes, void* stream);
+size_t moe_int8_packed_expert_weights_bytes(int E, int h, int F);
+int moe_int8_pack_expert_weights(const void* gate, const void* up, const void* down, int E, int h, int F, void* packed, void* stream);
+size_t moe_int8_expert_ffn_workspace_size(int E, int h, int F, int rows);
+int moe_int8_expert_ffn(const void* x, long long ldx, int x_rows, const int32_t* src, const int32_t* offsets,
+                        const int32_t* tile_sched, const void* packed, const float* gate_scales, const float* up_scales,
+                        const float* down_scales, int E, int h, int F, int rows, int dtype, void* out, long long ldo, int out_dtype,
+                        void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------------
  * Backward of the layer ("专家并行" (formulaic), section "BWD（反向传播）" and the overlap notes: the
  * gradients return to the experts along the routing path; each expert computes its own weight gradients).
  * The pages give no formulas: these are the chain rule through the forward calls above with the top-k
@@ -614,6 +661,29 @@ int moe_expert_up_gate_backward(const void* buf, const void* d_act, const int32_
 int moe_expert_up_gate_backward_saved(const void* gu, const void* d_act, const int32_t* tile_sched,
                                       const void* packed_bwd, int E, int h, int F, int rows, int dtype, void* d_gu,
                                       void* d_buf, void* stream);
+/* Activation checkpoints in 8 bits: a value kept as a code under the scale of its block of 128 columns, for a backward that then
+ * needs a byte and a 32nd a value where bf16 takes two.
+ *   scale = amax / 127 of the block (fp32), code the whole number nearest to x * 127 / amax, ties to even (decided exactly); a block
+ *   whose amax is below 2^-96: scale and codes 0; one that holds an infinity or a NaN: scale NaN, codes 0.
+ * moe_checkpoint8_save: x [rows, C] (MOE_F32, MOE_BF16 or MOE_F16, row stride ldx) -> codes [rows, C] int8, scales [rows, ceil(C / 128)].
+ *   With tile_sched (moe_dispatch's, of E experts; NULL: all rows) only the rows of its tiles are read and written.
+ * moe_checkpoint8_load: code * scale, rounded once to dtype.
+ * moe_checkpoint8_swiglu_backward: from the pre-activations gu [rows, 2 Fp] of moe_expert_up_gate_save kept that way (blocks of 128
+ *   columns of g, then of the u of the same features) and d_act [rows, F] bf16:
+ *     s = logistic(g); d_g = d_act u s (1 + g (1 - s)), d_u = d_act g s -> d_gu [rows, 2 Fp] bf16; act = g s u [rows, F] bf16
+ *   (act is that of the kept g and u: with it the weight gradients need no act of the forward). tile_sched as above.
+ * moe_expert_up_gate_backward_checkpoint8: that over the schedule's tiles, then d_buf [rows, h] as moe_expert_up_gate_backward.
+ *   Errors: MOE_ERR_UNSUPPORTED for a dtype outside the enum; MOE_ERR_INVALID_ARG for sizes out of range (1 <= C <= MOE_INT8_MAX_K, rows <=
+ *   MOE_INT8_MAX_ROWS, F % 8 == 0), a null pointer, one not aligned to its type (save, load) or to 16 bytes (the backward calls).
+ *   A schedule of another number of experts computes nothing and is reported by moe_check_device_error. */
+int moe_checkpoint8_save(const void* x, long long ldx, int rows, int C, int dtype, const int32_t* tile_sched, int E, void* codes,
+                         float* scales, void* stream);
+int moe_checkpoint8_load(const void* codes, const float* scales, int rows, int C, int dtype, void* out, long long ldo, void* stream);
+int moe_checkpoint8_swiglu_backward(const void* codes, const float* scales, const void* d_act, const int32_t* tile_sched, int E, int F,
+                                    int rows, void* d_gu, void* act, void* stream);
+int moe_expert_up_gate_backward_checkpoint8(const void* codes, const float* scales, const void* d_act, const int32_t* tile_sched,
+                                            const void* packed_bwd, int E, int h, int F, int rows, void* d_gu, void* act, void* d_buf,
+                                            void* stream);
 size_t moe_expert_weight_grads_workspace_size(int E, int h, int F, int rows, int dtype);
 int moe_expert_weight_grads(const void* buf, const void* act, const void* d_gu, const void* d_eout,
                             const int32_t* offsets, const int32_t* kept_counts, int E, int h, int F, int rows,

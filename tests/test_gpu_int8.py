@@ -1,0 +1,353 @@
+"""The 8-bit expert operators on the GPU against the float64 oracle: codes exactly, products within the roundings that follow the
+exact sums, the FFN within the steps that activations next to a border may take the other way."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import int8_oracle as Q
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+HALF_STEP = {k: torch.finfo(v).eps / 2 for k, v in DT.items()}
+F32 = HALF_STEP["fp32"]
+
+
+def data(shape, dtype="bf16", seed=0, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(DT[dtype]).cuda()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def ok(moe):
+    torch.cuda.synchronize()
+    assert moe.moe_check_device_error() == moe.MOE_OK, moe.moe_last_error_string()
+
+
+def weight(G, N, K, seed=1):
+    """Codes [G, N, K] with -128 among them, and scales [G, N]."""
+    g = torch.Generator().manual_seed(seed)
+    c = torch.randint(-128, 128, (G, N, K), generator=g, dtype=torch.int16).to(torch.int8)
+    return c.cuda(), (torch.rand(G, N, generator=g) * 2e-3 + 1e-4).cuda()
+
+
+def offsets_of(rows, G, seed=0, kind="random"):
+    g = np.random.default_rng(seed)
+    if kind == "one":                                    # all rows in one group
+        n = np.zeros(G, np.int64)
+        n[g.integers(G)] = rows
+    else:
+        n = g.multinomial(rows, g.dirichlet(np.full(G, 0.5)))
+    return np.concatenate([[0], np.cumsum(n)])
+
+
+def dev(offsets):
+    return torch.from_numpy(np.asarray(offsets, np.int32)).cuda()
+
+
+def near(got, want, dtype, extra=0.0):
+    """got (of dtype) is want after the three fp32 roundings of (sum * scale) * scale and the type's own; `extra`: absolute."""
+    got = f64(got)
+    tol = (3 * F32 + HALF_STEP[dtype]) * np.abs(want) * (1 + 1e-6) + extra + (2.0**-25 if dtype == "fp16" else 0.0)
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(want))
+    bad = np.abs(got - want) > tol
+    assert not bad[~np.isnan(want)].any(), (int(bad.sum()), float(np.nanmax(np.abs(got - want) / (np.abs(want) + 1e-30))))
+
+
+# ------------------------------------------------------------------------------------------ rows there and back
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows,K", [(1, 1), (1, 7168), (3, 15), (5, 16), (7, 31), (129, 64), (33, 100), (17, 999), (9, 2048), (4, 2064),
+                                    (5, 4096), (3, 8208), (2, 16384), (2, 16400), (3, 20001), (70, 768)])
+def test_quantize_is_the_definition(gpu_lib, dtype, rows, K):
+    x = data((rows, K), dtype, rows * 7919 + K, 3.0)
+    c, s = gpu_lib.moe_int8_quantize(x)
+    ok(gpu_lib)
+    code, scale = Q.quantize(f64(x))
+    np.testing.assert_array_equal(c.cpu().numpy(), code)
+    np.testing.assert_array_equal(f64(s), scale)
+    for out in ("fp32", dtype):
+        y = gpu_lib.moe_int8_dequantize(c, s, dtype=DT[out])
+        want = (c.float() * s.unsqueeze(1)).to(DT[out])      # one fp32 product, one rounding
+        assert torch.equal(y, want)
+    ok(gpu_lib)
+
+
+@pytest.mark.parametrize("K", [64, 999])
+def test_values_on_and_next_to_a_border(gpu_lib, K):
+    # amax = 254 * 2^e: every odd multiple of half a step is a tie; and fp32 neighbours of ties
+    base = np.arange(K) % 127 + 0.5
+    x = np.stack([base * 2.0, np.nextafter(np.float32(base * 2), np.float32(1e9)), np.nextafter(np.float32(base * 2), np.float32(-1e9)), -base * 2.0,
+                  base * 3.0, np.nextafter(np.float32(base * 3), np.float32(1e9))]).astype(np.float32)
+    x[:4, 0] = 254.0
+    x[4:, 0] = 381.0
+    x *= np.float32(2.0) ** np.array([0, 3, -20, 60, -60, 100], np.float32)[:, None]
+    t = torch.from_numpy(x).cuda()
+    c, s = gpu_lib.moe_int8_quantize(t)
+    ok(gpu_lib)
+    code, scale = Q.quantize(x)
+    np.testing.assert_array_equal(c.cpu().numpy(), code)
+    np.testing.assert_array_equal(f64(s), scale)
+
+
+def test_zero_tiny_infinite_and_nan_rows(gpu_lib):
+    x = torch.randn(8, 96, generator=torch.Generator().manual_seed(0))
+    x[0] = 0.0
+    x[1] *= 2.0**-110
+    x[2, 5] = float("inf")
+    x[3, 95] = float("nan")
+    x[4] = torch.nan_to_num(x[4]) * 1e38
+    x[5] = 0.0
+    x[5, 17] = 2.0**-96
+    for K in (96, 95):
+        v = x[:, :K].contiguous()
+        if K == 95:
+            v[3, 94] = float("nan")
+        c, s = gpu_lib.moe_int8_quantize(v.cuda())
+        ok(gpu_lib)
+        code, scale = Q.quantize(v.double().numpy())
+        np.testing.assert_array_equal(c.cpu().numpy(), code)
+        np.testing.assert_array_equal(f64(s), scale)
+        y = gpu_lib.moe_int8_dequantize(c, s, dtype=torch.float32)
+        # (the fourth row's 4.1e38 is an infinity in fp32)
+        finite = torch.isfinite(v).all(1)
+        assert finite.tolist() == [True, True, False, False, False, True, True, True]
+        assert y[~finite].isnan().all() and (y[:2] == 0).all() and torch.isfinite(y[finite]).all()
+
+
+def test_strides_gathered_rows_and_bounds(gpu_lib):
+    big = data((20, 300), "bf16", 3)
+    for x in (big[:, 8:136], big[:, 1:130], big[::2, :64], big.t().contiguous().t()[:, :1]):
+        c, s = gpu_lib.moe_int8_quantize(x)
+        ok(gpu_lib)
+        code, scale = Q.quantize(f64(x))
+        np.testing.assert_array_equal(c.cpu().numpy(), code)
+        out = torch.full((x.shape[0], 200), 7.0, dtype=torch.bfloat16, device="cuda")
+        for at in (0, 1):
+            view = out[:, at:at + x.shape[1]]
+            gpu_lib.moe_int8_dequantize(c, s, out=view)
+            assert torch.equal(view, (c.float() * s.unsqueeze(1)).bfloat16())
+        assert (out[:, x.shape[1] + 1:] == 7.0).all()
+    src = torch.tensor([3, -1, 0, 3, 19], dtype=torch.int32, device="cuda")
+    c, s = gpu_lib.moe_int8_quantize(big, src=src)
+    ok(gpu_lib)
+    rows = f64(big)[[3, 0, 0, 3, 19]]
+    rows[1] = 0.0
+    code, scale = Q.quantize(rows)
+    np.testing.assert_array_equal(c.cpu().numpy(), code)
+    src[2] = 20
+    c, _ = gpu_lib.moe_int8_quantize(big, src=src)
+    torch.cuda.synchronize()
+    assert gpu_lib.moe_check_device_error() == gpu_lib.MOE_ERR_INVALID_ARG
+    assert (c[2] == 0).all()
+    assert gpu_lib.moe_int8_quantize(big[:0])[0].shape == (0, 300)
+
+
+# ------------------------------------------------------------------------------------------ products
+
+
+LINEAR = [  # G, rows, N, K, kind
+    (1, 1, 1, 1, "random"), (1, 1, 128, 64, "random"), (3, 2, 33, 70, "random"), (1, 9, 130, 128, "random"), (5, 40, 256, 200, "random"),
+    (7, 300, 257, 136, "random"), (2, 33, 96, 1000, "one"), (16, 64, 384, 512, "random"), (3, 700, 512, 320, "random"), (1, 257, 640, 64, "one"),
+    (128, 200, 64, 64, "random"), (1024, 1500, 32, 64, "random"), (4, 1300, 300, 2048, "random"), (2, 600, 1001, 1044, "one"), (1, 31, 100, 16500, "one")]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("G,rows,N,K,kind", LINEAR)
+def test_linear(gpu_lib, dtype, G, rows, N, K, kind):
+    x = data((rows, K), dtype, G + rows)
+    w, ws = weight(G, N, K)
+    off = offsets_of(rows, G, rows, kind)
+    packed = gpu_lib.moe_int8_pack_weight(w)
+    y = gpu_lib.moe_int8_linear(x, dev(off), packed, ws)
+    ok(gpu_lib)
+    c, s = Q.quantize(f64(x))
+    want = Q.linear(c, s, off, w.cpu().numpy(), f64(ws))
+    # past 2^24 the sums of whole numbers round: K / 16 partial sums, each off by half a step of the largest
+    most = np.abs(c).sum(1).max() * 128.0
+    extra = 0.0 if most < 2**24 else (K / 16 + 1) * most * F32 * np.nanmax(s) * f64(ws).max()
+    near(y, want, dtype, extra)
+
+
+def test_linear_of_the_largest_codes(gpu_lib):
+    # the largest sums: 127 * 128 * K, past 2^24 in every channel
+    K, rows = 4096, 70
+    x = torch.ones(rows, K).cuda()
+    x[1::2] = -1.0
+    w = torch.full((1, 160, K), -128, dtype=torch.int8, device="cuda")
+    ws = torch.full((1, 160), 1.0, device="cuda")
+    for n in (3, rows):
+        y = gpu_lib.moe_int8_linear(x[:n], dev([0, n]), gpu_lib.moe_int8_pack_weight(w), ws)
+        ok(gpu_lib)
+        # every partial sum is a multiple of 128 * 127 * 16 below 2^24 of those: exact
+        want = -128.0 * 127 * K * f64(torch.tensor([1.0 / 127.0]))
+        np.testing.assert_allclose(f64(y), np.where(np.arange(n) % 2, -want, want)[:, None] * np.ones((1, 160)), rtol=4 * F32)
+
+
+@pytest.mark.parametrize("rows", [5, 400])
+def test_rows_of_no_group_strided_output_and_other_type(gpu_lib, rows):
+    x = data((rows, 192), "bf16", 9)
+    w, ws = weight(3, 70, 192)
+    off = np.array([1, 2, 2, rows - 1])
+    out = torch.full((rows, 90), 5.0, device="cuda")
+    gpu_lib.moe_int8_linear(x, dev(off), gpu_lib.moe_int8_pack_weight(w), ws, out=out[:, 3:73])
+    ok(gpu_lib)
+    c, s = Q.quantize(f64(x))
+    want = Q.linear(c, s, off, w.cpu().numpy(), f64(ws))
+    near(out[1:rows - 1, 3:73], want[1:rows - 1], "fp32")
+    assert (out[0] == 5).all() and (out[-1] == 5).all() and (out[:, :3] == 5).all() and (out[:, 73:] == 5).all()
+
+
+@pytest.mark.parametrize("rows", [4, 300])
+def test_a_bad_row_leaves_the_others(gpu_lib, rows):
+    x = data((rows, 128), "fp32", 2)
+    x[1, 7] = float("inf")
+    x[2] = 0.0
+    w, ws = weight(2, 64, 128)
+    off = [0, rows // 2, rows]
+    y = gpu_lib.moe_int8_linear(x, dev(off), gpu_lib.moe_int8_pack_weight(w), ws)
+    ok(gpu_lib)
+    c, s = Q.quantize(f64(x))
+    near(y, Q.linear(c, s, off, w.cpu().numpy(), f64(ws)), "fp32")
+    assert y[1].isnan().all() and (y[2] == 0).all()
+
+
+def test_offsets_that_fall_or_leave_the_rows_are_reported(gpu_lib):
+    for rows in (6, 400):
+        x = data((rows, 64))
+        w, ws = weight(3, 64, 64)
+        packed = gpu_lib.moe_int8_pack_weight(w)
+        for off in ([0, 4, 2, rows], [-1, 1, 2, rows], [0, 1, 2, rows + 1]):
+            out = torch.full((rows, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+            gpu_lib.moe_int8_linear(x, dev(off), packed, ws, out=out)
+            torch.cuda.synchronize()
+            assert gpu_lib.moe_check_device_error() == gpu_lib.MOE_ERR_INVALID_ARG
+            assert (out == 3).all()
+
+
+@pytest.mark.parametrize("T,capacity", [(3, 0), (200, 0), (200, 40), (700, 0)])
+def test_the_dispatchs_schedule(gpu_lib, T, capacity):
+    E, k, h, F = 6, 2, 128, 96
+    x = data((T, h), "bf16", 4)
+    ids = torch.stack([torch.randperm(E, generator=torch.Generator().manual_seed(i))[:k] for i in range(T)]).int().cuda()
+    d = gpu_lib.moe_dispatch(x, ids, E, capacity)
+    gate, gs = weight(E, F, h, 5)
+    up, us = weight(E, F, h, 6)
+    down, ds = weight(E, h, F, 7)
+    packed = gpu_lib.moe_int8_pack_expert_weights(gate, up, down)
+    rows = d["rows"]
+    out = torch.zeros((rows, h), dtype=torch.bfloat16, device="cuda")
+    gpu_lib.moe_int8_expert_ffn(x, None, packed, gs, us, ds, src=d["src_token"], tile_sched=d["tile_sched"], out=out)
+    again = torch.zeros_like(out)
+    gpu_lib.moe_int8_expert_ffn(d["buf"], None, packed, gs, us, ds, tile_sched=d["tile_sched"], out=again)
+    ok(gpu_lib)
+    assert torch.equal(out, again)
+    if not capacity:
+        third = gpu_lib.moe_int8_expert_ffn(d["buf"], d["offsets"], packed, gs, us, ds)
+        assert torch.equal(out, third)
+    y = gpu_lib.moe_int8_linear(d["buf"], None, gpu_lib.moe_int8_pack_weight(gate), gs, tile_sched=d["tile_sched"], out=torch.zeros((rows, F), dtype=torch.bfloat16, device="cuda"))
+    c, s = Q.quantize(f64(d["buf"]))
+    off, kept = d["offsets"].cpu().numpy(), d["kept_counts"].cpu().numpy()
+    for e in range(E):
+        lo, hi = off[e], off[e] + kept[e]
+        near(y[lo:hi], (c[lo:hi].astype(float) @ gate[e].cpu().numpy().astype(float).T) * s[lo:hi, None] * f64(gs)[e], "bf16")
+        assert (out[hi:off[e + 1]] == 0).all() and (y[hi:off[e + 1]] == 0).all()
+    # a schedule of other groups, and one whose rows are not the call's
+    other, os_ = weight(5, F, h, 8)
+    gpu_lib.moe_int8_linear(d["buf"], None, gpu_lib.moe_int8_pack_weight(other), os_, tile_sched=d["tile_sched"])
+    torch.cuda.synchronize()
+    assert gpu_lib.moe_check_device_error() == gpu_lib.MOE_ERR_INVALID_ARG
+
+
+FFN = [  # E, rows, h, F, kind
+    (1, 1, 64, 32, "random"), (4, 3, 128, 96, "random"), (8, 20, 256, 192, "random"), (3, 300, 136, 200, "random"), (2, 700, 256, 512, "one"),
+    (16, 900, 512, 320, "random"), (5, 33, 72, 1000, "random"), (2, 40, 7168, 64, "random"), (64, 500, 128, 64, "random")]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("E,rows,h,F,kind", FFN)
+def test_expert_ffn(gpu_lib, dtype, E, rows, h, F, kind):
+    x = data((rows, h), dtype, E * rows)
+    gate, gs = weight(E, F, h, 2)
+    up, us = weight(E, F, h, 3)
+    down, ds = weight(E, h, F, 4)
+    gs, us = gs * 0.05, us * 0.05                          # gates of a few units
+    off = offsets_of(rows, E, rows, kind)
+    y = gpu_lib.moe_int8_expert_ffn(x, dev(off), gpu_lib.moe_int8_pack_expert_weights(gate, up, down), gs, us, ds)
+    ok(gpu_lib)
+    a = Q.act(f64(x), off, gate.cpu().numpy(), f64(gs), up.cpu().numpy(), f64(us))
+    # act is within 16 half steps of fp32 and one for each unit of the gate, so its codes are those of `a` but where a * 127 / amax
+    # lies within 127 * that of a border; such a code may be one off
+    amax = np.abs(a).max(1, keepdims=True)
+    q = a * 127.0 / amax
+    codes = np.rint(q)
+    slack = 127.0 * 64 * F32 + 1e-9
+    open_ = (np.abs(np.abs(q - np.floor(q)) - 0.5) < slack)
+    scales = amax[:, 0] / 127.0
+    want = Q.linear(codes, scales, off, down.cpu().numpy(), f64(ds))
+    lim = np.zeros_like(want)
+    for e in range(E):
+        lo, hi = off[e], off[e + 1]
+        lim[lo:hi] = (open_[lo:hi].astype(float) @ np.abs(down[e].cpu().numpy().astype(float)).T) * scales[lo:hi, None] * f64(ds)[e][None]
+    # the scale itself carries act's error: 64 half steps of the sum of magnitudes
+    mag = Q.linear(np.abs(codes), scales, off, np.abs(down.cpu().numpy().astype(np.int64)), f64(ds))
+    near(y, want, dtype, lim + 64 * F32 * mag)
+
+
+def test_gates_far_from_zero(gpu_lib):
+    # gates near -200, 0 and 200: exp(-g) overflows on one side, and silu is 0 or g there
+    h = F = 64
+    x = torch.zeros(12, h)
+    x[:, 0] = 1.0
+    gate = torch.zeros(1, F, h, dtype=torch.int8)
+    gate[0, :, 0] = torch.arange(F) * 4 - 128
+    one = torch.zeros(1, F, h, dtype=torch.int8)
+    one[0, :, 0] = 1
+    down = torch.zeros(1, h, F, dtype=torch.int8)
+    down[0] = torch.eye(h, dtype=torch.int8)
+    gs, us, ds = torch.full((1, F), 1.6), torch.ones(1, F), torch.ones(1, h)
+    for n in (2, 12):
+        y = gpu_lib.moe_int8_expert_ffn(x[:n].cuda(), dev([0, n]), gpu_lib.moe_int8_pack_expert_weights(gate.cuda(), one.cuda(), down.cuda()), gs.cuda(), us.cuda(), ds.cuda())
+        ok(gpu_lib)
+        a = Q.act(x[:n].double().numpy(), [0, n], gate.numpy(), gs.double().numpy(), one.numpy(), us.double().numpy())
+        step = np.abs(a).max() / 127
+        assert torch.isfinite(y).all() and np.abs(f64(y) - a).max() <= step * 0.501
+
+
+def test_captured_on_streams_with_changing_rows(gpu_lib):
+    E, rows, h, F = 4, 500, 128, 96
+    x = data((rows, h), "bf16", 1)
+    gate, gs = weight(E, F, h, 2)
+    up, us = weight(E, F, h, 3)
+    down, ds = weight(E, h, F, 4)
+    packed = gpu_lib.moe_int8_pack_expert_weights(gate, up, down)
+    offs = [offsets_of(rows, E, i) for i in range(3)]
+    want = [gpu_lib.moe_int8_expert_ffn(x, dev(o), packed, gs, us, ds) for o in offs]
+    ok(gpu_lib)
+    off = dev(offs[0])
+    out = torch.empty((rows, h), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(gpu_lib.moe_int8_expert_ffn_workspace_size(E, h, F, rows), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        gpu_lib.moe_int8_expert_ffn(x, off, packed, gs, us, ds, out=out, ws=ws)
+    for i in (0, 1, 2, 1):
+        off.copy_(dev(offs[i]))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i])
+    # two streams, each with its own workspace, at once
+    outs = []
+    for i in range(2):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        outs.append(gpu_lib.moe_int8_expert_ffn(x, dev(offs[i]), packed, gs, us, ds, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    ok(gpu_lib)

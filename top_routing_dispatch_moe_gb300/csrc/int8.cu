@@ -1,0 +1,293 @@
+// Rows to 8-bit integers under one scale a row and back, and the packing of 8-bit weights.
+//
+// Both directions are bound by memory: x is read once and one byte a value written (two as fp16 operand), or the other way
+// round. A row is held in registers by one to eight warps between its largest magnitude and its codes; rows past 16384
+// columns are read twice.
+#include <algorithm>
+#include "int8.cuh"
+
+namespace moe {
+namespace int8 {
+
+constexpr int THREADS = 256;
+constexpr int WARPS = THREADS / 32;
+constexpr int SEG = 32 * UNIT;       // columns a warp takes at a time
+constexpr int HELD = 4;              // such pieces that a warp holds
+
+// Piece `c` of a row (columns 512 c ..): VEC: this lane's 16 consecutive columns; else (the row starts on no 16-byte boundary, or its
+// end cuts a unit) every 32nd column from the lane's own, so that loads and stores of a warp stay together.
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw16<T> load_piece(const T* row, int c, int K) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (VEC) return load_unit<T, true>(row, c * SEG + lane * UNIT, K);
+    Raw16<T> r;
+    T* e = reinterpret_cast<T*>(r.q);
+#pragma unroll
+    for (int j = 0; j < UNIT; ++j) {
+        const int k = c * SEG + j * 32 + lane;
+        e[j] = k < K ? row[k] : T(0.f);
+    }
+    return r;
+}
+template <typename T, int FORM, bool VEC>
+__device__ __forceinline__ void store_piece(const Raw16<T>& raw, void* codes, size_t base, int c, int width, float inv, float amax) {
+    const int lane = threadIdx.x & 31;
+    const T* e = reinterpret_cast<const T*>(raw.q);
+    float v[UNIT];
+#pragma unroll
+    for (int i = 0; i < UNIT; ++i) v[i] = as_f32(e[i]);
+    codes_of<UNIT>(v, inv, amax);
+    if constexpr (VEC) {
+        const int k = c * SEG + lane * UNIT;
+        if (k >= width) return;
+        if constexpr (FORM == FORM_F16) {
+            uint4 w[2];
+            __half2* h = reinterpret_cast<__half2*>(w);
+#pragma unroll
+            for (int i = 0; i < UNIT / 2; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            st32(static_cast<__half*>(codes) + base + k, w);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<int8_t*>(codes) + base + k) =
+                make_uint4(bytes4(v), bytes4(v + 4), bytes4(v + 8), bytes4(v + 12));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < UNIT; ++j) {
+            const int k = c * SEG + j * 32 + lane;
+            if (k >= width) continue;
+            if constexpr (FORM == FORM_F16) static_cast<__half*>(codes)[base + k] = __float2half_rn(v[j]);
+            else static_cast<int8_t*>(codes)[base + k] = (int8_t)(int)v[j];
+        }
+    }
+}
+
+// WPR warps to a row.
+template <typename T, int FORM, int WPR, bool VEC>
+__global__ void __launch_bounds__(THREADS)
+quantize_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, int rows, int K, int width, void* codes, float* scales,
+                unsigned* err) {
+    __shared__ float s_amax[WARPS];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % WPR;
+    const int row = blockIdx.x * (WARPS / WPR) + warp / WPR;
+    int from = row < rows ? row : -1;
+    if (from >= 0 && src) {
+        from = src[row];
+        if (from >= x_rows || from < -1) {
+            if (lane == 0) latch_device_error(err, kDevErrBadIndex, 0x310u);
+            from = -1;
+        }
+    }
+    const T* xr = x + (long long)max(from, 0) * ldx;
+    const int k_in = from >= 0 ? K : 0, pieces = (width + SEG - 1) / SEG;
+    const bool held = pieces <= HELD * WPR;
+    Raw16<T> raw[HELD];
+    float amax = 0.f;
+    if (held) {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            if (i * WPR + w < pieces) raw[i] = load_piece<T, VEC>(xr, i * WPR + w, k_in);
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            if (i * WPR + w < pieces) amax = max_nan(amax, unit_amax(raw[i]));
+    } else {
+        for (int c = w; c < pieces; c += WPR) amax = max_nan(amax, unit_amax(load_piece<T, VEC>(xr, c, k_in)));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if constexpr (WPR > 1) {
+        if (lane == 0) s_amax[warp] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) amax = max_nan(amax, s_amax[warp - w + i]);
+    }
+    if (row >= rows) return;
+    float inv;
+    const float scale = scale_of(amax, inv);
+    if (w == 0 && lane == 0) scales[row] = scale;
+    const size_t base = (size_t)row * width;
+    if (held) {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            if (i * WPR + w < pieces) store_piece<T, FORM, VEC>(raw[i], codes, base, i * WPR + w, width, inv, amax);
+    } else {
+        for (int c = w; c < pieces; c += WPR)
+            store_piece<T, FORM, VEC>(load_piece<T, VEC>(xr, c, k_in), codes, base, c, width, inv, amax);
+    }
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(THREADS)
+dequantize_kernel(const int8_t* codes, const float* scales, int rows, int K, T* out, long long ldo) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, nseg = (K + SEG - 1) / SEG;
+    Walk at((long long)blockIdx.x * WARPS + (threadIdx.x >> 5), (long long)gridDim.x * WARPS, (long long)rows * nseg, nseg);
+    for (; at.left > 0; at.next()) {
+        const int8_t* cr = codes + (size_t)at.row * K;
+        T* orow = out + at.row * ldo;
+        const float s = scales[at.row];
+        if constexpr (VEC) {
+            const int k = at.seg * SEG + lane * UNIT;
+            if (k >= K) continue;
+            const uint4 q = __ldcs(reinterpret_cast<const uint4*>(cr + k));
+            const int8_t* c = reinterpret_cast<const int8_t*>(&q);
+            alignas(16) T o[UNIT];
+#pragma unroll
+            for (int i = 0; i < UNIT; ++i) o[i] = rounded<T>((float)c[i] * s);
+            const uint4* ov = reinterpret_cast<const uint4*>(o);
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T); ++i) __stcs(reinterpret_cast<uint4*>(orow + k) + i, ov[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < UNIT; ++j) {
+                const int k = at.seg * SEG + j * 32 + lane;
+                if (k < K) orow[k] = rounded<T>((float)cr[k] * s);
+            }
+        }
+    }
+}
+
+// A 16-byte chunk of the packed weight a thread. b: null, or the rows that follow those of a in turn (gate, up).
+__global__ void __launch_bounds__(THREADS)
+pack_kernel(const int8_t* __restrict__ a, const int8_t* __restrict__ b, int N, int K, int NB, int KST, size_t chunks, uint4* __restrict__ out) {
+    for (size_t i = (size_t)blockIdx.x * THREADS + threadIdx.x; i < chunks; i += (size_t)gridDim.x * THREADS) {
+        const int r = (int)(i & 127), c = (int)(i >> 7 & 3);
+        const size_t piece = i >> 9, at = piece / KST;
+        const int k0 = (int)(piece - at * KST) * STAGE_K + c * UNIT, nb = (int)(at % NB);
+        const size_t g = at / NB;
+        const int n = nb * BLOCK_N + r, rows = b ? N / 2 : N;      // rows of each source
+        const int8_t* src = (b && (n & 1)) ? b : a;
+        const size_t row = g * rows + (b ? n >> 1 : n);
+        alignas(16) uint8_t v[UNIT];
+#pragma unroll
+        for (int j = 0; j < UNIT; ++j) v[j] = n < N && k0 + j < K ? (uint8_t)(src[row * K + k0 + j] + 128) : (uint8_t)128;
+        out[i] = *reinterpret_cast<const uint4*>(v);
+    }
+}
+
+static int launch_pack(const void* a, const void* b, int G, int N, int K, void* out, cudaStream_t s) {
+    const WeightLayout L = weight_layout(G, N, K);
+    const size_t chunks = L.total / 16;
+    const int grid = (int)std::min<size_t>((chunks + THREADS - 1) / THREADS, (size_t)num_sms() * 16);
+    pack_kernel<<<grid, THREADS, 0, s>>>(static_cast<const int8_t*>(a), static_cast<const int8_t*>(b), N, K, L.NB, L.KST, chunks,
+                                         static_cast<uint4*>(out));
+    return check_launch("int8 pack_kernel");
+}
+
+template <typename T, int FORM>
+static cudaError_t quantize_form(const void* x, long long ldx, int x_rows, const int32_t* src, int rows, int K, void* codes, float* scales,
+                                 unsigned* err, cudaStream_t s) {
+    const int width = FORM == FORM_ROWS ? K : pad64(K), pieces = (width + SEG - 1) / SEG;
+    const bool vec = K % UNIT == 0 && aligned16(x) && ldx * (long long)sizeof(T) % 16 == 0 && aligned16(codes);
+    const T* xt = static_cast<const T*>(x);
+    auto go = [&](auto kernel, int wpr) {
+        return launch_pdl(kernel, dim3(cdiv(rows, WARPS / wpr)), dim3(THREADS), 0, s, xt, ldx, x_rows, src, rows, K, width, codes, scales, err);
+    };
+    // a row's warps: as many as hold it four pieces each
+    if (vec) {
+        if (pieces <= HELD) return go(quantize_kernel<T, FORM, 1, true>, 1);
+        if (pieces <= 2 * HELD) return go(quantize_kernel<T, FORM, 2, true>, 2);
+        if (pieces <= 4 * HELD) return go(quantize_kernel<T, FORM, 4, true>, 4);
+        return go(quantize_kernel<T, FORM, 8, true>, 8);
+    }
+    if (pieces <= HELD) return go(quantize_kernel<T, FORM, 1, false>, 1);
+    return go(quantize_kernel<T, FORM, 8, false>, 8);
+}
+
+int launch_quantize(const void* x, long long ldx, int x_rows, const int32_t* src, int rows, int K, int dtype, int form, void* codes,
+                    float* scales, unsigned* err, cudaStream_t s) {
+    if (rows == 0) return MOE_OK;
+    cudaError_t e = cudaErrorInvalidValue;
+#define MOE_QUANT(T)                                                                                                       \
+    e = form == FORM_ROWS ? quantize_form<T, FORM_ROWS>(x, ldx, x_rows, src, rows, K, codes, scales, err, s)               \
+      : form == FORM_F16 ? quantize_form<T, FORM_F16>(x, ldx, x_rows, src, rows, K, codes, scales, err, s)                 \
+                         : quantize_form<T, FORM_BYTES>(x, ldx, x_rows, src, rows, K, codes, scales, err, s)
+    if (dtype == MOE_F32) MOE_QUANT(float);
+    else if (dtype == MOE_BF16) MOE_QUANT(__nv_bfloat16);
+    else MOE_QUANT(__half);
+#undef MOE_QUANT
+    return check_launch(e, "int8 quantize_kernel");
+}
+
+static bool known(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16; }
+static bool type_aligned(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % (dtype == MOE_F32 ? 4 : 2) == 0; }
+
+}  // namespace int8
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_int8_quantize(const void* x, long long ldx, int x_rows, const int32_t* src, int rows, int K, int dtype, void* codes,
+                                 float* scales, void* stream) {
+    const char* fn = "moe_int8_quantize";
+    MOE_REQUIRE(int8::known(dtype), MOE_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
+    MOE_REQUIRE(rows >= 0 && rows <= MOE_INT8_MAX_ROWS && K >= 1 && K <= MOE_INT8_MAX_K && ldx >= K && x_rows >= (src ? 0 : rows),
+                MOE_ERR_INVALID_ARG, "%s: rows=%d x_rows=%d K=%d ldx=%lld", fn, rows, x_rows, K, ldx);
+    if (rows == 0) return MOE_OK;
+    MOE_REQUIRE((x || x_rows == 0) && codes && scales, MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+    MOE_REQUIRE(int8::type_aligned(x, dtype) && int8::type_aligned(scales, MOE_F32) && int8::type_aligned(src, MOE_F32), MOE_ERR_INVALID_ARG,
+                "%s: misaligned pointer", fn);
+    unsigned* err = device_error_word();
+    MOE_REQUIRE(err, MOE_ERR_CUDA, "%s: device error word unavailable", fn);
+    return int8::launch_quantize(x, ldx, x_rows, src, rows, K, dtype, int8::FORM_ROWS, codes, scales, err, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int moe_int8_dequantize(const void* codes, const float* scales, int rows, int K, int dtype, void* out, long long ldo,
+                                   void* stream) {
+    const char* fn = "moe_int8_dequantize";
+    MOE_REQUIRE(int8::known(dtype), MOE_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
+    MOE_REQUIRE(rows >= 0 && rows <= MOE_INT8_MAX_ROWS && K >= 1 && K <= MOE_INT8_MAX_K && ldo >= K, MOE_ERR_INVALID_ARG,
+                "%s: rows=%d K=%d ldo=%lld", fn, rows, K, ldo);
+    if (rows == 0) return MOE_OK;
+    MOE_REQUIRE(codes && scales && out, MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+    MOE_REQUIRE(int8::type_aligned(out, dtype) && int8::type_aligned(scales, MOE_F32), MOE_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+    const long long items = (long long)rows * cdiv(K, int8::SEG);
+    const int grid = (int)std::min<long long>((items + int8::WARPS - 1) / int8::WARPS, 8LL * num_sms());
+    const int el = dtype == MOE_F32 ? 4 : 2;
+    const bool vec = K % UNIT == 0 && aligned16(codes) && aligned16(out) && ldo * el % 16 == 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto go = [&](auto kernel, auto* o) {
+        return launch_pdl(kernel, dim3(grid), dim3(int8::THREADS), 0, s, static_cast<const int8_t*>(codes), scales, rows, K, o, ldo);
+    };
+    cudaError_t e;
+    if (dtype == MOE_F32) {
+        auto* o = static_cast<float*>(out);
+        e = vec ? go(int8::dequantize_kernel<float, true>, o) : go(int8::dequantize_kernel<float, false>, o);
+    } else if (dtype == MOE_BF16) {
+        auto* o = static_cast<__nv_bfloat16*>(out);
+        e = vec ? go(int8::dequantize_kernel<__nv_bfloat16, true>, o) : go(int8::dequantize_kernel<__nv_bfloat16, false>, o);
+    } else {
+        auto* o = static_cast<__half*>(out);
+        e = vec ? go(int8::dequantize_kernel<__half, true>, o) : go(int8::dequantize_kernel<__half, false>, o);
+    }
+    return check_launch(e, "int8 dequantize_kernel");
+}
+
+static bool int8_sizes(int G, int N, int K) {
+    return G >= 1 && G <= 1024 && N >= 1 && N <= MOE_INT8_MAX_K && K >= 1 && K <= MOE_INT8_MAX_K;
+}
+
+extern "C" size_t moe_int8_packed_weight_bytes(int G, int N, int K) { return int8_sizes(G, N, K) ? int8::weight_layout(G, N, K).total : 0; }
+
+extern "C" int moe_int8_pack_weight(const void* codes, int G, int N, int K, void* packed, void* stream) {
+    MOE_REQUIRE(int8_sizes(G, N, K), MOE_ERR_INVALID_ARG, "moe_int8_pack_weight: G=%d N=%d K=%d", G, N, K);
+    MOE_REQUIRE(codes && packed && aligned16(packed), MOE_ERR_INVALID_ARG, "moe_int8_pack_weight: null or misaligned pointer");
+    return int8::launch_pack(codes, nullptr, G, N, K, packed, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t moe_int8_packed_expert_weights_bytes(int E, int h, int F) {
+    return int8_sizes(E, h, F) && F <= MOE_INT8_MAX_K / 2 ? int8::expert_layout(E, h, F).total : 0;
+}
+
+extern "C" int moe_int8_pack_expert_weights(const void* gate, const void* up, const void* down, int E, int h, int F, void* packed,
+                                            void* stream) {
+    const char* fn = "moe_int8_pack_expert_weights";
+    MOE_REQUIRE(int8_sizes(E, h, F) && F <= MOE_INT8_MAX_K / 2, MOE_ERR_INVALID_ARG, "%s: E=%d h=%d F=%d", fn, E, h, F);
+    MOE_REQUIRE(gate && up && down && packed && aligned16(packed), MOE_ERR_INVALID_ARG, "%s: null or misaligned pointer", fn);
+    const int8::ExpertLayout L = int8::expert_layout(E, h, F);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (int rc = int8::launch_pack(gate, up, E, 2 * F, h, packed, s)) return rc;
+    return int8::launch_pack(down, nullptr, E, h, F, static_cast<char*>(packed) + L.down_off, s);
+}

@@ -73,6 +73,16 @@ _SIGS = {
     "moe_fp4_expert_ffn_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
     "moe_fp4_expert_ffn": (_I, [_P, _LL, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _LL, _I, _P,
                                 _Z, _P]),
+    "moe_int8_quantize": (_I, [_P, _LL, _I, _P, _I, _I, _I, _P, _P, _P]),
+    "moe_int8_dequantize": (_I, [_P, _P, _I, _I, _I, _P, _LL, _P]),
+    "moe_int8_packed_weight_bytes": (_Z, [_I, _I, _I]),
+    "moe_int8_pack_weight": (_I, [_P, _I, _I, _I, _P, _P]),
+    "moe_int8_linear_workspace_size": (_Z, [_I, _I, _I, _I]),
+    "moe_int8_linear": (_I, [_P, _LL, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _LL, _I, _P, _Z, _P]),
+    "moe_int8_packed_expert_weights_bytes": (_Z, [_I, _I, _I]),
+    "moe_int8_pack_expert_weights": (_I, [_P, _P, _P, _I, _I, _I, _P, _P]),
+    "moe_int8_expert_ffn_workspace_size": (_Z, [_I, _I, _I, _I]),
+    "moe_int8_expert_ffn": (_I, [_P, _LL, _I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _LL, _I, _P, _Z, _P]),
     "moe_combine_backward": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
     "moe_router_backward_workspace_size": (_Z, [_I, _I]),
     "moe_router_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _F, _P, _P, _P, _Z, _P]),
@@ -86,6 +96,10 @@ _SIGS = {
     "moe_expert_up_gate_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
     "moe_expert_up_gate_save": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P]),
     "moe_expert_up_gate_backward_saved": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_checkpoint8_save": (_I, [_P, _LL, _I, _I, _I, _P, _I, _P, _P, _P]),
+    "moe_checkpoint8_load": (_I, [_P, _P, _I, _I, _I, _P, _LL, _P]),
+    "moe_checkpoint8_swiglu_backward": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "moe_expert_up_gate_backward_checkpoint8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P]),
     "moe_expert_weight_grads_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
     "moe_expert_weight_grads": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
     "moe_expert_down_shared": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _I, _P, _P]),
@@ -1024,3 +1038,196 @@ def moe_fp4_expert_ffn(x, offsets, packed, F: int, fmt="nv", *, E: int | None = 
                                    _fp4_dtype(x.dtype), out.data_ptr(), ldo, _fp4_dtype(out.dtype),
                                    _fp4_data(ws, 0, torch.uint8, "ws"), ws.numel(), _fp4_stream(stream, x)))
     return out
+
+
+# ----------------------------------------------------------------------------------------- 8-bit experts
+
+
+def moe_int8_quantize(x, *, src=None, codes=None, scales=None, stream=None):
+    """x [*, K] (bf16, fp16 or fp32, row stride free) -> (codes int8 [rows, K], scales fp32 [rows]): scale = amax / 127 of the
+    row, code the whole number nearest to x * 127 / amax. src [rows] int32: x's row of each row, -1 for zeros. A weight's rows are
+    its output channels."""
+    K, ldx = x.shape[-1], _fp4_rows(x, "x")
+    rows = x.shape[0] if src is None else src.numel()
+    codes = _fp4_empty((rows, K), torch.int8, x, stream) if codes is None else codes
+    scales = _fp4_empty((rows,), torch.float32, x, stream) if scales is None else scales
+    _check(_lib.moe_int8_quantize(x.data_ptr(), ldx, x.shape[0], _fp4_data(src, 0, torch.int32, "src"), rows, K, _fp4_dtype(x.dtype),
+                                  _fp4_data(codes, rows * K, torch.int8, "codes"), _fp4_data(scales, rows, torch.float32, "scales"),
+                                  _fp4_stream(stream, x)))
+    return codes, scales
+
+
+def moe_int8_dequantize(codes, scales, *, dtype=torch.bfloat16, out=None, stream=None):
+    """The rows [rows, K] that codes and scales stand for."""
+    if codes.dim() != 2:
+        _fp4_fail("codes: [rows, K]")
+    rows, K = codes.shape
+    out = _fp4_empty((rows, K), dtype, codes, stream) if out is None else out
+    ldo = _fp4_rows(out, "out")
+    if out.shape != codes.shape:
+        _fp4_fail(f"out: [{rows}, {K}]")
+    _check(_lib.moe_int8_dequantize(_fp4_data(codes, rows * K, torch.int8, "codes"), _fp4_data(scales, rows, torch.float32, "scales"),
+                                    rows, K, _fp4_dtype(out.dtype), out.data_ptr(), ldo, _fp4_stream(stream, codes)))
+    return out
+
+
+@functools.lru_cache(maxsize=None)
+def _int8_weight_bytes(G: int, N: int, K: int) -> int:
+    return _lib.moe_int8_packed_weight_bytes(G, N, K)
+
+
+@functools.lru_cache(maxsize=None)
+def _int8_experts_bytes(E: int, h: int, F: int) -> int:
+    return _lib.moe_int8_packed_expert_weights_bytes(E, h, F)
+
+
+def moe_int8_pack_weight(codes, packed=None, stream=None):
+    """8-bit codes [G, N, K] of a weight in the operand layout of moe_int8_linear."""
+    if codes.dim() != 3:
+        _fp4_fail("codes: [G, N, K]")
+    G, N, K = codes.shape
+    need = _int8_weight_bytes(G, N, K)
+    packed = _fp4_bytes(need, codes, stream) if packed is None else packed
+    _check(_lib.moe_int8_pack_weight(_fp4_data(codes, G * N * K, torch.int8, "codes"), G, N, K,
+                                     _fp4_data(packed, need, torch.uint8, "packed"), _fp4_stream(stream, codes)))
+    return packed
+
+
+def moe_int8_linear_workspace_size(G: int, N: int, K: int, rows: int) -> int:
+    return _lib.moe_int8_linear_workspace_size(G, N, K, rows)
+
+
+def _int8_scales(t, G: int, N: int, what: str):
+    if t.dim() != 2 or t.shape != (G, N):
+        _fp4_fail(f"{what}: [{G}, {N}]")
+    return _fp4_data(t, G * N, torch.float32, what)
+
+
+def moe_int8_linear(x, offsets, packed, scales, *, src=None, tile_sched=None, out=None, out_dtype=None, ws=None, stream=None):
+    """out [rows, N]: x's rows [offsets[g], offsets[g + 1]) quantised, times group g's packed 8-bit weight (moe_int8_pack_weight)
+    with its output channels' scales [G, N]. offsets [G + 1] int32 on the device, or None with tile_sched (moe_dispatch's). src as
+    for moe_int8_quantize. out: x's dtype unless out or out_dtype say otherwise. ws: moe_int8_linear_workspace_size bytes, kept
+    across calls."""
+    K, ldx = x.shape[-1], _fp4_rows(x, "x")
+    rows = x.shape[0] if src is None else src.numel()
+    if scales.dim() != 2 or (offsets is not None and offsets.numel() != scales.shape[0] + 1):
+        _fp4_fail("scales: [G, N], offsets: [G + 1]")
+    G, N = scales.shape
+    out = _fp4_empty((rows, N), out_dtype or x.dtype, x, stream) if out is None else out
+    ldo = _fp4_rows(out, "out")
+    if out.shape[0] != rows or out.shape[1] != N:
+        _fp4_fail(f"out: [{rows}, {N}]")
+    ws = _fp4_bytes(_lib.moe_int8_linear_workspace_size(G, N, K, rows), x, stream) if ws is None else ws
+    _check(_lib.moe_int8_linear(x.data_ptr(), ldx, x.shape[0], _fp4_data(src, 0, torch.int32, "src"),
+                                _fp4_data(offsets, 2, torch.int32, "offsets"), _fp4_data(tile_sched, 4, torch.int32, "tile_sched"),
+                                _fp4_data(packed, _int8_weight_bytes(G, N, K), torch.uint8, "packed"), _int8_scales(scales, G, N, "scales"),
+                                G, N, K, rows, _fp4_dtype(x.dtype), out.data_ptr(), ldo, _fp4_dtype(out.dtype),
+                                _fp4_data(ws, 0, torch.uint8, "ws"), ws.numel(), _fp4_stream(stream, x)))
+    return out
+
+
+def moe_int8_pack_expert_weights(gate, up, down, packed=None, stream=None):
+    """8-bit codes of gate and up [E, F, h] and down [E, h, F] in the operand layout of moe_int8_expert_ffn."""
+    if gate.dim() != 3 or up.shape != gate.shape or down.shape != (gate.shape[0], gate.shape[2], gate.shape[1]):
+        _fp4_fail("gate, up: [E, F, h], down: [E, h, F]")
+    E, F, h = gate.shape
+    need = _int8_experts_bytes(E, h, F)
+    packed = _fp4_bytes(need, gate, stream) if packed is None else packed
+    _check(_lib.moe_int8_pack_expert_weights(*(_fp4_data(c, E * F * h, torch.int8, what) for c, what in ((gate, "gate"), (up, "up"), (down, "down"))),
+                                             E, h, F, _fp4_data(packed, need, torch.uint8, "packed"), _fp4_stream(stream, gate)))
+    return packed
+
+
+def moe_int8_expert_ffn_workspace_size(E: int, h: int, F: int, rows: int) -> int:
+    return _lib.moe_int8_expert_ffn_workspace_size(E, h, F, rows)
+
+
+def moe_int8_expert_ffn(x, offsets, packed, gate_scales, up_scales, down_scales, *, src=None, tile_sched=None, out=None, out_dtype=None,
+                        ws=None, stream=None):
+    """out [rows, h]: the SwiGLU expert FFN in 8 bits on the rows of each expert (offsets, tile_sched, src as for
+    moe_int8_linear); gate_scales, up_scales [E, F], down_scales [E, h]; act is quantised by rows inside. ws:
+    moe_int8_expert_ffn_workspace_size bytes, kept across calls."""
+    h, ldx = x.shape[-1], _fp4_rows(x, "x")
+    rows = x.shape[0] if src is None else src.numel()
+    if gate_scales.dim() != 2 or (offsets is not None and offsets.numel() != gate_scales.shape[0] + 1):
+        _fp4_fail("gate_scales: [E, F], offsets: [E + 1]")
+    E, F = gate_scales.shape
+    out = _fp4_empty((rows, h), out_dtype or x.dtype, x, stream) if out is None else out
+    ldo = _fp4_rows(out, "out")
+    if out.shape[0] != rows or out.shape[1] != h:
+        _fp4_fail(f"out: [{rows}, {h}]")
+    ws = _fp4_bytes(_lib.moe_int8_expert_ffn_workspace_size(E, h, F, rows), x, stream) if ws is None else ws
+    _check(_lib.moe_int8_expert_ffn(x.data_ptr(), ldx, x.shape[0], _fp4_data(src, 0, torch.int32, "src"),
+                                    _fp4_data(offsets, 2, torch.int32, "offsets"), _fp4_data(tile_sched, 4, torch.int32, "tile_sched"),
+                                    _fp4_data(packed, _int8_experts_bytes(E, h, F), torch.uint8, "packed"),
+                                    _int8_scales(gate_scales, E, F, "gate_scales"), _int8_scales(up_scales, E, F, "up_scales"),
+                                    _int8_scales(down_scales, E, h, "down_scales"), E, h, F, rows, _fp4_dtype(x.dtype), out.data_ptr(), ldo,
+                                    _fp4_dtype(out.dtype), _fp4_data(ws, 0, torch.uint8, "ws"), ws.numel(), _fp4_stream(stream, x)))
+    return out
+
+
+# ------------------------------------------------------------------------------ activation checkpoints in 8 bits
+
+
+def moe_checkpoint8_save(x, *, tile_sched=None, E: int = 0, codes=None, scales=None, stream=None):
+    """x [rows, C] (bf16, fp16 or fp32, row stride free) -> (codes int8 [rows, C], scales fp32 [rows, ceil(C / 128)]): what a forward
+    keeps for its backward. With tile_sched (moe_dispatch's) of E experts only its rows."""
+    (rows, C), ldx = x.shape, _fp4_rows(x, "x")
+    nb = (C + 127) // 128
+    codes = _fp4_empty((rows, C), torch.int8, x, stream) if codes is None else codes
+    scales = _fp4_empty((rows, nb), torch.float32, x, stream) if scales is None else scales
+    _check(_lib.moe_checkpoint8_save(x.data_ptr(), ldx, rows, C, _fp4_dtype(x.dtype), _fp4_data(tile_sched, 4, torch.int32, "tile_sched"), E,
+                                     _fp4_data(codes, rows * C, torch.int8, "codes"), _fp4_data(scales, rows * nb, torch.float32, "scales"),
+                                     _fp4_stream(stream, x)))
+    return codes, scales
+
+
+def moe_checkpoint8_load(codes, scales, *, dtype=torch.bfloat16, out=None, stream=None):
+    """The values [rows, C] that a checkpoint stands for."""
+    if codes.dim() != 2:
+        _fp4_fail("codes: [rows, C]")
+    rows, C = codes.shape
+    out = _fp4_empty((rows, C), dtype, codes, stream) if out is None else out
+    ldo = _fp4_rows(out, "out")
+    if out.shape != codes.shape:
+        _fp4_fail(f"out: [{rows}, {C}]")
+    _check(_lib.moe_checkpoint8_load(_fp4_data(codes, rows * C, torch.int8, "codes"),
+                                     _fp4_data(scales, rows * ((C + 127) // 128), torch.float32, "scales"), rows, C, _fp4_dtype(out.dtype),
+                                     out.data_ptr(), ldo, _fp4_stream(stream, codes)))
+    return out
+
+
+def _checkpoint8_data(codes, scales, d_act):
+    """Rows, F and the checked addresses of a kept gu [rows, gu_cols(F)] and of d_act [rows, F]."""
+    if codes.dim() != 2 or d_act.dim() != 2 or codes.shape != (d_act.shape[0], gu_cols(d_act.shape[1])):
+        _fp4_fail("codes: [rows, gu_cols(F)], d_act: [rows, F]")
+    rows, F = d_act.shape
+    return rows, F, (_fp4_data(codes, codes.numel(), torch.int8, "codes"),
+                     _fp4_data(scales, codes.numel() // 128, torch.float32, "scales"), _fp4_data(d_act, rows * F, torch.bfloat16, "d_act"))
+
+
+def moe_checkpoint8_swiglu_backward(codes, scales, d_act, *, tile_sched=None, E: int = 0, d_gu=None, act=None, stream=None):
+    """(d_gu [rows, gu_cols(F)], act [rows, F]), bf16: the SwiGLU backward from pre-activations that moe_checkpoint8_save kept, and act
+    from the same. With tile_sched (moe_dispatch's) of E experts only its rows."""
+    rows, F, data = _checkpoint8_data(codes, scales, d_act)
+    d_gu = _fp4_empty((rows, gu_cols(F)), torch.bfloat16, d_act, stream) if d_gu is None else d_gu
+    act = _fp4_empty((rows, F), torch.bfloat16, d_act, stream) if act is None else act
+    _check(_lib.moe_checkpoint8_swiglu_backward(*data, _fp4_data(tile_sched, 4, torch.int32, "tile_sched"), E, F, rows,
+                                                _fp4_data(d_gu, codes.numel(), torch.bfloat16, "d_gu"),
+                                                _fp4_data(act, rows * F, torch.bfloat16, "act"), _fp4_stream(stream, d_act)))
+    return d_gu, act
+
+
+def moe_expert_up_gate_backward_checkpoint8(codes, scales, d_act, tile_sched, packed_bwd, E: int, h: int, *, d_gu=None, act=None, d_buf=None,
+                                            stream=None):
+    """moe_expert_up_gate_backward_saved from pre-activations kept in 8 bits: (d_gu, act, d_buf)."""
+    rows, F, data = _checkpoint8_data(codes, scales, d_act)
+    d_gu = _fp4_empty((rows, gu_cols(F)), torch.bfloat16, d_act, stream) if d_gu is None else d_gu
+    act = _fp4_empty((rows, F), torch.bfloat16, d_act, stream) if act is None else act
+    d_buf = _fp4_empty((rows, h), torch.bfloat16, d_act, stream) if d_buf is None else d_buf
+    _check(_lib.moe_expert_up_gate_backward_checkpoint8(*data, _fp4_data(tile_sched, 4, torch.int32, "tile_sched"),
+                                                        _fp4_data(packed_bwd, _lib.moe_packed_weights_backward_bytes(E, h, F, MOE_BF16), torch.uint8, "packed_bwd"),
+                                                        E, h, F, rows, _fp4_data(d_gu, codes.numel(), torch.bfloat16, "d_gu"),
+                                                        _fp4_data(act, rows * F, torch.bfloat16, "act"), _fp4_data(d_buf, rows * h, torch.bfloat16, "d_buf"),
+                                                        _fp4_stream(stream, d_act)))
+    return d_gu, act, d_buf
