@@ -17,10 +17,10 @@
 //
 // Every wait is bounded, as in the bf16 grouped GEMM: one that runs out latches MOE_ERR_TIMEOUT, every role leaves, the
 // copies and MMAs in flight are waited for and the tensor memory is freed.
-#include <cudaTypedefs.h>
 #include <algorithm>
 #include "fp4.cuh"
 #include "tc_elect.cuh"
+#include "tc_map.cuh"
 
 namespace moe {
 namespace fp4 {
@@ -873,18 +873,6 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
 // ---------------------------------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------------------------------
-static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
-}
-
 // Codes [rows][pitch bytes], boxes of box_rows x 128 bytes with 128-byte swizzling; zero past the pitch and the rows.
 static int codes_map(CUtensorMap* m, const void* base, long long rows, int pitch, int box_rows) {
     auto fn = encode_fn();

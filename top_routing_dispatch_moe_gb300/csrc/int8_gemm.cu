@@ -3,9 +3,12 @@
 //   y[r, n] = (sum_k A[r, k] W[g, n, k]) * a_scale[r] * w_scale[g, n]     for the rows r of group g
 #include <algorithm>
 #include "int8.cuh"
+#include "tc_elect.cuh"
+#include "tc_map.cuh"
 
 namespace moe {
 namespace int8 {
+using namespace moe::tc;
 
 constexpr int MAX_G = 1024;
 
@@ -210,7 +213,357 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_rows_kernel(const Params p
     }
 }
 
+// ---------------------------------------------------------------------------------------------------
+// many rows: fp16 tensor-core products of whole numbers, two SMs to a tile
+// ---------------------------------------------------------------------------------------------------
+// The chip's tensor cores have no integer kind. Whole numbers up to 2^11 are fp16 numbers, their products are exact in fp32, and so are
+// sums below 2^24: the rows' codes are kept as fp16 (written so by the quantisation), the weights stay bytes in memory and become fp16
+// on the chip, on their way into tensor memory, from where tcgen05.mma takes its first operand. The product is turned over for that:
+// the channels are its rows (M) and a group's rows its columns (N), which also fits N to the group: 32 to 256 in steps of 32.
+//
+// A cluster of two CTAs computes 256 channels x up to 256 rows with tcgen05.mma.cta_group::2: each converts its own 128 channels and
+// stages half of the rows. A persistent CTA per SM with eighteen warps:
+//   warp 0      producer: per stage of 64 columns 8 KB of packed weight by one bulk copy, and the CTA's half of the rows by TMA;
+//   warp 1      (of the even CTA) the MMAs of a stage;
+//   warps 2-9   epilogue, two to a quarter of the tensor memory lanes, 64 columns at a time in turn: a lane is a channel, a column a row
+//               of the output; SwiGLU's gate and up are neighbouring lanes and exchange halves;
+//   warps 10-17 converters, two to a quarter, stages in turn: a lane reads its channel's 64 bytes, puts each under 0x64 (the fp16 number
+//               1024 + byte), subtracts 1152 and stores 32 columns of tensor memory.
+// Tensor memory: two accumulators of 256 columns that share 128 (the epilogue reads the shared ones first and hands them back), and four
+// stages of converted weights, 32 columns each.
+constexpr int P_ROWS = 256;
+constexpr int EPI_WARPS = 8, CONV_WARPS = 8;
+constexpr int P_THREADS = 32 * (2 + EPI_WARPS + CONV_WARPS);
+constexpr int STAGES = 8;
+constexpr int ROWS_BYTES = P_ROWS / 2 * STAGE_K * 2;           // 16 KB
+constexpr int A_BUFS = 4, A_COLS = STAGE_K / 2;
+constexpr int ACC2 = 128, A_COL = ACC2 + P_ROWS;
+constexpr int TMEM_COLS = 512;
+static_assert(A_COL + A_BUFS * A_COLS == TMEM_COLS, "tensor memory columns");
+constexpr int P_SMEM = 1024 + STAGES * (PIECE + ROWS_BYTES) + 256 + GROUPS_INTS * 4 + 16;
+static_assert(P_SMEM <= 227 * 1024, "shared memory per CTA");
+
+// D fp32 (bits 4-5 = 1), A and B fp16 (0), K-major, N >> 3 at bits 17-22, M = 256 at bits 24-28.
+__device__ __forceinline__ uint32_t idesc_pair(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((256u >> 4) << 24); }
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+                 "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+                 "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+                 "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]) : "memory");
+}
+
+// Item w: group by group, 256-channel tile next, row tile fastest: pairs that run together share a weight tile. A group's row tiles
+// are of one size, a multiple of 32 (the last may be shorter).
+struct Item { int g, ch, row0, row1; };
+__device__ __forceinline__ Item map_item(const Params& p, const Groups& gs, int CT, int w, int& g) {
+    g = group_of(gs.first, p.G, CT, w, g);
+    const int nt = gs.first[g + 1] - gs.first[g], local = w - gs.first[g] * CT, ch = local / nt, t = local - ch * nt;
+    const int n = gs.end[g] - gs.beg[g], per = ((n + nt - 1) / nt + 31) & ~31;
+    return Item{g, ch, gs.beg[g] + t * per, gs.beg[g] + min(n, t * per + per)};
+}
+
+// 64 columns of the accumulator at tcol, the rows row0 .. of the output (n of them, at least one); this lane's channel is `ch`. `read`
+// runs once the columns are in registers.
+template <int EPI, typename Fn>
+__device__ __forceinline__ void epilogue_chunk(const Params& p, int g, uint32_t tcol, int ch, int row0, int n, float scale, Fn read) {
+    const int lane = threadIdx.x & 31;
+    const bool mine = ch < p.N;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float v[32];
+        tmem_ld32(tcol + 32 * h, v);
+        if (h == 1) read();
+        const int r0 = row0 + 32 * h, nr = n - 32 * h;
+        if (nr <= 0) continue;
+        const float xs = lane < nr ? p.a_scales[r0 + lane] : 0.f;
+        if constexpr (EPI == EPI_OUT) {
+            const int el = p.out_dtype == MOE_F32 ? 4 : 2;
+            uint8_t* at = static_cast<uint8_t*>(p.out) + ((size_t)r0 * p.ld + ch) * el;
+            const size_t step = (size_t)p.ld * el;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const float y = v[j] * __shfl_sync(0xffffffffu, xs, j) * scale;
+                if (mine && j < nr) {
+                    if (p.out_dtype == MOE_F32) *reinterpret_cast<float*>(at) = y;
+                    else if (p.out_dtype == MOE_BF16) *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16_rn(y);
+                    else *reinterpret_cast<__half*>(at) = __float2half_rn(y);
+                }
+                at += step;
+            }
+        } else {
+            // even lanes hold gates, odd lanes the ups of the same features: of two rows, the even lane finishes the first
+            const int F = p.N / 2, odd = lane & 1;
+            float* at = static_cast<float*>(p.out) + (size_t)(r0 + odd) * F + (ch >> 1);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+                const float y0 = v[j] * __shfl_sync(0xffffffffu, xs, j) * scale, y1 = v[j + 1] * __shfl_sync(0xffffffffu, xs, j + 1) * scale;
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
+                const float a = swiglu(odd ? got : y0, odd ? y1 : got);
+                if (mine && j + odd < nr) *at = a;
+                at += 2 * (size_t)F;
+            }
+        }
+    }
+}
+
+template <int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
+pair_kernel(const __grid_constant__ CUtensorMap tm128, const __grid_constant__ CUtensorMap tm16, const Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sX = smem_u32(smem), sW = sX + STAGES * ROWS_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * (PIECE + ROWS_BYTES));
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto afull = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
+    const uint32_t tfull = bar0 + 8u * (2 * STAGES + A_BUFS), tempty = tfull + 8u, mma_done = tempty + 8u;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + A_BUFS + 3);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const Groups gs = groups_at(reinterpret_cast<int*>(bars + 32));
+
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
+        for (int b = 0; b < A_BUFS; ++b) mbar_init(afull(b), 2 * 4);
+        mbar_init(tfull, 1);
+        mbar_init(tempty, 2 * EPI_WARPS);
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_tmap(&tm128);
+        prefetch_tmap(&tm16);
+    }
+    // (a programmatic dependent of the quantisation: the groups, the set-up and the first stages of weights do not wait for it)
+    find_groups<P_THREADS>(p, P_ROWS, gs);
+    if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+    tc_fence_before();
+    cluster_sync_all();                          // barriers initialised and both CTAs' tensor memory allocated
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t peer_abort = map_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
+    const int CT = (p.NB + 1) >> 1, NC = gridDim.x >> 1, cid = blockIdx.x >> 1, total = uniform(gs.first[p.G] * CT);
+    if (warp != 0) {
+        pdl_wait();
+        pdl_trigger();
+    }
+
+    if (warp == 0) {
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, last_par = 0;
+        bool ok = true, ready = false;              // ready: the next ring stage was seen free
+        int at = 0;
+        for (int w = cid; w < total && ok; w += NC) {
+            const Item it = map_item(p, gs, CT, w, at);
+            const int half = uniform(((it.row1 - it.row0 + 31) & ~31) >> 1), row = uniform(it.row0) + (int)rank * half;
+            const int nb = uniform(2 * it.ch + (int)rank);
+            const bool some = nb < p.NB;             // (the odd CTA of the last tile may have no channels)
+            const uint8_t* w0 = p.w + ((size_t)uniform(it.g) * p.NB + nb) * p.KST * PIECE;
+            const uint32_t tx = (uint32_t)(half * STAGE_K * 2 + (some ? PIECE : 0));
+            auto weights = [&](int st, int kb) {
+                expect_elected(full(st), tx);
+                if (some) bulk_elected(sW + st * PIECE, w0 + (size_t)kb * PIECE, PIECE, full(st));
+            };
+            int early = 0;                          // stages whose weights are on their way before the rows' codes are there
+            if (w == cid) {
+                for (; early < min(STAGES, p.KST); ++early) weights(early, early);
+                pdl_wait();
+                pdl_trigger();
+            }
+            for (int kb = 0; kb < p.KST; ++kb) {
+                if (kb >= early) {
+                    if (!ready) ok = wait_warp_pair(empty(stage), phase ^ 1u, p.wait_limit, abort_flag, peer_abort, p.err, 0x340u);
+                    if (!ok) break;
+                    weights(stage, kb);
+                }
+                const uint32_t f = full(stage), sx = sX + stage * ROWS_BYTES;
+                if (half == 128) tma_elected(sx, &tm128, kb * STAGE_K, row, f);
+                else
+                    for (int b = 0; b < half; b += 16) tma_elected(sx + b * 128, &tm16, kb * STAGE_K, row + b, f);
+                issued |= 1u << stage;
+                last_par = (last_par & ~(1u << stage)) | (phase << stage);
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                ready = kb + 1 >= early && test_warp(empty(stage), phase ^ 1u);
+            }
+        }
+        if (total <= cid) {                          // (no item: the wait that every thread makes)
+            pdl_wait();
+            pdl_trigger();
+        }
+        if (lane == 0)
+            for (int s = 0; s < STAGES; ++s)        // every issued copy has landed before the CTA exits
+                if (issued & (1u << s)) drain_phase(full(s), (last_par >> s) & 1u, p.err, 0x341u);
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            int stage = 0, b = 0, iter = 0, at = 0;
+            uint32_t phase = 0, bphase = 0;
+            bool ok = true, ready = false;
+            for (int w = cid; w < total && ok; w += NC, ++iter) {
+                const Item it = map_item(p, gs, CT, w, at);
+                const uint32_t id = idesc_pair(uniform((it.row1 - it.row0 + 31) & ~31)), d = tm + (iter & 1) * ACC2;
+                for (int kb = 0; kb < p.KST; ++kb) {
+                    if (!ready)
+                        ok = (kb > 0 || wait_warp_pair(tempty, (iter & 1) ^ 1u, p.wait_limit, abort_flag, peer_abort, p.err, 0x350u)) &&
+                             wait_warp_pair(afull(b), bphase, p.wait_limit, abort_flag, peer_abort, p.err, 0x351u) &&
+                             (test_warp(full(stage), phase) ||
+                              wait_warp_pair(full(stage), phase, p.wait_limit, abort_flag, peer_abort, p.err, 0x352u));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t s0 = stage, a = tm + A_COL + b * A_COLS;
+                    const bool last = kb + 1 == p.KST;
+                    const uint64_t db = sw128_desc(sX + s0 * ROWS_BYTES);
+                    mma_pair(d, a, db, id, kb != 0);
+                    mma_pair(d, a + 8, db + 2, id, 1u);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (++b == A_BUFS) { b = 0; bphase ^= 1u; }
+                    const bool t0 = test_phase(full(stage), phase), t1 = test_phase(afull(b), bphase);
+                    mma_pair(d, a + 16, db + 4, id, 1u);
+                    mma_pair(d, a + 24, db + 6, id, 1u);
+                    commit_pair_elected(empty(s0));
+                    if (last) commit_pair_elected(tfull);
+                    ready = __all_sync(0xffffffffu, t0 && t1 && !last);
+                }
+            }
+            commit_pair_elected(mma_done);          // both CTAs learn when every MMA has finished
+        }
+    } else if (warp >= 2 + EPI_WARPS) {
+        const int quarter = 32 * (warp & 3), turn = (warp - 2 - EPI_WARPS) >> 2;
+        const uint32_t afull0 = map_rank(afull(0), 0);
+        int i = 0;                                  // stages so far, this CTA's in all
+        bool ok = true;
+        for (int w = cid; w < total && ok; w += NC) {
+            for (int kb = 0; kb < p.KST; ++kb, ++i) {
+                if ((i & 1) != turn) continue;
+                const int st = i % STAGES, b = i % A_BUFS, old = (i - A_BUFS) % STAGES;
+                ok = test_warp(full(st), (i / STAGES) & 1) ||
+                     wait_warp_pair(full(st), (i / STAGES) & 1, p.wait_limit, abort_flag, peer_abort, p.err, 0x360u);
+                if (!ok) break;
+                uint32_t q[16], v[32];
+                const uint32_t src = sW + st * PIECE + (quarter + lane) * 16;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) ld_shared_v4(src + c * (BLOCK_N * 16), q + 4 * c);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const __half2 off = __float2half2_rn(-1152.f);
+                    const uint32_t lo = __byte_perm(q[c], 0x64646464u, 0x4140), hi = __byte_perm(q[c], 0x64646464u, 0x4342);
+                    const __half2 a = __hadd2(*reinterpret_cast<const __half2*>(&lo), off), e = __hadd2(*reinterpret_cast<const __half2*>(&hi), off);
+                    v[2 * c] = *reinterpret_cast<const uint32_t*>(&a);
+                    v[2 * c + 1] = *reinterpret_cast<const uint32_t*>(&e);
+                }
+                if (i >= A_BUFS) {                  // the buffer's last MMAs have completed
+                    const uint32_t par = ((i - A_BUFS) / STAGES) & 1;
+                    ok = test_warp(empty(old), par) || wait_warp_pair(empty(old), par, p.wait_limit, abort_flag, peer_abort, p.err, 0x361u);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                tmem_st32(tmem + ((uint32_t)quarter << 16) + A_COL + b * A_COLS, v);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_pair(afull0 + 8u * b);
+            }
+        }
+    } else {
+        const int quarter = 32 * (warp & 3), half = (warp - 2) >> 2;
+        const uint32_t tempty0 = map_rank(tempty, 0);
+        int iter = 0, at = 0;
+        for (int w = cid; w < total; w += NC, ++iter) {
+            const Item it = map_item(p, gs, CT, w, at);
+            const int ch = (2 * it.ch + (int)rank) * BLOCK_N + quarter + lane, F = p.N / 2;
+            float scale = 0.f;
+            if (ch < p.N) scale = EPI == EPI_OUT ? p.w_scales[(size_t)it.g * p.N + ch] : ((ch & 1) ? p.w_scales_up : p.w_scales)[(size_t)it.g * F + (ch >> 1)];
+            if (!wait_warp_pair(tfull, iter & 1, p.wait_limit, abort_flag, peer_abort, p.err, 0x370u)) break;
+            tc_fence_after();
+            const uint32_t tbase = tmem + (iter & 1) * ACC2 + ((uint32_t)quarter << 16);
+            auto hand_back = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_pair(tempty0);
+            };
+            // the chunks whose columns the next tile shares come first: the last two of an even tile, the first two of an odd
+            const int first = (iter & 1 ? 0 : 2) + half, second = first ^ 2, n = it.row1 - it.row0;
+            const bool warp_live = ch - lane < p.N;
+            if (warp_live && 64 * first < n)
+                epilogue_chunk<EPI>(p, it.g, tbase + 64 * first, ch, it.row0 + 64 * first, n - 64 * first, scale, hand_back);
+            else hand_back();
+            if (warp_live && 64 * second < n)
+                epilogue_chunk<EPI>(p, it.g, tbase + 64 * second, ch, it.row0 + 64 * second, n - 64 * second, scale, [] {});
+        }
+    }
+    cluster_sync_all();                          // every role of both CTAs has left its loop
+    if (warp == 1 && lane == 0) drain_phase(mma_done, 0, p.err, 0x353u);
+    tc_fence_before();
+    cluster_sync_all();                      // MMAs done, both CTAs' copies landed, all arrivals on the other CTA made
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, TMEM_COLS);
+    }
+}
+
+// Row codes [rows][width] fp16, boxes of box_rows x 64 columns with 128-byte swizzling; zero past the rows.
+static int rows_map(CUtensorMap* m, const void* base, long long rows, int width, int box_rows) {
+    auto fn = encode_fn();
+    MOE_REQUIRE(fn, MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable from the driver");
+    cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)width * 2};
+    cuuint32_t box[2] = {STAGE_K, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    MOE_REQUIRE(r == CUDA_SUCCESS, MOE_ERR_CUDA, "cuTensorMapEncodeTiled (8-bit rows) failed (%d) rows=%lld width=%d", (int)r, rows, width);
+    return MOE_OK;
+}
+
+template <int EPI>
+static int launch_pair(const Params& p, cudaStream_t s) {
+    static int clusters[64];                     // resident pairs, in the context they were asked for
+    static unsigned long long attr_ctx[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return set_error(MOE_ERR_CUDA, "int8 product: no usable current device");
+    const unsigned long long ctx = context_id();
+    if (!clusters[dev] || ctx == 0 || attr_ctx[dev] != ctx) {
+        cudaError_t e = cudaFuncSetAttribute(pair_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
+        if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "int8 product smem attribute: %s", cudaGetErrorString(e));
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * (num_sms() / 2));
+        cfg.blockDim = dim3(P_THREADS);
+        cfg.dynamicSmemBytes = P_SMEM;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, pair_kernel<EPI>, &cfg);
+        if (e != cudaSuccess || n <= 0) return set_error(MOE_ERR_CUDA, "int8 product: no resident cluster of two CTAs (%s)", cudaGetErrorString(e));
+        clusters[dev] = std::min(n, num_sms() / 2);
+        attr_ctx[dev] = context_id();
+    }
+    CUtensorMap m16, m128;
+    const int width = p.KST * STAGE_K;
+    if (int rc = rows_map(&m16, p.a, p.rows, width, 16)) return rc;
+    m128 = m16;                                  // (no tile of 256 rows: the map of whole halves is not used)
+    if (p.rows >= 128)
+        if (int rc = rows_map(&m128, p.a, p.rows, width, 128)) return rc;
+    return check_launch(launch_pdl(pair_kernel<EPI>, dim3(2 * clusters[dev]), dim3(P_THREADS), P_SMEM, s, m128, m16, p),
+                        EPI == EPI_SWIGLU ? "int8 pair_kernel<swiglu>" : "int8 pair_kernel");
+}
+
+// Dot products on the CUDA cores where the groups have few rows.
+static bool few_rows(int rows, int G) { return rows <= FEW_ROWS * std::min(G, 2); }
+static int operand_form(int rows, int G) { return few_rows(rows, G) ? FORM_BYTES : FORM_F16; }
+
 static int launch_product(const Params& p, int epi, cudaStream_t s) {
+    MOE_REQUIRE(((long long)p.rows / P_ROWS + p.G) * cdiv(p.NB, 2) < (1LL << 31), MOE_ERR_INVALID_ARG,
+                "8-bit product: %d rows by %d channels are over 2^31 tiles", p.rows, p.N);
+    if (!few_rows(p.rows, p.G)) return epi == EPI_OUT ? launch_pair<EPI_OUT>(p, s) : launch_pair<EPI_SWIGLU>(p, s);
     auto go = [&](auto kernel) {
         int per_sm = 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, FEW_THREADS, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
@@ -277,7 +630,7 @@ extern "C" int moe_int8_linear(const void* x, long long ldx, int x_rows, const i
     p.a = ws; p.a_scales = int8::scales_at(ws, rows, K);
     p.w_scales = w_scales; p.N = N; p.ld = ldo; p.out_dtype = out_dtype; p.out = out;
     p.err = err; p.wait_limit = wait_limit();
-    if (int rc = int8::launch_quantize(x, ldx, x_rows, src, rows, K, dtype, int8::FORM_BYTES, ws, int8::scales_at(ws, rows, K), err, s)) return rc;
+    if (int rc = int8::launch_quantize(x, ldx, x_rows, src, rows, K, dtype, int8::operand_form(rows, G), ws, int8::scales_at(ws, rows, K), err, s)) return rc;
     return int8::launch_product(p, int8::EPI_OUT, s);
 }
 
@@ -327,9 +680,9 @@ extern "C" int moe_int8_expert_ffn(const void* x, long long ldx, int x_rows, con
     p.a = w.x; p.a_scales = int8::scales_at(w.x, rows, h);
     p.w_scales = gate_scales; p.w_scales_up = up_scales; p.N = 2 * F; p.out_dtype = MOE_F32; p.out = w.act;
     p.err = err; p.wait_limit = wait_limit();
-    if (int rc = int8::launch_quantize(x, ldx, x_rows, src, rows, h, dtype, int8::FORM_BYTES, w.x, int8::scales_at(w.x, rows, h), err, s)) return rc;
+    if (int rc = int8::launch_quantize(x, ldx, x_rows, src, rows, h, dtype, int8::operand_form(rows, E), w.x, int8::scales_at(w.x, rows, h), err, s)) return rc;
     if (int rc = int8::launch_product(p, int8::EPI_SWIGLU, s)) return rc;
-    if (int rc = int8::launch_quantize(w.act, F, rows, nullptr, rows, F, MOE_F32, int8::FORM_BYTES, w.a, int8::scales_at(w.a, rows, F), err, s))
+    if (int rc = int8::launch_quantize(w.act, F, rows, nullptr, rows, F, MOE_F32, int8::operand_form(rows, E), w.a, int8::scales_at(w.a, rows, F), err, s))
         return rc;
     p.w += L.down_off; p.NB = L.down.NB; p.KST = L.down.KST;
     p.a = w.a; p.a_scales = int8::scales_at(w.a, rows, F);
