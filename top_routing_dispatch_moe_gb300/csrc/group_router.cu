@@ -112,6 +112,30 @@ __device__ __noinline__ int choose_exact(const Args& a, const float* L, const fl
     return my_id;
 }
 
+// The order of the chosen and the next best where only neighbours among them lie that near (sigmoid scores: each lane j <= k computes
+// its own in 64 bits, a hundredth of what the whole choice costs). id, l: lane j's expert and its logit, of
+// `n` in all; returns lane j's expert after ordering.
+__device__ __noinline__ int order_exact(float l, const float* bias, int id, int n) {
+    const int lane = threadIdx.x & 31;
+    double v = -INFINITY;
+    if (lane < n) {
+        v = l > -INFINITY ? 1.0 / (1.0 + exp(-(double)l)) + (double)bias[id] : (double)kMasked;
+        if (!(v == v)) v = (double)kMasked;
+    }
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+        const double o = __shfl_sync(0xffffffffu, v, j);
+        const int oi = __shfl_sync(0xffffffffu, id, j);
+        rank += o > v || (o == v && oi < id);
+    }
+    int out = id;
+    for (int j = 0; j < n; ++j) {
+        const int r = __shfl_sync(0xffffffffu, rank, j), oi = __shfl_sync(0xffffffffu, id, j);
+        if (lane == r) out = oi;
+    }
+    return out;
+}
+
 template <int NPL>
 __global__ void __launch_bounds__(kWarps * 32)
 group_gate_kernel(const Args a) {
@@ -267,21 +291,24 @@ group_gate_kernel(const Args a) {
 #pragma unroll
         for (int i = 1; i < NPL; ++i)
             if (key[i] > lmax) { lmax = key[i]; lslot = i; ls = s[i]; }
-        // k rounds, and one more that tells how near the best that was left out is
+        // k rounds; with a bias one more, and a look at what is left then, which tell how near the scores are that were left out
         int my_id = 0;
         float my_s = 0.f, sum = 0.f, pv_before = 0.f, m_before = 0.f;
-        bool close = false;
-        for (int j = 0; j <= a.k; ++j) {
-            if (j == a.k && !a.bias) break;
+        bool close = false, past = false;     // chosen (or the first left out) close to each other; the first two left out
+        // what two neighbours' difference has to pass: the error of s (a sigmoid's exponential and two roundings, of which the exponential's
+        // counts with 1 - s; softmax: the exponential, the difference of the logits, the sum) and that of adding the bias
+        auto near_by = [&](float x, float sx, float y, float sy) {
+            const float err = a.sigmoid ? sx * (1.4e-7f + 2.5e-7f * (1.f - sx)) + sy * (1.4e-7f + 2.5e-7f * (1.f - sy)) : 1e-6f * (sx + sy) + 6e-8f;
+            return !(x - y > err + 6.1e-8f * (fabsf(x) + fabsf(y))) && x > 0.1f * kMasked;
+        };
+        const int rounds = a.k + (a.bias ? 1 : 0);
+        for (int j = 0; j < rounds; ++j) {
             const unsigned m = __reduce_max_sync(0xffffffffu, lmax);
+            if (m == 0u) break;               // (no expert is left after the k)
             const int owner = __ffs(__ballot_sync(0xffffffffu, lmax == m)) - 1;
             const float pv = __shfl_sync(0xffffffffu, ls, owner), mv = value_of(m);
             const int id = __shfl_sync(0xffffffffu, e0 + lslot, owner);
-            if (a.bias && j > 0 && m != 0u) {
-                const float tol = 1e-6f * (pv + pv_before) + 1.2e-7f * (fabsf(mv) + fabsf(m_before)) + (a.sigmoid ? 0.f : 6e-8f);
-                close |= !(m_before - mv > tol) && m_before > 0.1f * kMasked;
-            }
-            if (j == a.k) break;
+            if (a.bias && j > 0) close |= near_by(m_before, pv_before, mv, pv);
             pv_before = pv;
             m_before = mv;
             if (lane == owner) {
@@ -299,10 +326,31 @@ group_gate_kernel(const Args a) {
                 my_id = id;
                 my_s = pv;
             }
-            sum += pv;
+            if (j < a.k) sum += pv;
         }
         if (near || close) {
-            my_id = choose_exact(a, L, a.bias, npl);
+            int n = a.k;                      // the candidates of a cheap ordering: the chosen and the next, if nothing comes near that
+            if (close) {
+                const unsigned m = __reduce_max_sync(0xffffffffu, lmax);
+                const int owner = __ffs(__ballot_sync(0xffffffffu, lmax == m)) - 1;
+                if (m != 0u) past = near_by(m_before, pv_before, value_of(m), __shfl_sync(0xffffffffu, ls, owner));
+                n = min(rounds, a.top_groups * a.per);
+            }
+            if (near || past || !a.sigmoid) {
+                my_id = choose_exact(a, L, a.bias, npl);
+            } else {
+                float my_l = 0.f;
+                for (int j = 0; j < n; ++j) {
+                    const int id = __shfl_sync(0xffffffffu, my_id, j);
+                    float v = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NPL; ++i)
+                        if (e0 + i == id && i < npl) v = L[i];
+                    v = __shfl_sync(0xffffffffu, v, id / npl);
+                    if (lane == j) my_l = v;
+                }
+                my_id = order_exact(my_l, a.bias, my_id, n);
+            }
             // the chosen experts' scores, from the lanes that hold them
             sum = 0.f;
             for (int j = 0; j < a.k; ++j) {

@@ -36,13 +36,25 @@ class MoELayer:
     before, e.g. calibrated to 448 * 6 / the largest magnitude expected; None: 1; copied at construction, where their
     inverses go into the experts' factors: another calibration is another layer). The FFN reads x through the dispatch's
     row indices (the send buffer is written all the same); both products and the quantisations between them are the stage
-    "up_gate", and "down" is empty."""
+    "up_gate", and "down" is empty.
+
+    experts="int8" (bf16, forward only) holds the experts as 8-bit integers with a scale for each output channel, quantised at
+    construction; the tokens' rows and the activations inside the FFN get a scale each in every call.
+
+    routing="group": the experts form `groups` groups, a token's k come from the top_groups best of them; gating "sigmoid" or
+    "softmax" names the scores, the bias takes part in the choice alone, and gates are renormalised (renorm) and times
+    route_scale (moe_group_router; group_best: how many of a group's scores make its own).
+
+    checkpoint="int8" (with backward=True): forward(save=True) keeps the pre-activations in 8 bits (a scale for 128 columns) instead
+    of bf16, and the backward computes act from them again. The bf16 pre-activations then pass through `scratch`, a bf16 tensor of
+    checkpoint_scratch(...) elements that layers run one after the other may share (None: the layer's own)."""
 
     STAGES = ("router", "dispatch", "up_gate", "down", "shared_up_gate", "shared_down", "combine")
 
     def __init__(self, *, T, h, E, k, F, gating, cf, R, alpha, w_r, bias, w_gate, w_up, w_down,
                  shared=None, device="cuda", routing="token", backward=False, payload="bf16", fuse_combine=False,
-                 experts="dtype", fp4_gscale=None, fp4_act_gscale=None):
+                 experts="dtype", fp4_gscale=None, fp4_act_gscale=None, groups=1, top_groups=1, group_best=2, renorm=True,
+                 route_scale=1.0, checkpoint="dtype", scratch=None):
         self.T, self.h, self.E, self.k, self.F = T, h, E, k, F
         self.gating, self.R, self.alpha = gating, R, alpha
         self.C = capacity_slots(cf, k, T, E)
@@ -53,14 +65,23 @@ class MoELayer:
         self.w_r = w_r
         self.w_r_packed = moe.moe_pack_router_weight(w_r)    # the router's operand layout, packed once
         self.bias = bias
-        if experts not in ("dtype", "nvfp4", "mxfp4"):
-            raise ValueError("experts: 'dtype', 'nvfp4' or 'mxfp4'")
-        self.fp4 = None if experts == "dtype" else experts[:2]
+        if experts not in ("dtype", "nvfp4", "mxfp4", "int8"):
+            raise ValueError("experts: 'dtype', 'nvfp4', 'mxfp4' or 'int8'")
+        self.fp4 = experts[:2] if experts in ("nvfp4", "mxfp4") else None
+        self.int8 = experts == "int8"
+        if self.int8 and (dt != torch.bfloat16 or backward or payload != "bf16" or fuse_combine):
+            raise ValueError("experts in 8 bits: bf16 with the bf16 send buffer, the separate combine and no backward")
+        if routing == "group" and gating not in ("sigmoid", "softmax"):
+            raise ValueError("routing='group': gating 'sigmoid' or 'softmax'")
+        self.group = dict(groups=groups, top_groups=top_groups, best=group_best, score=gating, renorm=renorm, scale=route_scale)
+        if checkpoint not in ("dtype", "int8") or (checkpoint == "int8" and not backward):
+            raise ValueError("checkpoint: 'dtype', or 'int8' with backward=True")
+        self.checkpoint = checkpoint
         if self.fp4 and (dt != torch.bfloat16 or backward or payload != "bf16" or fuse_combine):
             raise ValueError("experts in 4 bits: bf16 with the bf16 send buffer, the separate combine and no backward")
         # (the layer's own: the alphas hold their inverses, and the kernels read them in every call)
         self.fp4_gscale, self.fp4_act_gscale = (None if g is None else g.clone() for g in (fp4_gscale, fp4_act_gscale))
-        pack = moe.moe_pack_expert_weights if self.fp4 is None else self._pack_fp4
+        pack = self._pack_fp4 if self.fp4 else self._pack_int8 if self.int8 else moe.moe_pack_expert_weights
         self.packed = pack(w_gate, w_up, w_down)
         self.shared_packed = pack(*shared) if shared is not None else None
         # the dgrad GEMMs' weight operands (only when the layer will run backward: twice the weight memory)
@@ -92,7 +113,8 @@ class MoELayer:
                           gates=torch.empty((T, k), dtype=f32, device=dev),
                           counts=torch.empty(E, dtype=i32, device=dev), f=torch.empty(E, dtype=f32, device=dev),
                           P=torch.empty(E, dtype=f32, device=dev), aux=torch.empty(1, dtype=f32, device=dev))
-        self.r_ws = moe._bytes_tensor(moe.moe_router_workspace_size(T, h, E, k, code), dev)
+        self.r_ws = moe._bytes_tensor(moe.moe_group_router_workspace_size(T, h, E, code) if routing == "group"
+                                      else moe.moe_router_workspace_size(T, h, E, k, code), dev)
         self.d_out = dict(buf=torch.empty((self.rows, h), dtype=dt, device=dev),
                           offsets=torch.empty(E + 1, dtype=i32, device=dev),
                           kept_counts=torch.empty(E, dtype=i32, device=dev),
@@ -113,11 +135,15 @@ class MoELayer:
         if self.fp4:                                 # act stays in 4 bits, in the FFN's workspace
             self.fp4_ws = moe._bytes_tensor(max(moe.moe_fp4_expert_ffn_workspace_size(E, h, F, self.rows, self.fp4),
                                                 moe.moe_fp4_expert_ffn_workspace_size(1, h, F, T, self.fp4)), dev)
-        self.act = torch.empty((0 if self.fp4 else self.rows, F), dtype=dt, device=dev)
+        if self.int8:
+            self.int8_ws = moe._bytes_tensor(max(moe.moe_int8_expert_ffn_workspace_size(E, h, F, self.rows),
+                                                 moe.moe_int8_expert_ffn_workspace_size(1, h, F, T)), dev)
+        whole = bool(self.fp4 or self.int8)          # the FFN is one call, act inside it
+        self.act = torch.empty((0 if whole else self.rows, F), dtype=dt, device=dev)
         self.eout = torch.empty((self.rows, h), dtype=dt, device=dev)
         if self.shared_packed is not None:
             self.sh_sched = moe.moe_dense_tile_sched(T, device=dev)
-            self.sh_act = torch.empty((0 if self.fp4 else T, F), dtype=dt, device=dev)
+            self.sh_act = torch.empty((0 if whole else T, F), dtype=dt, device=dev)
             self.sh_out = torch.empty((T, h), dtype=dt, device=dev)
         self.y = torch.empty((T, h), dtype=dt, device=dev)
         # combine fused into the down GEMM's epilogue (bf16, token-choice or Sinkhorn routing): one launch fewer,
@@ -130,9 +156,37 @@ class MoELayer:
         self.arrivals = moe.moe_combine_arrivals(T, h, dev) if self.fuse_combine else None
         self._saved = False
         if backward:                                 # pre-activations kept by forward(save=True)
-            self.gu = torch.empty((self.rows, moe.gu_cols(F)), dtype=dt, device=dev)
-            self.sh_gu = (torch.empty((T, moe.gu_cols(F)), dtype=dt, device=dev)
-                          if self.shared_packed is not None else None)
+            cols = moe.gu_cols(F)
+            kept = [self.rows] + ([T] if self.shared_packed is not None else [])
+            if checkpoint == "int8":                 # kept in 8 bits: the routed rows', then the shared expert's
+                need = self.checkpoint_scratch(self.rows, F, T if self.shared_packed is not None else 0)
+                scratch = torch.empty(need, dtype=dt, device=dev) if scratch is None else scratch
+                if scratch.dtype != dt or scratch.numel() < need or not scratch.is_contiguous():
+                    raise ValueError(f"scratch: a contiguous {dt} tensor of {need} elements")
+                flat = scratch.view(-1)
+                gu = [flat[:self.rows * cols].view(self.rows, cols), flat[self.rows * cols:need].view(-1, cols)]
+                self.kept = [(torch.empty((n, cols), dtype=torch.int8, device=dev), torch.empty((n, cols // 128), dtype=f32, device=dev))
+                             for n in kept]
+            else:
+                gu = [torch.empty((n, cols), dtype=dt, device=dev) for n in kept]
+            self.gu = gu[0]
+            self.sh_gu = gu[1] if self.shared_packed is not None else None
+
+    @staticmethod
+    def checkpoint_scratch(rows: int, F: int, shared_rows: int = 0) -> int:
+        """Elements of the scratch of a layer with checkpoint="int8": its dispatched rows, and T rows with a shared expert."""
+        return (rows + shared_rows) * moe.gu_cols(F)
+
+    @staticmethod
+    def _pack_int8(gate, up, down):
+        """(packed 8-bit weights, the scales of gate, up and down) of bf16 weights [E, ...]."""
+        quantised = [moe.moe_int8_quantize(w.reshape(-1, w.shape[2])) for w in (gate, up, down)]
+        codes = [c.view(w.shape) for (c, _), w in zip(quantised, (gate, up, down))]
+        return moe.moe_int8_pack_expert_weights(*codes), [sc.view(w.shape[:2]) for (_, sc), w in zip(quantised, (gate, up, down))]
+
+    def _ffn_int8(self, x, packed, out, stream, **rows):
+        rows.pop("E")
+        moe.moe_int8_expert_ffn(x, None, packed[0], *packed[1], out=out, ws=self.int8_ws, stream=stream, **rows)
 
     @staticmethod
     def _fp4_multiplier(w):
@@ -164,7 +218,7 @@ class MoELayer:
                                act_gscale=self.fp4_act_gscale, out=out, ws=self.fp4_ws, stream=stream, **rows)
 
     def forward(self, x, stream=None, events=None, y=None, save=False):
-        if save and (self.packed_bwd is None or self.routing not in ("token", "sinkhorn")
+        if save and (self.packed_bwd is None or self.routing not in ("token", "sinkhorn", "group")
                      or self.dtype != torch.bfloat16 or self.payload != "bf16"):
             raise NotImplementedError("MoELayer.forward(save=True): a layer built with backward=True, token-choice or "
                                       "Sinkhorn routing in bf16 with the bf16 send buffer")
@@ -177,10 +231,14 @@ class MoELayer:
 
         mark("start")
         r = self.r_out
-        moe.moe_router(x, self.w_r, self.bias, self.k, "softmax" if self.routing == "sinkhorn" else self.gating,
-                       self.alpha, logits=r["logits"],
-                       topk_ids=r["topk_ids"], gates=r["gates"], counts=r["counts"], f=r["f"], P=r["P"], aux=r["aux"],
-                       ws=self.r_ws, stream=stream, w_packed=self.w_r_packed)
+        if self.routing == "group":
+            moe.moe_group_router(x, self.w_r_packed, self.E, self.bias, self.k, alpha=self.alpha, ws=self.r_ws, stream=stream,
+                                 **self.group, **r)
+        else:
+            moe.moe_router(x, self.w_r, self.bias, self.k, "softmax" if self.routing == "sinkhorn" else self.gating,
+                           self.alpha, logits=r["logits"],
+                           topk_ids=r["topk_ids"], gates=r["gates"], counts=r["counts"], f=r["f"], P=r["P"], aux=r["aux"],
+                           ws=self.r_ws, stream=stream, w_packed=self.w_r_packed)
         if self.routing == "expert_choice":
             moe.moe_expert_choice_route(r["logits"], self.C, tokens=self.ec["tokens"], gates=self.ec["gates"],
                                         slot=self.ec["slot"], ws=self.ec_ws, stream=stream)
@@ -202,13 +260,14 @@ class MoELayer:
         sched = self.d_out["tile_sched"]
         shared_out = None
         out = self.y if y is None else y
-        if self.fp4:
+        if self.fp4 or self.int8:
+            ffn = self._ffn_fp4 if self.fp4 else self._ffn_int8
             src = self.ec["tokens"].view(-1) if self.routing == "expert_choice" else self.d_out["src_token"]
-            self._ffn_fp4(x, self.packed, self.eout, stream, E=self.E, tile_sched=sched, src=src)
+            ffn(x, self.packed, self.eout, stream, E=self.E, tile_sched=sched, src=src)
             mark("up_gate")
             mark("down")
             if self.shared_packed is not None:
-                self._ffn_fp4(x, self.shared_packed, self.sh_out, stream, E=1, tile_sched=self.sh_sched)
+                ffn(x, self.shared_packed, self.sh_out, stream, E=1, tile_sched=self.sh_sched)
                 mark("shared_up_gate")
                 mark("shared_down")
                 shared_out = self.sh_out
@@ -256,6 +315,10 @@ class MoELayer:
         elif not self.fuse_combine:
             moe.moe_combine(self.eout, self.d_out["dest_row"], r["gates"], shared_out, y=out, stream=stream)
         mark("combine")
+        if save and self.checkpoint == "int8":       # from the scratch, before another layer uses it
+            moe.moe_checkpoint8_save(self.gu, tile_sched=sched, E=self.E, codes=self.kept[0][0], scales=self.kept[0][1], stream=stream)
+            if self.sh_gu is not None:
+                moe.moe_checkpoint8_save(self.sh_gu, codes=self.kept[1][0], scales=self.kept[1][1], stream=stream)
         self._saved = bool(save)
         return out
 
@@ -284,8 +347,8 @@ class MoELayer:
         "expert_dgrad", "expert_wgrad", ["shared_bwd"], "router_bwd", "dispatch_bwd")."""
         if self.packed_bwd is None:
             raise RuntimeError("MoELayer.backward: build the layer with backward=True")
-        if self.routing not in ("token", "sinkhorn") or self.dtype != torch.bfloat16 or self.payload != "bf16":
-            raise NotImplementedError("MoELayer.backward: token-choice or Sinkhorn routing in bf16 with the bf16 "
+        if self.routing not in ("token", "sinkhorn", "group") or self.dtype != torch.bfloat16 or self.payload != "bf16":
+            raise NotImplementedError("MoELayer.backward: token-choice, group or Sinkhorn routing in bf16 with the bf16 "
                                       "send buffer")
 
         def mark(stage):
@@ -334,7 +397,10 @@ class MoELayer:
                                  d_eout=b["d_eout"], d_gates=b["d_gates"], stream=stream)
         mark("combine_bwd")
         moe.moe_expert_down_backward(b["d_eout"], sched, self.packed_bwd, E, F, d_act=b["d_act"], stream=stream)
-        if self._saved:                  # g and u kept by forward(save=True)
+        if self._saved and self.checkpoint == "int8":    # g and u kept in 8 bits, and act from them
+            moe.moe_expert_up_gate_backward_checkpoint8(*self.kept[0], b["d_act"], sched, self.packed_bwd, E, h, d_gu=b["d_gu"],
+                                                        act=self.act, d_buf=b["d_buf"], stream=stream)
+        elif self._saved:                # g and u kept by forward(save=True)
             moe.moe_expert_up_gate_backward_saved(self.gu, b["d_act"], sched, self.packed_bwd, E, h, d_gu=b["d_gu"],
                                                   d_buf=b["d_buf"], stream=stream)
         else:
@@ -349,7 +415,10 @@ class MoELayer:
         if self.shared_packed is not None:
             moe.moe_expert_down_backward(dy, self.sh_sched, self.shared_packed_bwd, 1, F, d_act=b["sh_d_act"],
                                          stream=stream)
-            if self._saved:
+            if self._saved and self.checkpoint == "int8":
+                moe.moe_expert_up_gate_backward_checkpoint8(*self.kept[1], b["sh_d_act"], self.sh_sched, self.shared_packed_bwd, 1, h,
+                                                            d_gu=b["sh_d_gu"], act=self.sh_act, d_buf=b["sh_dx"], stream=stream)
+            elif self._saved:
                 moe.moe_expert_up_gate_backward_saved(self.sh_gu, b["sh_d_act"], self.sh_sched, self.shared_packed_bwd,
                                                       1, h, d_gu=b["sh_d_gu"], d_buf=b["sh_dx"], stream=stream)
             else:
@@ -364,9 +433,15 @@ class MoELayer:
         # the bias is part of the logits in the plain softmax modes and under Sinkhorn routing (whose router runs
         # in the plain softmax mode); the sigmoid mode's bias only selects
         want_bias = self.bias is not None and (self.gating in ("softmax", "softmax_renorm") or self.routing == "sinkhorn")
-        d_logits, d_bias = moe.moe_router_backward(r["logits"], r["topk_ids"], r["gates"], b["d_gates"], r["f"],
-                                                   self.gating, self.alpha, d_aux, d_logits=b["d_logits"],
-                                                   want_bias_grad=want_bias, ws=b["ws_rb"], stream=stream)
+        if self.routing == "group":                      # the bias only selects
+            d_bias = None
+            d_logits = moe.moe_group_route_backward(r["logits"], r["topk_ids"], b["d_gates"], r["f"], score=self.gating,
+                                                    renorm=self.group["renorm"], scale=self.group["scale"], alpha=self.alpha,
+                                                    d_aux=d_aux, d_logits=b["d_logits"], stream=stream)
+        else:
+            d_logits, d_bias = moe.moe_router_backward(r["logits"], r["topk_ids"], r["gates"], b["d_gates"], r["f"],
+                                                       self.gating, self.alpha, d_aux, d_logits=b["d_logits"],
+                                                       want_bias_grad=want_bias, ws=b["ws_rb"], stream=stream)
         moe.moe_router_weight_grad(x, d_logits, dW_r=b["dW_r"], ws=b["ws_rw"], stream=stream)
         mark("router_bwd")
         moe.moe_dispatch_backward(b["d_buf"], d["dest_row"], d_logits, self.w_r, dx_extra=sh_dx,
@@ -397,8 +472,10 @@ class MoELayer:
         """The moe_layer_desc of this layer for the one-call C entry points moe_layer_forward and
         moe_layer_forward_host (every routing mode and send buffer of `forward`, with the separate combine: the
         same launches): it points at this layer's packed parameters, which must outlive its use."""
-        if self.fp4:
+        if self.fp4 or self.int8:
             raise NotImplementedError("moe_layer_forward runs the experts in the layer's dtype (MoELayer(experts='dtype'))")
+        if self.routing == "group":
+            raise NotImplementedError("moe_layer_forward routes by moe_router's modes (MoELayer(routing='token'))")
         if self.fuse_combine:
             raise NotImplementedError("moe_layer_forward runs the separate combine (MoELayer(fuse_combine=False))")
         return moe.moe_layer_desc(T=self.T, h=self.h, E=self.E, k=self.k, F=self.F, dtype=self.dtype,
