@@ -20,34 +20,68 @@ __device__ __forceinline__ int tiles_of(const int32_t* sched, int E, int rows, u
     return fits ? sched[0] : 0;
 }
 
-// A warp takes 512 columns of a row at a time: 16 columns a lane, eight lanes to a block (VEC), or four blocks one after the other, a
-// lane every 32nd column.
+// The rows of a call, or of its schedule's tiles, as items of one segment each, `step` apart; row -1: no row of the call.
+struct Rows {
+    Walk at;
+    const int4* tiles;
+    int rows;
+    __device__ __forceinline__ Rows(const int32_t* sched, int E, int rows_, int nseg, unsigned* err)
+        : at((long long)blockIdx.x * C_WARPS + (threadIdx.x >> 5), (long long)gridDim.x * C_WARPS,
+             (sched ? (long long)tiles_of(sched, E, rows_, err) * MOE_TILE_M : rows_) * nseg, nseg),
+          tiles(sched ? reinterpret_cast<const int4*>(sched + sched_tiles_offset(E)) : nullptr), rows(rows_) {}
+    __device__ __forceinline__ int row() const {
+        if (!tiles) return at.row;
+        const int4 t = tiles[at.row / MOE_TILE_M];
+        const int r = t.y + at.row % MOE_TILE_M;
+        return r >= 0 && r < min(t.z, rows) ? r : -1;
+    }
+};
+
+// A warp takes 512 columns of a row at a time: 16 columns a lane, eight lanes to a block, as many such items under way as 4 KB hold
+// (one at a time left 40 KB under way on an SM: 16384 x 28672 bf16 in 690 us), or (!VEC) four blocks one after the other, a lane every 32nd
+// column.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(C_THREADS)
 checkpoint_save_kernel(const T* x, long long ldx, int rows, int C, const int32_t* sched, int E, int8_t* codes, float* scales, unsigned* err) {
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, nseg = (C + 511) / 512, nb = (C + CKPT - 1) / CKPT;
-    auto segment = [&](int row, int seg) {
-        const T* xr = x + row * ldx;
-        int8_t* cr = codes + (size_t)row * C;
+    const int lane = threadIdx.x & 31, nb = (C + CKPT - 1) / CKPT;
+    Rows it(sched, E, rows, (C + 511) / 512, err);
+    while (it.at.left > 0) {
         if constexpr (VEC) {
-            const int k = seg * 512 + lane * UNIT;
-            const Raw16<T> raw = load_unit<T, true>(xr, k, C);
-            float amax = unit_amax(raw), inv;
+            constexpr int U = 8 / (int)sizeof(T);
+            Raw16<T> raw[U];
+            int row[U], k[U];
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const float s = scale_of(amax, inv);
-            const T* e = reinterpret_cast<const T*>(raw.q);
-            float v[UNIT];
+            for (int u = 0; u < U; ++u) {
+                row[u] = it.at.left > 0 ? it.row() : -1;
+                k[u] = it.at.seg * 512 + lane * UNIT;
+                raw[u] = load_unit<T, true>(x + max(row[u], 0) * ldx, k[u], row[u] >= 0 ? C : 0);
+                if (it.at.left > 0) it.at.next();
+            }
 #pragma unroll
-            for (int i = 0; i < UNIT; ++i) v[i] = as_f32(e[i]);
-            codes_of<UNIT>(v, inv, amax);
-            if (k < C) {
-                *reinterpret_cast<uint4*>(cr + k) = make_uint4(bytes4(v), bytes4(v + 4), bytes4(v + 8), bytes4(v + 12));
-                if ((lane & 7) == 0) scales[(size_t)row * nb + k / CKPT] = s;
+            for (int u = 0; u < U; ++u) {
+                if (row[u] < 0) continue;
+                float amax = unit_amax(raw[u]), inv;
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                const float s = scale_of(amax, inv);
+                const T* e = reinterpret_cast<const T*>(raw[u].q);
+                float v[UNIT];
+#pragma unroll
+                for (int i = 0; i < UNIT; ++i) v[i] = as_f32(e[i]);
+                codes_of<UNIT>(v, inv, amax);
+                if (k[u] < C) {
+                    *reinterpret_cast<uint4*>(codes + (size_t)row[u] * C + k[u]) = make_uint4(bytes4(v), bytes4(v + 4), bytes4(v + 8), bytes4(v + 12));
+                    if ((lane & 7) == 0) scales[(size_t)row[u] * nb + k[u] / CKPT] = s;
+                }
             }
         } else {
+            const int row = it.row(), seg = it.at.seg;
+            it.at.next();
+            if (row < 0) continue;
+            const T* xr = x + row * ldx;
+            int8_t* cr = codes + (size_t)row * C;
 #pragma unroll 1
             for (int b = 0; b < 4; ++b) {
                 const int k0 = seg * 512 + b * CKPT;
@@ -64,21 +98,9 @@ checkpoint_save_kernel(const T* x, long long ldx, int rows, int C, const int32_t
                 codes_of<4>(v, inv, amax);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (k0 + j * 32 + lane < C) cr[k0 + j * 32 + lane] = (int8_t)(int)v[j];
+                    if (k0 + j * 32 + lane < C) cr[k0 + j * 32 + lane] = (int8_t)__float_as_uint(v[j]);
                 if (lane == 0) scales[(size_t)row * nb + k0 / CKPT] = s;
             }
-        }
-    };
-    const long long w0 = (long long)blockIdx.x * C_WARPS + (threadIdx.x >> 5), step = (long long)gridDim.x * C_WARPS;
-    if (!sched) {
-        for (Walk at(w0, step, (long long)rows * nseg, nseg); at.left > 0; at.next()) segment(at.row, at.seg);
-    } else {                                 // the rows of the schedule's tiles
-        const int4* tiles = reinterpret_cast<const int4*>(sched + sched_tiles_offset(E));
-        const int ntiles = tiles_of(sched, E, rows, err);
-        for (Walk at(w0, step, (long long)ntiles * MOE_TILE_M * nseg, nseg); at.left > 0; at.next()) {
-            const int4 t = tiles[at.row / MOE_TILE_M];
-            const int row = t.y + at.row % MOE_TILE_M;
-            if (row >= 0 && row < min(t.z, rows)) segment(row, at.seg);
         }
     }
 }
@@ -109,42 +131,50 @@ checkpoint_swiglu_backward_kernel(const int8_t* codes, const float* scales, cons
                                   int F, int Fp, __nv_bfloat16* d_gu, __nv_bfloat16* act, unsigned* err) {
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, nseg = (Fp + 255) / 256;
-    auto segment = [&](int row, int seg) {
-        const int f = seg * 256 + lane * 8;
-        if (f >= Fp) return;
-        const size_t col = (size_t)(f >> 7) * 256 + (f & 127), at = (size_t)row * 2 * Fp + col;
-        const uint2 cg = __ldcs(reinterpret_cast<const uint2*>(codes + at)), cu = __ldcs(reinterpret_cast<const uint2*>(codes + at + 128));
-        const float2 sc = *reinterpret_cast<const float2*>(scales + (size_t)row * (2 * Fp / CKPT) + (f >> 7) * 2);
-        Vec16<__nv_bfloat16> da, og, ou, oa;
-        const bool in = f < F;
-        if (in) da.v = __ldcs(reinterpret_cast<const uint4*>(d_act + (size_t)row * F + f));
-        else da.v = make_uint4(0u, 0u, 0u, 0u);
-        const int8_t* g8 = reinterpret_cast<const int8_t*>(&cg);
-        const int8_t* u8 = reinterpret_cast<const int8_t*>(&cu);
+    constexpr int U = 2;                      // items whose loads a lane has under way
+    const int lane = threadIdx.x & 31;
+    Rows it(sched, E, rows, (Fp + 255) / 256, err);
+    while (it.at.left > 0) {
+        uint2 cg[U], cu[U];
+        float2 sc[U];
+        Vec16<__nv_bfloat16> da[U];
+        size_t at[U], to[U];
+        bool live[U], in[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float g = (float)g8[i] * sc.x, u = (float)u8[i] * sc.y, a = da.get(i);
-            const float s = __fdividef(1.f, 1.f + __expf(-g));
-            const float gs = g * s;
-            og.set(i, a * u * (s + gs * (1.f - s)));
-            ou.set(i, a * gs);
-            oa.set(i, gs * u);
+        for (int i = 0; i < U; ++i) {
+            const int row = it.at.left > 0 ? it.row() : -1, f = it.at.seg * 256 + lane * 8;
+            live[i] = row >= 0 && f < Fp;
+            in[i] = row >= 0 && f < F;
+            at[i] = (size_t)max(row, 0) * 2 * Fp + (size_t)(f >> 7) * 256 + (f & 127);
+            to[i] = (size_t)max(row, 0) * F + f;
+            da[i].v = make_uint4(0u, 0u, 0u, 0u);
+            if (live[i]) {
+                cg[i] = __ldcs(reinterpret_cast<const uint2*>(codes + at[i]));
+                cu[i] = __ldcs(reinterpret_cast<const uint2*>(codes + at[i] + 128));
+                sc[i] = *reinterpret_cast<const float2*>(scales + (size_t)row * (2 * Fp / CKPT) + (f >> 7) * 2);
+            }
+            if (in[i]) da[i].v = __ldcs(reinterpret_cast<const uint4*>(d_act + to[i]));
+            if (it.at.left > 0) it.at.next();
         }
-        st16(d_gu + at, og);
-        st16(d_gu + at + 128, ou);
-        if (in) st16(act + (size_t)row * F + f, oa);
-    };
-    const long long w0 = (long long)blockIdx.x * C_WARPS + (threadIdx.x >> 5), step = (long long)gridDim.x * C_WARPS;
-    if (!sched) {
-        for (Walk at(w0, step, (long long)rows * nseg, nseg); at.left > 0; at.next()) segment(at.row, at.seg);
-    } else {
-        const int4* tiles = reinterpret_cast<const int4*>(sched + sched_tiles_offset(E));
-        const int ntiles = tiles_of(sched, E, rows, err);
-        for (Walk at(w0, step, (long long)ntiles * MOE_TILE_M * nseg, nseg); at.left > 0; at.next()) {
-            const int4 t = tiles[at.row / MOE_TILE_M];
-            const int row = t.y + at.row % MOE_TILE_M;
-            if (row >= 0 && row < min(t.z, rows)) segment(row, at.seg);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (!live[i]) continue;
+            float g[8], u[8];
+            values4(cg[i].x, sc[i].x, g);
+            values4(cg[i].y, sc[i].x, g + 4);
+            values4(cu[i].x, sc[i].y, u);
+            values4(cu[i].y, sc[i].y, u + 4);
+            Vec16<__nv_bfloat16> og, ou, oa;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float a = da[i].get(j), s = __fdividef(1.f, 1.f + __expf(-g[j])), gs = g[j] * s;
+                og.set(j, a * u[j] * (s + gs * (1.f - s)));
+                ou.set(j, a * gs);
+                oa.set(j, gs * u[j]);
+            }
+            st16(d_gu + at[i], og);
+            st16(d_gu + at[i] + 128, ou);
+            if (in[i]) st16(act + to[i], oa);
         }
     }
 }

@@ -29,7 +29,7 @@ struct Args {
     int nparts;
     size_t part_stride;
     const float* bias;                       // or null
-    int T, E, k, groups, per, top_groups, best, npl, lpg;   // per: experts of a group; lpg: lanes of a group (0: no whole lanes)
+    int T, E, k, groups, per, top_groups, best, npl, lpg, lpg_log;   // per: experts of a group; lpg: lanes of a group (0: no whole lanes)
     bool sigmoid, renorm, vec;
     float scale;
     float* logits_out;                       // or null
@@ -38,6 +38,9 @@ struct Args {
     float* partial_P;
     int32_t* partial_C;
     unsigned* ticket;
+    int32_t* counts;                         // null, or of a single block that finalizes too: counts, f, P, aux
+    float *f, *P, *aux;
+    float alpha;
 };
 
 __device__ __forceinline__ unsigned key_of(float v) {
@@ -48,61 +51,106 @@ __device__ __forceinline__ float value_of(unsigned key) {
     return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
 }
 
-// The choice in 64 bits, for a token with scores that are next to each other. Whole warp; returns lane j's choice j.
-__device__ __noinline__ int choose_exact(const Args& a, const float* L, const float* bias, int npl) {
-    const int lane = threadIdx.x & 31, e0 = lane * npl;
-    double sel[32];
-    double m = -INFINITY, z = 1.0;
-    if (!a.sigmoid) {
-        for (int i = 0; i < npl; ++i)
-            if (e0 + i < a.E) m = fmax(m, (double)L[i]);
-        for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-        z = 0.0;
-        for (int i = 0; i < npl; ++i)
-            if (e0 + i < a.E && L[i] > -INFINITY) z += exp((double)L[i] - m);
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    }
-    for (int i = 0; i < npl; ++i) {
-        sel[i] = -INFINITY;
-        if (e0 + i < a.E) {
-            const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)L[i])) : exp((double)L[i] - m) / z;
-            const double v = s + (bias ? (double)bias[e0 + i] : 0.0);
-            sel[i] = L[i] > -INFINITY && v == v ? v : (double)kMasked;
+// What follows runs for a token in some thousands, by one warp, and its latency is the call's: 64-bit arithmetic takes sixteen cycles an
+// instruction to issue and some sixty until its result, so scores are computed four at a time and compared as whole numbers (compared
+// and summed in turn as doubles, one such token made the call 40 us longer).
+// A selection score in 64 bits; m and z: softmax's largest logit and sum (z 0: sigmoid).
+__device__ __forceinline__ double exact_sel(float l, float bias, double m, double z) {
+    if (!(l > -INFINITY)) return (double)kMasked;
+    const double e = exp(z == 0.0 ? -(double)l : (double)l - m), v = (z == 0.0 ? 1.0 : e) / (z == 0.0 ? 1.0 + e : z) + (double)bias;
+    return v == v ? v : (double)kMasked;
+}
+// Its order as a whole number, and back.
+__device__ __forceinline__ long long order_of(double v) {
+    const long long b = __double_as_longlong(v + 0.0);
+    return b >= 0 ? b : b ^ 0x7fffffffffffffffLL;
+}
+__device__ __forceinline__ double of_order(long long b) { return __longlong_as_double(b >= 0 ? b : b ^ 0x7fffffffffffffffLL); }
+constexpr long long kLeast = -0x7fffffffffffffffLL - 1;
+
+struct Norm { double m, z; };
+__device__ __noinline__ Norm exact_norm(const float* L, int npl) {
+    float m = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < npl; ++i) m = fmaxf(m, L[i]);
+    Norm n{(double)warp_max(m), 0.0};
+    double z[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 1
+    for (int i = 0; i < npl; i += 4)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] += i + j < npl && L[i + j] > -INFINITY ? exp((double)L[i + j] - n.m) : 0.0;
+    n.z = (z[0] + z[1]) + (z[2] + z[3]);
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) n.z += __shfl_xor_sync(0xffffffffu, n.z, o);
+    return n;
+}
+
+// The groups that stay, in 64 bits: bit g of the result; sel: this lane's scores' order. Whole warp, as the two below; L: this lane's npl
+// logits (-inf past E).
+__device__ __noinline__ unsigned groups_exact(const Args& a, const float* L, long long* sel) {
+    const int lane = threadIdx.x & 31, npl = a.npl, e0 = lane * npl;
+    const Norm n = a.sigmoid ? Norm{0.0, 0.0} : exact_norm(L, npl);
+#pragma unroll 1
+    for (int i = 0; i < npl; i += 4) {
+        double v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool live = i + j < npl && e0 + i + j < a.E;
+            v[j] = exact_sel(live ? L[i + j] : 0.f, a.bias && live ? a.bias[e0 + i + j] : 0.f, n.m, n.z);
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j < npl) sel[i + j] = e0 + i + j < a.E ? order_of(v[j]) : kLeast;
     }
-    double gscore = 0.0;                     // lane g: group g's
+    long long gscore = kLeast;               // lane g: group g's
+#pragma unroll 1
     for (int g = 0; g < a.groups; ++g) {
-        double t1 = -INFINITY, t2 = -INFINITY;
-        for (int i = 0; i < npl; ++i) {
-            const int e = e0 + i;
-            if (e < g * a.per || e >= (g + 1) * a.per) continue;
-            if (sel[i] > t1) { t2 = t1; t1 = sel[i]; } else if (sel[i] > t2) t2 = sel[i];
+        long long t1 = kLeast, t2 = kLeast;
+        const int lo = max(g * a.per - e0, 0), hi = min((g + 1) * a.per - e0, npl);
+#pragma unroll 1
+        for (int i = lo; i < hi; ++i) {
+            t2 = max(t2, min(t1, sel[i]));
+            t1 = max(t1, sel[i]);
         }
+#pragma unroll 1
         for (int o = 16; o > 0; o >>= 1) {
-            const double b1 = __shfl_xor_sync(0xffffffffu, t1, o), b2 = __shfl_xor_sync(0xffffffffu, t2, o);
-            const double lo = fmin(t1, b1);
-            t1 = fmax(t1, b1);
-            t2 = fmax(lo, fmax(t2, b2));
+            const long long b1 = __shfl_xor_sync(0xffffffffu, t1, o), b2 = __shfl_xor_sync(0xffffffffu, t2, o);
+            t2 = max(min(t1, b1), max(t2, b2));
+            t1 = max(t1, b1);
         }
-        if (lane == g) gscore = a.best == 2 ? t1 + t2 : t1;
+        if (lane == g) gscore = a.best == 2 ? order_of(of_order(t1) + of_order(t2)) : t1;
     }
     int rank = 0;
+#pragma unroll 1
     for (int g = 0; g < a.groups; ++g) {
-        const double o = __shfl_sync(0xffffffffu, gscore, g);
+        const long long o = __shfl_sync(0xffffffffu, gscore, g);
         rank += o > gscore || (o == gscore && g < lane);
     }
-    const unsigned kept = __ballot_sync(0xffffffffu, lane < a.groups && rank < a.top_groups);
+    return __ballot_sync(0xffffffffu, lane < a.groups && rank < a.top_groups);
+}
+
+// The whole choice in 64 bits; returns lane j's choice j.
+__device__ __noinline__ int choose_exact(const Args& a, const float* L) {
+    const int lane = threadIdx.x & 31, npl = a.npl, e0 = lane * npl;
+    long long sel[32];
+    const unsigned kept = groups_exact(a, L, sel);
     unsigned taken = 0u;                     // slots of this lane that are out
-    for (int i = 0; i < npl; ++i)
+#pragma unroll 1
+    for (int i = 0; i < npl; ++i) {
         if (e0 + i >= a.E || !(kept >> ((e0 + i) / a.per) & 1u)) taken |= 1u << i;
+        if (!a.bias && L[i] > -INFINITY) sel[i] = order_of((double)L[i]);      // (ranked by the logits)
+    }
     int my_id = 0;
+#pragma unroll 1
     for (int j = 0; j < a.k; ++j) {
-        double v = -INFINITY;
+        long long v = kLeast;
         int id = 0x7fffffff;
+#pragma unroll 1
         for (int i = 0; i < npl; ++i)
             if (!(taken >> i & 1u) && (id == 0x7fffffff || sel[i] > v)) { v = sel[i]; id = e0 + i; }
+#pragma unroll 1
         for (int o = 16; o > 0; o >>= 1) {
-            const double ov = __shfl_xor_sync(0xffffffffu, v, o);
+            const long long ov = __shfl_xor_sync(0xffffffffu, v, o);
             const int oi = __shfl_xor_sync(0xffffffffu, id, o);
             if (oi != 0x7fffffff && (id == 0x7fffffff || ov > v || (ov == v && oi < id))) { v = ov; id = oi; }
         }
@@ -112,23 +160,26 @@ __device__ __noinline__ int choose_exact(const Args& a, const float* L, const fl
     return my_id;
 }
 
-// The order of the chosen and the next best where only neighbours among them lie that near (sigmoid scores: each lane j <= k computes
-// its own in 64 bits, a hundredth of what the whole choice costs). id, l: lane j's expert and its logit, of
-// `n` in all; returns lane j's expert after ordering.
-__device__ __noinline__ int order_exact(float l, const float* bias, int id, int n) {
+// The order of n candidates, lane j's being expert `id` with logit l, where only neighbours among them may be exchanged: a lane computes
+// its own score. Returns lane j's expert after ordering.
+__device__ __noinline__ int order_exact(const Args& a, const float* L, float l, int id, int n) {
     const int lane = threadIdx.x & 31;
-    double v = -INFINITY;
-    if (lane < n) {
-        v = l > -INFINITY ? 1.0 / (1.0 + exp(-(double)l)) + (double)bias[id] : (double)kMasked;
-        if (!(v == v)) v = (double)kMasked;
+    long long v = kLeast;
+    if (a.bias) {
+        const Norm norm = a.sigmoid ? Norm{0.0, 0.0} : exact_norm(L, a.npl);
+        if (lane < n) v = order_of(exact_sel(l, a.bias[id], norm.m, norm.z));
+    } else if (lane < n) {
+        v = order_of(l > -INFINITY ? (double)l : (double)kMasked);
     }
-    int rank = 0;
+    __syncwarp();
+    int rank = 0, out = id;
+#pragma unroll 1
     for (int j = 0; j < n; ++j) {
-        const double o = __shfl_sync(0xffffffffu, v, j);
+        const long long o = __shfl_sync(0xffffffffu, v, j);
         const int oi = __shfl_sync(0xffffffffu, id, j);
         rank += o > v || (o == v && oi < id);
     }
-    int out = id;
+#pragma unroll 1
     for (int j = 0; j < n; ++j) {
         const int r = __shfl_sync(0xffffffffu, rank, j), oi = __shfl_sync(0xffffffffu, id, j);
         if (lane == r) out = oi;
@@ -136,9 +187,49 @@ __device__ __noinline__ int order_exact(float l, const float* bias, int id, int 
     return out;
 }
 
-template <int NPL>
-__global__ void __launch_bounds__(kWarps * 32)
-group_gate_kernel(const Args a) {
+// 2^x and 1 / x of the special-function units: within 2 and 1 units in the last place.
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.44269504f;
+
+// Keys by falling order (Batcher's odd-even merge of N = 2^n).
+template <int N>
+__device__ __forceinline__ void sort_keys(unsigned (&key)[N]) {
+#pragma unroll
+    for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+        for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const unsigned x = key[i + j], y = key[i + j + k];
+                        key[i + j] = max(x, y);
+                        key[i + j + k] = min(x, y);
+                    }
+}
+
+// A lane sorts the keys of its experts once, the slot in a key's lowest bits (so that a comparison is a maximum and a minimum), and the
+// k rounds compare the lanes' heads without those bits: equal ones go to the lowest lane, and within a lane to the lowest slot. What
+// the missing bits, and the roundings of the scores, may have confused is found afterwards from the chosen keys' differences, each lane
+// looking at one, and put right in 64 bits.
+// (16384 tokens by 256 experts, k 8 of 4 of 8 groups; an argmax over unsorted slots in every round, with libm's exponential and
+// division, took 45 us of scores and rounds; the whole choice in 64 bits 50 us for the one token of some thousands that needs it.)
+// FULL: E = 32 NPL, and a group a run of lanes whose number is a power of two.
+template <int NPL, bool FULL>
+__global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL == 16 ? 2 : 1)
+group_gate_kernel(const __grid_constant__ Args a) {
+    constexpr unsigned SLOT = NPL - 1;
+    constexpr int SB = NPL == 1 ? 0 : NPL == 2 ? 1 : NPL == 4 ? 2 : NPL == 8 ? 3 : NPL == 16 ? 4 : 5;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     float* s_P = reinterpret_cast<float*>(smem_raw);                   // [warps][E]; a warp's row holds its selection scores before
     int* s_hist = reinterpret_cast<int*>(s_P + (size_t)kWarps * a.E);
@@ -147,95 +238,87 @@ group_gate_kernel(const Args a) {
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) s_hist[e] = 0;
     __syncthreads();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int npl = a.npl, e0 = lane * npl;
+    const int npl = FULL ? NPL : a.npl, e0 = lane * npl;
+    auto live = [&](int i) { return FULL || (i < npl && e0 + i < a.E); };
     float* row = s_P + (size_t)warp * a.E;
     float Pacc[NPL], bias[NPL];
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         Pacc[i] = 0.f;
-        bias[i] = a.bias && i < npl && e0 + i < a.E ? a.bias[e0 + i] : 0.f;
+        bias[i] = a.bias && live(i) ? a.bias[e0 + i] : 0.f;
     }
     for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
-        float L[NPL], s[NPL], r[NPL];                                // logits, scores, what the experts are ranked by
-        bool live[NPL];
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            live[i] = i < npl && e0 + i < a.E;
-            L[i] = -INFINITY;
-        }
+        float L[NPL], s[NPL];                                        // logits, scores
         const float* src = a.logits + (size_t)t * a.E;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) L[i] = -INFINITY;
         if (NPL % 4 == 0 && a.vec) {
-            if (e0 < a.E) {
+            if (FULL || e0 < a.E) {
 #pragma unroll
                 for (int i = 0; i < NPL; i += 4) *reinterpret_cast<float4*>(L + i) = *reinterpret_cast<const float4*>(src + e0 + i);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < NPL; ++i)
-                if (live[i]) L[i] = src[e0 + i];
+                if (live(i)) L[i] = src[e0 + i];
         }
         for (int q = 1; q < a.nparts; ++q) {
 #pragma unroll
             for (int i = 0; i < NPL; ++i)
-                if (live[i]) L[i] += src[q * a.part_stride + e0 + i];
+                if (live(i)) L[i] += src[q * a.part_stride + e0 + i];
         }
         if (a.logits_out) {
 #pragma unroll
             for (int i = 0; i < NPL; ++i)
-                if (live[i]) a.logits_out[(size_t)t * a.E + e0 + i] = L[i];
+                if (live(i)) a.logits_out[(size_t)t * a.E + e0 + i] = L[i];
         }
-        // scores
-        float total = 0.f;
-        if (a.sigmoid) {
+        // scores (0 of what is masked or past E)
+        float total = 0.f, m = 0.f, smax = 1.f;
+        if (!a.sigmoid) {
+            m = L[0];
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                s[i] = live[i] ? 1.f / (1.f + expf(-L[i])) : 0.f;
-                total += s[i];
-            }
-            total = warp_sum(total);
-            const float inv = total == 0.f ? 0.f : 1.f / total;
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) Pacc[i] += s[i] * inv;
-        } else {
-            float m = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) m = fmaxf(m, L[i]);
+            for (int i = 1; i < NPL; ++i) m = fmaxf(m, L[i]);
             m = warp_max(m);
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                s[i] = L[i] != -INFINITY ? expf(L[i] - m) : 0.f;
-                total += s[i];
-            }
-            total = warp_sum(total);
-            const float inv = total == 0.f ? 0.f : 1.f / total;
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                s[i] *= inv;
-                Pacc[i] += s[i];
-            }
         }
-        // selection scores; the group's score is of s + bias, the experts' order without a bias that of the logits
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            if (a.sigmoid) s[i] = rcp(1.f + ex2(-kLog2e * L[i]));
+            else s[i] = L[i] != -INFINITY ? ex2((L[i] - m) * kLog2e) : 0.f;
+            total += s[i];
+        }
+        total = warp_sum(total);
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) Pacc[i] += s[i] * inv;
+        if (!a.sigmoid) {
+            smax = inv;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) s[i] *= inv;
+        }
+        // Selection scores; the group's score is of s + bias, the experts' order without a bias that of the logits. The error of s: sigmoid's
+        // exponential and reciprocal, 2^-22 and 2^-24 of it and the rounding of -L log2(e) (|L| s (1 - s) is below 0.3); softmax's
+        // adds the rounded difference of the logits and the sum.
+        const float serr = a.sigmoid ? 3e-7f : 1e-6f * smax + 6e-8f;
         float t1 = -INFINITY, t2 = -INFINITY;
+        unsigned key[NPL];
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             const float v = s[i] + bias[i];
             const bool out = !(L[i] > -INFINITY) || !(v == v);
             const float sel = out ? kMasked : v;
-            r[i] = a.bias || out ? sel : L[i];
-            if (live[i]) {
+            key[i] = live(i) ? (key_of(a.bias || out ? sel : L[i]) & ~SLOT) | (SLOT - i) : 0u;
+            if (live(i)) {
                 t2 = fmaxf(t2, fminf(t1, sel));
                 t1 = fmaxf(t1, sel);
-                if (!a.lpg) row[e0 + i] = sel;
+                if (!FULL && !a.lpg) row[e0 + i] = sel;
             }
         }
-        bool near = false;                    // scores that 32 bits cannot tell apart
-        unsigned kept = 0xffffffffu;          // bit g: group g stays
         if (a.top_groups < a.groups) {
             int g = lane;                     // this lane's group
-            if (a.lpg) {
-                g = lane / a.lpg;
+            if (FULL || a.lpg) {
+                g = FULL ? lane >> a.lpg_log : lane / a.lpg;
                 const int pos = lane - g * a.lpg, g0 = lane - pos;
-                if ((a.lpg & (a.lpg - 1)) == 0) {
+                if (FULL || (a.lpg & (a.lpg - 1)) == 0) {
                     for (int o = 1; o < a.lpg; o <<= 1) {
                         const float b1 = __shfl_xor_sync(0xffffffffu, t1, o), b2 = __shfl_xor_sync(0xffffffffu, t2, o);
                         t2 = fmaxf(fminf(t1, b1), fmaxf(t2, b2));
@@ -264,117 +347,140 @@ group_gate_kernel(const Args a) {
             const float gs = a.best == 2 ? t1 + t2 : t1;
             int rank = 0;
             for (int o = 0; o < a.groups; ++o) {
-                const float v = __shfl_sync(0xffffffffu, gs, a.lpg ? o * a.lpg : o);
+                const float v = __shfl_sync(0xffffffffu, gs, FULL ? o << a.lpg_log : a.lpg ? o * a.lpg : o);
                 rank += v > gs || (v == gs && o < g);
             }
-            const bool is = g < a.groups, stays = is && rank < a.top_groups;
-            const unsigned last = __reduce_min_sync(0xffffffffu, stays ? key_of(gs) : 0xffffffffu),
-                           next = __reduce_max_sync(0xffffffffu, is && !stays ? key_of(gs) : 0u);
-            const float x = value_of(last), y = value_of(next);
-            // error of a group's score: with a bias 2^-21 for the s (all below 1) and the sum's rounding; without one
-            // relative to the score (softmax: the logits' difference is rounded too)
-            const float tol = a.bias ? 2e-6f + 2.4e-7f * (fabsf(x) + fabsf(y)) : (a.sigmoid ? 1e-6f : 4e-6f) * (x + y);
-            // (two masked groups are equal; the largest of a group without a bias is compared exactly below)
-            near = !(x - y > tol) && x > 0.1f * kMasked;
-            kept = __ballot_sync(0xffffffffu, stays);
-            if (a.lpg) kept = stays ? 0xffffffffu : 0u;                   // this lane's experts are all of one group
-        }
-        unsigned key[NPL];
+            const bool is = g < a.groups;
+            bool stays = is && rank < a.top_groups;
+            const float x = value_of(__reduce_min_sync(0xffffffffu, stays ? key_of(gs) : 0xffffffffu)),
+                        y = value_of(__reduce_max_sync(0xffffffffu, is && !stays ? key_of(gs) : 0u));
+            // the last that stays and the first that does not: two scores' errors each, and the roundings of the sums. Without a bias the
+            // errors are relative to the scores (softmax: one unit of the exponent's rounding for each of the logits' distance).
+            const float tol = a.bias ? 4.f * serr + 2.5e-7f * (fabsf(x) + fabsf(y)) : (a.sigmoid ? 1e-6f : 4e-6f) * (x + y);
+            // (groups without a live expert, or with one less than `best`, have whole multiples of the masked score: equal)
+            bool undecided = !(x - y > tol) && x > 0.1f * kMasked;
+            if (undecided && (FULL || a.lpg) && x == y) {
+                // equal scores: decided if the logits and biases of the token are all the same (a router at its start)
+                bool same = true;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const bool in = live[i] && (kept == 0xffffffffu || (kept >> ((e0 + i) / a.per) & 1u));
-            key[i] = in ? key_of(r[i]) : 0u;
-        }
-        unsigned lmax = key[0];
-        int lslot = 0;
-        float ls = s[0];
-#pragma unroll
-        for (int i = 1; i < NPL; ++i)
-            if (key[i] > lmax) { lmax = key[i]; lslot = i; ls = s[i]; }
-        // k rounds; with a bias one more, and a look at what is left then, which tell how near the scores are that were left out
-        int my_id = 0;
-        float my_s = 0.f, sum = 0.f, pv_before = 0.f, m_before = 0.f;
-        bool close = false, past = false;     // chosen (or the first left out) close to each other; the first two left out
-        // what two neighbours' difference has to pass: the error of s (a sigmoid's exponential and two roundings, of which the exponential's
-        // counts with 1 - s; softmax: the exponential, the difference of the logits, the sum) and that of adding the bias
-        auto near_by = [&](float x, float sx, float y, float sy) {
-            const float err = a.sigmoid ? sx * (1.4e-7f + 2.5e-7f * (1.f - sx)) + sy * (1.4e-7f + 2.5e-7f * (1.f - sy)) : 1e-6f * (sx + sy) + 6e-8f;
-            return !(x - y > err + 6.1e-8f * (fabsf(x) + fabsf(y))) && x > 0.1f * kMasked;
-        };
-        const int rounds = a.k + (a.bias ? 1 : 0);
-        for (int j = 0; j < rounds; ++j) {
-            const unsigned m = __reduce_max_sync(0xffffffffu, lmax);
-            if (m == 0u) break;               // (no expert is left after the k)
-            const int owner = __ffs(__ballot_sync(0xffffffffu, lmax == m)) - 1;
-            const float pv = __shfl_sync(0xffffffffu, ls, owner), mv = value_of(m);
-            const int id = __shfl_sync(0xffffffffu, e0 + lslot, owner);
-            if (a.bias && j > 0) close |= near_by(m_before, pv_before, mv, pv);
-            pv_before = pv;
-            m_before = mv;
-            if (lane == owner) {
-#pragma unroll
-                for (int i = 0; i < NPL; ++i)
-                    if (i == lslot) key[i] = 0u;
-                lmax = key[0];
-                lslot = 0;
-                ls = s[0];
-#pragma unroll
-                for (int i = 1; i < NPL; ++i)
-                    if (key[i] > lmax) { lmax = key[i]; lslot = i; ls = s[i]; }
-            }
-            if (lane == j) {
-                my_id = id;
-                my_s = pv;
-            }
-            if (j < a.k) sum += pv;
-        }
-        if (near || close) {
-            int n = a.k;                      // the candidates of a cheap ordering: the chosen and the next, if nothing comes near that
-            if (close) {
-                const unsigned m = __reduce_max_sync(0xffffffffu, lmax);
-                const int owner = __ffs(__ballot_sync(0xffffffffu, lmax == m)) - 1;
-                if (m != 0u) past = near_by(m_before, pv_before, value_of(m), __shfl_sync(0xffffffffu, ls, owner));
-                n = min(rounds, a.top_groups * a.per);
-            }
-            if (near || past || !a.sigmoid) {
-                my_id = choose_exact(a, L, a.bias, npl);
-            } else {
-                float my_l = 0.f;
-                for (int j = 0; j < n; ++j) {
-                    const int id = __shfl_sync(0xffffffffu, my_id, j);
-                    float v = 0.f;
-#pragma unroll
-                    for (int i = 0; i < NPL; ++i)
-                        if (e0 + i == id && i < npl) v = L[i];
-                    v = __shfl_sync(0xffffffffu, v, id / npl);
-                    if (lane == j) my_l = v;
+                for (int i = 0; i < NPL; ++i) {
+                    const float l0 = __shfl_sync(0xffffffffu, L[0], 0), b0 = __shfl_sync(0xffffffffu, bias[0], 0);
+                    if (live(i)) same = same && L[i] == l0 && bias[i] == b0;
                 }
-                my_id = order_exact(my_l, a.bias, my_id, n);
+                undecided = !__all_sync(0xffffffffu, same);
             }
-            // the chosen experts' scores, from the lanes that hold them
-            sum = 0.f;
-            for (int j = 0; j < a.k; ++j) {
-                const int id = __shfl_sync(0xffffffffu, my_id, j);
-                float v = 0.f;
+            unsigned kept = 0u;
+            if (undecided) {
+                long long sel[32];
+                float l[NPL];                 // (a copy: the logits themselves stay in registers)
 #pragma unroll
-                for (int i = 0; i < NPL; ++i)
-                    if (e0 + i == id && i < npl) v = s[i];
-                v = __shfl_sync(0xffffffffu, v, id / npl);
-                if (lane == j) my_s = v;
-                sum += v;
+                for (int i = 0; i < NPL; ++i) l[i] = L[i];
+                kept = groups_exact(a, l, sel);
+                stays = is && (kept >> g & 1u);
+            } else if (!FULL && !a.lpg) {
+                kept = __ballot_sync(0xffffffffu, stays);
             }
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+                if (FULL || a.lpg ? !stays : !(kept >> ((e0 + i) / a.per) & 1u)) key[i] = 0u;
+        }
+        if constexpr (NPL > 1) sort_keys(key);
+        // The next best: lane j takes it as its choice. Equal heads go to the lowest lane.
+        unsigned my_key = 0u;
+        int my_id = 0;
+        auto take = [&](int j) {
+            const unsigned head = key[0] >> SB, top = __reduce_max_sync(0xffffffffu, head);
+            const int owner = __ffs(__ballot_sync(0xffffffffu, head == top)) - 1;
+            const unsigned got = __shfl_sync(0xffffffffu, key[0], owner);
+            if (lane == j) {
+                my_key = got;
+                my_id = owner * npl + (int)(SLOT - (got & SLOT));
+            }
+            const bool pop = lane == owner;
+#pragma unroll
+            for (int i = 0; i + 1 < NPL; ++i) key[i] = pop ? key[i + 1] : key[i];
+            key[NPL - 1] = pop ? 0u : key[NPL - 1];
+            return got;
+        };
+        const int left = a.top_groups * a.per;                    // experts of the kept groups
+        int n = min(a.k + 1, left);                               // the k, and the first that is left out
+#pragma unroll 2
+        for (int j = 0; j < n; ++j) take(j);
+        // whether two neighbours' order may be another than their keys'
+        auto near = [&](unsigned hi, unsigned lo) {
+            if (!a.bias) return (hi >> SB) == (lo >> SB);
+            const float x = value_of(hi & ~SLOT), y = value_of(lo & ~SLOT);
+            return !(x - y > 2.f * serr + (6.1e-8f + 1.2e-7f * NPL) * (fabsf(x) + fabsf(y))) && x > 0.1f * kMasked;
+        };
+        auto logit_of = [&](int e) {                              // the parts in their order
+            float l = src[e];
+            for (int q = 1; q < a.nparts; ++q) l += src[q * a.part_stride + e];
+            return l;
+        };
+        const unsigned next = __shfl_down_sync(0xffffffffu, my_key, 1);      // (by all lanes, not behind a condition)
+        const bool close = lane + 1 < n && near(my_key, next);
+        float my_l = lane < n ? logit_of(my_id) : -INFINITY;
+        if (__any_sync(0xffffffffu, close)) {
+            // equal logits with equal biases are equal, and in order; the rest is looked at in 64 bits
+            const float b = a.bias && lane < n ? a.bias[my_id] : 0.f;
+            const float nl = __shfl_down_sync(0xffffffffu, my_l, 1), nb = __shfl_down_sync(0xffffffffu, b, 1);
+            const unsigned bad = __ballot_sync(0xffffffffu, close && !(nl == my_l && nb == b));
+            if (bad) {
+                // candidates until a clear distance, if one is within the warp's lanes
+                bool more = (bad >> (a.k - 1) & 1u) != 0;         // the first that is left out is near the last chosen
+                unsigned last = __shfl_sync(0xffffffffu, my_key, n - 1);
+                while (more && n < min(left, 32)) {
+                    const unsigned got = take(n);
+                    ++n;
+                    more = near(last, got);
+                    last = got;
+                }
+                float l[NPL];
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) l[i] = L[i];
+                if (lane < n) my_l = logit_of(my_id);
+                my_id = more && n < left ? choose_exact(a, l) : order_exact(a, l, my_l, my_id, n);
+                if (lane < a.k) my_l = logit_of(my_id);
+            }
+        }
+        float my_s = 0.f;
+        if (lane < a.k && !(my_l == -INFINITY)) my_s = a.sigmoid ? rcp(1.f + ex2(-kLog2e * my_l)) : ex2((my_l - m) * kLog2e) * inv;
+        if (a.renorm) {
+            const float sum = warp_sum(my_s);
+            my_s = sum == 0.f ? 0.f : my_s / sum;
         }
         if (lane < a.k) {
             a.ids[(size_t)t * a.k + lane] = my_id;
-            a.gates[(size_t)t * a.k + lane] = a.renorm ? (sum == 0.f ? 0.f : my_s * a.scale / sum) : my_s * a.scale;
+            a.gates[(size_t)t * a.k + lane] = my_s * a.scale;
             atomicAdd(&s_hist[my_id], 1);
         }
     }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
-        if (i < npl && e0 + i < a.E) row[e0 + i] = Pacc[i];
+        if (live(i)) row[e0 + i] = Pacc[i];
     __syncthreads();
+    if (a.counts) {                           // the only block: counts, f, P and aux as well
+        __shared__ float s_term[kWarps];
+        float term = 0.f;
+        for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+            float v = 0.f;
+            for (int w = 0; w < kWarps; ++w) v += s_P[(size_t)w * a.E + e];
+            const float P = v / (float)a.T, f = (float)s_hist[e] / ((float)a.k * (float)a.T);
+            a.counts[e] = s_hist[e];
+            a.f[e] = f;
+            a.P[e] = P;
+            term += f * P;
+        }
+        term = warp_sum(term);
+        if (lane == 0) s_term[warp] = term;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kWarps; ++w) term += s_term[w];
+            a.aux[0] = a.alpha * (float)a.E * term;
+        }
+        return;
+    }
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         float v = 0.f;
         for (int w = 0; w < kWarps; ++w) v += s_P[(size_t)w * a.E + e];
@@ -534,12 +640,22 @@ int launch_group_gate(const GroupGate& g, void* ws, cudaStream_t s) {
             int per_sm = 0;
             if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kWarps * 32, smem) != cudaSuccess || per_sm < 1) per_sm = 1;
             G = std::min(grid_of(g.T), per_sm * num_sms());
+            // up to two tokens a warp of one block: a second block and the finalize's launch cost more
+            if (g.T <= 2 * kWarps) {
+                G = 1;
+                a.counts = g.counts; a.f = g.f; a.P = g.P; a.aux = g.aux; a.alpha = g.alpha;
+            }
             return launch_pdl(kernel, dim3(G), dim3(kWarps * 32), smem, s, a);
         };
-        const cudaError_t e = a.npl <= 1 ? launch(group_gate_kernel<1>, 1) : a.npl <= 2 ? launch(group_gate_kernel<2>, 2)
-                            : a.npl <= 4 ? launch(group_gate_kernel<4>, 4) : a.npl <= 8 ? launch(group_gate_kernel<8>, 8)
-                            : a.npl <= 16 ? launch(group_gate_kernel<16>, 16) : launch(group_gate_kernel<32>, 32);
+        a.lpg_log = 0;
+        while (1 << (a.lpg_log + 1) <= a.lpg) ++a.lpg_log;
+        const bool full = a.lpg == 1 << a.lpg_log && g.E == 32 * a.npl;
+#define MOE_GATE(N) (full && a.npl == N ? launch(group_gate_kernel<N, true>, N) : launch(group_gate_kernel<N, false>, N))
+        const cudaError_t e = a.npl <= 1 ? MOE_GATE(1) : a.npl <= 2 ? MOE_GATE(2) : a.npl <= 4 ? MOE_GATE(4) : a.npl <= 8 ? MOE_GATE(8)
+                            : a.npl <= 16 ? MOE_GATE(16) : MOE_GATE(32);
+#undef MOE_GATE
         if (int rc = check_launch(e, "group_gate_kernel")) return rc;
+        if (a.counts) return MOE_OK;
     }
     return launch_router_finalize(w.partial_P, w.partial_C, G, g.T, g.E, g.k, g.alpha, g.counts, g.f, g.P, g.aux, w.term_part,
                                   w.ticket, s);

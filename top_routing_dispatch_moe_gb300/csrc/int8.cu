@@ -44,7 +44,7 @@ __device__ __forceinline__ void store_piece(const Raw16<T>& raw, void* codes, si
             uint4 w[2];
             __half2* h = reinterpret_cast<__half2*>(w);
 #pragma unroll
-            for (int i = 0; i < UNIT / 2; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            for (int i = 0; i < UNIT / 2; ++i) h[i] = halves2(v + 2 * i);
             st32(static_cast<__half*>(codes) + base + k, w);
         } else {
             *reinterpret_cast<uint4*>(static_cast<int8_t*>(codes) + base + k) =
@@ -55,8 +55,8 @@ __device__ __forceinline__ void store_piece(const Raw16<T>& raw, void* codes, si
         for (int j = 0; j < UNIT; ++j) {
             const int k = c * SEG + j * 32 + lane;
             if (k >= width) continue;
-            if constexpr (FORM == FORM_F16) static_cast<__half*>(codes)[base + k] = __float2half_rn(v[j]);
-            else static_cast<int8_t*>(codes)[base + k] = (int8_t)(int)v[j];
+            if constexpr (FORM == FORM_F16) static_cast<__half*>(codes)[base + k] = __float2half_rn(v[j] - MAGIC);
+            else static_cast<uint8_t*>(codes)[base + k] = (uint8_t)__float_as_uint(v[j]);
         }
     }
 }
@@ -122,29 +122,55 @@ __global__ void __launch_bounds__(THREADS)
 dequantize_kernel(const int8_t* codes, const float* scales, int rows, int K, T* out, long long ldo) {
     pdl_wait();
     pdl_trigger();
+    constexpr int U = VEC ? 4 : 1;       // pieces whose codes a lane has under way
     const int lane = threadIdx.x & 31, nseg = (K + SEG - 1) / SEG;
     Walk at((long long)blockIdx.x * WARPS + (threadIdx.x >> 5), (long long)gridDim.x * WARPS, (long long)rows * nseg, nseg);
-    for (; at.left > 0; at.next()) {
-        const int8_t* cr = codes + (size_t)at.row * K;
-        T* orow = out + at.row * ldo;
-        const float s = scales[at.row];
+    while (at.left > 0) {
         if constexpr (VEC) {
-            const int k = at.seg * SEG + lane * UNIT;
-            if (k >= K) continue;
-            const uint4 q = __ldcs(reinterpret_cast<const uint4*>(cr + k));
-            const int8_t* c = reinterpret_cast<const int8_t*>(&q);
-            alignas(16) T o[UNIT];
+            uint4 q[U];
+            float s[U];
+            T* to[U];
 #pragma unroll
-            for (int i = 0; i < UNIT; ++i) o[i] = rounded<T>((float)c[i] * s);
-            const uint4* ov = reinterpret_cast<const uint4*>(o);
+            for (int u = 0; u < U; ++u) {
+                const int k = at.seg * SEG + lane * UNIT;
+                to[u] = nullptr;
+                if (at.left > 0 && k < K) {
+                    q[u] = __ldcs(reinterpret_cast<const uint4*>(codes + (size_t)at.row * K + k));
+                    s[u] = scales[at.row];
+                    to[u] = out + at.row * ldo + k;
+                }
+                if (at.left > 0) at.next();
+            }
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(T); ++i) __stcs(reinterpret_cast<uint4*>(orow + k) + i, ov[i]);
+            for (int u = 0; u < U; ++u) {
+                if (!to[u]) continue;
+                float v[UNIT];
+                values4(q[u].x, s[u], v);
+                values4(q[u].y, s[u], v + 4);
+                values4(q[u].z, s[u], v + 8);
+                values4(q[u].w, s[u], v + 12);
+                alignas(16) T o[UNIT];
+#pragma unroll
+                for (int i = 0; i < UNIT; ++i) o[i] = rounded<T>(v[i]);
+                const uint4* ov = reinterpret_cast<const uint4*>(o);
+                if ((reinterpret_cast<uintptr_t>(to[u]) & 31u) == 0) {
+#pragma unroll
+                    for (int i = 0; i < (int)sizeof(T); i += 2) st32(reinterpret_cast<uint4*>(to[u]) + i, ov + i);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < (int)sizeof(T); ++i) reinterpret_cast<uint4*>(to[u])[i] = ov[i];
+                }
+            }
         } else {
+            const int8_t* cr = codes + (size_t)at.row * K;
+            T* orow = out + at.row * ldo;
+            const float s = scales[at.row];
 #pragma unroll
             for (int j = 0; j < UNIT; ++j) {
                 const int k = at.seg * SEG + j * 32 + lane;
                 if (k < K) orow[k] = rounded<T>((float)cr[k] * s);
             }
+            at.next();
         }
     }
 }

@@ -60,37 +60,62 @@ static __device__ __noinline__ float code_at_border(float x, float q, float amax
     return copysignf(up ? lo + 1.f : lo, x);
 }
 
-// N values (even) of one row -> their codes, as whole numbers in fp32. x * inv is off by less than 127 * 2^-23 (both roundings):
-// only a product that close to a border is looked at again.
+// 1.5 * 2^23: its sum with |q| < 2^22 is q rounded to a whole number, ties to even, whose two's complement are the sum's low bits.
+constexpr float MAGIC = 12582912.f;
+
+// N values (even) of one row -> MAGIC + their codes. x * inv is off by less than 127 * 2^-23 (both roundings): only a product that
+// close to a border is looked at again. Two at a time: the divisions that the definition names would cost four times as much.
 template <int N>
 __device__ __forceinline__ void codes_of(float* v, float inv, float amax) {
-    float q[N], far = 0.f;
-    const float magic = 12582912.f;                  // 1.5 * 2^23: its sum with |q| < 2^22 is q rounded to a whole number, ties to even
+    float t[N], far = 0.f;
+    if (inv == 0.f) {                                // (a row of zeros, or one that holds an infinity or a NaN)
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        q[i] = v[i] * inv;
-        const float n = __fadd_rn(__fadd_rn(q[i], magic), -magic);
-        far = fmaxf(far, fabsf(q[i] - n));
+        for (int i = 0; i < N; ++i) v[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        float q[2], d[2];
+        mul2(q, v + i, inv);
+        add2(t + i, q, MAGIC);
+        add2(d, t + i, -MAGIC);
+        sub2(d, q, d);
+        far = max3_abs(far, d[0], d[1]);
     }
     if (far > 0.49998f) {                            // (rolled, through local memory: it hardly runs)
         float x[N], y[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) { x[i] = v[i]; y[i] = q[i]; }
+        for (int i = 0; i < N; ++i) { x[i] = v[i]; y[i] = t[i]; }
 #pragma unroll 1
         for (int i = 0; i < N; ++i) {
-            const float n = __fadd_rn(__fadd_rn(y[i], magic), -magic);
-            if (fabsf(y[i] - n) > 0.49998f) y[i] = code_at_border(x[i], y[i], amax);
+            const float q = x[i] * inv;
+            if (fabsf(q - (y[i] - MAGIC)) > 0.49998f) y[i] = code_at_border(x[i], q, amax) + MAGIC;
         }
 #pragma unroll
-        for (int i = 0; i < N; ++i) q[i] = y[i];
+        for (int i = 0; i < N; ++i) t[i] = y[i];
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = inv == 0.f ? 0.f : __fadd_rn(__fadd_rn(q[i], magic), -magic);
+    for (int i = 0; i < N; ++i) v[i] = t[i];
 }
-// Four whole numbers -128 .. 127 -> bytes.
+// Four codes as codes_of leaves them -> bytes; two -> fp16 numbers.
 __device__ __forceinline__ uint32_t bytes4(const float* v) {
-    const uint32_t a = (uint32_t)(int)v[0], b = (uint32_t)(int)v[1], c = (uint32_t)(int)v[2], d = (uint32_t)(int)v[3];
-    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+    return __byte_perm(__byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x0040),
+                       __byte_perm(__float_as_uint(v[2]), __float_as_uint(v[3]), 0x0040), 0x5410);
+}
+__device__ __forceinline__ __half2 halves2(const float* v) {
+    float n[2];
+    add2(n, v, -MAGIC);
+    return __floats2half2_rn(n[0], n[1]);
+}
+// Four bytes of codes -> fp32 numbers times s: a byte with its sign bit turned, under 0x4B0000, is the number 2^23 + 128 + code.
+__device__ __forceinline__ void values4(uint32_t w, float s, float* v) {
+    w ^= 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + i));
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        add2(v + i, v + i, -8388736.f);
+        mul2(v + i, v + i, s);
+    }
 }
 #endif
 

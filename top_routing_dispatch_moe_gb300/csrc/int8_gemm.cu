@@ -221,27 +221,37 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) few_rows_kernel(const Params p
 // on the chip, on their way into tensor memory, from where tcgen05.mma takes its first operand. The product is turned over for that:
 // the channels are its rows (M) and a group's rows its columns (N), which also fits N to the group: 32 to 256 in steps of 32.
 //
-// A cluster of two CTAs computes 256 channels x up to 256 rows with tcgen05.mma.cta_group::2: each converts its own 128 channels and
+// A cluster of two CTAs computes 256 channels x up to ROWS rows with tcgen05.mma.cta_group::2: each converts its own 128 channels and
 // stages half of the rows. A persistent CTA per SM with eighteen warps:
-//   warp 0      producer: per stage of 64 columns 8 KB of packed weight by one bulk copy, and the CTA's half of the rows by TMA;
+//   warp 0      producer: per stage of 128 columns 16 KB of packed weight by one bulk copy, and the CTA's half of the rows by TMA;
 //   warp 1      (of the even CTA) the MMAs of a stage;
 //   warps 2-9   epilogue, two to a quarter of the tensor memory lanes, 64 columns at a time in turn: a lane is a channel, a column a row
 //               of the output; SwiGLU's gate and up are neighbouring lanes and exchange halves;
 //   warps 10-17 converters, two to a quarter, stages in turn: a lane reads its channel's 64 bytes, puts each under 0x64 (the fp16 number
-//               1024 + byte), subtracts 1152 and stores 32 columns of tensor memory.
-// Tensor memory: two accumulators of 256 columns that share 128 (the epilogue reads the shared ones first and hands them back), and four
-// stages of converted weights, 32 columns each.
-constexpr int P_ROWS = 256;
+//               1024 + byte), subtracts 1152 and stores 32 columns of tensor memory, twice a stage.
+// Tensor memory: two accumulators of 256 columns that share 128 (the epilogue reads the shared ones first and hands them back), and two
+// stages of converted weights, 64 columns each.
+//
+// ROWS, the most rows of a tile: 256 where groups have many; 128 and 64 leave more of the shared memory to stages under way where
+// the weights' bytes decide (64 KB of weights under way on an SM brought 3.8 TB/s, whatever the stages' size), and tensor memory to
+// accumulators that share nothing and four stages of converted weights.
 constexpr int EPI_WARPS = 8, CONV_WARPS = 8;
 constexpr int P_THREADS = 32 * (2 + EPI_WARPS + CONV_WARPS);
-constexpr int STAGES = 8;
-constexpr int ROWS_BYTES = P_ROWS / 2 * STAGE_K * 2;           // 16 KB
-constexpr int A_BUFS = 4, A_COLS = STAGE_K / 2;
-constexpr int ACC2 = 128, A_COL = ACC2 + P_ROWS;
+constexpr int PER = 2;                                         // packed pieces (64 columns) of a stage
+constexpr int A_COLS = PER * STAGE_K / 2;                      // tensor memory columns of a stage of converted weights
 constexpr int TMEM_COLS = 512;
-static_assert(A_COL + A_BUFS * A_COLS == TMEM_COLS, "tensor memory columns");
-constexpr int P_SMEM = 1024 + STAGES * (PIECE + ROWS_BYTES) + 256 + GROUPS_INTS * 4 + 16;
-static_assert(P_SMEM <= 227 * 1024, "shared memory per CTA");
+template <int ROWS>
+struct Tile {
+    static constexpr int STAGES = ROWS == 256 ? 4 : ROWS == 128 ? 6 : 8;
+    static constexpr int X_BYTES = ROWS / 2 * STAGE_K * 2;     // the rows' 64 columns that go with a piece
+    static constexpr int STAGE_BYTES = PER * (PIECE + X_BYTES);
+    static constexpr int ACC2 = ROWS == 256 ? 128 : ROWS;      // the second accumulator's first column
+    static constexpr int A_BUFS = ROWS == 256 ? 2 : 4, A_COL = ACC2 + ROWS;
+    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 256 + GROUPS_INTS * 4 + 16;
+    static_assert(A_COL + A_BUFS * A_COLS <= TMEM_COLS, "tensor memory columns");
+    static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+    static_assert(8 * (2 * STAGES + A_BUFS + 3) + 8 <= 256, "barriers");
+};
 
 // D fp32 (bits 4-5 = 1), A and B fp16 (0), K-major, N >> 3 at bits 17-22, M = 256 at bits 24-28.
 __device__ __forceinline__ uint32_t idesc_pair(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((256u >> 4) << 24); }
@@ -270,17 +280,17 @@ __device__ __forceinline__ Item map_item(const Params& p, const Groups& gs, int 
     return Item{g, ch, gs.beg[g] + t * per, gs.beg[g] + min(n, t * per + per)};
 }
 
-// 64 columns of the accumulator at tcol, the rows row0 .. of the output (n of them, at least one); this lane's channel is `ch`. `read`
+// COLS columns of the accumulator at tcol, the rows row0 .. of the output (n of them, at least one); this lane's channel is `ch`. `read`
 // runs once the columns are in registers.
-template <int EPI, typename Fn>
+template <int EPI, int COLS, typename Fn>
 __device__ __forceinline__ void epilogue_chunk(const Params& p, int g, uint32_t tcol, int ch, int row0, int n, float scale, Fn read) {
     const int lane = threadIdx.x & 31;
     const bool mine = ch < p.N;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < COLS / 32; ++h) {
         float v[32];
         tmem_ld32(tcol + 32 * h, v);
-        if (h == 1) read();
+        if (h == COLS / 32 - 1) read();
         const int r0 = row0 + 32 * h, nr = n - 32 * h;
         if (nr <= 0) continue;
         const float xs = lane < nr ? p.a_scales[r0 + lane] : 0.f;
@@ -314,13 +324,15 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, int g, uint32_t 
     }
 }
 
-template <int EPI>
+template <int EPI, int ROWS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tm128, const __grid_constant__ CUtensorMap tm16, const Params p) {
+    using C = Tile<ROWS>;
+    constexpr int STAGES = C::STAGES, A_BUFS = C::A_BUFS, X_BYTES = C::X_BYTES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const uint32_t sX = smem_u32(smem), sW = sX + STAGES * ROWS_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * (PIECE + ROWS_BYTES));
+    const uint32_t sX = smem_u32(smem), sW = sX + STAGES * PER * X_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE_BYTES);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
@@ -344,7 +356,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm128, const __grid_constant__ C
         prefetch_tmap(&tm16);
     }
     // (a programmatic dependent of the quantisation: the groups, the set-up and the first stages of weights do not wait for it)
-    find_groups<P_THREADS>(p, P_ROWS, gs);
+    find_groups<P_THREADS>(p, ROWS, gs);
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
     tc_fence_before();
     cluster_sync_all();                          // barriers initialised and both CTAs' tensor memory allocated
@@ -352,6 +364,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm128, const __grid_constant__ C
     const uint32_t tmem = *tmem_slot;
     const uint32_t peer_abort = map_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
     const int CT = (p.NB + 1) >> 1, NC = gridDim.x >> 1, cid = blockIdx.x >> 1, total = uniform(gs.first[p.G] * CT);
+    const int NS = (p.KST + PER - 1) / PER;      // stages of a tile
     if (warp != 0) {
         pdl_wait();
         pdl_trigger();
@@ -368,27 +381,32 @@ pair_kernel(const __grid_constant__ CUtensorMap tm128, const __grid_constant__ C
             const int nb = uniform(2 * it.ch + (int)rank);
             const bool some = nb < p.NB;             // (the odd CTA of the last tile may have no channels)
             const uint8_t* w0 = p.w + ((size_t)uniform(it.g) * p.NB + nb) * p.KST * PIECE;
-            const uint32_t tx = (uint32_t)(half * STAGE_K * 2 + (some ? PIECE : 0));
+            const int tx = half * STAGE_K * 2 + (some ? PIECE : 0);
             auto weights = [&](int st, int kb) {
-                expect_elected(full(st), tx);
-                if (some) bulk_elected(sW + st * PIECE, w0 + (size_t)kb * PIECE, PIECE, full(st));
+                const int n = min(PER, p.KST - kb * PER);
+                expect_elected(full(st), (uint32_t)(n * tx));
+                if (some) bulk_elected(sW + st * PER * PIECE, w0 + (size_t)kb * PER * PIECE, n * PIECE, full(st));
             };
             int early = 0;                          // stages whose weights are on their way before the rows' codes are there
             if (w == cid) {
-                for (; early < min(STAGES, p.KST); ++early) weights(early, early);
+                for (; early < min(STAGES, NS); ++early) weights(early, early);
                 pdl_wait();
                 pdl_trigger();
             }
-            for (int kb = 0; kb < p.KST; ++kb) {
+            for (int kb = 0; kb < NS; ++kb) {
                 if (kb >= early) {
                     if (!ready) ok = wait_warp_pair(empty(stage), phase ^ 1u, p.wait_limit, abort_flag, peer_abort, p.err, 0x340u);
                     if (!ok) break;
                     weights(stage, kb);
                 }
-                const uint32_t f = full(stage), sx = sX + stage * ROWS_BYTES;
-                if (half == 128) tma_elected(sx, &tm128, kb * STAGE_K, row, f);
-                else
-                    for (int b = 0; b < half; b += 16) tma_elected(sx + b * 128, &tm16, kb * STAGE_K, row + b, f);
+                const uint32_t f = full(stage);
+                for (int q = 0; q < min(PER, p.KST - kb * PER); ++q) {
+                    const uint32_t sx = sX + (stage * PER + q) * X_BYTES;
+                    const int k = (kb * PER + q) * STAGE_K;
+                    if (ROWS == 256 && half == 128) tma_elected(sx, &tm128, k, row, f);
+                    else
+                        for (int b = 0; b < half; b += 16) tma_elected(sx + b * 128, &tm16, k, row + b, f);
+                }
                 issued |= 1u << stage;
                 last_par = (last_par & ~(1u << stage)) | (phase << stage);
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -411,8 +429,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tm128, const __grid_constant__ C
             bool ok = true, ready = false;
             for (int w = cid; w < total && ok; w += NC, ++iter) {
                 const Item it = map_item(p, gs, CT, w, at);
-                const uint32_t id = idesc_pair(uniform((it.row1 - it.row0 + 31) & ~31)), d = tm + (iter & 1) * ACC2;
-                for (int kb = 0; kb < p.KST; ++kb) {
+                const uint32_t id = idesc_pair(uniform((it.row1 - it.row0 + 31) & ~31)), d = tm + (iter & 1) * C::ACC2;
+                for (int kb = 0; kb < NS; ++kb) {
                     if (!ready)
                         ok = (kb > 0 || wait_warp_pair(tempty, (iter & 1) ^ 1u, p.wait_limit, abort_flag, peer_abort, p.err, 0x350u)) &&
                              wait_warp_pair(afull(b), bphase, p.wait_limit, abort_flag, peer_abort, p.err, 0x351u) &&
@@ -420,16 +438,22 @@ pair_kernel(const __grid_constant__ CUtensorMap tm128, const __grid_constant__ C
                               wait_warp_pair(full(stage), phase, p.wait_limit, abort_flag, peer_abort, p.err, 0x352u));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t s0 = stage, a = tm + A_COL + b * A_COLS;
-                    const bool last = kb + 1 == p.KST;
-                    const uint64_t db = sw128_desc(sX + s0 * ROWS_BYTES);
+                    const uint32_t s0 = stage, a = tm + C::A_COL + b * A_COLS;
+                    const bool last = kb + 1 == NS, both = (kb + 1) * PER <= p.KST;
+                    const uint64_t db = sw128_desc(sX + s0 * PER * X_BYTES), db1 = sw128_desc(sX + (s0 * PER + 1) * X_BYTES);
                     mma_pair(d, a, db, id, kb != 0);
                     mma_pair(d, a + 8, db + 2, id, 1u);
+                    mma_pair(d, a + 16, db + 4, id, 1u);
+                    mma_pair(d, a + 24, db + 6, id, 1u);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                     if (++b == A_BUFS) { b = 0; bphase ^= 1u; }
                     const bool t0 = test_phase(full(stage), phase), t1 = test_phase(afull(b), bphase);
-                    mma_pair(d, a + 16, db + 4, id, 1u);
-                    mma_pair(d, a + 24, db + 6, id, 1u);
+                    if (both) {
+                        mma_pair(d, a + 32, db1, id, 1u);
+                        mma_pair(d, a + 40, db1 + 2, id, 1u);
+                        mma_pair(d, a + 48, db1 + 4, id, 1u);
+                        mma_pair(d, a + 56, db1 + 6, id, 1u);
+                    }
                     commit_pair_elected(empty(s0));
                     if (last) commit_pair_elected(tfull);
                     ready = __all_sync(0xffffffffu, t0 && t1 && !last);
@@ -443,31 +467,37 @@ pair_kernel(const __grid_constant__ CUtensorMap tm128, const __grid_constant__ C
         int i = 0;                                  // stages so far, this CTA's in all
         bool ok = true;
         for (int w = cid; w < total && ok; w += NC) {
-            for (int kb = 0; kb < p.KST; ++kb, ++i) {
+            for (int kb = 0; kb < NS; ++kb, ++i) {
                 if ((i & 1) != turn) continue;
                 const int st = i % STAGES, b = i % A_BUFS, old = (i - A_BUFS) % STAGES;
                 ok = test_warp(full(st), (i / STAGES) & 1) ||
                      wait_warp_pair(full(st), (i / STAGES) & 1, p.wait_limit, abort_flag, peer_abort, p.err, 0x360u);
                 if (!ok) break;
-                uint32_t q[16], v[32];
-                const uint32_t src = sW + st * PIECE + (quarter + lane) * 16;
+                const int n = min(PER, p.KST - kb * PER);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) ld_shared_v4(src + c * (BLOCK_N * 16), q + 4 * c);
+                for (int h = 0; h < PER; ++h) {
+                    if (h >= n) break;
+                    uint32_t q[16], v[32];
+                    const uint32_t src = sW + (st * PER + h) * PIECE + (quarter + lane) * 16;
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const __half2 off = __float2half2_rn(-1152.f);
-                    const uint32_t lo = __byte_perm(q[c], 0x64646464u, 0x4140), hi = __byte_perm(q[c], 0x64646464u, 0x4342);
-                    const __half2 a = __hadd2(*reinterpret_cast<const __half2*>(&lo), off), e = __hadd2(*reinterpret_cast<const __half2*>(&hi), off);
-                    v[2 * c] = *reinterpret_cast<const uint32_t*>(&a);
-                    v[2 * c + 1] = *reinterpret_cast<const uint32_t*>(&e);
+                    for (int c = 0; c < 4; ++c) ld_shared_v4(src + c * (BLOCK_N * 16), q + 4 * c);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const __half2 off = __float2half2_rn(-1152.f);
+                        const uint32_t lo = __byte_perm(q[c], 0x64646464u, 0x4140), hi = __byte_perm(q[c], 0x64646464u, 0x4342);
+                        const __half2 a = __hadd2(*reinterpret_cast<const __half2*>(&lo), off), e = __hadd2(*reinterpret_cast<const __half2*>(&hi), off);
+                        v[2 * c] = *reinterpret_cast<const uint32_t*>(&a);
+                        v[2 * c + 1] = *reinterpret_cast<const uint32_t*>(&e);
+                    }
+                    if (h == 0 && i >= A_BUFS) {    // the buffer's last MMAs have completed
+                        const uint32_t par = ((i - A_BUFS) / STAGES) & 1;
+                        ok = test_warp(empty(old), par) || wait_warp_pair(empty(old), par, p.wait_limit, abort_flag, peer_abort, p.err, 0x361u);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    tmem_st32(tmem + ((uint32_t)quarter << 16) + C::A_COL + b * A_COLS + h * (STAGE_K / 2), v);
                 }
-                if (i >= A_BUFS) {                  // the buffer's last MMAs have completed
-                    const uint32_t par = ((i - A_BUFS) / STAGES) & 1;
-                    ok = test_warp(empty(old), par) || wait_warp_pair(empty(old), par, p.wait_limit, abort_flag, peer_abort, p.err, 0x361u);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                tmem_st32(tmem + ((uint32_t)quarter << 16) + A_COL + b * A_COLS, v);
+                if (!ok) break;
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
@@ -485,20 +515,27 @@ pair_kernel(const __grid_constant__ CUtensorMap tm128, const __grid_constant__ C
             if (ch < p.N) scale = EPI == EPI_OUT ? p.w_scales[(size_t)it.g * p.N + ch] : ((ch & 1) ? p.w_scales_up : p.w_scales)[(size_t)it.g * F + (ch >> 1)];
             if (!wait_warp_pair(tfull, iter & 1, p.wait_limit, abort_flag, peer_abort, p.err, 0x370u)) break;
             tc_fence_after();
-            const uint32_t tbase = tmem + (iter & 1) * ACC2 + ((uint32_t)quarter << 16);
+            const uint32_t tbase = tmem + (iter & 1) * C::ACC2 + ((uint32_t)quarter << 16);
             auto hand_back = [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_pair(tempty0);
             };
-            // the chunks whose columns the next tile shares come first: the last two of an even tile, the first two of an odd
-            const int first = (iter & 1 ? 0 : 2) + half, second = first ^ 2, n = it.row1 - it.row0;
             const bool warp_live = ch - lane < p.N;
-            if (warp_live && 64 * first < n)
-                epilogue_chunk<EPI>(p, it.g, tbase + 64 * first, ch, it.row0 + 64 * first, n - 64 * first, scale, hand_back);
-            else hand_back();
-            if (warp_live && 64 * second < n)
-                epilogue_chunk<EPI>(p, it.g, tbase + 64 * second, ch, it.row0 + 64 * second, n - 64 * second, scale, [] {});
+            const int n = it.row1 - it.row0;
+            if constexpr (ROWS == 256) {
+                // the chunks whose columns the next tile shares come first: the last two of an even tile, the first two of an odd
+                const int first = 64 * ((iter & 1 ? 0 : 2) + half), second = first ^ 128;
+                if (warp_live && first < n) epilogue_chunk<EPI, 64>(p, it.g, tbase + first, ch, it.row0 + first, n - first, scale, hand_back);
+                else hand_back();
+                if (warp_live && second < n)
+                    epilogue_chunk<EPI, 64>(p, it.g, tbase + second, ch, it.row0 + second, n - second, scale, [] {});
+            } else {
+                const int first = ROWS / 2 * half;
+                if (warp_live && first < n)
+                    epilogue_chunk<EPI, ROWS / 2>(p, it.g, tbase + first, ch, it.row0 + first, n - first, scale, hand_back);
+                else hand_back();
+            }
         }
     }
     cluster_sync_all();                          // every role of both CTAs has left its loop
@@ -526,22 +563,24 @@ static int rows_map(CUtensorMap* m, const void* base, long long rows, int width,
     return MOE_OK;
 }
 
-template <int EPI>
+template <int EPI, int ROWS>
 static int launch_pair(const Params& p, cudaStream_t s) {
+    constexpr int P_SMEM = Tile<ROWS>::SMEM;
+    const auto kernel = pair_kernel<EPI, ROWS>;
     static int clusters[64];                     // resident pairs, in the context they were asked for
     static unsigned long long attr_ctx[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return set_error(MOE_ERR_CUDA, "int8 product: no usable current device");
     const unsigned long long ctx = context_id();
     if (!clusters[dev] || ctx == 0 || attr_ctx[dev] != ctx) {
-        cudaError_t e = cudaFuncSetAttribute(pair_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
         if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "int8 product smem attribute: %s", cudaGetErrorString(e));
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * (num_sms() / 2));
         cfg.blockDim = dim3(P_THREADS);
         cfg.dynamicSmemBytes = P_SMEM;
         int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, pair_kernel<EPI>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
         if (e != cudaSuccess || n <= 0) return set_error(MOE_ERR_CUDA, "int8 product: no resident cluster of two CTAs (%s)", cudaGetErrorString(e));
         clusters[dev] = std::min(n, num_sms() / 2);
         attr_ctx[dev] = context_id();
@@ -550,10 +589,18 @@ static int launch_pair(const Params& p, cudaStream_t s) {
     const int width = p.KST * STAGE_K;
     if (int rc = rows_map(&m16, p.a, p.rows, width, 16)) return rc;
     m128 = m16;                                  // (no tile of 256 rows: the map of whole halves is not used)
-    if (p.rows >= 128)
+    if (ROWS == 256 && p.rows >= 128)
         if (int rc = rows_map(&m128, p.a, p.rows, width, 128)) return rc;
-    return check_launch(launch_pdl(pair_kernel<EPI>, dim3(2 * clusters[dev]), dim3(P_THREADS), P_SMEM, s, m128, m16, p),
+    return check_launch(launch_pdl(kernel, dim3(2 * clusters[dev]), dim3(P_THREADS), P_SMEM, s, m128, m16, p),
                         EPI == EPI_SWIGLU ? "int8 pair_kernel<swiglu>" : "int8 pair_kernel");
+}
+
+template <int EPI>
+static int launch_pairs(const Params& p, cudaStream_t s) {
+    const long long avg = p.rows / p.G;          // a group's rows, if they are alike
+    if (avg <= 48) return launch_pair<EPI, 64>(p, s);
+    if (avg <= 128) return launch_pair<EPI, 128>(p, s);
+    return launch_pair<EPI, 256>(p, s);
 }
 
 // Dot products on the CUDA cores where the groups have few rows.
@@ -561,9 +608,9 @@ static bool few_rows(int rows, int G) { return rows <= FEW_ROWS * std::min(G, 2)
 static int operand_form(int rows, int G) { return few_rows(rows, G) ? FORM_BYTES : FORM_F16; }
 
 static int launch_product(const Params& p, int epi, cudaStream_t s) {
-    MOE_REQUIRE(((long long)p.rows / P_ROWS + p.G) * cdiv(p.NB, 2) < (1LL << 31), MOE_ERR_INVALID_ARG,
+    MOE_REQUIRE(((long long)p.rows / 64 + p.G) * cdiv(p.NB, 2) < (1LL << 31), MOE_ERR_INVALID_ARG,
                 "8-bit product: %d rows by %d channels are over 2^31 tiles", p.rows, p.N);
-    if (!few_rows(p.rows, p.G)) return epi == EPI_OUT ? launch_pair<EPI_OUT>(p, s) : launch_pair<EPI_SWIGLU>(p, s);
+    if (!few_rows(p.rows, p.G)) return epi == EPI_OUT ? launch_pairs<EPI_OUT>(p, s) : launch_pairs<EPI_SWIGLU>(p, s);
     auto go = [&](auto kernel) {
         int per_sm = 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, FEW_THREADS, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
