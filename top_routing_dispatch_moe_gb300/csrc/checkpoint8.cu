@@ -62,15 +62,16 @@ checkpoint_save_kernel(const T* x, long long ldx, int rows, int C, const int32_t
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (row[u] < 0) continue;
-                float amax = unit_amax(raw[u]), inv;
+                Steps st;
+                float amax = unit_amax(raw[u]);
 #pragma unroll
                 for (int o = 4; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                const float s = scale_of(amax, inv);
+                const float s = scale_of(amax, st);
                 const T* e = reinterpret_cast<const T*>(raw[u].q);
                 float v[UNIT];
 #pragma unroll
                 for (int i = 0; i < UNIT; ++i) v[i] = as_f32(e[i]);
-                codes_of<UNIT>(v, inv, amax);
+                codes_of<T, UNIT>(v, st);
                 if (k[u] < C) {
                     *reinterpret_cast<uint4*>(codes + (size_t)row[u] * C + k[u]) = make_uint4(bytes4(v), bytes4(v + 4), bytes4(v + 8), bytes4(v + 12));
                     if ((lane & 7) == 0) scales[(size_t)row[u] * nb + k[u] / CKPT] = s;
@@ -86,7 +87,8 @@ checkpoint_save_kernel(const T* x, long long ldx, int rows, int C, const int32_t
             for (int b = 0; b < 4; ++b) {
                 const int k0 = seg * 512 + b * CKPT;
                 if (k0 >= C) break;
-                float v[4], amax = 0.f, inv;
+                Steps st;
+                float v[4], amax = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     v[j] = k0 + j * 32 + lane < C ? as_f32(xr[k0 + j * 32 + lane]) : 0.f;
@@ -94,8 +96,8 @@ checkpoint_save_kernel(const T* x, long long ldx, int rows, int C, const int32_t
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                const float s = scale_of(amax, inv);
-                codes_of<4>(v, inv, amax);
+                const float s = scale_of(amax, st);
+                codes_of<T, 4>(v, st);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (k0 + j * 32 + lane < C) cr[k0 + j * 32 + lane] = (int8_t)__float_as_uint(v[j]);

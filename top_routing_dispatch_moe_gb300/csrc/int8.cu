@@ -30,13 +30,13 @@ __device__ __forceinline__ Raw16<T> load_piece(const T* row, int c, int K) {
     return r;
 }
 template <typename T, int FORM, bool VEC>
-__device__ __forceinline__ void store_piece(const Raw16<T>& raw, void* codes, size_t base, int c, int width, float inv, float amax) {
+__device__ __forceinline__ void store_piece(const Raw16<T>& raw, void* codes, size_t base, int c, int width, const Steps& st) {
     const int lane = threadIdx.x & 31;
     const T* e = reinterpret_cast<const T*>(raw.q);
     float v[UNIT];
 #pragma unroll
     for (int i = 0; i < UNIT; ++i) v[i] = as_f32(e[i]);
-    codes_of<UNIT>(v, inv, amax);
+    codes_of<T, UNIT>(v, st);
     if constexpr (VEC) {
         const int k = c * SEG + lane * UNIT;
         if (k >= width) return;
@@ -103,17 +103,17 @@ quantize_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, int r
         for (int i = 0; i < WPR; ++i) amax = max_nan(amax, s_amax[warp - w + i]);
     }
     if (row >= rows) return;
-    float inv;
-    const float scale = scale_of(amax, inv);
+    Steps st;
+    const float scale = scale_of(amax, st);
     if (w == 0 && lane == 0) scales[row] = scale;
     const size_t base = (size_t)row * width;
     if (held) {
 #pragma unroll
         for (int i = 0; i < HELD; ++i)
-            if (i * WPR + w < pieces) store_piece<T, FORM, VEC>(raw[i], codes, base, i * WPR + w, width, inv, amax);
+            if (i * WPR + w < pieces) store_piece<T, FORM, VEC>(raw[i], codes, base, i * WPR + w, width, st);
     } else {
         for (int c = w; c < pieces; c += WPR)
-            store_piece<T, FORM, VEC>(load_piece<T, VEC>(xr, c, k_in), codes, base, c, width, inv, amax);
+            store_piece<T, FORM, VEC>(load_piece<T, VEC>(xr, c, k_in), codes, base, c, width, st);
     }
 }
 
