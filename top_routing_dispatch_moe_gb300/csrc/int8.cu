@@ -179,7 +179,7 @@ dequantize_kernel(const int8_t* codes, const float* scales, int rows, int K, T* 
 __global__ void __launch_bounds__(THREADS)
 pack_kernel(const int8_t* __restrict__ a, const int8_t* __restrict__ b, int N, int K, int NB, int KST, size_t chunks, uint4* __restrict__ out) {
     for (size_t i = (size_t)blockIdx.x * THREADS + threadIdx.x; i < chunks; i += (size_t)gridDim.x * THREADS) {
-        const int r = (int)(i & 127), c = (int)(i >> 7 & 3);
+        const int c = (int)(i >> 7 & 3), r = (int)(i & 127) ^ (2 * c);
         const size_t piece = i >> 9, at = piece / KST;
         const int k0 = (int)(piece - at * KST) * STAGE_K + c * UNIT, nb = (int)(at % NB);
         const size_t g = at / NB;
@@ -228,8 +228,7 @@ int launch_quantize(const void* x, long long ldx, int x_rows, const int32_t* src
     cudaError_t e = cudaErrorInvalidValue;
 #define MOE_QUANT(T)                                                                                                       \
     e = form == FORM_ROWS ? quantize_form<T, FORM_ROWS>(x, ldx, x_rows, src, rows, K, codes, scales, err, s)               \
-      : form == FORM_F16 ? quantize_form<T, FORM_F16>(x, ldx, x_rows, src, rows, K, codes, scales, err, s)                 \
-                         : quantize_form<T, FORM_BYTES>(x, ldx, x_rows, src, rows, K, codes, scales, err, s)
+                          : quantize_form<T, FORM_F16>(x, ldx, x_rows, src, rows, K, codes, scales, err, s)
     if (dtype == MOE_F32) MOE_QUANT(float);
     else if (dtype == MOE_BF16) MOE_QUANT(__nv_bfloat16);
     else MOE_QUANT(__half);

@@ -19,8 +19,8 @@ constexpr int CKPT = 128;            // columns under one scale of a checkpoint
 inline int pad64(int k) { return (k + 63) / 64 * 64; }
 
 // A packed weight [G][N][K]: pieces [G][N / 128][K / 64] of 8 KB, the 16-byte chunk c (columns 16 c ..) of channel r of a piece at
-// (c * 128 + r) * 16, so that a warp whose lanes hold 32 channels reads 512 contiguous bytes. Bytes are code + 128 (the byte under
-// 0x64 is the fp16 number 1024 + byte), 128 past N and K.
+// (c * 128 + (r ^ 2 c)) * 16: eight lanes with a chunk of eight channels each, or with four chunks of two, read different banks. Bytes
+// are code + 128 (the byte under 0x64 is the fp16 number 1024 + byte), 128 past N and K.
 struct WeightLayout { int NB, KST; size_t total; };
 inline WeightLayout weight_layout(int G, int N, int K) {
     WeightLayout L;
@@ -146,9 +146,8 @@ __device__ __forceinline__ void values4(uint32_t w, float s, float* v) {
 }
 #endif
 
-// Form of quantised rows: codes [rows][K] as they are kept; the product's operands [rows][pad64(K)], codes as fp16 numbers or as
-// bytes, 0 past K.
-enum Form : int { FORM_ROWS = 0, FORM_F16 = 1, FORM_BYTES = 2 };
+// Form of quantised rows: codes [rows][K] as they are kept; the product's operand [rows][pad64(K)], codes as fp16 numbers, 0 past K.
+enum Form : int { FORM_ROWS = 0, FORM_F16 = 1 };
 // Rows of x (or those that src names, -1: a row of zeros) -> codes and scales, a programmatic dependent of the kernel before.
 int launch_quantize(const void* x, long long ldx, int x_rows, const int32_t* src, int rows, int K, int dtype, int form, void* codes,
                     float* scales, unsigned* err, cudaStream_t s);

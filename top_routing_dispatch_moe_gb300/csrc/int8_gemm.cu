@@ -120,96 +120,235 @@ __device__ __forceinline__ void store_value(const Params& p, long long at, float
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
 // ---------------------------------------------------------------------------------------------------
-// few rows: integer dot products on the CUDA cores
+// few rows: weights through shared memory to mma.sync
 // ---------------------------------------------------------------------------------------------------
-// Where groups have few rows the weights' bytes decide. A block takes 32 channels (a lane each) of a group and up to 8 of its rows;
-// its warps take the 64-column stages in turn, 16 bytes of weight a lane and load, the rows' codes the same for all lanes, and meet in
-// shared memory: exact integer sums, whatever the order. Groups with more rows are passed over several times, the weights then coming
-// from L2.
-constexpr int FEW_THREADS = 256, FEW_WARPS = FEW_THREADS / 32, FEW_ROWS = 8, FEW_N = 32;
+// Where groups have few rows the weights' bytes decide, and the way through tensor memory is the limit: each tcgen05.mma of 16 columns
+// reads its 4 KB of converted weights at the rate that 256 rows need, 128 cycles, however few rows there are (16 bytes of weights a cycle
+// and SM, 5.1 TB/s in all: 128 groups of 4 rows by 1536 x 2048 in 83 us). Here a lane takes 16 bytes of a channel from shared memory, makes
+// them fp16 as above and has them as a fragment of mma.sync.m16n8k16 (16 channels x 8 rows; the order of the columns within a piece is the
+// same for both operands). (Loaded straight into registers, two pieces ahead, the weights came at 3.3 TB/s: too few under way.)
+//
+// A persistent CTA per SM: one warp brings stages of 128 columns, 16 KB of weights of 128 channels and up to 16 rows' codes, eight of them under
+// way; four groups of four warps, 32 channels to a warp, take them in turn (where every warp took a part of every stage, the waits and arrivals on
+// the stages' barriers cost more than the work). Their sums meet in shared memory in a fixed order. Groups with
+// more rows are passed over several times, the weights then coming from L2.
+constexpr int FEW_ROWS = 16, FEW_STAGES = 8, FEW_GROUPS = 4, FEW_WARPS = 4 * FEW_GROUPS, FEW_THREADS = 32 * (1 + FEW_WARPS);
+constexpr int FEW_PITCH = 33;                    // words of a row's 32 channels in shared memory
+constexpr int FEW_X_BYTES = FEW_ROWS * STAGE_K * 2, FEW_STAGE = 2 * (PIECE + FEW_X_BYTES);
+constexpr int FEW_SUM = 4 * FEW_ROWS * FEW_PITCH, FEW_SUM_BYTES = (FEW_GROUPS - 1) * FEW_SUM * 4;
+constexpr int FEW_SMEM = 1024 + FEW_STAGES * FEW_STAGE + FEW_SUM_BYTES + 256 + GROUPS_INTS * 4 + 16;
+static_assert(FEW_SMEM <= 227 * 1024, "shared memory per CTA");
+// A stage of the ring is one group's in every round: a warp that waits for a round of it has seen the round before, and the barrier's
+// parity, all that a wait asks for, cannot be that of two rounds ago.
+static_assert(FEW_STAGES % FEW_GROUPS == 0, "stages of a group");
 
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Four packed bytes -> two pairs of fp16 numbers: a byte under 0x64 is 1024 + byte, byte = code + 128.
+__device__ __forceinline__ void halves4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const __half2 off = __float2half2_rn(-1152.f);
+    const uint32_t l = __byte_perm(w, 0x64646464u, 0x4140), h = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 a = __hadd2(*reinterpret_cast<const __half2*>(&l), off), b = __hadd2(*reinterpret_cast<const __half2*>(&h), off);
+    lo = *reinterpret_cast<const uint32_t*>(&a);
+    hi = *reinterpret_cast<const uint32_t*>(&b);
+}
+// A barrier of the groups' warps, and whether any of their threads says so.
+__device__ __forceinline__ bool few_any(bool v) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"((uint32_t)v), "n"(32 * FEW_WARPS) : "memory");
+    return r != 0;
+}
+
+struct FewRing {
+    uint32_t sW, sX, bar0;
+    volatile int* abort_flag;
+    int stage;
+    uint32_t phase;
+    __device__ __forceinline__ uint32_t full(int s) const { return bar0 + 8u * s; }
+    __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (FEW_STAGES + s); }
+};
+
+// One tile by one warp: the sums of its 32 channels x 8 NT rows over its group's stages meet those of the other groups' warps in `sum` [8 NT]
+// [FEW_PITCH], to which the first group adds in the groups' order. False: a wait ran out in some warp.
 template <int NT>
-__device__ __forceinline__ void few_dots(const uint8_t* w, const uint8_t* const (&a)[NT], int kst, int (&acc)[NT]) {
-    const int warp = threadIdx.x >> 5;
-    uint4 v[4];
-    auto fetch = [&](int kb) {
+__device__ __forceinline__ bool few_tile(const Params& p, FewRing& ring, int quarter, int group, float* sum) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, ns = (p.KST + 1) / 2;
+    float acc[2][NT][4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = __ldcs(reinterpret_cast<const uint4*>(w + (size_t)kb * PIECE + c * (BLOCK_N * 16)));
-    };
-    if (warp < kst) fetch(warp);
-#pragma unroll 1
-    for (int kb = warp; kb < kst; kb += FEW_WARPS) {
-        uint4 x[4];
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[c] = make_uint4(v[c].x ^ 0x80808080u, v[c].y ^ 0x80808080u, v[c].z ^ 0x80808080u, v[c].w ^ 0x80808080u);
-        if (kb + FEW_WARPS < kst) fetch(kb + FEW_WARPS);
+        for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+    // chunk t of channel r is at row r ^ 2 t of the chunk (of eight lanes, two channels and four chunks, no two on a bank); r = 32 quarter + g + 8 i
+    const uint32_t wat = (uint32_t)(t * BLOCK_N + ((quarter * 32 + g) ^ (2 * t))) * 16, xat = (uint32_t)(g * 128);
+    bool ok = true;
+    for (int kb = 0; kb < ns; ++kb) {
+        const int st = ring.stage;
+        const uint32_t ph = ring.phase;
+        if (++ring.stage == FEW_STAGES) { ring.stage = 0; ring.phase ^= 1u; }
+        if (st % FEW_GROUPS != group || !ok) continue;
+        ok = wait_warp(ring.full(st), ph, p.wait_limit, ring.abort_flag, p.err, 0x382u);
+        if (!ok) continue;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int h = 0; h < 2; ++h) {
+            if (2 * kb + h >= p.KST) break;
+            uint32_t w[4][4], x[NT][8];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const uint4 q = *reinterpret_cast<const uint4*>(a[t] + kb * STAGE_K + c * 16);
-                acc[t] = __dp4a((int)x[c].x, (int)q.x, acc[t]);
-                acc[t] = __dp4a((int)x[c].y, (int)q.y, acc[t]);
-                acc[t] = __dp4a((int)x[c].z, (int)q.z, acc[t]);
-                acc[t] = __dp4a((int)x[c].w, (int)q.w, acc[t]);
+            for (int i = 0; i < 4; ++i) ld_shared_v4(ring.sW + (st * 2 + h) * PIECE + wat + i * 128, w[i]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint32_t at = ring.sX + (st * 2 + h) * FEW_X_BYTES + xat + n * 1024;
+                ld_shared_v4(at + ((uint32_t)((2 * t) ^ g) << 4), x[n]);
+                ld_shared_v4(at + ((uint32_t)((2 * t + 1) ^ g) << 4), x[n] + 4);
             }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    uint32_t f[4];
+                    halves4(w[2 * m][s], f[0], f[2]);
+                    halves4(w[2 * m + 1][s], f[1], f[3]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_f16(acc[m][n], f, x[n][2 * s], x[n][2 * s + 1]);
+                }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ring.empty(st));
     }
+    auto at = [&](int m, int n, int i) { return (8 * n + 2 * t + (i & 1)) * FEW_PITCH + 16 * m + g + 8 * (i >> 1); };
+    if (group > 0) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[(group - 1) * FEW_SUM + at(m, n, i)] = acc[m][n][i];
+    }
+    if (few_any(!ok)) return false;
+    if (group == 0) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float v = acc[m][n][i];
+#pragma unroll
+                    for (int j = 0; j < FEW_GROUPS - 1; ++j) v += sum[j * FEW_SUM + at(m, n, i)];
+                    sum[at(m, n, i)] = v;
+                }
+    }
+    few_any(false);
+    return true;
 }
 
 template <int EPI>
-__global__ void __launch_bounds__(FEW_THREADS, 2) few_rows_kernel(const Params p) {
-    __shared__ int s_groups[GROUPS_INTS];
-    __shared__ int s_sum[FEW_WARPS][FEW_ROWS][32];
-    const Groups gs = groups_at(s_groups);
-    find_groups<FEW_THREADS>(p, FEW_ROWS, gs);
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nch = (p.N + FEW_N - 1) / FEW_N, width = p.KST * STAGE_K;
-    const long long items = (long long)gs.first[p.G] * nch;
-    int g = 0;
-    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-        g = group_of(gs.first, p.G, nch, it, g);
-        const int passes = gs.first[g + 1] - gs.first[g];
-        const int local = (int)(it - (long long)gs.first[g] * nch), ch = local / passes, row0 = gs.beg[g] + (local - ch * passes) * FEW_ROWS;
-        const int nt = min(FEW_ROWS, gs.end[g] - row0), n = ch * FEW_N + lane;
-        const uint8_t* w = p.w + ((size_t)g * p.NB + (ch >> 2)) * p.KST * PIECE + ((ch & 3) * 32 + lane) * 16;
-        const uint8_t* a0 = static_cast<const uint8_t*>(p.a) + (size_t)row0 * width;
-        auto run = [&](auto rows) {
-            constexpr int NT = decltype(rows)::value;
-            const uint8_t* a[NT];
-            int acc[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                a[t] = a0 + (size_t)min(t, nt - 1) * width;
-                acc[t] = 0;
+__global__ void __launch_bounds__(FEW_THREADS, 1) few_rows_kernel(const __grid_constant__ CUtensorMap tm16, const Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    FewRing ring;
+    ring.sX = smem_u32(smem);
+    ring.sW = ring.sX + FEW_STAGES * 2 * FEW_X_BYTES;
+    float* s_sum = reinterpret_cast<float*>(smem + FEW_STAGES * FEW_STAGE);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + FEW_STAGES * FEW_STAGE + FEW_SUM_BYTES);
+    ring.bar0 = smem_u32(bars);
+    ring.abort_flag = reinterpret_cast<volatile int*>(bars + 2 * FEW_STAGES);
+    ring.stage = 0;
+    ring.phase = 0;
+    const Groups gs = groups_at(reinterpret_cast<int*>(bars + 32));
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < FEW_STAGES; ++s) { mbar_init(ring.full(s), 1); mbar_init(ring.empty(s), 4); }
+        *ring.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_tmap(&tm16);
+    }
+    // (a programmatic dependent of the quantisation: the groups, the set-up and the first stages of weights do not wait for it)
+    find_groups<FEW_THREADS>(p, FEW_ROWS, gs);               // (its barriers also stand between the set-up and the roles)
+    const int total = uniform(gs.first[p.G] * p.NB), ns = (p.KST + 1) / 2;
+    // Item w: group by group, 128-channel block next, row tile fastest
+    auto map = [&](int w, int& g, int& nb, int& row0, int& row1) {
+        g = group_of(gs.first, p.G, p.NB, w, g);
+        const int nt = gs.first[g + 1] - gs.first[g], local = w - gs.first[g] * p.NB;
+        nb = local / nt;
+        row0 = gs.beg[g] + (local - nb * nt) * FEW_ROWS;
+        row1 = min(row0 + FEW_ROWS, gs.end[g]);
+    };
+    if (warp == FEW_WARPS) {
+        int stage = 0, g = 0;
+        uint32_t phase = 0, issued = 0, last_par = 0;
+        bool ok = true;
+        for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
+            int nb, row0, row1;
+            map(w, g, nb, row0, row1);
+            nb = uniform(nb); row0 = uniform(row0);
+            const uint8_t* w0 = p.w + ((size_t)uniform(g) * p.NB + nb) * p.KST * PIECE;
+            auto weights = [&](int st, int kb) {
+                const int n = min(2, p.KST - 2 * kb);
+                expect_elected(ring.full(st), (uint32_t)(n * (PIECE + FEW_X_BYTES)));
+                bulk_elected(ring.sW + st * (2 * PIECE), w0 + (size_t)kb * (2 * PIECE), n * PIECE, ring.full(st));
+            };
+            int early = 0;
+            if (w == (int)blockIdx.x) {
+                for (; early < min(FEW_STAGES, ns); ++early) weights(early, early);
+                pdl_wait();
+                pdl_trigger();
             }
-            few_dots<NT>(w, a, p.KST, acc);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) s_sum[warp][t][lane] = acc[t];
-        };
-        if (nt <= 1) run(std::integral_constant<int, 1>());
-        else if (nt <= 2) run(std::integral_constant<int, 2>());
-        else if (nt <= 4) run(std::integral_constant<int, 4>());
-        else run(std::integral_constant<int, 8>());
-        __syncthreads();
-        if (warp < nt) {
-            int sum = 0;
-#pragma unroll
-            for (int i = 0; i < FEW_WARPS; ++i) sum += s_sum[i][warp][lane];
-            const int row = row0 + warp;
-            const float v = (float)sum * p.a_scales[row];
-            if constexpr (EPI == EPI_OUT) {
-                if (n < p.N) store_value(p, row * p.ld + n, v * p.w_scales[(size_t)g * p.N + n]);
-            } else {
-                const int F = p.N / 2, f = n >> 1;
-                const float s = n < p.N ? ((n & 1) ? p.w_scales_up : p.w_scales)[(size_t)g * F + f] : 0.f;
-                const float x = v * s, u = __shfl_down_sync(0xffffffffu, x, 1);
-                if (!(n & 1) && n < p.N) static_cast<float*>(p.out)[(size_t)row * F + f] = swiglu(x, u);
+            for (int kb = 0; kb < ns; ++kb) {
+                if (kb >= early) {
+                    ok = test_warp(ring.empty(stage), phase ^ 1u) ||
+                         wait_warp(ring.empty(stage), phase ^ 1u, p.wait_limit, ring.abort_flag, p.err, 0x380u);
+                    if (!ok) break;
+                    weights(stage, kb);
+                }
+                for (int q = 0; q < min(2, p.KST - 2 * kb); ++q)
+                    tma_elected(ring.sX + (stage * 2 + q) * FEW_X_BYTES, &tm16, (2 * kb + q) * STAGE_K, row0, ring.full(stage));
+                issued |= 1u << stage;
+                last_par = (last_par & ~(1u << stage)) | (phase << stage);
+                if (++stage == FEW_STAGES) { stage = 0; phase ^= 1u; }
             }
         }
-        __syncthreads();
+        if (total <= (int)blockIdx.x) {          // (no item: the wait that every thread makes)
+            pdl_wait();
+            pdl_trigger();
+        }
+        if (lane == 0)
+            for (int s = 0; s < FEW_STAGES; ++s)    // every issued copy has landed before the CTA exits
+                if (issued & (1u << s)) drain_phase(ring.full(s), (last_par >> s) & 1u, p.err, 0x381u);
+        __syncwarp();
+        return;
+    }
+    pdl_wait();
+    pdl_trigger();
+    const int quarter = warp & 3, group = warp >> 2;
+    int g = 0;
+    for (int w = blockIdx.x; w < total; w += gridDim.x) {
+        int nb, row0, row1;
+        map(w, g, nb, row0, row1);
+        const int nt = row1 - row0, n = nb * BLOCK_N + quarter * 32 + lane;
+        float* sum = s_sum + quarter * (FEW_ROWS * FEW_PITCH);
+        const bool ok = nt <= 8 ? few_tile<1>(p, ring, quarter, group, sum) : few_tile<2>(p, ring, quarter, group, sum);
+        if (!ok) break;
+        if (n - lane < p.N) {                    // 32 channels of the group's share of the rows
+            const int F = p.N / 2, f = n >> 1;
+            float scale = 0.f;
+            if (n < p.N) scale = EPI == EPI_OUT ? p.w_scales[(size_t)g * p.N + n] : ((n & 1) ? p.w_scales_up : p.w_scales)[(size_t)g * F + f];
+#pragma unroll 4
+            for (int t = group; t < nt; t += FEW_GROUPS) {
+                const int row = row0 + t;
+                const float v = sum[t * FEW_PITCH + lane] * p.a_scales[row] * scale;
+                if constexpr (EPI == EPI_OUT) {
+                    if (n < p.N) store_value(p, row * p.ld + n, v);
+                } else {
+                    const float u = __shfl_down_sync(0xffffffffu, v, 1);
+                    if (!(n & 1) && n < p.N) static_cast<float*>(p.out)[(size_t)row * F + f] = swiglu(v, u);
+                }
+            }
+        }
+        if (w + (int)gridDim.x < total) few_any(false);      // the sums are read before the next tile's are written
     }
 }
 
@@ -251,6 +390,7 @@ struct Tile {
     static_assert(A_COL + A_BUFS * A_COLS <= TMEM_COLS, "tensor memory columns");
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
     static_assert(8 * (2 * STAGES + A_BUFS + 3) + 8 <= 256, "barriers");
+    static_assert(STAGES % 2 == 0 && A_BUFS % 2 == 0, "a stage and a buffer are the same converters' in every round");
 };
 
 // D fp32 (bits 4-5 = 1), A and B fp16 (0), K-major, N >> 3 at bits 17-22, M = 256 at bits 24-28.
@@ -478,17 +618,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tm128, const __grid_constant__ C
                 for (int h = 0; h < PER; ++h) {
                     if (h >= n) break;
                     uint32_t q[16], v[32];
-                    const uint32_t src = sW + (st * PER + h) * PIECE + (quarter + lane) * 16;
+                    const uint32_t src = sW + (st * PER + h) * PIECE + quarter * 16;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) ld_shared_v4(src + c * (BLOCK_N * 16), q + 4 * c);
+                    for (int c = 0; c < 4; ++c) ld_shared_v4(src + c * (BLOCK_N * 16) + (lane ^ (2 * c)) * 16, q + 4 * c);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const __half2 off = __float2half2_rn(-1152.f);
-                        const uint32_t lo = __byte_perm(q[c], 0x64646464u, 0x4140), hi = __byte_perm(q[c], 0x64646464u, 0x4342);
-                        const __half2 a = __hadd2(*reinterpret_cast<const __half2*>(&lo), off), e = __hadd2(*reinterpret_cast<const __half2*>(&hi), off);
-                        v[2 * c] = *reinterpret_cast<const uint32_t*>(&a);
-                        v[2 * c + 1] = *reinterpret_cast<const uint32_t*>(&e);
-                    }
+                    for (int c = 0; c < 16; ++c) halves4(q[c], v[2 * c], v[2 * c + 1]);
                     if (h == 0 && i >= A_BUFS) {    // the buffer's last MMAs have completed
                         const uint32_t par = ((i - A_BUFS) / STAGES) & 1;
                         ok = test_warp(empty(old), par) || wait_warp_pair(empty(old), par, p.wait_limit, abort_flag, peer_abort, p.err, 0x361u);
@@ -603,21 +737,30 @@ static int launch_pairs(const Params& p, cudaStream_t s) {
     return launch_pair<EPI, 256>(p, s);
 }
 
-// Dot products on the CUDA cores where the groups have few rows.
-static bool few_rows(int rows, int G) { return rows <= FEW_ROWS * std::min(G, 2); }
-static int operand_form(int rows, int G) { return few_rows(rows, G) ? FORM_BYTES : FORM_F16; }
+template <int EPI>
+static int launch_few(const Params& p, cudaStream_t s) {
+    static unsigned long long attr_ctx[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return set_error(MOE_ERR_CUDA, "int8 product: no usable current device");
+    const unsigned long long ctx = context_id();
+    if (ctx == 0 || attr_ctx[dev] != ctx) {
+        const cudaError_t e = cudaFuncSetAttribute(few_rows_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM);
+        if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "int8 product smem attribute: %s", cudaGetErrorString(e));
+        attr_ctx[dev] = context_id();
+    }
+    CUtensorMap m16;
+    if (int rc = rows_map(&m16, p.a, p.rows, p.KST * STAGE_K, 16)) return rc;
+    const long long most = ((long long)cdiv(p.rows, FEW_ROWS) + std::min(p.G, p.rows)) * p.NB;
+    return check_launch(launch_pdl(few_rows_kernel<EPI>, dim3((unsigned)std::min<long long>(most, num_sms())), dim3(FEW_THREADS), FEW_SMEM, s, m16, p),
+                        EPI == EPI_SWIGLU ? "int8 few_rows_kernel<swiglu>" : "int8 few_rows_kernel");
+}
 
-static int launch_product(const Params& p, int epi, cudaStream_t s) {
-    MOE_REQUIRE(((long long)p.rows / 64 + p.G) * cdiv(p.NB, 2) < (1LL << 31), MOE_ERR_INVALID_ARG,
+template <int EPI>
+static int launch_product(const Params& p, cudaStream_t s) {
+    MOE_REQUIRE(((long long)p.rows / 32 + p.G) * p.NB < (1LL << 31), MOE_ERR_INVALID_ARG,
                 "8-bit product: %d rows by %d channels are over 2^31 tiles", p.rows, p.N);
-    if (!few_rows(p.rows, p.G)) return epi == EPI_OUT ? launch_pairs<EPI_OUT>(p, s) : launch_pairs<EPI_SWIGLU>(p, s);
-    auto go = [&](auto kernel) {
-        int per_sm = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, FEW_THREADS, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
-        const long long most = ((long long)cdiv(p.rows, FEW_ROWS) + std::min(p.G, p.rows)) * cdiv(p.N, FEW_N);
-        return launch_pdl(kernel, dim3((unsigned)std::min<long long>(most, (long long)per_sm * num_sms())), dim3(FEW_THREADS), 0, s, p);
-    };
-    return check_launch(epi == EPI_OUT ? go(few_rows_kernel<EPI_OUT>) : go(few_rows_kernel<EPI_SWIGLU>), "int8 few_rows_kernel");
+    // few rows where a group has up to 16 on average
+    return p.rows / std::min(p.G, p.rows) <= FEW_ROWS ? launch_few<EPI>(p, s) : launch_pairs<EPI>(p, s);
 }
 
 // A row operand in the workspace: codes (room for fp16), then the rows' scales.
@@ -677,8 +820,8 @@ extern "C" int moe_int8_linear(const void* x, long long ldx, int x_rows, const i
     p.a = ws; p.a_scales = int8::scales_at(ws, rows, K);
     p.w_scales = w_scales; p.N = N; p.ld = ldo; p.out_dtype = out_dtype; p.out = out;
     p.err = err; p.wait_limit = wait_limit();
-    if (int rc = int8::launch_quantize(x, ldx, x_rows, src, rows, K, dtype, int8::operand_form(rows, G), ws, int8::scales_at(ws, rows, K), err, s)) return rc;
-    return int8::launch_product(p, int8::EPI_OUT, s);
+    if (int rc = int8::launch_quantize(x, ldx, x_rows, src, rows, K, dtype, int8::FORM_F16, ws, int8::scales_at(ws, rows, K), err, s)) return rc;
+    return int8::launch_product<int8::EPI_OUT>(p, s);
 }
 
 // The FFN's workspace: x's operand, act [rows][F] in fp32, act's operand.
@@ -727,12 +870,12 @@ extern "C" int moe_int8_expert_ffn(const void* x, long long ldx, int x_rows, con
     p.a = w.x; p.a_scales = int8::scales_at(w.x, rows, h);
     p.w_scales = gate_scales; p.w_scales_up = up_scales; p.N = 2 * F; p.out_dtype = MOE_F32; p.out = w.act;
     p.err = err; p.wait_limit = wait_limit();
-    if (int rc = int8::launch_quantize(x, ldx, x_rows, src, rows, h, dtype, int8::operand_form(rows, E), w.x, int8::scales_at(w.x, rows, h), err, s)) return rc;
-    if (int rc = int8::launch_product(p, int8::EPI_SWIGLU, s)) return rc;
-    if (int rc = int8::launch_quantize(w.act, F, rows, nullptr, rows, F, MOE_F32, int8::operand_form(rows, E), w.a, int8::scales_at(w.a, rows, F), err, s))
+    if (int rc = int8::launch_quantize(x, ldx, x_rows, src, rows, h, dtype, int8::FORM_F16, w.x, int8::scales_at(w.x, rows, h), err, s)) return rc;
+    if (int rc = int8::launch_product<int8::EPI_SWIGLU>(p, s)) return rc;
+    if (int rc = int8::launch_quantize(w.act, F, rows, nullptr, rows, F, MOE_F32, int8::FORM_F16, w.a, int8::scales_at(w.a, rows, F), err, s))
         return rc;
     p.w += L.down_off; p.NB = L.down.NB; p.KST = L.down.KST;
     p.a = w.a; p.a_scales = int8::scales_at(w.a, rows, F);
     p.w_scales = down_scales; p.w_scales_up = nullptr; p.N = h; p.ld = ldo; p.out_dtype = out_dtype; p.out = out;
-    return int8::launch_product(p, int8::EPI_OUT, s);
+    return int8::launch_product<int8::EPI_OUT>(p, s);
 }
