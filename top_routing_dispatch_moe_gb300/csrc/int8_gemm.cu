@@ -135,7 +135,7 @@ __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + ex
 constexpr int FEW_ROWS = 16, FEW_STAGES = 8, FEW_GROUPS = 4, FEW_WARPS = 4 * FEW_GROUPS, FEW_THREADS = 32 * (1 + FEW_WARPS);
 constexpr int FEW_PITCH = 33;                    // words of a row's 32 channels in shared memory
 constexpr int FEW_X_BYTES = FEW_ROWS * STAGE_K * 2, FEW_STAGE = 2 * (PIECE + FEW_X_BYTES);
-constexpr int FEW_SUM = 4 * FEW_ROWS * FEW_PITCH, FEW_SUM_BYTES = (FEW_GROUPS - 1) * FEW_SUM * 4;
+constexpr int FEW_SUM = 4 * FEW_ROWS * FEW_PITCH, FEW_SUM_BYTES = FEW_GROUPS * FEW_SUM * 4;
 constexpr int FEW_SMEM = 1024 + FEW_STAGES * FEW_STAGE + FEW_SUM_BYTES + 256 + GROUPS_INTS * 4 + 16;
 static_assert(FEW_SMEM <= 227 * 1024, "shared memory per CTA");
 // A stage of the ring is one group's in every round: a warp that waits for a round of it has seen the round before, and the barrier's
@@ -172,8 +172,8 @@ struct FewRing {
     __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (FEW_STAGES + s); }
 };
 
-// One tile by one warp: the sums of its 32 channels x 8 NT rows over its group's stages meet those of the other groups' warps in `sum` [8 NT]
-// [FEW_PITCH], to which the first group adds in the groups' order. False: a wait ran out in some warp.
+// One tile by one warp: the sums of its 32 channels x 8 NT rows over its group's stages, into `sum` [group][8 NT][FEW_PITCH] beside those of
+// the other groups, all of which are there on return. False: a wait ran out in some warp.
 template <int NT>
 __device__ __forceinline__ bool few_tile(const Params& p, FewRing& ring, int quarter, int group, float* sum) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, ns = (p.KST + 1) / 2;
@@ -219,30 +219,13 @@ __device__ __forceinline__ bool few_tile(const Params& p, FewRing& ring, int qua
         if (lane == 0) mbar_arrive(ring.empty(st));
     }
     auto at = [&](int m, int n, int i) { return (8 * n + 2 * t + (i & 1)) * FEW_PITCH + 16 * m + g + 8 * (i >> 1); };
-    if (group > 0) {
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum[(group - 1) * FEW_SUM + at(m, n, i)] = acc[m][n][i];
-    }
-    if (few_any(!ok)) return false;
-    if (group == 0) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float v = acc[m][n][i];
-#pragma unroll
-                    for (int j = 0; j < FEW_GROUPS - 1; ++j) v += sum[j * FEW_SUM + at(m, n, i)];
-                    sum[at(m, n, i)] = v;
-                }
-    }
-    few_any(false);
-    return true;
+            for (int i = 0; i < 4; ++i) sum[group * FEW_SUM + at(m, n, i)] = acc[m][n][i];
+    return !few_any(!ok);
 }
 
 template <int EPI>
@@ -330,16 +313,24 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) few_rows_kernel(const __grid_c
         map(w, g, nb, row0, row1);
         const int nt = row1 - row0, n = nb * BLOCK_N + quarter * 32 + lane;
         float* sum = s_sum + quarter * (FEW_ROWS * FEW_PITCH);
+        // (what the sums are multiplied with, under way while they are formed: loaded after them, it cost a tile of 768 columns a third of its
+        // time)
+        const int F = p.N / 2, f = n >> 1;
+        float scale = 0.f, xs[FEW_ROWS / FEW_GROUPS];
+        if (n < p.N) scale = EPI == EPI_OUT ? p.w_scales[(size_t)g * p.N + n] : ((n & 1) ? p.w_scales_up : p.w_scales)[(size_t)g * F + f];
+#pragma unroll
+        for (int i = 0; i < FEW_ROWS / FEW_GROUPS; ++i) xs[i] = p.a_scales[row0 + min(group + i * FEW_GROUPS, nt - 1)];
         const bool ok = nt <= 8 ? few_tile<1>(p, ring, quarter, group, sum) : few_tile<2>(p, ring, quarter, group, sum);
         if (!ok) break;
         if (n - lane < p.N) {                    // 32 channels of the group's share of the rows
-            const int F = p.N / 2, f = n >> 1;
-            float scale = 0.f;
-            if (n < p.N) scale = EPI == EPI_OUT ? p.w_scales[(size_t)g * p.N + n] : ((n & 1) ? p.w_scales_up : p.w_scales)[(size_t)g * F + f];
-#pragma unroll 4
-            for (int t = group; t < nt; t += FEW_GROUPS) {
-                const int row = row0 + t;
-                const float v = sum[t * FEW_PITCH + lane] * p.a_scales[row] * scale;
+#pragma unroll
+            for (int i = 0; i < FEW_ROWS / FEW_GROUPS; ++i) {
+                const int t = group + i * FEW_GROUPS, row = row0 + t;
+                if (t >= nt) break;
+                float v = 0.f;
+#pragma unroll
+                for (int j = 0; j < FEW_GROUPS; ++j) v += sum[j * FEW_SUM + t * FEW_PITCH + lane];
+                v = v * xs[i] * scale;
                 if constexpr (EPI == EPI_OUT) {
                     if (n < p.N) store_value(p, row * p.ld + n, v);
                 } else {
@@ -729,11 +720,14 @@ static int launch_pair(const Params& p, cudaStream_t s) {
                         EPI == EPI_SWIGLU ? "int8 pair_kernel<swiglu>" : "int8 pair_kernel");
 }
 
+// Rows of a tile. A stage takes its MMAs as long for 64 rows as for 256, so more rows mean fewer tiles; 64 and 128 where groups are no
+// larger on average, and where the tiles are no more than the pairs that run at once: a call is then one tile long, and the epilogue of fewer
+// rows is shorter (1003 rows by 7 x 1001 x 1044 in fp32, 256 rows 15.5 us).
 template <int EPI>
 static int launch_pairs(const Params& p, cudaStream_t s) {
-    const long long avg = p.rows / p.G;          // a group's rows, if they are alike
-    if (avg <= 48) return launch_pair<EPI, 64>(p, s);
-    if (avg <= 128) return launch_pair<EPI, 128>(p, s);
+    const long long avg = p.rows / p.G, used = std::min(p.G, p.rows), pairs = num_sms() / 2, blocks = (p.NB + 1) / 2;
+    if (avg <= 48 || (p.rows / 64 + used) * blocks <= pairs) return launch_pair<EPI, 64>(p, s);
+    if (avg <= 128 || (p.rows / 128 + used) * blocks <= pairs) return launch_pair<EPI, 128>(p, s);
     return launch_pair<EPI, 256>(p, s);
 }
 
