@@ -44,8 +44,8 @@ struct Args {
 };
 
 __device__ __forceinline__ unsigned key_of(float v) {
-    const unsigned u = __float_as_uint(v == 0.f ? 0.f : v);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const unsigned u = __float_as_uint(v + 0.f);               // (-0 as 0)
+    return u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(unsigned key) {
     return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
@@ -103,6 +103,23 @@ __device__ __noinline__ unsigned groups_exact(const Args& a, const float* L, lon
             if (i + j < npl) sel[i + j] = e0 + i + j < a.E ? order_of(v[j]) : kLeast;
     }
     long long gscore = kLeast;               // lane g: group g's
+    if (a.lpg && (a.lpg & (a.lpg - 1)) == 0) {           // a group is a run of lanes: all at once
+        long long t1 = kLeast, t2 = kLeast;
+#pragma unroll 1
+        for (int i = 0; i < npl; ++i) {
+            t2 = max(t2, min(t1, sel[i]));
+            t1 = max(t1, sel[i]);
+        }
+#pragma unroll 1
+        for (int o = 1; o < a.lpg; o <<= 1) {
+            const long long b1 = __shfl_xor_sync(0xffffffffu, t1, o), b2 = __shfl_xor_sync(0xffffffffu, t2, o);
+            t2 = max(min(t1, b1), max(t2, b2));
+            t1 = max(t1, b1);
+        }
+        const long long v = a.best == 2 ? order_of(of_order(t1) + of_order(t2)) : t1;
+        gscore = __shfl_sync(0xffffffffu, v, min(lane * a.lpg, 31));
+        if (lane >= a.groups) gscore = kLeast;
+    } else
 #pragma unroll 1
     for (int g = 0; g < a.groups; ++g) {
         long long t1 = kLeast, t2 = kLeast;
@@ -187,15 +204,16 @@ __device__ __noinline__ int order_exact(const Args& a, const float* L, float l, 
     return out;
 }
 
-// 2^x and 1 / x of the special-function units: within 2 and 1 units in the last place.
+// 2^x and 1 / x of the special-function units: within 2 and 1 units in the last place (0 below the normal range: a score of 2^-126 is
+// none).
 __device__ __forceinline__ float ex2(float x) {
     float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 __device__ __forceinline__ float rcp(float x) {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 constexpr float kLog2e = 1.44269504f;
@@ -226,7 +244,7 @@ __device__ __forceinline__ void sort_keys(unsigned (&key)[N]) {
 // division, took 45 us of scores and rounds; the whole choice in 64 bits 50 us for the one token of some thousands that needs it.)
 // FULL: E = 32 NPL, and a group a run of lanes whose number is a power of two.
 template <int NPL, bool FULL>
-__global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL == 16 ? 2 : 1)
+__global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 3 : NPL == 16 ? 2 : 1)
 group_gate_kernel(const __grid_constant__ Args a) {
     constexpr unsigned SLOT = NPL - 1;
     constexpr int SB = NPL == 1 ? 0 : NPL == 2 ? 1 : NPL == 4 ? 2 : NPL == 8 ? 3 : NPL == 16 ? 4 : 5;
@@ -287,7 +305,7 @@ group_gate_kernel(const __grid_constant__ Args a) {
             total += s[i];
         }
         total = warp_sum(total);
-        const float inv = total == 0.f ? 0.f : 1.f / total;
+        const float inv = total == 0.f ? 0.f : rcp(total);
 #pragma unroll
         for (int i = 0; i < NPL; ++i) Pacc[i] += s[i] * inv;
         if (!a.sigmoid) {
@@ -304,9 +322,9 @@ group_gate_kernel(const __grid_constant__ Args a) {
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             const float v = s[i] + bias[i];
-            const bool out = !(L[i] > -INFINITY) || !(v == v);
-            const float sel = out ? kMasked : v;
-            key[i] = live(i) ? (key_of(a.bias || out ? sel : L[i]) & ~SLOT) | (SLOT - i) : 0u;
+            const bool in = L[i] > -INFINITY && v == v;
+            const float sel = in ? v : kMasked;
+            key[i] = live(i) ? (key_of(a.bias || !in ? sel : L[i]) & ~SLOT) | (SLOT - i) : 0u;
             if (live(i)) {
                 t2 = fmaxf(t2, fminf(t1, sel));
                 t1 = fmaxf(t1, sel);
@@ -387,14 +405,14 @@ group_gate_kernel(const __grid_constant__ Args a) {
         if constexpr (NPL > 1) sort_keys(key);
         // The next best: lane j takes it as its choice. Equal heads go to the lowest lane.
         unsigned my_key = 0u;
-        int my_id = 0;
+        int my_owner = 0;
         auto take = [&](int j) {
             const unsigned head = key[0] >> SB, top = __reduce_max_sync(0xffffffffu, head);
             const int owner = __ffs(__ballot_sync(0xffffffffu, head == top)) - 1;
             const unsigned got = __shfl_sync(0xffffffffu, key[0], owner);
             if (lane == j) {
                 my_key = got;
-                my_id = owner * npl + (int)(SLOT - (got & SLOT));
+                my_owner = owner;
             }
             const bool pop = lane == owner;
 #pragma unroll
@@ -406,6 +424,8 @@ group_gate_kernel(const __grid_constant__ Args a) {
         int n = min(a.k + 1, left);                               // the k, and the first that is left out
 #pragma unroll 2
         for (int j = 0; j < n; ++j) take(j);
+        auto id_of = [&] { return my_owner * npl + (int)(SLOT - (my_key & SLOT)); };
+        int my_id = id_of();
         // whether two neighbours' order may be another than their keys'
         auto near = [&](unsigned hi, unsigned lo) {
             if (!a.bias) return (hi >> SB) == (lo >> SB);
@@ -438,6 +458,7 @@ group_gate_kernel(const __grid_constant__ Args a) {
                 float l[NPL];
 #pragma unroll
                 for (int i = 0; i < NPL; ++i) l[i] = L[i];
+                my_id = id_of();
                 if (lane < n) my_l = logit_of(my_id);
                 my_id = more && n < left ? choose_exact(a, l) : order_exact(a, l, my_l, my_id, n);
                 if (lane < a.k) my_l = logit_of(my_id);
@@ -447,7 +468,7 @@ group_gate_kernel(const __grid_constant__ Args a) {
         if (lane < a.k && !(my_l == -INFINITY)) my_s = a.sigmoid ? rcp(1.f + ex2(-kLog2e * my_l)) : ex2((my_l - m) * kLog2e) * inv;
         if (a.renorm) {
             const float sum = warp_sum(my_s);
-            my_s = sum == 0.f ? 0.f : my_s / sum;
+            my_s = sum == 0.f ? 0.f : my_s * rcp(sum);
         }
         if (lane < a.k) {
             a.ids[(size_t)t * a.k + lane] = my_id;

@@ -45,8 +45,8 @@ inline ExpertLayout expert_layout(int E, int h, int F) {
 constexpr float TINY = 1.262177448e-29f;             // 2^-96
 
 // The way of values whose largest magnitude is amax to their codes: x * c / a, c = 127 (both times 2^-32 where 127 x could leave
-// fp32's range), r the rounded reciprocal of a; live: the codes are not all 0.
-struct Steps { float c, a, r; bool live; };
+// fp32's range), r the rounded reciprocal of a, inv the rounded 127 / amax; live: the codes are not all 0.
+struct Steps { float c, a, r, inv; bool live; };
 // The scale of such values.
 __device__ __forceinline__ float scale_of(float amax, Steps& st) {
     const bool finite = amax < INFINITY;             // (NaN: not)
@@ -55,25 +55,28 @@ __device__ __forceinline__ float scale_of(float amax, Steps& st) {
     st.c = 127.f * f;
     st.a = st.live ? amax * f : 1.f;
     st.r = __frcp_rn(st.a);
+    st.inv = st.live ? __fdiv_rn(127.f, amax) : 0.f;
     return st.live ? __fdiv_rn(amax, 127.f) : finite ? 0.f : __uint_as_float(0x7FC00000u);
 }
 
 // 1.5 * 2^23: its sum with |q| < 2^22 is q rounded to a whole number, ties to even, whose two's complement are the sum's low bits.
 constexpr float MAGIC = 12582912.f;
 
-// MAGIC + the code of an fp32 value whose quotient rounds to half way between two codes without being it: the side that the
-// remainder x c - q a says (p + pe is x c, exactly).
-static __device__ __noinline__ float code_at_border(float q, float rest) {
-    const float lo = floorf(q);
-    return MAGIC + (rest > 0.f ? lo + 1.f : lo);
+// MAGIC + the code of an fp32 value whose product with inv lies so near the border between two codes that its roundings may have crossed
+// it: the side that x c - border a says, x c in two parts and each step exact.
+static __device__ __noinline__ float code_at_border(float x, float q, const Steps& st) {
+    const float n = rintf(q), border = q >= n ? n + 0.5f : n - 0.5f, lo = border - 0.5f;
+    const float p = x * st.c, pe = fmaf(-x, st.c, p), rest = fmaf(-border, st.a, p) - pe;
+    const bool up = rest > 0.f || (rest == 0.f && ((int)lo & 1));
+    return MAGIC + (up ? lo + 1.f : lo);
 }
 
-// N values (even) of one row, of type T -> MAGIC + their codes, two values an instruction. The quotient of x c and a is rounded
-// correctly: q = x c r is off by less than two units in its last place, and q + (x c - q a) r is the rounded quotient (Markstein's correction:
-// the remainder is exact in one fused step). Half way between two codes is a number of few bits, so a tie is one here. x of 16
-// bits: x c is exact, and no other quotient comes within 2^-20 of a border. fp32: x c in two parts, and a quotient that rounds to a
-// border without being it has a remainder. (With a test for quotients near a border instead, and the borders decided in 64 bits, two
-// thirds of all blocks of bf16 values had a tie, and 16384 x 28672 of them took 690 us.)
+// N values (even) of one row, of type T -> MAGIC + their codes, two values an instruction.
+// 16 bits: x c is exact, and its quotient by a is rounded correctly: q = x c r is off by less than two units in its last place, and
+// q + (x c - q a) r is the rounded quotient (Markstein's correction: the remainder is exact in one fused step). Half way between two codes
+// is a number of few bits, so a tie is one here, and no other quotient comes within 2^-20 of a border. (With a test for quotients near a
+// border instead, two thirds of all blocks of bf16 values had a tie, and 16384 x 28672 of them took 690 us.)
+// fp32: x inv is off by less than 127 * 2^-23; only a product that close to a border, which among sums and products few are, is looked at again.
 template <typename T, int N>
 __device__ __forceinline__ void codes_of(float* v, const Steps& st) {
     if (!st.live) {                                  // (zeros, or an infinity or a NaN among them)
@@ -92,35 +95,30 @@ __device__ __forceinline__ void codes_of(float* v, const Steps& st) {
             add2(v + i, q, MAGIC);
         }
     } else {
-        bool odd = false;
-        float q[N], rest[N];
+        float t[N], far = 0.f;
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            float p[2], pe[2], e[2], n[2];
-            const float m[2] = {-v[i], -v[i + 1]};
-            mul2(p, v + i, st.c);
-            fma2(pe, m, st.c, p);                    // p - x c
-            mul2(q + i, p, st.r);
-            fma2(e, q + i, -st.a, p);
-            sub2(e, e, pe);
-            fma2(q + i, e, st.r, q + i);
-            fma2(rest + i, q + i, -st.a, p);
-            sub2(rest + i, rest + i, pe);
-            add2(v + i, q + i, MAGIC);
-            add2(n, v + i, -MAGIC);
-            sub2(n, q + i, n);
-            odd |= (fabsf(n[0]) == 0.5f && rest[i] != 0.f) || (fabsf(n[1]) == 0.5f && rest[i + 1] != 0.f);
+            float q[2], d[2];
+            mul2(q, v + i, st.inv);
+            add2(t + i, q, MAGIC);
+            add2(d, t + i, -MAGIC);
+            sub2(d, q, d);
+            far = max3_abs(far, d[0], d[1]);
         }
-        if (odd) {                                   // (rolled, through local memory: it hardly runs)
-            float x[N], y[N], z[N];
+        if (far > 0.49998f) {                        // (rolled, through local memory: it hardly runs)
+            float x[N], y[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) { x[i] = q[i]; y[i] = rest[i]; z[i] = v[i]; }
+            for (int i = 0; i < N; ++i) { x[i] = v[i]; y[i] = t[i]; }
 #pragma unroll 1
-            for (int i = 0; i < N; ++i)
-                if (fabsf(x[i] - (z[i] - MAGIC)) == 0.5f && y[i] != 0.f) z[i] = code_at_border(x[i], y[i]);
+            for (int i = 0; i < N; ++i) {
+                const float q = x[i] * st.inv;
+                if (fabsf(q - (y[i] - MAGIC)) > 0.49998f) y[i] = code_at_border(x[i], q, st);
+            }
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = z[i];
+            for (int i = 0; i < N; ++i) t[i] = y[i];
         }
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = t[i];
     }
 }
 // Four codes as codes_of leaves them -> bytes; two -> fp16 numbers.

@@ -8,7 +8,6 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import math
 import os
 
 import torch
@@ -240,17 +239,12 @@ def _score(score: str | int) -> int:
     return int(score)
 
 
-def _route_outputs(T: int, E: int, k: int, t, stream, given: dict) -> dict:
-    """The routing outputs: those given, checked, and new ones for the rest."""
-    i32, f32 = torch.int32, torch.float32
-    want = dict(topk_ids=((T, k), i32), gates=((T, k), f32), counts=((E,), i32), f=((E,), f32), P=((E,), f32), aux=((1,), f32))
-    out = {}
-    for name, (shape, dtype) in want.items():
-        o = given.get(name)
-        out[name] = _fp4_empty(shape, dtype, t, stream) if o is None else o
-        if o is not None:
-            _fp4_data(o, math.prod(shape), dtype, name)
-    return out
+def _route_out(o, shape, n: int, dtype, t, stream, what: str):
+    """A routing output: `o`, checked, or a new one."""
+    if o is None:
+        return torch.empty(shape, dtype=dtype, device=t.device) if stream is None else _fp4_empty(shape, dtype, t, stream)
+    _fp4_data(o, n, dtype, what)
+    return o
 
 
 def moe_group_route_workspace_size(T: int, E: int) -> int:
@@ -266,13 +260,21 @@ def moe_group_route(logits, bias, k: int, groups: int, top_groups: int, *, score
     if logits.dim() != 2:
         _fp4_fail("logits: [T, E]")
     T, E = logits.shape
-    o = _route_outputs(T, E, k, logits, stream, dict(topk_ids=topk_ids, gates=gates, counts=counts, f=f, P=P, aux=aux))
+    i32, f32 = torch.int32, torch.float32
+    topk_ids = _route_out(topk_ids, (T, k), T * k, i32, logits, stream, "topk_ids")
+    gates = _route_out(gates, (T, k), T * k, f32, logits, stream, "gates")
+    counts = _route_out(counts, E, E, i32, logits, stream, "counts")
+    f = _route_out(f, E, E, f32, logits, stream, "f")
+    P = _route_out(P, E, E, f32, logits, stream, "P")
+    aux = _route_out(aux, 1, 1, f32, logits, stream, "aux")
     ws = _fp4_bytes(_lib.moe_group_route_workspace_size(T, E), logits, stream) if ws is None else ws
-    _check(_lib.moe_group_route(_fp4_data(logits, T * E, torch.float32, "logits"), _fp4_data(bias, E, torch.float32, "bias"), T, E,
-                                k, groups, top_groups, _score(score), best, int(renorm), scale, alpha,
-                                *(t.data_ptr() for t in o.values()), _fp4_data(ws, 0, torch.uint8, "ws"), ws.numel(),
-                                _fp4_stream(stream, logits)))
-    return o
+    rc = _lib.moe_group_route(_fp4_data(logits, T * E, f32, "logits"), _fp4_data(bias, E, f32, "bias"), T, E, k, groups, top_groups,
+                              _score(score), best, int(renorm), scale, alpha, topk_ids.data_ptr(), gates.data_ptr(), counts.data_ptr(),
+                              f.data_ptr(), P.data_ptr(), aux.data_ptr(), _fp4_data(ws, 0, torch.uint8, "ws"), ws.numel(),
+                              _fp4_stream(stream, logits))
+    if rc:
+        _check(rc)
+    return {"topk_ids": topk_ids, "gates": gates, "counts": counts, "f": f, "P": P, "aux": aux}
 
 
 def moe_group_router_workspace_size(T: int, h: int, E: int, dtype) -> int:
@@ -290,14 +292,20 @@ def moe_group_router(x, w_packed, E: int, bias, k: int, groups: int, top_groups:
         _fp4_fail("x: a contiguous device tensor")
     if logits is None and want_logits:
         logits = _fp4_empty((T, E), torch.float32, x, stream)
-    o = _route_outputs(T, E, k, x, stream, dict(topk_ids=topk_ids, gates=gates, counts=counts, f=f, P=P, aux=aux))
+    i32, f32 = torch.int32, torch.float32
+    topk_ids = _route_out(topk_ids, (T, k), T * k, i32, x, stream, "topk_ids")
+    gates = _route_out(gates, (T, k), T * k, f32, x, stream, "gates")
+    counts = _route_out(counts, E, E, i32, x, stream, "counts")
+    f = _route_out(f, E, E, f32, x, stream, "f")
+    P = _route_out(P, E, E, f32, x, stream, "P")
+    aux = _route_out(aux, 1, 1, f32, x, stream, "aux")
     ws = _fp4_bytes(_lib.moe_group_router_workspace_size(T, h, E, dt), x, stream) if ws is None else ws
     _check(_lib.moe_group_router(x.data_ptr(), _fp4_data(w_packed, _lib.moe_router_packed_bytes(h, E, dt), torch.uint8, "w_packed"),
                                  _fp4_data(bias, E, torch.float32, "bias"), T, h, E, k, dt, groups, top_groups, _score(score), best,
                                  int(renorm), scale, alpha, _fp4_data(logits, T * E, torch.float32, "logits"),
-                                 *(t.data_ptr() for t in o.values()), _fp4_data(ws, 0, torch.uint8, "ws"), ws.numel(),
-                                 _fp4_stream(stream, x)))
-    return dict(logits=logits, **o)
+                                 topk_ids.data_ptr(), gates.data_ptr(), counts.data_ptr(), f.data_ptr(), P.data_ptr(), aux.data_ptr(),
+                                 _fp4_data(ws, 0, torch.uint8, "ws"), ws.numel(), _fp4_stream(stream, x)))
+    return dict(logits=logits, topk_ids=topk_ids, gates=gates, counts=counts, f=f, P=P, aux=aux)
 
 
 def moe_group_route_backward(logits, topk_ids, d_gates, f, *, score="sigmoid", renorm: bool = True, scale: float = 1.0,
