@@ -212,3 +212,20 @@ def test_captured(gpu_lib):
     torch.cuda.synchronize()
     assert torch.equal(d_gu, want[0]) and torch.equal(act, want[1])
     ok(gpu_lib)
+
+
+def test_past_32_bit_offsets(gpu_lib):
+    rows, F = 76000, 14336                                # 76000 x 28672 values
+    gu = torch.zeros(rows, 2 * F, dtype=torch.bfloat16, device="cuda")
+    gu[-3:] = torch.randn(3, 2 * F, generator=torch.Generator().manual_seed(0)).bfloat16().cuda()
+    da = torch.ones(rows, F, dtype=torch.bfloat16, device="cuda")
+    c, s = gpu_lib.moe_checkpoint8_save(gu)
+    d_gu, act = gpu_lib.moe_checkpoint8_swiglu_backward(c, s, da)
+    ok(gpu_lib)
+    c3, s3 = gpu_lib.moe_checkpoint8_save(gu[-3:])
+    d3, a3 = gpu_lib.moe_checkpoint8_swiglu_backward(c3, s3, da[-3:])
+    assert torch.equal(c[-3:], c3) and torch.equal(s[-3:], s3) and torch.equal(d_gu[-3:], d3) and torch.equal(act[-3:], a3)
+    assert (c[:-3] == 0).all() and (act[40000] == 0).all()
+    assert torch.equal(gpu_lib.moe_checkpoint8_load(c, s)[-3:], gpu_lib.moe_checkpoint8_load(c3, s3))
+    del gu, da, c, s, d_gu, act
+    torch.cuda.empty_cache()

@@ -51,8 +51,6 @@ SHAPES = [  # T, E, k, groups, top_groups, best
                                                         (False, True, 1.0, 0.3)])
 @pytest.mark.parametrize("T,E,k,groups,top_groups,best", SHAPES)
 def test_route_and_its_gradient(gpu_lib, score, biased, renorm, scale, masked, T, E, k, groups, top_groups, best):
-    if T > 1000 and masked:
-        pytest.skip("once is enough")
     L, b = logits_of(T, E, T * 31 + E, masked), bias_of(E, E) if biased else None
     r = gpu_lib.moe_group_route(L.cuda(), b.cuda() if biased else None, k, groups, top_groups, score=score, best=best, renorm=renorm, scale=scale)
     ok(gpu_lib)
@@ -169,3 +167,30 @@ def test_captured_and_on_another_stream(gpu_lib):
         torch.cuda.synchronize()
     assert all(torch.equal(out[k], first[k]) for k in out) and torch.equal(d, d2)
     ok(gpu_lib)
+
+
+def test_logits_past_32_bit_offsets(gpu_lib):
+    T, E = 2_200_000, 1024
+    L = torch.zeros(T, E, device="cuda")
+    L[-5:] = logits_of(5, E, 3).cuda()
+    r = gpu_lib.moe_group_route(L, None, 8, 8, 4)
+    part = gpu_lib.moe_group_route(L[-5:].contiguous(), None, 8, 8, 4)
+    ok(gpu_lib)
+    assert torch.equal(r["topk_ids"][-5:], part["topk_ids"]) and torch.equal(r["gates"][-5:], part["gates"])
+    assert (r["topk_ids"][:-5] == torch.arange(8, device="cuda")).all() and r["counts"].sum().item() == 8 * T
+    del L
+    torch.cuda.empty_cache()
+
+
+def test_many_ties_of_few_values(gpu_lib):
+    # logits of a coarse grid: ties in every token, across lanes and groups, with and without equal biases
+    g = torch.Generator().manual_seed(2)
+    for E, groups in ((256, 8), (160, 8), (96, 32), (512, 4)):
+        L = torch.randint(-4, 5, (60, E), generator=g).float() * 0.5
+        for b in (None, torch.randint(0, 3, (E,), generator=g).float() * 0.125):
+            for score in ("sigmoid", "softmax"):
+                for best in (1, 2):
+                    r = gpu_lib.moe_group_route(L.cuda(), None if b is None else b.cuda(), 6, groups, 3, score=score, best=best)
+                    ok(gpu_lib)
+                    want = O.route(L.double().numpy(), None if b is None else b.numpy(), 6, groups, 3, score, best, True, 1.0)
+                    np.testing.assert_array_equal(r["topk_ids"].cpu().numpy(), want["ids"])

@@ -351,3 +351,115 @@ def test_captured_on_streams_with_changing_rows(gpu_lib):
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
     ok(gpu_lib)
+
+
+# ------------------------------------------------------------------------------------------ edges
+
+
+@pytest.mark.parametrize("G,rows", [(1, 3), (6, 40), (2, 60), (2, 200), (2, 700)])
+def test_waits_that_run_out_are_reported(gpu_lib, G, rows):
+    """Every tile shape of the product, with a single poll for each wait: one that runs out is reported and leaves the device usable, and
+    a call that reports none is whole. (A poll itself waits, as long as the chip sees fit.)"""
+    K, N = 4096, 300
+    x = data((rows, K), "bf16", 1)
+    w, ws = weight(G, N, K)
+    packed = gpu_lib.moe_int8_pack_weight(w)
+    off = dev(np.linspace(0, rows, G + 1).astype(int))
+    want = gpu_lib.moe_int8_linear(x, off, packed, ws)
+    ok(gpu_lib)
+    gpu_lib.moe_set_wait_limit(1)
+    try:
+        for _ in range(3):
+            y = gpu_lib.moe_int8_linear(x, off, packed, ws)
+            torch.cuda.synchronize()
+            status = gpu_lib.moe_check_device_error()
+            assert status == gpu_lib.MOE_ERR_TIMEOUT or (status == gpu_lib.MOE_OK and torch.equal(y, want))
+    finally:
+        gpu_lib.moe_set_wait_limit(0)
+    assert torch.equal(gpu_lib.moe_int8_linear(x, off, packed, ws), want)
+    ok(gpu_lib)
+
+
+@pytest.mark.parametrize("rows", [6, 70, 500])
+def test_a_bad_row_of_the_ffn_leaves_the_others(gpu_lib, rows):
+    E, h, F = 2, 128, 96
+    x = data((rows, h), "bf16", 3)
+    gate, gs = weight(E, F, h, 2)
+    up, us = weight(E, F, h, 3)
+    down, ds = weight(E, h, F, 4)
+    packed = gpu_lib.moe_int8_pack_expert_weights(gate, up, down)
+    off = dev([0, rows // 2, rows])
+    good = gpu_lib.moe_int8_expert_ffn(x, off, packed, gs, us, ds)
+    x[1, 5] = float("nan")
+    x[rows - 1, 0] = float("inf")
+    x[2] = 0.0
+    bad = gpu_lib.moe_int8_expert_ffn(x, off, packed, gs, us, ds)
+    ok(gpu_lib)
+    keep = torch.ones(rows, dtype=torch.bool)
+    keep[[1, 2, rows - 1]] = False
+    assert torch.equal(bad[keep], good[keep]) and bad[1].isnan().all() and bad[rows - 1].isnan().all() and (bad[2] == 0).all()
+
+
+def test_a_rows_result_does_not_depend_on_the_batch(gpu_lib):
+    """Sums below 2^24 are exact, so the kernels of few and of many rows give the same bits."""
+    K, N = 512, 200
+    x = data((900, K), "bf16", 5)
+    w, ws = weight(1, N, K)
+    packed = gpu_lib.moe_int8_pack_weight(w)
+    whole = gpu_lib.moe_int8_linear(x, dev([0, 900]), packed, ws, out_dtype=torch.float32)
+    for n in (1, 5, 8, 9, 16, 17, 33, 64, 100, 129, 256, 257):
+        part = gpu_lib.moe_int8_linear(x[:n], dev([0, n]), packed, ws, out_dtype=torch.float32)
+        assert torch.equal(part, whole[:n]), n
+    ok(gpu_lib)
+
+
+def test_outputs_and_rows_past_32_bit_offsets(gpu_lib):
+    # 40000 x 60000 outputs; 140000 x 16384 values of rows
+    K, N, rows = 64, 60000, 40000
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    x[-300:] = data((300, K), "bf16", 7)
+    w, ws = weight(1, N, K)
+    y = gpu_lib.moe_int8_linear(x, dev([0, rows]), gpu_lib.moe_int8_pack_weight(w), ws)
+    ok(gpu_lib)
+    assert (y[:1000] == 0).all()
+    part = gpu_lib.moe_int8_linear(x[-300:], dev([0, 300]), gpu_lib.moe_int8_pack_weight(w), ws)
+    assert torch.equal(y[-300:], part)
+    del y, x
+    x = torch.zeros(140000, 16384, dtype=torch.bfloat16, device="cuda")
+    x[-2:] = data((2, 16384), "bf16", 8)
+    c, s = gpu_lib.moe_int8_quantize(x)
+    d = gpu_lib.moe_int8_dequantize(c, s)
+    ok(gpu_lib)
+    code, scale = Q.quantize(f64(x[-2:]))
+    np.testing.assert_array_equal(c[-2:].cpu().numpy(), code)
+    assert torch.equal(d[-2:], (c[-2:].float() * s[-2:, None]).bfloat16()) and (s[:-2] == 0).all() and (d[70000] == 0).all()
+
+
+def test_a_schedule_past_the_rows_is_cut(gpu_lib):
+    w, ws = weight(1, 96, 64)
+    x = data((40, 64))
+    full = torch.full((60, 96), 5.0, dtype=torch.bfloat16, device="cuda")
+    gpu_lib.moe_int8_linear(x, None, gpu_lib.moe_int8_pack_weight(w), ws, tile_sched=gpu_lib.moe_dense_tile_sched(128), out=full[:40])
+    ok(gpu_lib)
+    assert torch.equal(full[:40], gpu_lib.moe_int8_linear(x, dev([0, 40]), gpu_lib.moe_int8_pack_weight(w), ws)) and (full[40:] == 5).all()
+    out = torch.full((40, 96), 5.0, dtype=torch.bfloat16, device="cuda")
+    gpu_lib.moe_int8_linear(x, None, gpu_lib.moe_int8_pack_weight(w), ws, tile_sched=gpu_lib.moe_dense_tile_sched(128 * 20), out=out)
+    torch.cuda.synchronize()
+    assert gpu_lib.moe_check_device_error() == gpu_lib.MOE_ERR_INVALID_ARG and (out == 5).all()
+
+
+def test_no_rows_and_groups_without_rows(gpu_lib):
+    w, ws = weight(4, 40, 64)
+    packed = gpu_lib.moe_int8_pack_weight(w)
+    assert gpu_lib.moe_int8_linear(data((0, 64)), dev([0] * 5), packed, ws).shape == (0, 40)
+    for rows in (3, 300):
+        out = torch.full((rows, 40), 2.0, dtype=torch.bfloat16, device="cuda")
+        gpu_lib.moe_int8_linear(data((rows, 64)), dev([0] * 5), packed, ws, out=out)
+        ok(gpu_lib)
+        assert (out == 2).all()
+        y = gpu_lib.moe_int8_linear(data((rows, 64)), dev([0, 0, rows, rows, rows]), packed, ws)
+        assert torch.equal(y, gpu_lib.moe_int8_linear(data((rows, 64)), dev([0, rows]), gpu_lib.moe_int8_pack_weight(w[1:2]), ws[1:2]))
+    none = torch.full((7,), -1, dtype=torch.int32, device="cuda")
+    y = gpu_lib.moe_int8_linear(data((0, 64)), dev([0, 2, 4, 5, 7]), packed, ws, src=none)
+    ok(gpu_lib)
+    assert (y == 0).all()
