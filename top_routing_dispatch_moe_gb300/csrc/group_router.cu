@@ -515,35 +515,51 @@ group_gate_kernel(const __grid_constant__ Args a) {
 //   ds_j = scale d_g_j, or with renormalised gates scale (d_g_j - sum_i d_g_i s_i / S) / S, S = sum_i s_i (0 where S is 0)
 //   c_e = d_aux alpha E f_e / T;  softmax: dp = ds + c, d_logits = p (dp - <dp, p>)
 //   sigmoid: d_logits = (ds + (c - <c, q>) / sum s) s (1 - s), q = s / sum s
+// The ds reach their experts through a row of shared memory that is zero but for them (compared with every slot of every lane instead, and the
+// scores taken from the lanes that hold them, a token cost 920 instructions: 16384 x 256 in 19.6 us).
+constexpr int kBwdWarps = 8;
 template <int NPL>
-__global__ void __launch_bounds__(256)
-group_gate_backward_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ d_gates,
-                           const float* __restrict__ f, int T, int E, int k, bool sigmoid, bool renorm, float scale, float coef,
-                           float* __restrict__ d_logits, unsigned* err) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+__global__ void __launch_bounds__(kBwdWarps * 32)
+group_gate_backward_kernel(const float* logits, const int32_t* ids, const float* d_gates, const float* f, int T, int E, int k, bool sigmoid,
+                           bool renorm, float scale, float coef, float* d_logits, unsigned* err) {
+    __shared__ float s_ds[kBwdWarps][32 * NPL];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float* row = s_ds[warp];
     float c[NPL];
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) c[i] = lane + 32 * i < E ? coef * f[lane + 32 * i] : 0.f;
-    for (int t = blockIdx.x * nw + warp; t < T; t += gridDim.x * nw) {
-        float s[NPL], n[NPL], d[NPL];                                // score, 1 - score, gradient of the score
+    for (int i = 0; i < NPL; ++i) {
+        c[i] = lane + 32 * i < E ? coef * f[lane + 32 * i] : 0.f;
+        row[lane + 32 * i] = 0.f;
+    }
+    __syncwarp();
+    for (int t = blockIdx.x * kBwdWarps + warp; t < T; t += gridDim.x * kBwdWarps) {
+        const float* src = logits + (size_t)t * E;
+        float s[NPL], n[NPL];                                        // score, 1 - score
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) s[i] = lane + 32 * i < E ? __ldcs(logits + (size_t)t * E + lane + 32 * i) : -INFINITY;
+        for (int i = 0; i < NPL; ++i) s[i] = lane + 32 * i < E ? src[lane + 32 * i] : -INFINITY;
         int id = -1;
-        float dg = 0.f;
+        float dg = 0.f, mine = 0.f;                                  // lane j: choice j, its gate's gradient and its score
         if (lane < k) {
             id = ids[(size_t)t * k + lane];
             dg = d_gates[(size_t)t * k + lane];
             if (id < 0 || id >= E) { latch_device_error(err, kDevErrBadIndex, 0x300u); id = -1; }
+            if (id >= 0) mine = src[id];
+            else dg = 0.f;
         }
         float total = 0.f, m = 0.f;
         if (sigmoid) {
+            // e = exp(-|L|): s and 1 - s are 1 / (1 + e) and e / (1 + e), neither a difference
 #pragma unroll
             for (int i = 0; i < NPL; ++i) {
-                const float e = expf(-fabsf(s[i])), inv = 1.f / (1.f + e), a = e * inv;
-                n[i] = s[i] >= 0.f ? a : inv;
-                s[i] = s[i] >= 0.f ? inv : a;
-                if (lane + 32 * i >= E) s[i] = 0.f;
+                const float e = ex2(-kLog2e * fabsf(s[i])), inv = rcp(1.f + e), b = e * inv;
+                const bool up = s[i] >= 0.f;
+                n[i] = up ? b : inv;
+                s[i] = up ? inv : b;
+                total += s[i];
             }
+            mine = id >= 0 ? rcp(1.f + ex2(-kLog2e * mine)) : 0.f;
         } else {
             m = s[0];
 #pragma unroll
@@ -551,59 +567,64 @@ group_gate_backward_kernel(const float* __restrict__ logits, const int32_t* __re
             m = warp_max(m);
 #pragma unroll
             for (int i = 0; i < NPL; ++i) {
-                s[i] = s[i] != -INFINITY ? expf(s[i] - m) : 0.f;
-                n[i] = 0.f;
+                s[i] = s[i] != -INFINITY ? ex2((s[i] - m) * kLog2e) : 0.f;
+                total += s[i];
             }
+            mine = id >= 0 && mine != -INFINITY ? ex2((mine - m) * kLog2e) : 0.f;
         }
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) total += s[i];
         total = warp_sum(total);
-        const float tinv = total == 0.f ? 0.f : 1.f / total;
+        const float tinv = total == 0.f ? 0.f : rcp(total);
         if (!sigmoid) {
+            mine *= tinv;
 #pragma unroll
             for (int i = 0; i < NPL; ++i) s[i] *= tinv;
         }
         float ds = scale * dg;
         if (renorm) {
-            float mine = 0.f;                                        // lane j: the score of choice j
-            for (int j = 0; j < k; ++j) {
-                const int e = __shfl_sync(0xffffffffu, id, j);
-                float v = 0.f;
-#pragma unroll
-                for (int i = 0; i < NPL; ++i)
-                    if (lane + 32 * i == e) v = s[i];
-                v = __shfl_sync(0xffffffffu, v, e & 31);
-                if (lane == j && e >= 0) mine = v;
-            }
             const float S = warp_sum(mine), w = warp_sum(mine * dg);
             const float inv = S == 0.f ? 0.f : 1.f / S;
             ds = scale * (dg - w * inv) * inv;
         }
-        float cq = 0.f;
+        // a choice that is there twice (no route has one) is added in the choices' order
+        const unsigned same = __match_any_sync(0xffffffffu, id >= 0 ? id : -1 - lane);
+        const bool first = id >= 0 && lane == __ffs(same) - 1;
+        if (__any_sync(0xffffffffu, __popc(same) > 1)) {
+            float sum = 0.f;
+            for (int j = 0; j < k; ++j) {
+                const float v = __shfl_sync(0xffffffffu, ds, j);
+                if (same >> j & 1u) sum += v;
+            }
+            ds = sum;
+        }
+        if (first) row[id] = ds;
+        __syncwarp();
+        float d[NPL];                                                // gradient of the score
         if (sigmoid) {
+            float cq = 0.f;
 #pragma unroll
             for (int i = 0; i < NPL; ++i) cq += c[i] * s[i];
             cq = warp_sum(cq) * tinv;
-        }
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) d[i] = sigmoid ? (c[i] - cq) * tinv : c[i];
-        for (int j = 0; j < k; ++j) {
-            const int e = __shfl_sync(0xffffffffu, id, j);
-            const float v = __shfl_sync(0xffffffffu, ds, j);
+            for (int i = 0; i < NPL; ++i) d[i] = row[lane + 32 * i] + (c[i] - cq) * tinv;
 #pragma unroll
-            for (int i = 0; i < NPL; ++i)
-                if (lane + 32 * i == e) d[i] += v;
-        }
-        float dot = 0.f;
-        if (!sigmoid) {
+            for (int i = 0; i < NPL; ++i) d[i] = d[i] * s[i] * n[i];
+        } else {
+            float dot = 0.f;
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) dot += d[i] * s[i];
+            for (int i = 0; i < NPL; ++i) {
+                d[i] = row[lane + 32 * i] + c[i];
+                dot += d[i] * s[i];
+            }
             dot = warp_sum(dot);
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) d[i] = s[i] * (d[i] - dot);
         }
+        __syncwarp();
+        if (first) row[id] = 0.f;
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
-            if (lane + 32 * i < E)
-                __stcs(d_logits + (size_t)t * E + lane + 32 * i, sigmoid ? d[i] * s[i] * n[i] : s[i] * (d[i] - dot));
+            if (lane + 32 * i < E) __stcs(d_logits + (size_t)t * E + lane + 32 * i, d[i]);
     }
 }
 
@@ -621,6 +642,29 @@ Ws ws_layout(void* ws, int T, int E) {
     w.term_part = reinterpret_cast<float*>(base + off); off = align_up(off + (size_t)finalize_grid(T, E) * 4, 256);
     w.bytes = off;
     return w;
+}
+
+// Launches on as many blocks as are resident at once (into *G; one that finalizes too where a.counts is set). What the runtime says of a
+// kernel is kept: asked in every call, it cost a small one two microseconds. (The shared memory is below 48 KB for any E.)
+template <int NPL, bool FULL>
+int launch_gate(Args& a, int* G, cudaStream_t s) {
+    static int per_sm[64];
+    static unsigned long long of_ctx[64];
+    const auto kernel = group_gate_kernel<NPL, FULL>;
+    auto smem_of = [](int E) { return (size_t)kWarps * E * sizeof(float) + (size_t)E * sizeof(int); };
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return set_error(MOE_ERR_CUDA, "group routing: no usable current device");
+    const unsigned long long ctx = context_id();
+    if (ctx == 0 || of_ctx[dev] != ctx || !per_sm[dev]) {
+        int n = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kWarps * 32, smem_of(32 * NPL));
+        per_sm[dev] = e == cudaSuccess && n > 0 ? n : 1;
+        of_ctx[dev] = context_id();
+    }
+    const size_t smem = smem_of(a.E);
+    a.vec = a.npl == NPL && NPL % 4 == 0 && a.E % 4 == 0 && aligned16(a.logits) && a.E % NPL == 0;
+    *G = a.counts ? 1 : std::min(grid_of(a.T), per_sm[dev] * num_sms());
+    return check_launch(launch_pdl(kernel, dim3(*G), dim3(kWarps * 32), smem, s, a), "group_gate_kernel");
 }
 
 int check_spec(const char* fn, int T, int E, int k, int groups, int top_groups, int score, int best, float scale) {
@@ -654,28 +698,18 @@ int launch_group_gate(const GroupGate& g, void* ws, cudaStream_t s) {
         a.lpg = 0;
         for (int n = least; n <= std::min(a.per, 32); ++n)
             if (a.per % n == 0 && (n <= 8 || n < 2 * least)) { a.npl = n; a.lpg = a.per / n; break; }
-        const size_t smem = (size_t)kWarps * g.E * sizeof(float) + (size_t)g.E * sizeof(int);
-        auto launch = [&](auto kernel, int n) {
-            a.vec = a.npl == n && n % 4 == 0 && g.E % 4 == 0 && aligned16(g.logits) && g.E % n == 0;
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            int per_sm = 0;
-            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kWarps * 32, smem) != cudaSuccess || per_sm < 1) per_sm = 1;
-            G = std::min(grid_of(g.T), per_sm * num_sms());
-            // up to two tokens a warp of one block: a second block and the finalize's launch cost more
-            if (g.T <= 2 * kWarps) {
-                G = 1;
-                a.counts = g.counts; a.f = g.f; a.P = g.P; a.aux = g.aux; a.alpha = g.alpha;
-            }
-            return launch_pdl(kernel, dim3(G), dim3(kWarps * 32), smem, s, a);
-        };
+        // up to two tokens a warp of one block: a second block and the finalize's launch cost more
+        if (g.T <= 2 * kWarps) {
+            a.counts = g.counts; a.f = g.f; a.P = g.P; a.aux = g.aux; a.alpha = g.alpha;
+        }
         a.lpg_log = 0;
         while (1 << (a.lpg_log + 1) <= a.lpg) ++a.lpg_log;
         const bool full = a.lpg == 1 << a.lpg_log && g.E == 32 * a.npl;
-#define MOE_GATE(N) (full && a.npl == N ? launch(group_gate_kernel<N, true>, N) : launch(group_gate_kernel<N, false>, N))
-        const cudaError_t e = a.npl <= 1 ? MOE_GATE(1) : a.npl <= 2 ? MOE_GATE(2) : a.npl <= 4 ? MOE_GATE(4) : a.npl <= 8 ? MOE_GATE(8)
+#define MOE_GATE(N) (full && a.npl == N ? launch_gate<N, true>(a, &G, s) : launch_gate<N, false>(a, &G, s))
+        const int rc = a.npl <= 1 ? MOE_GATE(1) : a.npl <= 2 ? MOE_GATE(2) : a.npl <= 4 ? MOE_GATE(4) : a.npl <= 8 ? MOE_GATE(8)
                             : a.npl <= 16 ? MOE_GATE(16) : MOE_GATE(32);
 #undef MOE_GATE
-        if (int rc = check_launch(e, "group_gate_kernel")) return rc;
+        if (rc) return rc;
         if (a.counts) return MOE_OK;
     }
     return launch_router_finalize(w.partial_P, w.partial_C, G, g.T, g.E, g.k, g.alpha, g.counts, g.f, g.P, g.aux, w.term_part,
@@ -723,11 +757,12 @@ extern "C" int moe_group_route_backward(const float* logits, const int32_t* topk
     unsigned* err = device_error_word();
     MOE_REQUIRE(err, MOE_ERR_CUDA, "%s: device error word unavailable", fn);
     const float coef = d_aux * alpha * (float)E / (float)T;
-    const int G = std::min(cdiv(T, 8), 8 * num_sms());
+    const int G = std::min(cdiv(T, kBwdWarps), 4 * num_sms());
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-#define MOE_GROUP_BWD(N)                                                                                              \
-    group_gate_backward_kernel<N><<<G, 256, 0, s>>>(logits, topk_ids, d_gates, f, T, E, k, score == MOE_SCORE_SIGMOID, renorm != 0, \
-                                                    scale, coef, d_logits, err)
+    cudaError_t e = cudaSuccess;
+#define MOE_GROUP_BWD(N)                                                                                                    \
+    e = launch_pdl(group_gate_backward_kernel<N>, dim3(G), dim3(kBwdWarps * 32), 0, s, logits, topk_ids, d_gates, f, T, E, k, \
+                   score == MOE_SCORE_SIGMOID, renorm != 0, scale, coef, d_logits, err)
     const int n = cdiv(E, 32);
     if (n <= 1) MOE_GROUP_BWD(1);
     else if (n <= 2) MOE_GROUP_BWD(2);
@@ -736,5 +771,5 @@ extern "C" int moe_group_route_backward(const float* logits, const int32_t* topk
     else if (n <= 16) MOE_GROUP_BWD(16);
     else MOE_GROUP_BWD(32);
 #undef MOE_GROUP_BWD
-    return check_launch("group_gate_backward_kernel");
+    return check_launch(e, "group_gate_backward_kernel");
 }

@@ -56,7 +56,8 @@ __device__ __forceinline__ float scale_of(float amax, Steps& st) {
     st.a = st.live ? amax * f : 1.f;
     st.r = __frcp_rn(st.a);
     st.inv = st.live ? __fdiv_rn(127.f, amax) : 0.f;
-    return st.live ? __fdiv_rn(amax, 127.f) : finite ? 0.f : __uint_as_float(0x7FC00000u);
+    const float q = amax * (1.f / 127.f), scale = fmaf(fmaf(-q, 127.f, amax), 1.f / 127.f, q);      // amax / 127, rounded (as codes_of has it)
+    return st.live ? scale : finite ? 0.f : __uint_as_float(0x7FC00000u);
 }
 
 // 1.5 * 2^23: its sum with |q| < 2^22 is q rounded to a whole number, ties to even, whose two's complement are the sum's low bits.

@@ -239,12 +239,37 @@ def _score(score: str | int) -> int:
     return int(score)
 
 
-def _route_out(o, shape, n: int, dtype, t, stream, what: str):
-    """A routing output: `o`, checked, or a new one."""
-    if o is None:
-        return torch.empty(shape, dtype=dtype, device=t.device) if stream is None else _fp4_empty(shape, dtype, t, stream)
-    _fp4_data(o, n, dtype, what)
-    return o
+def _route_outputs(T: int, E: int, k: int, t, stream, topk_ids, gates, counts, f, P, aux):
+    """The routing outputs: those given, checked, and new ones for the rest."""
+    i32, f32, dev, empty = torch.int32, torch.float32, t.device, torch.empty
+    if stream is not None:
+        def empty(shape, dtype, device):
+            return _fp4_empty(shape, dtype, t, stream)
+    if topk_ids is None:
+        topk_ids = empty((T, k), dtype=i32, device=dev)
+    else:
+        _fp4_data(topk_ids, T * k, i32, "topk_ids")
+    if gates is None:
+        gates = empty((T, k), dtype=f32, device=dev)
+    else:
+        _fp4_data(gates, T * k, f32, "gates")
+    if counts is None:
+        counts = empty(E, dtype=i32, device=dev)
+    else:
+        _fp4_data(counts, E, i32, "counts")
+    if f is None:
+        f = empty(E, dtype=f32, device=dev)
+    else:
+        _fp4_data(f, E, f32, "f")
+    if P is None:
+        P = empty(E, dtype=f32, device=dev)
+    else:
+        _fp4_data(P, E, f32, "P")
+    if aux is None:
+        aux = empty(1, dtype=f32, device=dev)
+    else:
+        _fp4_data(aux, 1, f32, "aux")
+    return topk_ids, gates, counts, f, P, aux
 
 
 def moe_group_route_workspace_size(T: int, E: int) -> int:
@@ -260,13 +285,8 @@ def moe_group_route(logits, bias, k: int, groups: int, top_groups: int, *, score
     if logits.dim() != 2:
         _fp4_fail("logits: [T, E]")
     T, E = logits.shape
-    i32, f32 = torch.int32, torch.float32
-    topk_ids = _route_out(topk_ids, (T, k), T * k, i32, logits, stream, "topk_ids")
-    gates = _route_out(gates, (T, k), T * k, f32, logits, stream, "gates")
-    counts = _route_out(counts, E, E, i32, logits, stream, "counts")
-    f = _route_out(f, E, E, f32, logits, stream, "f")
-    P = _route_out(P, E, E, f32, logits, stream, "P")
-    aux = _route_out(aux, 1, 1, f32, logits, stream, "aux")
+    f32 = torch.float32
+    topk_ids, gates, counts, f, P, aux = _route_outputs(T, E, k, logits, stream, topk_ids, gates, counts, f, P, aux)
     ws = _fp4_bytes(_lib.moe_group_route_workspace_size(T, E), logits, stream) if ws is None else ws
     rc = _lib.moe_group_route(_fp4_data(logits, T * E, f32, "logits"), _fp4_data(bias, E, f32, "bias"), T, E, k, groups, top_groups,
                               _score(score), best, int(renorm), scale, alpha, topk_ids.data_ptr(), gates.data_ptr(), counts.data_ptr(),
@@ -292,13 +312,7 @@ def moe_group_router(x, w_packed, E: int, bias, k: int, groups: int, top_groups:
         _fp4_fail("x: a contiguous device tensor")
     if logits is None and want_logits:
         logits = _fp4_empty((T, E), torch.float32, x, stream)
-    i32, f32 = torch.int32, torch.float32
-    topk_ids = _route_out(topk_ids, (T, k), T * k, i32, x, stream, "topk_ids")
-    gates = _route_out(gates, (T, k), T * k, f32, x, stream, "gates")
-    counts = _route_out(counts, E, E, i32, x, stream, "counts")
-    f = _route_out(f, E, E, f32, x, stream, "f")
-    P = _route_out(P, E, E, f32, x, stream, "P")
-    aux = _route_out(aux, 1, 1, f32, x, stream, "aux")
+    topk_ids, gates, counts, f, P, aux = _route_outputs(T, E, k, x, stream, topk_ids, gates, counts, f, P, aux)
     ws = _fp4_bytes(_lib.moe_group_router_workspace_size(T, h, E, dt), x, stream) if ws is None else ws
     _check(_lib.moe_group_router(x.data_ptr(), _fp4_data(w_packed, _lib.moe_router_packed_bytes(h, E, dt), torch.uint8, "w_packed"),
                                  _fp4_data(bias, E, torch.float32, "bias"), T, h, E, k, dt, groups, top_groups, _score(score), best,
