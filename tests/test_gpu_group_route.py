@@ -42,7 +42,7 @@ def compare(r, want, T, L):
 
 SHAPES = [  # T, E, k, groups, top_groups, best
     (1, 1, 1, 1, 1, 1), (3, 4, 2, 2, 1, 2), (5, 16, 4, 4, 2, 2), (7, 32, 8, 8, 4, 2), (9, 33, 3, 3, 2, 2), (4, 64, 16, 8, 2, 1),
-    (33, 72, 6, 8, 3, 2), (17, 96, 5, 32, 3, 2), (65, 160, 6, 8, 3, 1), (130, 256, 8, 8, 4, 2), (40, 256, 8, 1, 1, 1), (12, 300, 7, 6, 2, 2),
+    (33, 72, 6, 8, 3, 2), (17, 96, 5, 32, 3, 2), (65, 160, 6, 8, 3, 1), (29, 96, 8, 8, 4, 2), (31, 160, 8, 8, 3, 2), (33, 192, 8, 8, 2, 2), (23, 384, 8, 8, 4, 2), (14, 224, 7, 7, 3, 2), (130, 256, 8, 8, 4, 2), (40, 256, 8, 1, 1, 1), (12, 300, 7, 6, 2, 2),
     (21, 512, 8, 16, 4, 2), (6, 976, 16, 16, 5, 2), (11, 1024, 16, 32, 8, 2), (3, 1024, 4, 1, 1, 2), (2500, 256, 8, 8, 4, 2)]
 
 

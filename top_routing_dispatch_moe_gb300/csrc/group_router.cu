@@ -218,7 +218,7 @@ __device__ __forceinline__ float rcp(float x) {
 }
 constexpr float kLog2e = 1.44269504f;
 
-// Keys by falling order (Batcher's odd-even merge of N = 2^n).
+// Keys by falling order (Batcher's merge exchange).
 template <int N>
 __device__ __forceinline__ void sort_keys(unsigned (&key)[N]) {
 #pragma unroll
@@ -246,8 +246,8 @@ __device__ __forceinline__ void sort_keys(unsigned (&key)[N]) {
 template <int NPL, bool FULL>
 __global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 3 : NPL == 16 ? 2 : 1)
 group_gate_kernel(const __grid_constant__ Args a) {
-    constexpr unsigned SLOT = NPL - 1;
-    constexpr int SB = NPL == 1 ? 0 : NPL == 2 ? 1 : NPL == 4 ? 2 : NPL == 8 ? 3 : NPL == 16 ? 4 : 5;
+    constexpr int SB = NPL == 1 ? 0 : NPL == 2 ? 1 : NPL <= 4 ? 2 : NPL <= 8 ? 3 : NPL <= 16 ? 4 : 5;     // bits of a slot
+    constexpr unsigned SLOT = (1u << SB) - 1;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     float* s_P = reinterpret_cast<float*>(smem_raw);                   // [warps][E]; a warp's row holds its selection scores before
     int* s_hist = reinterpret_cast<int*>(s_P + (size_t)kWarps * a.E);
@@ -430,7 +430,7 @@ group_gate_kernel(const __grid_constant__ Args a) {
         auto near = [&](unsigned hi, unsigned lo) {
             if (!a.bias) return (hi >> SB) == (lo >> SB);
             const float x = value_of(hi & ~SLOT), y = value_of(lo & ~SLOT);
-            return !(x - y > 2.f * serr + (6.1e-8f + 1.2e-7f * NPL) * (fabsf(x) + fabsf(y))) && x > 0.1f * kMasked;
+            return !(x - y > 2.f * serr + (6.1e-8f + 1.2e-7f * (SLOT + 1)) * (fabsf(x) + fabsf(y))) && x > 0.1f * kMasked;
         };
         auto logit_of = [&](int e) {                              // the parts in their order
             float l = src[e];
@@ -706,8 +706,11 @@ int launch_group_gate(const GroupGate& g, void* ws, cudaStream_t s) {
         while (1 << (a.lpg_log + 1) <= a.lpg) ++a.lpg_log;
         const bool full = a.lpg == 1 << a.lpg_log && g.E == 32 * a.npl;
 #define MOE_GATE(N) (full && a.npl == N ? launch_gate<N, true>(a, &G, s) : launch_gate<N, false>(a, &G, s))
-        const int rc = a.npl <= 1 ? MOE_GATE(1) : a.npl <= 2 ? MOE_GATE(2) : a.npl <= 4 ? MOE_GATE(4) : a.npl <= 8 ? MOE_GATE(8)
-                            : a.npl <= 16 ? MOE_GATE(16) : MOE_GATE(32);
+        // (npl 3, 5, 6, 12: 96, 160, 192, 384 experts; those of other sizes have predicates on every slot)
+        const int rc = a.npl <= 1 ? MOE_GATE(1) : a.npl <= 2 ? MOE_GATE(2) : full && a.npl == 3 ? launch_gate<3, true>(a, &G, s)
+                     : a.npl <= 4 ? MOE_GATE(4) : full && a.npl == 5 ? launch_gate<5, true>(a, &G, s)
+                     : full && a.npl == 6 ? launch_gate<6, true>(a, &G, s) : a.npl <= 8 ? MOE_GATE(8)
+                     : full && a.npl == 12 ? launch_gate<12, true>(a, &G, s) : a.npl <= 16 ? MOE_GATE(16) : MOE_GATE(32);
 #undef MOE_GATE
         if (rc) return rc;
         if (a.counts) return MOE_OK;
