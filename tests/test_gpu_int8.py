@@ -356,7 +356,7 @@ def test_captured_on_streams_with_changing_rows(gpu_lib):
 # ------------------------------------------------------------------------------------------ edges
 
 
-@pytest.mark.parametrize("G,rows", [(1, 3), (6, 40), (2, 60), (2, 200), (2, 700)])
+@pytest.mark.parametrize("G,rows", [(1, 3), (6, 40), (2, 100), (2, 250), (2, 700), (20, 1000), (20, 2400)])
 def test_waits_that_run_out_are_reported(gpu_lib, G, rows):
     """Every tile shape of the product, with a single poll for each wait: one that runs out is reported and leaves the device usable, and
     a call that reports none is whole. (A poll itself waits, as long as the chip sees fit.)"""

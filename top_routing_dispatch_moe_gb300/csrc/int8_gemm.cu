@@ -720,14 +720,15 @@ static int launch_pair(const Params& p, cudaStream_t s) {
                         EPI == EPI_SWIGLU ? "int8 pair_kernel<swiglu>" : "int8 pair_kernel");
 }
 
-// Rows of a tile. A stage takes its MMAs as long for 64 rows as for 256, so more rows mean fewer tiles; 64 and 128 where groups are no
-// larger on average, and where the tiles are no more than the pairs that run at once: a call is then one tile long, and the epilogue of fewer
-// rows is shorter (1003 rows by 7 x 1001 x 1044 in fp32, 256 rows 15.5 us).
+// Rows of a tile. A stage takes its MMAs as long for 64 rows as for 256, so more rows mean fewer tiles where groups are larger than a tile;
+// where they are not, fewer rows leave more weights under way. 128 groups by 1536 x 2048, us by tiles of 64 / 128 / 256 rows: 64 rows a group
+// 90 / 94 / 107, 96: 153 / 105 / 116, 128: 158 / 114 / 126, 256: 304 / 197 / 174. And where the tiles are no more than the pairs that run at
+// once, a call is one tile long, and the epilogue of fewer rows is shorter (1003 rows by 7 x 1001 x 1044 in fp32: 13.4 / 12.3 / 14.5).
 template <int EPI>
 static int launch_pairs(const Params& p, cudaStream_t s) {
     const long long avg = p.rows / p.G, used = std::min(p.G, p.rows), pairs = num_sms() / 2, blocks = (p.NB + 1) / 2;
-    if (avg <= 48 || (p.rows / 64 + used) * blocks <= pairs) return launch_pair<EPI, 64>(p, s);
-    if (avg <= 128 || (p.rows / 128 + used) * blocks <= pairs) return launch_pair<EPI, 128>(p, s);
+    if (avg <= 64 || ((p.rows - used) / 64 + used) * blocks <= pairs) return launch_pair<EPI, 64>(p, s);
+    if (avg <= 128 || ((p.rows - used) / 128 + used) * blocks <= pairs) return launch_pair<EPI, 128>(p, s);
     return launch_pair<EPI, 256>(p, s);
 }
 
@@ -751,10 +752,13 @@ static int launch_few(const Params& p, cudaStream_t s) {
 
 template <int EPI>
 static int launch_product(const Params& p, cudaStream_t s) {
-    MOE_REQUIRE(((long long)p.rows / 32 + p.G) * p.NB < (1LL << 31), MOE_ERR_INVALID_ARG,
+    MOE_REQUIRE(((long long)p.rows / FEW_ROWS + p.G) * p.NB < (1LL << 31), MOE_ERR_INVALID_ARG,
                 "8-bit product: %d rows by %d channels are over 2^31 tiles", p.rows, p.N);
-    // few rows where a group has up to 16 on average
-    return p.rows / std::min(p.G, p.rows) <= FEW_ROWS ? launch_few<EPI>(p, s) : launch_pairs<EPI>(p, s);
+    // The few rows' kernel where a group has up to 8 on average (128 groups by 1536 x 2048, us by it / by pairs of 64 rows: 4 rows a group 67 / 73,
+    // 8: 69 / 73, 16: 76 / 76, and 16 unevenly 104 / 78), and where its tiles are no more than the SMs: pairs take longer to start (16 rows by
+    // 4096 x 4096: 13.7 / 16.7).
+    const long long used = std::min(p.G, p.rows);
+    return p.rows / used <= 8 || ((p.rows - used) / FEW_ROWS + used) * p.NB <= num_sms() ? launch_few<EPI>(p, s) : launch_pairs<EPI>(p, s);
 }
 
 // A row operand in the workspace: codes (room for fp16), then the rows' scales.
