@@ -134,7 +134,7 @@ int moe_router_from_logits(const float* logits, const float* bias, int T, int E,
  *     c_e = d_aux alpha E f_e / T;  softmax: dp = ds + c, d_logits = p (dp - <dp, p>);
  *     sigmoid: d_logits = (ds + (c - <c, q>) / sum s) s (1 - s), q = s / sum s.
  *   An id outside [0, E) counts as none and is reported by moe_check_device_error.
- *   Sizes: T >= 0, E <= 1024, groups <= 32 dividing E, best <= E / groups, 1 <= k <= min(16, top_groups E / groups), scale
+ *   Sizes: 0 <= T <= 2^30, E <= 1024, groups <= 32 dividing E, best <= E / groups, 1 <= k <= min(16, top_groups E / groups), scale
  *   finite. Deterministic. Workspaces 16-byte aligned.
  * ------------------------------------------------------------------------------------------------- */
 enum moe_score { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };

@@ -128,7 +128,8 @@ def test_layers_share_the_scratch(gpu_lib):
 def test_refusals(gpu_lib):
     p, x = parts(8, 64, 16, 64)
     for kw in (dict(experts="int4"), dict(gating="softmax_renorm"), dict(experts="int8", backward=True), dict(checkpoint="int8"),
-               dict(checkpoint="int4", backward=True)):
+               dict(checkpoint="int4", backward=True),
+               dict(checkpoint="int8", backward=True, scratch=torch.empty(1 << 16, dtype=torch.bfloat16))):      # (of the host)
         with pytest.raises(ValueError):
             layer(8, 64, 16, 2, 64, p, **kw)
     for kw in (dict(), dict(experts="int8")):

@@ -30,7 +30,7 @@ def test_refusals_before_any_cuda_call(lib):
     big = 1 << 30
     # logits, bias, T, E, k, groups, top_groups, score, best, renorm, scale, alpha, ids, gates, counts, f, P, aux, ws, bytes, stream
     args = [ok, n, 4, 64, 8, 8, 4, 0, 2, 1, 2.5, 0.01, ok, ok, ok, ok, ok, ok, ok, big, n]
-    for change, want in (({7: 2}, UNS), ({7: -1}, UNS), ({2: -1}, INV), ({3: 0}, INV), ({3: 1088, 5: 17}, INV), ({5: 7}, INV), ({5: 0}, INV),
+    for change, want in (({7: 2}, UNS), ({7: -1}, UNS), ({2: -1}, INV), ({2: (1 << 30) + 1}, INV), ({3: 0}, INV), ({3: 1088, 5: 17}, INV), ({5: 7}, INV), ({5: 0}, INV),
                          ({3: 1024, 5: 64}, INV), ({6: 0}, INV), ({6: 9}, INV), ({8: 0}, INV), ({8: 3}, INV), ({5: 64}, INV),
                          ({4: 0}, INV), ({4: 17, 6: 8}, INV), ({4: 9, 6: 1}, INV), ({10: float("inf")}, INV), ({0: n}, INV),
                          ({12: n}, INV), ({17: n}, INV), ({18: n}, WS), ({18: odd}, WS), ({19: 16}, WS)):
@@ -42,11 +42,21 @@ def test_refusals_before_any_cuda_call(lib):
         call(raw.moe_group_router, args, change, want)
     # logits, ids, d_gates, f, T, E, k, score, renorm, scale, alpha, d_aux, d_logits, stream
     args = [ok, ok, ok, ok, 4, 64, 8, 0, 1, 1.0, 0.01, 1.0, ok, n]
-    for change, want in (({7: 2}, UNS), ({4: -1}, INV), ({5: 1025}, INV), ({6: 0}, INV), ({6: 17}, INV), ({9: float("nan")}, INV), ({0: n}, INV),
+    for change, want in (({7: 2}, UNS), ({4: -1}, INV), ({4: (1 << 30) + 1}, INV), ({5: 1025}, INV), ({6: 0}, INV), ({6: 17}, INV), ({9: float("nan")}, INV), ({0: n}, INV),
                          ({1: n}, INV), ({2: n}, INV), ({3: n}, INV), ({12: n}, INV), ({4: 0, 0: n, 12: n}, lib.MOE_OK)):
         call(raw.moe_group_route_backward, args, change, want)
     assert lib.moe_group_route_workspace_size(16384, 256) > 0
+    assert lib.moe_group_route_workspace_size((1 << 30) + 1, 256) == 0
     assert lib.moe_group_route_workspace_size(-1, 256) == 0 and lib.moe_group_router_workspace_size(4, 0, 64, lib.MOE_BF16) == 0
+
+
+def test_sizes_that_no_int_holds_are_refused(lib):
+    """(ctypes takes a size modulo 2^32: 2^32 + 5 rows would be five.)"""
+    lib._counts(1, (1 << 31) - 1)
+    for n in (1 << 31, (1 << 32) + 5):
+        with pytest.raises(lib.MoEError) as e:
+            lib._counts(4, n)
+        assert e.value.code == lib.MOE_ERR_INVALID_ARG
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])

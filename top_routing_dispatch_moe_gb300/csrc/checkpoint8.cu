@@ -127,7 +127,8 @@ checkpoint_load_kernel(const int8_t* codes, const float* scales, int rows, int C
 // Block b of a row of gu: 128 codes of g, then the 128 of u of the same features, each under its own scale. A lane takes eight
 // features, sixteen lanes a block:
 //   s = 1 / (1 + exp(-g)), act = g s u, d_g = da u s (1 + g (1 - s)), d_u = da g s     (da 0 past F)
-// (The exponential and the quotient are the quick ones, off by about 2^-20: 2^-12 of bf16's half step.)
+// (The exponential and the quotient are the quick ones: s is off by 2^-21 of itself near g = 0 and by 2^-16 at g = -80, a 2^-7th of bf16's
+// half step.)
 __global__ void __launch_bounds__(C_THREADS)
 checkpoint_swiglu_backward_kernel(const int8_t* codes, const float* scales, const __nv_bfloat16* d_act, const int32_t* sched, int E, int rows,
                                   int F, int Fp, __nv_bfloat16* d_gu, __nv_bfloat16* act, unsigned* err) {

@@ -22,6 +22,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kMaxBlocks = 1024;             // rows of the per-block partial sums in the workspace
 constexpr int kMaxK = 16, kMaxGroups = 32, kMaxE = 1024;
+constexpr int kMaxT = 1 << 30;               // (a warp's steps through the tokens stay within an int)
 constexpr float kMasked = -1e30f;
 
 struct Args {
@@ -669,8 +670,8 @@ int launch_gate(Args& a, int* G, cudaStream_t s) {
 
 int check_spec(const char* fn, int T, int E, int k, int groups, int top_groups, int score, int best, float scale) {
     MOE_REQUIRE(score == MOE_SCORE_SIGMOID || score == MOE_SCORE_SOFTMAX, MOE_ERR_UNSUPPORTED, "%s: score %d", fn, score);
-    MOE_REQUIRE(T >= 0 && E >= 1 && E <= kMaxE && groups >= 1 && groups <= kMaxGroups && E % groups == 0, MOE_ERR_INVALID_ARG,
-                "%s: T=%d E=%d groups=%d (need E <= 1024, groups <= 32 of equal size)", fn, T, E, groups);
+    MOE_REQUIRE(T >= 0 && T <= kMaxT && E >= 1 && E <= kMaxE && groups >= 1 && groups <= kMaxGroups && E % groups == 0,
+                MOE_ERR_INVALID_ARG, "%s: T=%d E=%d groups=%d (need T <= 2^30, E <= 1024, groups <= 32 of equal size)", fn, T, E, groups);
     MOE_REQUIRE(top_groups >= 1 && top_groups <= groups && (best == 1 || best == 2) && best <= E / groups, MOE_ERR_INVALID_ARG,
                 "%s: top_groups=%d best=%d of %d groups of %d", fn, top_groups, best, groups, E / groups);
     MOE_REQUIRE(k >= 1 && k <= kMaxK && k <= top_groups * (E / groups), MOE_ERR_INVALID_ARG,
@@ -730,7 +731,7 @@ int check_group_gate(const char* fn, const GroupGate& g) {
 using namespace moe;
 
 extern "C" size_t moe_group_route_workspace_size(int T, int E) {
-    if (T < 0 || E <= 0) return 0;
+    if (T < 0 || T > kMaxT || E <= 0) return 0;
     return group_gate_ws_bytes(T, E);
 }
 

@@ -161,8 +161,8 @@ class MoELayer:
             if checkpoint == "int8":                 # kept in 8 bits: the routed rows', then the shared expert's
                 need = self.checkpoint_scratch(self.rows, F, T if self.shared_packed is not None else 0)
                 scratch = torch.empty(need, dtype=dt, device=dev) if scratch is None else scratch
-                if scratch.dtype != dt or scratch.numel() < need or not scratch.is_contiguous():
-                    raise ValueError(f"scratch: a contiguous {dt} tensor of {need} elements")
+                if scratch.dtype != dt or scratch.numel() < need or not scratch.is_contiguous() or scratch.device != self.y.device:
+                    raise ValueError(f"scratch: a contiguous {dt} tensor of {need} elements on {self.y.device}")
                 flat = scratch.view(-1)
                 gu = [flat[:self.rows * cols].view(self.rows, cols), flat[self.rows * cols:need].view(-1, cols)]
                 self.kept = [(torch.empty((n, cols), dtype=torch.int8, device=dev), torch.empty((n, cols // 128), dtype=f32, device=dev))

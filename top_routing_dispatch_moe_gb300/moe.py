@@ -231,6 +231,12 @@ def moe_sinkhorn_bias(logits, n_iter: int = 16, *, sel_bias=None, ws=None, strea
 
 # ------------------------------------------------------------------------------------- routing by groups
 
+def _counts(*n: int):
+    """Sizes on their way to C ints, which would take them modulo 2^32."""
+    if max(n) > 0x7FFFFFFF:
+        raise MoEError(MOE_ERR_INVALID_ARG, f"a size of {max(n)}")
+
+
 def _score(score: str | int) -> int:
     if isinstance(score, str):
         if score not in SCORE:
@@ -285,6 +291,7 @@ def moe_group_route(logits, bias, k: int, groups: int, top_groups: int, *, score
     if logits.dim() != 2:
         _fp4_fail("logits: [T, E]")
     T, E = logits.shape
+    _counts(T, E)
     f32 = torch.float32
     topk_ids, gates, counts, f, P, aux = _route_outputs(T, E, k, logits, stream, topk_ids, gates, counts, f, P, aux)
     ws = _fp4_bytes(_lib.moe_group_route_workspace_size(T, E), logits, stream) if ws is None else ws
@@ -307,6 +314,7 @@ def moe_group_router(x, w_packed, E: int, bias, k: int, groups: int, top_groups:
     """moe_group_route on the logits of x [T, h] (bf16 or fp32) and the packed router weight (moe_pack_router_weight) of E
     experts; the dict also holds the logits [T, E] (None with want_logits=False, unless given)."""
     T, h = x.shape
+    _counts(T, h, E)
     dt = dtype_code(x.dtype)
     if not x.is_contiguous() or not x.is_cuda:
         _fp4_fail("x: a contiguous device tensor")
@@ -328,6 +336,7 @@ def moe_group_route_backward(logits, topk_ids, d_gates, f, *, score="sigmoid", r
     if logits.dim() != 2 or topk_ids.dim() != 2 or topk_ids.shape[0] != logits.shape[0]:
         _fp4_fail("logits: [T, E], topk_ids: [T, k]")
     (T, E), k = logits.shape, topk_ids.shape[1]
+    _counts(T, E, k)
     d_logits = _fp4_empty((T, E), torch.float32, logits, stream) if d_logits is None else d_logits
     _check(_lib.moe_group_route_backward(_fp4_data(logits, T * E, torch.float32, "logits"),
                                          _fp4_data(topk_ids, T * k, torch.int32, "topk_ids"),
@@ -1071,6 +1080,7 @@ def moe_int8_quantize(x, *, src=None, codes=None, scales=None, stream=None):
     its output channels."""
     K, ldx = x.shape[-1], _fp4_rows(x, "x")
     rows = x.shape[0] if src is None else src.numel()
+    _counts(rows, x.shape[0], K)
     codes = _fp4_empty((rows, K), torch.int8, x, stream) if codes is None else codes
     scales = _fp4_empty((rows,), torch.float32, x, stream) if scales is None else scales
     _check(_lib.moe_int8_quantize(x.data_ptr(), ldx, x.shape[0], _fp4_data(src, 0, torch.int32, "src"), rows, K, _fp4_dtype(x.dtype),
@@ -1084,6 +1094,7 @@ def moe_int8_dequantize(codes, scales, *, dtype=torch.bfloat16, out=None, stream
     if codes.dim() != 2:
         _fp4_fail("codes: [rows, K]")
     rows, K = codes.shape
+    _counts(rows, K)
     out = _fp4_empty((rows, K), dtype, codes, stream) if out is None else out
     ldo = _fp4_rows(out, "out")
     if out.shape != codes.shape:
@@ -1108,6 +1119,7 @@ def moe_int8_pack_weight(codes, packed=None, stream=None):
     if codes.dim() != 3:
         _fp4_fail("codes: [G, N, K]")
     G, N, K = codes.shape
+    _counts(G, N, K)
     need = _int8_weight_bytes(G, N, K)
     packed = _fp4_bytes(need, codes, stream) if packed is None else packed
     _check(_lib.moe_int8_pack_weight(_fp4_data(codes, G * N * K, torch.int8, "codes"), G, N, K,
@@ -1135,6 +1147,7 @@ def moe_int8_linear(x, offsets, packed, scales, *, src=None, tile_sched=None, ou
     if scales.dim() != 2 or (offsets is not None and offsets.numel() != scales.shape[0] + 1):
         _fp4_fail("scales: [G, N], offsets: [G + 1]")
     G, N = scales.shape
+    _counts(rows, x.shape[0], K, G, N)
     out = _fp4_empty((rows, N), out_dtype or x.dtype, x, stream) if out is None else out
     ldo = _fp4_rows(out, "out")
     if out.shape[0] != rows or out.shape[1] != N:
@@ -1153,6 +1166,7 @@ def moe_int8_pack_expert_weights(gate, up, down, packed=None, stream=None):
     if gate.dim() != 3 or up.shape != gate.shape or down.shape != (gate.shape[0], gate.shape[2], gate.shape[1]):
         _fp4_fail("gate, up: [E, F, h], down: [E, h, F]")
     E, F, h = gate.shape
+    _counts(E, F, h)
     need = _int8_experts_bytes(E, h, F)
     packed = _fp4_bytes(need, gate, stream) if packed is None else packed
     _check(_lib.moe_int8_pack_expert_weights(*(_fp4_data(c, E * F * h, torch.int8, what) for c, what in ((gate, "gate"), (up, "up"), (down, "down"))),
@@ -1174,6 +1188,7 @@ def moe_int8_expert_ffn(x, offsets, packed, gate_scales, up_scales, down_scales,
     if gate_scales.dim() != 2 or (offsets is not None and offsets.numel() != gate_scales.shape[0] + 1):
         _fp4_fail("gate_scales: [E, F], offsets: [E + 1]")
     E, F = gate_scales.shape
+    _counts(rows, x.shape[0], h, E, F)
     out = _fp4_empty((rows, h), out_dtype or x.dtype, x, stream) if out is None else out
     ldo = _fp4_rows(out, "out")
     if out.shape[0] != rows or out.shape[1] != h:
@@ -1195,6 +1210,7 @@ def moe_checkpoint8_save(x, *, tile_sched=None, E: int = 0, codes=None, scales=N
     """x [rows, C] (bf16, fp16 or fp32, row stride free) -> (codes int8 [rows, C], scales fp32 [rows, ceil(C / 128)]): what a forward
     keeps for its backward. With tile_sched (moe_dispatch's) of E experts only its rows."""
     (rows, C), ldx = x.shape, _fp4_rows(x, "x")
+    _counts(rows, C)
     nb = (C + 127) // 128
     codes = _fp4_empty((rows, C), torch.int8, x, stream) if codes is None else codes
     scales = _fp4_empty((rows, nb), torch.float32, x, stream) if scales is None else scales
@@ -1209,6 +1225,7 @@ def moe_checkpoint8_load(codes, scales, *, dtype=torch.bfloat16, out=None, strea
     if codes.dim() != 2:
         _fp4_fail("codes: [rows, C]")
     rows, C = codes.shape
+    _counts(rows, C)
     out = _fp4_empty((rows, C), dtype, codes, stream) if out is None else out
     ldo = _fp4_rows(out, "out")
     if out.shape != codes.shape:
@@ -1224,6 +1241,7 @@ def _checkpoint8_data(codes, scales, d_act):
     if codes.dim() != 2 or d_act.dim() != 2 or codes.shape != (d_act.shape[0], gu_cols(d_act.shape[1])):
         _fp4_fail("codes: [rows, gu_cols(F)], d_act: [rows, F]")
     rows, F = d_act.shape
+    _counts(rows, F)
     return rows, F, (_fp4_data(codes, codes.numel(), torch.int8, "codes"),
                      _fp4_data(scales, codes.numel() // 128, torch.float32, "scales"), _fp4_data(d_act, rows * F, torch.bfloat16, "d_act"))
 
