@@ -463,3 +463,48 @@ def test_no_rows_and_groups_without_rows(gpu_lib):
     y = gpu_lib.moe_int8_linear(data((0, 64)), dev([0, 2, 4, 5, 7]), packed, ws, src=none)
     ok(gpu_lib)
     assert (y == 0).all()
+
+
+# few rows a group, one SM's worth of tiles, and every tile of pairs: 64, 128 and 256 rows
+@pytest.mark.parametrize("x_rows,rows,G,N,K", [(1, 5, 3, 40, 64), (7, 100, 20, 130, 200), (64, 512, 33, 257, 1044), (33, 700, 2, 520, 96),
+                                               (200, 6000, 64, 384, 160), (100, 12000, 64, 384, 64), (500, 3000, 5, 700, 320),
+                                               (2999, 3000, 3, 700, 70)])
+def test_rows_that_several_of_the_call_name(gpu_lib, x_rows, rows, G, N, K):
+    """x quantised once and its rows fetched by src: bit for bit the call on the rows written out, -1 among them."""
+    w, ws = weight(G, N, K, 3)
+    packed = gpu_lib.moe_int8_pack_weight(w)
+    gen = np.random.default_rng(rows)
+    src = gen.integers(-1, x_rows, rows).astype(np.int32)
+    src[gen.integers(rows)] = x_rows - 1
+    off = dev(offsets_of(rows, G, rows))
+    for dtype, wide in (("bf16", False), ("fp32", True)):
+        x = data((x_rows, K + 8), dtype, 2)[:, :K] if wide else data((x_rows, K), dtype, 2)
+        whole = torch.where(dev(src)[:, None] < 0, torch.zeros((), dtype=x.dtype, device="cuda"), x[dev(src).clamp(min=0).long()])
+        got = gpu_lib.moe_int8_linear(x, off, packed, ws, src=dev(src))
+        want = gpu_lib.moe_int8_linear(whole, off, packed, ws)
+        ok(gpu_lib)
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("rows", [20, 600, 6000])
+def test_a_wrong_row_among_those_named(gpu_lib, rows):
+    """Reported and taken as zeros; a row with an infinity is NaN wherever it is named, and nowhere else."""
+    G, N, K, x_rows = 6, 200, 128, 10
+    w, ws = weight(G, N, K, 4)
+    packed = gpu_lib.moe_int8_pack_weight(w)
+    x = data((x_rows, K), "bf16", 5)
+    x[3, 17] = float("inf")
+    src = torch.arange(rows, dtype=torch.int32, device="cuda") % x_rows
+    off = dev(offsets_of(rows, G, 6))
+    y = gpu_lib.moe_int8_linear(x, off, packed, ws, src=src)
+    ok(gpu_lib)
+    assert torch.equal(torch.isnan(y).any(1), src == 3) and torch.equal(torch.isnan(y).all(1), src == 3)
+    for bad in (x_rows, -2, 2**31 - 1, -(2**31)):
+        other = src.clone()
+        other[rows // 2] = bad
+        z = gpu_lib.moe_int8_linear(x, off, packed, ws, src=other)
+        torch.cuda.synchronize()
+        assert gpu_lib.moe_check_device_error() == gpu_lib.MOE_ERR_INVALID_ARG
+        assert (z[rows // 2] == 0).all()
+        z[rows // 2] = y[rows // 2]
+        assert torch.equal(z.nan_to_num(), y.nan_to_num())

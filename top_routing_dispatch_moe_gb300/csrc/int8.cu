@@ -17,9 +17,9 @@ constexpr int HELD = 4;              // such pieces that a warp holds
 // Piece `c` of a row (columns 512 c ..): VEC: this lane's 16 consecutive columns; else (the row starts on no 16-byte boundary, or its
 // end cuts a unit) every 32nd column from the lane's own, so that loads and stores of a warp stay together.
 template <typename T, bool VEC>
-__device__ __forceinline__ Raw16<T> load_piece(const T* row, int c, int K) {
+__device__ __forceinline__ Raw16<T> load_piece(const T* row, int c, int K, bool again) {
     const int lane = threadIdx.x & 31;
-    if constexpr (VEC) return load_unit<T, true>(row, c * SEG + lane * UNIT, K);
+    if constexpr (VEC) return load_unit<T, true>(row, c * SEG + lane * UNIT, K, again);
     Raw16<T> r;
     T* e = reinterpret_cast<T*>(r.q);
 #pragma unroll
@@ -81,18 +81,18 @@ quantize_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, int r
     }
     const T* xr = x + (long long)max(from, 0) * ldx;
     const int k_in = from >= 0 ? K : 0, pieces = (width + SEG - 1) / SEG;
-    const bool held = pieces <= HELD * WPR;
+    const bool held = pieces <= HELD * WPR, again = src != nullptr;
     Raw16<T> raw[HELD];
     float amax = 0.f;
     if (held) {
 #pragma unroll
         for (int i = 0; i < HELD; ++i)
-            if (i * WPR + w < pieces) raw[i] = load_piece<T, VEC>(xr, i * WPR + w, k_in);
+            if (i * WPR + w < pieces) raw[i] = load_piece<T, VEC>(xr, i * WPR + w, k_in, again);
 #pragma unroll
         for (int i = 0; i < HELD; ++i)
             if (i * WPR + w < pieces) amax = max_nan(amax, unit_amax(raw[i]));
     } else {
-        for (int c = w; c < pieces; c += WPR) amax = max_nan(amax, unit_amax(load_piece<T, VEC>(xr, c, k_in)));
+        for (int c = w; c < pieces; c += WPR) amax = max_nan(amax, unit_amax(load_piece<T, VEC>(xr, c, k_in, again)));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -113,7 +113,7 @@ quantize_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, int r
             if (i * WPR + w < pieces) store_piece<T, FORM, VEC>(raw[i], codes, base, i * WPR + w, width, st);
     } else {
         for (int c = w; c < pieces; c += WPR)
-            store_piece<T, FORM, VEC>(load_piece<T, VEC>(xr, c, k_in), codes, base, c, width, st);
+            store_piece<T, FORM, VEC>(load_piece<T, VEC>(xr, c, k_in, again), codes, base, c, width, st);
     }
 }
 

@@ -75,10 +75,16 @@ __device__ __forceinline__ void st32(void* p, const uint4* d) {
 
 // Columns [k0, k0 + 16) of a row as stored, zero past K. VEC: the row starts on 16 bytes. The caller's lanes of one warp
 // hold consecutive units of the same row in the other case too, where the elements are fetched one by one.
+// again: other rows of the call are the same one, which is to stay in L2 (16384 x 2048 bf16 read eight times over: 121 -> 107 us).
 template <typename T, bool VEC>
-__device__ __forceinline__ Raw16<T> load_unit(const T* row, int k0, int K) {
+__device__ __forceinline__ Raw16<T> load_unit(const T* row, int k0, int K, bool again = false) {
     Raw16<T> r;
     if (VEC && k0 + UNIT <= K) {
+        if (again) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T); ++i) r.q[i] = reinterpret_cast<const uint4*>(row + k0)[i];
+            return r;
+        }
         if (sizeof(T) == 4 && (reinterpret_cast<uintptr_t>(row) & 31u) == 0) {
 #pragma unroll
             for (int i = 0; i < (int)sizeof(T); i += 2) ld32(r.q + i, reinterpret_cast<const uint4*>(row + k0) + i);
