@@ -27,7 +27,7 @@ class MoELayer:
     bf16 the shared expert runs inside the "up_gate" and "down" launches; the two shared stages exist for fp32.
     forward(x, events=...) records one CUDA event before the first stage and after each stage when given
     a dict of lists, so callers can time the stages on the launching stream. forward(x, save=True) (a layer built
-    with backward=True, bf16 token-choice or Sinkhorn routing, bf16 payload) also keeps the experts'
+    with backward=True, bf16 token-choice, group or Sinkhorn routing, bf16 payload) also keeps the experts'
     pre-activations g and u, so that the next backward() needs no recompute of the up/gate GEMM.
 
     experts="nvfp4" or "mxfp4" (bf16, forward only) holds the experts in 4 bits: the weights are quantised at construction
@@ -220,8 +220,8 @@ class MoELayer:
     def forward(self, x, stream=None, events=None, y=None, save=False):
         if save and (self.packed_bwd is None or self.routing not in ("token", "sinkhorn", "group")
                      or self.dtype != torch.bfloat16 or self.payload != "bf16"):
-            raise NotImplementedError("MoELayer.forward(save=True): a layer built with backward=True, token-choice or "
-                                      "Sinkhorn routing in bf16 with the bf16 send buffer")
+            raise NotImplementedError("MoELayer.forward(save=True): a layer built with backward=True, token-choice, "
+                                      "group or Sinkhorn routing in bf16 with the bf16 send buffer")
 
         def mark(stage):
             if events is not None:
@@ -341,7 +341,7 @@ class MoELayer:
     def backward(self, x, dy, d_aux=1.0, stream=None, events=None):
         """Gradients of <dy, y> + d_aux * aux for the last forward(x): returns dict(dx, dW_r, d_bias, dW_gate,
         dW_up, dW_down[, shared_dW_gate, shared_dW_up, shared_dW_down]); weight gradients fp32, dx in the
-        layer's dtype. Token-choice or Sinkhorn routing, bf16, and a layer built with backward=True. Order of the calls:
+        layer's dtype. Token-choice, group or Sinkhorn routing, bf16, and a layer built with backward=True. Order of the calls:
         combine, expert down / up-gate dgrad, expert weight gradients, [shared expert], router, router weight,
         dispatch (+ the router and shared terms of dx). `events` as in forward (stages "combine_bwd",
         "expert_dgrad", "expert_wgrad", ["shared_bwd"], "router_bwd", "dispatch_bwd")."""
