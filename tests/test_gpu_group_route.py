@@ -194,3 +194,19 @@ def test_many_ties_of_few_values(gpu_lib):
                     ok(gpu_lib)
                     want = O.route(L.double().numpy(), None if b is None else b.numpy(), 6, groups, 3, score, best, True, 1.0)
                     np.testing.assert_array_equal(r["topk_ids"].cpu().numpy(), want["ids"])
+
+
+@pytest.mark.parametrize("E", [4, 64])
+def test_large_biases_that_cancel_in_a_groups_score(gpu_lib, E):
+    """The first group's two best scores are near 1000 and -1000, where fp32 steps by 6e-5, and their sum is near 1: in 32 bits it is
+    1 + 6e-5, above the other group's 1 + 4e-5, and exactly it is 1 + 3e-5, below."""
+    per = E // 2
+    L = np.full((3, E), -1.0, np.float32)
+    bias = np.full(E, -2000.0, np.float32)
+    L[:, 0], L[:, 1], L[:, per], L[:, per + 1] = 1.28e-4, 0.0, 1.6e-4, 0.0
+    bias[[0, 1, per, per + 1]] = 1000.0, -1000.0, 0.0, 0.0
+    want = O.route(L.astype(np.float64), bias.astype(np.float64), 2, 2, 1, "sigmoid", 2, True, 1.0)
+    assert (want["ids"] >= per).all()
+    r = gpu_lib.moe_group_route(torch.from_numpy(L).cuda(), torch.from_numpy(bias).cuda(), 2, 2, 1)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(r["topk_ids"].cpu().numpy(), want["ids"])

@@ -147,6 +147,67 @@ __device__ __noinline__ unsigned groups_exact(const Args& a, const float* L, lon
     return __ballot_sync(0xffffffffu, lane < a.groups && rank < a.top_groups);
 }
 
+struct Candidate { float l, bias; int e, pad; };
+
+// The same where a group is a run of lanes and this lane's group has the score gs in 32 bits, t1 and t2 the largest of its selection
+// scores v: only the groups with scores in [lo, hi] may stay or not (what is above stays: fewer than top_groups scores can be above its
+// own; what is below does not), and of those only the experts within tol of the ones that count are looked at, one to a lane. list: 32 of
+// the warp's own. (Every expert in 64 bits, eight to a lane: 4 us of a call's 33.)
+__device__ __noinline__ unsigned groups_near(const Args& a, const float* L, const float* v, Candidate* list, float gs, float t1, float t2,
+                                             float lo, float hi, float tol) {
+    const int lane = threadIdx.x & 31, npl = a.npl, e0 = lane * npl, g = lane / a.lpg;
+    const bool is = g < a.groups, first = is && lane == g * a.lpg, near = is && gs >= lo && gs <= hi;
+    const unsigned near_at = __ballot_sync(0xffffffffu, first && near), above_at = __ballot_sync(0xffffffffu, first && gs > hi);
+    unsigned mine = 0u;                      // slots of this lane
+    const float least = (a.best == 2 ? t2 : t1) - tol;
+#pragma unroll 1
+    for (int i = 0; i < npl; ++i)
+        if (near && e0 + i < a.E && v[i] >= least) mine |= 1u << i;
+    int at = __popc(mine);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += n;
+    }
+    const int n = __shfl_sync(0xffffffffu, at, 31);
+    if (n > 32) {
+        long long sel[32];
+        return groups_exact(a, L, sel);
+    }
+    for (at -= __popc(mine); mine; mine &= mine - 1, ++at) {
+        const int i = __ffs(mine) - 1;
+        list[at] = Candidate{L[i], a.bias ? a.bias[e0 + i] : 0.f, e0 + i, 0};
+    }
+    const Norm norm = a.sigmoid ? Norm{0.0, 0.0} : exact_norm(L, npl);
+    __syncwarp();
+    long long x = kLeast, b1 = kLeast, b2 = kLeast;       // lane j: candidate j; lane g: the best of group g
+    int of = -1;
+    if (lane < n) {
+        x = order_of(exact_sel(list[lane].l, list[lane].bias, norm.m, norm.z));
+        of = list[lane].e / a.per;
+    }
+    __syncwarp();
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+        const long long o = __shfl_sync(0xffffffffu, x, j);
+        if (__shfl_sync(0xffffffffu, of, j) == lane) {
+            b2 = max(b2, min(b1, o));
+            b1 = max(b1, o);
+        }
+    }
+    const int at_lane = min(lane * a.lpg, 31);
+    const bool nearg = lane < a.groups && (near_at >> at_lane & 1u), aboveg = lane < a.groups && (above_at >> at_lane & 1u);
+    const long long score = nearg ? (a.best == 2 ? order_of(of_order(b1) + of_order(b2)) : b1) : kLeast;
+    int rank = 0;
+#pragma unroll 1
+    for (unsigned left = __ballot_sync(0xffffffffu, nearg); left; left &= left - 1) {
+        const int j = __ffs(left) - 1;
+        const long long o = __shfl_sync(0xffffffffu, score, j);
+        rank += o > score || (o == score && j < lane);
+    }
+    return __ballot_sync(0xffffffffu, aboveg || (nearg && rank < a.top_groups - __popc(above_at)));
+}
+
 // The whole choice in 64 bits; returns lane j's choice j.
 __device__ __noinline__ int choose_exact(const Args& a, const float* L) {
     const int lane = threadIdx.x & 31, npl = a.npl, e0 = lane * npl;
@@ -180,7 +241,7 @@ __device__ __noinline__ int choose_exact(const Args& a, const float* L) {
 
 // The order of n candidates, lane j's being expert `id` with logit l, where only neighbours among them may be exchanged: a lane computes
 // its own score. Returns lane j's expert after ordering.
-__device__ __noinline__ int order_exact(const Args& a, const float* L, float l, int id, int n) {
+__device__ __noinline__ int order_exact(const Args& a, const float* L, Candidate* list, float l, int id, int n) {
     const int lane = threadIdx.x & 31;
     long long v = kLeast;
     if (a.bias) {
@@ -190,18 +251,17 @@ __device__ __noinline__ int order_exact(const Args& a, const float* L, float l, 
         v = order_of(l > -INFINITY ? (double)l : (double)kMasked);
     }
     __syncwarp();
-    int rank = 0, out = id;
-#pragma unroll 1
+    int rank = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) {
         const long long o = __shfl_sync(0xffffffffu, v, j);
         const int oi = __shfl_sync(0xffffffffu, id, j);
         rank += o > v || (o == v && oi < id);
     }
-#pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-        const int r = __shfl_sync(0xffffffffu, rank, j), oi = __shfl_sync(0xffffffffu, id, j);
-        if (lane == r) out = oi;
-    }
+    if (lane < n) list[rank].e = id;
+    __syncwarp();
+    const int out = lane < n ? list[lane].e : id;
+    __syncwarp();
     return out;
 }
 
@@ -250,6 +310,7 @@ group_gate_kernel(const __grid_constant__ Args a) {
     constexpr int SB = NPL == 1 ? 0 : NPL == 2 ? 1 : NPL <= 4 ? 2 : NPL <= 8 ? 3 : NPL <= 16 ? 4 : 5;     // bits of a slot
     constexpr unsigned SLOT = (1u << SB) - 1;
     extern __shared__ __align__(16) unsigned char smem_raw[];
+    __shared__ __align__(16) Candidate s_list[kWarps][32];
     float* s_P = reinterpret_cast<float*>(smem_raw);                   // [warps][E]; a warp's row holds its selection scores before
     int* s_hist = reinterpret_cast<int*>(s_P + (size_t)kWarps * a.E);
     pdl_wait();
@@ -260,12 +321,14 @@ group_gate_kernel(const __grid_constant__ Args a) {
     const int npl = FULL ? NPL : a.npl, e0 = lane * npl;
     auto live = [&](int i) { return FULL || (i < npl && e0 + i < a.E); };
     float* row = s_P + (size_t)warp * a.E;
-    float Pacc[NPL], bias[NPL];
+    float Pacc[NPL], bias[NPL], most = 0.f;  // most: the largest magnitude of the bias
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         Pacc[i] = 0.f;
         bias[i] = a.bias && live(i) ? a.bias[e0 + i] : 0.f;
+        most = fmaxf(most, fabsf(bias[i]));
     }
+    if (a.bias) most = warp_max(most);
     for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
         float L[NPL], s[NPL];                                        // logits, scores
         const float* src = a.logits + (size_t)t * a.E;
@@ -373,9 +436,11 @@ group_gate_kernel(const __grid_constant__ Args a) {
             bool stays = is && rank < a.top_groups;
             const float x = value_of(__reduce_min_sync(0xffffffffu, stays ? key_of(gs) : 0xffffffffu)),
                         y = value_of(__reduce_max_sync(0xffffffffu, is && !stays ? key_of(gs) : 0u));
-            // the last that stays and the first that does not: two scores' errors each, and the roundings of the sums. Without a bias the
-            // errors are relative to the scores (softmax: one unit of the exponent's rounding for each of the logits' distance).
-            const float tol = a.bias ? 4.f * serr + 2.5e-7f * (fabsf(x) + fabsf(y)) : (a.sigmoid ? 1e-6f : 4e-6f) * (x + y);
+            // the last that stays and the first that does not: two scores' errors each, and the roundings of their sums with the bias (which
+            // may leave a small sum of large terms) and of the groups'. Without a bias the errors are relative to the scores
+            // (softmax: one unit of the exponent's rounding for each of the logits' distance).
+            const float tol = a.bias ? 4.f * (serr + 7e-8f * (1.f + most)) + 1.3e-7f * (fabsf(x) + fabsf(y))
+                                     : (a.sigmoid ? 1e-6f : 4e-6f) * (x + y);
             // (groups without a live expert, or with one less than `best`, have whole multiples of the masked score: equal)
             bool undecided = !(x - y > tol) && x > 0.1f * kMasked;
             if (undecided && (FULL || a.lpg) && x == y) {
@@ -390,11 +455,18 @@ group_gate_kernel(const __grid_constant__ Args a) {
             }
             unsigned kept = 0u;
             if (undecided) {
-                long long sel[32];
-                float l[NPL];                 // (a copy: the logits themselves stay in registers)
+                float l[NPL], v[NPL];         // (copies: what they are of stays in registers)
 #pragma unroll
-                for (int i = 0; i < NPL; ++i) l[i] = L[i];
-                kept = groups_exact(a, l, sel);
+                for (int i = 0; i < NPL; ++i) {
+                    l[i] = L[i];
+                    v[i] = L[i] > -INFINITY ? s[i] + bias[i] : kMasked;
+                }
+                if (FULL || a.lpg) {
+                    kept = groups_near(a, l, v, s_list[warp], gs, t1, t2, y - tol, x + tol, tol);
+                } else {
+                    long long sel[32];
+                    kept = groups_exact(a, l, sel);
+                }
                 stays = is && (kept >> g & 1u);
             } else if (!FULL && !a.lpg) {
                 kept = __ballot_sync(0xffffffffu, stays);
@@ -461,7 +533,7 @@ group_gate_kernel(const __grid_constant__ Args a) {
                 for (int i = 0; i < NPL; ++i) l[i] = L[i];
                 my_id = id_of();
                 if (lane < n) my_l = logit_of(my_id);
-                my_id = more && n < left ? choose_exact(a, l) : order_exact(a, l, my_l, my_id, n);
+                my_id = more && n < left ? choose_exact(a, l) : order_exact(a, l, s_list[warp], my_l, my_id, n);
                 if (lane < a.k) my_l = logit_of(my_id);
             }
         }
