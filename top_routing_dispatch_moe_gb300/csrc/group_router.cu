@@ -518,9 +518,27 @@ group_gate_kernel(const __grid_constant__ Args a) {
             const float b = a.bias && lane < n ? a.bias[my_id] : 0.f;
             const float nl = __shfl_down_sync(0xffffffffu, my_l, 1), nb = __shfl_down_sync(0xffffffffu, b, 1);
             const unsigned bad = __ballot_sync(0xffffffffu, close && !(nl == my_l && nb == b));
-            if (bad) {
+            // what is left out may be above something chosen: if the first left out is near the last chosen, unless all that are
+            // near one another about there (those before the last from the first gap on; any after it) are equal
+            const unsigned chosen = (2u << (a.k - 1)) - 1u, near_bits = __ballot_sync(0xffffffffu, close);
+            const bool border = (near_bits >> (a.k - 1) & 1u) != 0;
+            const unsigned gaps = ~near_bits & chosen, run = gaps ? chosen & ~((2u << (31 - __clz(gaps))) - 1u) : chosen;
+            bool more = border && (bad & run) != 0;
+            if (border && !more) {
+                const unsigned last = __shfl_sync(0xffffffffu, my_key, a.k - 1);
+                const float ll = __shfl_sync(0xffffffffu, my_l, a.k - 1), lb = __shfl_sync(0xffffffffu, b, a.k - 1);
+                float l[NPL];
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) l[i] = L[i];
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) {
+                    const int slot = (int)(SLOT - (key[i] & SLOT));
+                    if (key[i] && near(last, key[i])) more = more || l[slot] != ll || (a.bias && a.bias[e0 + slot] != lb);
+                }
+                more = __any_sync(0xffffffffu, more);
+            }
+            if (bad || more) {
                 // candidates until a clear distance, if one is within the warp's lanes
-                bool more = (bad >> (a.k - 1) & 1u) != 0;         // the first that is left out is near the last chosen
                 unsigned last = __shfl_sync(0xffffffffu, my_key, n - 1);
                 while (more && n < min(left, 32)) {
                     const unsigned got = take(n);
