@@ -26,7 +26,9 @@ def route(L, bias, k, groups, top_groups, score, best, renorm, scale, alpha=0.01
     gates = np.zeros((T, k))
     for t in range(T):
         per = E // groups
-        g = [sum(sorted(sel[t, i * per:(i + 1) * per], reverse=True)[:best]) for i in range(groups)]
+        with np.errstate(invalid="ignore"):      # (opposite infinities of the bias: a masked group)
+            g = [sum(sorted(sel[t, i * per:(i + 1) * per], reverse=True)[:best]) for i in range(groups)]
+        g = [MASKED if np.isnan(v) else v for v in g]
         kept = sorted(range(groups), key=lambda i: (-g[i], i))[:top_groups]
         cand = [e for i in kept for e in range(i * per, (i + 1) * per)]
         ids[t] = sorted(cand, key=lambda e: (-rank[t, e], e))[:k]

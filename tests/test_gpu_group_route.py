@@ -232,3 +232,19 @@ def test_near_ties_in_every_token(gpu_lib, E, groups, top_groups, k):
                 ok(gpu_lib)
                 want = O.route(L.double().numpy(), b.double().numpy() if spread else None, k, groups, top_groups, score, best, True, 1.0)
                 np.testing.assert_array_equal(r["topk_ids"].cpu().numpy(), want["ids"])
+
+
+def test_infinite_biases_choose_and_exclude(gpu_lib):
+    """+inf: chosen whatever its score, groups of two such by index; -inf: behind all others; a sum of both: as masked."""
+    L = logits_of(70, 64, 9)
+    b = bias_of(64, 10)
+    for plus, minus in (([5], []), ([5, 9, 20, 21, 40, 41, 56, 63], []), ([], list(range(8, 24))), ([3, 33], [0, 1, 60]),
+                        (list(range(0, 64, 8)), [e for e in range(64) if e % 8]),            # +inf and -inf: every group's sum
+                        ([0, 8, 16, 24, 32, 40], [e for e in range(48) if e % 8])):          # and of all but two
+        bias = b.clone()
+        bias[plus], bias[minus] = float("inf"), -float("inf")
+        for best in (1, 2):
+            r = gpu_lib.moe_group_route(L.cuda(), bias.cuda(), 6, 8, 3, best=best)
+            ok(gpu_lib)
+            want = O.route(L.double().numpy(), bias.double().numpy(), 6, 8, 3, "sigmoid", best, True, 1.0)
+            np.testing.assert_array_equal(r["topk_ids"].cpu().numpy(), want["ids"])

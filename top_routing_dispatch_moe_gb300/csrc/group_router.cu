@@ -68,6 +68,11 @@ __device__ __forceinline__ long long order_of(double v) {
 }
 __device__ __forceinline__ double of_order(long long b) { return __longlong_as_double(b >= 0 ? b : b ^ 0x7fffffffffffffffLL); }
 constexpr long long kLeast = -0x7fffffffffffffffLL - 1;
+// The order of a group's score, the sum of the scores in these two places; opposite infinities: as masked.
+__device__ __forceinline__ long long order_of_sum(long long b1, long long b2) {
+    const double v = of_order(b1) + of_order(b2);
+    return order_of(v == v ? v : (double)kMasked);
+}
 
 struct Norm { double m, z; };
 __device__ __noinline__ Norm exact_norm(const float* L, int npl) {
@@ -117,7 +122,7 @@ __device__ __noinline__ unsigned groups_exact(const Args& a, const float* L, lon
             t2 = max(min(t1, b1), max(t2, b2));
             t1 = max(t1, b1);
         }
-        const long long v = a.best == 2 ? order_of(of_order(t1) + of_order(t2)) : t1;
+        const long long v = a.best == 2 ? order_of_sum(t1, t2) : t1;
         gscore = __shfl_sync(0xffffffffu, v, min(lane * a.lpg, 31));
         if (lane >= a.groups) gscore = kLeast;
     } else
@@ -136,7 +141,7 @@ __device__ __noinline__ unsigned groups_exact(const Args& a, const float* L, lon
             t2 = max(min(t1, b1), max(t2, b2));
             t1 = max(t1, b1);
         }
-        if (lane == g) gscore = a.best == 2 ? order_of(of_order(t1) + of_order(t2)) : t1;
+        if (lane == g) gscore = a.best == 2 ? order_of_sum(t1, t2) : t1;
     }
     int rank = 0;
 #pragma unroll 1
@@ -197,7 +202,7 @@ __device__ __noinline__ unsigned groups_near(const Args& a, const float* L, cons
     }
     const int at_lane = min(lane * a.lpg, 31);
     const bool nearg = lane < a.groups && (near_at >> at_lane & 1u), aboveg = lane < a.groups && (above_at >> at_lane & 1u);
-    const long long score = nearg ? (a.best == 2 ? order_of(of_order(b1) + of_order(b2)) : b1) : kLeast;
+    const long long score = nearg ? (a.best == 2 ? order_of_sum(b1, b2) : b1) : kLeast;
     int rank = 0;
 #pragma unroll 1
     for (unsigned left = __ballot_sync(0xffffffffu, nearg); left; left &= left - 1) {
@@ -258,6 +263,8 @@ __device__ __noinline__ int order_exact(const Args& a, const float* L, Candidate
         const int oi = __shfl_sync(0xffffffffu, id, j);
         rank += o > v || (o == v && oi < id);
     }
+    list[lane].e = id;                       // (candidates are different, and ranks a permutation)
+    __syncwarp();
     if (lane < n) list[rank].e = id;
     __syncwarp();
     const int out = lane < n ? list[lane].e : id;
@@ -301,8 +308,10 @@ __device__ __forceinline__ void sort_keys(unsigned (&key)[N]) {
 // k rounds compare the lanes' heads without those bits: equal ones go to the lowest lane, and within a lane to the lowest slot. What
 // the missing bits, and the roundings of the scores, may have confused is found afterwards from the chosen keys' differences, each lane
 // looking at one, and put right in 64 bits.
-// (16384 tokens by 256 experts, k 8 of 4 of 8 groups; an argmax over unsorted slots in every round, with libm's exponential and
-// division, took 45 us of scores and rounds; the whole choice in 64 bits 50 us for the one token of some thousands that needs it.)
+// (16384 tokens by 256 experts, k 8 of 4 of 8 groups: 29 us with the finalize, 2 of them for the tokens that 64 bits decide; bound by
+// instructions, 850 a token. An argmax over unsorted slots in every round, with libm's exponential and division, took 45 us of
+// scores and rounds; the whole choice in 64 bits 50 us for the one token of some thousands that needs it. Two or four blocks an SM
+// instead of three: 30 and 31 us.)
 // FULL: E = 32 NPL, and a group a run of lanes whose number is a power of two.
 template <int NPL, bool FULL>
 __global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 3 : NPL == 16 ? 2 : 1)
@@ -321,12 +330,12 @@ group_gate_kernel(const __grid_constant__ Args a) {
     const int npl = FULL ? NPL : a.npl, e0 = lane * npl;
     auto live = [&](int i) { return FULL || (i < npl && e0 + i < a.E); };
     float* row = s_P + (size_t)warp * a.E;
-    float Pacc[NPL], bias[NPL], most = 0.f;  // most: the largest magnitude of the bias
+    float Pacc[NPL], bias[NPL], most = 0.f;  // most: the largest finite magnitude of the bias
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         Pacc[i] = 0.f;
         bias[i] = a.bias && live(i) ? a.bias[e0 + i] : 0.f;
-        most = fmaxf(most, fabsf(bias[i]));
+        if (fabsf(bias[i]) < INFINITY) most = fmaxf(most, fabsf(bias[i]));
     }
     if (a.bias) most = warp_max(most);
     for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
@@ -426,7 +435,7 @@ group_gate_kernel(const __grid_constant__ Args a) {
                     }
                 __syncwarp();
             }
-            const float gs = a.best == 2 ? t1 + t2 : t1;
+            const float two = t1 + t2, gs = a.best == 1 ? t1 : two == two ? two : kMasked;      // (opposite infinities: as masked)
             int rank = 0;
             for (int o = 0; o < a.groups; ++o) {
                 const float v = __shfl_sync(0xffffffffu, gs, FULL ? o << a.lpg_log : a.lpg ? o * a.lpg : o);
@@ -439,7 +448,8 @@ group_gate_kernel(const __grid_constant__ Args a) {
             // the last that stays and the first that does not: two scores' errors each, and the roundings of their sums with the bias (which
             // may leave a small sum of large terms) and of the groups'. Without a bias the errors are relative to the scores
             // (softmax: one unit of the exponent's rounding for each of the logits' distance).
-            const float tol = a.bias ? 4.f * (serr + 7e-8f * (1.f + most)) + 1.3e-7f * (fabsf(x) + fabsf(y))
+            // (Finite: infinite sums are equal, and above all others.)
+            const float tol = a.bias ? fminf(4.f * (serr + 7e-8f * (1.f + most)) + 1.3e-7f * (fabsf(x) + fabsf(y)), 3e38f)
                                      : (a.sigmoid ? 1e-6f : 4e-6f) * (x + y);
             // (groups without a live expert, or with one less than `best`, have whole multiples of the masked score: equal)
             bool undecided = !(x - y > tol) && x > 0.1f * kMasked;
