@@ -508,3 +508,31 @@ def test_a_wrong_row_among_those_named(gpu_lib, rows):
         assert (z[rows // 2] == 0).all()
         z[rows // 2] = y[rows // 2]
         assert torch.equal(z.nan_to_num(), y.nan_to_num())
+
+
+@pytest.mark.parametrize("dtype,bits", [("bf16", 7), ("fp16", 10)])
+def test_every_quotient_of_16_bit_numbers(gpu_lib, dtype, bits):
+    """Codes of all significands under all largest ones, over the exponents that give codes other than 0: by whole numbers, ties to even."""
+    n, one = 1 << bits, 1 << bits
+    X = np.concatenate([np.arange(one, 2 * one, dtype=np.int64)] * 10)             # x = X 2^-d of the largest's exponent
+    d = np.repeat(np.arange(10), n)
+    for exponent in ((-60, 0, 120) if dtype == "bf16" else (-4, 0, 15)):
+        for A0 in range(one, 2 * one, 128):
+            A = np.arange(A0, A0 + 128, dtype=np.int64)[:, None]
+            keep = (X[None] <= A) | (d[None] > 0)                                # below the largest
+            num, den = 127 * X[None], A << d[None]
+            q, r = num // den, num % den
+            q += (2 * r > den) | ((2 * r == den) & (q & 1 == 1))
+            x = np.where(keep, X * 2.0 ** -d, 0.0)
+            x[:, 1::2] *= -1
+            x = np.concatenate([A.astype(float), x], 1) * 2.0 ** (exponent - bits)
+            t = torch.from_numpy(x).to(DT[dtype]).cuda()
+            # (fp16's lowest exponent: what is subnormal loses bits, and counts with the bits it has)
+            exact = t.double().cpu().numpy() == x
+            want = np.concatenate([np.full((128, 1), 127), np.where(keep, q, 0) * np.where(np.arange(len(X)) % 2, -1, 1)], 1)
+            c, _ = gpu_lib.moe_int8_quantize(t)
+            assert exact[:, : 2 * n].all()
+            np.testing.assert_array_equal(c.cpu().numpy()[exact], want[exact])
+            codes, _ = gpu_lib.moe_checkpoint8_save(torch.cat([t[:, :1], t[:, 1:128]], 1).contiguous())
+            np.testing.assert_array_equal(codes.cpu().numpy()[exact[:, :128]], want[:, :128][exact[:, :128]])
+    ok(gpu_lib)

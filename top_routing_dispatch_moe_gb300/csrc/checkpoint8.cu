@@ -66,7 +66,7 @@ checkpoint_save_kernel(const T* x, long long ldx, int rows, int C, const int32_t
                 float amax = unit_amax(raw[u]);
 #pragma unroll
                 for (int o = 4; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                const float s = scale_of(amax, st);
+                const float s = scale_of<T>(amax, st);
                 const T* e = reinterpret_cast<const T*>(raw[u].q);
                 float v[UNIT];
 #pragma unroll
@@ -96,7 +96,7 @@ checkpoint_save_kernel(const T* x, long long ldx, int rows, int C, const int32_t
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                const float s = scale_of(amax, st);
+                const float s = scale_of<T>(amax, st);
                 codes_of<T, 4>(v, st);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)

@@ -104,7 +104,7 @@ quantize_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, int r
     }
     if (row >= rows) return;
     Steps st;
-    const float scale = scale_of(amax, st);
+    const float scale = scale_of<T>(amax, st);
     if (w == 0 && lane == 0) scales[row] = scale;
     const size_t base = (size_t)row * width;
     if (held) {
@@ -206,7 +206,8 @@ template <typename T, int FORM>
 static cudaError_t quantize_form(const void* x, long long ldx, int x_rows, const int32_t* src, int rows, int K, void* codes, float* scales,
                                  unsigned* err, cudaStream_t s) {
     const int width = FORM == FORM_ROWS ? K : pad64(K), pieces = (width + SEG - 1) / SEG;
-    const bool vec = K % UNIT == 0 && aligned16(x) && ldx * (long long)sizeof(T) % 16 == 0 && aligned16(codes);
+    // whole 16-byte pieces of x's rows and of the codes' (the operand's rows are padded: any K)
+    const bool vec = width % UNIT == 0 && aligned16(x) && ldx * (long long)sizeof(T) % 16 == 0 && aligned16(codes);
     const T* xt = static_cast<const T*>(x);
     auto go = [&](auto kernel, int wpr) {
         return launch_pdl(kernel, dim3(cdiv(rows, WARPS / wpr)), dim3(THREADS), 0, s, xt, ldx, x_rows, src, rows, K, width, codes, scales, err);

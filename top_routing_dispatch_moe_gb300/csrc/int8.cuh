@@ -44,19 +44,26 @@ inline ExpertLayout expert_layout(int E, int h, int F) {
 #ifdef __CUDACC__
 constexpr float TINY = 1.262177448e-29f;             // 2^-96
 
-// The way of values whose largest magnitude is amax to their codes: x * c / a, c = 127 (both times 2^-32 where 127 x could leave
-// fp32's range), r the rounded reciprocal of a, inv the rounded 127 / amax; live: the codes are not all 0.
-struct Steps { float c, a, r, inv; bool live; };
+// The way of values whose largest magnitude is amax to their codes, x * 127 / amax; live: the codes are not all 0.
+// 16-bit types: inv + low is 127 / amax to 2^-28 of it or better. fp32: inv the rounded 127 / amax, and x * c / a with c = 127 (both times
+// 2^-32 where 127 x could leave fp32's range).
+struct Steps { float c, a, inv, low; bool live; };
 // The scale of such values.
+template <typename T>
 __device__ __forceinline__ float scale_of(float amax, Steps& st) {
     const bool finite = amax < INFINITY;             // (NaN: not)
     st.live = finite && amax >= TINY;
-    const float f = amax > 1e30f ? 2.3283064365386963e-10f : 1.f;
-    st.c = 127.f * f;
-    st.a = st.live ? amax * f : 1.f;
-    st.r = __frcp_rn(st.a);
-    st.inv = st.live ? __fdiv_rn(127.f, amax) : 0.f;
-    const float q = amax * (1.f / 127.f), scale = fmaf(fmaf(-q, 127.f, amax), 1.f / 127.f, q);      // amax / 127, rounded (as codes_of has it)
+    if constexpr (sizeof(T) == 2) {
+        const float a = st.live ? amax : 1.f, r = __frcp_rn(a);
+        st.inv = 127.f * r;
+        st.low = fmaf(-st.inv, a, 127.f) * r;
+    } else {
+        const float f = amax > 1e30f ? 2.3283064365386963e-10f : 1.f;
+        st.c = 127.f * f;
+        st.a = st.live ? amax * f : 1.f;
+        st.inv = st.live ? __fdiv_rn(127.f, amax) : 0.f;
+    }
+    const float q = amax * (1.f / 127.f), scale = fmaf(fmaf(-q, 127.f, amax), 1.f / 127.f, q);      // amax / 127, rounded
     return st.live ? scale : finite ? 0.f : __uint_as_float(0x7FC00000u);
 }
 
@@ -73,10 +80,11 @@ static __device__ __noinline__ float code_at_border(float x, float q, const Step
 }
 
 // N values (even) of one row, of type T -> MAGIC + their codes, two values an instruction.
-// 16 bits: x c is exact, and its quotient by a is rounded correctly: q = x c r is off by less than two units in its last place, and
-// q + (x c - q a) r is the rounded quotient (Markstein's correction: the remainder is exact in one fused step). Half way between two codes
-// is a number of few bits, so a tie is one here, and no other quotient comes within 2^-20 of a border. (With a test for quotients near a
-// border instead, two thirds of all blocks of bf16 values had a tie, and 16384 x 28672 of them took 690 us.)
+// 16 bits: x inv + x low, the second rounded by itself, is the quotient to 2^-27 of it before its one rounding. Half way between two codes
+// is a number of eight bits, so a tie is met to the bit, and no other quotient of numbers of 11 bits comes within 2^-20 of itself to a border.
+// (With a test for quotients near a border instead, two thirds of all blocks of bf16 values had a tie, and 16384 x 28672 of them
+// took 690 us; with the quotient corrected by its exact remainder, two more steps a value, those kept
+// and through the SwiGLU backward took 617 us, now 606.)
 // fp32: x inv is off by less than 127 * 2^-23; only a product that close to a border, which among sums and products few are, is looked at again.
 template <typename T, int N>
 __device__ __forceinline__ void codes_of(float* v, const Steps& st) {
@@ -88,11 +96,9 @@ __device__ __forceinline__ void codes_of(float* v, const Steps& st) {
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            float q[2], e[2];
-            mul2(v + i, v + i, st.c);
-            mul2(q, v + i, st.r);
-            fma2(e, q, -st.a, v + i);
-            fma2(q, e, st.r, q);
+            float q[2];
+            mul2(q, v + i, st.low);
+            fma2(q, v + i, st.inv, q);
             add2(v + i, q, MAGIC);
         }
     } else {
