@@ -12,6 +12,10 @@ namespace moe {
 namespace int8 {
 
 constexpr int C_THREADS = 256, C_WARPS = C_THREADS / 32;
+// Blocks of an SM, as many as are resident, with half the loads under way in a lane that three would have room for, each passing
+// over its share: 16384 x 28672 bf16 kept in 227 us and through the backward in 361 (6.3 and 6.5 TB/s), where three blocks, and eight an SM launched,
+// took 233 and 368.
+constexpr int RESIDENT = 4;
 
 // Tiles of a schedule; none (reported) of one of other experts, or of more tiles than the call's rows can have.
 __device__ __forceinline__ int tiles_of(const int32_t* sched, int E, int rows, unsigned* err) {
@@ -37,11 +41,10 @@ struct Rows {
     }
 };
 
-// A warp takes 512 columns of a row at a time: 16 columns a lane, eight lanes to a block, as many such items under way as 4 KB hold
-// (one at a time left 40 KB under way on an SM: 16384 x 28672 bf16 in 690 us), or (!VEC) four blocks one after the other, a lane every 32nd
-// column.
+// A warp takes 512 columns of a row at a time: 16 columns a lane, eight lanes to a block, two such items of 16-bit types under way, or
+// (!VEC) four blocks one after the other, a lane every 32nd column.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(C_THREADS)
+__global__ void __launch_bounds__(C_THREADS, RESIDENT)
 checkpoint_save_kernel(const T* x, long long ldx, int rows, int C, const int32_t* sched, int E, int8_t* codes, float* scales, unsigned* err) {
     pdl_wait();
     pdl_trigger();
@@ -49,7 +52,7 @@ checkpoint_save_kernel(const T* x, long long ldx, int rows, int C, const int32_t
     Rows it(sched, E, rows, (C + 511) / 512, err);
     while (it.at.left > 0) {
         if constexpr (VEC) {
-            constexpr int U = 8 / (int)sizeof(T);
+            constexpr int U = 4 / (int)sizeof(T);
             Raw16<T> raw[U];
             int row[U], k[U];
 #pragma unroll
@@ -73,7 +76,7 @@ checkpoint_save_kernel(const T* x, long long ldx, int rows, int C, const int32_t
                 for (int i = 0; i < UNIT; ++i) v[i] = as_f32(e[i]);
                 codes_of<T, UNIT>(v, st);
                 if (k[u] < C) {
-                    *reinterpret_cast<uint4*>(codes + (size_t)row[u] * C + k[u]) = make_uint4(bytes4(v), bytes4(v + 4), bytes4(v + 8), bytes4(v + 12));
+                    __stcs(reinterpret_cast<uint4*>(codes + (size_t)row[u] * C + k[u]), make_uint4(bytes4(v), bytes4(v + 4), bytes4(v + 8), bytes4(v + 12)));
                     if ((lane & 7) == 0) scales[(size_t)row[u] * nb + k[u] / CKPT] = s;
                 }
             }
@@ -107,34 +110,17 @@ checkpoint_save_kernel(const T* x, long long ldx, int rows, int C, const int32_t
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(C_THREADS)
-checkpoint_load_kernel(const int8_t* codes, const float* scales, int rows, int C, T* out, long long ldo) {
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31, nseg = (C + CKPT - 1) / CKPT;
-    for (Walk at((long long)blockIdx.x * C_WARPS + (threadIdx.x >> 5), (long long)gridDim.x * C_WARPS, (long long)rows * nseg, nseg); at.left > 0;
-         at.next()) {
-        const float s = scales[(size_t)at.row * nseg + at.seg];
-#pragma unroll
-        for (int j = 0; j < CKPT / 32; ++j) {
-            const int k = at.seg * CKPT + j * 32 + lane;
-            if (k < C) out[at.row * ldo + k] = rounded<T>((float)codes[(size_t)at.row * C + k] * s);
-        }
-    }
-}
-
 // Block b of a row of gu: 128 codes of g, then the 128 of u of the same features, each under its own scale. A lane takes eight
 // features, sixteen lanes a block:
 //   s = 1 / (1 + exp(-g)), act = g s u, d_g = da u s (1 + g (1 - s)), d_u = da g s     (da 0 past F)
 // (The exponential and the quotient are the quick ones: s is off by 2^-21 of itself near g = 0 and by 2^-16 at g = -80, a 2^-7th of bf16's
 // half step.)
-__global__ void __launch_bounds__(C_THREADS)
+__global__ void __launch_bounds__(C_THREADS, RESIDENT)
 checkpoint_swiglu_backward_kernel(const int8_t* codes, const float* scales, const __nv_bfloat16* d_act, const int32_t* sched, int E, int rows,
                                   int F, int Fp, __nv_bfloat16* d_gu, __nv_bfloat16* act, unsigned* err) {
     pdl_wait();
     pdl_trigger();
-    constexpr int U = 2;                      // items whose loads a lane has under way
+    constexpr int U = 1;                      // items whose loads a lane has under way
     const int lane = threadIdx.x & 31;
     Rows it(sched, E, rows, (Fp + 255) / 256, err);
     while (it.at.left > 0) {
@@ -182,7 +168,7 @@ checkpoint_swiglu_backward_kernel(const int8_t* codes, const float* scales, cons
     }
 }
 
-static int ckpt_grid(long long items) { return (int)std::max<long long>(1, std::min<long long>((items + C_WARPS - 1) / C_WARPS, 8LL * num_sms())); }
+static int ckpt_grid(long long items) { return (int)std::max<long long>(1, std::min<long long>((items + C_WARPS - 1) / C_WARPS, (long long)RESIDENT * num_sms())); }
 
 static int backward_launch(const void* codes, const float* scales, const void* d_act, const int32_t* sched, int E, int rows, int F, void* d_gu,
                            void* act, cudaStream_t s) {
@@ -245,15 +231,7 @@ extern "C" int moe_checkpoint8_load(const void* codes, const float* scales, int 
     if (rows == 0) return MOE_OK;
     MOE_REQUIRE(codes && scales && out, MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
     MOE_REQUIRE(on_type(out, dtype) && on_type(scales, MOE_F32), MOE_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int grid = int8::ckpt_grid((long long)rows * ((C + 127) / 128));
-    auto go = [&](auto kernel, auto* o) {
-        return launch_pdl(kernel, dim3(grid), dim3(int8::C_THREADS), 0, s, static_cast<const int8_t*>(codes), scales, rows, C, o, ldo);
-    };
-    const cudaError_t e = dtype == MOE_F32    ? go(int8::checkpoint_load_kernel<float>, static_cast<float*>(out))
-                          : dtype == MOE_BF16 ? go(int8::checkpoint_load_kernel<__nv_bfloat16>, static_cast<__nv_bfloat16*>(out))
-                                              : go(int8::checkpoint_load_kernel<__half>, static_cast<__half*>(out));
-    return check_launch(e, "checkpoint_load_kernel");
+    return int8::launch_dequantize(codes, scales, rows, C, dtype, out, ldo, true, static_cast<cudaStream_t>(stream));
 }
 
 static int ckpt_backward_check(const char* fn, const void* codes, const float* scales, const void* d_act, const int32_t* sched, int E, int F,

@@ -117,13 +117,15 @@ quantize_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, int r
     }
 }
 
-template <typename T, bool VEC>
+// BLOCKS: a scale for 128 columns (a checkpoint) instead of one for a row.
+template <typename T, bool VEC, bool BLOCKS>
 __global__ void __launch_bounds__(THREADS)
 dequantize_kernel(const int8_t* codes, const float* scales, int rows, int K, T* out, long long ldo) {
     pdl_wait();
     pdl_trigger();
     constexpr int U = VEC ? 4 : 1;       // pieces whose codes a lane has under way
     const int lane = threadIdx.x & 31, nseg = (K + SEG - 1) / SEG;
+    auto scale = [&](int row, int k) { return scales[BLOCKS ? (size_t)row * ((K + CKPT - 1) / CKPT) + k / CKPT : row]; };
     Walk at((long long)blockIdx.x * WARPS + (threadIdx.x >> 5), (long long)gridDim.x * WARPS, (long long)rows * nseg, nseg);
     while (at.left > 0) {
         if constexpr (VEC) {
@@ -136,7 +138,7 @@ dequantize_kernel(const int8_t* codes, const float* scales, int rows, int K, T* 
                 to[u] = nullptr;
                 if (at.left > 0 && k < K) {
                     q[u] = __ldcs(reinterpret_cast<const uint4*>(codes + (size_t)at.row * K + k));
-                    s[u] = scales[at.row];
+                    s[u] = scale(at.row, k);
                     to[u] = out + at.row * ldo + k;
                 }
                 if (at.left > 0) at.next();
@@ -164,11 +166,10 @@ dequantize_kernel(const int8_t* codes, const float* scales, int rows, int K, T* 
         } else {
             const int8_t* cr = codes + (size_t)at.row * K;
             T* orow = out + at.row * ldo;
-            const float s = scales[at.row];
 #pragma unroll
             for (int j = 0; j < UNIT; ++j) {
                 const int k = at.seg * SEG + j * 32 + lane;
-                if (k < K) orow[k] = rounded<T>((float)cr[k] * s);
+                if (k < K) orow[k] = rounded<T>((float)cr[k] * scale(at.row, k));
             }
             at.next();
         }
@@ -237,6 +238,29 @@ int launch_quantize(const void* x, long long ldx, int x_rows, const int32_t* src
     return check_launch(e, "int8 quantize_kernel");
 }
 
+template <typename T, bool VEC>
+static cudaError_t dequantize_form(const void* codes, const float* scales, int rows, int K, void* out, long long ldo, bool blocks, cudaStream_t s) {
+    const long long items = (long long)rows * cdiv(K, SEG);
+    const int grid = (int)std::min<long long>((items + WARPS - 1) / WARPS, 8LL * num_sms());
+    auto go = [&](auto kernel) {
+        return launch_pdl(kernel, dim3(grid), dim3(THREADS), 0, s, static_cast<const int8_t*>(codes), scales, rows, K, static_cast<T*>(out), ldo);
+    };
+    return blocks ? go(dequantize_kernel<T, VEC, true>) : go(dequantize_kernel<T, VEC, false>);
+}
+
+int launch_dequantize(const void* codes, const float* scales, int rows, int K, int dtype, void* out, long long ldo, bool blocks, cudaStream_t s) {
+    const bool vec = K % UNIT == 0 && aligned16(codes) && aligned16(out) && ldo * (dtype == MOE_F32 ? 4 : 2) % 16 == 0;
+    cudaError_t e = cudaErrorInvalidValue;
+#define MOE_DEQUANT(T)                                                                     \
+    e = vec ? dequantize_form<T, true>(codes, scales, rows, K, out, ldo, blocks, s)        \
+            : dequantize_form<T, false>(codes, scales, rows, K, out, ldo, blocks, s)
+    if (dtype == MOE_F32) MOE_DEQUANT(float);
+    else if (dtype == MOE_BF16) MOE_DEQUANT(__nv_bfloat16);
+    else MOE_DEQUANT(__half);
+#undef MOE_DEQUANT
+    return check_launch(e, "int8 dequantize_kernel");
+}
+
 static bool known(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16; }
 static bool type_aligned(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % (dtype == MOE_F32 ? 4 : 2) == 0; }
 
@@ -269,26 +293,7 @@ extern "C" int moe_int8_dequantize(const void* codes, const float* scales, int r
     if (rows == 0) return MOE_OK;
     MOE_REQUIRE(codes && scales && out, MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
     MOE_REQUIRE(int8::type_aligned(out, dtype) && int8::type_aligned(scales, MOE_F32), MOE_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
-    const long long items = (long long)rows * cdiv(K, int8::SEG);
-    const int grid = (int)std::min<long long>((items + int8::WARPS - 1) / int8::WARPS, 8LL * num_sms());
-    const int el = dtype == MOE_F32 ? 4 : 2;
-    const bool vec = K % UNIT == 0 && aligned16(codes) && aligned16(out) && ldo * el % 16 == 0;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    auto go = [&](auto kernel, auto* o) {
-        return launch_pdl(kernel, dim3(grid), dim3(int8::THREADS), 0, s, static_cast<const int8_t*>(codes), scales, rows, K, o, ldo);
-    };
-    cudaError_t e;
-    if (dtype == MOE_F32) {
-        auto* o = static_cast<float*>(out);
-        e = vec ? go(int8::dequantize_kernel<float, true>, o) : go(int8::dequantize_kernel<float, false>, o);
-    } else if (dtype == MOE_BF16) {
-        auto* o = static_cast<__nv_bfloat16*>(out);
-        e = vec ? go(int8::dequantize_kernel<__nv_bfloat16, true>, o) : go(int8::dequantize_kernel<__nv_bfloat16, false>, o);
-    } else {
-        auto* o = static_cast<__half*>(out);
-        e = vec ? go(int8::dequantize_kernel<__half, true>, o) : go(int8::dequantize_kernel<__half, false>, o);
-    }
-    return check_launch(e, "int8 dequantize_kernel");
+    return int8::launch_dequantize(codes, scales, rows, K, dtype, out, ldo, false, static_cast<cudaStream_t>(stream));
 }
 
 static bool int8_sizes(int G, int N, int K) {

@@ -156,6 +156,8 @@ enum Form : int { FORM_ROWS = 0, FORM_F16 = 1 };
 // Rows of x (or those that src names, -1: a row of zeros) -> codes and scales, a programmatic dependent of the kernel before.
 int launch_quantize(const void* x, long long ldx, int x_rows, const int32_t* src, int rows, int K, int dtype, int form, void* codes,
                     float* scales, unsigned* err, cudaStream_t s);
+// Codes [rows][K] -> values; blocks: under the scales of a checkpoint.
+int launch_dequantize(const void* codes, const float* scales, int rows, int K, int dtype, void* out, long long ldo, bool blocks, cudaStream_t s);
 
 }  // namespace int8
 }  // namespace moe
