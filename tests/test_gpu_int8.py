@@ -536,3 +536,31 @@ def test_every_quotient_of_16_bit_numbers(gpu_lib, dtype, bits):
             codes, _ = gpu_lib.moe_checkpoint8_save(torch.cat([t[:, :1], t[:, 1:128]], 1).contiguous())
             np.testing.assert_array_equal(codes.cpu().numpy()[exact[:, :128]], want[:, :128][exact[:, :128]])
     ok(gpu_lib)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows,K", [(40, 33), (19, 47), (35, 2033), (18, 2047), (35, 3001), (33, 4081), (17, 4097), (16, 17), (3, 9999)])
+def test_rows_that_start_on_no_boundary(gpu_lib, dtype, rows, K):
+    """Contiguous matrices whose rows begin and end within 16-byte pieces, there and back; the same with row strides, which go another way;
+    with what lies around left alone."""
+    x = data((rows, K), dtype, K, 2.0)
+    code, scale = Q.quantize(f64(x))
+    room = torch.full((rows * K + 64,), 77, dtype=torch.int8, device="cuda")
+    codes = room[16: 16 + rows * K].view(rows, K)
+    c, s = gpu_lib.moe_int8_quantize(x, codes=codes)
+    wide = torch.zeros((rows, K + 3), dtype=x.dtype, device="cuda")
+    wide[:, :K] = x
+    c2, s2 = gpu_lib.moe_int8_quantize(wide[:, :K])
+    ok(gpu_lib)
+    np.testing.assert_array_equal(c.cpu().numpy(), code)
+    np.testing.assert_array_equal(f64(s), scale)
+    assert torch.equal(c, c2) and torch.equal(s, s2)
+    assert (room[:16] == 77).all() and (room[16 + rows * K:] == 77).all()
+    back = torch.full((rows * K + 64,), 5.0, dtype=x.dtype, device="cuda")
+    out = back[32: 32 + rows * K].view(rows, K)
+    gpu_lib.moe_int8_dequantize(codes, s, out=out)
+    strided = gpu_lib.moe_int8_dequantize(codes, s, out=wide[:, :K])
+    ok(gpu_lib)
+    want = (c.float() * s.unsqueeze(1)).to(x.dtype)
+    assert torch.equal(out, want) and torch.equal(strided, want)
+    assert (back[:32] == 5).all() and (back[32 + rows * K:] == 5).all() and (wide[:, K:] == 0).all()

@@ -14,31 +14,41 @@ constexpr int WARPS = THREADS / 32;
 constexpr int SEG = 32 * UNIT;       // columns a warp takes at a time
 constexpr int HELD = 4;              // such pieces that a warp holds
 
-// Piece `c` of a row (columns 512 c ..): VEC: this lane's 16 consecutive columns; else (the row starts on no 16-byte boundary, or its
-// end cuts a unit) every 32nd column from the lane's own, so that loads and stores of a warp stay together.
-template <typename T, bool VEC>
-__device__ __forceinline__ Raw16<T> load_piece(const T* row, int c, int K, bool again) {
-    const int lane = threadIdx.x & 31;
-    if constexpr (VEC) return load_unit<T, true>(row, c * SEG + lane * UNIT, K, again);
+// How a row lies: its 16-column units on 16 bytes in x and in the codes (WHOLE), both after `skip` columns of a contiguous matrix's row
+// before (FLAT: the unit that holds the row's start, and its last, are the neighbours' too), or on no boundary (ANY).
+enum Lie { WHOLE, FLAT, ANY };
+
+// Piece `c` of a row: WHOLE, FLAT: this lane's 16 consecutive columns; ANY: every 32nd column from the lane's own, so that loads and stores
+// of a warp stay together.
+template <typename T, Lie LIE>
+__device__ __forceinline__ Raw16<T> load_piece(const T* row, int c, int K, int skip, bool again) {
+    const int lane = threadIdx.x & 31, k0 = c * SEG + lane * UNIT - skip;
+    if constexpr (LIE == WHOLE) return load_unit<T, true>(row, k0, K, again);
     Raw16<T> r;
     T* e = reinterpret_cast<T*>(r.q);
+    if constexpr (LIE == FLAT) {
+        if (k0 >= 0 && k0 + UNIT <= K) return load_unit<T, true>(row, k0, K, again);
 #pragma unroll
-    for (int j = 0; j < UNIT; ++j) {
-        const int k = c * SEG + j * 32 + lane;
-        e[j] = k < K ? row[k] : T(0.f);
+        for (int j = 0; j < UNIT; ++j) e[j] = k0 + j >= 0 && k0 + j < K ? row[k0 + j] : T(0.f);
+    } else {
+#pragma unroll
+        for (int j = 0; j < UNIT; ++j) {
+            const int k = c * SEG + j * 32 + lane;
+            e[j] = k < K ? row[k] : T(0.f);
+        }
     }
     return r;
 }
-template <typename T, int FORM, bool VEC>
-__device__ __forceinline__ void store_piece(const Raw16<T>& raw, void* codes, size_t base, int c, int width, const Steps& st) {
+template <typename T, int FORM, Lie LIE>
+__device__ __forceinline__ void store_piece(const Raw16<T>& raw, void* codes, size_t base, int c, int width, int skip, const Steps& st) {
     const int lane = threadIdx.x & 31;
     const T* e = reinterpret_cast<const T*>(raw.q);
     float v[UNIT];
 #pragma unroll
     for (int i = 0; i < UNIT; ++i) v[i] = as_f32(e[i]);
     codes_of<T, UNIT>(v, st);
-    if constexpr (VEC) {
-        const int k = c * SEG + lane * UNIT;
+    if constexpr (LIE != ANY) {
+        const int k = c * SEG + lane * UNIT - skip;
         if (k >= width) return;
         if constexpr (FORM == FORM_F16) {
             uint4 w[2];
@@ -46,9 +56,13 @@ __device__ __forceinline__ void store_piece(const Raw16<T>& raw, void* codes, si
 #pragma unroll
             for (int i = 0; i < UNIT / 2; ++i) h[i] = halves2(v + 2 * i);
             st32(static_cast<__half*>(codes) + base + k, w);
-        } else {
+        } else if (LIE == WHOLE || (k >= 0 && k + UNIT <= width)) {
             *reinterpret_cast<uint4*>(static_cast<int8_t*>(codes) + base + k) =
                 make_uint4(bytes4(v), bytes4(v + 4), bytes4(v + 8), bytes4(v + 12));
+        } else {
+#pragma unroll
+            for (int j = 0; j < UNIT; ++j)
+                if (k + j >= 0 && k + j < width) static_cast<uint8_t*>(codes)[base + k + j] = (uint8_t)__float_as_uint(v[j]);
         }
     } else {
 #pragma unroll
@@ -62,7 +76,7 @@ __device__ __forceinline__ void store_piece(const Raw16<T>& raw, void* codes, si
 }
 
 // WPR warps to a row.
-template <typename T, int FORM, int WPR, bool VEC>
+template <typename T, int FORM, int WPR, Lie LIE>
 __global__ void __launch_bounds__(THREADS)
 quantize_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, int rows, int K, int width, void* codes, float* scales,
                 unsigned* err) {
@@ -80,19 +94,20 @@ quantize_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, int r
         }
     }
     const T* xr = x + (long long)max(from, 0) * ldx;
-    const int k_in = from >= 0 ? K : 0, pieces = (width + SEG - 1) / SEG;
+    const int k_in = from >= 0 ? K : 0, skip = LIE == FLAT ? (row & 15) * (K & 15) & 15 : 0,
+              pieces = (width + skip + SEG - 1) / SEG;
     const bool held = pieces <= HELD * WPR, again = src != nullptr;
     Raw16<T> raw[HELD];
     float amax = 0.f;
     if (held) {
 #pragma unroll
         for (int i = 0; i < HELD; ++i)
-            if (i * WPR + w < pieces) raw[i] = load_piece<T, VEC>(xr, i * WPR + w, k_in, again);
+            if (i * WPR + w < pieces) raw[i] = load_piece<T, LIE>(xr, i * WPR + w, k_in, skip, again);
 #pragma unroll
         for (int i = 0; i < HELD; ++i)
             if (i * WPR + w < pieces) amax = max_nan(amax, unit_amax(raw[i]));
     } else {
-        for (int c = w; c < pieces; c += WPR) amax = max_nan(amax, unit_amax(load_piece<T, VEC>(xr, c, k_in, again)));
+        for (int c = w; c < pieces; c += WPR) amax = max_nan(amax, unit_amax(load_piece<T, LIE>(xr, c, k_in, skip, again)));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -110,10 +125,10 @@ quantize_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, int r
     if (held) {
 #pragma unroll
         for (int i = 0; i < HELD; ++i)
-            if (i * WPR + w < pieces) store_piece<T, FORM, VEC>(raw[i], codes, base, i * WPR + w, width, st);
+            if (i * WPR + w < pieces) store_piece<T, FORM, LIE>(raw[i], codes, base, i * WPR + w, width, skip, st);
     } else {
         for (int c = w; c < pieces; c += WPR)
-            store_piece<T, FORM, VEC>(load_piece<T, VEC>(xr, c, k_in, again), codes, base, c, width, st);
+            store_piece<T, FORM, LIE>(load_piece<T, LIE>(xr, c, k_in, skip, again), codes, base, c, width, skip, st);
     }
 }
 
@@ -176,6 +191,51 @@ dequantize_kernel(const int8_t* codes, const float* scales, int rows, int K, T* 
     }
 }
 
+// Contiguous rows of any width from 16 on (a scale a row): 16 elements a lane across the rows' ends, two scales at most.
+template <typename T>
+__global__ void __launch_bounds__(THREADS)
+dequantize_flat_kernel(const int8_t* codes, const float* scales, long long total, int K, T* out) {
+    pdl_wait();
+    pdl_trigger();
+    constexpr int U = 2;                 // units whose codes a lane has under way
+    const long long units = (total + UNIT - 1) / UNIT, step = (long long)gridDim.x * THREADS;
+    const bool small = total < (1LL << 31);
+    for (long long i = (long long)blockIdx.x * THREADS + threadIdx.x; i < units; i += U * step) {
+        uint4 q[U];
+        float s0[U], s1[U];
+        int here[U];                     // elements of the first row
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long at = (i + u * step) * UNIT;
+            here[u] = 0;
+            if (at + UNIT > total) continue;
+            const long long row = small ? (long long)((unsigned)at / (unsigned)K) : at / K;
+            here[u] = (int)min((row + 1) * K - at, (long long)UNIT);
+            q[u] = __ldcs(reinterpret_cast<const uint4*>(codes + at));
+            s0[u] = scales[row];
+            s1[u] = here[u] < UNIT ? scales[row + 1] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (here[u] == 0) continue;
+            T* to = out + (i + u * step) * UNIT;
+            float v[UNIT];
+            values4(q[u].x, 1.f, v);
+            values4(q[u].y, 1.f, v + 4);
+            values4(q[u].z, 1.f, v + 8);
+            values4(q[u].w, 1.f, v + 12);
+            alignas(16) T o[UNIT];
+#pragma unroll
+            for (int j = 0; j < UNIT; ++j) o[j] = rounded<T>(v[j] * (j < here[u] ? s0[u] : s1[u]));
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(T); ++j) reinterpret_cast<uint4*>(to)[j] = reinterpret_cast<const uint4*>(o)[j];
+        }
+    }
+    // the last elements, less than a unit (all of the last row)
+    const long long at = total / UNIT * UNIT + threadIdx.x;
+    if (blockIdx.x == 0 && at < total) out[at] = rounded<T>((float)codes[at] * scales[at / K]);
+}
+
 // A 16-byte chunk of the packed weight a thread. b: null, or the rows that follow those of a in turn (gate, up).
 __global__ void __launch_bounds__(THREADS)
 pack_kernel(const int8_t* __restrict__ a, const int8_t* __restrict__ b, int N, int K, int NB, int KST, size_t chunks, uint4* __restrict__ out) {
@@ -206,22 +266,35 @@ static int launch_pack(const void* a, const void* b, int G, int N, int K, void* 
 template <typename T, int FORM>
 static cudaError_t quantize_form(const void* x, long long ldx, int x_rows, const int32_t* src, int rows, int K, void* codes, float* scales,
                                  unsigned* err, cudaStream_t s) {
-    const int width = FORM == FORM_ROWS ? K : pad64(K), pieces = (width + SEG - 1) / SEG;
-    // whole 16-byte pieces of x's rows and of the codes' (the operand's rows are padded: any K)
-    const bool vec = width % UNIT == 0 && aligned16(x) && ldx * (long long)sizeof(T) % 16 == 0 && aligned16(codes);
+    const int width = FORM == FORM_ROWS ? K : pad64(K);
     const T* xt = static_cast<const T*>(x);
+    // whole 16-byte pieces of x's rows and of the codes' (the operand's rows are padded: any K)
+    const bool aligned = aligned16(x) && aligned16(codes), vec = width % UNIT == 0 && aligned && ldx * (long long)sizeof(T) % 16 == 0;
     auto go = [&](auto kernel, int wpr) {
         return launch_pdl(kernel, dim3(cdiv(rows, WARPS / wpr)), dim3(THREADS), 0, s, xt, ldx, x_rows, src, rows, K, width, codes, scales, err);
     };
-    // a row's warps: as many as hold it four pieces each
+    // a row's warps: as many as hold it four pieces each (16384 x 3001 fp32, six pieces, by eight warps instead of two 110 us, not 60)
+    const int pieces = (width + SEG - 1) / SEG;
     if (vec) {
-        if (pieces <= HELD) return go(quantize_kernel<T, FORM, 1, true>, 1);
-        if (pieces <= 2 * HELD) return go(quantize_kernel<T, FORM, 2, true>, 2);
-        if (pieces <= 4 * HELD) return go(quantize_kernel<T, FORM, 4, true>, 4);
-        return go(quantize_kernel<T, FORM, 8, true>, 8);
+        if (pieces <= HELD) return go(quantize_kernel<T, FORM, 1, WHOLE>, 1);
+        if (pieces <= 2 * HELD) return go(quantize_kernel<T, FORM, 2, WHOLE>, 2);
+        if (pieces <= 4 * HELD) return go(quantize_kernel<T, FORM, 4, WHOLE>, 4);
+        return go(quantize_kernel<T, FORM, 8, WHOLE>, 8);
     }
-    if (pieces <= HELD) return go(quantize_kernel<T, FORM, 1, false>, 1);
-    return go(quantize_kernel<T, FORM, 8, false>, 8);
+    // contiguous rows of other widths, of 16-bit types (65536 x 999 fp16 69 -> 52 us, x 1500 bf16 90 -> 62; fp32, whose lanes already load
+    // whole sectors, 74 -> 88)
+    if constexpr (FORM == FORM_ROWS && sizeof(T) == 2)
+        if (aligned && !src && ldx == K && K >= 2 * UNIT) {
+            const int most = (K + UNIT - 1 + SEG - 1) / SEG;
+            if (most <= HELD) return go(quantize_kernel<T, FORM, 1, FLAT>, 1);
+            if (most <= 2 * HELD) return go(quantize_kernel<T, FORM, 2, FLAT>, 2);
+            if (most <= 4 * HELD) return go(quantize_kernel<T, FORM, 4, FLAT>, 4);
+            return go(quantize_kernel<T, FORM, 8, FLAT>, 8);
+        }
+    if (pieces <= HELD) return go(quantize_kernel<T, FORM, 1, ANY>, 1);
+    if (pieces <= 2 * HELD) return go(quantize_kernel<T, FORM, 2, ANY>, 2);
+    if (pieces <= 4 * HELD) return go(quantize_kernel<T, FORM, 4, ANY>, 4);
+    return go(quantize_kernel<T, FORM, 8, ANY>, 8);
 }
 
 int launch_quantize(const void* x, long long ldx, int x_rows, const int32_t* src, int rows, int K, int dtype, int form, void* codes,
@@ -248,12 +321,23 @@ static cudaError_t dequantize_form(const void* codes, const float* scales, int r
     return blocks ? go(dequantize_kernel<T, VEC, true>) : go(dequantize_kernel<T, VEC, false>);
 }
 
+// (4099 x 999 fp16 5.4 -> 3.7 us, 65536 x 999 69 -> 33; before, a lane took every 32nd column.)
+template <typename T>
+static cudaError_t dequantize_flat(const void* codes, const float* scales, int rows, int K, void* out, cudaStream_t s) {
+    const long long total = (long long)rows * K, units = (total + UNIT - 1) / UNIT;
+    const int grid = (int)std::min<long long>((units + 2 * THREADS - 1) / (2 * THREADS), 8LL * num_sms());
+    return launch_pdl(dequantize_flat_kernel<T>, dim3(grid), dim3(THREADS), 0, s, static_cast<const int8_t*>(codes), scales, total, K,
+                      static_cast<T*>(out));
+}
+
 int launch_dequantize(const void* codes, const float* scales, int rows, int K, int dtype, void* out, long long ldo, bool blocks, cudaStream_t s) {
+    const bool flat = !blocks && K % UNIT != 0 && K > UNIT && ldo == K && aligned16(codes) && aligned16(out);
     const bool vec = K % UNIT == 0 && aligned16(codes) && aligned16(out) && ldo * (dtype == MOE_F32 ? 4 : 2) % 16 == 0;
     cudaError_t e = cudaErrorInvalidValue;
 #define MOE_DEQUANT(T)                                                                     \
-    e = vec ? dequantize_form<T, true>(codes, scales, rows, K, out, ldo, blocks, s)        \
-            : dequantize_form<T, false>(codes, scales, rows, K, out, ldo, blocks, s)
+    e = flat  ? dequantize_flat<T>(codes, scales, rows, K, out, s)                         \
+        : vec ? dequantize_form<T, true>(codes, scales, rows, K, out, ldo, blocks, s)      \
+              : dequantize_form<T, false>(codes, scales, rows, K, out, ldo, blocks, s)
     if (dtype == MOE_F32) MOE_DEQUANT(float);
     else if (dtype == MOE_BF16) MOE_DEQUANT(__nv_bfloat16);
     else MOE_DEQUANT(__half);

@@ -134,6 +134,15 @@ struct Walk {
     int row, seg, drow, dseg, nseg;
     long long left;                      // items still to come, this one included, in steps
     __device__ __forceinline__ Walk(long long first, long long step, long long items, int nseg_) : nseg(nseg_) {
+        if (((items | (first + step)) >> 30) == 0) {     // (a 64-bit division takes some hundred instructions)
+            const unsigned f = (unsigned)first, st = (unsigned)step, n = (unsigned)nseg;
+            left = first < items ? ((unsigned)items - f + st - 1) / st : 0;
+            row = (int)(f / n);
+            seg = (int)(f - (unsigned)row * n);
+            drow = (int)(st / n);
+            dseg = (int)(st - (unsigned)drow * n);
+            return;
+        }
         left = first < items ? (items - first + step - 1) / step : 0;
         row = (int)(first / nseg);
         seg = (int)(first - (long long)row * nseg);
