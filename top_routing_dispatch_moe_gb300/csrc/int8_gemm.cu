@@ -26,7 +26,7 @@ struct Params {
     int N;                       // output channels (EPI_SWIGLU: 2 F)
     long long ld;                // row stride of the output
     int out_dtype;
-    void* out;                   // EPI_SWIGLU: act [rows][N / 2] fp32
+    void* out;                   // EPI_SWIGLU: act [rows][N / 2] fp32, its rows ld apart as well
     unsigned* err;
     long long wait_limit;
 };
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) few_rows_kernel(const __grid_c
                     if (n < p.N) store_value(p, row * p.ld + n, v);
                 } else {
                     const float u = __shfl_down_sync(0xffffffffu, v, 1);
-                    if (!(n & 1) && n < p.N) static_cast<float*>(p.out)[(size_t)row * F + f] = swiglu(v, u);
+                    if (!(n & 1) && n < p.N) static_cast<float*>(p.out)[row * p.ld + f] = swiglu(v, u);
                 }
             }
         }
@@ -441,15 +441,15 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, int g, uint32_t 
             }
         } else {
             // even lanes hold gates, odd lanes the ups of the same features: of two rows, the even lane finishes the first
-            const int F = p.N / 2, odd = lane & 1;
-            float* at = static_cast<float*>(p.out) + (size_t)(r0 + odd) * F + (ch >> 1);
+            const int odd = lane & 1;
+            float* at = static_cast<float*>(p.out) + (r0 + odd) * p.ld + (ch >> 1);
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
                 const float y0 = v[j] * __shfl_sync(0xffffffffu, xs, j) * scale, y1 = v[j + 1] * __shfl_sync(0xffffffffu, xs, j + 1) * scale;
                 const float got = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
                 const float a = swiglu(odd ? got : y0, odd ? y1 : got);
                 if (mine && j + odd < nr) *at = a;
-                at += 2 * (size_t)F;
+                at += 2 * p.ld;
             }
         }
     }
@@ -822,17 +822,18 @@ extern "C" int moe_int8_linear(const void* x, long long ldx, int x_rows, const i
     return int8::launch_product<int8::EPI_OUT>(p, s);
 }
 
-// The FFN's workspace: x's operand, act [rows][F] in fp32, act's operand.
+// The FFN's workspace: x's operand, act [rows][F] in fp32 with rows of whole 16 bytes, act's operand.
 namespace moe {
 namespace int8 {
-struct FfnWs { char* x; float* act; char* a; size_t bytes; };
+struct FfnWs { char* x; float* act; int ld; char* a; size_t bytes; };
 static FfnWs ffn_ws(void* ws, int h, int F, long long rows) {
     FfnWs w{};
     char* base = static_cast<char*>(ws);
     w.x = base;
     size_t off = operand_bytes(rows, h);
     w.act = reinterpret_cast<float*>(base + off);
-    off = align_up(off + (size_t)rows * F * 4, 256);
+    w.ld = (F + 3) / 4 * 4;
+    off = align_up(off + (size_t)rows * w.ld * 4, 256);
     w.a = base + off;
     w.bytes = off + operand_bytes(rows, F);
     return w;
@@ -866,11 +867,11 @@ extern "C" int moe_int8_expert_ffn(const void* x, long long ldx, int x_rows, con
     p.offsets = offsets; p.sched = tile_sched; p.G = E; p.rows = rows; p.max_tiles = (int)sched_max_tiles(rows, E);
     p.w = static_cast<const uint8_t*>(packed); p.NB = L.gu.NB; p.KST = L.gu.KST;
     p.a = w.x; p.a_scales = int8::scales_at(w.x, rows, h);
-    p.w_scales = gate_scales; p.w_scales_up = up_scales; p.N = 2 * F; p.out_dtype = MOE_F32; p.out = w.act;
+    p.w_scales = gate_scales; p.w_scales_up = up_scales; p.N = 2 * F; p.ld = w.ld; p.out_dtype = MOE_F32; p.out = w.act;
     p.err = err; p.wait_limit = wait_limit();
     if (int rc = int8::launch_quantize(x, ldx, x_rows, src, rows, h, dtype, int8::FORM_F16, w.x, int8::scales_at(w.x, rows, h), err, s)) return rc;
     if (int rc = int8::launch_product<int8::EPI_SWIGLU>(p, s)) return rc;
-    if (int rc = int8::launch_quantize(w.act, F, rows, nullptr, rows, F, MOE_F32, int8::FORM_F16, w.a, int8::scales_at(w.a, rows, F), err, s))
+    if (int rc = int8::launch_quantize(w.act, w.ld, rows, nullptr, rows, F, MOE_F32, int8::FORM_F16, w.a, int8::scales_at(w.a, rows, F), err, s))
         return rc;
     p.w += L.down_off; p.NB = L.down.NB; p.KST = L.down.KST;
     p.a = w.a; p.a_scales = int8::scales_at(w.a, rows, F);
