@@ -213,7 +213,9 @@ def test_large_biases_that_cancel_in_a_groups_score(gpu_lib, E):
 
 
 @pytest.mark.parametrize("E,groups,top_groups,k", [(256, 8, 4, 8), (160, 8, 3, 6), (96, 32, 5, 4), (64, 2, 1, 16), (66, 6, 2, 5), (40, 8, 7, 3), (1024, 4, 3, 16),
-                                                   (32, 32, 9, 9)])
+                                                   (32, 32, 9, 9), (296, 8, 3, 8), (200, 4, 2, 8), (992, 16, 5, 9), (900, 9, 4, 7), (35, 5, 2, 6),
+                                                   (51, 17, 6, 5), (1023, 3, 2, 12), (144, 16, 8, 8), (1020, 17, 8, 10), (150, 3, 3, 10),
+                                                   (7, 7, 2, 2), (1, 1, 1, 1)])
 def test_near_ties_in_every_token(gpu_lib, E, groups, top_groups, k):
     """Logits and biases of a few values, off by some units in the last place: the order of most groups and experts is lost in 32 bits. With
     large biases too, the same for the experts of a group's place in all groups, so that the groups stay close."""

@@ -8,8 +8,10 @@
 // The choice is that of exact scores: two scores that 32 bits cannot tell apart are compared in 64. Without a bias the
 // experts are ranked by the logits themselves (both scores rise with them), which needs no such comparison.
 //
-// One warp to a token, lane l holding the experts l npl .. l npl + npl - 1, so that a group is a run of lanes (where its
-// size is a multiple of npl; through shared memory otherwise) and equal scores go to the lowest lane.
+// One warp to a token. A group is a run of lpg lanes, a power of two, and a lane holds npl of its group's experts in a row (the last
+// lanes of a group fewer), so that equal scores go to the lowest lane. Where that were over 32 experts to a lane (9 groups of 100), lane l
+// holds the experts l npl .. l npl + npl - 1 and the groups' scores go through shared memory.
+// (16384 tokens by 8 groups of 37: 67 us that way, 40 with runs of lanes; 4 of 50: 57 and 29; 16 of 48: 166 and 93.)
 #include <math.h>
 #include <algorithm>
 #include "common.cuh"
@@ -30,7 +32,7 @@ struct Args {
     int nparts;
     size_t part_stride;
     const float* bias;                       // or null
-    int T, E, k, groups, per, top_groups, best, npl, lpg, lpg_log;   // per: experts of a group; lpg: lanes of a group (0: no whole lanes)
+    int T, E, k, groups, per, top_groups, best, npl, lpg, lpg_log;   // per: experts of a group; lpg: lanes of a group, or 0
     bool sigmoid, renorm, vec;
     float scale;
     float* logits_out;                       // or null
@@ -43,6 +45,14 @@ struct Args {
     float *f, *P, *aux;
     float alpha;
 };
+
+// A lane's first expert, and how many it holds.
+struct Held { int e0, n; };
+__device__ __forceinline__ Held held_by(const Args& a, int lane) {
+    if (!a.lpg) return Held{lane * a.npl, min(max(a.E - lane * a.npl, 0), a.npl)};
+    const int at = (lane & (a.lpg - 1)) * a.npl, g = lane >> a.lpg_log;
+    return Held{g * a.per + at, g < a.groups ? min(max(a.per - at, 0), a.npl) : 0};
+}
 
 __device__ __forceinline__ unsigned key_of(float v) {
     const unsigned u = __float_as_uint(v + 0.f);               // (-0 as 0)
@@ -94,22 +104,23 @@ __device__ __noinline__ Norm exact_norm(const float* L, int npl) {
 // The groups that stay, in 64 bits: bit g of the result; sel: this lane's scores' order. Whole warp, as the two below; L: this lane's npl
 // logits (-inf past E).
 __device__ __noinline__ unsigned groups_exact(const Args& a, const float* L, long long* sel) {
-    const int lane = threadIdx.x & 31, npl = a.npl, e0 = lane * npl;
+    const int lane = threadIdx.x & 31, npl = a.npl;
+    const Held h = held_by(a, lane);
     const Norm n = a.sigmoid ? Norm{0.0, 0.0} : exact_norm(L, npl);
 #pragma unroll 1
     for (int i = 0; i < npl; i += 4) {
         double v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const bool live = i + j < npl && e0 + i + j < a.E;
-            v[j] = exact_sel(live ? L[i + j] : 0.f, a.bias && live ? a.bias[e0 + i + j] : 0.f, n.m, n.z);
+            const bool live = i + j < h.n;
+            v[j] = exact_sel(live ? L[i + j] : 0.f, a.bias && live ? a.bias[h.e0 + i + j] : 0.f, n.m, n.z);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (i + j < npl) sel[i + j] = e0 + i + j < a.E ? order_of(v[j]) : kLeast;
+            if (i + j < npl) sel[i + j] = i + j < h.n ? order_of(v[j]) : kLeast;
     }
     long long gscore = kLeast;               // lane g: group g's
-    if (a.lpg && (a.lpg & (a.lpg - 1)) == 0) {           // a group is a run of lanes: all at once
+    if (a.lpg) {                             // a group is a run of lanes: all at once
         long long t1 = kLeast, t2 = kLeast;
 #pragma unroll 1
         for (int i = 0; i < npl; ++i) {
@@ -123,13 +134,13 @@ __device__ __noinline__ unsigned groups_exact(const Args& a, const float* L, lon
             t1 = max(t1, b1);
         }
         const long long v = a.best == 2 ? order_of_sum(t1, t2) : t1;
-        gscore = __shfl_sync(0xffffffffu, v, min(lane * a.lpg, 31));
+        gscore = __shfl_sync(0xffffffffu, v, min(lane << a.lpg_log, 31));
         if (lane >= a.groups) gscore = kLeast;
     } else
 #pragma unroll 1
     for (int g = 0; g < a.groups; ++g) {
         long long t1 = kLeast, t2 = kLeast;
-        const int lo = max(g * a.per - e0, 0), hi = min((g + 1) * a.per - e0, npl);
+        const int lo = max(g * a.per - h.e0, 0), hi = min((g + 1) * a.per - h.e0, npl);
 #pragma unroll 1
         for (int i = lo; i < hi; ++i) {
             t2 = max(t2, min(t1, sel[i]));
@@ -160,14 +171,16 @@ struct Candidate { float l, bias; int e, pad; };
 // the warp's own. (Every expert in 64 bits, eight to a lane: 4 us of a call's 33.)
 __device__ __noinline__ unsigned groups_near(const Args& a, const float* L, const float* v, Candidate* list, float gs, float t1, float t2,
                                              float lo, float hi, float tol) {
-    const int lane = threadIdx.x & 31, npl = a.npl, e0 = lane * npl, g = lane / a.lpg;
-    const bool is = g < a.groups, first = is && lane == g * a.lpg, near = is && gs >= lo && gs <= hi;
+    const int lane = threadIdx.x & 31, npl = a.npl, g = lane >> a.lpg_log;
+    const Held h = held_by(a, lane);
+    const bool is = g < a.groups, first = is && lane == g << a.lpg_log, near = is && gs >= lo && gs <= hi;
     const unsigned near_at = __ballot_sync(0xffffffffu, first && near), above_at = __ballot_sync(0xffffffffu, first && gs > hi);
     unsigned mine = 0u;                      // slots of this lane
     const float least = (a.best == 2 ? t2 : t1) - tol;
 #pragma unroll 1
-    for (int i = 0; i < npl; ++i)
-        if (near && e0 + i < a.E && v[i] >= least) mine |= 1u << i;
+    for (int i = 0; i < h.n; ++i)
+        if (near && v[i] >= least) mine |= 1u << i;
+    __syncwarp();
     int at = __popc(mine);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -181,7 +194,7 @@ __device__ __noinline__ unsigned groups_near(const Args& a, const float* L, cons
     }
     for (at -= __popc(mine); mine; mine &= mine - 1, ++at) {
         const int i = __ffs(mine) - 1;
-        list[at] = Candidate{L[i], a.bias ? a.bias[e0 + i] : 0.f, e0 + i, 0};
+        list[at] = Candidate{L[i], a.bias ? a.bias[h.e0 + i] : 0.f, h.e0 + i, 0};
     }
     const Norm norm = a.sigmoid ? Norm{0.0, 0.0} : exact_norm(L, npl);
     __syncwarp();
@@ -200,7 +213,7 @@ __device__ __noinline__ unsigned groups_near(const Args& a, const float* L, cons
             b1 = max(b1, o);
         }
     }
-    const int at_lane = min(lane * a.lpg, 31);
+    const int at_lane = min(lane << a.lpg_log, 31);
     const bool nearg = lane < a.groups && (near_at >> at_lane & 1u), aboveg = lane < a.groups && (above_at >> at_lane & 1u);
     const long long score = nearg ? (a.best == 2 ? order_of_sum(b1, b2) : b1) : kLeast;
     int rank = 0;
@@ -215,13 +228,14 @@ __device__ __noinline__ unsigned groups_near(const Args& a, const float* L, cons
 
 // The whole choice in 64 bits; returns lane j's choice j.
 __device__ __noinline__ int choose_exact(const Args& a, const float* L) {
-    const int lane = threadIdx.x & 31, npl = a.npl, e0 = lane * npl;
+    const int lane = threadIdx.x & 31, npl = a.npl;
+    const Held h = held_by(a, lane);
     long long sel[32];
     const unsigned kept = groups_exact(a, L, sel);
     unsigned taken = 0u;                     // slots of this lane that are out
 #pragma unroll 1
     for (int i = 0; i < npl; ++i) {
-        if (e0 + i >= a.E || !(kept >> ((e0 + i) / a.per) & 1u)) taken |= 1u << i;
+        if (i >= h.n || !(kept >> ((h.e0 + i) / a.per) & 1u)) taken |= 1u << i;
         if (!a.bias && L[i] > -INFINITY) sel[i] = order_of((double)L[i]);      // (ranked by the logits)
     }
     int my_id = 0;
@@ -231,14 +245,14 @@ __device__ __noinline__ int choose_exact(const Args& a, const float* L) {
         int id = 0x7fffffff;
 #pragma unroll 1
         for (int i = 0; i < npl; ++i)
-            if (!(taken >> i & 1u) && (id == 0x7fffffff || sel[i] > v)) { v = sel[i]; id = e0 + i; }
+            if (!(taken >> i & 1u) && (id == 0x7fffffff || sel[i] > v)) { v = sel[i]; id = h.e0 + i; }
 #pragma unroll 1
         for (int o = 16; o > 0; o >>= 1) {
             const long long ov = __shfl_xor_sync(0xffffffffu, v, o);
             const int oi = __shfl_xor_sync(0xffffffffu, id, o);
             if (oi != 0x7fffffff && (id == 0x7fffffff || ov > v || (ov == v && oi < id))) { v = ov; id = oi; }
         }
-        if (id / npl == lane) taken |= 1u << (id - e0);
+        if (id >= h.e0 && id < h.e0 + h.n) taken |= 1u << (id - h.e0);
         if (lane == j) my_id = id;
     }
     return my_id;
@@ -312,9 +326,9 @@ __device__ __forceinline__ void sort_keys(unsigned (&key)[N]) {
 // instructions, 850 a token. An argmax over unsorted slots in every round, with libm's exponential and division, took 45 us of
 // scores and rounds; the whole choice in 64 bits 50 us for the one token of some thousands that needs it. Two or four blocks an SM
 // instead of three: 30 and 31 us.)
-// FULL: E = 32 NPL, and a group a run of lanes whose number is a power of two.
+// FULL: every lane holds NPL experts.
 template <int NPL, bool FULL>
-__global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 3 : NPL == 16 ? 2 : 1)
+__global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 3 : NPL <= 16 ? 2 : 1)
 group_gate_kernel(const __grid_constant__ Args a) {
     constexpr int SB = NPL == 1 ? 0 : NPL == 2 ? 1 : NPL <= 4 ? 2 : NPL <= 8 ? 3 : NPL <= 16 ? 4 : 5;     // bits of a slot
     constexpr unsigned SLOT = (1u << SB) - 1;
@@ -327,8 +341,9 @@ group_gate_kernel(const __grid_constant__ Args a) {
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) s_hist[e] = 0;
     __syncthreads();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int npl = FULL ? NPL : a.npl, e0 = lane * npl;
-    auto live = [&](int i) { return FULL || (i < npl && e0 + i < a.E); };
+    const Held h = FULL ? Held{lane * NPL, NPL} : held_by(a, lane);
+    const int e0 = h.e0;
+    auto live = [&](int i) { return FULL || i < h.n; };
     float* row = s_P + (size_t)warp * a.E;
     float Pacc[NPL], bias[NPL], most = 0.f;  // most: the largest finite magnitude of the bias
 #pragma unroll
@@ -344,7 +359,7 @@ group_gate_kernel(const __grid_constant__ Args a) {
 #pragma unroll
         for (int i = 0; i < NPL; ++i) L[i] = -INFINITY;
         if (NPL % 4 == 0 && a.vec) {
-            if (FULL || e0 < a.E) {
+            if (FULL || h.n > 0) {
 #pragma unroll
                 for (int i = 0; i < NPL; i += 4) *reinterpret_cast<float4*>(L + i) = *reinterpret_cast<const float4*>(src + e0 + i);
             }
@@ -407,22 +422,11 @@ group_gate_kernel(const __grid_constant__ Args a) {
         if (a.top_groups < a.groups) {
             int g = lane;                     // this lane's group
             if (FULL || a.lpg) {
-                g = FULL ? lane >> a.lpg_log : lane / a.lpg;
-                const int pos = lane - g * a.lpg, g0 = lane - pos;
-                if (FULL || (a.lpg & (a.lpg - 1)) == 0) {
-                    for (int o = 1; o < a.lpg; o <<= 1) {
-                        const float b1 = __shfl_xor_sync(0xffffffffu, t1, o), b2 = __shfl_xor_sync(0xffffffffu, t2, o);
-                        t2 = fmaxf(fminf(t1, b1), fmaxf(t2, b2));
-                        t1 = fmaxf(t1, b1);
-                    }
-                } else {
-                    const float m1 = t1, m2 = t2;
-                    for (int o = 1; o < a.lpg; ++o) {
-                        const int from = g0 + (pos + o < a.lpg ? pos + o : pos + o - a.lpg);
-                        const float b1 = __shfl_sync(0xffffffffu, m1, from & 31), b2 = __shfl_sync(0xffffffffu, m2, from & 31);
-                        t2 = fmaxf(fminf(t1, b1), fmaxf(t2, b2));
-                        t1 = fmaxf(t1, b1);
-                    }
+                g = lane >> a.lpg_log;
+                for (int o = 1; o < a.lpg; o <<= 1) {
+                    const float b1 = __shfl_xor_sync(0xffffffffu, t1, o), b2 = __shfl_xor_sync(0xffffffffu, t2, o);
+                    t2 = fmaxf(fminf(t1, b1), fmaxf(t2, b2));
+                    t1 = fmaxf(t1, b1);
                 }
             } else {
                 __syncwarp();
@@ -438,7 +442,7 @@ group_gate_kernel(const __grid_constant__ Args a) {
             const float two = t1 + t2, gs = a.best == 1 ? t1 : two == two ? two : kMasked;      // (opposite infinities: as masked)
             int rank = 0;
             for (int o = 0; o < a.groups; ++o) {
-                const float v = __shfl_sync(0xffffffffu, gs, FULL ? o << a.lpg_log : a.lpg ? o * a.lpg : o);
+                const float v = __shfl_sync(0xffffffffu, gs, FULL || a.lpg ? o << a.lpg_log : o);
                 rank += v > gs || (v == gs && o < g);
             }
             const bool is = g < a.groups;
@@ -507,7 +511,7 @@ group_gate_kernel(const __grid_constant__ Args a) {
         int n = min(a.k + 1, left);                               // the k, and the first that is left out
 #pragma unroll 2
         for (int j = 0; j < n; ++j) take(j);
-        auto id_of = [&] { return my_owner * npl + (int)(SLOT - (my_key & SLOT)); };
+        auto id_of = [&] { return (FULL ? my_owner * NPL : held_by(a, my_owner).e0) + (int)(SLOT - (my_key & SLOT)); };
         int my_id = id_of();
         // whether two neighbours' order may be another than their keys'
         auto near = [&](unsigned hi, unsigned lo) {
@@ -763,7 +767,7 @@ int launch_gate(Args& a, int* G, cudaStream_t s) {
         of_ctx[dev] = context_id();
     }
     const size_t smem = smem_of(a.E);
-    a.vec = a.npl == NPL && NPL % 4 == 0 && a.E % 4 == 0 && aligned16(a.logits) && a.E % NPL == 0;
+    a.vec = a.npl == NPL && NPL % 4 == 0 && a.E % 4 == 0 && aligned16(a.logits) && a.per == a.lpg * NPL;
     *G = a.counts ? 1 : std::min(grid_of(a.T), per_sm[dev] * num_sms());
     return check_launch(launch_pdl(kernel, dim3(*G), dim3(kWarps * 32), smem, s, a), "group_gate_kernel");
 }
@@ -793,25 +797,29 @@ int launch_group_gate(const GroupGate& g, void* ws, cudaStream_t s) {
         a.T = g.T; a.E = g.E; a.k = g.k; a.groups = g.groups; a.per = g.E / g.groups; a.top_groups = g.top_groups; a.best = g.best;
         a.sigmoid = g.score == MOE_SCORE_SIGMOID; a.renorm = g.renorm; a.scale = g.scale;
         a.ids = g.ids; a.gates = g.gates; a.partial_P = w.partial_P; a.partial_C = w.partial_C; a.ticket = w.ticket;
-        // experts to a lane: as few as hold E, and a divisor of the group's size where one fits
-        const int least = cdiv(g.E, 32);
-        a.npl = least;
-        a.lpg = 0;
-        for (int n = least; n <= std::min(a.per, 32); ++n)
-            if (a.per % n == 0 && (n <= 8 || n < 2 * least)) { a.npl = n; a.lpg = a.per / n; break; }
+        if (a.top_groups == a.groups) {           // no choice of groups
+            a.groups = a.top_groups = 1;
+            a.per = a.E;
+        }
+        a.lpg_log = 0;
+        while (a.groups << (a.lpg_log + 1) <= 32) ++a.lpg_log;
+        a.lpg = 1 << a.lpg_log;
+        a.npl = cdiv(a.per, a.lpg);
+        if (a.npl > 32) {
+            a.lpg = a.lpg_log = 0;
+            a.npl = cdiv(a.E, 32);
+        }
         // up to two tokens a warp of one block: a second block and the finalize's launch cost more
         if (g.T <= 2 * kWarps) {
             a.counts = g.counts; a.f = g.f; a.P = g.P; a.aux = g.aux; a.alpha = g.alpha;
         }
-        a.lpg_log = 0;
-        while (1 << (a.lpg_log + 1) <= a.lpg) ++a.lpg_log;
-        const bool full = a.lpg == 1 << a.lpg_log && g.E == 32 * a.npl;
+        const bool full = a.lpg && g.E == 32 * a.npl;
 #define MOE_GATE(N) (full && a.npl == N ? launch_gate<N, true>(a, &G, s) : launch_gate<N, false>(a, &G, s))
-        // (npl 3, 5, 6, 12: 96, 160, 192, 384 experts; those of other sizes have predicates on every slot)
+        // (3 and 5: 96 and 160 experts, without predicates)
         const int rc = a.npl <= 1 ? MOE_GATE(1) : a.npl <= 2 ? MOE_GATE(2) : full && a.npl == 3 ? launch_gate<3, true>(a, &G, s)
-                     : a.npl <= 4 ? MOE_GATE(4) : full && a.npl == 5 ? launch_gate<5, true>(a, &G, s)
-                     : full && a.npl == 6 ? launch_gate<6, true>(a, &G, s) : a.npl <= 8 ? MOE_GATE(8)
-                     : full && a.npl == 12 ? launch_gate<12, true>(a, &G, s) : a.npl <= 16 ? MOE_GATE(16) : MOE_GATE(32);
+                     : a.npl <= 4 ? MOE_GATE(4) : full && a.npl == 5 ? launch_gate<5, true>(a, &G, s) : a.npl <= 6 ? MOE_GATE(6)
+                     : a.npl <= 8 ? MOE_GATE(8) : a.npl <= 12 ? MOE_GATE(12) : a.npl <= 16 ? MOE_GATE(16)
+                     : a.npl <= 24 ? MOE_GATE(24) : MOE_GATE(32);
 #undef MOE_GATE
         if (rc) return rc;
         if (a.counts) return MOE_OK;
