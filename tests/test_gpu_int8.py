@@ -564,3 +564,43 @@ def test_rows_that_start_on_no_boundary(gpu_lib, dtype, rows, K):
     want = (c.float() * s.unsqueeze(1)).to(x.dtype)
     assert torch.equal(out, want) and torch.equal(strided, want)
     assert (back[:32] == 5).all() and (back[32 + rows * K:] == 5).all() and (wide[:, K:] == 0).all()
+
+
+# 8, 4 and 2 CTAs to a tile (by its columns and the number of tiles), groups without rows, tiles of one row to sixteen, ragged columns
+@pytest.mark.parametrize("G,rows,N,K", [(1, 1, 96, 6528), (2, 16, 96, 6528), (2, 2, 32, 2720), (3, 7, 130, 4099), (1, 16, 128, 1024), (1, 40, 257, 3000),
+                                       (2, 30, 64, 16384), (5, 9, 384, 2048), (1, 16, 2000, 1500), (40, 12, 70, 5000), (1, 33, 1, 131072)])
+def test_long_rows_by_few_channels(gpu_lib, G, rows, N, K):
+    w, ws = weight(G, N, K, 5)
+    packed = gpu_lib.moe_int8_pack_weight(w)
+    off = offsets_of(rows, G, G)
+    for dtype in ("bf16", "fp32"):
+        x = data((rows, K), dtype, 6)
+        y = gpu_lib.moe_int8_linear(x, dev(off), packed, ws)
+        again = gpu_lib.moe_int8_linear(x, dev(off), packed, ws)
+        ok(gpu_lib)
+        c, s = Q.quantize(f64(x))
+        want = np.concatenate([(c[a:b].astype(float) @ w[g].cpu().numpy().astype(float).T) * s[a:b, None] * f64(ws)[g] for g, (a, b) in
+                               enumerate(zip(off[:-1], off[1:]))])
+        assert torch.equal(y, again)
+        near(y, want, dtype)
+
+
+@pytest.mark.parametrize("T", [1, 9])
+def test_an_ffn_of_few_channels_and_long_rows(gpu_lib, T):
+    E, h, F = 2, 96, 6528
+    gate, gs = weight(E, F, h, 1)
+    up, us = weight(E, F, h, 2)
+    down, ds = weight(E, h, F, 3)
+    packed = gpu_lib.moe_int8_pack_expert_weights(gate, up, down)
+    x = data((T, h), "bf16", T)
+    off = dev([0, T // 2, T])
+    y = gpu_lib.moe_int8_expert_ffn(x, off, packed, gs, us, ds)
+    # of its parts: the two products and the activation in fp32, quantised by rows
+    g = gpu_lib.moe_int8_linear(x, off, gpu_lib.moe_int8_pack_weight(gate), gs, out_dtype=torch.float32)
+    u = gpu_lib.moe_int8_linear(x, off, gpu_lib.moe_int8_pack_weight(up), us, out_dtype=torch.float32)
+    act = torch.nn.functional.silu(g.double()) * u.double()
+    want = gpu_lib.moe_int8_linear(act.float(), off, gpu_lib.moe_int8_pack_weight(down), ds, out_dtype=torch.float32).double()
+    ok(gpu_lib)
+    # an activation in another last bit moves a code by one step at most: 6528 of them, a hundredth near a border at the very most
+    step = act.abs().amax(1, keepdim=True) / 127 * 128 * ds.double().max()
+    assert ((y.double() - want).abs() <= want.abs() * HALF_STEP["bf16"] + 65 * step).all()

@@ -132,6 +132,9 @@ __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + ex
 // way; four groups of four warps, 32 channels to a warp, take them in turn (where every warp took a part of every stage, the waits and arrivals on
 // the stages' barriers cost more than the work). Their sums meet in shared memory in a fixed order. Groups with
 // more rows are passed over several times, the weights then coming from L2.
+//
+// SPLIT: where that leaves most SMs without a tile, a cluster of two to eight CTAs takes one, each a share of its columns (a tile of
+// 6528 columns is 51 stages by one SM); the CTAs' sums meet through distributed shared memory, in their order, each finishing some of the rows.
 constexpr int FEW_ROWS = 16, FEW_STAGES = 8, FEW_GROUPS = 4, FEW_WARPS = 4 * FEW_GROUPS, FEW_THREADS = 32 * (1 + FEW_WARPS);
 constexpr int FEW_PITCH = 33;                    // words of a row's 32 channels in shared memory
 constexpr int FEW_X_BYTES = FEW_ROWS * STAGE_K * 2, FEW_STAGE = 2 * (PIECE + FEW_X_BYTES);
@@ -163,6 +166,17 @@ __device__ __forceinline__ bool few_any(bool v) {
     return r != 0;
 }
 
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 struct FewRing {
     uint32_t sW, sX, bar0;
     volatile int* abort_flag;
@@ -172,11 +186,11 @@ struct FewRing {
     __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (FEW_STAGES + s); }
 };
 
-// One tile by one warp: the sums of its 32 channels x 8 NT rows over its group's stages, into `sum` [group][8 NT][FEW_PITCH] beside those of
+// One tile by one warp: the sums of its 32 channels x 8 NT rows over its group's stages of kb0 .. kb1 - 1, into `sum` [group][8 NT][FEW_PITCH] beside those of
 // the other groups, all of which are there on return. False: a wait ran out in some warp.
 template <int NT>
-__device__ __forceinline__ bool few_tile(const Params& p, FewRing& ring, int quarter, int group, float* sum) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, ns = (p.KST + 1) / 2;
+__device__ __forceinline__ bool few_tile(const Params& p, FewRing& ring, int quarter, int group, float* sum, int kb0, int kb1) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float acc[2][NT][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -185,7 +199,7 @@ __device__ __forceinline__ bool few_tile(const Params& p, FewRing& ring, int qua
     // chunk t of channel r is at row r ^ 2 t of the chunk (of eight lanes, two channels and four chunks, no two on a bank); r = 32 quarter + g + 8 i
     const uint32_t wat = (uint32_t)(t * BLOCK_N + ((quarter * 32 + g) ^ (2 * t))) * 16, xat = (uint32_t)(g * 128);
     bool ok = true;
-    for (int kb = 0; kb < ns; ++kb) {
+    for (int kb = kb0; kb < kb1; ++kb) {
         const int st = ring.stage;
         const uint32_t ph = ring.phase;
         if (++ring.stage == FEW_STAGES) { ring.stage = 0; ring.phase ^= 1u; }
@@ -228,7 +242,7 @@ __device__ __forceinline__ bool few_tile(const Params& p, FewRing& ring, int qua
     return !few_any(!ok);
 }
 
-template <int EPI>
+template <int EPI, bool SPLIT>
 __global__ void __launch_bounds__(FEW_THREADS, 1) few_rows_kernel(const __grid_constant__ CUtensorMap tm16, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -252,6 +266,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) few_rows_kernel(const __grid_c
     // (a programmatic dependent of the quantisation: the groups, the set-up and the first stages of weights do not wait for it)
     find_groups<FEW_THREADS>(p, FEW_ROWS, gs);               // (its barriers also stand between the set-up and the roles)
     const int total = uniform(gs.first[p.G] * p.NB), ns = (p.KST + 1) / 2;
+    // SPLIT: a cluster has one item at most, and whatever becomes of it, every thread meets the two barriers of the cluster
+    const int ranks = SPLIT ? (int)cluster_size() : 1, rank = SPLIT ? (int)cluster_rank() : 0;
+    const int first = (int)blockIdx.x / ranks, step = SPLIT ? total : (int)gridDim.x;
+    const int kb0 = ns * rank / ranks, kb1 = ns * (rank + 1) / ranks;      // (ns * ranks: at most 1024 * 8)
     // Item w: group by group, 128-channel block next, row tile fastest
     auto map = [&](int w, int& g, int& nb, int& row0, int& row1) {
         g = group_of(gs.first, p.G, p.NB, w, g);
@@ -264,7 +282,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) few_rows_kernel(const __grid_c
         int stage = 0, g = 0;
         uint32_t phase = 0, issued = 0, last_par = 0;
         bool ok = true;
-        for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
+        for (int w = first; w < total && ok; w += step) {
             int nb, row0, row1;
             map(w, g, nb, row0, row1);
             nb = uniform(nb); row0 = uniform(row0);
@@ -275,13 +293,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) few_rows_kernel(const __grid_c
                 bulk_elected(ring.sW + st * (2 * PIECE), w0 + (size_t)kb * (2 * PIECE), n * PIECE, ring.full(st));
             };
             int early = 0;
-            if (w == (int)blockIdx.x) {
-                for (; early < min(FEW_STAGES, ns); ++early) weights(early, early);
+            if (w == first) {
+                for (; early < min(FEW_STAGES, kb1 - kb0); ++early) weights(early, kb0 + early);
                 pdl_wait();
                 pdl_trigger();
             }
-            for (int kb = 0; kb < ns; ++kb) {
-                if (kb >= early) {
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (kb >= kb0 + early) {
                     ok = test_warp(ring.empty(stage), phase ^ 1u) ||
                          wait_warp(ring.empty(stage), phase ^ 1u, p.wait_limit, ring.abort_flag, p.err, 0x380u);
                     if (!ok) break;
@@ -294,7 +312,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) few_rows_kernel(const __grid_c
                 if (++stage == FEW_STAGES) { stage = 0; phase ^= 1u; }
             }
         }
-        if (total <= (int)blockIdx.x) {          // (no item: the wait that every thread makes)
+        if (total <= first) {                    // (no item: the wait that every thread makes)
             pdl_wait();
             pdl_trigger();
         }
@@ -302,12 +320,48 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) few_rows_kernel(const __grid_c
             for (int s = 0; s < FEW_STAGES; ++s)    // every issued copy has landed before the CTA exits
                 if (issued & (1u << s)) drain_phase(ring.full(s), (last_par >> s) & 1u, p.err, 0x381u);
         __syncwarp();
+        if constexpr (SPLIT) {
+            cluster_sync_all();
+            cluster_sync_all();
+        }
         return;
     }
     pdl_wait();
     pdl_trigger();
     const int quarter = warp & 3, group = warp >> 2;
     int g = 0;
+    if constexpr (SPLIT) {
+        const bool some = first < total;
+        int nb = 0, row0 = 0, row1 = 0;
+        if (some) map(first, g, nb, row0, row1);
+        const int nt = row1 - row0, n = nb * BLOCK_N + quarter * 32 + lane, F = p.N / 2, f = n >> 1;
+        float* sum = s_sum + quarter * (FEW_ROWS * FEW_PITCH);
+        float scale = 0.f;
+        if (some && n < p.N) scale = EPI == EPI_OUT ? p.w_scales[(size_t)g * p.N + n] : ((n & 1) ? p.w_scales_up : p.w_scales)[(size_t)g * F + f];
+        bool ok = false;
+        if (some) ok = nt <= 8 ? few_tile<1>(p, ring, quarter, group, sum, kb0, kb1) : few_tile<2>(p, ring, quarter, group, sum, kb0, kb1);
+        cluster_sync_all();                      // every CTA's sums are there
+        if (ok && n - lane < p.N) {
+            for (int t = rank + ranks * group; t < nt; t += ranks * FEW_GROUPS) {
+                const float xs = p.a_scales[row0 + t];
+                float v = 0.f;
+                for (int r = 0; r < ranks; ++r) {
+                    const uint32_t at = map_rank(smem_u32(sum + t * FEW_PITCH + lane), r);
+#pragma unroll
+                    for (int j = 0; j < FEW_GROUPS; ++j) v += ld_cluster(at + j * (FEW_SUM * 4));
+                }
+                v = v * xs * scale;
+                if constexpr (EPI == EPI_OUT) {
+                    if (n < p.N) store_value(p, (row0 + t) * p.ld + n, v);
+                } else {
+                    const float u = __shfl_down_sync(0xffffffffu, v, 1);
+                    if (!(n & 1) && n < p.N) static_cast<float*>(p.out)[(row0 + t) * p.ld + f] = swiglu(v, u);
+                }
+            }
+        }
+        cluster_sync_all();                      // and have been read
+        return;
+    }
     for (int w = blockIdx.x; w < total; w += gridDim.x) {
         int nb, row0, row1;
         map(w, g, nb, row0, row1);
@@ -320,7 +374,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) few_rows_kernel(const __grid_c
         if (n < p.N) scale = EPI == EPI_OUT ? p.w_scales[(size_t)g * p.N + n] : ((n & 1) ? p.w_scales_up : p.w_scales)[(size_t)g * F + f];
 #pragma unroll
         for (int i = 0; i < FEW_ROWS / FEW_GROUPS; ++i) xs[i] = p.a_scales[row0 + min(group + i * FEW_GROUPS, nt - 1)];
-        const bool ok = nt <= 8 ? few_tile<1>(p, ring, quarter, group, sum) : few_tile<2>(p, ring, quarter, group, sum);
+        const bool ok = nt <= 8 ? few_tile<1>(p, ring, quarter, group, sum, 0, ns) : few_tile<2>(p, ring, quarter, group, sum, 0, ns);
         if (!ok) break;
         if (n - lane < p.N) {                    // 32 channels of the group's share of the rows
 #pragma unroll
@@ -732,22 +786,70 @@ static int launch_pairs(const Params& p, cudaStream_t s) {
     return launch_pair<EPI, 256>(p, s);
 }
 
-template <int EPI>
-static int launch_few(const Params& p, cudaStream_t s) {
+// Tiles of a call at most.
+static long long most_tiles(const Params& p) {
+    const long long used = std::min(p.G, p.rows);
+    return ((p.rows - used) / FEW_ROWS + used) * p.NB;
+}
+
+template <int EPI, bool SPLIT>
+static int launch_few_as(const Params& p, int ranks, cudaStream_t s) {
+    const auto kernel = few_rows_kernel<EPI, SPLIT>;
     static unsigned long long attr_ctx[64];
+    static int resident[64][9];                  // clusters of 2, 4 and 8 at once
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return set_error(MOE_ERR_CUDA, "int8 product: no usable current device");
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
     const unsigned long long ctx = context_id();
     if (ctx == 0 || attr_ctx[dev] != ctx) {
-        const cudaError_t e = cudaFuncSetAttribute(few_rows_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM);
         if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "int8 product smem attribute: %s", cudaGetErrorString(e));
+        for (int r = 2; SPLIT && r <= 8; r *= 2) {
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = r;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3(num_sms() / r * r);
+            cfg.blockDim = dim3(FEW_THREADS);
+            cfg.dynamicSmemBytes = FEW_SMEM;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&resident[dev][r], kernel, &cfg) != cudaSuccess) {
+                (void)cudaGetLastError();
+                resident[dev][r] = 0;
+            }
+        }
         attr_ctx[dev] = context_id();
+    }
+    if constexpr (SPLIT) {
+        while (ranks > 1 && most_tiles(p) > resident[dev][ranks]) ranks /= 2;
+        if (ranks == 1) return launch_few_as<EPI, false>(p, 1, s);
     }
     CUtensorMap m16;
     if (int rc = rows_map(&m16, p.a, p.rows, p.KST * STAGE_K, 16)) return rc;
-    const long long most = ((long long)cdiv(p.rows, FEW_ROWS) + std::min(p.G, p.rows)) * p.NB;
-    return check_launch(launch_pdl(few_rows_kernel<EPI>, dim3((unsigned)std::min<long long>(most, num_sms())), dim3(FEW_THREADS), FEW_SMEM, s, m16, p),
-                        EPI == EPI_SWIGLU ? "int8 few_rows_kernel<swiglu>" : "int8 few_rows_kernel");
+    cfg.gridDim = dim3((unsigned)(SPLIT ? most_tiles(p) * ranks : std::min<long long>(most_tiles(p), num_sms())));
+    cfg.blockDim = dim3(FEW_THREADS);
+    cfg.dynamicSmemBytes = FEW_SMEM;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = SPLIT ? 2 : 1;
+    return check_launch(cudaLaunchKernelEx(&cfg, kernel, m16, p), EPI == EPI_SWIGLU ? "int8 few_rows_kernel<swiglu>" : "int8 few_rows_kernel");
+}
+// CTAs to a tile: as many as leave each four stages of columns, and all clusters resident at once; one where a tile's columns are no more
+// than the stages under way. Rows by channels x columns, us by one CTA and split: 16 by 96 x 6528 17.6 / 8.1, 8 by 192 x 7168 16.9 / 7.1, 16 by
+// 4096 x 4096 12.8 / 8.7, 8 by 2048 x 2048 7.7 / 6.2; but 8 by 1024 x 1024 5.6 / 6.2, and 60 by 512 x 4096 in more clusters than are resident
+// 12.8 / 14.0.
+template <int EPI>
+static int launch_few(const Params& p, cudaStream_t s) {
+    int ranks = 1;
+    const int stages = (p.KST + 1) / 2;
+    while (stages > FEW_STAGES && ranks < 8 && most_tiles(p) * 2 * ranks <= num_sms() && stages >= 2 * ranks * 4) ranks *= 2;
+    return ranks > 1 ? launch_few_as<EPI, true>(p, ranks, s) : launch_few_as<EPI, false>(p, 1, s);
 }
 
 template <int EPI>
@@ -758,7 +860,7 @@ static int launch_product(const Params& p, cudaStream_t s) {
     // 8: 69 / 73, 16: 76 / 76, and 16 unevenly 104 / 78), and where its tiles are no more than the SMs: pairs take longer to start (16 rows by
     // 4096 x 4096: 13.7 / 16.7).
     const long long used = std::min(p.G, p.rows);
-    return p.rows / used <= 8 || ((p.rows - used) / FEW_ROWS + used) * p.NB <= num_sms() ? launch_few<EPI>(p, s) : launch_pairs<EPI>(p, s);
+    return p.rows / used <= 8 || most_tiles(p) <= num_sms() ? launch_few<EPI>(p, s) : launch_pairs<EPI>(p, s);
 }
 
 // A row operand in the workspace: codes (room for fp16), then the rows' scales.
