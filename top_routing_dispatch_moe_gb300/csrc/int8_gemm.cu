@@ -269,6 +269,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) few_rows_kernel(const __grid_c
     // SPLIT: a cluster has one item at most, and whatever becomes of it, every thread meets the two barriers of the cluster
     const int ranks = SPLIT ? (int)cluster_size() : 1, rank = SPLIT ? (int)cluster_rank() : 0;
     const int first = (int)blockIdx.x / ranks, step = SPLIT ? total : (int)gridDim.x;
+    if (SPLIT && total > (int)gridDim.x / ranks && blockIdx.x == 0 && threadIdx.x == 0)       // (a schedule whose groups overlap)
+        latch_device_error(p.err, kDevErrBadIndex, 0x322u);
     const int kb0 = ns * rank / ranks, kb1 = ns * (rank + 1) / ranks;      // (ns * ranks: at most 1024 * 8)
     // Item w: group by group, 128-channel block next, row tile fastest
     auto map = [&](int w, int& g, int& nb, int& row0, int& row1) {
