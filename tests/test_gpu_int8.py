@@ -604,3 +604,26 @@ def test_an_ffn_of_few_channels_and_long_rows(gpu_lib, T):
     # an activation in another last bit moves a code by one step at most: 6528 of them, a hundredth near a border at the very most
     step = act.abs().amax(1, keepdim=True) / 127 * 128 * ds.double().max()
     assert ((y.double() - want).abs() <= want.abs() * HALF_STEP["bf16"] + 65 * step).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows,K", [(1, 16), (300, 16), (77, 32), (1000, 48), (33, 64), (5, 112), (129, 128), (64, 144), (17, 240), (40, 256), (9, 272)])
+def test_short_rows(gpu_lib, dtype, rows, K):
+    """Several rows to a warp; an infinite row and one of zeros between others, rows named by src, and as a product's operand."""
+    x = data((rows, K), dtype, K, 2.0)
+    if rows > 4:
+        x[1, K - 1], x[3] = float("inf"), 0.0
+    src = torch.randint(-1, rows, (2 * rows + 1,), generator=torch.Generator().manual_seed(K)).int().cuda()
+    code, scale = Q.quantize(f64(x))
+    c, s = gpu_lib.moe_int8_quantize(x)
+    cs, ss = gpu_lib.moe_int8_quantize(x, src=src)
+    ok(gpu_lib)
+    np.testing.assert_array_equal(c.cpu().numpy(), code)
+    np.testing.assert_array_equal(f64(s), scale)
+    at, none = src.clamp(min=0).long(), src < 0
+    assert torch.equal(cs, torch.where(none[:, None], 0, c[at]).to(torch.int8))
+    np.testing.assert_array_equal(f64(ss), f64(torch.where(none, 0.0, s[at])))
+    w, ws = weight(1, 24, K, 3)
+    y = gpu_lib.moe_int8_linear(x, dev([0, rows]), gpu_lib.moe_int8_pack_weight(w), ws)
+    near(y, (code.astype(float) @ w[0].cpu().numpy().astype(float).T) * scale[:, None] * f64(ws)[0], dtype)
+    ok(gpu_lib)

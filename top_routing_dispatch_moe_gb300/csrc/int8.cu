@@ -132,6 +132,34 @@ quantize_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, int r
     }
 }
 
+// Rows of up to 256 columns: 1, 2, 4, 8 or 16 lanes (1 << lanes_log) to a row. (65536 x 96 bf16 4.5 us,
+// x 256 8.4; by a warp a row 17.6 and 20.)
+template <typename T, int FORM>
+__global__ void __launch_bounds__(THREADS)
+quantize_short_kernel(const T* x, long long ldx, int x_rows, const int32_t* src, int rows, int K, int width, int lanes_log, void* codes,
+                      float* scales, unsigned* err) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, in_row = lane & ((1 << lanes_log) - 1), skip = (lane - in_row) * UNIT;
+    const int row = (int)(blockIdx.x * (THREADS >> lanes_log) + (threadIdx.x >> lanes_log));
+    int from = row < rows ? row : -1;
+    if (from >= 0 && src) {
+        from = src[row];
+        if (from >= x_rows || from < -1) {
+            if (in_row == 0) latch_device_error(err, kDevErrBadIndex, 0x310u);
+            from = -1;
+        }
+    }
+    const Raw16<T> raw = load_piece<T, WHOLE>(x + (long long)max(from, 0) * ldx, 0, from >= 0 ? K : 0, skip, src != nullptr);
+    float amax = unit_amax(raw);
+    for (int o = 1 << lanes_log >> 1; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (row >= rows) return;
+    Steps st;
+    const float scale = scale_of<T>(amax, st);
+    if (in_row == 0) scales[row] = scale;
+    store_piece<T, FORM, WHOLE>(raw, codes, (size_t)row * width, 0, width, skip, st);
+}
+
 // BLOCKS: a scale for 128 columns (a checkpoint) instead of one for a row.
 template <typename T, bool VEC, bool BLOCKS>
 __global__ void __launch_bounds__(THREADS)
@@ -191,7 +219,8 @@ dequantize_kernel(const int8_t* codes, const float* scales, int rows, int K, T* 
     }
 }
 
-// Contiguous rows of any width from 16 on (a scale a row): 16 elements a lane across the rows' ends, two scales at most.
+// Contiguous rows of any width from 16 on (a scale a row): 16 elements a lane across the rows' ends, two scales at most. For widths that are
+// no whole units, and for short rows.
 template <typename T>
 __global__ void __launch_bounds__(THREADS)
 dequantize_flat_kernel(const int8_t* codes, const float* scales, long long total, int K, T* out) {
@@ -227,8 +256,14 @@ dequantize_flat_kernel(const int8_t* codes, const float* scales, long long total
             alignas(16) T o[UNIT];
 #pragma unroll
             for (int j = 0; j < UNIT; ++j) o[j] = rounded<T>(v[j] * (j < here[u] ? s0[u] : s1[u]));
+            const uint4* ov = reinterpret_cast<const uint4*>(o);
+            if ((reinterpret_cast<uintptr_t>(to) & 31u) == 0) {
 #pragma unroll
-            for (int j = 0; j < (int)sizeof(T); ++j) reinterpret_cast<uint4*>(to)[j] = reinterpret_cast<const uint4*>(o)[j];
+                for (int j = 0; j < (int)sizeof(T); j += 2) st32(reinterpret_cast<uint4*>(to) + j, ov + j);
+            } else {
+#pragma unroll
+                for (int j = 0; j < (int)sizeof(T); ++j) reinterpret_cast<uint4*>(to)[j] = ov[j];
+            }
         }
     }
     // the last elements, less than a unit (all of the last row)
@@ -275,6 +310,12 @@ static cudaError_t quantize_form(const void* x, long long ldx, int x_rows, const
     };
     // a row's warps: as many as hold it four pieces each (16384 x 3001 fp32, six pieces, by eight warps instead of two 110 us, not 60)
     const int pieces = (width + SEG - 1) / SEG;
+    if (vec && width <= SEG / 2) {
+        int lanes_log = 0;
+        while (UNIT << lanes_log < width) ++lanes_log;
+        return launch_pdl(quantize_short_kernel<T, FORM>, dim3(cdiv(rows, THREADS >> lanes_log)), dim3(THREADS), 0, s, xt, ldx, x_rows, src, rows,
+                          K, width, lanes_log, codes, scales, err);
+    }
     if (vec) {
         if (pieces <= HELD) return go(quantize_kernel<T, FORM, 1, WHOLE>, 1);
         if (pieces <= 2 * HELD) return go(quantize_kernel<T, FORM, 2, WHOLE>, 2);
@@ -321,7 +362,8 @@ static cudaError_t dequantize_form(const void* codes, const float* scales, int r
     return blocks ? go(dequantize_kernel<T, VEC, true>) : go(dequantize_kernel<T, VEC, false>);
 }
 
-// (4099 x 999 fp16 5.4 -> 3.7 us, 65536 x 999 69 -> 33; before, a lane took every 32nd column.)
+// (4099 x 999 fp16 5.4 -> 3.1 us, 65536 x 999 fp16 69 -> 33, fp32 73 -> 54: before, a lane took every 32nd column; 65536 x 96 bf16 9.0 -> 4.1:
+// before, a warp took a row.)
 template <typename T>
 static cudaError_t dequantize_flat(const void* codes, const float* scales, int rows, int K, void* out, cudaStream_t s) {
     const long long total = (long long)rows * K, units = (total + UNIT - 1) / UNIT;
@@ -331,7 +373,7 @@ static cudaError_t dequantize_flat(const void* codes, const float* scales, int r
 }
 
 int launch_dequantize(const void* codes, const float* scales, int rows, int K, int dtype, void* out, long long ldo, bool blocks, cudaStream_t s) {
-    const bool flat = !blocks && K % UNIT != 0 && K > UNIT && ldo == K && aligned16(codes) && aligned16(out);
+    const bool flat = !blocks && (K % UNIT != 0 || K <= SEG / 2) && K >= UNIT && ldo == K && aligned16(codes) && aligned16(out);
     const bool vec = K % UNIT == 0 && aligned16(codes) && aligned16(out) && ldo * (dtype == MOE_F32 ? 4 : 2) % 16 == 0;
     cudaError_t e = cudaErrorInvalidValue;
 #define MOE_DEQUANT(T)                                                                     \
