@@ -450,11 +450,16 @@ group_gate_kernel(const __grid_constant__ Args a) {
             const float x = value_of(__reduce_min_sync(0xffffffffu, stays ? key_of(gs) : 0xffffffffu)),
                         y = value_of(__reduce_max_sync(0xffffffffu, is && !stays ? key_of(gs) : 0u));
             // the last that stays and the first that does not: two scores' errors each, and the roundings of their sums with the bias (which
-            // may leave a small sum of large terms) and of the groups'. Without a bias the errors are relative to the scores
-            // (softmax: one unit of the exponent's rounding for each of the logits' distance).
+            // may leave a small sum of large terms) and of the groups'.
             // (Finite: infinite sums are equal, and above all others.)
+            // Without a bias the errors are relative to the scores: 5e-7 for the exponential, the quotient and the sums; and the exponential's
+            // argument is off by 7.3e-8 of itself (sigmoid: log2(e) and the product, rounded) or 1.35e-7 (softmax: the difference of the logits
+            // too), which is the error of its power for each unit. The argument is the score's logarithm, at most one more
+            // than that of the group's; an exponential below 2^-126 is 0. (The differences of all groups above or below these two are larger than
+            // their errors likewise: the error grows more slowly than the score.)
+            const float below = fmaxf(-__log2f(fmaxf(y, 1.2e-38f)), 0.f);        // bits of y below 1
             const float tol = a.bias ? fminf(4.f * (serr + 7e-8f * (1.f + most)) + 1.3e-7f * (fabsf(x) + fabsf(y)), 3e38f)
-                                     : (a.sigmoid ? 1e-6f : 4e-6f) * (x + y);
+                                     : (1.6e-6f + (a.sigmoid ? 1.4e-7f : 2.5e-7f) * below) * x + 5e-38f;
             // (groups without a live expert, or with one less than `best`, have whole multiples of the masked score: equal)
             bool undecided = !(x - y > tol) && x > 0.1f * kMasked;
             if (undecided && (FULL || a.lpg) && x == y) {
