@@ -124,13 +124,13 @@ int moe_router_from_logits(const float* logits, const float* bias, int T, int E,
  *   sel (-1e30 where those are opposite infinities); the top_groups groups with the largest scores stay, and topk_ids are the
  *   k experts of those with the largest sel, by falling sel. Equal scores: lower index. The choice is that of exact scores, not of rounded ones: what 32 bits cannot
  *   tell apart is compared in 64; without a bias the experts are ranked by their logits.
- *   gates[t,j] = scale * s, with renorm scale * s / (sum of the chosen s), 0 where that sum is 0 (all masked).
- *   counts, f, aux as moe_router; P the mean of softmax(L), or of s_e / sum s (0 for a token whose experts are all masked).
+ *   gates[t,j] = scale * s, with renorm scale * s / (sum of the chosen s), 0 where all of those are below e^-700 (masked ones are 0).
+ *   counts, f, aux as moe_router; P the mean of softmax(L), or of s_e / sum s (0 for a token whose scores are all below e^-700).
  *   Under softmax, a NaN or +inf logit makes its token's gates and P NaN.
  * moe_group_route: on given fp32 logits [T,E]. moe_group_router: from x [T,h] and the packed router weight
  *   (moe_pack_router_weight), the logits as moe_router_packed computes them, without a bias in them; logits [T,E] may be NULL.
  * moe_group_route_backward: d_logits [T,E] fp32 from d_gates [T,k] and d_aux, the choice held fixed (the bias gets none):
- *     ds_j = scale d_g_j, with renorm scale (d_g_j - sum_i d_g_i s_i / S) / S, S = sum_i s_i (0 where S is 0)
+ *     ds_j = scale d_g_j, with renorm scale (d_g_j - sum_i d_g_i s_i / S) / S, S = sum_i s_i (0 where all s_i are below e^-700)
  *     c_e = d_aux alpha E f_e / T;  softmax: dp = ds + c, d_logits = p (dp - <dp, p>);
  *     sigmoid: d_logits = (ds + (c - <c, q>) / sum s) s (1 - s), q = s / sum s.
  *   An id outside [0, E) counts as none and is reported by moe_check_device_error.

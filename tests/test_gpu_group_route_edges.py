@@ -63,3 +63,90 @@ def test_a_group_that_leads_in_32_bits_alone(gpu_lib):
         want = O.route(L.astype(np.float64), None, 2, 2, 1, "sigmoid", 2, True, 1.0)
         assert (want["ids"] >= 2).all()
         np.testing.assert_array_equal(r["topk_ids"].cpu().numpy(), want["ids"])
+
+
+def far_logits(T, E, chosen, distance, score, seed):
+    """Logits whose `chosen` experts have scores near exp(-distance): under softmax that far below the others, under sigmoid with all of them
+    (another expert's score would be the sum's)."""
+    L = torch.randn(T, E, generator=torch.Generator().manual_seed(seed)).numpy()
+    if score == "sigmoid":
+        return L - np.float32(distance)
+    L[:, chosen] -= np.float32(distance)
+    return L
+
+
+@pytest.mark.parametrize("distance", [0.0, 60.0, 69.5, 80.0, 84.0, 87.0, 88.0, 95.0, 104.0, 200.0, 690.0])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,groups", [(3, 8, 1), (70, 64, 8), (40, 320, 4)])
+def test_renormalised_gates_and_their_gradient_at_any_distance(gpu_lib, T, E, groups, score, distance):
+    """A bias chooses experts whose scores, or their sum, are below fp32's normal range: the gates are their shares all the same."""
+    k, chosen = 4, [1, 3, 4, 6]
+    L = far_logits(T, E, chosen, distance, score, E)
+    b = np.zeros(E, np.float32)
+    b[chosen] = 2.0
+    r = gpu_lib.moe_group_route(torch.from_numpy(L).cuda(), torch.from_numpy(b).cuda(), k, groups, 1, score=score, scale=2.5)
+    ok(gpu_lib)
+    L64 = L.astype(np.float64)
+    want = O.route(L64, b, k, groups, 1, score, 2, True, 2.5)
+    assert (np.sort(want["ids"], 1) == chosen).all()
+    np.testing.assert_array_equal(r["topk_ids"].cpu().numpy(), want["ids"])
+    # exponentials (4 half steps each, and 2 for each unit of their argument, up to 2^-100: 70), the sums of k and the quotient
+    rel = (32 + 2 * min(distance + 8, 80)) * EPS
+    np.testing.assert_allclose(r["gates"].double().cpu().numpy(), want["gates"], rtol=rel, atol=1e-37)
+    dg = torch.randn(T, k, generator=torch.Generator().manual_seed(7))
+    f = r["f"].double().cpu().numpy()
+    for d_aux in (0.0, 0.7):
+        d = gpu_lib.moe_group_route_backward(torch.from_numpy(L).cuda(), r["topk_ids"], dg.cuda(), r["f"], score=score, scale=2.5, alpha=0.5, d_aux=d_aux)
+        ok(gpu_lib)
+        dwant = O.backward(L64, want["ids"], dg.double().numpy(), f, score, True, 2.5, 0.5, d_aux)
+        # the gates' part: share times a difference of gates' gradients; the balance loss's: share of all scores times coefficients
+        s = O.scores(L64, score)
+        share = np.zeros_like(s)
+        np.put_along_axis(share, want["ids"], want["gates"], 1)
+        big = share * 2 * np.abs(dg.numpy()).max() + d_aux * 0.5 * E / T * s / s.sum(1, keepdims=True) * 2
+        # (under softmax <dp, p> holds all of the chosen experts' terms, which cancel: in the ordinary case to roundings of their largest)
+        big += s * big.max(1, keepdims=True)
+        assert (np.abs(d.double().cpu().numpy() - dwant) <= (2 * rel + (96 + E) * EPS) * big + 1e-37).all()
+
+
+def test_renormalised_gates_where_nothing_is_chosen_alive(gpu_lib):
+    """Masked experts, and scores that 64 bits do not hold either: gates 0, and no gradient from them."""
+    for low in (-float("inf"), -3.4e38, -1000.0):
+        for score in ("sigmoid", "softmax"):
+            L = torch.zeros(20, 64)
+            L[:, :32] = low
+            b = torch.zeros(64)
+            b[:32] = 5.0
+            r = gpu_lib.moe_group_route(L.cuda(), b.cuda(), 4, 2, 1, score=score, best=1) if low != -float("inf") else \
+                gpu_lib.moe_group_route(torch.full_like(L, low).cuda(), b.cuda(), 4, 2, 1, score=score, best=1)
+            ok(gpu_lib)
+            assert (r["topk_ids"].cpu() == torch.arange(4)).all() and (r["gates"] == 0).all(), (low, score)
+            d = gpu_lib.moe_group_route_backward(L.cuda(), r["topk_ids"], torch.randn(20, 4).cuda(), r["f"], score=score, d_aux=0.0)
+            assert (d == 0).all(), (low, score)
+
+
+@pytest.mark.parametrize("distance", [0.0, 60.0, 75.0, 86.0, 88.0, 104.0, 300.0, 690.0])
+@pytest.mark.parametrize("T,E", [(5, 8), (60, 96), (30, 320), (2, 1024)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_shares_of_sigmoid_scores_that_are_all_small(gpu_lib, T, E, distance, renorm):
+    """P, the balance loss and its gradient are of s_e / sum s, whatever the sum."""
+    g = torch.Generator().manual_seed(E)
+    L = torch.randn(T, E, generator=g) - distance
+    L[:, torch.rand(E, generator=g) < 0.2] = -float("inf")
+    L[:, :2] = torch.randn(T, 2, generator=g) - distance
+    L64 = L.double().numpy()
+    r = gpu_lib.moe_group_route(L.cuda(), None, 2, 1, 1, renorm=renorm)
+    ok(gpu_lib)
+    want = O.route(L64, None, 2, 1, 1, "sigmoid", 2, renorm, 1.0)
+    # a score's exponential (2 half steps a unit of its argument up to where 64 bits take over, 70) and quotient, sums of E / 32 + 5 terms and of T
+    rel = (32 + 2 * min(distance + 8, 80) + E / 32 + T) * EPS
+    np.testing.assert_array_equal(r["topk_ids"].cpu().numpy(), want["ids"])
+    np.testing.assert_allclose(r["P"].double().cpu().numpy(), want["P"], rtol=rel, atol=1e-37)
+    np.testing.assert_allclose(r["aux"].item(), want["aux"], rtol=rel + E * EPS)
+    d = gpu_lib.moe_group_route_backward(L.cuda(), r["topk_ids"], torch.zeros(T, 2).cuda(), r["f"], renorm=renorm, alpha=0.5, d_aux=0.7)
+    ok(gpu_lib)
+    f = r["f"].double().cpu().numpy()
+    dwant = O.backward(L64, want["ids"], np.zeros((T, 2)), f, "sigmoid", renorm, 1.0, 0.5, 0.7)
+    s = O.scores(L64, "sigmoid")
+    big = 0.35 * E / T * s / s.sum(1, keepdims=True) * 2
+    assert (np.abs(d.double().cpu().numpy() - dwant) <= 2 * rel * big + 1e-37).all()

@@ -4,7 +4,7 @@
 //   s = sigmoid(L) or softmax(L);  sel_e = s_e + bias_e, -1e30 where L_e = -inf (a masked expert) or is NaN
 //   score of a group = the sum of its `best` (1 or 2) largest sel; the top_groups best groups stay, equal scores: lower index
 //   the k experts of those groups with the largest sel, equal ones: lower index
-//   gate_j = scale * s_j, or scale * s_j / (sum of the chosen s) (0 where that sum is 0)
+//   gate_j = scale * s_j, or scale * s_j / (sum of the chosen s) (0 where all of them are below e^-700)
 // The choice is that of exact scores: two scores that 32 bits cannot tell apart are compared in 64. Without a bias the
 // experts are ranked by the logits themselves (both scores rise with them), which needs no such comparison.
 //
@@ -300,6 +300,17 @@ __device__ __forceinline__ float rcp(float x) {
 }
 constexpr float kLog2e = 1.44269504f;
 
+// A sum of scores below this, 2^-100, may have lost some of them (they are 0 below 2^-126), and its reciprocal may be infinite. Shares in
+// it are formed from exp(L - the largest L) instead, to which scores that small are proportional (1 + exp(L) is 1), if the largest score is
+// above e^kNoScore. Tokens with such a sum, but for a router's gates, are noted and seen to after the others: in their place the branches
+// held up every token (backward of 16384 x 256 9.5 -> 10.5 us).
+constexpr float kSmallSum = 7.8886e-31f, kNoScore = -700.f;
+// The share of this lane's logit (-inf: none) in the sum of the warp's scores; unit: the logit whose score would be 1.
+__device__ __forceinline__ float share_of(float l, float unit) {
+    const float top = warp_max(l), s = top - unit > kNoScore ? ex2((l - top) * kLog2e) : 0.f, sum = warp_sum(s);
+    return sum == 0.f ? 0.f : s * rcp(sum);
+}
+
 // Keys by falling order (Batcher's merge exchange).
 template <int N>
 __device__ __forceinline__ void sort_keys(unsigned (&key)[N]) {
@@ -353,6 +364,7 @@ group_gate_kernel(const __grid_constant__ Args a) {
         if (fabsf(bias[i]) < INFINITY) most = fmaxf(most, fabsf(bias[i]));
     }
     if (a.bias) most = warp_max(most);
+    bool empty = false;                       // a token whose scores have a small sum
     for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
         float L[NPL], s[NPL];                                        // logits, scores
         const float* src = a.logits + (size_t)t * a.E;
@@ -393,7 +405,8 @@ group_gate_kernel(const __grid_constant__ Args a) {
             total += s[i];
         }
         total = warp_sum(total);
-        const float inv = total == 0.f ? 0.f : rcp(total);
+        const float inv = total < kSmallSum ? 0.f : rcp(total);      // (softmax's total is 1 or more, or 0 where all are masked)
+        empty = empty || total < kSmallSum;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) Pacc[i] += s[i] * inv;
         if (!a.sigmoid) {
@@ -578,7 +591,8 @@ group_gate_kernel(const __grid_constant__ Args a) {
         if (lane < a.k && !(my_l == -INFINITY)) my_s = a.sigmoid ? rcp(1.f + ex2(-kLog2e * my_l)) : ex2((my_l - m) * kLog2e) * inv;
         if (a.renorm) {
             const float sum = warp_sum(my_s);
-            my_s = sum == 0.f ? 0.f : my_s * rcp(sum);
+            if (sum < kSmallSum) my_s = share_of(lane < a.k ? my_l : -INFINITY, a.sigmoid ? 0.f : m);
+            else my_s *= rcp(sum);
         }
         if (lane < a.k) {
             a.ids[(size_t)t * a.k + lane] = my_id;
@@ -590,6 +604,29 @@ group_gate_kernel(const __grid_constant__ Args a) {
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
         if (live(i)) row[e0 + i] = Pacc[i];
+    if (empty && a.sigmoid) {                 // the shares of such tokens' scores
+        for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
+            const float* src = a.logits + (size_t)t * a.E;
+            float l[NPL], top = -INFINITY, total = 0.f;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                l[i] = live(i) ? src[e0 + i] : -INFINITY;
+                for (int q = 1; q < a.nparts; ++q)
+                    if (live(i)) l[i] += src[q * a.part_stride + e0 + i];
+                top = fmaxf(top, l[i]);
+                total += rcp(1.f + ex2(-kLog2e * l[i]));             // (as above)
+            }
+            top = warp_max(top);
+            if (!(warp_sum(total) < kSmallSum) || !(top > kNoScore)) continue;
+            total = 0.f;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) total += l[i] = ex2((l[i] - top) * kLog2e);
+            total = rcp(warp_sum(total));
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+                if (live(i)) row[e0 + i] += l[i] * total;
+        }
+    }
     __syncthreads();
     if (a.counts) {                           // the only block: counts, f, P and aux as well
         __shared__ float s_term[kWarps];
@@ -628,8 +665,58 @@ group_gate_kernel(const __grid_constant__ Args a) {
 // The ds reach their experts through a row of shared memory that is zero but for them (compared with every slot of every lane instead, and the
 // scores taken from the lanes that hold them, a token cost 920 instructions: 16384 x 256 in 19.6 us).
 constexpr int kBwdWarps = 8;
+// A token whose S is small, or under sigmoid the sum of all its s (so large or infinite ds): t_j = scale (s_j / S) (d_g_j - sum_i d_g_i s_i / S) from the
+// shares s_j / S, or scale s_j d_g_j, in place of ds s; under softmax of p (ds - <ds, p>) too, since the t add up to 0. id, d_g: of lane j, choice j and
+// its gate's gradient.
+__device__ __forceinline__ void group_gate_backward_small(const float* src, const float* f, int E, int k, int id, float dg, bool sigmoid, bool renorm,
+                                                       float scale, float coef, float* out) {
+    const int lane = threadIdx.x & 31;
+    if (id < 0 || id >= E) id = -1;
+    const float l = id >= 0 ? src[id] : -INFINITY;
+    float top = -INFINITY, total = 0.f, cq = 0.f;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) top = fmaxf(top, src[e]);
+    top = warp_max(top);
+    if (!(top > (sigmoid ? kNoScore : -INFINITY))) {                 // no score at all
+        for (int e = lane; e < E; e += 32) out[e] = 0.f;
+        return;
+    }
+    const bool tiny = sigmoid && top < -60.f;
+    // scores, of softmax and tiny ones multiples
+    auto score = [&](float x) { return sigmoid && !tiny ? rcp(1.f + ex2(-kLog2e * x)) : ex2((x - top) * kLog2e); };
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) {
+        const float s = score(src[e]);
+        total += s;
+        cq += coef * f[e] * s;
+    }
+    total = warp_sum(total);
+    const float inv = total == 0.f ? 0.f : rcp(total);
+    cq = warp_sum(cq) * inv;
+    float t = ex2(l * kLog2e) * dg;                                  // (all scores are small: exp(L))
+    if (renorm) {
+        const float share = share_of(l, sigmoid ? 0.f : top);
+        if (id < 0) dg = 0.f;
+        t = share * (dg - warp_sum(share * dg));
+    }
+    t *= scale;
+#pragma unroll 1
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + lane;
+        const float x = e < E ? src[e] : -INFINITY;
+        float d = e < E ? score(x) * inv * (coef * f[e] - cq) : 0.f;
+#pragma unroll 1
+        for (int j = 0; j < k; ++j) {
+            const int at = __shfl_sync(0xffffffffu, id, j);
+            const float v = __shfl_sync(0xffffffffu, t, j);
+            if (at == e) d += v;
+        }
+        if (e < E) out[e] = sigmoid ? d * rcp(1.f + ex2(kLog2e * x)) : d;
+    }
+}
+// (Four blocks an SM are launched: up to 256 experts they are all resident, up to 64 those of the next call beside them.)
 template <int NPL>
-__global__ void __launch_bounds__(kBwdWarps * 32)
+__global__ void __launch_bounds__(kBwdWarps * 32, NPL <= 2 ? 8 : NPL <= 8 ? 4 : 1)
 group_gate_backward_kernel(const float* logits, const int32_t* ids, const float* d_gates, const float* f, int T, int E, int k, bool sigmoid,
                            bool renorm, float scale, float coef, float* d_logits, unsigned* err) {
     __shared__ float s_ds[kBwdWarps][32 * NPL];
@@ -644,97 +731,109 @@ group_gate_backward_kernel(const float* logits, const int32_t* ids, const float*
         row[lane + 32 * i] = 0.f;
     }
     __syncwarp();
-    for (int t = blockIdx.x * kBwdWarps + warp; t < T; t += gridDim.x * kBwdWarps) {
-        const float* src = logits + (size_t)t * E;
-        float s[NPL], n[NPL];                                        // score, 1 - score
+    const int step = gridDim.x * kBwdWarps;
+    for (int t0 = blockIdx.x * kBwdWarps + warp; t0 < T; t0 += 32 * step) {
+        unsigned small = 0u, bit = 1u;
+        for (int t = t0; t < T && bit; t += step, bit <<= 1) {
+            const float* src = logits + (size_t)t * E;
+            float s[NPL], n[NPL];                                        // score, 1 - score
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) s[i] = lane + 32 * i < E ? src[lane + 32 * i] : -INFINITY;
-        int id = -1;
-        float dg = 0.f, mine = 0.f;                                  // lane j: choice j, its gate's gradient and its score
-        if (lane < k) {
-            id = ids[(size_t)t * k + lane];
-            dg = d_gates[(size_t)t * k + lane];
-            if (id < 0 || id >= E) { latch_device_error(err, kDevErrBadIndex, 0x300u); id = -1; }
-            if (id >= 0) mine = src[id];
-            else dg = 0.f;
-        }
-        float total = 0.f, m = 0.f;
-        if (sigmoid) {
-            // e = exp(-|L|): s and 1 - s are 1 / (1 + e) and e / (1 + e), neither a difference
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                const float e = ex2(-kLog2e * fabsf(s[i])), inv = rcp(1.f + e), b = e * inv;
-                const bool up = s[i] >= 0.f;
-                n[i] = up ? b : inv;
-                s[i] = up ? inv : b;
-                total += s[i];
+            for (int i = 0; i < NPL; ++i) s[i] = lane + 32 * i < E ? src[lane + 32 * i] : -INFINITY;
+            int id = -1;
+            float dg = 0.f, mine = 0.f;                                  // lane j: choice j, its gate's gradient and its score
+            if (lane < k) {
+                id = ids[(size_t)t * k + lane];
+                dg = d_gates[(size_t)t * k + lane];
+                if (id < 0 || id >= E) { latch_device_error(err, kDevErrBadIndex, 0x300u); id = -1; }
+                if (id >= 0) mine = src[id];
+                else dg = 0.f;
             }
-            mine = id >= 0 ? rcp(1.f + ex2(-kLog2e * mine)) : 0.f;
-        } else {
-            m = s[0];
+            float total = 0.f, m = 0.f;
+            if (sigmoid) {
+                // e = exp(-|L|): s and 1 - s are 1 / (1 + e) and e / (1 + e), neither a difference
 #pragma unroll
-            for (int i = 1; i < NPL; ++i) m = fmaxf(m, s[i]);
-            m = warp_max(m);
+                for (int i = 0; i < NPL; ++i) {
+                    const float e = ex2(-kLog2e * fabsf(s[i])), inv = rcp(1.f + e), b = e * inv;
+                    const bool up = s[i] >= 0.f;
+                    n[i] = up ? b : inv;
+                    s[i] = up ? inv : b;
+                    total += s[i];
+                }
+                mine = id >= 0 ? rcp(1.f + ex2(-kLog2e * mine)) : 0.f;
+            } else {
+                m = s[0];
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                s[i] = s[i] != -INFINITY ? ex2((s[i] - m) * kLog2e) : 0.f;
-                total += s[i];
+                for (int i = 1; i < NPL; ++i) m = fmaxf(m, s[i]);
+                m = warp_max(m);
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) {
+                    s[i] = s[i] != -INFINITY ? ex2((s[i] - m) * kLog2e) : 0.f;
+                    total += s[i];
+                }
+                mine = id >= 0 && mine != -INFINITY ? ex2((mine - m) * kLog2e) : 0.f;
             }
-            mine = id >= 0 && mine != -INFINITY ? ex2((mine - m) * kLog2e) : 0.f;
-        }
-        total = warp_sum(total);
-        const float tinv = total == 0.f ? 0.f : rcp(total);
-        if (!sigmoid) {
-            mine *= tinv;
+            total = warp_sum(total);
+            const float tinv = total == 0.f ? 0.f : rcp(total);
+            if (!sigmoid) {
+                mine *= tinv;
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) s[i] *= tinv;
-        }
-        float ds = scale * dg;
-        if (renorm) {
-            const float S = warp_sum(mine), w = warp_sum(mine * dg);
-            const float inv = S == 0.f ? 0.f : 1.f / S;
-            ds = scale * (dg - w * inv) * inv;
-        }
-        // a choice that is there twice (no route has one) is added in the choices' order
-        const unsigned same = __match_any_sync(0xffffffffu, id >= 0 ? id : -1 - lane);
-        const bool first = id >= 0 && lane == __ffs(same) - 1;
-        if (__any_sync(0xffffffffu, __popc(same) > 1)) {
-            float sum = 0.f;
-            for (int j = 0; j < k; ++j) {
-                const float v = __shfl_sync(0xffffffffu, ds, j);
-                if (same >> j & 1u) sum += v;
+                for (int i = 0; i < NPL; ++i) s[i] *= tinv;
             }
-            ds = sum;
-        }
-        if (first) row[id] = ds;
-        __syncwarp();
-        float d[NPL];                                                // gradient of the score
-        if (sigmoid) {
-            float cq = 0.f;
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) cq += c[i] * s[i];
-            cq = warp_sum(cq) * tinv;
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) d[i] = row[lane + 32 * i] + (c[i] - cq) * tinv;
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) d[i] = d[i] * s[i] * n[i];
-        } else {
-            float dot = 0.f;
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                d[i] = row[lane + 32 * i] + c[i];
-                dot += d[i] * s[i];
+            float ds = scale * dg, S = total;
+            if (renorm) {
+                S = warp_sum(mine);
+                const float w = warp_sum(mine * dg);
+                const float inv = S == 0.f ? 0.f : 1.f / S;
+                ds = scale * (dg - w * inv) * inv;
             }
-            dot = warp_sum(dot);
+            // a choice that is there twice (no route has one) is added in the choices' order
+            const unsigned same = __match_any_sync(0xffffffffu, id >= 0 ? id : -1 - lane);
+            const bool first = id >= 0 && lane == __ffs(same) - 1;
+            if (__any_sync(0xffffffffu, __popc(same) > 1)) {
+                float sum = 0.f;
+                for (int j = 0; j < k; ++j) {
+                    const float v = __shfl_sync(0xffffffffu, ds, j);
+                    if (same >> j & 1u) sum += v;
+                }
+                ds = sum;
+            }
+            if (first) row[id] = ds;
+            __syncwarp();
+            float d[NPL];                                                // gradient of the score
+            if (sigmoid) {
+                float cq = 0.f;
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) d[i] = s[i] * (d[i] - dot);
+                for (int i = 0; i < NPL; ++i) cq += c[i] * s[i];
+                cq = warp_sum(cq) * tinv;
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) d[i] = row[lane + 32 * i] + (c[i] - cq) * tinv;
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) d[i] = d[i] * s[i] * n[i];
+            } else {
+                float dot = 0.f;
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) {
+                    d[i] = row[lane + 32 * i] + c[i];
+                    dot += d[i] * s[i];
+                }
+                dot = warp_sum(dot);
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) d[i] = s[i] * (d[i] - dot);
+            }
+            __syncwarp();
+            if (first) row[id] = 0.f;
+            __syncwarp();
+            const bool is_small = S < kSmallSum;             // (its row is not written yet: d_logits may be logits)
+            if (is_small) small |= bit;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+                if (lane + 32 * i < E && !is_small) __stcs(d_logits + (size_t)t * E + lane + 32 * i, d[i]);
         }
-        __syncwarp();
-        if (first) row[id] = 0.f;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (lane + 32 * i < E) __stcs(d_logits + (size_t)t * E + lane + 32 * i, d[i]);
+        for (; small; small &= small - 1) {
+            const size_t t = t0 + (__ffs(small) - 1) * step;
+            group_gate_backward_small(logits + t * E, f, E, k, lane < k ? ids[t * k + lane] : -1, lane < k ? d_gates[t * k + lane] : 0.f, sigmoid, renorm, scale,
+                                      coef, d_logits + t * E);
+        }
     }
 }
 
