@@ -123,7 +123,7 @@ int moe_router_from_logits(const float* logits, const float* bias, int T, int E,
  *   The E experts form `groups` groups of equal size, consecutive; a group's score is the sum of its `best` (1 or 2) largest
  *   sel (-1e30 where those are opposite infinities); the top_groups groups with the largest scores stay, and topk_ids are the
  *   k experts of those with the largest sel, by falling sel. Equal scores: lower index. The choice is that of exact scores, not of rounded ones: what 32 bits cannot
- *   tell apart is compared in 64; without a bias the experts are ranked by their logits.
+ *   tell apart is compared in 64; without a bias the experts are ranked by their logits, masked ones last.
  *   gates[t,j] = scale * s, with renorm scale * s / (sum of the chosen s), 0 where all of those are below e^-700 (masked ones are 0).
  *   counts, f, aux as moe_router; P the mean of softmax(L), or of s_e / sum s (0 for a token whose scores are all below e^-700).
  *   Under softmax, a NaN or +inf logit makes its token's gates and P NaN.

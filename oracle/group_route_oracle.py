@@ -19,9 +19,9 @@ def route(L, bias, k, groups, top_groups, score, best, renorm, scale, alpha=0.01
     L = np.asarray(L, np.float64)
     T, E = L.shape
     s = scores(L, score)
-    # without a bias the order is that of the logits themselves (exact where s saturates)
+    # without a bias the order is that of the logits themselves (exact where s saturates), masked experts behind all of them
     sel = np.where(np.isneginf(L), MASKED, s + (0.0 if bias is None else np.asarray(bias, np.float64)))
-    rank = sel if bias is not None else np.where(np.isneginf(L), MASKED, L)
+    rank = sel if bias is not None else np.where(np.isneginf(L), -np.inf, L)
     ids = np.zeros((T, k), np.int64)
     gates = np.zeros((T, k))
     for t in range(T):

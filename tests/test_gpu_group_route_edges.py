@@ -150,3 +150,24 @@ def test_shares_of_sigmoid_scores_that_are_all_small(gpu_lib, T, E, distance, re
     s = O.scores(L64, "sigmoid")
     big = 0.35 * E / T * s / s.sum(1, keepdims=True) * 2
     assert (np.abs(d.double().cpu().numpy() - dwant) <= 2 * rel * big + 1e-37).all()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_the_lowest_finite_logits_come_before_masked_ones(gpu_lib, score):
+    """Without a bias: a masked expert's -1e30 is below every score, not below every logit."""
+    low, out = np.finfo(np.float32).min, -np.inf
+    r = gpu_lib.moe_group_route(torch.tensor([[out, -3e38, -1e31, out, np.nan if score == "sigmoid" else out, low]]).cuda(), None, 6, 1, 1, score=score)
+    ok(gpu_lib)
+    assert r["topk_ids"].tolist() == [[2, 1, 5, 0, 3, 4]]
+    # among many: a few that only their last bits tell apart, and more than a warp has lanes
+    g = np.random.default_rng(4)
+    for E, groups, top_groups, live in ((64, 1, 1, 5), (64, 4, 2, 9), (256, 1, 1, 100), (256, 8, 3, 200), (900, 9, 4, 400), (1024, 1, 1, 3)):
+        L = np.full((30, E), out, np.float32)
+        for row in L:
+            row[g.permutation(E)[:live]] = low
+        steps = g.integers(0, 40, size=L.shape)
+        L = np.where(np.isneginf(L), L, (low * (1.0 - steps * 2.0**-24)).astype(np.float32))
+        r = gpu_lib.moe_group_route(torch.from_numpy(L).cuda(), None, 8, groups, top_groups, score=score)
+        ok(gpu_lib)
+        want = O.route(L.astype(np.float64), None, 8, groups, top_groups, score, 2, True, 1.0)
+        np.testing.assert_array_equal(r["topk_ids"].cpu().numpy(), want["ids"])

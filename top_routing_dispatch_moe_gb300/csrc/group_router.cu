@@ -6,7 +6,7 @@
 //   the k experts of those groups with the largest sel, equal ones: lower index
 //   gate_j = scale * s_j, or scale * s_j / (sum of the chosen s) (0 where all of them are below e^-700)
 // The choice is that of exact scores: two scores that 32 bits cannot tell apart are compared in 64. Without a bias the
-// experts are ranked by the logits themselves (both scores rise with them), which needs no such comparison.
+// experts are ranked by the logits themselves (both scores rise with them), masked ones last, which needs no such comparison.
 //
 // One warp to a token. A group is a run of lpg lanes, a power of two, and a lane holds npl of its group's experts in a row (the last
 // lanes of a group fewer), so that equal scores go to the lowest lane. Where that were over 32 experts to a lane (9 groups of 100), lane l
@@ -236,7 +236,7 @@ __device__ __noinline__ int choose_exact(const Args& a, const float* L) {
 #pragma unroll 1
     for (int i = 0; i < npl; ++i) {
         if (i >= h.n || !(kept >> ((h.e0 + i) / a.per) & 1u)) taken |= 1u << i;
-        if (!a.bias && L[i] > -INFINITY) sel[i] = order_of((double)L[i]);      // (ranked by the logits)
+        if (!a.bias) sel[i] = order_of((double)fmaxf(L[i], -INFINITY));        // (ranked by the logits; a NaN as masked)
     }
     int my_id = 0;
 #pragma unroll 1
@@ -267,7 +267,7 @@ __device__ __noinline__ int order_exact(const Args& a, const float* L, Candidate
         const Norm norm = a.sigmoid ? Norm{0.0, 0.0} : exact_norm(L, a.npl);
         if (lane < n) v = order_of(exact_sel(l, a.bias[id], norm.m, norm.z));
     } else if (lane < n) {
-        v = order_of(l > -INFINITY ? (double)l : (double)kMasked);
+        v = order_of((double)fmaxf(l, -INFINITY));
     }
     __syncwarp();
     int rank = 0;
@@ -425,7 +425,8 @@ group_gate_kernel(const __grid_constant__ Args a) {
             const float v = s[i] + bias[i];
             const bool in = L[i] > -INFINITY && v == v;
             const float sel = in ? v : kMasked;
-            key[i] = live(i) ? (key_of(a.bias || !in ? sel : L[i]) & ~SLOT) | (SLOT - i) : 0u;
+            // (without a bias: the logit, and for what is masked one below all of them)
+            key[i] = live(i) ? (key_of(a.bias ? sel : in ? L[i] : -INFINITY) & ~SLOT) | (SLOT - i) : 0u;
             if (live(i)) {
                 t2 = fmaxf(t2, fminf(t1, sel));
                 t1 = fmaxf(t1, sel);
