@@ -171,3 +171,18 @@ def test_the_lowest_finite_logits_come_before_masked_ones(gpu_lib, score):
         ok(gpu_lib)
         want = O.route(L.astype(np.float64), None, 8, groups, top_groups, score, 2, True, 1.0)
         np.testing.assert_array_equal(r["topk_ids"].cpu().numpy(), want["ids"])
+
+
+@pytest.mark.parametrize("E", [128, 256, 384, 512, 768, 1024])
+def test_logits_on_no_boundary_are_routed_as_those_on_one(gpu_lib, E):
+    """Rows on 16 bytes are read in pieces of four logits, others one by one."""
+    g = torch.Generator().manual_seed(E)
+    flat = torch.zeros(37 * E + 1, device="cuda")
+    L = torch.randn(37, E, generator=g).cuda()
+    flat[1:].copy_(L.view(-1))
+    b = (torch.randn(E, generator=g) * 0.05).cuda()
+    for bias in (None, b):
+        for score in ("sigmoid", "softmax"):
+            on, off = (gpu_lib.moe_group_route(x, bias, 8, 8, 3, score=score) for x in (L, flat[1:].view(37, E)))
+            ok(gpu_lib)
+            assert all(torch.equal(on[name], off[name]) for name in on)

@@ -366,7 +366,8 @@ group_gate_kernel(const __grid_constant__ Args a) {
     if (a.bias) most = warp_max(most);
     bool empty = false;                       // a token whose scores have a small sum
     for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
-        float L[NPL], s[NPL];                                        // logits, scores
+        alignas(16) float L[NPL];                                    // logits (16 bytes of them a load)
+        float s[NPL];                                                // scores
         const float* src = a.logits + (size_t)t * a.E;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) L[i] = -INFINITY;
