@@ -232,9 +232,9 @@ def moe_sinkhorn_bias(logits, n_iter: int = 16, *, sel_bias=None, ws=None, strea
 # ------------------------------------------------------------------------------------- routing by groups
 
 def _counts(*n: int):
-    """Sizes on their way to C ints, which would take them modulo 2^32."""
-    if max(n) > 0x7FFFFFFF:
-        raise MoEError(MOE_ERR_INVALID_ARG, f"a size of {max(n)}")
+    """Numbers on their way to C ints, which would take them modulo 2^32."""
+    if max(n) > 0x7FFFFFFF or min(n) < -0x80000000:
+        raise MoEError(MOE_ERR_INVALID_ARG, f"a size of {max(n, key=abs)}")
 
 
 def _score(score: str | int) -> int:
@@ -242,6 +242,7 @@ def _score(score: str | int) -> int:
         if score not in SCORE:
             raise MoEError(MOE_ERR_UNSUPPORTED, f"score {score!r}")
         return SCORE[score]
+    _counts(int(score))
     return int(score)
 
 
@@ -291,12 +292,13 @@ def moe_group_route(logits, bias, k: int, groups: int, top_groups: int, *, score
     if logits.dim() != 2:
         _fp4_fail("logits: [T, E]")
     T, E = logits.shape
-    _counts(T, E)
+    score = _score(score)
+    _counts(T, E, k, groups, top_groups, best)
     f32 = torch.float32
     topk_ids, gates, counts, f, P, aux = _route_outputs(T, E, k, logits, stream, topk_ids, gates, counts, f, P, aux)
     ws = _fp4_bytes(_lib.moe_group_route_workspace_size(T, E), logits, stream) if ws is None else ws
     rc = _lib.moe_group_route(_fp4_data(logits, T * E, f32, "logits"), _fp4_data(bias, E, f32, "bias"), T, E, k, groups, top_groups,
-                              _score(score), best, int(renorm), scale, alpha, topk_ids.data_ptr(), gates.data_ptr(), counts.data_ptr(),
+                              score, best, int(renorm), scale, alpha, topk_ids.data_ptr(), gates.data_ptr(), counts.data_ptr(),
                               f.data_ptr(), P.data_ptr(), aux.data_ptr(), _fp4_data(ws, 0, torch.uint8, "ws"), ws.numel(),
                               _fp4_stream(stream, logits))
     if rc:
@@ -314,7 +316,8 @@ def moe_group_router(x, w_packed, E: int, bias, k: int, groups: int, top_groups:
     """moe_group_route on the logits of x [T, h] (bf16 or fp32) and the packed router weight (moe_pack_router_weight) of E
     experts; the dict also holds the logits [T, E] (None with want_logits=False, unless given)."""
     T, h = x.shape
-    _counts(T, h, E)
+    score = _score(score)
+    _counts(T, h, E, k, groups, top_groups, best)
     dt = dtype_code(x.dtype)
     if not x.is_contiguous() or not x.is_cuda:
         _fp4_fail("x: a contiguous device tensor")
@@ -323,7 +326,7 @@ def moe_group_router(x, w_packed, E: int, bias, k: int, groups: int, top_groups:
     topk_ids, gates, counts, f, P, aux = _route_outputs(T, E, k, x, stream, topk_ids, gates, counts, f, P, aux)
     ws = _fp4_bytes(_lib.moe_group_router_workspace_size(T, h, E, dt), x, stream) if ws is None else ws
     _check(_lib.moe_group_router(x.data_ptr(), _fp4_data(w_packed, _lib.moe_router_packed_bytes(h, E, dt), torch.uint8, "w_packed"),
-                                 _fp4_data(bias, E, torch.float32, "bias"), T, h, E, k, dt, groups, top_groups, _score(score), best,
+                                 _fp4_data(bias, E, torch.float32, "bias"), T, h, E, k, dt, groups, top_groups, score, best,
                                  int(renorm), scale, alpha, _fp4_data(logits, T * E, torch.float32, "logits"),
                                  topk_ids.data_ptr(), gates.data_ptr(), counts.data_ptr(), f.data_ptr(), P.data_ptr(), aux.data_ptr(),
                                  _fp4_data(ws, 0, torch.uint8, "ws"), ws.numel(), _fp4_stream(stream, x)))
@@ -336,12 +339,13 @@ def moe_group_route_backward(logits, topk_ids, d_gates, f, *, score="sigmoid", r
     if logits.dim() != 2 or topk_ids.dim() != 2 or topk_ids.shape[0] != logits.shape[0]:
         _fp4_fail("logits: [T, E], topk_ids: [T, k]")
     (T, E), k = logits.shape, topk_ids.shape[1]
+    score = _score(score)
     _counts(T, E, k)
     d_logits = _fp4_empty((T, E), torch.float32, logits, stream) if d_logits is None else d_logits
     _check(_lib.moe_group_route_backward(_fp4_data(logits, T * E, torch.float32, "logits"),
                                          _fp4_data(topk_ids, T * k, torch.int32, "topk_ids"),
                                          _fp4_data(d_gates, T * k, torch.float32, "d_gates"), _fp4_data(f, E, torch.float32, "f"),
-                                         T, E, k, _score(score), int(renorm), scale, alpha, d_aux,
+                                         T, E, k, score, int(renorm), scale, alpha, d_aux,
                                          _fp4_data(d_logits, T * E, torch.float32, "d_logits"), _fp4_stream(stream, logits)))
     return d_logits
 
@@ -1209,6 +1213,7 @@ def moe_int8_expert_ffn(x, offsets, packed, gate_scales, up_scales, down_scales,
 def moe_checkpoint8_save(x, *, tile_sched=None, E: int = 0, codes=None, scales=None, stream=None):
     """x [rows, C] (bf16, fp16 or fp32, row stride free) -> (codes int8 [rows, C], scales fp32 [rows, ceil(C / 128)]): what a forward
     keeps for its backward. With tile_sched (moe_dispatch's) of E experts only its rows."""
+    _counts(E)
     (rows, C), ldx = x.shape, _fp4_rows(x, "x")
     _counts(rows, C)
     nb = (C + 127) // 128
@@ -1249,6 +1254,7 @@ def _checkpoint8_data(codes, scales, d_act):
 def moe_checkpoint8_swiglu_backward(codes, scales, d_act, *, tile_sched=None, E: int = 0, d_gu=None, act=None, stream=None):
     """(d_gu [rows, gu_cols(F)], act [rows, F]), bf16: the SwiGLU backward from pre-activations that moe_checkpoint8_save kept, and act
     from the same. With tile_sched (moe_dispatch's) of E experts only its rows."""
+    _counts(E)
     rows, F, data = _checkpoint8_data(codes, scales, d_act)
     d_gu = _fp4_empty((rows, gu_cols(F)), torch.bfloat16, d_act, stream) if d_gu is None else d_gu
     act = _fp4_empty((rows, F), torch.bfloat16, d_act, stream) if act is None else act
@@ -1261,6 +1267,7 @@ def moe_checkpoint8_swiglu_backward(codes, scales, d_act, *, tile_sched=None, E:
 def moe_expert_up_gate_backward_checkpoint8(codes, scales, d_act, tile_sched, packed_bwd, E: int, h: int, *, d_gu=None, act=None, d_buf=None,
                                             stream=None):
     """moe_expert_up_gate_backward_saved from pre-activations kept in 8 bits: (d_gu, act, d_buf)."""
+    _counts(E, h)
     rows, F, data = _checkpoint8_data(codes, scales, d_act)
     d_gu = _fp4_empty((rows, gu_cols(F)), torch.bfloat16, d_act, stream) if d_gu is None else d_gu
     act = _fp4_empty((rows, F), torch.bfloat16, d_act, stream) if act is None else act
