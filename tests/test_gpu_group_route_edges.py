@@ -186,3 +186,34 @@ def test_logits_on_no_boundary_are_routed_as_those_on_one(gpu_lib, E):
             on, off = (gpu_lib.moe_group_route(x, bias, 8, 8, 3, score=score) for x in (L, flat[1:].view(37, E)))
             ok(gpu_lib)
             assert all(torch.equal(on[name], off[name]) for name in on)
+
+
+@pytest.mark.parametrize("level", [-22.0, -45.0, -62.0, -66.0, -68.0])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_shares_of_scores_that_are_nothing_beside_larger_ones(gpu_lib, score, level):
+    """Chosen scores of exp(level) and others down to below 2^-126, where the larger ones' sum is an ordinary number: the small shares
+    are there to 2^-86 (fp32's smallest number in a sum of 2^-40)."""
+    L = torch.full((5, 16), level - 3.0)
+    L[:, [1, 4, 6, 7]] = torch.tensor([level, level - 0.7, -88.5, -95.0]) + torch.randn(5, 4, generator=torch.Generator().manual_seed(3)) * 0.2
+    if score == "softmax":
+        L[:, 12] = 0.0
+    b = torch.zeros(16)
+    b[[1, 4, 6, 7]] = 2.0
+    r = gpu_lib.moe_group_route(L.cuda(), b.cuda(), 4, 2, 1, score=score)
+    ok(gpu_lib)
+    L64 = L.double().numpy()
+    want = O.route(L64, b.numpy(), 4, 2, 1, score, 2, True, 1.0)
+    np.testing.assert_array_equal(r["topk_ids"].cpu().numpy(), want["ids"])
+    rel = (32 + 2 * 100) * EPS
+    np.testing.assert_allclose(r["gates"].double().cpu().numpy(), want["gates"], rtol=rel, atol=2.0**-85)
+    np.testing.assert_allclose(r["P"].double().cpu().numpy(), want["P"], rtol=rel, atol=2.0**-85)
+    dg = torch.randn(5, 4, generator=torch.Generator().manual_seed(7))
+    d = gpu_lib.moe_group_route_backward(L.cuda(), r["topk_ids"], dg.cuda(), r["f"], score=score, d_aux=0.0)
+    ok(gpu_lib)
+    dwant = O.backward(L64, want["ids"], dg.double().numpy(), r["f"].double().cpu().numpy(), score, True, 1.0, 0.01, 0.0)
+    share = np.zeros((5, 16))
+    np.put_along_axis(share, want["ids"], want["gates"], 1)
+    # a share times a difference of gates' gradients; under softmax, in the ordinary way, <dp, p> cancels to roundings of the largest term
+    s = O.scores(L64, score)
+    big = 2 * float(dg.abs().max()) * (share + s * share.max(1, keepdims=True))
+    assert (np.abs(d.double().cpu().numpy() - dwant) <= 2 * rel * big + 2.0**-83).all()

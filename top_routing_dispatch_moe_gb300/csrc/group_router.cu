@@ -300,11 +300,11 @@ __device__ __forceinline__ float rcp(float x) {
 }
 constexpr float kLog2e = 1.44269504f;
 
-// A sum of scores below this, 2^-100, may have lost some of them (they are 0 below 2^-126), and its reciprocal may be infinite. Shares in
-// it are formed from exp(L - the largest L) instead, to which scores that small are proportional (1 + exp(L) is 1), if the largest score is
+// A sum of scores below this, 2^-40, loses some of them (they are 0 below 2^-126), and its reciprocal may be infinite. Shares in it are
+// formed from exp(L - the largest L) instead, to which scores that small are proportional (1 + exp(L) is 1), if the largest score is
 // above e^kNoScore. Tokens with such a sum, but for a router's gates, are noted and seen to after the others: in their place the branches
 // held up every token (backward of 16384 x 256 9.5 -> 10.5 us).
-constexpr float kSmallSum = 7.8886e-31f, kNoScore = -700.f;
+constexpr float kSmallSum = 9.094947e-13f, kNoScore = -700.f;
 // The share of this lane's logit (-inf: none) in the sum of the warp's scores; unit: the logit whose score would be 1.
 __device__ __forceinline__ float share_of(float l, float unit) {
     const float top = warp_max(l), s = top - unit > kNoScore ? ex2((l - top) * kLog2e) : 0.f, sum = warp_sum(s);
@@ -683,7 +683,7 @@ __device__ __forceinline__ void group_gate_backward_small(const float* src, cons
         for (int e = lane; e < E; e += 32) out[e] = 0.f;
         return;
     }
-    const bool tiny = sigmoid && top < -60.f;
+    const bool tiny = sigmoid && top < -30.f;
     // scores, of softmax and tiny ones multiples
     auto score = [&](float x) { return sigmoid && !tiny ? rcp(1.f + ex2(-kLog2e * x)) : ex2((x - top) * kLog2e); };
 #pragma unroll 1
