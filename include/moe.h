@@ -126,7 +126,7 @@ int moe_router_from_logits(const float* logits, const float* bias, int T, int E,
  *   tell apart is compared in 64; without a bias the experts are ranked by their logits, masked ones last.
  *   gates[t,j] = scale * s, with renorm scale * s / (sum of the chosen s), 0 where all of those are below e^-700 (masked ones are 0).
  *   counts, f, aux as moe_router; P the mean of softmax(L), or of s_e / sum s (0 for a token whose scores are all below e^-700).
- *   Under softmax, a NaN or +inf logit makes its token's gates and P NaN.
+ *   Under softmax, a NaN or +inf logit makes its token's gates and P NaN; under sigmoid a NaN logit makes P NaN.
  * moe_group_route: on given fp32 logits [T,E]. moe_group_router: from x [T,h] and the packed router weight
  *   (moe_pack_router_weight), the logits as moe_router_packed computes them, without a bias in them; logits [T,E] may be NULL.
  * moe_group_route_backward: d_logits [T,E] fp32 from d_gates [T,k] and d_aux, the choice held fixed (the bias gets none):

@@ -11,7 +11,7 @@
 // One warp to a token. A group is a run of lpg lanes, a power of two, and a lane holds npl of its group's experts in a row (the last
 // lanes of a group fewer), so that equal scores go to the lowest lane. Where that were over 32 experts to a lane (9 groups of 100), lane l
 // holds the experts l npl .. l npl + npl - 1 and the groups' scores go through shared memory.
-// (16384 tokens by 8 groups of 37: 67 us that way, 40 with runs of lanes; 4 of 50: 57 and 29; 16 of 48: 166 and 93.)
+// (16384 tokens by 8 groups of 37: 67 us that way, 43 with runs of lanes; 4 of 50: 57 and 29; 16 of 48: 166 and 96.)
 #include <math.h>
 #include <algorithm>
 #include "common.cuh"
@@ -333,10 +333,10 @@ __device__ __forceinline__ void sort_keys(unsigned (&key)[N]) {
 // k rounds compare the lanes' heads without those bits: equal ones go to the lowest lane, and within a lane to the lowest slot. What
 // the missing bits, and the roundings of the scores, may have confused is found afterwards from the chosen keys' differences, each lane
 // looking at one, and put right in 64 bits.
-// (16384 tokens by 256 experts, k 8 of 4 of 8 groups: 29 us with the finalize, 2 of them for the tokens that 64 bits decide; bound by
-// instructions, 850 a token. An argmax over unsorted slots in every round, with libm's exponential and division, took 45 us of
-// scores and rounds; the whole choice in 64 bits 50 us for the one token of some thousands that needs it. Two or four blocks an SM
-// instead of three: 30 and 31 us.)
+// (16384 tokens by 256 experts, k 8 of 4 of 8 groups: 25 us with the finalize, from a graph; bound by instructions, 850 a token. When it was
+// 29, 2 of them were the tokens that 64 bits decide, and two or four blocks an SM instead of three took 30 and 31. An argmax over
+// unsorted slots in every round, with libm's exponential and division, took 45 us of scores and rounds; the whole choice in 64 bits
+// 50 us for the one token of some thousands that needs it.)
 // FULL: every lane holds NPL experts.
 template <int NPL, bool FULL>
 __global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 3 : NPL <= 16 ? 2 : 1)

@@ -860,7 +860,7 @@ static int launch_product(const Params& p, cudaStream_t s) {
                 "8-bit product: %d rows by %d channels are over 2^31 tiles", p.rows, p.N);
     // The few rows' kernel where a group has up to 8 on average (128 groups by 1536 x 2048, us by it / by pairs of 64 rows: 4 rows a group 67 / 73,
     // 8: 69 / 73, 16: 76 / 76, and 16 unevenly 104 / 78), and where its tiles are no more than the SMs: pairs take longer to start (16 rows by
-    // 4096 x 4096: 13.7 / 16.7).
+    // 4096 x 4096: 8.7 / 16.7). The mean is all that the host knows: rows of which most go to one group pass over its weights once for 16 of them.
     const long long used = std::min(p.G, p.rows);
     return p.rows / used <= 8 || most_tiles(p) <= num_sms() ? launch_few<EPI>(p, s) : launch_pairs<EPI>(p, s);
 }

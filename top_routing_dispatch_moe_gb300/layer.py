@@ -47,7 +47,9 @@ class MoELayer:
 
     checkpoint="int8" (with backward=True): forward(save=True) keeps the pre-activations in 8 bits (a scale for 128 columns) instead
     of bf16, and the backward computes act from them again. The bf16 pre-activations then pass through `scratch`, a bf16 tensor of
-    checkpoint_scratch(...) elements that layers run one after the other may share (None: the layer's own)."""
+    checkpoint_scratch(...) elements that layers run one after the other may share. None: the layer's own, held as long as the
+    layer, which then takes half as much memory again as with checkpoint="dtype"; memory is saved by three layers or more that share
+    one."""
 
     STAGES = ("router", "dispatch", "up_gate", "down", "shared_up_gate", "shared_down", "combine")
 
