@@ -217,3 +217,37 @@ def test_shares_of_scores_that_are_nothing_beside_larger_ones(gpu_lib, score, le
     s = O.scores(L64, score)
     big = 2 * float(dg.abs().max()) * (share + s * share.max(1, keepdims=True))
     assert (np.abs(d.double().cpu().numpy() - dwant) <= 2 * rel * big + 2.0**-83).all()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_many_tokens_of_small_sums_among_others(gpu_lib, score):
+    """More tokens than all warps take in 32 steps each: every row as in a call of its own, and with the logits' gradient in their place."""
+    T, E = 400_000, 32
+    g = torch.Generator("cuda").manual_seed(1)
+    L = torch.randn(T, E, device="cuda", generator=g)
+    far = torch.rand(T, device="cuda", generator=g) < 0.4
+    if score == "sigmoid":
+        L[far] -= 90.0
+    else:
+        L[far, :8] -= 90.0
+    L[::97] = -float("inf")
+    b = torch.zeros(E, device="cuda")
+    b[:8] = 2.0
+    dg = torch.randn(T, 4, device="cuda", generator=g)
+    r = gpu_lib.moe_group_route(L, b, 4, 4, 1, score=score)
+    d = gpu_lib.moe_group_route_backward(L, r["topk_ids"], dg, r["f"], score=score, d_aux=0.0)
+    ok(gpu_lib)
+    assert torch.isfinite(r["gates"]).all() and torch.isfinite(d).all()
+    live = torch.isfinite(L).any(1)
+    assert (r["gates"].sum(1) - live.float()).abs().max().item() <= 32 * EPS
+    # P adds the shares of some 400 of a block's tokens in turn, then the blocks'
+    assert abs(r["P"].sum().item() - live.double().mean().item()) <= (64 + T / 800) * EPS
+    for lo in (0, 155_600, 311_200, T - 50):
+        part = slice(lo, lo + 50)
+        one = gpu_lib.moe_group_route(L[part].contiguous(), b, 4, 4, 1, score=score)
+        d_one = gpu_lib.moe_group_route_backward(L[part].contiguous(), one["topk_ids"], dg[part].contiguous(), one["f"], score=score, d_aux=0.0)
+        ok(gpu_lib)
+        assert torch.equal(one["gates"], r["gates"][part]) and torch.equal(one["topk_ids"], r["topk_ids"][part]) and torch.equal(d_one, d[part])
+    gpu_lib.moe_group_route_backward(L, r["topk_ids"], dg, r["f"], score=score, d_aux=0.0, d_logits=L)
+    ok(gpu_lib)
+    assert torch.equal(L, d)

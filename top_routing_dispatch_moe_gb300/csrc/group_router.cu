@@ -307,6 +307,7 @@ constexpr float kLog2e = 1.44269504f;
 constexpr float kSmallSum = 9.094947e-13f, kNoScore = -700.f;
 // The share of this lane's logit (-inf: none) in the sum of the warp's scores; unit: the logit whose score would be 1.
 __device__ __forceinline__ float share_of(float l, float unit) {
+    if (!__any_sync(0xffffffffu, l > -INFINITY)) return 0.f;
     const float top = warp_max(l), s = top - unit > kNoScore ? ex2((l - top) * kLog2e) : 0.f, sum = warp_sum(s);
     return sum == 0.f ? 0.f : s * rcp(sum);
 }
@@ -407,7 +408,12 @@ group_gate_kernel(const __grid_constant__ Args a) {
         }
         total = warp_sum(total);
         const float inv = total < kSmallSum ? 0.f : rcp(total);      // (softmax's total is 1 or more, or 0 where all are masked)
-        empty = empty || total < kSmallSum;
+        if (total < kSmallSum) {
+            bool some = false;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) some = some || L[i] > kNoScore;
+            empty = __any_sync(0xffffffffu, some) || empty;
+        }
 #pragma unroll
         for (int i = 0; i < NPL; ++i) Pacc[i] += s[i] * inv;
         if (!a.sigmoid) {
@@ -668,10 +674,10 @@ group_gate_kernel(const __grid_constant__ Args a) {
 // scores taken from the lanes that hold them, a token cost 920 instructions: 16384 x 256 in 19.6 us).
 constexpr int kBwdWarps = 8;
 // A token whose S is small, or under sigmoid the sum of all its s (so large or infinite ds): t_j = scale (s_j / S) (d_g_j - sum_i d_g_i s_i / S) from the
-// shares s_j / S, or scale s_j d_g_j, in place of ds s; under softmax of p (ds - <ds, p>) too, since the t add up to 0. id, d_g: of lane j, choice j and
-// its gate's gradient.
+// shares s_j / S, or scale s_j d_g_j, in place of ds s; under softmax of p (ds - <ds, p>) too, since the t add up to 0. Some expert has a
+// score. id, dg: of lane j, choice j and its gate's gradient.
 __device__ __forceinline__ void group_gate_backward_small(const float* src, const float* f, int E, int k, int id, float dg, bool sigmoid, bool renorm,
-                                                       float scale, float coef, float* out) {
+                                                          float scale, float coef, float* out) {
     const int lane = threadIdx.x & 31;
     if (id < 0 || id >= E) id = -1;
     const float l = id >= 0 ? src[id] : -INFINITY;
@@ -679,10 +685,6 @@ __device__ __forceinline__ void group_gate_backward_small(const float* src, cons
 #pragma unroll 1
     for (int e = lane; e < E; e += 32) top = fmaxf(top, src[e]);
     top = warp_max(top);
-    if (!(top > (sigmoid ? kNoScore : -INFINITY))) {                 // no score at all
-        for (int e = lane; e < E; e += 32) out[e] = 0.f;
-        return;
-    }
     const bool tiny = sigmoid && top < -30.f;
     // scores, of softmax and tiny ones multiples
     auto score = [&](float x) { return sigmoid && !tiny ? rcp(1.f + ex2(-kLog2e * x)) : ex2((x - top) * kLog2e); };
@@ -716,9 +718,9 @@ __device__ __forceinline__ void group_gate_backward_small(const float* src, cons
         if (e < E) out[e] = sigmoid ? d * rcp(1.f + ex2(kLog2e * x)) : d;
     }
 }
-// (Four blocks an SM are launched: up to 256 experts they are all resident, up to 64 those of the next call beside them.)
+// (Four blocks an SM are launched, and are all resident up to 256 experts.)
 template <int NPL>
-__global__ void __launch_bounds__(kBwdWarps * 32, NPL <= 2 ? 8 : NPL <= 8 ? 4 : 1)
+__global__ void __launch_bounds__(kBwdWarps * 32, NPL <= 8 ? 4 : 1)
 group_gate_backward_kernel(const float* logits, const int32_t* ids, const float* d_gates, const float* f, int T, int E, int k, bool sigmoid,
                            bool renorm, float scale, float coef, float* d_logits, unsigned* err) {
     __shared__ float s_ds[kBwdWarps][32 * NPL];
@@ -750,7 +752,9 @@ group_gate_backward_kernel(const float* logits, const int32_t* ids, const float*
                 if (id >= 0) mine = src[id];
                 else dg = 0.f;
             }
-            float total = 0.f, m = 0.f;
+            float total = 0.f, m = 0.f, top = -INFINITY;                 // (top: this lane's)
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) top = fmaxf(top, s[i]);
             if (sigmoid) {
                 // e = exp(-|L|): s and 1 - s are 1 / (1 + e) and e / (1 + e), neither a difference
 #pragma unroll
@@ -763,10 +767,7 @@ group_gate_backward_kernel(const float* logits, const int32_t* ids, const float*
                 }
                 mine = id >= 0 ? rcp(1.f + ex2(-kLog2e * mine)) : 0.f;
             } else {
-                m = s[0];
-#pragma unroll
-                for (int i = 1; i < NPL; ++i) m = fmaxf(m, s[i]);
-                m = warp_max(m);
+                m = warp_max(top);
 #pragma unroll
                 for (int i = 0; i < NPL; ++i) {
                     s[i] = s[i] != -INFINITY ? ex2((s[i] - m) * kLog2e) : 0.f;
@@ -825,7 +826,8 @@ group_gate_backward_kernel(const float* logits, const int32_t* ids, const float*
             __syncwarp();
             if (first) row[id] = 0.f;
             __syncwarp();
-            const bool is_small = S < kSmallSum;             // (its row is not written yet: d_logits may be logits)
+            // (its row is not written yet: d_logits may be logits; of tokens without any score all is 0)
+            const bool is_small = S < kSmallSum && __any_sync(0xffffffffu, top > (sigmoid ? kNoScore : -INFINITY));
             if (is_small) small |= bit;
 #pragma unroll
             for (int i = 0; i < NPL; ++i)
